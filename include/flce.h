@@ -1,7 +1,7 @@
 /*
  * flce.h -- C ABI of the GB300 (sm_103a) fused linear cross entropy library.
  *
- * Two operations:
+ * The loss of a language-model head and what a training step runs around it:
  *
  *  flce_fwd_bwd  Fused linear cross entropy (FLCE): the lm_head projection
  *                z = H W^T (+ b) fused with softmax cross entropy (ignore_index,
@@ -27,14 +27,21 @@
  *                vocab-parallel CE backend), "Changes" and "Real-device
  *                validation".
  *
+ *  ln_fwd, ln_bwd  Layer norm, or its form without the mean, in front of the
+ *                head: it gives flce_fwd_bwd its hidden states and takes their
+ *                gradient.
+ *
+ *  grad_norm, adamw_step  The norm of all gradients and one AdamW step over
+ *                many tensors, with moments in fp32 or in 8 bits.
+ *
  * Conventions shared by every entry point
  * ---------------------------------------
  *  - Every tensor pointer is a DEVICE pointer to memory the caller owns.  The
  *    library never allocates, frees or synchronises; all work is enqueued on
  *    `stream` (a cudaStream_t; NULL is the legacy default stream) and runs
  *    asynchronously.  Outputs are valid once the stream reaches the call.
- *  - Matrices are row-major and contiguous.  bf16 is IEEE bfloat16; results
- *    stored as bf16 are rounded to nearest even.
+ *  - Matrices are row-major and, where no ld is given, contiguous.  bf16 is
+ *    IEEE bfloat16; results stored as bf16 are rounded to nearest even.
  *  - Host-checkable faults (NULL required pointer, bad enum, bad shape or
  *    alignment, workspace too small) return an error code BEFORE anything is
  *    enqueued.  FLCE_ERR_CUDA means a launch failed (cudaGetLastError).
@@ -353,6 +360,200 @@ flce_status_t ce_fwd_bwd_noalloc(const void* logits, int dtype, void* grad_logit
                                  flce_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * Layer norm in front of the head
+ * ------------------------------------------------------------------------
+ * Per row n of x [N, H]:
+ *     s    = x (+ residual, rounded to the type of x)
+ *     mu   = sum_h s / H            (FLCE_NORM_LAYER; 0 for FLCE_NORM_RMS)
+ *     rstd = 1 / sqrt(sum_h (s - mu)^2 / H + eps)
+ *     xhat = (s - mu) * rstd,   y = xhat * weight + bias
+ * and backward, with u = grad_y * weight:
+ *     grad_s = rstd * (u - mean_h(u) [layer only] - xhat * mean_h(u * xhat))
+ *     grad_x = grad_residual = grad_s + grad_sum
+ *     grad_weight = sum_n grad_y * xhat,   grad_bias = sum_n grad_y
+ * Everything between loading and storing is fp32; the rows' sums of squares
+ * are taken about the mean, in a second pass over the row held on the chip.
+ *
+ * Matrices here are rows of H contiguous elements, `ld` elements apart: for an
+ * input any ld >= 0 (0 repeats one row), for an output ld >= H, at most 2^29.
+ * Pointers need
+ * the alignment of their elements only; 16-byte aligned rows (pointer and ld)
+ * are the fast case.  Except where said, buffers do not overlap.  Rows that
+ * hold an infinity or NaN get NaN in that row alone (and in the column sums).
+ */
+typedef enum {
+  FLCE_NORM_LAYER = 0, /* mean and variance                     */
+  FLCE_NORM_RMS = 1    /* no mean: the root of the mean square  */
+} flce_norm_t;
+
+/*
+ * ln_fwd
+ *
+ *  kind          flce_norm_t.
+ *  dtype         type of x, residual, y and sum: FLCE_DTYPE_BF16, _FP16 or _FP32.
+ *  residual      [N, H] or NULL: added to x first.
+ *  weight, bias  [H] of `param_dtype` (any of the three types), either NULL
+ *                (1 and 0).
+ *  N, H          rows (>= 0) and columns (1 to 2^24 - 1).
+ *  eps           >= 0.
+ *  y             [N, H] output.
+ *  sum           [N, H] output: s, what the row statistics are taken of, or
+ *                NULL (must be NULL without residual).
+ *  mean, rstd    fp32 [N] outputs or NULL (mean must be NULL for FLCE_NORM_RMS).
+ *
+ * y or sum may be x or residual itself (same pointer and ld).
+ */
+flce_status_t ln_fwd(int kind, int dtype, const void* x, int64_t ld_x, const void* residual,
+                     int64_t ld_residual, const void* weight, const void* bias, int param_dtype,
+                     int64_t N, int64_t H, float eps, void* y, int64_t ld_y, void* sum,
+                     int64_t ld_sum, float* mean, float* rstd, flce_stream_t stream);
+
+/* Bytes of workspace ln_bwd needs; 0 for invalid sizes. */
+size_t ln_workspace_size(int64_t N, int64_t H);
+
+/*
+ * ln_bwd
+ *
+ *  x             what ln_fwd normalised (`sum` where it had a residual).
+ *  mean, rstd    fp32 [N], as ln_fwd wrote them (mean NULL for FLCE_NORM_RMS).
+ *  grad_sum      [N, H] of `dtype` or NULL: the gradient that reaches `sum`
+ *                from elsewhere (the residual stream), added to grad_x.
+ *  grad_x        [N, H] of `dtype` output, or NULL to skip.
+ *  grad_weight, grad_bias  fp32 [H] outputs, or NULL to skip.
+ *  accumulate    0: grad_weight / grad_bias are overwritten; 1: added to.
+ *  workspace     >= ln_workspace_size(N, H) bytes, 256-byte aligned; contents
+ *                on entry are ignored.
+ *
+ * grad_x may be grad_y, grad_sum or x itself (same pointer and ld; with ld at
+ * least H).  The sums over rows run in an order that the sizes fix: the results
+ * are the same from run to run.
+ */
+flce_status_t ln_bwd(int kind, int dtype, const void* grad_y, int64_t ld_grad_y, const void* x,
+                     int64_t ld_x, const void* weight, int param_dtype, const float* mean,
+                     const float* rstd, const void* grad_sum, int64_t ld_grad_sum, int64_t N,
+                     int64_t H, void* grad_x, int64_t ld_grad_x, float* grad_weight,
+                     float* grad_bias, int accumulate, void* workspace, size_t workspace_bytes,
+                     flce_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The optimiser's step
+ * ------------------------------------------------------------------------
+ * The tables of tensors below are HOST memory and are read before the call
+ * returns; the pointers in them are device pointers.
+ */
+
+/* A tensor of n contiguous elements of `dtype` (BF16, FP16 or FP32). */
+typedef struct {
+  const void* data;
+  int64_t n;
+  int32_t dtype;
+  int32_t reserved; /* 0 */
+} flce_tensor_t;
+
+/* Bytes of workspace grad_norm needs for `count` tensors; 0 for count < 0. */
+size_t grad_norm_workspace_size(int64_t count);
+
+/*
+ * grad_norm -- the 2-norm of many gradients together, and the factor for the
+ * step that clips it:
+ *     out[0] = norm  = |grad_scale| * sqrt(sum of all squares)
+ *     out[1] = scale = grad_scale * min(1, max_norm / (norm + eps))
+ *  or NaN as scale where the norm is not finite (adamw_step can then skip the
+ *  step).  Squares are summed in fp32: a gradient above 1.8e19 in size makes
+ *  the norm infinite, and squares of gradients below 1e-19 lose bits.
+ *
+ *  tensors, count  `count` >= 0 tensors; n = 0 is allowed.
+ *  grad_scale      finite; what the gradients are to be multiplied by (1, or
+ *                  the inverse of a loss scale).
+ *  max_norm, eps   >= 0; max_norm infinity: no clipping.
+ *  out             fp32 [2], device.
+ *  workspace       >= grad_norm_workspace_size(count) bytes, 256-byte aligned;
+ *                  contents on entry are ignored.
+ *
+ * The sum's order is fixed by the sizes: the same result from run to run.
+ */
+flce_status_t grad_norm(const flce_tensor_t* tensors, int64_t count, float grad_scale,
+                        float max_norm, float eps, float* out, void* workspace,
+                        size_t workspace_bytes, flce_stream_t stream);
+
+/* Elements that share a scale in 8-bit moments. */
+#define FLCE_ADAMW_BLOCK 256
+
+/*
+ * One tensor of an AdamW step: n contiguous elements each.
+ *  moment_bits  32: exp_avg and exp_avg_sq are fp32 [n], the scales NULL.
+ *               8:  both are e4m3 numbers (1 byte) [n], and the scales fp32
+ *                   [ceil(n / FLCE_ADAMW_BLOCK)]; element i of exp_avg stands
+ *                   for number * scale[i / FLCE_ADAMW_BLOCK], element i of
+ *                   exp_avg_sq for the square of that.
+ *  copy         [n] of copy_dtype, or NULL: also gets the new parameter,
+ *               rounded (the 16-bit weight that the products read).
+ *  lr_scale     multiplies the step's lr for this tensor.
+ * param and grad may each be BF16, FP16 or FP32.  No tensor of a call overlaps
+ * another that the call writes.
+ */
+typedef struct {
+  void* param;
+  const void* grad;
+  void* exp_avg;
+  void* exp_avg_sq;
+  float* exp_avg_scale;
+  float* exp_avg_sq_scale;
+  void* copy;
+  int64_t n;
+  float lr_scale;
+  float weight_decay;
+  int32_t param_dtype, grad_dtype, copy_dtype, moment_bits;
+} flce_adamw_tensor_t;
+
+/*
+ * The step's numbers.
+ *  step            t >= 1, this step's number (the first is 1); step_dev, when
+ *                  not NULL, is a device int64 that holds it instead.
+ *  lr_dev          device fp32 that holds lr, or NULL.
+ *  grad_scale_dev  device fp32 that the gradients are multiplied by (out + 1 of
+ *                  grad_norm), or NULL: grad_scale is that factor then.
+ *  skip_nonfinite  1: when the factor is not finite, nothing is written.
+ *  stochastic      1: 8-bit moments are rounded stochastically, by bits that
+ *                  `seed`, the step, the tensor's place in the call's table
+ *                  and the element's place in the tensor fix; 0: to nearest.
+ */
+typedef struct {
+  double lr, beta1, beta2, eps;
+  int64_t step;
+  const int64_t* step_dev;
+  const float* lr_dev;
+  const float* grad_scale_dev;
+  float grad_scale;
+  int32_t skip_nonfinite;
+  int32_t stochastic;
+  int32_t reserved; /* 0 */
+  uint64_t seed;
+} flce_adamw_t;
+
+/*
+ * adamw_step -- one AdamW step (decoupled weight decay) over `count` tensors:
+ *     g = grad * factor
+ *     m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2
+ *     p = p (1 - lr weight_decay)
+ *         - lr / (1 - beta1^t) * m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+ * in fp32, with lr the step's times the tensor's lr_scale; p is rounded to its
+ * type once.  The update takes m and v before they are rounded to 8 bits.
+ *
+ * 8-bit moments: each block of FLCE_ADAMW_BLOCK elements (counted from the
+ * tensor's start) has scale = its largest |m| (or sqrt v) * (1 / 448), at least
+ * 2^-126 unless the block is 0, and holds m * (1 / scale) (or sqrt v) as e4m3
+ * numbers, each of these operations rounded to fp32.  A root that is not 0 is held as at least the smallest number,
+ * 2^-9, so that no step divides a moment by a root that was rounded to 0.  A
+ * moment that is not finite is held as NaN and leaves the rest of its block
+ * alone.
+ *
+ * betas in [0, 1), eps >= 0, lr finite.  Needs no workspace.
+ */
+flce_status_t adamw_step(const flce_adamw_tensor_t* tensors, int64_t count,
+                         const flce_adamw_t* numbers, flce_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * Diagnostics (no counterpart on the pages)
  * ------------------------------------------------------------------------ */
 
@@ -381,7 +582,12 @@ enum {
   FLCE_KERNEL_CE_ROWS = 6,
   FLCE_KERNEL_ZERO = 7,
   FLCE_KERNEL_BIAS_REDUCE = 8,
-  FLCE_KERNEL_GH_REDUCE = 9
+  FLCE_KERNEL_GH_REDUCE = 9,
+  FLCE_KERNEL_LN_FWD = 10,
+  FLCE_KERNEL_LN_BWD = 11,
+  FLCE_KERNEL_LN_REDUCE = 12,
+  FLCE_KERNEL_GRAD_NORM = 13,
+  FLCE_KERNEL_ADAMW = 14
 };
 const char* flce_kernel_name(int kernel_id);
 flce_status_t flce_profile_enable(int capacity);

@@ -7,6 +7,8 @@ address or ``None``.  ``fused_linear_cross_entropy`` and ``cross_entropy``
 add output / workspace allocation with torch and raise on an error status.
 Every step of the computation runs in the library's CUDA kernels; there is
 no fallback.  If the library has not been built, every call raises.
+``layer_norm``, ``layer_norm_backward``, ``grad_norm`` and ``AdamW`` are what a
+training step runs around the loss (``_training.py``).
 """
 from __future__ import annotations
 
@@ -22,6 +24,9 @@ __all__ = [
     "flce_set_wait_timeout_ns", "flce_selftest_wait_timeout", "flce_kernel_name",
     "flce_profile_enable", "flce_profile_disable", "flce_profile_read",
     "fused_linear_cross_entropy", "cross_entropy", "FlceError",
+    "NORM_KINDS", "ADAMW_BLOCK", "TensorEntry", "AdamWEntry", "AdamWNumbers", "ln_workspace_size", "ln_fwd", "ln_bwd",
+    "grad_norm_workspace_size", "grad_norm_raw", "adamw_step", "layer_norm", "layer_norm_backward", "grad_norm",
+    "AdamW",
 ]
 
 REDUCTIONS = {"none": 0, "sum": 1, "mean": 2}
@@ -29,7 +34,8 @@ DTYPES = {"bf16": 0, "fp32": 1, "fp16": 2, "fp32_rounded": 3}
 STATUS_BIT_TARGET_RANGE = 0x1
 STATUS_BIT_TIMEOUT = 0x2
 KERNEL_NAMES = ("count_targets", "gemm_forward", "row_finalize", "grad_logits", "gemm_backward",
-                "loss_reduce", "ce_rows", "zero", "bias_reduce", "gh_reduce")
+                "loss_reduce", "ce_rows", "zero", "bias_reduce", "gh_reduce", "ln_fwd", "ln_bwd", "ln_reduce",
+                "grad_norm", "adamw")
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "_lib", "libflce03.so")
@@ -62,6 +68,14 @@ _SIGNATURES = {
                                         ctypes.c_int, _P, _SZ, _P, _P]),
     "ce_vp_partials": (ctypes.c_int, [_P, ctypes.c_int, _P, _I64, _I64, _I64, _I64, _P, _P, _P, _P]),
     "ce_vp_backward": (ctypes.c_int, [_P, ctypes.c_int, _P, _P, _I64, _I64, _I64, _I64, _P, _P, _P, _P]),
+    "ln_workspace_size": (_SZ, [_I64, _I64]),
+    "ln_fwd": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, _P, _I64, _P, _I64, _P, _P, ctypes.c_int, _I64, _I64,
+                              ctypes.c_float, _P, _I64, _P, _I64, _P, _P, _P]),
+    "ln_bwd": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, _P, _I64, _P, _I64, _P, ctypes.c_int, _P, _P, _P, _I64,
+                              _I64, _I64, _P, _I64, _P, _P, ctypes.c_int, _P, _SZ, _P]),
+    "grad_norm_workspace_size": (_SZ, [_I64]),
+    "grad_norm": (ctypes.c_int, [_P, _I64, ctypes.c_float, ctypes.c_float, ctypes.c_float, _P, _P, _SZ, _P]),
+    "adamw_step": (ctypes.c_int, [_P, _I64, _P, _P]),
     "flce_set_wait_timeout_ns": (None, [ctypes.c_uint64]),
     "flce_selftest_wait_timeout": (ctypes.c_int, [_P, ctypes.c_uint64, _P]),
     "flce_kernel_name": (ctypes.c_char_p, [ctypes.c_int]),
@@ -352,3 +366,8 @@ def cross_entropy(logits, target, *, ignore_index: int = -100, reduction="mean",
                     workspace, ws_bytes, status, stream)
     _check(st, "ce_fwd_bwd")
     return dict(loss=loss if red == 0 else loss[0], grad_logits=grad, status=status)
+
+
+from ._training import (  # noqa: E402  (it uses the names above)
+    ADAMW_BLOCK, NORM_KINDS, AdamW, AdamWEntry, AdamWNumbers, TensorEntry, adamw_step, grad_norm, grad_norm_raw,
+    grad_norm_workspace_size, layer_norm, layer_norm_backward, ln_bwd, ln_fwd, ln_workspace_size)

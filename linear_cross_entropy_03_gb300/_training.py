@@ -1,0 +1,459 @@
+"""What a training step runs around the fused linear cross entropy: the norm in
+front of the head, the gradients' norm, and the optimiser's step.
+
+``ln_fwd``, ``ln_bwd``, ``grad_norm_raw`` and ``adamw_step`` marshal their
+arguments for the C entry points; ``layer_norm``, ``layer_norm_backward``,
+``grad_norm`` and ``AdamW`` take tensors, check them, allocate what is not given
+and raise on an error status.  Memory that a call allocates belongs to the
+stream that the call runs on; as with any torch operation, a tensor that was
+written on another stream has to be waited for by the caller.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+import math
+
+from . import FlceError, _check, _dt, _ptr, _stream, lib
+
+NORM_KINDS = {"layer": 0, "rms": 1}
+ADAMW_BLOCK = 256
+
+
+class TensorEntry(ctypes.Structure):
+    """flce_tensor_t"""
+    _fields_ = [("data", ctypes.c_void_p), ("n", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class AdamWEntry(ctypes.Structure):
+    """flce_adamw_tensor_t"""
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("exp_avg", ctypes.c_void_p),
+                ("exp_avg_sq", ctypes.c_void_p), ("exp_avg_scale", ctypes.c_void_p),
+                ("exp_avg_sq_scale", ctypes.c_void_p), ("copy", ctypes.c_void_p), ("n", ctypes.c_int64),
+                ("lr_scale", ctypes.c_float), ("weight_decay", ctypes.c_float), ("param_dtype", ctypes.c_int32),
+                ("grad_dtype", ctypes.c_int32), ("copy_dtype", ctypes.c_int32), ("moment_bits", ctypes.c_int32)]
+
+
+class AdamWNumbers(ctypes.Structure):
+    """flce_adamw_t"""
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("step", ctypes.c_int64), ("step_dev", ctypes.c_void_p),
+                ("lr_dev", ctypes.c_void_p), ("grad_scale_dev", ctypes.c_void_p), ("grad_scale", ctypes.c_float),
+                ("skip_nonfinite", ctypes.c_int32), ("stochastic", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("seed", ctypes.c_uint64)]
+
+
+# ------------------------------------------------------------------ raw ABI
+
+def _kind(kind) -> int:
+    return NORM_KINDS.get(kind, -1) if isinstance(kind, str) else int(kind)
+
+
+def ln_workspace_size(N: int, H: int) -> int:
+    return lib().ln_workspace_size(N, H)
+
+
+def ln_fwd(kind, dtype, x, ld_x, residual, ld_residual, weight, bias, param_dtype, N, H, eps, y, ld_y, sum, ld_sum,
+           mean, rstd, stream=None) -> int:
+    return lib().ln_fwd(_kind(kind), _dt(dtype), _ptr(x), ld_x, _ptr(residual), ld_residual, _ptr(weight), _ptr(bias),
+                        _dt(param_dtype), N, H, float(eps), _ptr(y), ld_y, _ptr(sum), ld_sum, _ptr(mean), _ptr(rstd),
+                        _stream(stream))
+
+
+def ln_bwd(kind, dtype, grad_y, ld_grad_y, x, ld_x, weight, param_dtype, mean, rstd, grad_sum, ld_grad_sum, N, H,
+           grad_x, ld_grad_x, grad_weight, grad_bias, accumulate, workspace, workspace_bytes, stream=None) -> int:
+    return lib().ln_bwd(_kind(kind), _dt(dtype), _ptr(grad_y), ld_grad_y, _ptr(x), ld_x, _ptr(weight),
+                        _dt(param_dtype), _ptr(mean), _ptr(rstd), _ptr(grad_sum), ld_grad_sum, N, H, _ptr(grad_x),
+                        ld_grad_x, _ptr(grad_weight), _ptr(grad_bias), int(accumulate), _ptr(workspace),
+                        int(workspace_bytes), _stream(stream))
+
+
+def grad_norm_workspace_size(count: int) -> int:
+    return lib().grad_norm_workspace_size(count)
+
+
+def grad_norm_raw(tensors, count, grad_scale, max_norm, eps, out, workspace, workspace_bytes, stream=None) -> int:
+    """The C entry point grad_norm; `tensors` is an array of TensorEntry."""
+    return lib().grad_norm(tensors, count, float(grad_scale), float(max_norm), float(eps), _ptr(out), _ptr(workspace),
+                           int(workspace_bytes), _stream(stream))
+
+
+def adamw_step(tensors, count, numbers, stream=None) -> int:
+    """The C entry point; `tensors` is an array of AdamWEntry, `numbers` an AdamWNumbers."""
+    return lib().adamw_step(tensors, count, None if numbers is None else ctypes.byref(numbers), _stream(stream))
+
+
+# ------------------------------------------------------------------ checks
+
+_codes = {}
+
+
+def _code(t, where) -> int:
+    """The dtype code of a tensor that has to be bf16, fp16 or fp32 on the current GPU."""
+    if not _codes:
+        import torch
+        _codes.update({torch.bfloat16: 0, torch.float32: 1, torch.float16: 2})
+    code = _codes.get(t.dtype)
+    if code is None:
+        raise FlceError(2, f"{where}: {t.dtype}")
+    return code
+
+
+def _here(t, where):
+    import torch
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise FlceError(1, f"{where}: on {t.device}, not on the current GPU")
+
+
+def _rows(t, where):
+    """(rows, columns, distance of rows) of a tensor whose last dimension is contiguous and whose
+    others, taken together, have one stride."""
+    h = t.shape[-1] if t.dim() else 0
+    if h < 1:
+        raise FlceError(1, f"{where}: shape {tuple(t.shape)}")
+    if t.is_contiguous():
+        return t.numel() // h, h, h
+    shape, stride = t.shape[:-1], t.stride()
+    if h > 1 and stride[-1] != 1:
+        raise FlceError(2, f"{where}: its last dimension is not contiguous")
+    n, ld = 1, 0
+    for size, step in zip(reversed(shape), reversed(stride[:-1])):
+        if size != 1:
+            if n > 1 and step != ld * n:
+                raise FlceError(2, f"{where}: its rows have no one stride")
+            n, ld = n * size, step if n == 1 else ld
+    return n, h, ld if n > 1 else h
+
+
+def _vector(t, h, where):
+    if t.dim() != 1 or t.shape[0] != h or not t.is_contiguous():
+        raise FlceError(1, f"{where}: a contiguous [{h}] is wanted, not {tuple(t.shape)}")
+    _here(t, where)
+    return t
+
+
+def _floats(t, n, where):
+    import torch
+    if t.dtype is not torch.float32 or t.numel() != n or not t.is_contiguous():
+        raise FlceError(1, f"{where}: a contiguous fp32 tensor of {n} elements is wanted")
+    _here(t, where)
+    return t
+
+
+def _like(t, x, where):
+    """Rows of a second matrix, which has to have the first's shape and type."""
+    if t.shape != x.shape or t.dtype != x.dtype:
+        raise FlceError(1, f"{where}: {tuple(t.shape)} {t.dtype}, and not {tuple(x.shape)} {x.dtype}")
+    _here(t, where)
+    return _rows(t, where)[2]
+
+
+def _on(stream):
+    """Makes `stream` torch's current one for a call, so that what it allocates is that stream's."""
+    if stream is None:
+        return contextlib.nullcontext()
+    import torch
+    return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+
+
+# ------------------------------------------------------------------ layer norm
+
+def layer_norm(x, weight=None, bias=None, *, kind="layer", eps: float = 1e-5, residual=None, out=None, sum_out=None,
+               row_stats: bool = True, stream=None) -> dict:
+    """Layer norm over the last dimension of x (+ residual), or with ``kind="rms"`` its form without the mean.
+
+    x [..., H] bf16, fp16 or fp32, its rows contiguous and one stride apart;
+    residual of its shape and type, added first; weight and bias [H], each or
+    both, of one of the three types.  Returns a dict with ``y``, ``sum`` (x +
+    residual in the type of x, or None without residual), ``mean`` (fp32, None
+    for rms) and ``rstd``, one a row (both None with ``row_stats=False``).
+    ``out`` and ``sum_out`` may be x or residual.
+    """
+    import torch
+    dtype = _code(x, "layer_norm: x")
+    _here(x, "layer_norm: x")
+    n, h, ld = _rows(x, "layer_norm: x")
+    code = _kind(kind)
+    ld_r = _like(residual, x, "layer_norm: residual") if residual is not None else 0
+    param = weight if weight is not None else bias
+    if weight is not None:
+        _vector(weight, h, "layer_norm: weight")
+    if bias is not None:
+        _vector(bias, h, "layer_norm: bias")
+        if bias.dtype != param.dtype:
+            raise FlceError(2, "layer_norm: weight and bias have different types")
+    param_dtype = _code(param, "layer_norm: weight") if param is not None else dtype
+    with _on(stream):
+        y = out if out is not None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        total = sum_out
+        if residual is not None and total is None:
+            total = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        rows = x.shape[:-1]
+        mean = torch.empty(rows, dtype=torch.float32, device=x.device) if row_stats and code == 0 else None
+        rstd = torch.empty(rows, dtype=torch.float32, device=x.device) if row_stats else None
+        ld_y = _like(out, x, "layer_norm: out") if out is not None else h
+        ld_s = _like(sum_out, x, "layer_norm: sum_out") if sum_out is not None else h
+        _check(ln_fwd(code, dtype, x, ld, residual, ld_r, weight, bias, param_dtype, n, h, eps, y, ld_y, total, ld_s,
+                      mean, rstd, stream), "ln_fwd")
+    return dict(y=y, sum=total, mean=mean, rstd=rstd)
+
+
+def layer_norm_backward(grad_y, x, weight=None, *, mean=None, rstd, kind="layer", grad_sum=None, grad_x: bool = True,
+                        grad_weight: bool = True, grad_bias: bool = True, out=None, grad_weight_out=None,
+                        grad_bias_out=None, accumulate: bool = False, workspace=None, stream=None) -> dict:
+    """Gradients of layer_norm.
+
+    x is what was normalised (``sum`` where there was a residual), mean and rstd
+    are layer_norm's; ``grad_sum`` is the gradient that reaches ``sum`` from
+    elsewhere.  Returns a dict with ``grad_x`` (the residual's gradient too),
+    ``grad_weight`` and ``grad_bias`` (fp32 [H]; None where switched off).
+    ``accumulate`` adds to ``grad_weight_out`` and ``grad_bias_out``.  ``out``
+    may be grad_y, grad_sum or x.
+    """
+    import torch
+    dtype = _code(x, "layer_norm_backward: x")
+    _here(x, "layer_norm_backward: x")
+    n, h, ld = _rows(x, "layer_norm_backward: x")
+    ld_g = _like(grad_y, x, "layer_norm_backward: grad_y")
+    code = _kind(kind)
+    if weight is not None:
+        _vector(weight, h, "layer_norm_backward: weight")
+    param_dtype = _code(weight, "layer_norm_backward: weight") if weight is not None else dtype
+    if mean is not None:
+        _floats(mean, n, "layer_norm_backward: mean")
+    _floats(rstd, n, "layer_norm_backward: rstd")
+    ld_s = _like(grad_sum, x, "layer_norm_backward: grad_sum") if grad_sum is not None else 0
+    want_w = grad_weight or grad_weight_out is not None
+    want_b = grad_bias or grad_bias_out is not None
+    if accumulate and ((want_w and grad_weight_out is None) or (want_b and grad_bias_out is None)):
+        raise FlceError(1, "layer_norm_backward: accumulate adds to grad_weight_out and grad_bias_out")
+    if out is not None:
+        grad_x = True
+    ld_x = _like(out, x, "layer_norm_backward: out") if out is not None else h
+    with _on(stream):
+        gx = out if out is not None else (
+            torch.empty(x.shape, dtype=x.dtype, device=x.device) if grad_x else None)
+        gw, gb = grad_weight_out, grad_bias_out
+        if gw is not None:
+            _floats(gw, h, "layer_norm_backward: grad_weight_out")
+        elif want_w:
+            gw = torch.empty(h, dtype=torch.float32, device=x.device)
+        if gb is not None:
+            _floats(gb, h, "layer_norm_backward: grad_bias_out")
+        elif want_b:
+            gb = torch.empty(h, dtype=torch.float32, device=x.device)
+        size = ln_workspace_size(n, h)
+        if size == 0:
+            raise FlceError(1, "ln_workspace_size")
+        if workspace is None or workspace.numel() * workspace.element_size() < size:
+            workspace = torch.empty(size, dtype=torch.uint8, device=x.device)
+        _check(ln_bwd(code, dtype, grad_y, ld_g, x, ld, weight, param_dtype, mean, rstd, grad_sum, ld_s, n, h, gx, ld_x,
+                      gw, gb, accumulate, workspace, size, stream), "ln_bwd")
+    return dict(grad_x=gx, grad_weight=gw, grad_bias=gb)
+
+
+# ------------------------------------------------------------------ optimiser
+
+def _flat(t, where):
+    """A dense tensor in any order of its dimensions is taken as its elements lie in memory."""
+    if t.is_contiguous():
+        return t.numel()
+    raise FlceError(2, f"{where}: not contiguous")
+
+
+def grad_norm(grads, *, max_norm=None, grad_scale: float = 1.0, eps: float = 1e-6, out=None, workspace=None,
+              stream=None) -> dict:
+    """The 2-norm of all of ``grads`` together, times ``grad_scale``, and the factor that clips it to ``max_norm``.
+
+    Returns ``norm`` and ``scale``, one fp32 element each on the device: scale =
+    grad_scale * min(1, max_norm / (norm + eps)), or NaN where the norm is not
+    finite.  ``AdamW.step`` takes ``scale`` as it is, so nothing waits for the
+    host.  Gradients may be bf16, fp16 or fp32 in any mixture; None is passed
+    over.
+    """
+    import torch
+    grads = [g for g in grads if g is not None]
+    table = (TensorEntry * len(grads))()
+    for entry, g in zip(table, grads):
+        entry.dtype = _code(g, "grad_norm")
+        _here(g, "grad_norm")
+        entry.n = _flat(g, "grad_norm")
+        entry.data = g.data_ptr()
+    size = grad_norm_workspace_size(len(grads))
+    with _on(stream):
+        if out is None:
+            out = torch.empty(2, dtype=torch.float32, device="cuda")
+        _floats(out, 2, "grad_norm: out")
+        if workspace is None or workspace.numel() * workspace.element_size() < size:
+            workspace = torch.empty(size, dtype=torch.uint8, device="cuda")
+        _check(grad_norm_raw(table, len(grads), grad_scale, math.inf if max_norm is None else max_norm, eps, out,
+                             workspace, size, stream), "grad_norm")
+    return dict(norm=out[0], scale=out[1])
+
+
+def _each(value, count, where):
+    """A number for every tensor, from one or from a sequence."""
+    if isinstance(value, (int, float)):
+        return [float(value)] * count
+    value = [float(v) for v in value]
+    if len(value) != count:
+        raise FlceError(1, f"{where}: {len(value)} numbers for {count} tensors")
+    return value
+
+
+class AdamW:
+    """AdamW over many tensors at once, with decoupled weight decay.
+
+    params        contiguous bf16, fp16 or fp32 tensors, updated in place.
+    weight_decay, lr_scale  one number, or one for each tensor.
+    moments       "fp32", or "8bit": e4m3 numbers with an fp32 scale for each
+                  block of 256; tensors below ``min_8bit_size`` elements keep
+                  fp32 moments.
+    seed          rounds 8-bit moments stochastically, so that changes smaller
+                  than a number's spacing are kept on average; None: to nearest.
+    copies        for each tensor another of its size that gets the rounded new
+                  parameter (the 16-bit weight that products read), or None.
+    state, step   moments and the number of steps already taken, from
+                  ``state_dict()``; without them the moments start at 0.
+    capturable    keeps the step's number on the device, so that ``step`` can be
+                  captured in a graph and replayed.
+    """
+
+    def __init__(self, params, *, lr: float, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay=0.01, lr_scale=1.0,
+                 moments: str = "fp32", min_8bit_size: int = 4096, copies=None, seed=None, state=None, step=None,
+                 capturable: bool = False):
+        import torch
+        self.params = list(params)
+        count = len(self.params)
+        if moments not in ("fp32", "8bit"):
+            raise FlceError(1, f"AdamW: moments {moments!r}")
+        if not (0 <= betas[0] < 1 and 0 <= betas[1] < 1) or not 0 <= eps < math.inf or not math.isfinite(lr):
+            raise FlceError(1, "AdamW: betas lie in [0, 1), eps is at least 0 and lr finite")
+        if seed is not None and not 0 <= seed < 1 << 64:
+            raise FlceError(1, "AdamW: seed is a whole number of 64 bits")
+        decay, scale = _each(weight_decay, count, "AdamW: weight_decay"), _each(lr_scale, count, "AdamW: lr_scale")
+        copies = [None] * count if copies is None else list(copies)
+        if len(copies) != count:
+            raise FlceError(1, f"AdamW: {len(copies)} copies for {count} tensors")
+        self.lr, self.copies = lr, copies
+        names = ("exp_avg", "exp_avg_sq", "exp_avg_scale", "exp_avg_sq_scale")
+        if state is not None:
+            given = [list(state.get(k) or [None] * count) for k in names]
+            if any(len(v) != count for v in given):
+                raise FlceError(1, f"AdamW: state of another number of tensors than {count}")
+            step = state.get("step", 0) if step is None else step
+        else:
+            given = [[None] * count for _ in names]
+        step = 0 if step is None else int(step)
+        if step < 0:
+            raise FlceError(1, "AdamW: a negative step")
+        self._table = (AdamWEntry * count)()
+        self._numel = []
+        memory = []
+        for i, p in enumerate(self.params):
+            e, where = self._table[i], f"AdamW: tensor {i}"
+            e.param_dtype, n = _code(p, where), _flat(p, where)
+            _here(p, where)
+            m, v, ms, vs = (x[i] for x in given)
+            if state is None:
+                small = moments == "8bit" and n >= min_8bit_size
+                kind = torch.float8_e4m3fn if small else torch.float32
+                m, v = (torch.zeros(p.shape, dtype=kind, device=p.device) for _ in range(2))
+                if small:
+                    ms, vs = (torch.zeros(-(-n // ADAMW_BLOCK), device=p.device) for _ in range(2))
+            e.moment_bits = self._state_bits(m, v, ms, vs, n, where)
+            c = copies[i]
+            if c is not None:
+                e.copy_dtype = _code(c, where + ", copy")
+                _here(c, where + ", copy")
+                if _flat(c, where + ", copy") != n:
+                    raise FlceError(1, f"{where}: its copy has another size")
+            for x, t in zip(given, (m, v, ms, vs)):
+                x[i] = t
+            e.param, e.exp_avg, e.exp_avg_sq, e.exp_avg_scale, e.exp_avg_sq_scale, e.copy = (
+                _ptr(t) for t in (p, m, v, ms, vs, c))
+            e.n, e.weight_decay, e.lr_scale = n, decay[i], scale[i]
+            self._numel.append(n)
+            memory += [(t.data_ptr(), t.numel() * t.element_size(), i) for t in (p, m, v, ms, vs, c) if t is not None]
+        memory = sorted(x for x in memory if x[1])
+        for (start, size, i), (after, _, k) in zip(memory, memory[1:]):
+            if start + size > after:
+                raise FlceError(1, f"AdamW: tensors {i} and {k} share memory")
+        self.exp_avg, self.exp_avg_sq, self.exp_avg_scale, self.exp_avg_sq_scale = given
+        self._numbers = AdamWNumbers(beta1=betas[0], beta2=betas[1], eps=eps, stochastic=int(seed is not None),
+                                     seed=seed or 0)
+        self._steps = step
+        self._step_dev = torch.full((1,), step, dtype=torch.int64, device="cuda") if capturable else None
+
+    @staticmethod
+    def _state_bits(m, v, ms, vs, n, where):
+        import torch
+        for t in (m, v):
+            if t is None or t.dtype not in (torch.float32, torch.float8_e4m3fn) or t.dtype != m.dtype:
+                raise FlceError(2, f"{where}: moments are both fp32 or both float8_e4m3fn")
+            _here(t, where + ", moments")
+            if _flat(t, where + ", moments") != n:
+                raise FlceError(1, f"{where}: moments of another size")
+        scaled = m.dtype is torch.float8_e4m3fn
+        if (ms is not None) != scaled or (vs is not None) != scaled:
+            raise FlceError(1, f"{where}: 8-bit moments come with scales, and fp32 ones without")
+        if scaled:
+            _floats(ms, -(-n // ADAMW_BLOCK), where + ", exp_avg_scale")
+            _floats(vs, -(-n // ADAMW_BLOCK), where + ", exp_avg_sq_scale")
+        return 8 if scaled else 32
+
+    @property
+    def steps(self) -> int:
+        """Steps taken; with ``capturable`` this reads the device and waits for it."""
+        return self._steps if self._step_dev is None else int(self._step_dev.item())
+
+    def state_dict(self) -> dict:
+        """The moments (the tensors themselves) and the number of steps: what ``state`` takes."""
+        return dict(step=self.steps, exp_avg=self.exp_avg, exp_avg_sq=self.exp_avg_sq,
+                    exp_avg_scale=self.exp_avg_scale, exp_avg_sq_scale=self.exp_avg_sq_scale)
+
+    def step(self, grads, *, lr=None, grad_scale=None, skip_nonfinite: bool = False, stream=None) -> None:
+        """One step.  ``grads``: a contiguous tensor of each parameter's size, or None to leave it out.
+
+        lr           a number (default: the constructor's) or a device fp32 element.
+        grad_scale   what the gradients are multiplied by: a number or a device
+                     fp32 element, as ``grad_norm`` leaves it.
+        skip_nonfinite  writes nothing when that factor is not finite.  Such a
+                     step does not count, unless the factor lies on the device
+                     and the step's number does not (``capturable``): the host
+                     cannot know then.
+        """
+        import torch
+        if len(grads) != len(self.params):
+            raise FlceError(1, f"AdamW.step: {len(grads)} gradients for {len(self.params)} tensors")
+        here = torch.cuda.current_device()
+        for entry, n, g in zip(self._table, self._numel, grads):
+            if g is None:
+                entry.n = 0
+                continue
+            entry.grad_dtype = _code(g, "AdamW.step")
+            if g.get_device() != here or not g.is_contiguous() or g.numel() != n:
+                raise FlceError(1, f"AdamW.step: a gradient is no contiguous tensor of {n} elements on the current GPU")
+            entry.grad = g.data_ptr()
+            entry.n = n
+        k = self._numbers
+        lr = self.lr if lr is None else lr
+        k.lr, k.lr_dev = (0.0, _floats(lr, 1, "AdamW.step: lr").data_ptr()) if isinstance(lr, torch.Tensor) else (lr, None)
+        factor = None
+        if isinstance(grad_scale, torch.Tensor):
+            factor = _floats(grad_scale, 1, "AdamW.step: grad_scale")
+        elif skip_nonfinite and grad_scale is not None and not math.isfinite(grad_scale):
+            return
+        k.grad_scale = 1.0 if grad_scale is None or factor is not None else grad_scale
+        k.grad_scale_dev = _ptr(factor)
+        k.skip_nonfinite = int(skip_nonfinite)
+        k.step, k.step_dev = self._steps + 1, _ptr(self._step_dev)
+        with _on(stream):
+            if self._step_dev is not None:
+                if skip_nonfinite and factor is not None:
+                    self._step_dev.add_(torch.isfinite(factor).view(1))
+                else:
+                    self._step_dev.add_(1)
+            _check(adamw_step(self._table, len(self.params), k, stream), "adamw_step")
+        self._steps += 1

@@ -796,6 +796,11 @@ const char* flce_kernel_name(int id) {
     case FLCE_KERNEL_ZERO: return "zero";
     case FLCE_KERNEL_BIAS_REDUCE: return "bias_reduce";
     case FLCE_KERNEL_GH_REDUCE: return "gh_reduce";
+    case FLCE_KERNEL_LN_FWD: return "ln_fwd";
+    case FLCE_KERNEL_LN_BWD: return "ln_bwd";
+    case FLCE_KERNEL_LN_REDUCE: return "ln_reduce";
+    case FLCE_KERNEL_GRAD_NORM: return "grad_norm";
+    case FLCE_KERNEL_ADAMW: return "adamw";
   }
   return "unknown";
 }

@@ -1,0 +1,460 @@
+// The optimiser's step over many tensors at once: the 2-norm of all gradients
+// with the factor that clips it, and AdamW with moments in fp32 or in 8 bits.
+//
+// The tables of tensors travel as kernel parameters (up to 32 KB), so a call
+// copies nothing to the device and can be captured in a graph.  Every element
+// is read and written once with a few dozen operations on it: memory bandwidth
+// bounds both.
+#include <cuda_fp8.h>
+#include <math.h>
+
+#include <algorithm>
+
+#include "elem.cuh"
+#include "ptx.cuh"
+
+namespace flce {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int64_t kMaxElems = int64_t(1) << 46;  // of one tensor
+
+// Entries are ordered by first chunk: the one that holds chunk c.
+template <typename E>
+__device__ __forceinline__ int entry_of(const E* entry, int count, unsigned int c) {
+  int lo = 0, hi = count - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (entry[mid].chunk0 <= c)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  return lo;
+}
+
+// ------------------------------------------------------------ gradient norm
+
+constexpr int kNormChunk = 16384;  // elements a CTA takes at a time
+constexpr int kNormParts = 608;    // most CTAs, and partial sums, of a launch
+
+struct NormEntry {
+  const void* data;
+  int64_t n;
+  unsigned int chunk0;
+  int dtype;
+};
+
+constexpr int kNormEntries = 1280;
+struct NormArgs {
+  NormEntry entry[kNormEntries];
+  int count;
+  unsigned int chunks;
+  float* part;  // [gridDim.x]
+};
+
+// Partial sums of squares: CTA b takes chunks b, b + gridDim.x, ...
+__global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_constant__ NormArgs a) {
+  __shared__ float scratch[kThreads / 32];
+  float sum = 0.f;
+  for (unsigned int c = blockIdx.x; c < a.chunks; c += gridDim.x) {
+    const NormEntry& e = a.entry[entry_of(a.entry, a.count, c)];
+    const int64_t i0 = static_cast<int64_t>(c - e.chunk0) * kNormChunk;
+    const int64_t i1 = min(i0 + kNormChunk, e.n);
+    for (int64_t i = i0 + threadIdx.x; i < i1; i += kThreads) {
+      const float g = load_elem(e.data, e.dtype, i);
+      sum += g * g;
+    }
+  }
+  sum = warp_sum(sum);
+  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    float t = 0.f;
+    for (int k = 0; k < kThreads / 32; ++k) t += scratch[k];
+    a.part[blockIdx.x] = t;
+  }
+}
+
+// Adds the partial sums in a fixed order and forms the norm and the factor.
+__global__ void __launch_bounds__(1024)
+    grad_norm_finish_kernel(const float* part, int parts, float grad_scale, float max_norm, float eps, float* out) {
+  __shared__ float scratch[32];
+  grid_dependency_wait();
+  float sum = 0.f;
+  for (int k = threadIdx.x; k < parts; k += 1024) sum += part[k];
+  sum = warp_sum(sum);
+  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = sum;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    sum = warp_sum(scratch[threadIdx.x]);
+    if (threadIdx.x == 0) {
+      const float norm = sqrtf(sum) * fabsf(grad_scale);
+      out[0] = norm;
+      out[1] = isfinite(norm) ? grad_scale * fminf(1.f, max_norm / (norm + eps)) : __int_as_float(0x7FFFFFFF);
+    }
+  }
+}
+
+// -------------------------------------------------------------------- AdamW
+
+constexpr int kAdamChunk = 4096;  // elements of a CTA: a whole number of 8-bit blocks
+static_assert(kAdamChunk % (FLCE_ADAMW_BLOCK * (kThreads / 32)) == 0, "whole blocks for every warp");
+constexpr float kE4m3Max = 448.f, kE4m3MinNormal = 0x1p-6f;
+constexpr unsigned int kE4m3Nan = 0x7Fu;
+
+struct AdamEntry {
+  void* param;
+  const void* grad;
+  void *m, *v;
+  float *m_scale, *v_scale;
+  void* copy;
+  int64_t n;
+  float lr_scale, decay;
+  unsigned int chunk0;
+  int index;  // place in the call's table
+  int8_t param_dtype, grad_dtype, copy_dtype, bits;
+};
+
+struct AdamNumbers {
+  const int64_t* step_dev;
+  const float* lr_dev;
+  const float* grad_scale_dev;
+  int64_t step;
+  float lr, b1, c1, b2, c2, eps;     // c = 1 - b
+  float rate, correction;            // 1 / (1 - b1^t), 1 / sqrt(1 - b2^t) when the step is known here
+  float log_b1, log_b2;              // for them otherwise
+  float grad_scale;
+  int skip_nonfinite, stochastic;
+  unsigned int seed_lo, seed_hi;
+};
+
+template <int MAX>
+struct AdamArgs {
+  AdamEntry entry[MAX];
+  int count;
+  AdamNumbers num;
+};
+
+// 32 bits to 32 bits: two multiplications between shifted exclusive ors.  Every
+// output bit flips with probability 0.5 +- 0.005 when any input bit does.
+__device__ __forceinline__ unsigned int mix(unsigned int x) {
+  x = (x ^ (x >> 16)) * 0xA54D2F6Bu;
+  x = (x ^ (x >> 15)) * 0xD1B54A33u;
+  return x ^ (x >> 16);
+}
+
+// One element's new moments.  The products and sums round one by one (no
+// contraction), as the formulas read: what is then rounded to 8 bits does not
+// depend on how the compiler fuses them.
+__device__ __forceinline__ void moments(const AdamNumbers& k, float g, float& m, float& v) {
+  m = __fadd_rn(__fmul_rn(m, k.b1), __fmul_rn(g, k.c1));
+  v = __fadd_rn(__fmul_rn(v, k.b2), __fmul_rn(__fmul_rn(g, g), k.c2));
+}
+
+__device__ __forceinline__ float updated(float p, float keep, float rate, float correction, float eps, float m,
+                                         float root) {
+  return p * keep - m / (root * correction + eps) * rate;
+}
+
+// |x| <= 448 as an e4m3 number: to nearest, or stochastically by 16 bits.
+// The normal numbers have three bits of mantissa, so fp32 loses its lower 20:
+// adding random bits below them and cutting off rounds up with the probability
+// of what is cut off.  Below 2^-6 the spacing stays 2^-9: there 2^-6 is added
+// first, which gives the sum that spacing.
+__device__ __forceinline__ unsigned int to_e4m3(float x, bool stochastic, unsigned int bits16) {
+  if (stochastic) {
+    const float a = fminf(fabsf(x), kE4m3Max);
+    const float lift = a < kE4m3MinNormal ? kE4m3MinNormal : 0.f;
+    const unsigned int r = (__float_as_uint(a + lift) + (bits16 << 4)) & ~0xFFFFFu;
+    x = copysignf(fminf(__uint_as_float(r) - lift, kE4m3Max), x);
+  }
+  return __nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3);
+}
+
+__device__ __forceinline__ float from_e4m3(unsigned int code) {
+  return __half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(code), __NV_E4M3)));
+}
+
+// A block's scale from its largest finite magnitude, and what divides by it.
+__device__ __forceinline__ float block_scale(float largest, float* inverse) {
+  float s = __fmul_rn(largest, 1.f / kE4m3Max);
+  if (largest > 0.f) s = fmaxf(s, 0x1p-126f);
+  *inverse = s > 0.f ? __frcp_rn(s) : 0.f;
+  return s;
+}
+
+// The largest of the warp's non-negative finite numbers, which order like their bits.
+__device__ __forceinline__ float warp_max_bits(float v) {
+  return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
+}
+
+__device__ __forceinline__ float finite_abs(float x) {
+  const float a = fabsf(x);
+  return a <= 3.402823466e38f ? a : 0.f;
+}
+
+template <int MAX>
+__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ AdamArgs<MAX> a) {
+  const AdamEntry& e = a.entry[entry_of(a.entry, a.count, blockIdx.x)];
+  const AdamNumbers& k = a.num;
+  const float factor = k.grad_scale_dev != nullptr ? *k.grad_scale_dev : k.grad_scale;
+  if (k.skip_nonfinite && !isfinite(factor)) return;
+  const float lr = (k.lr_dev != nullptr ? *k.lr_dev : k.lr) * e.lr_scale;
+  float rate = k.rate, correction = k.correction;
+  int64_t step = k.step;
+  if (k.step_dev != nullptr) {  // 1 - b^t = -(e^(t ln b) - 1), without the cancellation
+    step = *k.step_dev;
+    rate = 1.f / -expm1f(static_cast<float>(step) * k.log_b1);
+    correction = rsqrtf(-expm1f(static_cast<float>(step) * k.log_b2));
+  }
+  rate *= lr;
+  const float keep = 1.f - lr * e.decay;
+  const int64_t i0 = static_cast<int64_t>(blockIdx.x - e.chunk0) * kAdamChunk;
+  const int64_t i1 = min(i0 + kAdamChunk, e.n);
+
+  if (e.bits == 32) {
+    float* mp = static_cast<float*>(e.m);
+    float* vp = static_cast<float*>(e.v);
+    for (int64_t i = i0 + threadIdx.x; i < i1; i += kThreads) {
+      float m = mp[i], v = vp[i];
+      moments(k, load_elem(e.grad, e.grad_dtype, i) * factor, m, v);
+      const float p =
+          updated(load_elem(e.param, e.param_dtype, i), keep, rate, correction, k.eps, m, __fsqrt_rn(v));
+      mp[i] = m;
+      vp[i] = v;
+      store_elem(e.param, e.param_dtype, i, p);
+      if (e.copy != nullptr) store_elem(e.copy, e.copy_dtype, i, p);
+    }
+    return;
+  }
+
+  // 8-bit moments: a warp takes a block, lane l its elements l, l + 32, ...
+  constexpr int kPer = FLCE_ADAMW_BLOCK / 32;
+  unsigned int key = 0;
+  if (k.stochastic) {
+    key = mix(k.seed_lo);
+    key = mix(key ^ k.seed_hi);
+    key = mix(key ^ static_cast<unsigned int>(step));
+    key = mix(key ^ static_cast<unsigned int>(e.index));
+  }
+  uint8_t* mp = static_cast<uint8_t*>(e.m);
+  uint8_t* vp = static_cast<uint8_t*>(e.v);
+  const int lane = threadIdx.x & 31;
+  for (int64_t b0 = i0 + (threadIdx.x >> 5) * FLCE_ADAMW_BLOCK; b0 < i1; b0 += kThreads / 32 * FLCE_ADAMW_BLOCK) {
+    const int64_t block = b0 / FLCE_ADAMW_BLOCK;
+    const float ms = e.m_scale[block], vs = e.v_scale[block];
+    float m[kPer], r[kPer];
+    float m_largest = 0.f, r_largest = 0.f;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int64_t i = b0 + j * 32 + lane;
+      m[j] = r[j] = 0.f;
+      if (i < e.n) {
+        m[j] = from_e4m3(mp[i]) * ms;
+        const float root = from_e4m3(vp[i]) * vs;
+        float v = __fmul_rn(root, root);
+        moments(k, load_elem(e.grad, e.grad_dtype, i) * factor, m[j], v);
+        r[j] = __fsqrt_rn(v);
+        const float p = updated(load_elem(e.param, e.param_dtype, i), keep, rate, correction, k.eps, m[j], r[j]);
+        store_elem(e.param, e.param_dtype, i, p);
+        if (e.copy != nullptr) store_elem(e.copy, e.copy_dtype, i, p);
+      }
+      m_largest = fmaxf(m_largest, finite_abs(m[j]));
+      r_largest = fmaxf(r_largest, finite_abs(r[j]));
+    }
+    float m_inv, r_inv;
+    const float m_scale = block_scale(warp_max_bits(m_largest), &m_inv);
+    const float r_scale = block_scale(warp_max_bits(r_largest), &r_inv);
+    const unsigned int key_hi = mix(key ^ static_cast<unsigned int>(static_cast<uint64_t>(b0) >> 32));
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int64_t i = b0 + j * 32 + lane;
+      if (i >= e.n) break;
+      const unsigned int bits = k.stochastic ? mix(static_cast<unsigned int>(i) ^ key_hi) : 0u;
+      unsigned int mc = to_e4m3(__fmul_rn(m[j], m_inv), k.stochastic, bits >> 16);
+      unsigned int rc = to_e4m3(__fmul_rn(r[j], r_inv), k.stochastic, bits & 0xFFFFu);
+      if (rc == 0u && r[j] > 0.f) rc = 1u;  // the smallest number, 2^-9
+      if (!isfinite(m[j])) mc = kE4m3Nan;
+      if (!isfinite(r[j])) rc = kE4m3Nan;
+      mp[i] = static_cast<uint8_t>(mc);
+      vp[i] = static_cast<uint8_t>(rc);
+    }
+    if (lane == 0) {
+      e.m_scale[block] = m_scale;
+      e.v_scale[block] = r_scale;
+    }
+  }
+}
+
+template <int MAX>
+cudaError_t launch_adamw(const AdamEntry* entry, int count, unsigned int chunks, const AdamNumbers& num,
+                         cudaStream_t s) {
+  AdamArgs<MAX> a;
+  std::copy(entry, entry + count, a.entry);
+  a.count = count;
+  a.num = num;
+  prof_begin(s, FLCE_KERNEL_ADAMW);
+  adamw_kernel<MAX><<<chunks, kThreads, 0, s>>>(a);
+  const cudaError_t e = cudaGetLastError();
+  prof_end(s);
+  return e;
+}
+
+// Tables of three sizes: a launch copies its whole parameter block.
+constexpr int kAdamEntries = 360, kAdamMiddle = 40, kAdamFew = 4;
+static_assert(sizeof(AdamArgs<kAdamEntries>) <= 32764, "kernel parameters");
+static_assert(sizeof(NormArgs) <= 32764, "kernel parameters");
+
+cudaError_t launch_adamw_any(const AdamEntry* entry, int count, unsigned int chunks, const AdamNumbers& num,
+                             cudaStream_t s) {
+  if (count <= kAdamFew) return launch_adamw<kAdamFew>(entry, count, chunks, num, s);
+  if (count <= kAdamMiddle) return launch_adamw<kAdamMiddle>(entry, count, chunks, num, s);
+  return launch_adamw<kAdamEntries>(entry, count, chunks, num, s);
+}
+
+size_t norm_workspace(int64_t count) {
+  return align_up(static_cast<size_t>(std::max<int64_t>(1, div_up(count, kNormEntries))) * kNormParts * 4, 256);
+}
+
+flce_status_t check_tensor(const flce_adamw_tensor_t& t) {
+  if (t.n < 0 || t.n > kMaxElems) return FLCE_ERR_INVALID_ARG;
+  if (!float_dtype(t.param_dtype) || !float_dtype(t.grad_dtype) || (t.copy != nullptr && !float_dtype(t.copy_dtype)))
+    return FLCE_ERR_UNSUPPORTED;
+  if (t.moment_bits != 8 && t.moment_bits != 32) return FLCE_ERR_UNSUPPORTED;
+  if (!isfinite(t.lr_scale) || !isfinite(t.weight_decay)) return FLCE_ERR_INVALID_ARG;
+  if (t.n == 0) return FLCE_OK;
+  if (t.param == nullptr || t.grad == nullptr || t.exp_avg == nullptr || t.exp_avg_sq == nullptr)
+    return FLCE_ERR_INVALID_ARG;
+  const bool scaled = t.moment_bits == 8;
+  if (scaled != (t.exp_avg_scale != nullptr) || scaled != (t.exp_avg_sq_scale != nullptr)) return FLCE_ERR_INVALID_ARG;
+  const size_t state = scaled ? 1 : 4;
+  if (!aligned_to(t.param, elem_size(t.param_dtype)) || !aligned_to(t.grad, elem_size(t.grad_dtype)) ||
+      (t.copy != nullptr && !aligned_to(t.copy, elem_size(t.copy_dtype))) || !aligned_to(t.exp_avg, state) ||
+      !aligned_to(t.exp_avg_sq, state) || !aligned_to(t.exp_avg_scale, 4) || !aligned_to(t.exp_avg_sq_scale, 4))
+    return FLCE_ERR_MISALIGNED;
+  return FLCE_OK;
+}
+
+}  // namespace
+}  // namespace flce
+
+using namespace flce;
+
+extern "C" {
+
+size_t grad_norm_workspace_size(int64_t count) { return count < 0 ? 0 : norm_workspace(count); }
+
+flce_status_t grad_norm(const flce_tensor_t* tensors, int64_t count, float grad_scale, float max_norm, float eps,
+                        float* out, void* workspace, size_t workspace_bytes, flce_stream_t stream_) {
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream_);
+  if (count < 0 || (count > 0 && tensors == nullptr) || out == nullptr) return FLCE_ERR_INVALID_ARG;
+  if (!isfinite(grad_scale) || !(max_norm >= 0.f) || !(eps >= 0.f) || isinf(eps)) return FLCE_ERR_INVALID_ARG;
+  for (int64_t i = 0; i < count; ++i) {
+    const flce_tensor_t& t = tensors[i];
+    if (t.n < 0 || t.n > kMaxElems || (t.n > 0 && t.data == nullptr)) return FLCE_ERR_INVALID_ARG;
+    if (!float_dtype(t.dtype)) return FLCE_ERR_UNSUPPORTED;
+    if (!aligned_to(t.data, elem_size(t.dtype))) return FLCE_ERR_MISALIGNED;
+  }
+  if (!aligned_to(out, 4)) return FLCE_ERR_MISALIGNED;
+  if (workspace == nullptr || !aligned_to(workspace, 256) || workspace_bytes < norm_workspace(count))
+    return FLCE_ERR_WORKSPACE;
+  float* part = static_cast<float*>(workspace);
+  const int most = std::min(kNormParts, 4 * device_sm_count());
+  int parts = 0;
+  NormArgs a;
+  for (int64_t i = 0; i < count;) {
+    int64_t chunks = 0;
+    a.count = 0;
+    for (; i < count && a.count < kNormEntries; ++i) {
+      if (tensors[i].n == 0) continue;
+      const int64_t more = div_up(tensors[i].n, kNormChunk);
+      if (chunks + more > 0x7fffffff) {
+        if (a.count == 0) return FLCE_ERR_UNSUPPORTED;
+        break;
+      }
+      a.entry[a.count++] = {tensors[i].data, tensors[i].n, static_cast<unsigned int>(chunks), tensors[i].dtype};
+      chunks += more;
+    }
+    if (a.count == 0) break;
+    a.chunks = static_cast<unsigned int>(chunks);
+    a.part = part + parts;
+    const int grid = static_cast<int>(std::min<int64_t>(chunks, most));
+    prof_begin(s, FLCE_KERNEL_GRAD_NORM);
+    grad_norm_kernel<<<grid, kThreads, 0, s>>>(a);
+    const cudaError_t e = cudaGetLastError();
+    prof_end(s);
+    if (e != cudaSuccess) return FLCE_ERR_CUDA;
+    parts += grid;
+  }
+  prof_begin(s, FLCE_KERNEL_GRAD_NORM);
+  grad_norm_finish_kernel<<<1, 1024, 0, s>>>(part, parts, grad_scale, max_norm, eps, out);
+  const cudaError_t e = cudaGetLastError();
+  prof_end(s);
+  return e == cudaSuccess ? FLCE_OK : FLCE_ERR_CUDA;
+}
+
+flce_status_t adamw_step(const flce_adamw_tensor_t* tensors, int64_t count, const flce_adamw_t* numbers,
+                         flce_stream_t stream_) {
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream_);
+  if (numbers == nullptr || count < 0 || count > 0x7fffffff || (count > 0 && tensors == nullptr))
+    return FLCE_ERR_INVALID_ARG;
+  const flce_adamw_t& u = *numbers;
+  if (!(u.beta1 >= 0 && u.beta1 < 1 && u.beta2 >= 0 && u.beta2 < 1) || !(u.eps >= 0) || !isfinite(u.eps))
+    return FLCE_ERR_INVALID_ARG;
+  if ((u.lr_dev == nullptr && !isfinite(u.lr)) || (u.step_dev == nullptr && u.step < 1)) return FLCE_ERR_INVALID_ARG;
+  if ((u.skip_nonfinite != 0 && u.skip_nonfinite != 1) || (u.stochastic != 0 && u.stochastic != 1))
+    return FLCE_ERR_INVALID_ARG;
+  if (!aligned_to(u.step_dev, 8) || !aligned_to(u.lr_dev, 4) || !aligned_to(u.grad_scale_dev, 4))
+    return FLCE_ERR_MISALIGNED;
+  for (int64_t i = 0; i < count; ++i) {
+    const flce_status_t st = check_tensor(tensors[i]);
+    if (st != FLCE_OK) return st;
+  }
+  const double t = static_cast<double>(u.step);
+  AdamNumbers num = {};
+  num.step_dev = u.step_dev;
+  num.lr_dev = u.lr_dev;
+  num.grad_scale_dev = u.grad_scale_dev;
+  num.step = u.step;
+  num.lr = static_cast<float>(u.lr);
+  num.b1 = static_cast<float>(u.beta1);
+  num.c1 = static_cast<float>(1 - u.beta1);
+  num.b2 = static_cast<float>(u.beta2);
+  num.c2 = static_cast<float>(1 - u.beta2);
+  num.eps = static_cast<float>(u.eps);
+  num.log_b1 = static_cast<float>(log(u.beta1));
+  num.log_b2 = static_cast<float>(log(u.beta2));
+  num.rate = static_cast<float>(1 / (1 - pow(u.beta1, t)));
+  num.correction = static_cast<float>(1 / sqrt(1 - pow(u.beta2, t)));
+  num.grad_scale = u.grad_scale;
+  num.skip_nonfinite = u.skip_nonfinite;
+  num.stochastic = u.stochastic;
+  num.seed_lo = static_cast<unsigned int>(u.seed);
+  num.seed_hi = static_cast<unsigned int>(u.seed >> 32);
+  AdamEntry entry[kAdamEntries];
+  for (int64_t i = 0; i < count;) {
+    int filled = 0;
+    int64_t chunks = 0;
+    for (; i < count && filled < kAdamEntries; ++i) {
+      const flce_adamw_tensor_t& x = tensors[i];
+      if (x.n == 0) continue;
+      const int64_t more = div_up(x.n, kAdamChunk);
+      if (chunks + more > 0x7fffffff) {
+        if (filled == 0) return FLCE_ERR_UNSUPPORTED;
+        break;
+      }
+      entry[filled++] = {x.param, x.grad, x.exp_avg, x.exp_avg_sq, x.exp_avg_scale, x.exp_avg_sq_scale, x.copy, x.n,
+                         x.lr_scale, x.weight_decay, static_cast<unsigned int>(chunks), static_cast<int>(i),
+                         static_cast<int8_t>(x.param_dtype), static_cast<int8_t>(x.grad_dtype),
+                         static_cast<int8_t>(x.copy_dtype), static_cast<int8_t>(x.moment_bits)};
+      chunks += more;
+    }
+    if (filled == 0) break;
+    if (launch_adamw_any(entry, filled, static_cast<unsigned int>(chunks), num, s) != cudaSuccess)
+      return FLCE_ERR_CUDA;
+  }
+  return FLCE_OK;
+}
+
+}  // extern "C"
