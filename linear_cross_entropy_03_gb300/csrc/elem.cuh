@@ -39,6 +39,34 @@ __device__ __forceinline__ void store_elem(void* p, int dtype, int64_t i, float 
     static_cast<__half*>(p)[i] = from_float<__half>(v);
 }
 
+// Four elements from i on, which lie on a boundary of four; read or written once
+// (streamed: first to leave the caches).
+__device__ __forceinline__ float4 load_four(const void* p, int dtype, int64_t i) {
+  if (dtype == FLCE_DTYPE_FP32) return __ldcs(reinterpret_cast<const float4*>(static_cast<const float*>(p) + i));
+  const uint2 r = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i));
+  if (dtype == FLCE_DTYPE_BF16)
+    return make_float4(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xFFFF0000u), __uint_as_float(r.y << 16),
+                       __uint_as_float(r.y & 0xFFFF0000u));
+  const float2 a = __half22float2(reinterpret_cast<const __half2&>(r.x));
+  const float2 b = __half22float2(reinterpret_cast<const __half2&>(r.y));
+  return make_float4(a.x, a.y, b.x, b.y);
+}
+__device__ __forceinline__ void store_four(void* p, int dtype, int64_t i, const float4& v) {
+  if (dtype == FLCE_DTYPE_FP32) {
+    __stcs(reinterpret_cast<float4*>(static_cast<float*>(p) + i), v);
+    return;
+  }
+  uint2 r;
+  if (dtype == FLCE_DTYPE_BF16) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+    r = make_uint2(reinterpret_cast<const uint32_t&>(a), reinterpret_cast<const uint32_t&>(b));
+  } else {
+    const __half2 a = __floats2half2_rn(v.x, v.y), b = __floats2half2_rn(v.z, v.w);
+    r = make_uint2(reinterpret_cast<const uint32_t&>(a), reinterpret_cast<const uint32_t&>(b));
+  }
+  __stcs(reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + i), r);
+}
+
 inline bool float_dtype(int dtype) {
   return dtype == FLCE_DTYPE_BF16 || dtype == FLCE_DTYPE_FP16 || dtype == FLCE_DTYPE_FP32;
 }
@@ -46,5 +74,21 @@ inline size_t elem_size(int dtype) { return dtype == FLCE_DTYPE_FP32 ? 4 : 2; }
 inline bool aligned_to(const void* p, size_t a) { return reinterpret_cast<uintptr_t>(p) % a == 0; }
 inline int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+
+// Launches a kernel that may start while its predecessor on the stream still
+// runs, up to its griddepcontrol.wait.
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, dim3 block, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.stream = s;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
 
 }  // namespace flce

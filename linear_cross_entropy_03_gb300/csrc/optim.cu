@@ -35,7 +35,7 @@ __device__ __forceinline__ int entry_of(const E* entry, int count, unsigned int 
 
 // ------------------------------------------------------------ gradient norm
 
-constexpr int kNormChunk = 16384;  // elements a CTA takes at a time
+constexpr int kNormChunk = 4096;   // 16-byte vectors a CTA takes at a time
 constexpr int kNormParts = 608;    // most CTAs, and partial sums, of a launch
 
 struct NormEntry {
@@ -53,17 +53,56 @@ struct NormArgs {
   float* part;  // [gridDim.x]
 };
 
-// Partial sums of squares: CTA b takes chunks b, b + gridDim.x, ...
+// Squares of the elements in 16 bytes.
+__device__ __forceinline__ float squares(const uint4& r, int dtype) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+  float s = 0.f;
+  if (dtype == FLCE_DTYPE_FP32) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) s = fmaf(__uint_as_float(w[k]), __uint_as_float(w[k]), s);
+  } else if (dtype == FLCE_DTYPE_BF16) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) s = fmaf(bf16_lo(w[k]), bf16_lo(w[k]), fmaf(bf16_hi(w[k]), bf16_hi(w[k]), s));
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 f = __half22float2(reinterpret_cast<const __half2&>(w[k]));
+      s = fmaf(f.x, f.x, fmaf(f.y, f.y, s));
+    }
+  }
+  return s;
+}
+
+// Partial sums of squares: CTA b takes chunks b, b + gridDim.x, ...  A chunk is
+// 16-byte vectors from the tensor's first 16-byte boundary on; the elements
+// before it, and those after the last vector, go with the first chunk.
 __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_constant__ NormArgs a) {
+  grid_dependents_launch();
   __shared__ float scratch[kThreads / 32];
   float sum = 0.f;
   for (unsigned int c = blockIdx.x; c < a.chunks; c += gridDim.x) {
     const NormEntry& e = a.entry[entry_of(a.entry, a.count, c)];
-    const int64_t i0 = static_cast<int64_t>(c - e.chunk0) * kNormChunk;
-    const int64_t i1 = min(i0 + kNormChunk, e.n);
-    for (int64_t i = i0 + threadIdx.x; i < i1; i += kThreads) {
-      const float g = load_elem(e.data, e.dtype, i);
-      sum += g * g;
+    const int per = e.dtype == FLCE_DTYPE_FP32 ? 4 : 8;  // elements of a vector
+    const int64_t esz = 16 / per;
+    const int64_t head = min(static_cast<int64_t>((16 - reinterpret_cast<uintptr_t>(e.data) % 16) % 16) / esz, e.n);
+    const uint4* v = reinterpret_cast<const uint4*>(static_cast<const char*>(e.data) + head * esz);
+    const int64_t vectors = (e.n - head) / per;
+    const int64_t v0 = static_cast<int64_t>(c - e.chunk0) * kNormChunk, v1 = min(v0 + kNormChunk, vectors);
+    constexpr int kBatch = 8;
+    int64_t i = v0 + threadIdx.x;
+    for (; i + (kBatch - 1) * kThreads < v1; i += kBatch * kThreads) {
+      uint4 r[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) r[k] = __ldcs(v + i + k * kThreads);
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) sum += squares(r[k], e.dtype);
+    }
+    for (; i < v1; i += kThreads) sum += squares(__ldcs(v + i), e.dtype);
+    if (v0 == 0) {
+      const int64_t tail = head + vectors * per + threadIdx.x;
+      const float g = threadIdx.x < head ? load_elem(e.data, e.dtype, threadIdx.x) : 0.f;
+      const float h = tail < e.n ? load_elem(e.data, e.dtype, tail) : 0.f;
+      sum = fmaf(g, g, fmaf(h, h, sum));
     }
   }
   sum = warp_sum(sum);
@@ -114,6 +153,7 @@ struct AdamEntry {
   unsigned int chunk0;
   int index;  // place in the call's table
   int8_t param_dtype, grad_dtype, copy_dtype, bits;
+  int head;  // elements before the first vector of four in every array, or -1: the arrays differ in this
 };
 
 struct AdamNumbers {
@@ -176,6 +216,17 @@ __device__ __forceinline__ float from_e4m3(unsigned int code) {
   return __half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(code), __NV_E4M3)));
 }
 
+// Four codes, lowest byte first, times the block's scale.
+__device__ __forceinline__ void from_e4m3_four(unsigned int codes, float scale, float* out) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const __half2_raw raw = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(codes >> (16 * h)), __NV_E4M3);
+    const float2 f = __half22float2(__half2(raw));
+    out[2 * h] = f.x * scale;
+    out[2 * h + 1] = f.y * scale;
+  }
+}
+
 // A block's scale from its largest finite magnitude, and what divides by it.
 __device__ __forceinline__ float block_scale(float largest, float* inverse) {
   float s = __fmul_rn(largest, 1.f / kE4m3Max);
@@ -216,20 +267,46 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
   if (e.bits == 32) {
     float* mp = static_cast<float*>(e.m);
     float* vp = static_cast<float*>(e.v);
-    for (int64_t i = i0 + threadIdx.x; i < i1; i += kThreads) {
+    const auto one = [&](int64_t i) {
       float m = mp[i], v = vp[i];
       moments(k, load_elem(e.grad, e.grad_dtype, i) * factor, m, v);
-      const float p =
-          updated(load_elem(e.param, e.param_dtype, i), keep, rate, correction, k.eps, m, __fsqrt_rn(v));
+      const float p = updated(load_elem(e.param, e.param_dtype, i), keep, rate, correction, k.eps, m, __fsqrt_rn(v));
       mp[i] = m;
       vp[i] = v;
       store_elem(e.param, e.param_dtype, i, p);
       if (e.copy != nullptr) store_elem(e.copy, e.copy_dtype, i, p);
+    };
+    if (e.head < 0) {
+      for (int64_t i = i0 + threadIdx.x; i < i1; i += kThreads) one(i);
+      return;
     }
+    // vectors of four from element `head` on; what is left at the tensor's ends goes one by one
+    const int64_t whole = e.n - (e.n - e.head) % 4;
+    for (int64_t i = i0 + e.head + threadIdx.x * 4; i < min(i0 + e.head + kAdamChunk, whole); i += kThreads * 4) {
+      float4 m = __ldcs(reinterpret_cast<const float4*>(mp + i)), v = __ldcs(reinterpret_cast<const float4*>(vp + i));
+      float4 p = load_four(e.param, e.param_dtype, i);
+      const float4 g = load_four(e.grad, e.grad_dtype, i);
+      const auto part = [&](float& p1, float g1, float& m1, float& v1) {
+        moments(k, g1 * factor, m1, v1);
+        p1 = updated(p1, keep, rate, correction, k.eps, m1, __fsqrt_rn(v1));
+      };
+      part(p.x, g.x, m.x, v.x);
+      part(p.y, g.y, m.y, v.y);
+      part(p.z, g.z, m.z, v.z);
+      part(p.w, g.w, m.w, v.w);
+      __stcs(reinterpret_cast<float4*>(mp + i), m);
+      __stcs(reinterpret_cast<float4*>(vp + i), v);
+      store_four(e.param, e.param_dtype, i, p);
+      if (e.copy != nullptr) store_four(e.copy, e.copy_dtype, i, p);
+    }
+    if (i0 == 0 && threadIdx.x < e.head) one(threadIdx.x);
+    if (whole + threadIdx.x < e.n && whole < i0 + e.head + kAdamChunk && whole >= i0 + e.head) one(whole + threadIdx.x);
     return;
   }
 
-  // 8-bit moments: a warp takes a block, lane l its elements l, l + 32, ...
+  // 8-bit moments: a warp takes a block of 256, of which each lane holds two
+  // fours (elements 4 lane.. and 128 + 4 lane..), or, where the arrays are not
+  // aligned for that, every 32nd element
   constexpr int kPer = FLCE_ADAMW_BLOCK / 32;
   unsigned int key = 0;
   if (k.stochastic) {
@@ -244,22 +321,43 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
   for (int64_t b0 = i0 + (threadIdx.x >> 5) * FLCE_ADAMW_BLOCK; b0 < i1; b0 += kThreads / 32 * FLCE_ADAMW_BLOCK) {
     const int64_t block = b0 / FLCE_ADAMW_BLOCK;
     const float ms = e.m_scale[block], vs = e.v_scale[block];
-    float m[kPer], r[kPer];
+    const bool vector = e.head == 0 && b0 + FLCE_ADAMW_BLOCK <= e.n;
+    const auto place = [&](int j) {  // of the lane's j-th element
+      return b0 + (vector ? (j >> 2) * 128 + lane * 4 + (j & 3) : j * 32 + lane);
+    };
+    float m[kPer], r[kPer], p[kPer], g[kPer];
+    if (vector) {
+#pragma unroll
+      for (int q = 0; q < kPer / 4; ++q) {
+        const int64_t i = b0 + q * 128 + lane * 4;
+        const float4 pv = load_four(e.param, e.param_dtype, i), gv = load_four(e.grad, e.grad_dtype, i);
+        const unsigned int mc = __ldcs(reinterpret_cast<const unsigned int*>(mp + i));
+        const unsigned int rc = __ldcs(reinterpret_cast<const unsigned int*>(vp + i));
+        p[4 * q] = pv.x, p[4 * q + 1] = pv.y, p[4 * q + 2] = pv.z, p[4 * q + 3] = pv.w;
+        g[4 * q] = gv.x, g[4 * q + 1] = gv.y, g[4 * q + 2] = gv.z, g[4 * q + 3] = gv.w;
+        from_e4m3_four(mc, ms, m + 4 * q);
+        from_e4m3_four(rc, vs, r + 4 * q);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const int64_t i = place(j);
+        p[j] = g[j] = m[j] = r[j] = 0.f;
+        if (i < e.n) {
+          p[j] = load_elem(e.param, e.param_dtype, i);
+          g[j] = load_elem(e.grad, e.grad_dtype, i);
+          m[j] = from_e4m3(mp[i]) * ms;
+          r[j] = from_e4m3(vp[i]) * vs;
+        }
+      }
+    }
     float m_largest = 0.f, r_largest = 0.f;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-      const int64_t i = b0 + j * 32 + lane;
-      m[j] = r[j] = 0.f;
-      if (i < e.n) {
-        m[j] = from_e4m3(mp[i]) * ms;
-        const float root = from_e4m3(vp[i]) * vs;
-        float v = __fmul_rn(root, root);
-        moments(k, load_elem(e.grad, e.grad_dtype, i) * factor, m[j], v);
-        r[j] = __fsqrt_rn(v);
-        const float p = updated(load_elem(e.param, e.param_dtype, i), keep, rate, correction, k.eps, m[j], r[j]);
-        store_elem(e.param, e.param_dtype, i, p);
-        if (e.copy != nullptr) store_elem(e.copy, e.copy_dtype, i, p);
-      }
+      float v = __fmul_rn(r[j], r[j]);
+      moments(k, g[j] * factor, m[j], v);
+      r[j] = __fsqrt_rn(v);
+      p[j] = updated(p[j], keep, rate, correction, k.eps, m[j], r[j]);
       m_largest = fmaxf(m_largest, finite_abs(m[j]));
       r_largest = fmaxf(r_largest, finite_abs(r[j]));
     }
@@ -267,18 +365,38 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
     const float m_scale = block_scale(warp_max_bits(m_largest), &m_inv);
     const float r_scale = block_scale(warp_max_bits(r_largest), &r_inv);
     const unsigned int key_hi = mix(key ^ static_cast<unsigned int>(static_cast<uint64_t>(b0) >> 32));
+    unsigned int mc[kPer], rc[kPer];
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-      const int64_t i = b0 + j * 32 + lane;
-      if (i >= e.n) break;
-      const unsigned int bits = k.stochastic ? mix(static_cast<unsigned int>(i) ^ key_hi) : 0u;
-      unsigned int mc = to_e4m3(__fmul_rn(m[j], m_inv), k.stochastic, bits >> 16);
-      unsigned int rc = to_e4m3(__fmul_rn(r[j], r_inv), k.stochastic, bits & 0xFFFFu);
-      if (rc == 0u && r[j] > 0.f) rc = 1u;  // the smallest number, 2^-9
-      if (!isfinite(m[j])) mc = kE4m3Nan;
-      if (!isfinite(r[j])) rc = kE4m3Nan;
-      mp[i] = static_cast<uint8_t>(mc);
-      vp[i] = static_cast<uint8_t>(rc);
+      const unsigned int bits = k.stochastic ? mix(static_cast<unsigned int>(place(j)) ^ key_hi) : 0u;
+      mc[j] = to_e4m3(__fmul_rn(m[j], m_inv), k.stochastic, bits >> 16);
+      rc[j] = to_e4m3(__fmul_rn(r[j], r_inv), k.stochastic, bits & 0xFFFFu);
+      if (rc[j] == 0u && r[j] > 0.f) rc[j] = 1u;  // the smallest number, 2^-9
+      if (!isfinite(m[j])) mc[j] = kE4m3Nan;
+      if (!isfinite(r[j])) rc[j] = kE4m3Nan;
+    }
+    if (vector) {
+#pragma unroll
+      for (int q = 0; q < kPer / 4; ++q) {
+        const int64_t i = b0 + q * 128 + lane * 4;
+        const int j = 4 * q;
+        const float4 pv = make_float4(p[j], p[j + 1], p[j + 2], p[j + 3]);
+        store_four(e.param, e.param_dtype, i, pv);
+        if (e.copy != nullptr) store_four(e.copy, e.copy_dtype, i, pv);
+        __stcs(reinterpret_cast<unsigned int*>(mp + i), mc[j] | mc[j + 1] << 8 | mc[j + 2] << 16 | mc[j + 3] << 24);
+        __stcs(reinterpret_cast<unsigned int*>(vp + i), rc[j] | rc[j + 1] << 8 | rc[j + 2] << 16 | rc[j + 3] << 24);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const int64_t i = place(j);
+        if (i < e.n) {
+          store_elem(e.param, e.param_dtype, i, p[j]);
+          if (e.copy != nullptr) store_elem(e.copy, e.copy_dtype, i, p[j]);
+          mp[i] = static_cast<uint8_t>(mc[j]);
+          vp[i] = static_cast<uint8_t>(rc[j]);
+        }
+      }
     }
     if (lane == 0) {
       e.m_scale[block] = m_scale;
@@ -311,6 +429,21 @@ cudaError_t launch_adamw_any(const AdamEntry* entry, int count, unsigned int chu
   if (count <= kAdamFew) return launch_adamw<kAdamFew>(entry, count, chunks, num, s);
   if (count <= kAdamMiddle) return launch_adamw<kAdamMiddle>(entry, count, chunks, num, s);
   return launch_adamw<kAdamEntries>(entry, count, chunks, num, s);
+}
+
+// Elements before every array's first boundary of four, where that is the same
+// for all of them; else -1.  (Blocks of 8-bit moments are counted from the
+// start, so that only 0 serves there.)
+int common_head(const flce_adamw_tensor_t& t) {
+  const size_t state = t.moment_bits == 8 ? 1 : 4;
+  const auto before = [](const void* p, size_t esz) {
+    return static_cast<int>((4 - reinterpret_cast<uintptr_t>(p) / esz % 4) % 4);
+  };
+  const int head = before(t.param, elem_size(t.param_dtype));
+  if (head != before(t.grad, elem_size(t.grad_dtype)) || head != before(t.exp_avg, state) ||
+      head != before(t.exp_avg_sq, state) || (t.copy != nullptr && head != before(t.copy, elem_size(t.copy_dtype))))
+    return -1;
+  return t.n > head ? head : -1;
 }
 
 size_t norm_workspace(int64_t count) {
@@ -368,7 +501,8 @@ flce_status_t grad_norm(const flce_tensor_t* tensors, int64_t count, float grad_
     a.count = 0;
     for (; i < count && a.count < kNormEntries; ++i) {
       if (tensors[i].n == 0) continue;
-      const int64_t more = div_up(tensors[i].n, kNormChunk);
+      // at least the vectors from the first boundary on (a chunk too many finds nothing)
+      const int64_t more = div_up(tensors[i].n, kNormChunk * static_cast<int64_t>(16 / elem_size(tensors[i].dtype)));
       if (chunks + more > 0x7fffffff) {
         if (a.count == 0) return FLCE_ERR_UNSUPPORTED;
         break;
@@ -388,8 +522,8 @@ flce_status_t grad_norm(const flce_tensor_t* tensors, int64_t count, float grad_
     parts += grid;
   }
   prof_begin(s, FLCE_KERNEL_GRAD_NORM);
-  grad_norm_finish_kernel<<<1, 1024, 0, s>>>(part, parts, grad_scale, max_norm, eps, out);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_after(grad_norm_finish_kernel, dim3(1), dim3(1024), s, static_cast<const float*>(part),
+                                     parts, grad_scale, max_norm, eps, out);
   prof_end(s);
   return e == cudaSuccess ? FLCE_OK : FLCE_ERR_CUDA;
 }
@@ -439,7 +573,8 @@ flce_status_t adamw_step(const flce_adamw_tensor_t* tensors, int64_t count, cons
     for (; i < count && filled < kAdamEntries; ++i) {
       const flce_adamw_tensor_t& x = tensors[i];
       if (x.n == 0) continue;
-      const int64_t more = div_up(x.n, kAdamChunk);
+      const int head = common_head(x);
+      const int64_t more = div_up(x.moment_bits == 32 && head > 0 ? x.n - head : x.n, kAdamChunk);
       if (chunks + more > 0x7fffffff) {
         if (filled == 0) return FLCE_ERR_UNSUPPORTED;
         break;
@@ -447,7 +582,7 @@ flce_status_t adamw_step(const flce_adamw_tensor_t* tensors, int64_t count, cons
       entry[filled++] = {x.param, x.grad, x.exp_avg, x.exp_avg_sq, x.exp_avg_scale, x.exp_avg_sq_scale, x.copy, x.n,
                          x.lr_scale, x.weight_decay, static_cast<unsigned int>(chunks), static_cast<int>(i),
                          static_cast<int8_t>(x.param_dtype), static_cast<int8_t>(x.grad_dtype),
-                         static_cast<int8_t>(x.copy_dtype), static_cast<int8_t>(x.moment_bits)};
+                         static_cast<int8_t>(x.copy_dtype), static_cast<int8_t>(x.moment_bits), head};
       chunks += more;
     }
     if (filled == 0) break;
