@@ -192,24 +192,39 @@ __device__ __forceinline__ void moments(const AdamNumbers& k, float g, float& m,
   v = __fadd_rn(__fmul_rn(v, k.b2), __fmul_rn(__fmul_rn(g, g), k.c2));
 }
 
+// The new parameter.  The divisor is 0 or far above the subnormal numbers (the
+// root of the smallest positive fp32 is 3.7e-23), which the approximate
+// reciprocal needs; its error, a unit or two of 2^-23, is the update's alone.
 __device__ __forceinline__ float updated(float p, float keep, float rate, float correction, float eps, float m,
                                          float root) {
-  return p * keep - m / (root * correction + eps) * rate;
+  return p * keep - m * rcp_approx(root * correction + eps) * rate;
 }
 
-// |x| <= 448 as an e4m3 number: to nearest, or stochastically by 16 bits.
-// The normal numbers have three bits of mantissa, so fp32 loses its lower 20:
-// adding random bits below them and cutting off rounds up with the probability
-// of what is cut off.  Below 2^-6 the spacing stays 2^-9: there 2^-6 is added
-// first, which gives the sum that spacing.
-__device__ __forceinline__ unsigned int to_e4m3(float x, bool stochastic, unsigned int bits16) {
-  if (stochastic) {
-    const float a = fminf(fabsf(x), kE4m3Max);
-    const float lift = a < kE4m3MinNormal ? kE4m3MinNormal : 0.f;
-    const unsigned int r = (__float_as_uint(a + lift) + (bits16 << 4)) & ~0xFFFFFu;
-    x = copysignf(fminf(__uint_as_float(r) - lift, kE4m3Max), x);
+// Rounds x (a moment over its block's scale, so at most 448 in size but for
+// rounding) to an e4m3 number's value or just past the largest, up with the
+// probability of what is cut off.  The normal numbers have three bits of
+// mantissa, so fp32 loses its lower 20: random bits (`noise`: 16 of them, at bits
+// 4 to 19) are added to those, and they are cut.  Below 2^-6 the spacing stays
+// 2^-9: there 2^-6 is added first, which gives the sum that spacing.
+__device__ __forceinline__ float round_stochastic(float x, unsigned int noise) {
+  const float lift = fabsf(x) < kE4m3MinNormal ? copysignf(kE4m3MinNormal, x) : 0.f;
+  return copysignf(__uint_as_float((__float_as_uint(x + lift) + noise) & ~0xFFFFFu) - lift, x);
+}
+
+// Four moments as e4m3 numbers, the first in the lowest byte.  KEEP (roots): what
+// is not 0 is held as at least the smallest number, 2^-9.
+template <bool STOCHASTIC, bool KEEP>
+__device__ __forceinline__ unsigned int to_e4m3_four(const float* x, float inverse, const unsigned int* noise) {
+  float y[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    y[j] = __fmul_rn(x[j], inverse);
+    if (STOCHASTIC) y[j] = round_stochastic(y[j], noise[j]);
+    if (KEEP && x[j] > 0.f) y[j] = fmaxf(y[j], 0x1p-9f);
   }
-  return __nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3);
+  const unsigned int low = __nv_cvt_float2_to_fp8x2(make_float2(y[0], y[1]), __NV_SATFINITE, __NV_E4M3);
+  const unsigned int high = __nv_cvt_float2_to_fp8x2(make_float2(y[2], y[3]), __NV_SATFINITE, __NV_E4M3);
+  return low | high << 16;
 }
 
 __device__ __forceinline__ float from_e4m3(unsigned int code) {
@@ -235,14 +250,139 @@ __device__ __forceinline__ float block_scale(float largest, float* inverse) {
   return s;
 }
 
-// The largest of the warp's non-negative finite numbers, which order like their bits.
-__device__ __forceinline__ float warp_max_bits(float v) {
-  return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(v)));
+// Bits of |x|: they order like the numbers, infinities and NaN above all.
+__device__ __forceinline__ unsigned int magnitude(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
+constexpr unsigned int kInfinityBits = 0x7F800000u;
+
+// The scale of the warp's moments x, and what multiplies by its inverse.  False:
+// some are not finite, which the scale passes over.
+template <int N>
+__device__ __forceinline__ bool warp_scale(const float* x, float* scale, float* inverse) {
+  unsigned int largest = 0;
+#pragma unroll
+  for (int j = 0; j < N; ++j) largest = max(largest, magnitude(x[j]));
+  largest = __reduce_max_sync(0xffffffffu, largest);
+  const bool finite = largest < kInfinityBits;
+  if (!finite) {
+    largest = 0;
+#pragma unroll
+    for (int j = 0; j < N; ++j) largest = max(largest, magnitude(x[j]) < kInfinityBits ? magnitude(x[j]) : 0u);
+    largest = __reduce_max_sync(0xffffffffu, largest);
+  }
+  *scale = block_scale(__uint_as_float(largest), inverse);
+  return finite;
 }
 
-__device__ __forceinline__ float finite_abs(float x) {
-  const float a = fabsf(x);
-  return a <= 3.402823466e38f ? a : 0.f;
+// `codes` with NaN where x is not finite.
+__device__ __forceinline__ unsigned int mark_nan(unsigned int codes, const float* x) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (magnitude(x[j]) >= kInfinityBits) codes = (codes & ~(0xFFu << (8 * j))) | kE4m3Nan << (8 * j);
+  return codes;
+}
+
+struct AdamStep {
+  float factor, keep, rate, correction;
+  unsigned int key;  // of this tensor and step, for the random bits
+};
+
+// A block of 256 elements from b0 on with moments in 8 bits, by one warp: each
+// lane holds two fours (elements 4 lane.. and 128 + 4 lane..), or, where the
+// arrays are not aligned for that, eight elements one by one.
+template <bool STOCHASTIC>
+__device__ __forceinline__ void adam8_block(const AdamEntry& e, const AdamNumbers& k, const AdamStep& st, int64_t b0) {
+  constexpr int kPer = FLCE_ADAMW_BLOCK / 32;
+  uint8_t* mp = static_cast<uint8_t*>(e.m);
+  uint8_t* vp = static_cast<uint8_t*>(e.v);
+  const int lane = threadIdx.x & 31;
+  const int64_t block = b0 / FLCE_ADAMW_BLOCK;
+  const float ms = e.m_scale[block], vs = e.v_scale[block];
+  const bool vector = e.head == 0 && b0 + FLCE_ADAMW_BLOCK <= e.n;
+  float m[kPer], r[kPer], p[kPer], g[kPer];
+  if (vector) {
+    unsigned int mc[kPer / 4], rc[kPer / 4];
+#pragma unroll
+    for (int q = 0; q < kPer / 4; ++q) {
+      const int64_t i = b0 + q * 128 + lane * 4;
+      mc[q] = __ldcs(reinterpret_cast<const unsigned int*>(mp + i));
+      rc[q] = __ldcs(reinterpret_cast<const unsigned int*>(vp + i));
+      const float4 gv = load_four(e.grad, e.grad_dtype, i), pv = load_four(e.param, e.param_dtype, i);
+      p[4 * q] = pv.x, p[4 * q + 1] = pv.y, p[4 * q + 2] = pv.z, p[4 * q + 3] = pv.w;
+      g[4 * q] = gv.x, g[4 * q + 1] = gv.y, g[4 * q + 2] = gv.z, g[4 * q + 3] = gv.w;
+    }
+#pragma unroll
+    for (int q = 0; q < kPer / 4; ++q) {
+      from_e4m3_four(mc[q], ms, m + 4 * q);
+      from_e4m3_four(rc[q], vs, r + 4 * q);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int64_t i = b0 + (j >> 2) * 128 + lane * 4 + (j & 3);
+      p[j] = g[j] = m[j] = r[j] = 0.f;
+      if (i < e.n) {
+        p[j] = load_elem(e.param, e.param_dtype, i);
+        g[j] = load_elem(e.grad, e.grad_dtype, i);
+        m[j] = from_e4m3(mp[i]) * ms;
+        r[j] = from_e4m3(vp[i]) * vs;
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    float v = __fmul_rn(r[j], r[j]);
+    moments(k, g[j] * st.factor, m[j], v);
+    r[j] = __fsqrt_rn(v);
+    p[j] = updated(p[j], st.keep, st.rate, st.correction, k.eps, m[j], r[j]);
+  }
+  if (vector) {
+#pragma unroll
+    for (int q = 0; q < kPer / 4; ++q) {
+      const int64_t i = b0 + q * 128 + lane * 4;
+      const float4 pv = make_float4(p[4 * q], p[4 * q + 1], p[4 * q + 2], p[4 * q + 3]);
+      store_four(e.param, e.param_dtype, i, pv);
+      if (e.copy != nullptr) store_four(e.copy, e.copy_dtype, i, pv);
+    }
+  }
+  float m_scale, r_scale, m_inverse, r_inverse;
+  const bool m_finite = warp_scale<kPer>(m, &m_scale, &m_inverse);
+  const bool r_finite = warp_scale<kPer>(r, &r_scale, &r_inverse);
+  // a block lies on one side of every multiple of 2^32
+  const unsigned int key = STOCHASTIC ? mix(st.key ^ static_cast<unsigned int>(static_cast<uint64_t>(b0) >> 32)) : 0u;
+#pragma unroll
+  for (int q = 0; q < kPer / 4; ++q) {
+    const int64_t i = b0 + q * 128 + lane * 4;
+    unsigned int m_noise[4], r_noise[4];
+    if (STOCHASTIC) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const unsigned int bits = mix((static_cast<unsigned int>(i) + j) ^ key);
+        m_noise[j] = bits >> 12 & 0xFFFF0u;
+        r_noise[j] = bits << 4 & 0xFFFF0u;
+      }
+    }
+    unsigned int mc = to_e4m3_four<STOCHASTIC, false>(m + 4 * q, m_inverse, m_noise);
+    unsigned int rc = to_e4m3_four<STOCHASTIC, true>(r + 4 * q, r_inverse, r_noise);
+    if (!m_finite) mc = mark_nan(mc, m + 4 * q);
+    if (!r_finite) rc = mark_nan(rc, r + 4 * q);
+    if (vector) {
+      __stcs(reinterpret_cast<unsigned int*>(mp + i), mc);
+      __stcs(reinterpret_cast<unsigned int*>(vp + i), rc);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (i + j < e.n) {
+          store_elem(e.param, e.param_dtype, i + j, p[4 * q + j]);
+          if (e.copy != nullptr) store_elem(e.copy, e.copy_dtype, i + j, p[4 * q + j]);
+          mp[i + j] = static_cast<uint8_t>(mc >> (8 * j));
+          vp[i + j] = static_cast<uint8_t>(rc >> (8 * j));
+        }
+    }
+  }
+  if (lane == 0) {
+    e.m_scale[block] = m_scale;
+    e.v_scale[block] = r_scale;
+  }
 }
 
 template <int MAX>
@@ -304,104 +444,18 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
     return;
   }
 
-  // 8-bit moments: a warp takes a block of 256, of which each lane holds two
-  // fours (elements 4 lane.. and 128 + 4 lane..), or, where the arrays are not
-  // aligned for that, every 32nd element
-  constexpr int kPer = FLCE_ADAMW_BLOCK / 32;
-  unsigned int key = 0;
+  AdamStep st = {factor, keep, rate, correction, 0u};
   if (k.stochastic) {
-    key = mix(k.seed_lo);
-    key = mix(key ^ k.seed_hi);
-    key = mix(key ^ static_cast<unsigned int>(step));
-    key = mix(key ^ static_cast<unsigned int>(e.index));
+    st.key = mix(k.seed_lo);
+    st.key = mix(st.key ^ k.seed_hi);
+    st.key = mix(st.key ^ static_cast<unsigned int>(step));
+    st.key = mix(st.key ^ static_cast<unsigned int>(e.index));
   }
-  uint8_t* mp = static_cast<uint8_t*>(e.m);
-  uint8_t* vp = static_cast<uint8_t*>(e.v);
-  const int lane = threadIdx.x & 31;
   for (int64_t b0 = i0 + (threadIdx.x >> 5) * FLCE_ADAMW_BLOCK; b0 < i1; b0 += kThreads / 32 * FLCE_ADAMW_BLOCK) {
-    const int64_t block = b0 / FLCE_ADAMW_BLOCK;
-    const float ms = e.m_scale[block], vs = e.v_scale[block];
-    const bool vector = e.head == 0 && b0 + FLCE_ADAMW_BLOCK <= e.n;
-    const auto place = [&](int j) {  // of the lane's j-th element
-      return b0 + (vector ? (j >> 2) * 128 + lane * 4 + (j & 3) : j * 32 + lane);
-    };
-    float m[kPer], r[kPer], p[kPer], g[kPer];
-    if (vector) {
-#pragma unroll
-      for (int q = 0; q < kPer / 4; ++q) {
-        const int64_t i = b0 + q * 128 + lane * 4;
-        const float4 pv = load_four(e.param, e.param_dtype, i), gv = load_four(e.grad, e.grad_dtype, i);
-        const unsigned int mc = __ldcs(reinterpret_cast<const unsigned int*>(mp + i));
-        const unsigned int rc = __ldcs(reinterpret_cast<const unsigned int*>(vp + i));
-        p[4 * q] = pv.x, p[4 * q + 1] = pv.y, p[4 * q + 2] = pv.z, p[4 * q + 3] = pv.w;
-        g[4 * q] = gv.x, g[4 * q + 1] = gv.y, g[4 * q + 2] = gv.z, g[4 * q + 3] = gv.w;
-        from_e4m3_four(mc, ms, m + 4 * q);
-        from_e4m3_four(rc, vs, r + 4 * q);
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        const int64_t i = place(j);
-        p[j] = g[j] = m[j] = r[j] = 0.f;
-        if (i < e.n) {
-          p[j] = load_elem(e.param, e.param_dtype, i);
-          g[j] = load_elem(e.grad, e.grad_dtype, i);
-          m[j] = from_e4m3(mp[i]) * ms;
-          r[j] = from_e4m3(vp[i]) * vs;
-        }
-      }
-    }
-    float m_largest = 0.f, r_largest = 0.f;
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      float v = __fmul_rn(r[j], r[j]);
-      moments(k, g[j] * factor, m[j], v);
-      r[j] = __fsqrt_rn(v);
-      p[j] = updated(p[j], keep, rate, correction, k.eps, m[j], r[j]);
-      m_largest = fmaxf(m_largest, finite_abs(m[j]));
-      r_largest = fmaxf(r_largest, finite_abs(r[j]));
-    }
-    float m_inv, r_inv;
-    const float m_scale = block_scale(warp_max_bits(m_largest), &m_inv);
-    const float r_scale = block_scale(warp_max_bits(r_largest), &r_inv);
-    const unsigned int key_hi = mix(key ^ static_cast<unsigned int>(static_cast<uint64_t>(b0) >> 32));
-    unsigned int mc[kPer], rc[kPer];
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const unsigned int bits = k.stochastic ? mix(static_cast<unsigned int>(place(j)) ^ key_hi) : 0u;
-      mc[j] = to_e4m3(__fmul_rn(m[j], m_inv), k.stochastic, bits >> 16);
-      rc[j] = to_e4m3(__fmul_rn(r[j], r_inv), k.stochastic, bits & 0xFFFFu);
-      if (rc[j] == 0u && r[j] > 0.f) rc[j] = 1u;  // the smallest number, 2^-9
-      if (!isfinite(m[j])) mc[j] = kE4m3Nan;
-      if (!isfinite(r[j])) rc[j] = kE4m3Nan;
-    }
-    if (vector) {
-#pragma unroll
-      for (int q = 0; q < kPer / 4; ++q) {
-        const int64_t i = b0 + q * 128 + lane * 4;
-        const int j = 4 * q;
-        const float4 pv = make_float4(p[j], p[j + 1], p[j + 2], p[j + 3]);
-        store_four(e.param, e.param_dtype, i, pv);
-        if (e.copy != nullptr) store_four(e.copy, e.copy_dtype, i, pv);
-        __stcs(reinterpret_cast<unsigned int*>(mp + i), mc[j] | mc[j + 1] << 8 | mc[j + 2] << 16 | mc[j + 3] << 24);
-        __stcs(reinterpret_cast<unsigned int*>(vp + i), rc[j] | rc[j + 1] << 8 | rc[j + 2] << 16 | rc[j + 3] << 24);
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        const int64_t i = place(j);
-        if (i < e.n) {
-          store_elem(e.param, e.param_dtype, i, p[j]);
-          if (e.copy != nullptr) store_elem(e.copy, e.copy_dtype, i, p[j]);
-          mp[i] = static_cast<uint8_t>(mc[j]);
-          vp[i] = static_cast<uint8_t>(rc[j]);
-        }
-      }
-    }
-    if (lane == 0) {
-      e.m_scale[block] = m_scale;
-      e.v_scale[block] = r_scale;
-    }
+    if (k.stochastic)
+      adam8_block<true>(e, k, st, b0);
+    else
+      adam8_block<false>(e, k, st, b0);
   }
 }
 
