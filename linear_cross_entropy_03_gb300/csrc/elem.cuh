@@ -67,6 +67,37 @@ __device__ __forceinline__ void store_four(void* p, int dtype, int64_t i, const 
   __stcs(reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + i), r);
 }
 
+// Two fp32 operations in one instruction.
+struct Pair {
+  uint64_t v;
+};
+__device__ __forceinline__ Pair pair(float lo, float hi) {
+  Pair r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ Pair pair(float both) { return pair(both, both); }
+__device__ __forceinline__ float2 unpair(Pair a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+  return r;
+}
+__device__ __forceinline__ Pair operator*(Pair a, Pair b) {
+  Pair r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ Pair operator+(Pair a, Pair b) {
+  Pair r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ Pair fma_pair(Pair a, Pair b, Pair c) {
+  Pair r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+
 inline bool float_dtype(int dtype) {
   return dtype == FLCE_DTYPE_BF16 || dtype == FLCE_DTYPE_FP16 || dtype == FLCE_DTYPE_FP32;
 }

@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(1024)
 
 constexpr int kAdamChunk = 4096;  // elements of a CTA: a whole number of 8-bit blocks
 static_assert(kAdamChunk % (FLCE_ADAMW_BLOCK * (kThreads / 32)) == 0, "whole blocks for every warp");
-constexpr float kE4m3Max = 448.f, kE4m3MinNormal = 0x1p-6f;
+constexpr float kE4m3Max = 448.f;
 constexpr unsigned int kE4m3Nan = 0x7Fu;
 
 struct AdamEntry {
@@ -165,6 +165,7 @@ struct AdamNumbers {
   float rate, correction;            // 1 / (1 - b1^t), 1 / sqrt(1 - b2^t) when the step is known here
   float log_b1, log_b2;              // for them otherwise
   float grad_scale;
+  float one, minus_zero;
   int skip_nonfinite, stochastic;
   unsigned int seed_lo, seed_hi;
 };
@@ -184,47 +185,71 @@ __device__ __forceinline__ unsigned int mix(unsigned int x) {
   return x ^ (x >> 16);
 }
 
-// One element's new moments.  The products and sums round one by one (no
-// contraction), as the formulas read: what is then rounded to 8 bits does not
-// depend on how the compiler fuses them.
-__device__ __forceinline__ void moments(const AdamNumbers& k, float g, float& m, float& v) {
-  m = __fadd_rn(__fmul_rn(m, k.b1), __fmul_rn(g, k.c1));
-  v = __fadd_rn(__fmul_rn(v, k.b2), __fmul_rn(__fmul_rn(g, g), k.c2));
+// Two elements' new moments.  Each product and sum rounds by itself, as the
+// formulas read, so that what is then rounded to 8 bits does not depend on how
+// the compiler fuses them.  It fuses products and sums of pairs whatever their
+// rounding says; a fused operation whose neutral operand (-0 to add, 1 to multiply
+// by) it cannot know stays by itself, at the same cost.
+__device__ __forceinline__ void moments(const AdamNumbers& k, Pair g, Pair& m, Pair& v) {
+  const Pair zero = pair(k.minus_zero), one = pair(k.one);
+  m = fma_pair(fma_pair(m, pair(k.b1), zero), one, fma_pair(g, pair(k.c1), zero));
+  v = fma_pair(fma_pair(v, pair(k.b2), zero), one, fma_pair(fma_pair(g, g, zero), pair(k.c2), zero));
 }
 
-// The new parameter.  The divisor is 0 or far above the subnormal numbers (the
+__device__ __forceinline__ Pair sqrt_pair(Pair a) {
+  const float2 f = unpair(a);
+  return pair(__fsqrt_rn(f.x), __fsqrt_rn(f.y));
+}
+
+struct AdamStep {
+  float factor, keep, rate, correction;
+  unsigned int key;  // of this tensor and step, for the random bits
+};
+
+// The new parameters.  The divisors are 0 or far above the subnormal numbers (the
 // root of the smallest positive fp32 is 3.7e-23), which the approximate
 // reciprocal needs; its error, a unit or two of 2^-23, is the update's alone.
-__device__ __forceinline__ float updated(float p, float keep, float rate, float correction, float eps, float m,
-                                         float root) {
-  return p * keep - m * rcp_approx(root * correction + eps) * rate;
+__device__ __forceinline__ Pair updated(const AdamNumbers& k, const AdamStep& st, Pair p, Pair m, Pair root) {
+  const float2 d = unpair(fma_pair(root, pair(st.correction), pair(k.eps)));
+  return fma_pair(m * pair(rcp_approx(d.x), rcp_approx(d.y)), pair(-st.rate), p * pair(st.keep));
 }
 
-// Rounds x (a moment over its block's scale, so at most 448 in size but for
-// rounding) to an e4m3 number's value or just past the largest, up with the
-// probability of what is cut off.  The normal numbers have three bits of
-// mantissa, so fp32 loses its lower 20: random bits (`noise`: 16 of them, at bits
-// 4 to 19) are added to those, and they are cut.  Below 2^-6 the spacing stays
-// 2^-9: there 2^-6 is added first, which gives the sum that spacing.
-__device__ __forceinline__ float round_stochastic(float x, unsigned int noise) {
-  const float lift = fabsf(x) < kE4m3MinNormal ? copysignf(kE4m3MinNormal, x) : 0.f;
-  return copysignf(__uint_as_float((__float_as_uint(x + lift) + noise) & ~0xFFFFFu) - lift, x);
-}
-
-// Four moments as e4m3 numbers, the first in the lowest byte.  KEEP (roots): what
-// is not 0 is held as at least the smallest number, 2^-9.
-template <bool STOCHASTIC, bool KEEP>
-__device__ __forceinline__ unsigned int to_e4m3_four(const float* x, float inverse, const unsigned int* noise) {
-  float y[4];
+// Four moments over their block's scale as e4m3 numbers, the first in the lowest
+// byte.  2^-120 times an e4m3 number is an fp32 number of the same exponent field,
+// the normal numbers' and the subnormal ones', whose mantissa has only its upper
+// three bits: bits 20 to 26 of the scaled fp32 number are the code, and the 20
+// below are what rounding cuts off.  To nearest adds half of it (less one unit,
+// where the code's last bit is 0, for ties to even); stochastically adds 16 random
+// bits at 4 to 19, so that it rounds up with the probability of what is cut.  The
+// largest, 448 but for rounding, stays below the next number either way.  (Four
+// bits further left, as below, the code is the upper byte.)
+//
+// `random`: 32 bits an element, of which the upper half (HIGH) or the lower serves.
+// KEEP (roots, not negative): what is not 0 is held as at least the smallest number.
+template <bool STOCHASTIC, bool HIGH, bool KEEP>
+__device__ __forceinline__ unsigned int to_e4m3_four(const float* x, float inverse, const unsigned int* random) {
+  unsigned int t[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    y[j] = __fmul_rn(x[j], inverse);
-    if (STOCHASTIC) y[j] = round_stochastic(y[j], noise[j]);
-    if (KEEP && x[j] > 0.f) y[j] = fmaxf(y[j], 0x1p-9f);
+  for (int j = 0; j < 4; j += 2) {
+    const float2 y = unpair(pair(x[j], x[j + 1]) * pair(inverse) * pair(0x1p-120f));
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const unsigned int u = __float_as_uint(h == 0 ? y.x : y.y);
+      unsigned int r;  // what is added, four bits to the left
+      if (STOCHASTIC)
+        r = __byte_perm(random[j + h], 0, HIGH ? 0x4324 : 0x4104);
+      else
+        r = (0x7FFFFu + (u >> 20 & 1u)) << 4;
+      unsigned int c = (u << 4) + r;
+      if (KEEP) {
+        if (x[j + h] > 0.f) c = max(c, 0x01000000u);
+      } else {
+        c = (c & 0x7FFFFFFFu) | (u & 0x80000000u);
+      }
+      t[j + h] = c;
+    }
   }
-  const unsigned int low = __nv_cvt_float2_to_fp8x2(make_float2(y[0], y[1]), __NV_SATFINITE, __NV_E4M3);
-  const unsigned int high = __nv_cvt_float2_to_fp8x2(make_float2(y[2], y[3]), __NV_SATFINITE, __NV_E4M3);
-  return low | high << 16;
+  return __byte_perm(__byte_perm(t[0], t[1], 0x0073), __byte_perm(t[2], t[3], 0x0073), 0x5410);
 }
 
 __device__ __forceinline__ float from_e4m3(unsigned int code) {
@@ -281,11 +306,6 @@ __device__ __forceinline__ unsigned int mark_nan(unsigned int codes, const float
   return codes;
 }
 
-struct AdamStep {
-  float factor, keep, rate, correction;
-  unsigned int key;  // of this tensor and step, for the random bits
-};
-
 // A block of 256 elements from b0 on with moments in 8 bits, by one warp: each
 // lane holds two fours (elements 4 lane.. and 128 + 4 lane..), or, where the
 // arrays are not aligned for that, eight elements one by one.
@@ -329,11 +349,13 @@ __device__ __forceinline__ void adam8_block(const AdamEntry& e, const AdamNumber
     }
   }
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    float v = __fmul_rn(r[j], r[j]);
-    moments(k, g[j] * st.factor, m[j], v);
-    r[j] = __fsqrt_rn(v);
-    p[j] = updated(p[j], st.keep, st.rate, st.correction, k.eps, m[j], r[j]);
+  for (int j = 0; j < kPer; j += 2) {
+    Pair m2 = pair(m[j], m[j + 1]), r2 = pair(r[j], r[j + 1]);
+    Pair v2 = r2 * r2;
+    moments(k, pair(g[j], g[j + 1]) * pair(st.factor), m2, v2);
+    r2 = sqrt_pair(v2);
+    const float2 pf = unpair(updated(k, st, pair(p[j], p[j + 1]), m2, r2)), mf = unpair(m2), rf = unpair(r2);
+    p[j] = pf.x, p[j + 1] = pf.y, m[j] = mf.x, m[j + 1] = mf.y, r[j] = rf.x, r[j + 1] = rf.y;
   }
   if (vector) {
 #pragma unroll
@@ -347,22 +369,16 @@ __device__ __forceinline__ void adam8_block(const AdamEntry& e, const AdamNumber
   float m_scale, r_scale, m_inverse, r_inverse;
   const bool m_finite = warp_scale<kPer>(m, &m_scale, &m_inverse);
   const bool r_finite = warp_scale<kPer>(r, &r_scale, &r_inverse);
-  // a block lies on one side of every multiple of 2^32
-  const unsigned int key = STOCHASTIC ? mix(st.key ^ static_cast<unsigned int>(static_cast<uint64_t>(b0) >> 32)) : 0u;
 #pragma unroll
   for (int q = 0; q < kPer / 4; ++q) {
     const int64_t i = b0 + q * 128 + lane * 4;
-    unsigned int m_noise[4], r_noise[4];
+    unsigned int random[4];
     if (STOCHASTIC) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const unsigned int bits = mix((static_cast<unsigned int>(i) + j) ^ key);
-        m_noise[j] = bits >> 12 & 0xFFFF0u;
-        r_noise[j] = bits << 4 & 0xFFFF0u;
-      }
+      for (int j = 0; j < 4; ++j) random[j] = mix((static_cast<unsigned int>(i) | j) ^ st.key);
     }
-    unsigned int mc = to_e4m3_four<STOCHASTIC, false>(m + 4 * q, m_inverse, m_noise);
-    unsigned int rc = to_e4m3_four<STOCHASTIC, true>(r + 4 * q, r_inverse, r_noise);
+    unsigned int mc = to_e4m3_four<STOCHASTIC, true, false>(m + 4 * q, m_inverse, random);
+    unsigned int rc = to_e4m3_four<STOCHASTIC, false, true>(r + 4 * q, r_inverse, random);
     if (!m_finite) mc = mark_nan(mc, m + 4 * q);
     if (!r_finite) rc = mark_nan(rc, r + 4 * q);
     if (vector) {
@@ -399,8 +415,7 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
     rate = 1.f / -expm1f(static_cast<float>(step) * k.log_b1);
     correction = rsqrtf(-expm1f(static_cast<float>(step) * k.log_b2));
   }
-  rate *= lr;
-  const float keep = 1.f - lr * e.decay;
+  AdamStep st = {factor, 1.f - lr * e.decay, rate * lr, correction, 0u};
   const int64_t i0 = static_cast<int64_t>(blockIdx.x - e.chunk0) * kAdamChunk;
   const int64_t i1 = min(i0 + kAdamChunk, e.n);
 
@@ -408,11 +423,11 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
     float* mp = static_cast<float*>(e.m);
     float* vp = static_cast<float*>(e.v);
     const auto one = [&](int64_t i) {
-      float m = mp[i], v = vp[i];
-      moments(k, load_elem(e.grad, e.grad_dtype, i) * factor, m, v);
-      const float p = updated(load_elem(e.param, e.param_dtype, i), keep, rate, correction, k.eps, m, __fsqrt_rn(v));
-      mp[i] = m;
-      vp[i] = v;
+      Pair m = pair(mp[i]), v = pair(vp[i]);
+      moments(k, pair(load_elem(e.grad, e.grad_dtype, i) * factor), m, v);
+      const float p = unpair(updated(k, st, pair(load_elem(e.param, e.param_dtype, i)), m, sqrt_pair(v))).x;
+      mp[i] = unpair(m).x;
+      vp[i] = unpair(v).x;
       store_elem(e.param, e.param_dtype, i, p);
       if (e.copy != nullptr) store_elem(e.copy, e.copy_dtype, i, p);
     };
@@ -426,14 +441,14 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
       float4 m = __ldcs(reinterpret_cast<const float4*>(mp + i)), v = __ldcs(reinterpret_cast<const float4*>(vp + i));
       float4 p = load_four(e.param, e.param_dtype, i);
       const float4 g = load_four(e.grad, e.grad_dtype, i);
-      const auto part = [&](float& p1, float g1, float& m1, float& v1) {
-        moments(k, g1 * factor, m1, v1);
-        p1 = updated(p1, keep, rate, correction, k.eps, m1, __fsqrt_rn(v1));
+      const auto part = [&](float& p0, float& p1, float g0, float g1, float& m0, float& m1, float& v0, float& v1) {
+        Pair m2 = pair(m0, m1), v2 = pair(v0, v1);
+        moments(k, pair(g0, g1) * pair(factor), m2, v2);
+        const float2 pf = unpair(updated(k, st, pair(p0, p1), m2, sqrt_pair(v2))), mf = unpair(m2), vf = unpair(v2);
+        p0 = pf.x, p1 = pf.y, m0 = mf.x, m1 = mf.y, v0 = vf.x, v1 = vf.y;
       };
-      part(p.x, g.x, m.x, v.x);
-      part(p.y, g.y, m.y, v.y);
-      part(p.z, g.z, m.z, v.z);
-      part(p.w, g.w, m.w, v.w);
+      part(p.x, p.y, g.x, g.y, m.x, m.y, v.x, v.y);
+      part(p.z, p.w, g.z, g.w, m.z, m.w, v.z, v.w);
       __stcs(reinterpret_cast<float4*>(mp + i), m);
       __stcs(reinterpret_cast<float4*>(vp + i), v);
       store_four(e.param, e.param_dtype, i, p);
@@ -444,12 +459,12 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
     return;
   }
 
-  AdamStep st = {factor, keep, rate, correction, 0u};
   if (k.stochastic) {
     st.key = mix(k.seed_lo);
     st.key = mix(st.key ^ k.seed_hi);
     st.key = mix(st.key ^ static_cast<unsigned int>(step));
     st.key = mix(st.key ^ static_cast<unsigned int>(e.index));
+    st.key = mix(st.key ^ static_cast<unsigned int>(static_cast<uint64_t>(i0) >> 32));  // the whole chunk's
   }
   for (int64_t b0 = i0 + (threadIdx.x >> 5) * FLCE_ADAMW_BLOCK; b0 < i1; b0 += kThreads / 32 * FLCE_ADAMW_BLOCK) {
     if (k.stochastic)
@@ -616,6 +631,8 @@ flce_status_t adamw_step(const flce_adamw_tensor_t* tensors, int64_t count, cons
   num.rate = static_cast<float>(1 / (1 - pow(u.beta1, t)));
   num.correction = static_cast<float>(1 / sqrt(1 - pow(u.beta2, t)));
   num.grad_scale = u.grad_scale;
+  num.one = 1.f;
+  num.minus_zero = -0.f;
   num.skip_nonfinite = u.skip_nonfinite;
   num.stochastic = u.stochastic;
   num.seed_lo = static_cast<unsigned int>(u.seed);
