@@ -40,10 +40,22 @@ __device__ __forceinline__ void store_elem(void* p, int dtype, int64_t i, float 
 }
 
 // Four elements from i on, which lie on a boundary of four; read or written once
-// (streamed: first to leave the caches).
-__device__ __forceinline__ float4 load_four(const void* p, int dtype, int64_t i) {
-  if (dtype == FLCE_DTYPE_FP32) return __ldcs(reinterpret_cast<const float4*>(static_cast<const float*>(p) + i));
-  const uint2 r = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i));
+// (streamed: first to leave the caches).  Loading and converting are apart, so
+// that several loads are under way before the first is waited for.
+__device__ __forceinline__ uint4 load_four_bits(const void* p, int dtype, int64_t i) {
+  uint4 r = make_uint4(0, 0, 0, 0);
+  if (dtype == FLCE_DTYPE_FP32) {
+    r = __ldcs(reinterpret_cast<const uint4*>(static_cast<const float*>(p) + i));
+  } else {
+    const uint2 h = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i));
+    r.x = h.x;
+    r.y = h.y;
+  }
+  return r;
+}
+__device__ __forceinline__ float4 four_floats(const uint4& r, int dtype) {
+  if (dtype == FLCE_DTYPE_FP32)
+    return make_float4(__uint_as_float(r.x), __uint_as_float(r.y), __uint_as_float(r.z), __uint_as_float(r.w));
   if (dtype == FLCE_DTYPE_BF16)
     return make_float4(__uint_as_float(r.x << 16), __uint_as_float(r.x & 0xFFFF0000u), __uint_as_float(r.y << 16),
                        __uint_as_float(r.y & 0xFFFF0000u));

@@ -17,7 +17,7 @@ namespace flce {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int64_t kMaxElems = int64_t(1) << 46;  // of one tensor
+constexpr int64_t kMaxElems = int64_t(1) << 42;  // of one tensor: its chunks fit a launch
 
 // Entries are ordered by first chunk: the one that holds chunk c.
 template <typename E>
@@ -137,8 +137,12 @@ __global__ void __launch_bounds__(1024)
 
 // -------------------------------------------------------------------- AdamW
 
-constexpr int kAdamChunk = 4096;  // elements of a CTA: a whole number of 8-bit blocks
-static_assert(kAdamChunk % (FLCE_ADAMW_BLOCK * (kThreads / 32)) == 0, "whole blocks for every warp");
+constexpr int kAdamChunk = 4096;   // elements of a CTA
+// With 8-bit moments: two blocks a warp, the second loading while the first is
+// worked on.  525M elements with a 16-bit copy took 1.52 ms so; with one block
+// 1.61 ms, with four 1.86, with eight 1.75.
+constexpr int kAdamChunk8 = 4096;
+static_assert(kAdamChunk8 % (FLCE_ADAMW_BLOCK * (kThreads / 32)) == 0, "whole blocks for every warp");
 constexpr float kE4m3Max = 448.f;
 constexpr unsigned int kE4m3Nan = 0x7Fu;
 
@@ -152,7 +156,7 @@ struct AdamEntry {
   float lr_scale, decay;
   unsigned int chunk0;
   int index;  // place in the call's table
-  int8_t param_dtype, grad_dtype, copy_dtype, bits;
+  int8_t param_dtype, grad_dtype, copy_dtype;
   int head;  // elements before the first vector of four in every array, or -1: the arrays differ in this
 };
 
@@ -306,36 +310,50 @@ __device__ __forceinline__ unsigned int mark_nan(unsigned int codes, const float
   return codes;
 }
 
-// A block of 256 elements from b0 on with moments in 8 bits, by one warp: each
-// lane holds two fours (elements 4 lane.. and 128 + 4 lane..), or, where the
-// arrays are not aligned for that, eight elements one by one.
-template <bool STOCHASTIC>
-__device__ __forceinline__ void adam8_block(const AdamEntry& e, const AdamNumbers& k, const AdamStep& st, int64_t b0) {
-  constexpr int kPer = FLCE_ADAMW_BLOCK / 32;
+// A block of 256 elements with moments in 8 bits belongs to one warp: each lane
+// holds two fours (elements 4 lane.. and 128 + 4 lane..).
+constexpr int kPer = FLCE_ADAMW_BLOCK / 32;
+
+// What a lane loads of a block.
+struct Block8 {
+  uint4 p[kPer / 4], g[kPer / 4];
+  unsigned int m[kPer / 4], r[kPer / 4];
+  float m_scale, r_scale;
+};
+
+__device__ __forceinline__ void load_block(const AdamEntry& e, int64_t b0, int lane, Block8& x) {
+  x.m_scale = e.m_scale[b0 / FLCE_ADAMW_BLOCK];
+  x.r_scale = e.v_scale[b0 / FLCE_ADAMW_BLOCK];
+#pragma unroll
+  for (int q = 0; q < kPer / 4; ++q) {
+    const int64_t i = b0 + q * 128 + lane * 4;
+    x.m[q] = __ldcs(reinterpret_cast<const unsigned int*>(static_cast<const uint8_t*>(e.m) + i));
+    x.r[q] = __ldcs(reinterpret_cast<const unsigned int*>(static_cast<const uint8_t*>(e.v) + i));
+    x.g[q] = load_four_bits(e.grad, e.grad_dtype, i);
+    x.p[q] = load_four_bits(e.param, e.param_dtype, i);
+  }
+}
+
+// Its step.  VECTOR: from what load_block loaded; otherwise (arrays that are not
+// aligned for that, and a tensor's last block) element by element.
+template <bool STOCHASTIC, bool VECTOR>
+__device__ __forceinline__ void step_block(const AdamEntry& e, const AdamNumbers& k, const AdamStep& st, int64_t b0,
+                                           int lane, const Block8& x) {
   uint8_t* mp = static_cast<uint8_t*>(e.m);
   uint8_t* vp = static_cast<uint8_t*>(e.v);
-  const int lane = threadIdx.x & 31;
   const int64_t block = b0 / FLCE_ADAMW_BLOCK;
-  const float ms = e.m_scale[block], vs = e.v_scale[block];
-  const bool vector = e.head == 0 && b0 + FLCE_ADAMW_BLOCK <= e.n;
   float m[kPer], r[kPer], p[kPer], g[kPer];
-  if (vector) {
-    unsigned int mc[kPer / 4], rc[kPer / 4];
+  if (VECTOR) {
 #pragma unroll
     for (int q = 0; q < kPer / 4; ++q) {
-      const int64_t i = b0 + q * 128 + lane * 4;
-      mc[q] = __ldcs(reinterpret_cast<const unsigned int*>(mp + i));
-      rc[q] = __ldcs(reinterpret_cast<const unsigned int*>(vp + i));
-      const float4 gv = load_four(e.grad, e.grad_dtype, i), pv = load_four(e.param, e.param_dtype, i);
+      const float4 gv = four_floats(x.g[q], e.grad_dtype), pv = four_floats(x.p[q], e.param_dtype);
       p[4 * q] = pv.x, p[4 * q + 1] = pv.y, p[4 * q + 2] = pv.z, p[4 * q + 3] = pv.w;
       g[4 * q] = gv.x, g[4 * q + 1] = gv.y, g[4 * q + 2] = gv.z, g[4 * q + 3] = gv.w;
-    }
-#pragma unroll
-    for (int q = 0; q < kPer / 4; ++q) {
-      from_e4m3_four(mc[q], ms, m + 4 * q);
-      from_e4m3_four(rc[q], vs, r + 4 * q);
+      from_e4m3_four(x.m[q], x.m_scale, m + 4 * q);
+      from_e4m3_four(x.r[q], x.r_scale, r + 4 * q);
     }
   } else {
+    const float ms = e.m_scale[block], rs = e.v_scale[block];
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       const int64_t i = b0 + (j >> 2) * 128 + lane * 4 + (j & 3);
@@ -344,7 +362,7 @@ __device__ __forceinline__ void adam8_block(const AdamEntry& e, const AdamNumber
         p[j] = load_elem(e.param, e.param_dtype, i);
         g[j] = load_elem(e.grad, e.grad_dtype, i);
         m[j] = from_e4m3(mp[i]) * ms;
-        r[j] = from_e4m3(vp[i]) * vs;
+        r[j] = from_e4m3(vp[i]) * rs;
       }
     }
   }
@@ -357,7 +375,7 @@ __device__ __forceinline__ void adam8_block(const AdamEntry& e, const AdamNumber
     const float2 pf = unpair(updated(k, st, pair(p[j], p[j + 1]), m2, r2)), mf = unpair(m2), rf = unpair(r2);
     p[j] = pf.x, p[j + 1] = pf.y, m[j] = mf.x, m[j + 1] = mf.y, r[j] = rf.x, r[j + 1] = rf.y;
   }
-  if (vector) {
+  if (VECTOR) {
 #pragma unroll
     for (int q = 0; q < kPer / 4; ++q) {
       const int64_t i = b0 + q * 128 + lane * 4;
@@ -381,7 +399,7 @@ __device__ __forceinline__ void adam8_block(const AdamEntry& e, const AdamNumber
     unsigned int rc = to_e4m3_four<STOCHASTIC, false, true>(r + 4 * q, r_inverse, random);
     if (!m_finite) mc = mark_nan(mc, m + 4 * q);
     if (!r_finite) rc = mark_nan(rc, r + 4 * q);
-    if (vector) {
+    if (VECTOR) {
       __stcs(reinterpret_cast<unsigned int*>(mp + i), mc);
       __stcs(reinterpret_cast<unsigned int*>(vp + i), rc);
     } else {
@@ -395,94 +413,122 @@ __device__ __forceinline__ void adam8_block(const AdamEntry& e, const AdamNumber
         }
     }
   }
+  __syncwarp();  // every lane has read the old scales
   if (lane == 0) {
     e.m_scale[block] = m_scale;
     e.v_scale[block] = r_scale;
   }
 }
 
-template <int MAX>
-__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ AdamArgs<MAX> a) {
-  const AdamEntry& e = a.entry[entry_of(a.entry, a.count, blockIdx.x)];
-  const AdamNumbers& k = a.num;
-  const float factor = k.grad_scale_dev != nullptr ? *k.grad_scale_dev : k.grad_scale;
-  if (k.skip_nonfinite && !isfinite(factor)) return;
+// The numbers of one tensor's step; false: it is to be skipped.
+__device__ __forceinline__ bool step_numbers(const AdamEntry& e, const AdamNumbers& k, AdamStep& st) {
+  st.factor = k.grad_scale_dev != nullptr ? *k.grad_scale_dev : k.grad_scale;
   const float lr = (k.lr_dev != nullptr ? *k.lr_dev : k.lr) * e.lr_scale;
-  float rate = k.rate, correction = k.correction;
+  float rate = k.rate;
+  st.correction = k.correction;
   int64_t step = k.step;
   if (k.step_dev != nullptr) {  // 1 - b^t = -(e^(t ln b) - 1), without the cancellation
     step = *k.step_dev;
     rate = 1.f / -expm1f(static_cast<float>(step) * k.log_b1);
-    correction = rsqrtf(-expm1f(static_cast<float>(step) * k.log_b2));
+    st.correction = rsqrtf(-expm1f(static_cast<float>(step) * k.log_b2));
   }
-  AdamStep st = {factor, 1.f - lr * e.decay, rate * lr, correction, 0u};
-  const int64_t i0 = static_cast<int64_t>(blockIdx.x - e.chunk0) * kAdamChunk;
-  const int64_t i1 = min(i0 + kAdamChunk, e.n);
+  st.rate = rate * lr;
+  st.keep = 1.f - lr * e.decay;
+  st.key = mix(k.seed_lo);
+  st.key = mix(st.key ^ k.seed_hi);
+  st.key = mix(st.key ^ static_cast<unsigned int>(step));
+  st.key = mix(st.key ^ static_cast<unsigned int>(e.index));
+  return !k.skip_nonfinite || isfinite(st.factor);
+}
 
-  if (e.bits == 32) {
-    float* mp = static_cast<float*>(e.m);
-    float* vp = static_cast<float*>(e.v);
-    const auto one = [&](int64_t i) {
-      Pair m = pair(mp[i]), v = pair(vp[i]);
-      moments(k, pair(load_elem(e.grad, e.grad_dtype, i) * factor), m, v);
-      const float p = unpair(updated(k, st, pair(load_elem(e.param, e.param_dtype, i)), m, sqrt_pair(v))).x;
-      mp[i] = unpair(m).x;
-      vp[i] = unpair(v).x;
-      store_elem(e.param, e.param_dtype, i, p);
-      if (e.copy != nullptr) store_elem(e.copy, e.copy_dtype, i, p);
-    };
-    if (e.head < 0) {
-      for (int64_t i = i0 + threadIdx.x; i < i1; i += kThreads) one(i);
-      return;
-    }
-    // vectors of four from element `head` on; what is left at the tensor's ends goes one by one
-    const int64_t whole = e.n - (e.n - e.head) % 4;
-    for (int64_t i = i0 + e.head + threadIdx.x * 4; i < min(i0 + e.head + kAdamChunk, whole); i += kThreads * 4) {
-      float4 m = __ldcs(reinterpret_cast<const float4*>(mp + i)), v = __ldcs(reinterpret_cast<const float4*>(vp + i));
-      float4 p = load_four(e.param, e.param_dtype, i);
-      const float4 g = load_four(e.grad, e.grad_dtype, i);
-      const auto part = [&](float& p0, float& p1, float g0, float g1, float& m0, float& m1, float& v0, float& v1) {
-        Pair m2 = pair(m0, m1), v2 = pair(v0, v1);
-        moments(k, pair(g0, g1) * pair(factor), m2, v2);
-        const float2 pf = unpair(updated(k, st, pair(p0, p1), m2, sqrt_pair(v2))), mf = unpair(m2), vf = unpair(v2);
-        p0 = pf.x, p1 = pf.y, m0 = mf.x, m1 = mf.y, v0 = vf.x, v1 = vf.y;
-      };
-      part(p.x, p.y, g.x, g.y, m.x, m.y, v.x, v.y);
-      part(p.z, p.w, g.z, g.w, m.z, m.w, v.z, v.w);
-      __stcs(reinterpret_cast<float4*>(mp + i), m);
-      __stcs(reinterpret_cast<float4*>(vp + i), v);
-      store_four(e.param, e.param_dtype, i, p);
-      if (e.copy != nullptr) store_four(e.copy, e.copy_dtype, i, p);
-    }
-    if (i0 == 0 && threadIdx.x < e.head) one(threadIdx.x);
-    if (whole + threadIdx.x < e.n && whole < i0 + e.head + kAdamChunk && whole >= i0 + e.head) one(whole + threadIdx.x);
+// Tensors with fp32 moments.  A thread takes four elements of every array at a
+// time; what is left at a tensor's ends goes one by one.
+template <int MAX>
+__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ AdamArgs<MAX> a) {
+  const AdamEntry& e = a.entry[entry_of(a.entry, a.count, blockIdx.x)];
+  const AdamNumbers& k = a.num;
+  AdamStep st;
+  if (!step_numbers(e, k, st)) return;
+  const int64_t i0 = static_cast<int64_t>(blockIdx.x - e.chunk0) * kAdamChunk;
+  float* mp = static_cast<float*>(e.m);
+  float* vp = static_cast<float*>(e.v);
+  const auto one = [&](int64_t i) {
+    Pair m = pair(mp[i]), v = pair(vp[i]);
+    moments(k, pair(load_elem(e.grad, e.grad_dtype, i) * st.factor), m, v);
+    const float p = unpair(updated(k, st, pair(load_elem(e.param, e.param_dtype, i)), m, sqrt_pair(v))).x;
+    mp[i] = unpair(m).x;
+    vp[i] = unpair(v).x;
+    store_elem(e.param, e.param_dtype, i, p);
+    if (e.copy != nullptr) store_elem(e.copy, e.copy_dtype, i, p);
+  };
+  if (e.head < 0) {
+    const int64_t i1 = min(i0 + kAdamChunk, e.n);
+    for (int64_t i = i0 + threadIdx.x; i < i1; i += kThreads) one(i);
     return;
   }
+  // vectors of four from element `head` on
+  const int64_t whole = e.n - (e.n - e.head) % 4;
+  for (int64_t i = i0 + e.head + threadIdx.x * 4; i < min(i0 + e.head + kAdamChunk, whole); i += kThreads * 4) {
+    float4 m = __ldcs(reinterpret_cast<const float4*>(mp + i)), v = __ldcs(reinterpret_cast<const float4*>(vp + i));
+    const uint4 pb = load_four_bits(e.param, e.param_dtype, i), gb = load_four_bits(e.grad, e.grad_dtype, i);
+    float4 p = four_floats(pb, e.param_dtype);
+    const float4 g = four_floats(gb, e.grad_dtype);
+    const auto part = [&](float& p0, float& p1, float g0, float g1, float& m0, float& m1, float& v0, float& v1) {
+      Pair m2 = pair(m0, m1), v2 = pair(v0, v1);
+      moments(k, pair(g0, g1) * pair(st.factor), m2, v2);
+      const float2 pf = unpair(updated(k, st, pair(p0, p1), m2, sqrt_pair(v2))), mf = unpair(m2), vf = unpair(v2);
+      p0 = pf.x, p1 = pf.y, m0 = mf.x, m1 = mf.y, v0 = vf.x, v1 = vf.y;
+    };
+    part(p.x, p.y, g.x, g.y, m.x, m.y, v.x, v.y);
+    part(p.z, p.w, g.z, g.w, m.z, m.w, v.z, v.w);
+    __stcs(reinterpret_cast<float4*>(mp + i), m);
+    __stcs(reinterpret_cast<float4*>(vp + i), v);
+    store_four(e.param, e.param_dtype, i, p);
+    if (e.copy != nullptr) store_four(e.copy, e.copy_dtype, i, p);
+  }
+  if (i0 == 0 && threadIdx.x < e.head) one(threadIdx.x);
+  if (whole + threadIdx.x < e.n && whole < i0 + e.head + kAdamChunk && whole >= i0 + e.head) one(whole + threadIdx.x);
+}
 
-  if (k.stochastic) {
-    st.key = mix(k.seed_lo);
-    st.key = mix(st.key ^ k.seed_hi);
-    st.key = mix(st.key ^ static_cast<unsigned int>(step));
-    st.key = mix(st.key ^ static_cast<unsigned int>(e.index));
-    st.key = mix(st.key ^ static_cast<unsigned int>(static_cast<uint64_t>(i0) >> 32));  // the whole chunk's
+// Tensors with 8-bit moments.  A warp takes blocks, and has the next one's loads
+// under way while it works on one: the two maxima over the block and the roundings
+// behind them are a long chain.
+template <int MAX, bool STOCHASTIC>
+__global__ void __launch_bounds__(kThreads) adamw8_kernel(const __grid_constant__ AdamArgs<MAX> a) {
+  const AdamEntry& e = a.entry[entry_of(a.entry, a.count, blockIdx.x)];
+  const AdamNumbers& k = a.num;
+  constexpr int64_t kStep = kThreads / 32 * FLCE_ADAMW_BLOCK;
+  const int lane = threadIdx.x & 31;
+  const int64_t i0 = static_cast<int64_t>(blockIdx.x - e.chunk0) * kAdamChunk8, i1 = min(i0 + kAdamChunk8, e.n);
+  const int64_t whole = e.head == 0 ? e.n - e.n % FLCE_ADAMW_BLOCK : 0;  // where blocks by vectors end
+  int64_t b0 = i0 + (threadIdx.x >> 5) * FLCE_ADAMW_BLOCK;
+  Block8 next;
+  if (b0 < min(i1, whole)) load_block(e, b0, lane, next);
+  AdamStep st;
+  if (!step_numbers(e, k, st)) return;
+  st.key = mix(st.key ^ static_cast<unsigned int>(static_cast<uint64_t>(i0) >> 32));  // the whole chunk's
+  for (; b0 < min(i1, whole); b0 += kStep) {
+    const Block8 now = next;
+    if (b0 + kStep < min(i1, whole)) load_block(e, b0 + kStep, lane, next);
+    step_block<STOCHASTIC, true>(e, k, st, b0, lane, now);
   }
-  for (int64_t b0 = i0 + (threadIdx.x >> 5) * FLCE_ADAMW_BLOCK; b0 < i1; b0 += kThreads / 32 * FLCE_ADAMW_BLOCK) {
-    if (k.stochastic)
-      adam8_block<true>(e, k, st, b0);
-    else
-      adam8_block<false>(e, k, st, b0);
-  }
+  for (; b0 < i1; b0 += kStep) step_block<STOCHASTIC, false>(e, k, st, b0, lane, next);
 }
 
 template <int MAX>
-cudaError_t launch_adamw(const AdamEntry* entry, int count, unsigned int chunks, const AdamNumbers& num,
+cudaError_t launch_adamw(const AdamEntry* entry, int count, unsigned int chunks, const AdamNumbers& num, int bits,
                          cudaStream_t s) {
   AdamArgs<MAX> a;
   std::copy(entry, entry + count, a.entry);
   a.count = count;
   a.num = num;
   prof_begin(s, FLCE_KERNEL_ADAMW);
-  adamw_kernel<MAX><<<chunks, kThreads, 0, s>>>(a);
+  if (bits == 32)
+    adamw_kernel<MAX><<<chunks, kThreads, 0, s>>>(a);
+  else if (num.stochastic)
+    adamw8_kernel<MAX, true><<<chunks, kThreads, 0, s>>>(a);
+  else
+    adamw8_kernel<MAX, false><<<chunks, kThreads, 0, s>>>(a);
   const cudaError_t e = cudaGetLastError();
   prof_end(s);
   return e;
@@ -493,11 +539,11 @@ constexpr int kAdamEntries = 360, kAdamMiddle = 40, kAdamFew = 4;
 static_assert(sizeof(AdamArgs<kAdamEntries>) <= 32764, "kernel parameters");
 static_assert(sizeof(NormArgs) <= 32764, "kernel parameters");
 
-cudaError_t launch_adamw_any(const AdamEntry* entry, int count, unsigned int chunks, const AdamNumbers& num,
+cudaError_t launch_adamw_any(const AdamEntry* entry, int count, unsigned int chunks, const AdamNumbers& num, int bits,
                              cudaStream_t s) {
-  if (count <= kAdamFew) return launch_adamw<kAdamFew>(entry, count, chunks, num, s);
-  if (count <= kAdamMiddle) return launch_adamw<kAdamMiddle>(entry, count, chunks, num, s);
-  return launch_adamw<kAdamEntries>(entry, count, chunks, num, s);
+  if (count <= kAdamFew) return launch_adamw<kAdamFew>(entry, count, chunks, num, bits, s);
+  if (count <= kAdamMiddle) return launch_adamw<kAdamMiddle>(entry, count, chunks, num, bits, s);
+  return launch_adamw<kAdamEntries>(entry, count, chunks, num, bits, s);
 }
 
 // Elements before every array's first boundary of four, where that is the same
@@ -572,10 +618,7 @@ flce_status_t grad_norm(const flce_tensor_t* tensors, int64_t count, float grad_
       if (tensors[i].n == 0) continue;
       // at least the vectors from the first boundary on (a chunk too many finds nothing)
       const int64_t more = div_up(tensors[i].n, kNormChunk * static_cast<int64_t>(16 / elem_size(tensors[i].dtype)));
-      if (chunks + more > 0x7fffffff) {
-        if (a.count == 0) return FLCE_ERR_UNSUPPORTED;
-        break;
-      }
+      if (chunks + more > 0x7fffffff) break;
       a.entry[a.count++] = {tensors[i].data, tensors[i].n, static_cast<unsigned int>(chunks), tensors[i].dtype};
       chunks += more;
     }
@@ -638,27 +681,26 @@ flce_status_t adamw_step(const flce_adamw_tensor_t* tensors, int64_t count, cons
   num.seed_lo = static_cast<unsigned int>(u.seed);
   num.seed_hi = static_cast<unsigned int>(u.seed >> 32);
   AdamEntry entry[kAdamEntries];
-  for (int64_t i = 0; i < count;) {
-    int filled = 0;
-    int64_t chunks = 0;
-    for (; i < count && filled < kAdamEntries; ++i) {
-      const flce_adamw_tensor_t& x = tensors[i];
-      if (x.n == 0) continue;
-      const int head = common_head(x);
-      const int64_t more = div_up(x.moment_bits == 32 && head > 0 ? x.n - head : x.n, kAdamChunk);
-      if (chunks + more > 0x7fffffff) {
-        if (filled == 0) return FLCE_ERR_UNSUPPORTED;
-        break;
+  for (const int bits : {32, 8}) {
+    for (int64_t i = 0; i < count;) {
+      int filled = 0;
+      int64_t chunks = 0;
+      for (; i < count && filled < kAdamEntries; ++i) {
+        const flce_adamw_tensor_t& x = tensors[i];
+        if (x.n == 0 || x.moment_bits != bits) continue;
+        const int head = common_head(x);
+        const int64_t more = bits == 8 ? div_up(x.n, kAdamChunk8) : div_up(head > 0 ? x.n - head : x.n, kAdamChunk);
+        if (chunks + more > 0x7fffffff) break;
+        entry[filled++] = {x.param, x.grad, x.exp_avg, x.exp_avg_sq, x.exp_avg_scale, x.exp_avg_sq_scale, x.copy, x.n,
+                           x.lr_scale, x.weight_decay, static_cast<unsigned int>(chunks), static_cast<int>(i),
+                           static_cast<int8_t>(x.param_dtype), static_cast<int8_t>(x.grad_dtype),
+                           static_cast<int8_t>(x.copy_dtype), head};
+        chunks += more;
       }
-      entry[filled++] = {x.param, x.grad, x.exp_avg, x.exp_avg_sq, x.exp_avg_scale, x.exp_avg_sq_scale, x.copy, x.n,
-                         x.lr_scale, x.weight_decay, static_cast<unsigned int>(chunks), static_cast<int>(i),
-                         static_cast<int8_t>(x.param_dtype), static_cast<int8_t>(x.grad_dtype),
-                         static_cast<int8_t>(x.copy_dtype), static_cast<int8_t>(x.moment_bits), head};
-      chunks += more;
+      if (filled == 0) break;
+      if (launch_adamw_any(entry, filled, static_cast<unsigned int>(chunks), num, bits, s) != cudaSuccess)
+        return FLCE_ERR_CUDA;
     }
-    if (filled == 0) break;
-    if (launch_adamw_any(entry, filled, static_cast<unsigned int>(chunks), num, s) != cudaSuccess)
-      return FLCE_ERR_CUDA;
   }
   return FLCE_OK;
 }
