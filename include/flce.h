@@ -378,8 +378,8 @@ flce_status_t ce_fwd_bwd_noalloc(const void* logits, int dtype, void* grad_logit
  * input any ld >= 0 (0 repeats one row), for an output ld >= H, at most 2^29.
  * Pointers need
  * the alignment of their elements only; 16-byte aligned rows (pointer and ld)
- * are the fast case.  Except where said, buffers do not overlap.  Rows that
- * hold an infinity or NaN get NaN in that row alone (and in the column sums).
+ * are the fast case.  Except where said, buffers do not overlap.  An infinity
+ * or NaN spoils its own row (and the column sums), no other.
  */
 typedef enum {
   FLCE_NORM_LAYER = 0, /* mean and variance                     */

@@ -53,6 +53,239 @@ __device__ __forceinline__ float2 block_sum2(float2 v, float2* scratch) {
   return v;
 }
 
+// ------------------------------------------------------- rows by 16-byte vectors
+
+// The elements of 16 bytes.
+template <typename T>
+struct Vec;
+template <>
+struct Vec<float> {
+  static constexpr int kN = 4;
+  static __device__ __forceinline__ void unpack(const uint4& r, float* f) {
+    f[0] = __uint_as_float(r.x), f[1] = __uint_as_float(r.y), f[2] = __uint_as_float(r.z), f[3] = __uint_as_float(r.w);
+  }
+  static __device__ __forceinline__ uint4 pack(const float* f) {
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+  }
+};
+template <>
+struct Vec<__nv_bfloat16> {
+  static constexpr int kN = 8;
+  static __device__ __forceinline__ void unpack(const uint4& r, float* f) {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) f[2 * k] = bf16_lo(w[k]), f[2 * k + 1] = bf16_hi(w[k]);
+  }
+  static __device__ __forceinline__ uint4 pack(const float* f) {
+    return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                      pack_bf16x2(f[6], f[7]));
+  }
+};
+template <>
+struct Vec<__half> {
+  static constexpr int kN = 8;
+  static __device__ __forceinline__ void unpack(const uint4& r, float* f) {
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 v = __half22float2(reinterpret_cast<const __half2&>(w[k]));
+      f[2 * k] = v.x, f[2 * k + 1] = v.y;
+    }
+  }
+  static __device__ __forceinline__ uint4 pack(const float* f) {
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const __half2 h = __floats2half2_rn(f[2 * k], f[2 * k + 1]);
+      w[k] = reinterpret_cast<const uint32_t&>(h);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+};
+
+// A row as the 16-byte vectors that cover it.  Without SHIFTED the row is a whole
+// number of them.  With it the row starts `shift` elements into its first one and
+// ends anywhere in its last: these two are read and written element by element,
+// what is not the row's reading as 0.
+template <typename T, bool SHIFTED>
+struct Row {
+  static constexpr int kN = Vec<T>::kN;
+  int shift, length, vectors;
+  __device__ __forceinline__ Row(const void* first, int64_t H) {
+    length = static_cast<int>(H);
+    shift = SHIFTED ? static_cast<int>(reinterpret_cast<uintptr_t>(first) % 16 / sizeof(T)) : 0;
+    vectors = (shift + length + kN - 1) / kN;
+  }
+  __device__ __forceinline__ int column(int j) const { return j * kN - shift; }  // of vector j's first element
+  __device__ __forceinline__ bool whole(int j) const {
+    return !SHIFTED || (j * kN >= shift && (j + 1) * kN <= shift + length);
+  }
+  __device__ __forceinline__ bool inside(int c) const { return !SHIFTED || (c >= 0 && c < length); }
+  __device__ __forceinline__ uint4 load(const T* row, int j) const {
+    if (whole(j)) return *reinterpret_cast<const uint4*>(row + column(j));
+    float f[kN];
+#pragma unroll
+    for (int k = 0; k < kN; ++k) f[k] = inside(column(j) + k) ? to_float(row[column(j) + k]) : 0.f;
+    return Vec<T>::pack(f);
+  }
+  __device__ __forceinline__ void store(T* row, int j, const uint4& v) const {
+    if (whole(j)) {
+      *reinterpret_cast<uint4*>(row + column(j)) = v;
+      return;
+    }
+    float f[kN];
+    Vec<T>::unpack(v, f);
+#pragma unroll
+    for (int k = 0; k < kN; ++k)
+      if (inside(column(j) + k)) row[column(j) + k] = from_float<T>(f[k]);
+  }
+  // Weights or biases of vector j's columns (which never change while a kernel runs).
+  __device__ __forceinline__ void params(const void* p, int dtype, int j, float* f) const {
+    const int c = column(j);
+    if (!SHIFTED) {
+#pragma unroll
+      for (int k = 0; k < kN; k += 4) {
+        float4 v;
+        if (dtype == FLCE_DTYPE_FP32) {
+          v = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + c + k));
+        } else {
+          const uint2 h = __ldg(reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + c + k));
+          v = four_floats(make_uint4(h.x, h.y, 0, 0), dtype);
+        }
+        f[k] = v.x, f[k + 1] = v.y, f[k + 2] = v.z, f[k + 3] = v.w;
+      }
+      return;
+    }
+    int at[kN];
+#pragma unroll
+    for (int k = 0; k < kN; ++k) at[k] = min(max(c + k, 0), length - 1);
+    if (dtype == FLCE_DTYPE_FP32) {
+#pragma unroll
+      for (int k = 0; k < kN; ++k) f[k] = __ldg(static_cast<const float*>(p) + at[k]);
+    } else if (dtype == FLCE_DTYPE_BF16) {
+#pragma unroll
+      for (int k = 0; k < kN; ++k) f[k] = to_float(__ldg(static_cast<const __nv_bfloat16*>(p) + at[k]));
+    } else {
+#pragma unroll
+      for (int k = 0; k < kN; ++k) f[k] = to_float(__ldg(static_cast<const __half*>(p) + at[k]));
+    }
+  }
+};
+
+// Sum over a row's threads: one warp, or the CTA (`scratch`: 32 numbers that no
+// other sum of the kernel uses).
+template <bool WARP>
+__device__ __forceinline__ float row_sum(float v, float* scratch) {
+  v = warp_sum(v);
+  if (WARP) return v;
+  const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
+  if (lane == 0) scratch[threadIdx.x >> 5] = v;
+  __syncthreads();
+  return warp_sum(lane < warps ? scratch[lane] : 0.f);
+}
+
+// Forward with the row in registers, VPT vectors a thread: a warp (WARP) or a CTA
+// takes one row, which is read once; the mean and then the sum of squares about it
+// are taken from the registers.
+template <typename T, bool RMS, int VPT, bool WARP, bool SHIFTED>
+__global__ void __launch_bounds__(WARP ? 256 : 1024) ln_fwd_kernel(const LnForward p) {
+  using V = Vec<T>;
+  __shared__ float scratch[2][32];
+  const int threads = WARP ? 32 : blockDim.x, t = WARP ? threadIdx.x & 31 : threadIdx.x;
+  const int64_t n = WARP ? static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
+  if (n >= p.N) return;
+  const T* x = static_cast<const T*>(p.x) + n * p.ld_x;
+  const Row<T, SHIFTED> row(x, p.H);
+  uint4 v[VPT];
+#pragma unroll
+  for (int k = 0; k < VPT; ++k) {
+    const int j = t + k * threads;
+    v[k] = j < row.vectors ? row.load(x, j) : make_uint4(0, 0, 0, 0);
+  }
+  if (p.residual != nullptr) {
+    const T* r = static_cast<const T*>(p.residual) + n * p.ld_residual;
+    uint4 w[VPT];
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+      const int j = t + k * threads;
+      w[k] = j < row.vectors ? row.load(r, j) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+      float a[V::kN], b[V::kN];
+      V::unpack(v[k], a);
+      V::unpack(w[k], b);
+#pragma unroll
+      for (int i = 0; i < V::kN; ++i) a[i] += b[i];
+      v[k] = V::pack(a);
+    }
+    if (p.sum != nullptr) {
+      T* s = static_cast<T*>(p.sum) + n * p.ld_sum;
+#pragma unroll
+      for (int k = 0; k < VPT; ++k)
+        if (t + k * threads < row.vectors) row.store(s, t + k * threads, v[k]);
+    }
+  }
+  const float over = 1.f / static_cast<float>(row.length);
+  float mu = 0.f;
+  if (!RMS) {
+    float a = 0.f;
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+      float f[V::kN];
+      V::unpack(v[k], f);
+#pragma unroll
+      for (int i = 0; i < V::kN; ++i) a += f[i];
+    }
+    mu = row_sum<WARP>(a, scratch[0]) * over;
+  }
+  float q = 0.f;
+#pragma unroll
+  for (int k = 0; k < VPT; ++k) {
+    const int j = t + k * threads;
+    if (RMS || j < row.vectors) {
+      const bool all = RMS || row.whole(j);
+      float f[V::kN];
+      V::unpack(v[k], f);
+#pragma unroll
+      for (int i = 0; i < V::kN; ++i) {
+        const float d = f[i] - mu;
+        if (all || row.inside(row.column(j) + i)) q = fmaf(d, d, q);
+      }
+    }
+  }
+  q = row_sum<WARP>(q, scratch[1]) * over;
+  const float inv = rsqrtf(q + p.eps);
+  T* y = static_cast<T*>(p.y) + n * p.ld_y;
+#pragma unroll
+  for (int k = 0; k < VPT; ++k) {
+    const int j = t + k * threads;
+    if (j < row.vectors) {
+      float f[V::kN];
+      V::unpack(v[k], f);
+#pragma unroll
+      for (int i = 0; i < V::kN; ++i) f[i] = (f[i] - mu) * inv;
+      if (p.weight != nullptr) {
+        float w[V::kN];
+        row.params(p.weight, p.param_dtype, j, w);
+#pragma unroll
+        for (int i = 0; i < V::kN; ++i) f[i] *= w[i];
+      }
+      if (p.bias != nullptr) {
+        float b[V::kN];
+        row.params(p.bias, p.param_dtype, j, b);
+#pragma unroll
+        for (int i = 0; i < V::kN; ++i) f[i] += b[i];
+      }
+      row.store(y, j, V::pack(f));
+    }
+  }
+  if (t == 0) {
+    if (p.mean != nullptr) p.mean[n] = mu;
+    if (p.rstd != nullptr) p.rstd[n] = inv;
+  }
+}
+
 // ------------------------------------------------------- any layout, by elements
 
 constexpr int kAnyThreads = 256;
@@ -184,11 +417,68 @@ __global__ void __launch_bounds__(1024)
 
 // ------------------------------------------------------------------ launches
 
+// How a call's matrices lie to 16-byte vectors.
+enum Fit {
+  kFitNot,      // rows of different matrices start at different places of a vector
+  kFitShifted,  // at the same place, row by row
+  kFitWhole     // at a vector's start, with a whole number of vectors
+};
+
+struct Matrix {
+  const void* p;
+  int64_t ld;
+};
+
+template <typename T, typename... M>
+Fit fit_of(int64_t N, int64_t H, const void* weight, const void* bias, int param_dtype, M... matrices) {
+  const Matrix all[] = {matrices...};
+  const size_t params = 4 * elem_size(param_dtype);  // parameters are read by fours
+  bool whole = H % Vec<T>::kN == 0 && aligned_to(weight, params) && aligned_to(bias, params);
+  const uintptr_t start = reinterpret_cast<uintptr_t>(all[0].p) % 16;
+  const uintptr_t step = N > 1 ? static_cast<uintptr_t>(all[0].ld) * sizeof(T) % 16 : 0;
+  for (const Matrix& m : all) {
+    if (m.p == nullptr) continue;
+    const uintptr_t s = reinterpret_cast<uintptr_t>(m.p) % 16;
+    const uintptr_t d = N > 1 ? static_cast<uintptr_t>(m.ld) * sizeof(T) % 16 : 0;
+    if (s != start || d != step) return kFitNot;
+    whole = whole && s == 0 && d == 0;
+  }
+  return whole ? kFitWhole : kFitShifted;
+}
+
+// Most vectors of a row that the register forms take (eight for each of 1024 threads).
+constexpr int64_t kMaxRowVectors = 8192;
+
+template <typename T, bool RMS, bool SHIFTED>
+void forward_rows(const LnForward& p, int64_t vectors, cudaStream_t s) {
+  const unsigned int rows = static_cast<unsigned int>(p.N), warps = 4;
+  const unsigned int grid = (rows + warps - 1) / warps;
+  if (vectors <= 32) {
+    ln_fwd_kernel<T, RMS, 1, true, SHIFTED><<<grid, 32 * warps, 0, s>>>(p);
+  } else if (vectors <= 64) {
+    ln_fwd_kernel<T, RMS, 2, true, SHIFTED><<<grid, 32 * warps, 0, s>>>(p);
+  } else if (vectors <= 128) {
+    ln_fwd_kernel<T, RMS, 4, true, SHIFTED><<<grid, 32 * warps, 0, s>>>(p);
+  } else if (vectors <= 4096) {
+    ln_fwd_kernel<T, RMS, 4, false, SHIFTED><<<rows, static_cast<unsigned int>(div_up(vectors, 128) * 32), 0, s>>>(p);
+  } else {
+    ln_fwd_kernel<T, RMS, 8, false, SHIFTED><<<rows, 1024, 0, s>>>(p);
+  }
+}
+
 template <typename T, bool RMS>
 cudaError_t forward(const LnForward& p, cudaStream_t s) {
-  const int grid = static_cast<int>(std::min<int64_t>(p.N, int64_t(8) * device_sm_count()));
+  const Fit fit = fit_of<T>(p.N, p.H, p.weight, p.bias, p.param_dtype, Matrix{p.x, p.ld_x},
+                            Matrix{p.residual, p.ld_residual}, Matrix{p.y, p.ld_y}, Matrix{p.sum, p.ld_sum});
+  const int64_t vectors = fit == kFitWhole ? p.H / Vec<T>::kN : div_up(p.H + Vec<T>::kN - 1, Vec<T>::kN);
   prof_begin(s, FLCE_KERNEL_LN_FWD);
-  ln_fwd_any_kernel<T, RMS><<<grid, kAnyThreads, 0, s>>>(p);
+  if (fit == kFitNot || vectors > kMaxRowVectors)
+    ln_fwd_any_kernel<T, RMS>
+        <<<static_cast<int>(std::min<int64_t>(p.N, int64_t(8) * device_sm_count())), kAnyThreads, 0, s>>>(p);
+  else if (fit == kFitWhole)
+    forward_rows<T, RMS, false>(p, vectors, s);
+  else
+    forward_rows<T, RMS, true>(p, vectors, s);
   const cudaError_t e = cudaGetLastError();
   prof_end(s);
   return e;
