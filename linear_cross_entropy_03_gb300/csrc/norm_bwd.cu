@@ -1,0 +1,470 @@
+// Layer norm, and its form without the mean (rms), in front of the head: the
+// backward pass, with the column sums that give the weight's and the bias's
+// gradient.
+//
+// Every element is moved once (3 N H b bytes, 4 N H b with the gradient of the
+// residual stream), with about fifteen operations on it: memory bandwidth bounds it.
+#include <math.h>
+
+#include "norm.cuh"
+
+namespace flce {
+namespace {
+
+// Column sums of the backward pass are taken by at most this many CTAs, each
+// leaving one partial row of H sums (the workspace holds them all).
+constexpr int kMaxParts = 304;
+
+struct LnBackward {
+  const void *grad_y, *x, *weight, *grad_sum;
+  const float *mean, *rstd;
+  void* grad_x;
+  int64_t ld_grad_y, ld_x, ld_grad_sum, ld_grad_x, N, H;
+  int param_dtype;
+  float2* row_terms;   // [N]: mean(u) * rstd, mean(u * xhat) * rstd
+  float *part_w, *part_b;  // [parts][H]
+  int parts;
+};
+
+// ------------------------------------------------------- rows by 16-byte vectors
+
+// 16 bytes from global to shared memory, without a register between; the thread
+// that issued it sees them after copies_arrived.
+__device__ __forceinline__ void copy_16(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_issued() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LATER>
+__device__ __forceinline__ void copies_arrived() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(LATER) : "memory");
+}
+
+// A barrier of `threads` threads (whole warps) of the CTA; 0 is __syncthreads'.
+__device__ __forceinline__ void group_barrier(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+constexpr int kMaxGroups = 15;  // named barriers 1 to 15
+
+// grad_x and column sums.  `group` threads take a row, VPT vectors each, and a CTA
+// holds as many such groups as fit.  A thread keeps its columns from row to row, so
+// that the sums over the rows stay in its registers until the end; so where rows
+// start inside a vector, a group takes only rows that start at the same place (every
+// eighth, or every fourth fp32 one).  Rows are fetched DEPTH ahead into shared memory
+// by asynchronous copies, each thread its own vectors: nothing waits for another
+// thread but the two sums over the row.
+template <typename T, bool RMS, bool BIAS, int VPT, int DEPTH, bool SHIFTED>
+__global__ void __launch_bounds__(1024) ln_bwd_kernel(const LnBackward p, int group, int groups) {
+  using V = Vec<T>;
+  constexpr int kN = V::kN;
+  extern __shared__ __align__(16) unsigned char ring[];
+  __shared__ float2 scratch[2][kMaxGroups + 1][32];
+  const int in_cta = threadIdx.x / group, t = threadIdx.x % group, lane = threadIdx.x & 31;
+  const int warps = group >> 5, warp = t >> 5;
+  const int64_t all = static_cast<int64_t>(gridDim.x) * groups;
+  const int64_t id = static_cast<int64_t>(blockIdx.x) * groups + in_cta;
+  const int64_t n0 = id, step = all;  // rows n0, n0 + step, ... (SHIFTED: step a multiple of kN)
+  const Row<T, SHIFTED> row(static_cast<const T*>(p.x) + n0 * p.ld_x, p.H);
+  const int arrays = p.grad_sum != nullptr ? 3 : 2;
+  const uint32_t stage_bytes = static_cast<uint32_t>(blockDim.x) * VPT * 16 * arrays;
+  unsigned char* mine = ring + threadIdx.x * 16;
+  const auto slot = [&](int stage, int array, int k) {
+    return mine + stage * stage_bytes + (array * VPT + k) * blockDim.x * 16;
+  };
+  const T* const base[3] = {static_cast<const T*>(p.grad_y), static_cast<const T*>(p.x), static_cast<const T*>(p.grad_sum)};
+  const int64_t ld[3] = {p.ld_grad_y, p.ld_x, p.ld_grad_sum};
+  const auto fetch = [&](int64_t n, int stage) {
+#pragma unroll
+    for (int a = 0; a < 3; ++a) {
+      if (a < arrays) {
+        const T* from = base[a] + n * ld[a];
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+          const int j = t + k * group;
+          if (j < row.vectors) {
+            const T* vector = from + row.column(j);
+            // a vector at a row's end may hold other rows' elements (masked later), but nothing outside the matrix
+            if (row.whole(j) || (vector >= base[a] && vector + kN <= base[a] + (p.N - 1) * ld[a] + p.H))
+              copy_16(smem_addr(slot(stage, a, k)), vector);
+            else
+              *reinterpret_cast<uint4*>(slot(stage, a, k)) = row.load(from, j);
+          }
+        }
+      }
+    }
+  };
+  // The row's elements of a vector, 0 outside the row.
+  const auto elements = [&](int stage, int array, int k, float* f) {
+    V::unpack(*reinterpret_cast<const uint4*>(slot(stage, array, k)), f);
+    const int j = t + k * group;
+    if (SHIFTED && !row.whole(j)) {
+#pragma unroll
+      for (int i = 0; i < kN; ++i)
+        if (!row.inside(row.column(j) + i)) f[i] = 0.f;
+    }
+  };
+#pragma unroll
+  for (int d = 0; d < DEPTH - 1; ++d) {
+    if (n0 + d * step < p.N) fetch(n0 + d * step, d);
+    copies_issued();
+  }
+  grid_dependents_launch();
+
+  float sw[VPT][kN], sb[BIAS ? VPT : 1][kN], w[VPT == 1 ? kN : 1];
+#pragma unroll
+  for (int k = 0; k < VPT; ++k)
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      sw[k][i] = 0.f;
+      if (BIAS) sb[k][i] = 0.f;
+    }
+  const auto weights = [&](int k, float* f) {
+    if (p.weight != nullptr && t + k * group < row.vectors) {
+      row.params(p.weight, p.param_dtype, t + k * group, f);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kN; ++i) f[i] = 1.f;
+    }
+  };
+  if (VPT == 1) weights(0, w);  // kept; with more vectors read again (from the first-level cache)
+  const float over = 1.f / static_cast<float>(p.H);
+  float next_mu = 0.f, next_inv = 0.f;
+  if (n0 < p.N) {
+    next_mu = RMS ? 0.f : p.mean[n0];
+    next_inv = p.rstd[n0];
+  }
+  int stage = 0, turn = 0;
+  for (int64_t n = n0; n < p.N; n += step) {
+    const float mu = next_mu, inv = next_inv;
+    if (n + step < p.N) {
+      next_mu = RMS ? 0.f : p.mean[n + step];
+      next_inv = p.rstd[n + step];
+    }
+    copies_arrived<DEPTH - 2>();
+    // the next row to fetch goes where this thread's part of the row before this one was
+    if (n + (DEPTH - 1) * step < p.N) fetch(n + (DEPTH - 1) * step, stage == 0 ? DEPTH - 1 : stage - 1);
+    copies_issued();
+    float2 s = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+      if (t + k * group < row.vectors) {
+        float g[kN], x[kN], wk[kN];
+        elements(stage, 0, k, g);
+        elements(stage, 1, k, x);
+        if (VPT > 1) weights(k, wk);
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+          const float xhat = (x[i] - mu) * inv, u = g[i] * (VPT > 1 ? wk[i] : w[i]);
+          sw[k][i] = fmaf(g[i], xhat, sw[k][i]);
+          if (BIAS) sb[k][i] += g[i];
+          if (!RMS) s.x += u;
+          s.y = fmaf(u, xhat, s.y);
+        }
+      }
+    }
+    if (!RMS) s.x = warp_sum(s.x);
+    s.y = warp_sum(s.y);
+    if (warps > 1) {
+      // one barrier a row: the scratch of a row is written again two rows later
+      if (lane == 0) scratch[turn][in_cta][warp] = s;
+      group_barrier(1 + in_cta, group);
+      s = lane < warps ? scratch[turn][in_cta][lane] : make_float2(0.f, 0.f);
+      if (!RMS) s.x = warp_sum(s.x);
+      s.y = warp_sum(s.y);
+      turn ^= 1;
+    }
+    const float c1 = s.x * over, c2 = s.y * over;
+    if (p.grad_x != nullptr) {
+      T* to = static_cast<T*>(p.grad_x) + n * p.ld_grad_x;
+#pragma unroll
+      for (int k = 0; k < VPT; ++k) {
+        const int j = t + k * group;
+        if (j < row.vectors) {
+          float g[kN], x[kN], wk[kN];
+          V::unpack(*reinterpret_cast<const uint4*>(slot(stage, 0, k)), g);
+          V::unpack(*reinterpret_cast<const uint4*>(slot(stage, 1, k)), x);
+          if (VPT > 1) weights(k, wk);
+#pragma unroll
+          for (int i = 0; i < kN; ++i) {
+            const float xhat = (x[i] - mu) * inv, u = g[i] * (VPT > 1 ? wk[i] : w[i]);
+            g[i] = (u - c1 - xhat * c2) * inv;
+          }
+          if (arrays == 3) {
+            V::unpack(*reinterpret_cast<const uint4*>(slot(stage, 2, k)), x);
+#pragma unroll
+            for (int i = 0; i < kN; ++i) g[i] += x[i];
+          }
+          row.store(to, j, V::pack(g));
+        }
+      }
+    }
+    stage = stage == DEPTH - 1 ? 0 : stage + 1;
+  }
+
+  if (p.part_w == nullptr && p.part_b == nullptr) return;
+  // the CTA's groups one after another into shared memory, or, with one, as they are
+  float* part_w = p.part_w != nullptr ? p.part_w + static_cast<int64_t>(blockIdx.x) * p.H : nullptr;
+  float* part_b = BIAS && p.part_b != nullptr ? p.part_b + static_cast<int64_t>(blockIdx.x) * p.H : nullptr;
+  float* sum_w = groups > 1 ? reinterpret_cast<float*>(ring) : part_w;
+  float* sum_b = groups > 1 ? sum_w + p.H : part_b;
+  copies_arrived<0>();
+  for (int turns = 0; turns < groups; ++turns) {
+    __syncthreads();
+    if (in_cta != turns) continue;
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+      const int j = t + k * group;
+      if (j < row.vectors) {
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+          const int c = row.column(j) + i;
+          if (row.inside(c)) {
+            if (sum_w != nullptr) sum_w[c] = turns == 0 ? sw[k][i] : sum_w[c] + sw[k][i];
+            if (BIAS && sum_b != nullptr) sum_b[c] = turns == 0 ? sb[k][i] : sum_b[c] + sb[k][i];
+          }
+        }
+      }
+    }
+  }
+  if (groups == 1) return;
+  __syncthreads();
+  for (int c = threadIdx.x; c < row.length; c += blockDim.x) {
+    if (part_w != nullptr) part_w[c] = sum_w[c];
+    if (part_b != nullptr) part_b[c] = sum_b[c];
+  }
+}
+
+// ------------------------------------------------------- any layout, by elements
+
+// The two row means of the backward pass, one CTA a row.
+template <typename T, bool RMS>
+__global__ void __launch_bounds__(kAnyThreads) ln_bwd_rows_any_kernel(const LnBackward p) {
+  __shared__ float2 scratch[32];
+  for (int64_t n = blockIdx.x; n < p.N; n += gridDim.x) {
+    const T* x = static_cast<const T*>(p.x) + n * p.ld_x;
+    const T* g = static_cast<const T*>(p.grad_y) + n * p.ld_grad_y;
+    const float mu = RMS ? 0.f : p.mean[n], inv = p.rstd[n];
+    float2 a = make_float2(0.f, 0.f);
+    for (int64_t h = threadIdx.x; h < p.H; h += kAnyThreads) {
+      float u = to_float(g[h]);
+      if (p.weight != nullptr) u *= load_elem(p.weight, p.param_dtype, h);
+      a.x += u;
+      a.y += u * ((to_float(x[h]) - mu) * inv);
+    }
+    a = block_sum2(a, scratch);
+    if (threadIdx.x == 0) p.row_terms[n] = make_float2(RMS ? 0.f : a.x / p.H, a.y / p.H);
+  }
+}
+
+// grad_x and the column sums, 64 columns by 4 rows a CTA at a time: CTA
+// (c, s) takes columns 64 c.. and the s-th of gridDim.y ranges of rows.
+template <typename T, bool RMS>
+__global__ void __launch_bounds__(kAnyThreads) ln_bwd_cols_any_kernel(const LnBackward p) {
+  __shared__ float2 scratch[4][64];
+  const int col = threadIdx.x & 63, lane = threadIdx.x >> 6;
+  const int64_t h = static_cast<int64_t>(blockIdx.x) * 64 + col;
+  const int64_t per = (p.N + gridDim.y - 1) / gridDim.y;
+  const int64_t n0 = per * blockIdx.y, n1 = min(n0 + per, p.N);
+  float sw = 0.f, sb = 0.f;
+  if (h < p.H) {
+    const float w = p.weight != nullptr ? load_elem(p.weight, p.param_dtype, h) : 1.f;
+    for (int64_t n = n0 + lane; n < n1; n += 4) {
+      const float mu = RMS ? 0.f : p.mean[n], inv = p.rstd[n];
+      const float g = to_float(static_cast<const T*>(p.grad_y)[n * p.ld_grad_y + h]);
+      const float xhat = (to_float(static_cast<const T*>(p.x)[n * p.ld_x + h]) - mu) * inv;
+      sw += g * xhat;
+      sb += g;
+      if (p.grad_x != nullptr) {
+        const float2 t = p.row_terms[n];
+        float o = (g * w - t.x - xhat * t.y) * inv;
+        if (p.grad_sum != nullptr) o += to_float(static_cast<const T*>(p.grad_sum)[n * p.ld_grad_sum + h]);
+        static_cast<T*>(p.grad_x)[n * p.ld_grad_x + h] = from_float<T>(o);
+      }
+    }
+  }
+  scratch[lane][col] = make_float2(sw, sb);
+  __syncthreads();
+  if (lane == 0 && h < p.H) {
+    float2 a = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      a.x += scratch[k][col].x;
+      a.y += scratch[k][col].y;
+    }
+    if (p.part_w != nullptr) p.part_w[static_cast<int64_t>(blockIdx.y) * p.H + h] = a.x;
+    if (p.part_b != nullptr) p.part_b[static_cast<int64_t>(blockIdx.y) * p.H + h] = a.y;
+  }
+}
+
+// Adds the partial rows of column sums in a fixed order: 32 columns by 32
+// lanes a CTA, blockIdx.y 0 the weight's and 1 the bias's.
+__global__ void __launch_bounds__(1024)
+    ln_reduce_kernel(const float* part_w, const float* part_b, int parts, int64_t H, float* grad_weight,
+                     float* grad_bias, int accumulate) {
+  __shared__ float scratch[32][33];
+  grid_dependency_wait();
+  const float* part = blockIdx.y == 0 ? part_w : part_b;
+  float* out = blockIdx.y == 0 ? grad_weight : grad_bias;
+  if (out == nullptr) return;
+  const int col = threadIdx.x & 31, lane = threadIdx.x >> 5;
+  const int64_t h = static_cast<int64_t>(blockIdx.x) * 32 + col;
+  float a = 0.f;
+  if (h < H) {
+#pragma unroll 5
+    for (int k = lane; k < parts; k += 32) a += part[static_cast<int64_t>(k) * H + h];
+  }
+  scratch[lane][col] = a;
+  __syncthreads();
+  a = warp_sum(scratch[col][lane]);  // lane `col` of warp `lane`: partial `col` of column `lane`
+  const int64_t ho = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+  if (col == 0 && ho < H) out[ho] = accumulate ? out[ho] + a : a;
+}
+
+// ------------------------------------------------------------------ launches
+
+cudaError_t reduce_columns(const LnBackward& p, float* grad_weight, float* grad_bias, int accumulate,
+                           cudaStream_t s) {
+  if (grad_weight == nullptr && grad_bias == nullptr) return cudaSuccess;
+  prof_begin(s, FLCE_KERNEL_LN_REDUCE);
+  const cudaError_t e =
+      launch_after(ln_reduce_kernel, dim3(static_cast<unsigned>(div_up(p.H, 32)), 2), dim3(1024), s,
+                   static_cast<const float*>(p.part_w), static_cast<const float*>(p.part_b), p.parts, p.H, grad_weight,
+                   grad_bias, accumulate);
+  prof_end(s);
+  return e;
+}
+
+// Most vectors of a row that the vector form takes (two for each of 1024 threads).
+constexpr int64_t kMaxRowVectors = 2048;
+
+template <typename T, bool RMS, bool BIAS, int VPT, int DEPTH, bool SHIFTED>
+cudaError_t backward_rows(LnBackward& p, int64_t vectors, cudaStream_t s) {
+  constexpr int kN = Vec<T>::kN;
+  const int group = static_cast<int>(div_up(vectors, 32 * VPT) * 32);
+  const int groups = std::max(1, std::min(512 / group, kMaxGroups));
+  const int threads = group * groups;
+  const size_t smem = static_cast<size_t>(threads) * VPT * 16 * (p.grad_sum != nullptr ? 3 : 2) * DEPTH;
+  const int64_t most = threads <= 512 ? 2 * device_sm_count() : device_sm_count();
+  int64_t grid = std::min<int64_t>({div_up(p.N, groups), most, kMaxParts});
+  if (SHIFTED) {  // groups a multiple of kN
+    int64_t unit = kN;
+    while (unit > 1 && groups * (unit / 2) % kN == 0) unit /= 2;
+    grid = std::min<int64_t>(div_up(grid, unit), kMaxParts / unit) * unit;
+  }
+  p.parts = static_cast<int>(grid);
+  const auto kernel = ln_bwd_kernel<T, RMS, BIAS, VPT, DEPTH, SHIFTED>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  kernel<<<static_cast<unsigned int>(grid), threads, smem, s>>>(p, group, groups);
+  return cudaGetLastError();
+}
+
+template <typename T, bool RMS, bool BIAS, bool SHIFTED>
+cudaError_t backward_rows(LnBackward& p, int64_t vectors, cudaStream_t s) {
+  return vectors <= 1024 ? backward_rows<T, RMS, BIAS, 1, 4, SHIFTED>(p, vectors, s)
+                         : backward_rows<T, RMS, BIAS, 2, 2, SHIFTED>(p, vectors, s);
+}
+
+template <typename T, bool RMS>
+cudaError_t backward(LnBackward p, float* grad_weight, float* grad_bias, int accumulate, cudaStream_t s) {
+  p.parts = 0;
+  const Fit fit = fit_of<T>(p.N, p.H, p.weight, nullptr, p.param_dtype, Matrix{p.x, p.ld_x},
+                            Matrix{p.grad_y, p.ld_grad_y}, Matrix{p.grad_sum, p.ld_grad_sum},
+                            Matrix{p.grad_x, p.ld_grad_x});
+  const int64_t vectors = fit == kFitWhole ? p.H / Vec<T>::kN : div_up(p.H + Vec<T>::kN - 1, Vec<T>::kN);
+  cudaError_t e = cudaSuccess;
+  if (p.N > 0 && fit != kFitNot && vectors <= kMaxRowVectors) {
+    prof_begin(s, FLCE_KERNEL_LN_BWD);
+    // a bias is rare without a mean and usual with one: without a mean it has a form of its own
+    if (RMS && p.part_b == nullptr)
+      e = fit == kFitWhole ? backward_rows<T, RMS, !RMS, false>(p, vectors, s)
+                           : backward_rows<T, RMS, !RMS, true>(p, vectors, s);
+    else
+      e = fit == kFitWhole ? backward_rows<T, RMS, true, false>(p, vectors, s)
+                           : backward_rows<T, RMS, true, true>(p, vectors, s);
+    prof_end(s);
+    if (e != cudaSuccess) return e;
+  } else if (p.N > 0) {
+    const int sms = device_sm_count();
+    if (p.grad_x != nullptr) {
+      prof_begin(s, FLCE_KERNEL_LN_BWD);
+      ln_bwd_rows_any_kernel<T, RMS>
+          <<<static_cast<int>(std::min<int64_t>(p.N, int64_t(8) * sms)), kAnyThreads, 0, s>>>(p);
+      e = cudaGetLastError();
+      prof_end(s);
+      if (e != cudaSuccess) return e;
+    }
+    const int64_t strips = div_up(p.H, 64);
+    p.parts = static_cast<int>(std::min<int64_t>({div_up(int64_t(8) * sms, strips), div_up(p.N, 4), kMaxParts}));
+    prof_begin(s, FLCE_KERNEL_LN_BWD);
+    ln_bwd_cols_any_kernel<T, RMS><<<dim3(static_cast<unsigned>(strips), p.parts), kAnyThreads, 0, s>>>(p);
+    e = cudaGetLastError();
+    prof_end(s);
+    if (e != cudaSuccess) return e;
+  }
+  return reduce_columns(p, grad_weight, grad_bias, accumulate, s);
+}
+
+struct LnLayout {
+  size_t row_terms, part_w, part_b, total;
+};
+
+LnLayout ln_layout(int64_t N, int64_t H) {
+  LnLayout L;
+  // a partial row of sums for each CTA: at most one a row, rounded up to eight (the places in a vector where rows start)
+  const int64_t parts = std::min<int64_t>(div_up(std::max<int64_t>(N, 1), 8) * 8, kMaxParts);
+  const size_t part = align_up(static_cast<size_t>(parts) * H * 4, 256);
+  L.row_terms = 0;
+  L.part_w = align_up(static_cast<size_t>(N) * sizeof(float2), 256);
+  L.part_b = L.part_w + part;
+  L.total = L.part_b + part;
+  return L;
+}
+
+}  // namespace
+}  // namespace flce
+
+using namespace flce;
+
+extern "C" {
+
+size_t ln_workspace_size(int64_t N, int64_t H) { return sizes_ok(N, H) ? ln_layout(N, H).total : 0; }
+
+flce_status_t ln_bwd(int kind, int dtype, const void* grad_y, int64_t ld_grad_y, const void* x, int64_t ld_x,
+                     const void* weight, int param_dtype, const float* mean, const float* rstd,
+                     const void* grad_sum, int64_t ld_grad_sum, int64_t N, int64_t H, void* grad_x,
+                     int64_t ld_grad_x, float* grad_weight, float* grad_bias, int accumulate, void* workspace,
+                     size_t workspace_bytes, flce_stream_t stream_) {
+  if (kind != FLCE_NORM_LAYER && kind != FLCE_NORM_RMS) return FLCE_ERR_INVALID_ARG;
+  if (!float_dtype(dtype) || !float_dtype(param_dtype)) return FLCE_ERR_UNSUPPORTED;
+  if (!sizes_ok(N, H) || (accumulate != 0 && accumulate != 1)) return FLCE_ERR_INVALID_ARG;
+  if (ld_grad_y < 0 || ld_grad_y > kMaxLd || ld_x < 0 || ld_x > kMaxLd) return FLCE_ERR_INVALID_ARG;
+  if (grad_sum != nullptr && (ld_grad_sum < 0 || ld_grad_sum > kMaxLd)) return FLCE_ERR_INVALID_ARG;
+  if (grad_x != nullptr && (ld_grad_x < H || ld_grad_x > kMaxLd)) return FLCE_ERR_INVALID_ARG;
+  if (grad_sum != nullptr && grad_x == nullptr) return FLCE_ERR_INVALID_ARG;
+  if (mean != nullptr && kind == FLCE_NORM_RMS) return FLCE_ERR_INVALID_ARG;
+  if (N > 0 && (grad_y == nullptr || x == nullptr || rstd == nullptr || (kind == FLCE_NORM_LAYER && mean == nullptr)))
+    return FLCE_ERR_INVALID_ARG;
+  const size_t esz = elem_size(dtype), psz = elem_size(param_dtype);
+  if (!aligned_to(grad_y, esz) || !aligned_to(x, esz) || !aligned_to(grad_sum, esz) || !aligned_to(grad_x, esz) ||
+      !aligned_to(weight, psz) || !aligned_to(mean, 4) || !aligned_to(rstd, 4) || !aligned_to(grad_weight, 4) ||
+      !aligned_to(grad_bias, 4))
+    return FLCE_ERR_MISALIGNED;
+  if (clashes(grad_x, ld_grad_x, grad_y, ld_grad_y, N, H, esz) || clashes(grad_x, ld_grad_x, x, ld_x, N, H, esz) ||
+      clashes(grad_x, ld_grad_x, grad_sum, ld_grad_sum, N, H, esz))
+    return FLCE_ERR_INVALID_ARG;
+  if (grad_x == nullptr && grad_weight == nullptr && grad_bias == nullptr) return FLCE_OK;
+  const LnLayout L = ln_layout(N, H);
+  if (workspace == nullptr || !aligned_to(workspace, 256) || workspace_bytes < L.total) return FLCE_ERR_WORKSPACE;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  LnBackward p = {grad_y, x, weight, grad_sum, mean, rstd, grad_x, ld_grad_y, ld_x, ld_grad_sum, ld_grad_x, N, H,
+                  param_dtype, reinterpret_cast<float2*>(ws + L.row_terms),
+                  grad_weight != nullptr ? reinterpret_cast<float*>(ws + L.part_w) : nullptr,
+                  grad_bias != nullptr ? reinterpret_cast<float*>(ws + L.part_b) : nullptr, 0};
+  return LN_BY_TYPE(backward, p, grad_weight, grad_bias, accumulate, reinterpret_cast<cudaStream_t>(stream_)) ==
+                 cudaSuccess
+             ? FLCE_OK
+             : FLCE_ERR_CUDA;
+}
+
+}  // extern "C"
