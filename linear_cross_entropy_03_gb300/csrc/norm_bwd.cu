@@ -39,101 +39,142 @@ __device__ __forceinline__ void copies_arrived() {
   asm volatile("cp.async.wait_group %0;" ::"n"(LATER) : "memory");
 }
 
+__device__ __forceinline__ uint4 load_shared(uint32_t a) {
+  uint4 r;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a) : "memory");
+  return r;
+}
+__device__ __forceinline__ void store_shared(uint32_t a, const uint4& v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
 // A barrier of `threads` threads (whole warps) of the CTA; 0 is __syncthreads'.
 __device__ __forceinline__ void group_barrier(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
-constexpr int kMaxGroups = 15;  // named barriers 1 to 15
+// Threads of a CTA, one CTA on each SM: 128 registers for each.  What a row costs a
+// thread beside its elements (addresses, sums, a barrier) is as much as eight elements
+// do, so a thread takes two vectors rather than there being twice as many threads: at
+// [16384, 4096] in bf16 with one vector each 5000 instructions a row, near all that the
+// SM can issue while memory moves it.
+constexpr int kBwdThreads = 512;
+
+// Groups of more than a warp have a named barrier each (1 to 15).
+constexpr int kMaxBarriers = 15;
+
+// Sums of both numbers over the warp, to all lanes, in six exchanges: the lower
+// half of the lanes goes on with the first, the upper half with the second.
+__device__ __forceinline__ float2 warp_sum2(float2 v) {
+  const bool upper = threadIdx.x & 16;
+  float mine = upper ? v.y : v.x;
+  mine += __shfl_xor_sync(0xffffffffu, upper ? v.x : v.y, 16);
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+  const float other = __shfl_xor_sync(0xffffffffu, mine, 16);
+  return upper ? make_float2(other, mine) : make_float2(mine, other);
+}
 
 // grad_x and column sums.  `group` threads take a row, VPT vectors each, and a CTA
 // holds as many such groups as fit.  A thread keeps its columns from row to row, so
 // that the sums over the rows stay in its registers until the end; so where rows
 // start inside a vector, a group takes only rows that start at the same place (every
-// eighth, or every fourth fp32 one).  Rows are fetched DEPTH ahead into shared memory
-// by asynchronous copies, each thread its own vectors: nothing waits for another
-// thread but the two sums over the row.
+// eighth, or every fourth fp32 one).  Rows are fetched DEPTH - 1 ahead into shared
+// memory by asynchronous copies, each thread its own vectors: nothing waits for
+// another thread but the two sums over the row.
 template <typename T, bool RMS, bool BIAS, int VPT, int DEPTH, bool SHIFTED>
-__global__ void __launch_bounds__(1024) ln_bwd_kernel(const LnBackward p, int group, int groups) {
+__global__ void __launch_bounds__(kBwdThreads) ln_bwd_kernel(const LnBackward p, int group, int groups) {
   using V = Vec<T>;
-  constexpr int kN = V::kN;
+  constexpr int kN = V::kN, kP = kN / 2;
   extern __shared__ __align__(16) unsigned char ring[];
-  __shared__ float2 scratch[2][kMaxGroups + 1][32];
+  __shared__ float2 scratch[2][kMaxBarriers][32];
   const int in_cta = threadIdx.x / group, t = threadIdx.x % group, lane = threadIdx.x & 31;
   const int warps = group >> 5, warp = t >> 5;
-  const int64_t all = static_cast<int64_t>(gridDim.x) * groups;
-  const int64_t id = static_cast<int64_t>(blockIdx.x) * groups + in_cta;
-  const int64_t n0 = id, step = all;  // rows n0, n0 + step, ... (SHIFTED: step a multiple of kN)
+  // rows n0, n0 + step, ... (SHIFTED: step is a multiple of kN)
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * groups + in_cta;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
   const Row<T, SHIFTED> row(static_cast<const T*>(p.x) + n0 * p.ld_x, p.H);
   const int arrays = p.grad_sum != nullptr ? 3 : 2;
-  const uint32_t stage_bytes = static_cast<uint32_t>(blockDim.x) * VPT * 16 * arrays;
-  unsigned char* mine = ring + threadIdx.x * 16;
-  const auto slot = [&](int stage, int array, int k) {
-    return mine + stage * stage_bytes + (array * VPT + k) * blockDim.x * 16;
-  };
-  const T* const base[3] = {static_cast<const T*>(p.grad_y), static_cast<const T*>(p.x), static_cast<const T*>(p.grad_sum)};
-  const int64_t ld[3] = {p.ld_grad_y, p.ld_x, p.ld_grad_sum};
-  const auto fetch = [&](int64_t n, int stage) {
+  const uint32_t vector_bytes = blockDim.x * 16, array_bytes = vector_bytes * VPT, stage_bytes = array_bytes * arrays;
+  const uint32_t mine = smem_addr(ring) + threadIdx.x * 16;
+  // this thread's first vector of the next row to fetch, in each array
+  const int64_t lane_offset = row.column(t);
+  const T* next_g = static_cast<const T*>(p.grad_y) + n0 * p.ld_grad_y + lane_offset;
+  const T* next_x = static_cast<const T*>(p.x) + n0 * p.ld_x + lane_offset;
+  const T* next_s = static_cast<const T*>(p.grad_sum) + n0 * p.ld_grad_sum + lane_offset;
+  const auto fetch_array = [&](const T* base, int64_t ld, const T*& vector, uint32_t to) {
 #pragma unroll
-    for (int a = 0; a < 3; ++a) {
-      if (a < arrays) {
-        const T* from = base[a] + n * ld[a];
-#pragma unroll
-        for (int k = 0; k < VPT; ++k) {
-          const int j = t + k * group;
-          if (j < row.vectors) {
-            const T* vector = from + row.column(j);
-            // a vector at a row's end may hold other rows' elements (masked later), but nothing outside the matrix
-            if (row.whole(j) || (vector >= base[a] && vector + kN <= base[a] + (p.N - 1) * ld[a] + p.H))
-              copy_16(smem_addr(slot(stage, a, k)), vector);
-            else
-              *reinterpret_cast<uint4*>(slot(stage, a, k)) = row.load(from, j);
-          }
+    for (int k = 0; k < VPT; ++k) {
+      const int j = t + k * group;
+      if (j < row.vectors) {
+        const T* v = vector + k * group * kN;
+        // a vector at a row's end may hold other rows' elements (masked later), but nothing outside the matrix
+        if (row.whole(j) || (v >= base && v + kN <= base + (p.N - 1) * ld + p.H)) {
+          copy_16(to + k * vector_bytes, v);
+        } else {
+          store_shared(to + k * vector_bytes, row.load(vector - lane_offset, j));
         }
       }
     }
+    vector += step * ld;
   };
-  // The row's elements of a vector, 0 outside the row.
-  const auto elements = [&](int stage, int array, int k, float* f) {
-    V::unpack(*reinterpret_cast<const uint4*>(slot(stage, array, k)), f);
-    const int j = t + k * group;
-    if (SHIFTED && !row.whole(j)) {
-#pragma unroll
-      for (int i = 0; i < kN; ++i)
-        if (!row.inside(row.column(j) + i)) f[i] = 0.f;
-    }
+  const auto fetch = [&](uint32_t stage) {
+    fetch_array(static_cast<const T*>(p.grad_y), p.ld_grad_y, next_g, mine + stage);
+    fetch_array(static_cast<const T*>(p.x), p.ld_x, next_x, mine + stage + array_bytes);
+    if (arrays == 3) fetch_array(static_cast<const T*>(p.grad_sum), p.ld_grad_sum, next_s, mine + stage + 2 * array_bytes);
   };
 #pragma unroll
   for (int d = 0; d < DEPTH - 1; ++d) {
-    if (n0 + d * step < p.N) fetch(n0 + d * step, d);
+    if (n0 + d * step < p.N) fetch(d * stage_bytes);
     copies_issued();
   }
   grid_dependents_launch();
 
-  float sw[VPT][kN], sb[BIAS ? VPT : 1][kN], w[VPT == 1 ? kN : 1];
+  Pair sw[VPT][kP], sb[VPT][kP], w[VPT][kP];
 #pragma unroll
   for (int k = 0; k < VPT; ++k)
 #pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      sw[k][i] = 0.f;
-      if (BIAS) sb[k][i] = 0.f;
-    }
-  const auto weights = [&](int k, float* f) {
+    for (int i = 0; i < kP; ++i) sw[k][i] = sb[k][i] = pair(0.f);
+  // kept with one or two vectors a thread; with more read again (from the first-level cache)
+  constexpr bool kKeep = VPT <= 2;
+  const auto weights = [&](int k) {
+    float f[kN];
     if (p.weight != nullptr && t + k * group < row.vectors) {
       row.params(p.weight, p.param_dtype, t + k * group, f);
     } else {
 #pragma unroll
       for (int i = 0; i < kN; ++i) f[i] = 1.f;
     }
+#pragma unroll
+    for (int i = 0; i < kP; ++i) w[k][i] = pair(f[2 * i], f[2 * i + 1]);
   };
-  if (VPT == 1) weights(0, w);  // kept; with more vectors read again (from the first-level cache)
+  if (kKeep) {
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) weights(k);
+  }
+  // The row's elements of a vector, 0 outside the row.
+  const auto elements = [&](uint32_t stage, int array, int k, Pair* f2) {
+    float f[kN];
+    V::unpack(load_shared(mine + stage + array * array_bytes + k * vector_bytes), f);
+    const int j = t + k * group;
+    if (SHIFTED && !row.whole(j)) {
+#pragma unroll
+      for (int i = 0; i < kN; ++i)
+        if (!row.inside(row.column(j) + i)) f[i] = 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < kP; ++i) f2[i] = pair(f[2 * i], f[2 * i + 1]);
+  };
   const float over = 1.f / static_cast<float>(p.H);
   float next_mu = 0.f, next_inv = 0.f;
   if (n0 < p.N) {
     next_mu = RMS ? 0.f : p.mean[n0];
     next_inv = p.rstd[n0];
   }
-  int stage = 0, turn = 0;
+  uint32_t stage = 0;
+  const uint32_t last_stage = (DEPTH - 1) * stage_bytes;
+  int turn = 0;
+  T* to = static_cast<T*>(p.grad_x) + n0 * p.ld_grad_x;
   for (int64_t n = n0; n < p.N; n += step) {
     const float mu = next_mu, inv = next_inv;
     if (n + step < p.N) {
@@ -142,95 +183,125 @@ __global__ void __launch_bounds__(1024) ln_bwd_kernel(const LnBackward p, int gr
     }
     copies_arrived<DEPTH - 2>();
     // the next row to fetch goes where this thread's part of the row before this one was
-    if (n + (DEPTH - 1) * step < p.N) fetch(n + (DEPTH - 1) * step, stage == 0 ? DEPTH - 1 : stage - 1);
+    if (n + (DEPTH - 1) * step < p.N) fetch(stage == 0 ? last_stage : stage - stage_bytes);
     copies_issued();
-    float2 s = make_float2(0.f, 0.f);
+    Pair g[VPT][kP], xhat[VPT][kP];  // g: grad_y, then u
+    const auto read = [&](int k) {
+      elements(stage, 0, k, g[k]);
+      elements(stage, 1, k, xhat[k]);
+      if (!kKeep) weights(k);
+#pragma unroll
+      for (int i = 0; i < kP; ++i)
+        xhat[k][i] = RMS ? xhat[k][i] * pair(inv) : (xhat[k][i] + pair(-mu)) * pair(inv);
+    };
+    Pair s1 = pair(0.f), s2 = pair(0.f);
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
       if (t + k * group < row.vectors) {
-        float g[kN], x[kN], wk[kN];
-        elements(stage, 0, k, g);
-        elements(stage, 1, k, x);
-        if (VPT > 1) weights(k, wk);
+        read(k);
 #pragma unroll
-        for (int i = 0; i < kN; ++i) {
-          const float xhat = (x[i] - mu) * inv, u = g[i] * (VPT > 1 ? wk[i] : w[i]);
-          sw[k][i] = fmaf(g[i], xhat, sw[k][i]);
-          if (BIAS) sb[k][i] += g[i];
-          if (!RMS) s.x += u;
-          s.y = fmaf(u, xhat, s.y);
+        for (int i = 0; i < kP; ++i) {
+          sw[k][i] = fma_pair(g[k][i], xhat[k][i], sw[k][i]);
+          if (BIAS) sb[k][i] = sb[k][i] + g[k][i];
+          g[k][i] = g[k][i] * w[k][i];
+          if (!RMS) s1 = s1 + g[k][i];
+          s2 = fma_pair(g[k][i], xhat[k][i], s2);
         }
       }
     }
-    if (!RMS) s.x = warp_sum(s.x);
-    s.y = warp_sum(s.y);
+    const float2 f1 = unpair(s1), f2 = unpair(s2);
+    float2 s = make_float2(f1.x + f1.y, f2.x + f2.y);
+    if (RMS)
+      s.y = warp_sum(s.y);
+    else
+      s = warp_sum2(s);
     if (warps > 1) {
       // one barrier a row: the scratch of a row is written again two rows later
       if (lane == 0) scratch[turn][in_cta][warp] = s;
       group_barrier(1 + in_cta, group);
       s = lane < warps ? scratch[turn][in_cta][lane] : make_float2(0.f, 0.f);
-      if (!RMS) s.x = warp_sum(s.x);
-      s.y = warp_sum(s.y);
+      if (RMS)
+        s.y = warp_sum(s.y);
+      else
+        s = warp_sum2(s);
       turn ^= 1;
     }
-    const float c1 = s.x * over, c2 = s.y * over;
     if (p.grad_x != nullptr) {
-      T* to = static_cast<T*>(p.grad_x) + n * p.ld_grad_x;
+      // (u - mean(u) - xhat mean(u xhat)) rstd + grad_sum
+      const Pair c1 = pair(-s.x * over * inv), c2 = pair(-s.y * over * inv);
 #pragma unroll
       for (int k = 0; k < VPT; ++k) {
         const int j = t + k * group;
         if (j < row.vectors) {
-          float g[kN], x[kN], wk[kN];
-          V::unpack(*reinterpret_cast<const uint4*>(slot(stage, 0, k)), g);
-          V::unpack(*reinterpret_cast<const uint4*>(slot(stage, 1, k)), x);
-          if (VPT > 1) weights(k, wk);
+          if (!kKeep) {
+            read(k);
 #pragma unroll
-          for (int i = 0; i < kN; ++i) {
-            const float xhat = (x[i] - mu) * inv, u = g[i] * (VPT > 1 ? wk[i] : w[i]);
-            g[i] = (u - c1 - xhat * c2) * inv;
+            for (int i = 0; i < kP; ++i) g[k][i] = g[k][i] * w[k][i];
           }
+          Pair rest[kP];
           if (arrays == 3) {
-            V::unpack(*reinterpret_cast<const uint4*>(slot(stage, 2, k)), x);
+            elements(stage, 2, k, rest);
 #pragma unroll
-            for (int i = 0; i < kN; ++i) g[i] += x[i];
+            for (int i = 0; i < kP; ++i) rest[i] = RMS ? rest[i] : rest[i] + c1;
+          } else {
+#pragma unroll
+            for (int i = 0; i < kP; ++i) rest[i] = c1;
           }
-          row.store(to, j, V::pack(g));
+          float f[kN];
+#pragma unroll
+          for (int i = 0; i < kP; ++i) {
+            const float2 o = unpair(fma_pair(g[k][i], pair(inv), fma_pair(xhat[k][i], c2, rest[i])));
+            f[2 * i] = o.x, f[2 * i + 1] = o.y;
+          }
+          row.store(to, j, V::pack(f));
         }
       }
+      to += step * p.ld_grad_x;
     }
-    stage = stage == DEPTH - 1 ? 0 : stage + 1;
+    stage = stage == last_stage ? 0 : stage + stage_bytes;
   }
 
   if (p.part_w == nullptr && p.part_b == nullptr) return;
-  // the CTA's groups one after another into shared memory, or, with one, as they are
-  float* part_w = p.part_w != nullptr ? p.part_w + static_cast<int64_t>(blockIdx.x) * p.H : nullptr;
-  float* part_b = BIAS && p.part_b != nullptr ? p.part_b + static_cast<int64_t>(blockIdx.x) * p.H : nullptr;
-  float* sum_w = groups > 1 ? reinterpret_cast<float*>(ring) : part_w;
-  float* sum_b = groups > 1 ? sum_w + p.H : part_b;
-  copies_arrived<0>();
-  for (int turns = 0; turns < groups; ++turns) {
+  // each group's sums go to shared memory and are added there, or, from one group, out as they are
+  float* const part_w = p.part_w != nullptr ? p.part_w + static_cast<int64_t>(blockIdx.x) * p.H : nullptr;
+  float* const part_b = BIAS && p.part_b != nullptr ? p.part_b + static_cast<int64_t>(blockIdx.x) * p.H : nullptr;
+  float* to_w = part_w;
+  float* to_b = part_b;
+  if (groups > 1) {
+    copies_arrived<0>();
     __syncthreads();
-    if (in_cta != turns) continue;
+    to_w = reinterpret_cast<float*>(ring) + in_cta * row.length;
+    to_b = to_w + groups * row.length;
+  }
 #pragma unroll
-    for (int k = 0; k < VPT; ++k) {
-      const int j = t + k * group;
-      if (j < row.vectors) {
+  for (int k = 0; k < VPT; ++k) {
+    const int j = t + k * group;
+    if (j < row.vectors) {
 #pragma unroll
-        for (int i = 0; i < kN; ++i) {
-          const int c = row.column(j) + i;
-          if (row.inside(c)) {
-            if (sum_w != nullptr) sum_w[c] = turns == 0 ? sw[k][i] : sum_w[c] + sw[k][i];
-            if (BIAS && sum_b != nullptr) sum_b[c] = turns == 0 ? sb[k][i] : sum_b[c] + sb[k][i];
-          }
+      for (int i = 0; i < kN; ++i) {
+        const int c = row.column(j) + i;
+        if (row.inside(c)) {
+          const float2 fw = unpair(sw[k][i / 2]), fb = unpair(sb[k][i / 2]);
+          if (part_w != nullptr) to_w[c] = i % 2 ? fw.y : fw.x;
+          if (part_b != nullptr) to_b[c] = i % 2 ? fb.y : fb.x;
         }
       }
     }
   }
   if (groups == 1) return;
   __syncthreads();
+  const float* const sums = reinterpret_cast<const float*>(ring);
   for (int c = threadIdx.x; c < row.length; c += blockDim.x) {
-    if (part_w != nullptr) part_w[c] = sum_w[c];
-    if (part_b != nullptr) part_b[c] = sum_b[c];
+    if (part_w != nullptr) {
+      float a = 0.f;
+      for (int k = 0; k < groups; ++k) a += sums[k * row.length + c];
+      part_w[c] = a;
+    }
+    if (part_b != nullptr) {
+      float a = 0.f;
+      for (int k = 0; k < groups; ++k) a += sums[(groups + k) * row.length + c];
+      part_b[c] = a;
+    }
   }
 }
 
@@ -334,18 +405,17 @@ cudaError_t reduce_columns(const LnBackward& p, float* grad_weight, float* grad_
   return e;
 }
 
-// Most vectors of a row that the vector form takes (two for each of 1024 threads).
+// Most vectors of a row that the vector form takes (four for each thread).
 constexpr int64_t kMaxRowVectors = 2048;
 
 template <typename T, bool RMS, bool BIAS, int VPT, int DEPTH, bool SHIFTED>
 cudaError_t backward_rows(LnBackward& p, int64_t vectors, cudaStream_t s) {
   constexpr int kN = Vec<T>::kN;
   const int group = static_cast<int>(div_up(vectors, 32 * VPT) * 32);
-  const int groups = std::max(1, std::min(512 / group, kMaxGroups));
+  const int groups = group == 32 ? kBwdThreads / 32 : std::min(kBwdThreads / group, kMaxBarriers);
   const int threads = group * groups;
   const size_t smem = static_cast<size_t>(threads) * VPT * 16 * (p.grad_sum != nullptr ? 3 : 2) * DEPTH;
-  const int64_t most = threads <= 512 ? 2 * device_sm_count() : device_sm_count();
-  int64_t grid = std::min<int64_t>({div_up(p.N, groups), most, kMaxParts});
+  int64_t grid = std::min<int64_t>({div_up(p.N, groups), device_sm_count(), kMaxParts});
   if (SHIFTED) {  // groups a multiple of kN
     int64_t unit = kN;
     while (unit > 1 && groups * (unit / 2) % kN == 0) unit /= 2;
@@ -361,8 +431,9 @@ cudaError_t backward_rows(LnBackward& p, int64_t vectors, cudaStream_t s) {
 
 template <typename T, bool RMS, bool BIAS, bool SHIFTED>
 cudaError_t backward_rows(LnBackward& p, int64_t vectors, cudaStream_t s) {
-  return vectors <= 1024 ? backward_rows<T, RMS, BIAS, 1, 4, SHIFTED>(p, vectors, s)
-                         : backward_rows<T, RMS, BIAS, 2, 2, SHIFTED>(p, vectors, s);
+  if (vectors <= 32) return backward_rows<T, RMS, BIAS, 1, 4, SHIFTED>(p, vectors, s);
+  if (vectors <= 2 * kBwdThreads) return backward_rows<T, RMS, BIAS, 2, 4, SHIFTED>(p, vectors, s);
+  return backward_rows<T, RMS, BIAS, 4, 2, SHIFTED>(p, vectors, s);
 }
 
 template <typename T, bool RMS>
