@@ -15,6 +15,9 @@ namespace {
 // leaving one partial row of H sums (the workspace holds them all).
 constexpr int kMaxParts = 304;
 
+// Elements between partial rows: they are read by fours.
+__host__ __device__ inline int64_t part_ld(int64_t H) { return (H + 3) / 4 * 4; }
+
 struct LnBackward {
   const void *grad_y, *x, *weight, *grad_sum;
   const float *mean, *rstd;
@@ -22,7 +25,7 @@ struct LnBackward {
   int64_t ld_grad_y, ld_x, ld_grad_sum, ld_grad_x, N, H;
   int param_dtype;
   float2* row_terms;   // [N]: mean(u) * rstd, mean(u * xhat) * rstd
-  float *part_w, *part_b;  // [parts][H]
+  float *part_w, *part_b;  // [parts][part_ld(H)]
   int parts;
 };
 
@@ -53,7 +56,9 @@ __device__ __forceinline__ void group_barrier(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
-// Threads of a CTA, one CTA on each SM: 128 registers for each.  What a row costs a
+// Threads of a CTA, one CTA on each SM: 112 registers each, which leaves the kernel
+// that adds up the CTAs' sums 8192 (128 where a bias's sums need them too: the few
+// that would be spilled cost more, with the first-level cache this small).  What a row costs a
 // thread beside its elements (addresses, sums, a barrier) is as much as eight elements
 // do, so a thread takes two vectors rather than there being twice as many threads: at
 // [16384, 4096] in bf16 with one vector each 5000 instructions a row, near all that the
@@ -82,8 +87,10 @@ __device__ __forceinline__ float2 warp_sum2(float2 v) {
 // eighth, or every fourth fp32 one).  Rows are fetched DEPTH - 1 ahead into shared
 // memory by asynchronous copies, each thread its own vectors: nothing waits for
 // another thread but the two sums over the row.
-template <typename T, bool RMS, bool BIAS, int VPT, int DEPTH, bool SHIFTED>
-__global__ void __launch_bounds__(kBwdThreads) ln_bwd_kernel(const LnBackward p, int group, int groups) {
+//
+// FULL: every thread has all of its vectors (the usual widths), so nothing asks.
+template <typename T, bool RMS, bool BIAS, int VPT, int DEPTH, bool SHIFTED, bool FULL>
+__global__ void __maxnreg__(BIAS && sizeof(T) == 2 ? 128 : 112) ln_bwd_kernel(const LnBackward p, int group, int groups) {
   using V = Vec<T>;
   constexpr int kN = V::kN, kP = kN / 2;
   extern __shared__ __align__(16) unsigned char ring[];
@@ -94,6 +101,7 @@ __global__ void __launch_bounds__(kBwdThreads) ln_bwd_kernel(const LnBackward p,
   const int64_t n0 = static_cast<int64_t>(blockIdx.x) * groups + in_cta;
   const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
   const Row<T, SHIFTED> row(static_cast<const T*>(p.x) + n0 * p.ld_x, p.H);
+  const auto has = [&](int k) { return FULL || t + k * group < row.vectors; };  // whether there is a k-th vector
   const int arrays = p.grad_sum != nullptr ? 3 : 2;
   const uint32_t vector_bytes = blockDim.x * 16, array_bytes = vector_bytes * VPT, stage_bytes = array_bytes * arrays;
   const uint32_t mine = smem_addr(ring) + threadIdx.x * 16;
@@ -106,7 +114,7 @@ __global__ void __launch_bounds__(kBwdThreads) ln_bwd_kernel(const LnBackward p,
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
       const int j = t + k * group;
-      if (j < row.vectors) {
+      if (has(k)) {
         const T* v = vector + k * group * kN;
         // a vector at a row's end may hold other rows' elements (masked later), but nothing outside the matrix
         if (row.whole(j) || (v >= base && v + kN <= base + (p.N - 1) * ld + p.H)) {
@@ -139,7 +147,7 @@ __global__ void __launch_bounds__(kBwdThreads) ln_bwd_kernel(const LnBackward p,
   constexpr bool kKeep = VPT <= 2;
   const auto weights = [&](int k) {
     float f[kN];
-    if (p.weight != nullptr && t + k * group < row.vectors) {
+    if (p.weight != nullptr && has(k)) {
       row.params(p.weight, p.param_dtype, t + k * group, f);
     } else {
 #pragma unroll
@@ -197,7 +205,7 @@ __global__ void __launch_bounds__(kBwdThreads) ln_bwd_kernel(const LnBackward p,
     Pair s1 = pair(0.f), s2 = pair(0.f);
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-      if (t + k * group < row.vectors) {
+      if (has(k)) {
         read(k);
 #pragma unroll
         for (int i = 0; i < kP; ++i) {
@@ -232,7 +240,7 @@ __global__ void __launch_bounds__(kBwdThreads) ln_bwd_kernel(const LnBackward p,
 #pragma unroll
       for (int k = 0; k < VPT; ++k) {
         const int j = t + k * group;
-        if (j < row.vectors) {
+        if (has(k)) {
           if (!kKeep) {
             read(k);
 #pragma unroll
@@ -263,8 +271,8 @@ __global__ void __launch_bounds__(kBwdThreads) ln_bwd_kernel(const LnBackward p,
 
   if (p.part_w == nullptr && p.part_b == nullptr) return;
   // each group's sums go to shared memory and are added there, or, from one group, out as they are
-  float* const part_w = p.part_w != nullptr ? p.part_w + static_cast<int64_t>(blockIdx.x) * p.H : nullptr;
-  float* const part_b = BIAS && p.part_b != nullptr ? p.part_b + static_cast<int64_t>(blockIdx.x) * p.H : nullptr;
+  float* const part_w = p.part_w != nullptr ? p.part_w + static_cast<int64_t>(blockIdx.x) * part_ld(p.H) : nullptr;
+  float* const part_b = BIAS && p.part_b != nullptr ? p.part_b + static_cast<int64_t>(blockIdx.x) * part_ld(p.H) : nullptr;
   float* to_w = part_w;
   float* to_b = part_b;
   if (groups > 1) {
@@ -276,7 +284,7 @@ __global__ void __launch_bounds__(kBwdThreads) ln_bwd_kernel(const LnBackward p,
 #pragma unroll
   for (int k = 0; k < VPT; ++k) {
     const int j = t + k * group;
-    if (j < row.vectors) {
+    if (has(k)) {
 #pragma unroll
       for (int i = 0; i < kN; ++i) {
         const int c = row.column(j) + i;
@@ -362,33 +370,48 @@ __global__ void __launch_bounds__(kAnyThreads) ln_bwd_cols_any_kernel(const LnBa
       a.x += scratch[k][col].x;
       a.y += scratch[k][col].y;
     }
-    if (p.part_w != nullptr) p.part_w[static_cast<int64_t>(blockIdx.y) * p.H + h] = a.x;
-    if (p.part_b != nullptr) p.part_b[static_cast<int64_t>(blockIdx.y) * p.H + h] = a.y;
+    if (p.part_w != nullptr) p.part_w[static_cast<int64_t>(blockIdx.y) * part_ld(p.H) + h] = a.x;
+    if (p.part_b != nullptr) p.part_b[static_cast<int64_t>(blockIdx.y) * part_ld(p.H) + h] = a.y;
   }
 }
 
-// Adds the partial rows of column sums in a fixed order: 32 columns by 32
-// lanes a CTA, blockIdx.y 0 the weight's and 1 the bias's.
-__global__ void __launch_bounds__(1024)
-    ln_reduce_kernel(const float* part_w, const float* part_b, int parts, int64_t H, float* grad_weight,
+// Adds the partial rows of column sums in a fixed order: a CTA takes 32 columns, by
+// fours, and 32 rows at a time.  It is launched while the kernel above still runs,
+// which leaves registers enough for it to be on the SMs by then.
+constexpr int kReduceThreads = 256;
+__global__ void __launch_bounds__(kReduceThreads)
+    ln_reduce_kernel(const float* part_w, const float* part_b, int parts, int64_t ld, int64_t H, float* grad_weight,
                      float* grad_bias, int accumulate) {
-  __shared__ float scratch[32][33];
+  __shared__ float scratch[kReduceThreads / 32][32];
+  const bool weight = grad_weight != nullptr && blockIdx.y == 0;  // one of the two may be left out
+  const float* part = weight ? part_w : part_b;
+  float* out = weight ? grad_weight : grad_bias;
+  const int quad = threadIdx.x & 7, warp = threadIdx.x >> 5;
+  const int64_t h = static_cast<int64_t>(blockIdx.x) * 32 + quad * 4;
   grid_dependency_wait();
-  const float* part = blockIdx.y == 0 ? part_w : part_b;
-  float* out = blockIdx.y == 0 ? grad_weight : grad_bias;
-  if (out == nullptr) return;
-  const int col = threadIdx.x & 31, lane = threadIdx.x >> 5;
-  const int64_t h = static_cast<int64_t>(blockIdx.x) * 32 + col;
-  float a = 0.f;
-  if (h < H) {
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (h < ld) {
 #pragma unroll 5
-    for (int k = lane; k < parts; k += 32) a += part[static_cast<int64_t>(k) * H + h];
+    for (int k = threadIdx.x >> 3; k < parts; k += kReduceThreads / 8) {
+      const float4 v = *reinterpret_cast<const float4*>(part + static_cast<int64_t>(k) * ld + h);
+      a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
+    }
   }
-  scratch[lane][col] = a;
+#pragma unroll
+  for (int o = 8; o < 32; o <<= 1) {
+    a.x += __shfl_xor_sync(0xffffffffu, a.x, o);
+    a.y += __shfl_xor_sync(0xffffffffu, a.y, o);
+    a.z += __shfl_xor_sync(0xffffffffu, a.z, o);
+    a.w += __shfl_xor_sync(0xffffffffu, a.w, o);
+  }
+  if ((threadIdx.x & 31) < 8) *reinterpret_cast<float4*>(&scratch[warp][quad * 4]) = a;
   __syncthreads();
-  a = warp_sum(scratch[col][lane]);  // lane `col` of warp `lane`: partial `col` of column `lane`
-  const int64_t ho = static_cast<int64_t>(blockIdx.x) * 32 + lane;
-  if (col == 0 && ho < H) out[ho] = accumulate ? out[ho] + a : a;
+  const int64_t ho = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x;
+  if (threadIdx.x >= 32 || ho >= H) return;
+  float sum = 0.f;
+#pragma unroll
+  for (int k = 0; k < kReduceThreads / 32; ++k) sum += scratch[k][threadIdx.x];
+  out[ho] = accumulate ? out[ho] + sum : sum;
 }
 
 // ------------------------------------------------------------------ launches
@@ -398,9 +421,10 @@ cudaError_t reduce_columns(const LnBackward& p, float* grad_weight, float* grad_
   if (grad_weight == nullptr && grad_bias == nullptr) return cudaSuccess;
   prof_begin(s, FLCE_KERNEL_LN_REDUCE);
   const cudaError_t e =
-      launch_after(ln_reduce_kernel, dim3(static_cast<unsigned>(div_up(p.H, 32)), 2), dim3(1024), s,
-                   static_cast<const float*>(p.part_w), static_cast<const float*>(p.part_b), p.parts, p.H, grad_weight,
-                   grad_bias, accumulate);
+      launch_after(ln_reduce_kernel,
+                   dim3(static_cast<unsigned>(div_up(p.H, 32)), grad_weight != nullptr && grad_bias != nullptr ? 2 : 1),
+                   dim3(kReduceThreads), s, static_cast<const float*>(p.part_w), static_cast<const float*>(p.part_b),
+                   p.parts, part_ld(p.H), p.H, grad_weight, grad_bias, accumulate);
   prof_end(s);
   return e;
 }
@@ -422,7 +446,9 @@ cudaError_t backward_rows(LnBackward& p, int64_t vectors, cudaStream_t s) {
     grid = std::min<int64_t>(div_up(grid, unit), kMaxParts / unit) * unit;
   }
   p.parts = static_cast<int>(grid);
-  const auto kernel = ln_bwd_kernel<T, RMS, BIAS, VPT, DEPTH, SHIFTED>;
+  const bool full = !SHIFTED && vectors == static_cast<int64_t>(group) * VPT;
+  const auto kernel = full ? ln_bwd_kernel<T, RMS, BIAS, VPT, DEPTH, SHIFTED, !SHIFTED>
+                           : ln_bwd_kernel<T, RMS, BIAS, VPT, DEPTH, SHIFTED, false>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   kernel<<<static_cast<unsigned int>(grid), threads, smem, s>>>(p, group, groups);
@@ -484,7 +510,7 @@ LnLayout ln_layout(int64_t N, int64_t H) {
   LnLayout L;
   // a partial row of sums for each CTA: at most one a row, rounded up to eight (the places in a vector where rows start)
   const int64_t parts = std::min<int64_t>(div_up(std::max<int64_t>(N, 1), 8) * 8, kMaxParts);
-  const size_t part = align_up(static_cast<size_t>(parts) * H * 4, 256);
+  const size_t part = align_up(static_cast<size_t>(parts) * part_ld(H) * 4, 256);
   L.row_terms = 0;
   L.part_w = align_up(static_cast<size_t>(N) * sizeof(float2), 256);
   L.part_b = L.part_w + part;
