@@ -1,8 +1,10 @@
-"""Builds the CUDA library in-tree: csrc/*.cu -> _lib/libflce03.so (sm_103a).
+"""Builds the CUDA library in-tree: csrc/*.cu -> _lib/libflce03.so (sm_103a), and
+the Python extension that calls it with tensors: csrc/binding.cpp ->
+_lib/flce_torch-<torch version>.so.
 
-Each translation unit is compiled by its own nvcc process (in parallel), then
-linked with the static CUDA runtime.  A rebuild happens only when a source or
-header is newer than the library.
+Each translation unit is compiled by its own process (in parallel), then linked,
+the library with the static CUDA runtime.  A rebuild happens only when a source
+or header is newer than what is built.
 """
 from __future__ import annotations
 
@@ -11,6 +13,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -33,15 +36,21 @@ def _sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
+def binding_path() -> str:
+    import torch
+    return os.path.join(OUT_DIR, f"flce_torch-{torch.__version__}.so")
+
+
 def _inputs():
-    return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
+    return _sources() + [os.path.join(CSRC, "binding.cpp")] + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
         [os.path.join(ROOT, "include", "flce.h"), os.path.abspath(__file__)]
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    built = (LIB, binding_path())
+    if not all(map(os.path.exists, built)):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(map(os.path.getmtime, built))
     return all(os.path.getmtime(p) <= t for p in _inputs())
 
 
@@ -60,18 +69,42 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             raise RuntimeError(f"nvcc failed on {os.path.basename(src)}:\n{r.stdout}\n{r.stderr}")
         return r.stdout + r.stderr
 
-    with concurrent.futures.ThreadPoolExecutor(len(srcs)) as ex:
+    def compile_binding():
+        import torch
+        root = os.path.dirname(os.path.abspath(torch.__file__))
+        cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc)))
+        include = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+                   sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+        obj = os.path.join(OUT_DIR, "binding.o")
+        cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+               f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+               *(f"-I{p}" for p in include), "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"g++ failed on binding.cpp:\n{r.stdout}\n{r.stderr}")
+        return obj, os.path.join(root, "lib")
+
+    with concurrent.futures.ThreadPoolExecutor(len(srcs) + 1) as ex:
+        binding = ex.submit(compile_binding)
         logs = list(ex.map(compile_one, srcs, objs))
     if verbose:
         for s, log in zip(srcs, logs):
             if log.strip():
                 print(f"--- {os.path.basename(s)}\n{log}")
     tmp = LIB + ".tmp"
-    cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-lcudart_static", "-ldl", "-lpthread", "-lrt"]
+    cmd = [nvcc, *ARCH, "-shared", "-Xlinker", "-soname=libflce03.so", "-o", tmp, *objs, "-lcudart_static", "-ldl", "-lpthread", "-lrt"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    obj, torch_lib = binding.result()
+    tmp = binding_path() + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, LIB, f"-L{torch_lib}", "-ltorch_python", "-ltorch",
+           "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, binding_path())
     return LIB
 
 

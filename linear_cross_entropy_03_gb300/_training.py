@@ -4,17 +4,19 @@ front of the head, the gradients' norm, and the optimiser's step.
 ``ln_fwd``, ``ln_bwd``, ``grad_norm_raw`` and ``adamw_step`` marshal their
 arguments for the C entry points; ``layer_norm``, ``layer_norm_backward``,
 ``grad_norm`` and ``AdamW`` take tensors, check them, allocate what is not given
-and raise on an error status.  Memory that a call allocates belongs to the
+and raise on an error status (in csrc/binding.cpp).  Memory that a call allocates belongs to the
 stream that the call runs on; as with any torch operation, a tensor that was
 written on another stream has to be waited for by the caller.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import importlib.machinery
+import importlib.util
 import math
+import os
 
-from . import FlceError, _check, _dt, _ptr, _stream, lib
+from . import FlceError, _build, _dt, _ptr, _stream, lib
 
 NORM_KINDS = {"layer": 0, "rms": 1}
 ADAMW_BLOCK = 256
@@ -84,17 +86,31 @@ def adamw_step(tensors, count, numbers, stream=None) -> int:
     return lib().adamw_step(tensors, count, None if numbers is None else ctypes.byref(numbers), _stream(stream))
 
 
-# ------------------------------------------------------------------ checks
+# ------------------------------------------------------------------ tensors
 
-_codes = {}
+_binding = None
+
+
+def _native():
+    """The extension that checks tensors and calls the library; raises if it has not been built."""
+    global _binding
+    if _binding is None:
+        lib()
+        path = _build.binding_path()
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path} is missing: build it with `python -c 'import __graft_entry__ as g; g.build()'`")
+        loader = importlib.machinery.ExtensionFileLoader("flce_torch", path)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_file_location("flce_torch", path, loader=loader))
+        loader.exec_module(module)
+        module.set_error(FlceError)
+        _binding = module
+    return _binding
 
 
 def _code(t, where) -> int:
-    """The dtype code of a tensor that has to be bf16, fp16 or fp32 on the current GPU."""
-    if not _codes:
-        import torch
-        _codes.update({torch.bfloat16: 0, torch.float32: 1, torch.float16: 2})
-    code = _codes.get(t.dtype)
+    """The dtype code of a bf16, fp16 or fp32 tensor."""
+    import torch
+    code = {torch.bfloat16: 0, torch.float32: 1, torch.float16: 2}.get(t.dtype)
     if code is None:
         raise FlceError(2, f"{where}: {t.dtype}")
     return code
@@ -102,35 +118,14 @@ def _code(t, where) -> int:
 
 def _here(t, where):
     import torch
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
         raise FlceError(1, f"{where}: on {t.device}, not on the current GPU")
 
 
-def _rows(t, where):
-    """(rows, columns, distance of rows) of a tensor whose last dimension is contiguous and whose
-    others, taken together, have one stride."""
-    h = t.shape[-1] if t.dim() else 0
-    if h < 1:
-        raise FlceError(1, f"{where}: shape {tuple(t.shape)}")
-    if t.is_contiguous():
-        return t.numel() // h, h, h
-    shape, stride = t.shape[:-1], t.stride()
-    if h > 1 and stride[-1] != 1:
-        raise FlceError(2, f"{where}: its last dimension is not contiguous")
-    n, ld = 1, 0
-    for size, step in zip(reversed(shape), reversed(stride[:-1])):
-        if size != 1:
-            if n > 1 and step != ld * n:
-                raise FlceError(2, f"{where}: its rows have no one stride")
-            n, ld = n * size, step if n == 1 else ld
-    return n, h, ld if n > 1 else h
-
-
-def _vector(t, h, where):
-    if t.dim() != 1 or t.shape[0] != h or not t.is_contiguous():
-        raise FlceError(1, f"{where}: a contiguous [{h}] is wanted, not {tuple(t.shape)}")
-    _here(t, where)
-    return t
+def _flat(t, where) -> int:
+    if not t.is_contiguous():
+        raise FlceError(2, f"{where}: not contiguous")
+    return t.numel()
 
 
 def _floats(t, n, where):
@@ -141,18 +136,8 @@ def _floats(t, n, where):
     return t
 
 
-def _like(t, x, where):
-    """Rows of a second matrix, which has to have the first's shape and type."""
-    if t.shape != x.shape or t.dtype != x.dtype:
-        raise FlceError(1, f"{where}: {tuple(t.shape)} {t.dtype}, and not {tuple(x.shape)} {x.dtype}")
-    _here(t, where)
-    return _rows(t, where)[2]
-
-
 def _on(stream):
     """Makes `stream` torch's current one for a call, so that what it allocates is that stream's."""
-    if stream is None:
-        return contextlib.nullcontext()
     import torch
     return torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
 
@@ -170,33 +155,12 @@ def layer_norm(x, weight=None, bias=None, *, kind="layer", eps: float = 1e-5, re
     for rms) and ``rstd``, one a row (both None with ``row_stats=False``).
     ``out`` and ``sum_out`` may be x or residual.
     """
-    import torch
-    dtype = _code(x, "layer_norm: x")
-    _here(x, "layer_norm: x")
-    n, h, ld = _rows(x, "layer_norm: x")
-    code = _kind(kind)
-    ld_r = _like(residual, x, "layer_norm: residual") if residual is not None else 0
-    param = weight if weight is not None else bias
-    if weight is not None:
-        _vector(weight, h, "layer_norm: weight")
-    if bias is not None:
-        _vector(bias, h, "layer_norm: bias")
-        if bias.dtype != param.dtype:
-            raise FlceError(2, "layer_norm: weight and bias have different types")
-    param_dtype = _code(param, "layer_norm: weight") if param is not None else dtype
-    with _on(stream):
-        y = out if out is not None else torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        total = sum_out
-        if residual is not None and total is None:
-            total = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        rows = x.shape[:-1]
-        mean = torch.empty(rows, dtype=torch.float32, device=x.device) if row_stats and code == 0 else None
-        rstd = torch.empty(rows, dtype=torch.float32, device=x.device) if row_stats else None
-        ld_y = _like(out, x, "layer_norm: out") if out is not None else h
-        ld_s = _like(sum_out, x, "layer_norm: sum_out") if sum_out is not None else h
-        _check(ln_fwd(code, dtype, x, ld, residual, ld_r, weight, bias, param_dtype, n, h, eps, y, ld_y, total, ld_s,
-                      mean, rstd, stream), "ln_fwd")
-    return dict(y=y, sum=total, mean=mean, rstd=rstd)
+    if stream is not None:
+        with _on(stream):
+            return layer_norm(x, weight, bias, kind=kind, eps=eps, residual=residual, out=out, sum_out=sum_out,
+                              row_stats=row_stats)
+    y, total, mean, rstd = _native().layer_norm(x, weight, bias, _kind(kind), eps, residual, out, sum_out, row_stats)
+    return {"y": y, "sum": total, "mean": mean, "rstd": rstd}
 
 
 def layer_norm_backward(grad_y, x, weight=None, *, mean=None, rstd, kind="layer", grad_sum=None, grad_x: bool = True,
@@ -211,56 +175,19 @@ def layer_norm_backward(grad_y, x, weight=None, *, mean=None, rstd, kind="layer"
     ``accumulate`` adds to ``grad_weight_out`` and ``grad_bias_out``.  ``out``
     may be grad_y, grad_sum or x.
     """
-    import torch
-    dtype = _code(x, "layer_norm_backward: x")
-    _here(x, "layer_norm_backward: x")
-    n, h, ld = _rows(x, "layer_norm_backward: x")
-    ld_g = _like(grad_y, x, "layer_norm_backward: grad_y")
-    code = _kind(kind)
-    if weight is not None:
-        _vector(weight, h, "layer_norm_backward: weight")
-    param_dtype = _code(weight, "layer_norm_backward: weight") if weight is not None else dtype
-    if mean is not None:
-        _floats(mean, n, "layer_norm_backward: mean")
-    _floats(rstd, n, "layer_norm_backward: rstd")
-    ld_s = _like(grad_sum, x, "layer_norm_backward: grad_sum") if grad_sum is not None else 0
-    want_w = grad_weight or grad_weight_out is not None
-    want_b = grad_bias or grad_bias_out is not None
-    if accumulate and ((want_w and grad_weight_out is None) or (want_b and grad_bias_out is None)):
-        raise FlceError(1, "layer_norm_backward: accumulate adds to grad_weight_out and grad_bias_out")
-    if out is not None:
-        grad_x = True
-    ld_x = _like(out, x, "layer_norm_backward: out") if out is not None else h
-    with _on(stream):
-        gx = out if out is not None else (
-            torch.empty(x.shape, dtype=x.dtype, device=x.device) if grad_x else None)
-        gw, gb = grad_weight_out, grad_bias_out
-        if gw is not None:
-            _floats(gw, h, "layer_norm_backward: grad_weight_out")
-        elif want_w:
-            gw = torch.empty(h, dtype=torch.float32, device=x.device)
-        if gb is not None:
-            _floats(gb, h, "layer_norm_backward: grad_bias_out")
-        elif want_b:
-            gb = torch.empty(h, dtype=torch.float32, device=x.device)
-        size = ln_workspace_size(n, h)
-        if size == 0:
-            raise FlceError(1, "ln_workspace_size")
-        if workspace is None or workspace.numel() * workspace.element_size() < size:
-            workspace = torch.empty(size, dtype=torch.uint8, device=x.device)
-        _check(ln_bwd(code, dtype, grad_y, ld_g, x, ld, weight, param_dtype, mean, rstd, grad_sum, ld_s, n, h, gx, ld_x,
-                      gw, gb, accumulate, workspace, size, stream), "ln_bwd")
-    return dict(grad_x=gx, grad_weight=gw, grad_bias=gb)
+    if stream is not None:
+        with _on(stream):
+            return layer_norm_backward(grad_y, x, weight, mean=mean, rstd=rstd, kind=kind, grad_sum=grad_sum,
+                                       grad_x=grad_x, grad_weight=grad_weight, grad_bias=grad_bias, out=out,
+                                       grad_weight_out=grad_weight_out, grad_bias_out=grad_bias_out,
+                                       accumulate=accumulate, workspace=workspace)
+    gx, gw, gb = _native().layer_norm_backward(grad_y, x, weight, mean, rstd, _kind(kind), grad_sum, grad_x,
+                                               grad_weight, grad_bias, out, grad_weight_out, grad_bias_out, accumulate,
+                                               workspace)
+    return {"grad_x": gx, "grad_weight": gw, "grad_bias": gb}
 
 
 # ------------------------------------------------------------------ optimiser
-
-def _flat(t, where):
-    """A dense tensor in any order of its dimensions is taken as its elements lie in memory."""
-    if t.is_contiguous():
-        return t.numel()
-    raise FlceError(2, f"{where}: not contiguous")
-
 
 def grad_norm(grads, *, max_norm=None, grad_scale: float = 1.0, eps: float = 1e-6, out=None, workspace=None,
               stream=None) -> dict:
@@ -272,24 +199,11 @@ def grad_norm(grads, *, max_norm=None, grad_scale: float = 1.0, eps: float = 1e-
     host.  Gradients may be bf16, fp16 or fp32 in any mixture; None is passed
     over.
     """
-    import torch
-    grads = [g for g in grads if g is not None]
-    table = (TensorEntry * len(grads))()
-    for entry, g in zip(table, grads):
-        entry.dtype = _code(g, "grad_norm")
-        _here(g, "grad_norm")
-        entry.n = _flat(g, "grad_norm")
-        entry.data = g.data_ptr()
-    size = grad_norm_workspace_size(len(grads))
-    with _on(stream):
-        if out is None:
-            out = torch.empty(2, dtype=torch.float32, device="cuda")
-        _floats(out, 2, "grad_norm: out")
-        if workspace is None or workspace.numel() * workspace.element_size() < size:
-            workspace = torch.empty(size, dtype=torch.uint8, device="cuda")
-        _check(grad_norm_raw(table, len(grads), grad_scale, math.inf if max_norm is None else max_norm, eps, out,
-                             workspace, size, stream), "grad_norm")
-    return dict(norm=out[0], scale=out[1])
+    if stream is not None:
+        with _on(stream):
+            return grad_norm(grads, max_norm=max_norm, grad_scale=grad_scale, eps=eps, out=out, workspace=workspace)
+    norm, scale = _native().grad_norm(grads, grad_scale, math.inf if max_norm is None else max_norm, eps, out, workspace)
+    return {"norm": norm, "scale": scale}
 
 
 def _each(value, count, where):
@@ -349,7 +263,7 @@ class AdamW:
         if step < 0:
             raise FlceError(1, "AdamW: a negative step")
         self._table = (AdamWEntry * count)()
-        self._numel = []
+        self._numel = (ctypes.c_int64 * count)()
         memory = []
         for i, p in enumerate(self.params):
             e, where = self._table[i], f"AdamW: tensor {i}"
@@ -374,7 +288,7 @@ class AdamW:
             e.param, e.exp_avg, e.exp_avg_sq, e.exp_avg_scale, e.exp_avg_sq_scale, e.copy = (
                 _ptr(t) for t in (p, m, v, ms, vs, c))
             e.n, e.weight_decay, e.lr_scale = n, decay[i], scale[i]
-            self._numel.append(n)
+            self._numel[i] = n
             memory += [(t.data_ptr(), t.numel() * t.element_size(), i) for t in (p, m, v, ms, vs, c) if t is not None]
         memory = sorted(x for x in memory if x[1])
         for (start, size, i), (after, _, k) in zip(memory, memory[1:]):
@@ -383,6 +297,7 @@ class AdamW:
         self.exp_avg, self.exp_avg_sq, self.exp_avg_scale, self.exp_avg_sq_scale = given
         self._numbers = AdamWNumbers(beta1=betas[0], beta2=betas[1], eps=eps, stochastic=int(seed is not None),
                                      seed=seed or 0)
+        self._addresses = tuple(map(ctypes.addressof, (self._table, self._numel, self._numbers)))
         self._steps = step
         self._step_dev = torch.full((1,), step, dtype=torch.int64, device="cuda") if capturable else None
 
@@ -425,18 +340,9 @@ class AdamW:
                      cannot know then.
         """
         import torch
-        if len(grads) != len(self.params):
-            raise FlceError(1, f"AdamW.step: {len(grads)} gradients for {len(self.params)} tensors")
-        here = torch.cuda.current_device()
-        for entry, n, g in zip(self._table, self._numel, grads):
-            if g is None:
-                entry.n = 0
-                continue
-            entry.grad_dtype = _code(g, "AdamW.step")
-            if g.get_device() != here or not g.is_contiguous() or g.numel() != n:
-                raise FlceError(1, f"AdamW.step: a gradient is no contiguous tensor of {n} elements on the current GPU")
-            entry.grad = g.data_ptr()
-            entry.n = n
+        if stream is not None:
+            with _on(stream):
+                return self.step(grads, lr=lr, grad_scale=grad_scale, skip_nonfinite=skip_nonfinite)
         k = self._numbers
         lr = self.lr if lr is None else lr
         k.lr, k.lr_dev = (0.0, _floats(lr, 1, "AdamW.step: lr").data_ptr()) if isinstance(lr, torch.Tensor) else (lr, None)
@@ -447,13 +353,17 @@ class AdamW:
             return
         k.grad_scale = 1.0 if grad_scale is None or factor is not None else grad_scale
         k.grad_scale_dev = _ptr(factor)
-        k.skip_nonfinite = int(skip_nonfinite)
-        k.step, k.step_dev = self._steps + 1, _ptr(self._step_dev)
-        with _on(stream):
+        k.skip_nonfinite = skip_nonfinite
+        k.step = self._steps + 1
+        if self._step_dev is not None:
+            # counted on the device, and not at all where the step is skipped; taken back if the call is refused
+            one = torch.isfinite(factor).view(1) if skip_nonfinite and factor is not None else 1
+            self._step_dev.add_(one)
+            k.step_dev = self._step_dev.data_ptr()
+        try:
+            _native().adamw(self._addresses[0], self._addresses[1], len(self.params), self._addresses[2], grads)
+        except Exception:
             if self._step_dev is not None:
-                if skip_nonfinite and factor is not None:
-                    self._step_dev.add_(torch.isfinite(factor).view(1))
-                else:
-                    self._step_dev.add_(1)
-            _check(adamw_step(self._table, len(self.params), k, stream), "adamw_step")
+                self._step_dev.sub_(one)
+            raise
         self._steps += 1
