@@ -60,41 +60,54 @@ struct Vec<__half> {
   }
 };
 
-// A row as the 16-byte vectors that cover it.  Without SHIFTED the row is a whole
-// number of them.  With it the row starts `shift` elements into its first one and
-// ends anywhere in its last: these two are read and written element by element,
-// what is not the row's reading as 0.
+// OUT words from a 4-byte boundary on, by 16-byte loads from the boundary of 16 before
+// it (of memory that never changes while a kernel runs).
+template <int OUT>
+__device__ __forceinline__ void words_at(uintptr_t from, uint32_t* out) {
+  constexpr int kLoads = (OUT + 6) / 4;
+  uint32_t w[kLoads * 4];
+#pragma unroll
+  for (int k = 0; k < kLoads; ++k) {
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(from & ~uintptr_t(15)) + k);
+    w[4 * k] = v.x, w[4 * k + 1] = v.y, w[4 * k + 2] = v.z, w[4 * k + 3] = v.w;
+  }
+#pragma unroll
+  for (int k = 0; k < OUT + 1; ++k) w[k] = from & 8 ? w[k + 2] : w[k];
+#pragma unroll
+  for (int k = 0; k < OUT; ++k) out[k] = from & 4 ? w[k + 1] : w[k];
+}
+
+// A row as 16-byte vectors.  Without SHIFTED it is a whole number of them.  With it,
+// vectors start at the boundaries of 16 bytes inside the row, `before` elements (at
+// least kMargin) after its start, and end at least kMargin before its end; what lies
+// before and after, at most 30 elements, goes one by one to the row's first threads.
+// The margins keep the reads of a vector's weights (below) inside their array.
 template <typename T, bool SHIFTED>
 struct Row {
   static constexpr int kN = Vec<T>::kN;
-  int shift, length, vectors;
+  static constexpr int kMargin = kN == 8 ? 8 : 12;
+  int before, vectors, length;
   __device__ __forceinline__ Row(const void* first, int64_t H) {
     length = static_cast<int>(H);
-    shift = SHIFTED ? static_cast<int>(reinterpret_cast<uintptr_t>(first) % 16 / sizeof(T)) : 0;
-    vectors = (shift + length + kN - 1) / kN;
+    before = 0;
+    vectors = length / kN;
+    if (SHIFTED) {
+      before = kMargin + (kN - (static_cast<int>(reinterpret_cast<uintptr_t>(first) / sizeof(T)) + kMargin) % kN) % kN;
+      vectors = (length - before - kMargin) / kN;
+    }
   }
-  __device__ __forceinline__ int column(int j) const { return j * kN - shift; }  // of vector j's first element
-  __device__ __forceinline__ bool whole(int j) const {
-    return !SHIFTED || (j * kN >= shift && (j + 1) * kN <= shift + length);
+  __device__ __forceinline__ int column(int j) const { return before + j * kN; }  // of vector j's first element
+  // The column that thread t of the row has beside its vectors, or -1.
+  __device__ __forceinline__ int extra(int t) const {
+    if (!SHIFTED) return -1;
+    const int c = t < before ? t : t + vectors * kN;
+    return c < length ? c : -1;
   }
-  __device__ __forceinline__ bool inside(int c) const { return !SHIFTED || (c >= 0 && c < length); }
   __device__ __forceinline__ uint4 load(const T* row, int j) const {
-    if (whole(j)) return *reinterpret_cast<const uint4*>(row + column(j));
-    float f[kN];
-#pragma unroll
-    for (int k = 0; k < kN; ++k) f[k] = inside(column(j) + k) ? to_float(row[column(j) + k]) : 0.f;
-    return Vec<T>::pack(f);
+    return *reinterpret_cast<const uint4*>(row + column(j));
   }
   __device__ __forceinline__ void store(T* row, int j, const uint4& v) const {
-    if (whole(j)) {
-      *reinterpret_cast<uint4*>(row + column(j)) = v;
-      return;
-    }
-    float f[kN];
-    Vec<T>::unpack(v, f);
-#pragma unroll
-    for (int k = 0; k < kN; ++k)
-      if (inside(column(j) + k)) row[column(j) + k] = from_float<T>(f[k]);
+    *reinterpret_cast<uint4*>(row + column(j)) = v;
   }
   // Weights or biases of vector j's columns (which never change while a kernel runs).
   __device__ __forceinline__ void params(const void* p, int dtype, int j, float* f) const {
@@ -112,19 +125,21 @@ struct Row {
         }
         f[k] = v.x, f[k + 1] = v.y, f[k + 2] = v.z, f[k + 3] = v.w;
       }
+    } else if (dtype == FLCE_DTYPE_FP32) {
+      uint32_t w[kN];
+      words_at<kN>(reinterpret_cast<uintptr_t>(static_cast<const float*>(p) + c), w);
+#pragma unroll
+      for (int k = 0; k < kN; ++k) f[k] = __uint_as_float(w[k]);
     } else {
-      int at[kN];
+      const uintptr_t from = reinterpret_cast<uintptr_t>(static_cast<const uint16_t*>(p) + c);
+      const unsigned int pick = from & 2 ? 0x5432 : 0x3210;
+      uint32_t w[kN / 2 + 1];
+      words_at<kN / 2 + 1>(from & ~uintptr_t(3), w);
 #pragma unroll
-      for (int k = 0; k < kN; ++k) at[k] = min(max(c + k, 0), length - 1);
-      if (dtype == FLCE_DTYPE_FP32) {
-#pragma unroll
-        for (int k = 0; k < kN; ++k) f[k] = __ldg(static_cast<const float*>(p) + at[k]);
-      } else if (dtype == FLCE_DTYPE_BF16) {
-#pragma unroll
-        for (int k = 0; k < kN; ++k) f[k] = to_float(__ldg(static_cast<const __nv_bfloat16*>(p) + at[k]));
-      } else {
-#pragma unroll
-        for (int k = 0; k < kN; ++k) f[k] = to_float(__ldg(static_cast<const __half*>(p) + at[k]));
+      for (int k = 0; k < kN / 4; ++k) {
+        const float4 v = four_floats(make_uint4(__byte_perm(w[2 * k], w[2 * k + 1], pick),
+                                                __byte_perm(w[2 * k + 1], w[2 * k + 2], pick), 0, 0), dtype);
+        f[4 * k] = v.x, f[4 * k + 1] = v.y, f[4 * k + 2] = v.z, f[4 * k + 3] = v.w;
       }
     }
   }
@@ -157,6 +172,8 @@ enum Fit {
   kFitWhole     // at a vector's start, with a whole number of vectors
 };
 
+constexpr int64_t kMinShifted = 64;  // columns: both margins and a few vectors
+
 struct Matrix {
   const void* p;
   int64_t ld;
@@ -176,7 +193,7 @@ Fit fit_of(int64_t N, int64_t H, const void* weight, const void* bias, int param
     if (s != start || d != step) return kFitNot;
     whole = whole && s == 0 && d == 0;
   }
-  return whole ? kFitWhole : kFitShifted;
+  return whole ? kFitWhole : H >= kMinShifted ? kFitShifted : kFitNot;
 }
 
 // ------------------------------------------------------------------- checks

@@ -47,8 +47,12 @@ __device__ __forceinline__ uint4 load_shared(uint32_t a) {
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a) : "memory");
   return r;
 }
-__device__ __forceinline__ void store_shared(uint32_t a, const uint4& v) {
-  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+
+__device__ __forceinline__ void load_pairs(uint32_t a, Pair& x, Pair& y) {
+  asm volatile("ld.shared.v2.u64 {%0, %1}, [%2];" : "=l"(x.v), "=l"(y.v) : "r"(a) : "memory");
+}
+__device__ __forceinline__ void store_pairs(uint32_t a, Pair x, Pair y) {
+  asm volatile("st.shared.v2.u64 [%0], {%1, %2};" ::"r"(a), "l"(x.v), "l"(y.v) : "memory");
 }
 
 // A barrier of `threads` threads (whole warps) of the CTA; 0 is __syncthreads'.
@@ -57,13 +61,21 @@ __device__ __forceinline__ void group_barrier(int id, int threads) {
 }
 
 // Threads of a CTA, one CTA on each SM: 112 registers each, which leaves the kernel
-// that adds up the CTAs' sums 8192 (128 where a bias's sums need them too: the few
-// that would be spilled cost more, with the first-level cache this small).  What a row costs a
+// that adds up the CTAs' sums 8192 (128 where a bias's sums need more).  What a row costs a
 // thread beside its elements (addresses, sums, a barrier) is as much as eight elements
 // do, so a thread takes two vectors rather than there being twice as many threads: at
 // [16384, 4096] in bf16 with one vector each 5000 instructions a row, near all that the
 // SM can issue while memory moves it.
 constexpr int kBwdThreads = 512;
+
+// Whether the weights lie in shared memory: where the sums for a bias with the tests
+// for missing vectors, or the column beside the vectors, take the registers.  (Spilled
+// ones cost far more, as next to the ring the first-level cache has room for little:
+// bf16 [20000, 1001] took 72 us with 56 bytes a thread spilled and 42 so.)
+template <typename T, int VPT>
+constexpr bool share_weights(bool bias, bool shifted, bool full) {
+  return sizeof(T) == 2 && VPT == 2 && (shifted || (bias && !full));
+}
 
 // Groups of more than a warp have a named barrier each (1 to 15).
 constexpr int kMaxBarriers = 15;
@@ -90,7 +102,9 @@ __device__ __forceinline__ float2 warp_sum2(float2 v) {
 //
 // FULL: every thread has all of its vectors (the usual widths), so nothing asks.
 template <typename T, bool RMS, bool BIAS, int VPT, int DEPTH, bool SHIFTED, bool FULL>
-__global__ void __maxnreg__(BIAS && sizeof(T) == 2 ? 128 : 112) ln_bwd_kernel(const LnBackward p, int group, int groups) {
+__global__ void __maxnreg__((VPT > 2 || (sizeof(T) == 2 && (BIAS || SHIFTED)) ? 128 : 112))
+    ln_bwd_kernel(const LnBackward p, int group, int groups) {
+  constexpr bool kShareWeights = share_weights<T, VPT>(BIAS, SHIFTED, FULL);
   using V = Vec<T>;
   constexpr int kN = V::kN, kP = kN / 2;
   extern __shared__ __align__(16) unsigned char ring[];
@@ -110,26 +124,16 @@ __global__ void __maxnreg__(BIAS && sizeof(T) == 2 ? 128 : 112) ln_bwd_kernel(co
   const T* next_g = static_cast<const T*>(p.grad_y) + n0 * p.ld_grad_y + lane_offset;
   const T* next_x = static_cast<const T*>(p.x) + n0 * p.ld_x + lane_offset;
   const T* next_s = static_cast<const T*>(p.grad_sum) + n0 * p.ld_grad_sum + lane_offset;
-  const auto fetch_array = [&](const T* base, int64_t ld, const T*& vector, uint32_t to) {
+  const auto fetch_array = [&](int64_t ld, const T*& vector, uint32_t to) {
 #pragma unroll
-    for (int k = 0; k < VPT; ++k) {
-      const int j = t + k * group;
-      if (has(k)) {
-        const T* v = vector + k * group * kN;
-        // a vector at a row's end may hold other rows' elements (masked later), but nothing outside the matrix
-        if (row.whole(j) || (v >= base && v + kN <= base + (p.N - 1) * ld + p.H)) {
-          copy_16(to + k * vector_bytes, v);
-        } else {
-          store_shared(to + k * vector_bytes, row.load(vector - lane_offset, j));
-        }
-      }
-    }
+    for (int k = 0; k < VPT; ++k)
+      if (has(k)) copy_16(to + k * vector_bytes, vector + k * group * kN);
     vector += step * ld;
   };
   const auto fetch = [&](uint32_t stage) {
-    fetch_array(static_cast<const T*>(p.grad_y), p.ld_grad_y, next_g, mine + stage);
-    fetch_array(static_cast<const T*>(p.x), p.ld_x, next_x, mine + stage + array_bytes);
-    if (arrays == 3) fetch_array(static_cast<const T*>(p.grad_sum), p.ld_grad_sum, next_s, mine + stage + 2 * array_bytes);
+    fetch_array(p.ld_grad_y, next_g, mine + stage);
+    fetch_array(p.ld_x, next_x, mine + stage + array_bytes);
+    if (arrays == 3) fetch_array(p.ld_grad_sum, next_s, mine + stage + 2 * array_bytes);
   };
 #pragma unroll
   for (int d = 0; d < DEPTH - 1; ++d) {
@@ -143,8 +147,12 @@ __global__ void __maxnreg__(BIAS && sizeof(T) == 2 ? 128 : 112) ln_bwd_kernel(co
   for (int k = 0; k < VPT; ++k)
 #pragma unroll
     for (int i = 0; i < kP; ++i) sw[k][i] = sb[k][i] = pair(0.f);
-  // kept with one or two vectors a thread; with more read again (from the first-level cache)
+  // kept with one or two vectors a thread, in registers or (kWeightsShared) in this
+  // thread's part of shared memory behind the ring; with more read again
   constexpr bool kKeep = VPT <= 2;
+  // whether u and xhat are formed again for grad_x instead of being kept over the barrier
+  constexpr bool kAgain = !kKeep || (kShareWeights && BIAS && SHIFTED);
+  const uint32_t my_weights = mine + DEPTH * stage_bytes;
   const auto weights = [&](int k) {
     float f[kN];
     if (p.weight != nullptr && has(k)) {
@@ -158,37 +166,53 @@ __global__ void __maxnreg__(BIAS && sizeof(T) == 2 ? 128 : 112) ln_bwd_kernel(co
   };
   if (kKeep) {
 #pragma unroll
-    for (int k = 0; k < VPT; ++k) weights(k);
+    for (int k = 0; k < VPT; ++k) {
+      weights(k);
+      if (kShareWeights) {
+#pragma unroll
+        for (int i = 0; i < kP; i += 2) store_pairs(my_weights + (k * kP + i) / 2 * vector_bytes, w[k][i], w[k][i + 1]);
+      }
+    }
   }
-  // The row's elements of a vector, 0 outside the row.
   const auto elements = [&](uint32_t stage, int array, int k, Pair* f2) {
     float f[kN];
     V::unpack(load_shared(mine + stage + array * array_bytes + k * vector_bytes), f);
-    const int j = t + k * group;
-    if (SHIFTED && !row.whole(j)) {
-#pragma unroll
-      for (int i = 0; i < kN; ++i)
-        if (!row.inside(row.column(j) + i)) f[i] = 0.f;
-    }
 #pragma unroll
     for (int i = 0; i < kP; ++i) f2[i] = pair(f[2 * i], f[2 * i + 1]);
   };
   const float over = 1.f / static_cast<float>(p.H);
+  // SHIFTED: the element beside the vectors, loaded a row ahead like the row's statistics
+  const int c_extra = row.extra(t);
+  const T* extra_g = static_cast<const T*>(p.grad_y) + n0 * p.ld_grad_y + c_extra;
+  const T* extra_x = static_cast<const T*>(p.x) + n0 * p.ld_x + c_extra;
+  const T* extra_s = static_cast<const T*>(p.grad_sum) + n0 * p.ld_grad_sum + c_extra;
+  const float w_extra = c_extra >= 0 && p.weight != nullptr ? load_elem(p.weight, p.param_dtype, c_extra) : 1.f;
+  float sw_extra = 0.f, sb_extra = 0.f;
   float next_mu = 0.f, next_inv = 0.f;
-  if (n0 < p.N) {
-    next_mu = RMS ? 0.f : p.mean[n0];
-    next_inv = p.rstd[n0];
-  }
+  T next_ge = from_float<T>(0.f), next_xe = next_ge, next_se = next_ge;
+  const auto ahead = [&](int64_t n) {
+    next_mu = RMS ? 0.f : p.mean[n];
+    next_inv = p.rstd[n];
+    if (c_extra >= 0) {
+      next_ge = *extra_g;
+      next_xe = *extra_x;
+      if (arrays == 3) next_se = *extra_s;
+    }
+    if (SHIFTED) {
+      extra_g += step * p.ld_grad_y;
+      extra_x += step * p.ld_x;
+      extra_s += step * p.ld_grad_sum;
+    }
+  };
+  if (n0 < p.N) ahead(n0);
   uint32_t stage = 0;
   const uint32_t last_stage = (DEPTH - 1) * stage_bytes;
   int turn = 0;
   T* to = static_cast<T*>(p.grad_x) + n0 * p.ld_grad_x;
   for (int64_t n = n0; n < p.N; n += step) {
     const float mu = next_mu, inv = next_inv;
-    if (n + step < p.N) {
-      next_mu = RMS ? 0.f : p.mean[n + step];
-      next_inv = p.rstd[n + step];
-    }
+    const T ge = next_ge, xe = next_xe, se = next_se;
+    if (n + step < p.N) ahead(n + step);
     copies_arrived<DEPTH - 2>();
     // the next row to fetch goes where this thread's part of the row before this one was
     if (n + (DEPTH - 1) * step < p.N) fetch(stage == 0 ? last_stage : stage - stage_bytes);
@@ -198,6 +222,10 @@ __global__ void __maxnreg__(BIAS && sizeof(T) == 2 ? 128 : 112) ln_bwd_kernel(co
       elements(stage, 0, k, g[k]);
       elements(stage, 1, k, xhat[k]);
       if (!kKeep) weights(k);
+      if (kShareWeights) {
+#pragma unroll
+        for (int i = 0; i < kP; i += 2) load_pairs(my_weights + (k * kP + i) / 2 * vector_bytes, w[k][i], w[k][i + 1]);
+      }
 #pragma unroll
       for (int i = 0; i < kP; ++i)
         xhat[k][i] = RMS ? xhat[k][i] * pair(inv) : (xhat[k][i] + pair(-mu)) * pair(inv);
@@ -219,6 +247,15 @@ __global__ void __maxnreg__(BIAS && sizeof(T) == 2 ? 128 : 112) ln_bwd_kernel(co
     }
     const float2 f1 = unpair(s1), f2 = unpair(s2);
     float2 s = make_float2(f1.x + f1.y, f2.x + f2.y);
+    float u_extra = 0.f, xhat_extra = 0.f;
+    if (c_extra >= 0) {
+      xhat_extra = (to_float(xe) - mu) * inv;
+      sw_extra = fmaf(to_float(ge), xhat_extra, sw_extra);
+      sb_extra += to_float(ge);
+      u_extra = to_float(ge) * w_extra;
+      s.x += u_extra;
+      s.y = fmaf(u_extra, xhat_extra, s.y);
+    }
     if (RMS)
       s.y = warp_sum(s.y);
     else
@@ -241,7 +278,7 @@ __global__ void __maxnreg__(BIAS && sizeof(T) == 2 ? 128 : 112) ln_bwd_kernel(co
       for (int k = 0; k < VPT; ++k) {
         const int j = t + k * group;
         if (has(k)) {
-          if (!kKeep) {
+          if (kAgain) {
             read(k);
 #pragma unroll
             for (int i = 0; i < kP; ++i) g[k][i] = g[k][i] * w[k][i];
@@ -253,7 +290,7 @@ __global__ void __maxnreg__(BIAS && sizeof(T) == 2 ? 128 : 112) ln_bwd_kernel(co
             for (int i = 0; i < kP; ++i) rest[i] = RMS ? rest[i] : rest[i] + c1;
           } else {
 #pragma unroll
-            for (int i = 0; i < kP; ++i) rest[i] = c1;
+            for (int i = 0; i < kP; ++i) rest[i] = RMS ? pair(0.f) : c1;
           }
           float f[kN];
 #pragma unroll
@@ -263,6 +300,12 @@ __global__ void __maxnreg__(BIAS && sizeof(T) == 2 ? 128 : 112) ln_bwd_kernel(co
           }
           row.store(to, j, V::pack(f));
         }
+      }
+      if (c_extra >= 0) {
+        const float2 k1 = unpair(c1), k2 = unpair(c2);
+        float o = fmaf(u_extra, inv, fmaf(xhat_extra, k2.x, RMS ? 0.f : k1.x));
+        if (arrays == 3) o += to_float(se);
+        to[c_extra] = from_float<T>(o);
       }
       to += step * p.ld_grad_x;
     }
@@ -288,13 +331,15 @@ __global__ void __maxnreg__(BIAS && sizeof(T) == 2 ? 128 : 112) ln_bwd_kernel(co
 #pragma unroll
       for (int i = 0; i < kN; ++i) {
         const int c = row.column(j) + i;
-        if (row.inside(c)) {
-          const float2 fw = unpair(sw[k][i / 2]), fb = unpair(sb[k][i / 2]);
-          if (part_w != nullptr) to_w[c] = i % 2 ? fw.y : fw.x;
-          if (part_b != nullptr) to_b[c] = i % 2 ? fb.y : fb.x;
-        }
+        const float2 fw = unpair(sw[k][i / 2]), fb = unpair(sb[k][i / 2]);
+        if (part_w != nullptr) to_w[c] = i % 2 ? fw.y : fw.x;
+        if (part_b != nullptr) to_b[c] = i % 2 ? fb.y : fb.x;
       }
     }
+  }
+  if (c_extra >= 0) {
+    if (part_w != nullptr) to_w[c_extra] = sw_extra;
+    if (part_b != nullptr) to_b[c_extra] = sb_extra;
   }
   if (groups == 1) return;
   __syncthreads();
@@ -432,13 +477,15 @@ cudaError_t reduce_columns(const LnBackward& p, float* grad_weight, float* grad_
 // Most vectors of a row that the vector form takes (four for each thread).
 constexpr int64_t kMaxRowVectors = 2048;
 
-template <typename T, bool RMS, bool BIAS, int VPT, int DEPTH, bool SHIFTED>
-cudaError_t backward_rows(LnBackward& p, int64_t vectors, cudaStream_t s) {
+template <typename T, bool RMS, bool BIAS, int VPT, bool SHIFTED, bool FULL>
+cudaError_t launch_rows(LnBackward& p, int group, cudaStream_t s) {
   constexpr int kN = Vec<T>::kN;
-  const int group = static_cast<int>(div_up(vectors, 32 * VPT) * 32);
+  constexpr bool kShareWeights = share_weights<T, VPT>(BIAS, SHIFTED, FULL);
+  constexpr int kDepth = VPT > 2 ? 2 : kShareWeights ? 3 : 4;  // what 227 KB hold
   const int groups = group == 32 ? kBwdThreads / 32 : std::min(kBwdThreads / group, kMaxBarriers);
   const int threads = group * groups;
-  const size_t smem = static_cast<size_t>(threads) * VPT * 16 * (p.grad_sum != nullptr ? 3 : 2) * DEPTH;
+  const int slots = (p.grad_sum != nullptr ? 3 : 2) * kDepth + (kShareWeights ? 2 : 0);
+  const size_t smem = static_cast<size_t>(threads) * VPT * 16 * slots;
   int64_t grid = std::min<int64_t>({div_up(p.N, groups), device_sm_count(), kMaxParts});
   if (SHIFTED) {  // groups a multiple of kN
     int64_t unit = kN;
@@ -446,20 +493,26 @@ cudaError_t backward_rows(LnBackward& p, int64_t vectors, cudaStream_t s) {
     grid = std::min<int64_t>(div_up(grid, unit), kMaxParts / unit) * unit;
   }
   p.parts = static_cast<int>(grid);
-  const bool full = !SHIFTED && vectors == static_cast<int64_t>(group) * VPT;
-  const auto kernel = full ? ln_bwd_kernel<T, RMS, BIAS, VPT, DEPTH, SHIFTED, !SHIFTED>
-                           : ln_bwd_kernel<T, RMS, BIAS, VPT, DEPTH, SHIFTED, false>;
+  const auto kernel = ln_bwd_kernel<T, RMS, BIAS, VPT, kDepth, SHIFTED, FULL>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   kernel<<<static_cast<unsigned int>(grid), threads, smem, s>>>(p, group, groups);
   return cudaGetLastError();
 }
 
+template <typename T, bool RMS, bool BIAS, int VPT, bool SHIFTED>
+cudaError_t backward_rows(LnBackward& p, int64_t vectors, cudaStream_t s) {
+  const int group = static_cast<int>(div_up(vectors, 32 * VPT) * 32);
+  return !SHIFTED && vectors == static_cast<int64_t>(group) * VPT
+             ? launch_rows<T, RMS, BIAS, VPT, SHIFTED, !SHIFTED>(p, group, s)
+             : launch_rows<T, RMS, BIAS, VPT, SHIFTED, false>(p, group, s);
+}
+
 template <typename T, bool RMS, bool BIAS, bool SHIFTED>
 cudaError_t backward_rows(LnBackward& p, int64_t vectors, cudaStream_t s) {
-  if (vectors <= 32) return backward_rows<T, RMS, BIAS, 1, 4, SHIFTED>(p, vectors, s);
-  if (vectors <= 2 * kBwdThreads) return backward_rows<T, RMS, BIAS, 2, 4, SHIFTED>(p, vectors, s);
-  return backward_rows<T, RMS, BIAS, 4, 2, SHIFTED>(p, vectors, s);
+  if (vectors <= 32) return backward_rows<T, RMS, BIAS, 1, SHIFTED>(p, vectors, s);
+  if (vectors <= 2 * kBwdThreads) return backward_rows<T, RMS, BIAS, 2, SHIFTED>(p, vectors, s);
+  return backward_rows<T, RMS, BIAS, 4, SHIFTED>(p, vectors, s);
 }
 
 template <typename T, bool RMS>
@@ -468,7 +521,7 @@ cudaError_t backward(LnBackward p, float* grad_weight, float* grad_bias, int acc
   const Fit fit = fit_of<T>(p.N, p.H, p.weight, nullptr, p.param_dtype, Matrix{p.x, p.ld_x},
                             Matrix{p.grad_y, p.ld_grad_y}, Matrix{p.grad_sum, p.ld_grad_sum},
                             Matrix{p.grad_x, p.ld_grad_x});
-  const int64_t vectors = fit == kFitWhole ? p.H / Vec<T>::kN : div_up(p.H + Vec<T>::kN - 1, Vec<T>::kN);
+  const int64_t vectors = p.H / Vec<T>::kN;  // where rows start inside one, a few less
   cudaError_t e = cudaSuccess;
   if (p.N > 0 && fit != kFitNot && vectors <= kMaxRowVectors) {
     prof_begin(s, FLCE_KERNEL_LN_BWD);

@@ -32,105 +32,130 @@ __device__ __forceinline__ float row_sum(float v, float* scratch) {
   return warp_sum(lane < warps ? scratch[lane] : 0.f);
 }
 
-// Forward with the row in registers, VPT vectors a thread: a warp (WARP) or a CTA
-// takes one row, which is read once; the mean and then the sum of squares about it
-// are taken from the registers.
-template <typename T, bool RMS, int VPT, bool WARP, bool SHIFTED>
-__global__ void __launch_bounds__(WARP ? 256 : 1024) ln_fwd_kernel(const LnForward p) {
+// Forward with the row in registers, VPT vectors a thread: a warp (WARP) takes ROWS
+// rows, or a CTA one.  A row is read once; the mean and then the sum of squares about
+// it are taken from the registers.  48 registers a thread let 40 warps have their rows
+// under way on an SM: bf16 [16384, 4096] without residual took 51.3 us with 64, 48.2
+// so, and 55.3 with 32, where some are spilled.
+template <typename T, bool RMS, int VPT, int ROWS, bool WARP, bool SHIFTED>
+__global__ void __maxnreg__(VPT == 8 ? 64 : 48) ln_fwd_kernel(const LnForward p) {
   using V = Vec<T>;
   __shared__ float scratch[2][32];
   const int threads = WARP ? 32 : blockDim.x, t = WARP ? threadIdx.x & 31 : threadIdx.x;
-  const int64_t n = WARP ? static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
-  if (n >= p.N) return;
-  const T* x = static_cast<const T*>(p.x) + n * p.ld_x;
-  const Row<T, SHIFTED> row(x, p.H);
-  uint4 v[VPT];
-#pragma unroll
-  for (int k = 0; k < VPT; ++k) {
-    const int j = t + k * threads;
-    v[k] = j < row.vectors ? row.load(x, j) : make_uint4(0, 0, 0, 0);
-  }
-  if (p.residual != nullptr) {
-    const T* r = static_cast<const T*>(p.residual) + n * p.ld_residual;
-    uint4 w[VPT];
+  const int64_t first =
+      WARP ? (static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5)) * ROWS : blockIdx.x;
+  const int rows = static_cast<int>(min(p.N - first, static_cast<int64_t>(ROWS)));
+  if (rows <= 0) return;
+  uint4 v[ROWS][VPT];
+  float extra[ROWS];  // SHIFTED: the element beside the vectors
+  const auto load = [&](const void* m, int64_t ld, int i, uint4* to, float* one) {
+    const T* from = static_cast<const T*>(m) + (first + i) * ld;
+    const Row<T, SHIFTED> row(from, p.H);
+    const bool there = i < rows;
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
       const int j = t + k * threads;
-      w[k] = j < row.vectors ? row.load(r, j) : make_uint4(0, 0, 0, 0);
+      to[k] = there && j < row.vectors ? row.load(from, j) : make_uint4(0, 0, 0, 0);
     }
+    const int c = row.extra(t);
+    *one = there && c >= 0 ? to_float(from[c]) : 0.f;
+  };
 #pragma unroll
-    for (int k = 0; k < VPT; ++k) {
-      float a[V::kN], b[V::kN];
-      V::unpack(v[k], a);
-      V::unpack(w[k], b);
+  for (int i = 0; i < ROWS; ++i) load(p.x, p.ld_x, i, v[i], &extra[i]);
+  if (p.residual != nullptr) {
+    uint4 w[ROWS][VPT];
+    float one[ROWS];
 #pragma unroll
-      for (int i = 0; i < V::kN; ++i) a[i] += b[i];
-      v[k] = V::pack(a);
+    for (int i = 0; i < ROWS; ++i) load(p.residual, p.ld_residual, i, w[i], &one[i]);
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+#pragma unroll
+      for (int k = 0; k < VPT; ++k) {
+        float a[V::kN], b[V::kN];
+        V::unpack(v[i][k], a);
+        V::unpack(w[i][k], b);
+#pragma unroll
+        for (int e = 0; e < V::kN; ++e) a[e] += b[e];
+        v[i][k] = V::pack(a);
+      }
+      extra[i] = to_float(from_float<T>(extra[i] + one[i]));
     }
+  }
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) {
+    if (i >= rows) return;
+    const int64_t n = first + i;
+    T* y = static_cast<T*>(p.y) + n * p.ld_y;
+    const Row<T, SHIFTED> row(y, p.H);
+    const int c = row.extra(t);
     if (p.sum != nullptr) {
       T* s = static_cast<T*>(p.sum) + n * p.ld_sum;
 #pragma unroll
       for (int k = 0; k < VPT; ++k)
-        if (t + k * threads < row.vectors) row.store(s, t + k * threads, v[k]);
+        if (t + k * threads < row.vectors) row.store(s, t + k * threads, v[i][k]);
+      if (c >= 0) s[c] = from_float<T>(extra[i]);
     }
-  }
-  const float over = 1.f / static_cast<float>(row.length);
-  float mu = 0.f;
-  if (!RMS) {
-    float a = 0.f;
+    const float over = 1.f / static_cast<float>(row.length);
+    float mu = 0.f;
+    if (!RMS) {
+      float a = extra[i];
+#pragma unroll
+      for (int k = 0; k < VPT; ++k) {
+        float f[V::kN];
+        V::unpack(v[i][k], f);
+#pragma unroll
+        for (int e = 0; e < V::kN; ++e) a += f[e];
+      }
+      mu = row_sum<WARP>(a, scratch[0]) * over;
+    }
+    float q = c >= 0 ? (extra[i] - mu) * (extra[i] - mu) : 0.f;
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-      float f[V::kN];
-      V::unpack(v[k], f);
+      if (RMS || t + k * threads < row.vectors) {
+        float f[V::kN];
+        V::unpack(v[i][k], f);
 #pragma unroll
-      for (int i = 0; i < V::kN; ++i) a += f[i];
-    }
-    mu = row_sum<WARP>(a, scratch[0]) * over;
-  }
-  float q = 0.f;
-#pragma unroll
-  for (int k = 0; k < VPT; ++k) {
-    const int j = t + k * threads;
-    if (RMS || j < row.vectors) {
-      const bool all = RMS || row.whole(j);
-      float f[V::kN];
-      V::unpack(v[k], f);
-#pragma unroll
-      for (int i = 0; i < V::kN; ++i) {
-        const float d = f[i] - mu;
-        if (all || row.inside(row.column(j) + i)) q = fmaf(d, d, q);
+        for (int e = 0; e < V::kN; ++e) {
+          const float d = f[e] - mu;
+          q = fmaf(d, d, q);
+        }
       }
     }
-  }
-  q = row_sum<WARP>(q, scratch[1]) * over;
-  const float inv = rsqrtf(q + p.eps);
-  T* y = static_cast<T*>(p.y) + n * p.ld_y;
+    q = row_sum<WARP>(q, scratch[1]) * over;
+    const float inv = rsqrtf(q + p.eps);
 #pragma unroll
-  for (int k = 0; k < VPT; ++k) {
-    const int j = t + k * threads;
-    if (j < row.vectors) {
-      float f[V::kN];
-      V::unpack(v[k], f);
+    for (int k = 0; k < VPT; ++k) {
+      const int j = t + k * threads;
+      if (j < row.vectors) {
+        float f[V::kN];
+        V::unpack(v[i][k], f);
 #pragma unroll
-      for (int i = 0; i < V::kN; ++i) f[i] = (f[i] - mu) * inv;
-      if (p.weight != nullptr) {
-        float w[V::kN];
-        row.params(p.weight, p.param_dtype, j, w);
+        for (int e = 0; e < V::kN; ++e) f[e] = (f[e] - mu) * inv;
+        if (p.weight != nullptr) {
+          float w[V::kN];
+          row.params(p.weight, p.param_dtype, j, w);
 #pragma unroll
-        for (int i = 0; i < V::kN; ++i) f[i] *= w[i];
+          for (int e = 0; e < V::kN; ++e) f[e] *= w[e];
+        }
+        if (p.bias != nullptr) {
+          float b[V::kN];
+          row.params(p.bias, p.param_dtype, j, b);
+#pragma unroll
+          for (int e = 0; e < V::kN; ++e) f[e] += b[e];
+        }
+        row.store(y, j, V::pack(f));
       }
-      if (p.bias != nullptr) {
-        float b[V::kN];
-        row.params(p.bias, p.param_dtype, j, b);
-#pragma unroll
-        for (int i = 0; i < V::kN; ++i) f[i] += b[i];
-      }
-      row.store(y, j, V::pack(f));
     }
-  }
-  if (t == 0) {
-    if (p.mean != nullptr) p.mean[n] = mu;
-    if (p.rstd != nullptr) p.rstd[n] = inv;
+    if (c >= 0) {
+      float o = (extra[i] - mu) * inv;
+      if (p.weight != nullptr) o *= load_elem(p.weight, p.param_dtype, c);
+      if (p.bias != nullptr) o += load_elem(p.bias, p.param_dtype, c);
+      y[c] = from_float<T>(o);
+    }
+    if (t == 0) {
+      if (p.mean != nullptr) p.mean[n] = mu;
+      if (p.rstd != nullptr) p.rstd[n] = inv;
+    }
   }
 }
 
@@ -186,18 +211,25 @@ constexpr int64_t kMaxRowVectors = 8192;
 
 template <typename T, bool RMS, bool SHIFTED>
 void forward_rows(const LnForward& p, int64_t vectors, cudaStream_t s) {
-  const unsigned int rows = static_cast<unsigned int>(p.N), warps = 4;
-  const unsigned int grid = (rows + warps - 1) / warps;
-  if (vectors <= 32) {
-    ln_fwd_kernel<T, RMS, 1, true, SHIFTED><<<grid, 32 * warps, 0, s>>>(p);
+  constexpr int kWarps = 4;
+  // several short rows to a warp once every SM has all the warps it holds
+  const int rows = p.N >= int64_t(64) * device_sm_count() ? (vectors <= 32 ? 4 : vectors <= 64 ? 2 : 1) : 1;
+  const unsigned int grid = static_cast<unsigned int>(div_up(p.N, kWarps * rows));
+  if (vectors <= 32 && rows == 4) {
+    ln_fwd_kernel<T, RMS, 1, 4, true, SHIFTED><<<grid, 32 * kWarps, 0, s>>>(p);
+  } else if (vectors <= 32) {
+    ln_fwd_kernel<T, RMS, 1, 1, true, SHIFTED><<<grid, 32 * kWarps, 0, s>>>(p);
+  } else if (vectors <= 64 && rows == 2) {
+    ln_fwd_kernel<T, RMS, 2, 2, true, SHIFTED><<<grid, 32 * kWarps, 0, s>>>(p);
   } else if (vectors <= 64) {
-    ln_fwd_kernel<T, RMS, 2, true, SHIFTED><<<grid, 32 * warps, 0, s>>>(p);
+    ln_fwd_kernel<T, RMS, 2, 1, true, SHIFTED><<<grid, 32 * kWarps, 0, s>>>(p);
   } else if (vectors <= 128) {
-    ln_fwd_kernel<T, RMS, 4, true, SHIFTED><<<grid, 32 * warps, 0, s>>>(p);
+    ln_fwd_kernel<T, RMS, 4, 1, true, SHIFTED><<<grid, 32 * kWarps, 0, s>>>(p);
   } else if (vectors <= 4096) {
-    ln_fwd_kernel<T, RMS, 4, false, SHIFTED><<<rows, static_cast<unsigned int>(div_up(vectors, 128) * 32), 0, s>>>(p);
+    const unsigned int threads = static_cast<unsigned int>(div_up(vectors, 128) * 32);
+    ln_fwd_kernel<T, RMS, 4, 1, false, SHIFTED><<<static_cast<unsigned int>(p.N), threads, 0, s>>>(p);
   } else {
-    ln_fwd_kernel<T, RMS, 8, false, SHIFTED><<<rows, 1024, 0, s>>>(p);
+    ln_fwd_kernel<T, RMS, 8, 1, false, SHIFTED><<<static_cast<unsigned int>(p.N), 1024, 0, s>>>(p);
   }
 }
 
@@ -205,7 +237,7 @@ template <typename T, bool RMS>
 cudaError_t forward(const LnForward& p, cudaStream_t s) {
   const Fit fit = fit_of<T>(p.N, p.H, p.weight, p.bias, p.param_dtype, Matrix{p.x, p.ld_x},
                             Matrix{p.residual, p.ld_residual}, Matrix{p.y, p.ld_y}, Matrix{p.sum, p.ld_sum});
-  const int64_t vectors = fit == kFitWhole ? p.H / Vec<T>::kN : div_up(p.H + Vec<T>::kN - 1, Vec<T>::kN);
+  const int64_t vectors = p.H / Vec<T>::kN;  // where rows start inside one, a few less
   prof_begin(s, FLCE_KERNEL_LN_FWD);
   if (fit == kFitNot || vectors > kMaxRowVectors)
     ln_fwd_any_kernel<T, RMS>
