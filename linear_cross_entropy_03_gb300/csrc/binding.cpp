@@ -5,6 +5,7 @@
 // norm of 300 gradients took 365 us a call (here 32) and the norm of one row 25 us (7.5).
 #include <Python.h>
 
+#include <algorithm>
 #include <cstdarg>
 #include <vector>
 
@@ -47,16 +48,18 @@ int code_of(const at::Tensor& t) {
   }
 }
 
-bool here(const at::Tensor& t) { return t.is_cuda() && t.get_device() == c10::cuda::current_device(); }
-
 // An argument that is a tensor on the current GPU, or None where that is allowed.
-bool tensor_of(PyObject* o, const char* where, bool optional, const at::Tensor** t) {
+// `device`: the current GPU, looked up with the first tensor (-1 before).
+bool tensor_of(PyObject* o, const char* where, bool optional, const at::Tensor** t, int* device) {
   *t = nullptr;
   if (o == Py_None && optional) return true;
   if (!THPVariable_Check(o)) return fail(FLCE_ERR_INVALID_ARG, "%s: a tensor is wanted", where), false;
   *t = &THPVariable_Unpack(o);
-  if (!here(**t)) return fail(FLCE_ERR_INVALID_ARG, "%s: not on the current GPU", where), false;
-  return true;
+  if ((*t)->is_cuda()) {
+    if (*device < 0) *device = c10::cuda::current_device();
+    if ((*t)->get_device() == *device) return true;
+  }
+  return fail(FLCE_ERR_INVALID_ARG, "%s: not on the current GPU", where), false;
 }
 
 // A matrix: rows of contiguous elements at one distance.
@@ -139,10 +142,11 @@ bool flag(PyObject* o) { return o != Py_None && PyObject_IsTrue(o) == 1; }
 PyObject* layer_norm(PyObject*, PyObject* const* a, Py_ssize_t count) {
   HANDLE_TH_ERRORS
   if (count != 9) return fail(FLCE_ERR_INVALID_ARG, "layer_norm: arguments");
+  int device = -1;
   const at::Tensor *x, *w, *b, *r, *out, *sum_out;
-  if (!tensor_of(a[0], "layer_norm: x", false, &x) || !tensor_of(a[1], "layer_norm: weight", true, &w) ||
-      !tensor_of(a[2], "layer_norm: bias", true, &b) || !tensor_of(a[5], "layer_norm: residual", true, &r) ||
-      !tensor_of(a[6], "layer_norm: out", true, &out) || !tensor_of(a[7], "layer_norm: sum_out", true, &sum_out))
+  if (!tensor_of(a[0], "layer_norm: x", false, &x, &device) || !tensor_of(a[1], "layer_norm: weight", true, &w, &device) ||
+      !tensor_of(a[2], "layer_norm: bias", true, &b, &device) || !tensor_of(a[5], "layer_norm: residual", true, &r, &device) ||
+      !tensor_of(a[6], "layer_norm: out", true, &out, &device) || !tensor_of(a[7], "layer_norm: sum_out", true, &sum_out, &device))
     return nullptr;
   const long kind = PyLong_AsLong(a[3]);
   const double eps = PyFloat_AsDouble(a[4]);
@@ -183,16 +187,17 @@ PyObject* layer_norm(PyObject*, PyObject* const* a, Py_ssize_t count) {
 PyObject* layer_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t count) {
   HANDLE_TH_ERRORS
   if (count != 15) return fail(FLCE_ERR_INVALID_ARG, "layer_norm_backward: arguments");
+  int device = -1;
   const at::Tensor *gy, *x, *w, *mean, *rstd, *gs, *out, *gw_out, *gb_out, *ws;
-  if (!tensor_of(a[0], "layer_norm_backward: grad_y", false, &gy) || !tensor_of(a[1], "layer_norm_backward: x", false, &x) ||
-      !tensor_of(a[2], "layer_norm_backward: weight", true, &w) ||
-      !tensor_of(a[3], "layer_norm_backward: mean", true, &mean) ||
-      !tensor_of(a[4], "layer_norm_backward: rstd", false, &rstd) ||
-      !tensor_of(a[6], "layer_norm_backward: grad_sum", true, &gs) ||
-      !tensor_of(a[10], "layer_norm_backward: out", true, &out) ||
-      !tensor_of(a[11], "layer_norm_backward: grad_weight_out", true, &gw_out) ||
-      !tensor_of(a[12], "layer_norm_backward: grad_bias_out", true, &gb_out) ||
-      !tensor_of(a[14], "layer_norm_backward: workspace", true, &ws))
+  if (!tensor_of(a[0], "layer_norm_backward: grad_y", false, &gy, &device) || !tensor_of(a[1], "layer_norm_backward: x", false, &x, &device) ||
+      !tensor_of(a[2], "layer_norm_backward: weight", true, &w, &device) ||
+      !tensor_of(a[3], "layer_norm_backward: mean", true, &mean, &device) ||
+      !tensor_of(a[4], "layer_norm_backward: rstd", false, &rstd, &device) ||
+      !tensor_of(a[6], "layer_norm_backward: grad_sum", true, &gs, &device) ||
+      !tensor_of(a[10], "layer_norm_backward: out", true, &out, &device) ||
+      !tensor_of(a[11], "layer_norm_backward: grad_weight_out", true, &gw_out, &device) ||
+      !tensor_of(a[12], "layer_norm_backward: grad_bias_out", true, &gb_out, &device) ||
+      !tensor_of(a[14], "layer_norm_backward: workspace", true, &ws, &device))
     return nullptr;
   const long kind = PyLong_AsLong(a[5]);
   if (PyErr_Occurred()) return nullptr;
@@ -238,10 +243,11 @@ bool for_each(PyObject* sequence, const char* where, F f) {
   PyObject* fast = PySequence_Fast(sequence, "a sequence of tensors is wanted");
   if (fast == nullptr) return false;
   bool ok = true;
+  int device = -1;
   const Py_ssize_t n = PySequence_Fast_GET_SIZE(fast);
   for (Py_ssize_t i = 0; ok && i < n; ++i) {
     const at::Tensor* t;
-    ok = tensor_of(PySequence_Fast_GET_ITEM(fast, i), where, true, &t) && f(i, t);
+    ok = tensor_of(PySequence_Fast_GET_ITEM(fast, i), where, true, &t, &device) && f(i, t);
   }
   Py_DECREF(fast);
   return ok;
@@ -252,6 +258,9 @@ PyObject* grad_norm_of(PyObject*, PyObject* const* a, Py_ssize_t count) {
   HANDLE_TH_ERRORS
   if (count != 6) return fail(FLCE_ERR_INVALID_ARG, "grad_norm: arguments");
   std::vector<flce_tensor_t> table;
+  const Py_ssize_t expected = PySequence_Size(a[0]);
+  if (expected < 0) PyErr_Clear();
+  table.reserve(static_cast<size_t>(std::max<Py_ssize_t>(expected, 0)));
   const bool ok = for_each(a[0], "grad_norm", [&](Py_ssize_t, const at::Tensor* t) {
     if (t == nullptr) return true;
     const int dtype = code_of(*t);
@@ -263,8 +272,9 @@ PyObject* grad_norm_of(PyObject*, PyObject* const* a, Py_ssize_t count) {
   if (!ok) return nullptr;
   const double scale = PyFloat_AsDouble(a[1]), most = PyFloat_AsDouble(a[2]), eps = PyFloat_AsDouble(a[3]);
   if (PyErr_Occurred()) return nullptr;
+  int device = -1;
   const at::Tensor *out, *ws;
-  if (!tensor_of(a[4], "grad_norm: out", true, &out) || !tensor_of(a[5], "grad_norm: workspace", true, &ws) ||
+  if (!tensor_of(a[4], "grad_norm: out", true, &out, &device) || !tensor_of(a[5], "grad_norm: workspace", true, &ws, &device) ||
       (out != nullptr && !floats_of(*out, 2, "grad_norm: out")))
     return nullptr;
   const auto options = at::TensorOptions().device(at::kCUDA, c10::cuda::current_device());

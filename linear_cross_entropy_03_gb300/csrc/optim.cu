@@ -35,7 +35,7 @@ __device__ __forceinline__ int entry_of(const E* entry, int count, unsigned int 
 
 // ------------------------------------------------------------ gradient norm
 
-constexpr int kNormChunk = 4096;   // 16-byte vectors a CTA takes at a time
+constexpr int kNormChunk = 1024;   // 16-byte vectors
 constexpr int kNormParts = 608;    // most CTAs, and partial sums, of a launch
 
 struct NormEntry {
@@ -45,9 +45,10 @@ struct NormEntry {
   int dtype;
 };
 
-constexpr int kNormEntries = 1280;
+constexpr int kNormEntries = 1280, kNormMiddle = 320, kNormFew = 16;
+template <int MAX>
 struct NormArgs {
-  NormEntry entry[kNormEntries];
+  NormEntry entry[MAX];
   int count;
   unsigned int chunks;
   float* part;  // [gridDim.x]
@@ -73,21 +74,29 @@ __device__ __forceinline__ float squares(const uint4& r, int dtype) {
   return s;
 }
 
-// Partial sums of squares: CTA b takes chunks b, b + gridDim.x, ...  A chunk is
-// 16-byte vectors from the tensor's first 16-byte boundary on; the elements
-// before it, and those after the last vector, go with the first chunk.
-__global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_constant__ NormArgs a) {
+// Partial sums of squares: each CTA takes a range of chunks, going from one tensor to
+// the next.  A chunk is 16-byte vectors from the tensor's first 16-byte boundary on;
+// the elements before it, and those after the last vector, go with the first chunk.
+template <int MAX>
+__global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_constant__ NormArgs<MAX> a) {
   grid_dependents_launch();
   __shared__ float scratch[kThreads / 32];
   float sum = 0.f;
-  for (unsigned int c = blockIdx.x; c < a.chunks; c += gridDim.x) {
-    const NormEntry& e = a.entry[entry_of(a.entry, a.count, c)];
+  const uint64_t all = a.chunks;
+  unsigned int c = static_cast<unsigned int>(all * blockIdx.x / gridDim.x);
+  const unsigned int c_end = static_cast<unsigned int>(all * (blockIdx.x + 1) / gridDim.x);
+  int at = entry_of(a.entry, a.count, c);
+  while (c < c_end) {
+    const NormEntry& e = a.entry[at];
+    const unsigned int e_end = at + 1 < a.count ? a.entry[at + 1].chunk0 : a.chunks;
+    const unsigned int stop = min(c_end, e_end);
     const int per = e.dtype == FLCE_DTYPE_FP32 ? 4 : 8;  // elements of a vector
     const int64_t esz = 16 / per;
     const int64_t head = min(static_cast<int64_t>((16 - reinterpret_cast<uintptr_t>(e.data) % 16) % 16) / esz, e.n);
     const uint4* v = reinterpret_cast<const uint4*>(static_cast<const char*>(e.data) + head * esz);
     const int64_t vectors = (e.n - head) / per;
-    const int64_t v0 = static_cast<int64_t>(c - e.chunk0) * kNormChunk, v1 = min(v0 + kNormChunk, vectors);
+    const int64_t v0 = static_cast<int64_t>(c - e.chunk0) * kNormChunk;
+    const int64_t v1 = min(static_cast<int64_t>(stop - e.chunk0) * kNormChunk, vectors);
     constexpr int kBatch = 8;
     int64_t i = v0 + threadIdx.x;
     for (; i + (kBatch - 1) * kThreads < v1; i += kBatch * kThreads) {
@@ -104,6 +113,8 @@ __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_consta
       const float h = tail < e.n ? load_elem(e.data, e.dtype, tail) : 0.f;
       sum = fmaf(g, g, fmaf(h, h, sum));
     }
+    c = stop;
+    ++at;
   }
   sum = warp_sum(sum);
   if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = sum;
@@ -138,11 +149,11 @@ __global__ void __launch_bounds__(1024)
 // -------------------------------------------------------------------- AdamW
 
 constexpr int kAdamChunk = 4096;   // elements of a CTA
-// With 8-bit moments: two blocks a warp, the second loading while the first is
-// worked on.  525M elements with a 16-bit copy took 1.52 ms so; with one block
-// 1.61 ms, with four 1.86, with eight 1.75.
-constexpr int kAdamChunk8 = 4096;
-static_assert(kAdamChunk8 % (FLCE_ADAMW_BLOCK * (kThreads / 32)) == 0, "whole blocks for every warp");
+// With 8-bit moments: two blocks a warp, the second loading while the first is worked
+// on, and four warps.  525M elements with a 16-bit copy took 1.42 ms so; with eight
+// warps 1.52 ms, with two 1.67; with four blocks a warp 1.63, with one 1.61 (8 warps).
+constexpr int kAdamChunk8 = 2048, kThreads8 = 128;
+static_assert(kAdamChunk8 % (FLCE_ADAMW_BLOCK * (kThreads8 / 32)) == 0, "whole blocks for every warp");
 constexpr float kE4m3Max = 448.f;
 constexpr unsigned int kE4m3Nan = 0x7Fu;
 
@@ -494,10 +505,10 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
 // under way while it works on one: the two maxima over the block and the roundings
 // behind them are a long chain.
 template <int MAX, bool STOCHASTIC>
-__global__ void __launch_bounds__(kThreads) adamw8_kernel(const __grid_constant__ AdamArgs<MAX> a) {
+__global__ void __launch_bounds__(kThreads8) adamw8_kernel(const __grid_constant__ AdamArgs<MAX> a) {
   const AdamEntry& e = a.entry[entry_of(a.entry, a.count, blockIdx.x)];
   const AdamNumbers& k = a.num;
-  constexpr int64_t kStep = kThreads / 32 * FLCE_ADAMW_BLOCK;
+  constexpr int64_t kStep = kThreads8 / 32 * FLCE_ADAMW_BLOCK;
   const int lane = threadIdx.x & 31;
   const int64_t i0 = static_cast<int64_t>(blockIdx.x - e.chunk0) * kAdamChunk8, i1 = min(i0 + kAdamChunk8, e.n);
   const int64_t whole = e.head == 0 ? e.n - e.n % FLCE_ADAMW_BLOCK : 0;  // where blocks by vectors end
@@ -516,6 +527,20 @@ __global__ void __launch_bounds__(kThreads) adamw8_kernel(const __grid_constant_
 }
 
 template <int MAX>
+cudaError_t launch_norm(const NormEntry* entry, int count, unsigned int chunks, float* part, int grid, cudaStream_t s) {
+  NormArgs<MAX> a;
+  std::copy(entry, entry + count, a.entry);
+  a.count = count;
+  a.chunks = chunks;
+  a.part = part;
+  prof_begin(s, FLCE_KERNEL_GRAD_NORM);
+  grad_norm_kernel<MAX><<<grid, kThreads, 0, s>>>(a);
+  const cudaError_t e = cudaGetLastError();
+  prof_end(s);
+  return e;
+}
+
+template <int MAX>
 cudaError_t launch_adamw(const AdamEntry* entry, int count, unsigned int chunks, const AdamNumbers& num, int bits,
                          cudaStream_t s) {
   AdamArgs<MAX> a;
@@ -526,23 +551,31 @@ cudaError_t launch_adamw(const AdamEntry* entry, int count, unsigned int chunks,
   if (bits == 32)
     adamw_kernel<MAX><<<chunks, kThreads, 0, s>>>(a);
   else if (num.stochastic)
-    adamw8_kernel<MAX, true><<<chunks, kThreads, 0, s>>>(a);
+    adamw8_kernel<MAX, true><<<chunks, kThreads8, 0, s>>>(a);
   else
-    adamw8_kernel<MAX, false><<<chunks, kThreads, 0, s>>>(a);
+    adamw8_kernel<MAX, false><<<chunks, kThreads8, 0, s>>>(a);
   const cudaError_t e = cudaGetLastError();
   prof_end(s);
   return e;
 }
 
-// Tables of three sizes: a launch copies its whole parameter block.
-constexpr int kAdamEntries = 360, kAdamMiddle = 40, kAdamFew = 4;
+// Tables of a few sizes: a launch copies its whole parameter block.
+constexpr int kAdamEntries = 360, kAdamMore = 128, kAdamMiddle = 40, kAdamFew = 4;
 static_assert(sizeof(AdamArgs<kAdamEntries>) <= 32764, "kernel parameters");
-static_assert(sizeof(NormArgs) <= 32764, "kernel parameters");
+static_assert(sizeof(NormArgs<kNormEntries>) <= 32764, "kernel parameters");
+
+cudaError_t launch_norm_any(const NormEntry* entry, int count, unsigned int chunks, float* part, int grid,
+                            cudaStream_t s) {
+  if (count <= kNormFew) return launch_norm<kNormFew>(entry, count, chunks, part, grid, s);
+  if (count <= kNormMiddle) return launch_norm<kNormMiddle>(entry, count, chunks, part, grid, s);
+  return launch_norm<kNormEntries>(entry, count, chunks, part, grid, s);
+}
 
 cudaError_t launch_adamw_any(const AdamEntry* entry, int count, unsigned int chunks, const AdamNumbers& num, int bits,
                              cudaStream_t s) {
   if (count <= kAdamFew) return launch_adamw<kAdamFew>(entry, count, chunks, num, bits, s);
   if (count <= kAdamMiddle) return launch_adamw<kAdamMiddle>(entry, count, chunks, num, bits, s);
+  if (count <= kAdamMore) return launch_adamw<kAdamMore>(entry, count, chunks, num, bits, s);
   return launch_adamw<kAdamEntries>(entry, count, chunks, num, bits, s);
 }
 
@@ -550,13 +583,14 @@ cudaError_t launch_adamw_any(const AdamEntry* entry, int count, unsigned int chu
 // for all of them; else -1.  (Blocks of 8-bit moments are counted from the
 // start, so that only 0 serves there.)
 int common_head(const flce_adamw_tensor_t& t) {
-  const size_t state = t.moment_bits == 8 ? 1 : 4;
-  const auto before = [](const void* p, size_t esz) {
-    return static_cast<int>((4 - reinterpret_cast<uintptr_t>(p) / esz % 4) % 4);
+  const int state = t.moment_bits == 8 ? 0 : 2;  // log2 of an element's size
+  const auto size = [](int dtype) { return dtype == FLCE_DTYPE_FP32 ? 2 : 1; };
+  const auto before = [](const void* p, int log2_size) {
+    return static_cast<int>(-(reinterpret_cast<uintptr_t>(p) >> log2_size) & 3);
   };
-  const int head = before(t.param, elem_size(t.param_dtype));
-  if (head != before(t.grad, elem_size(t.grad_dtype)) || head != before(t.exp_avg, state) ||
-      head != before(t.exp_avg_sq, state) || (t.copy != nullptr && head != before(t.copy, elem_size(t.copy_dtype))))
+  const int head = before(t.param, size(t.param_dtype));
+  if (head != before(t.grad, size(t.grad_dtype)) || head != before(t.exp_avg, state) ||
+      head != before(t.exp_avg_sq, state) || (t.copy != nullptr && head != before(t.copy, size(t.copy_dtype))))
     return -1;
   return t.n > head ? head : -1;
 }
@@ -610,27 +644,22 @@ flce_status_t grad_norm(const flce_tensor_t* tensors, int64_t count, float grad_
   float* part = static_cast<float*>(workspace);
   const int most = std::min(kNormParts, 4 * device_sm_count());
   int parts = 0;
-  NormArgs a;
+  NormEntry entry[kNormEntries];
   for (int64_t i = 0; i < count;) {
     int64_t chunks = 0;
-    a.count = 0;
-    for (; i < count && a.count < kNormEntries; ++i) {
+    int filled = 0;
+    for (; i < count && filled < kNormEntries; ++i) {
       if (tensors[i].n == 0) continue;
       // at least the vectors from the first boundary on (a chunk too many finds nothing)
       const int64_t more = div_up(tensors[i].n, kNormChunk * static_cast<int64_t>(16 / elem_size(tensors[i].dtype)));
       if (chunks + more > 0x7fffffff) break;
-      a.entry[a.count++] = {tensors[i].data, tensors[i].n, static_cast<unsigned int>(chunks), tensors[i].dtype};
+      entry[filled++] = {tensors[i].data, tensors[i].n, static_cast<unsigned int>(chunks), tensors[i].dtype};
       chunks += more;
     }
-    if (a.count == 0) break;
-    a.chunks = static_cast<unsigned int>(chunks);
-    a.part = part + parts;
+    if (filled == 0) break;
     const int grid = static_cast<int>(std::min<int64_t>(chunks, most));
-    prof_begin(s, FLCE_KERNEL_GRAD_NORM);
-    grad_norm_kernel<<<grid, kThreads, 0, s>>>(a);
-    const cudaError_t e = cudaGetLastError();
-    prof_end(s);
-    if (e != cudaSuccess) return FLCE_ERR_CUDA;
+    if (launch_norm_any(entry, filled, static_cast<unsigned int>(chunks), part + parts, grid, s) != cudaSuccess)
+      return FLCE_ERR_CUDA;
     parts += grid;
   }
   prof_begin(s, FLCE_KERNEL_GRAD_NORM);
