@@ -110,6 +110,13 @@ __device__ __forceinline__ Pair fma_pair(Pair a, Pair b, Pair c) {
   return r;
 }
 
+// load_four_bits' four elements as two pairs.
+__device__ __forceinline__ void four_pairs(const uint4& r, int dtype, Pair* to) {
+  const float4 f = four_floats(r, dtype);
+  to[0] = pair(f.x, f.y);
+  to[1] = pair(f.z, f.w);
+}
+
 inline bool float_dtype(int dtype) {
   return dtype == FLCE_DTYPE_BF16 || dtype == FLCE_DTYPE_FP16 || dtype == FLCE_DTYPE_FP32;
 }

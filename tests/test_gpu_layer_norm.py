@@ -115,6 +115,56 @@ def test_many_rows(n, h):
     check_backward(grads, gy, x, w, out["mean"], out["rstd"], None, False, "bf16")
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("h", [1, 8, 63, 64, 65, 100, 129, 200, 256, 261, 512, 515, 1027])
+def test_many_short_rows(h, dtype):
+    """More rows than the SMs hold warps: several a warp, and many a group of the backward pass."""
+    n = 12001
+    x, gy = rows(n, h, dtype, 1), rows(n, h, dtype, 2, 1e-2, 0.0)
+    r, w, b = rows(n, h, dtype, 5), vector(h, dtype, 3, 1.0), vector(h, dtype, 4, 0.0)
+    out = flce.layer_norm(x, w, b, residual=r)
+    check_forward(out, x, r, w, b, 1e-5, False, dtype)
+    grads = flce.layer_norm_backward(gy, out["sum"], w, mean=out["mean"], rstd=out["rstd"], grad_sum=x)
+    check_backward(grads, gy, out["sum"], w, out["mean"], out["rstd"], x, False, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("h,first", [(500, 1), (1000, 7), (2047, 3), (2048, 5), (4099, 2), (8200, 6)])
+def test_rows_that_start_inside_a_vector(h, first, dtype):
+    """Contiguous matrices whose first element lies anywhere in 16 bytes, with weights at another such place."""
+    n = 37
+    def shifted(k, scale=1.0):
+        flat = rows(1, n * h + 16, dtype, k, scale)[0]
+        return flat[first:first + n * h].view(n, h)
+    x, r, gy, gs = shifted(1), shifted(2), shifted(3, 1e-2), shifted(4, 1e-2)
+    out_y, out_s, out_g = shifted(5), shifted(6), shifted(7)
+    for at in (0, 1, 3):
+        w, b = vector(h + 8, dtype, 8, 1.0)[at:at + h], vector(h + 8, "fp32", 9, 0.0)[at:at + h].to(TYPES[dtype])
+        out = flce.layer_norm(x, w, b, residual=r, out=out_y, sum_out=out_s)
+        check_forward(out, x, r, w, b, 1e-5, False, dtype)
+        grads = flce.layer_norm_backward(gy, out_s, w, mean=out["mean"], rstd=out["rstd"], grad_sum=gs, out=out_g)
+        check_backward(grads, gy, out_s, w, out["mean"], out["rstd"], gs, False, dtype)
+        grads = flce.layer_norm_backward(gy, out_s, w.float(), mean=out["mean"], rstd=out["rstd"])
+        check_backward(grads, gy, out_s, w.float(), out["mean"], out["rstd"], None, False, dtype)
+
+
+@pytest.mark.parametrize("n,h,dtype", [(1, 64, "bf16"), (3, 2047, "bf16"), (9, 1001, "fp16"), (29, 2048, "fp32"), (7, 77, "fp32"),
+                                       (500, 4096, "bf16"), (400, 513, "bf16"), (5, 30, "bf16"), (700, 20001, "bf16")])
+def test_workspace_of_the_stated_size_is_enough(n, h, dtype):
+    """Nothing behind the workspace or the column sums is written."""
+    x, gy = rows(n, h, dtype, 1), rows(n, h, dtype, 2)
+    out = flce.layer_norm(x)
+    stats = dict(mean=out["mean"], rstd=out["rstd"])
+    want = flce.layer_norm_backward(gy, x, **stats)
+    size = flce.ln_workspace_size(n, h)
+    room = torch.full((size + 4096,), 77, dtype=torch.uint8, device="cuda")
+    sums = torch.full((2, h + 64), 9.0, device="cuda")
+    got = flce.layer_norm_backward(gy, x, **stats, workspace=room[:size], grad_weight_out=sums[0, :h],
+                                   grad_bias_out=sums[1, :h])
+    assert (room[size:] == 77).all() and (sums[:, h:] == 9).all()
+    assert torch.equal(got["grad_weight"], want["grad_weight"]) and torch.equal(got["grad_x"], want["grad_x"])
+
+
 @pytest.mark.parametrize("n,h,dtype", [(2, 40000, "bf16"), (3, 70001, "bf16"), (2, 33000, "fp32"), (5, 65536, "fp16")])
 def test_long_rows(n, h, dtype):
     x, gy = rows(n, h, dtype, 1), rows(n, h, dtype, 2, 1e-2, 0.0)
