@@ -107,32 +107,12 @@ def _native():
     return _binding
 
 
-def _code(t, where) -> int:
-    """The dtype code of a bf16, fp16 or fp32 tensor."""
-    import torch
-    code = {torch.bfloat16: 0, torch.float32: 1, torch.float16: 2}.get(t.dtype)
-    if code is None:
-        raise FlceError(2, f"{where}: {t.dtype}")
-    return code
-
-
-def _here(t, where):
-    import torch
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
-        raise FlceError(1, f"{where}: on {t.device}, not on the current GPU")
-
-
-def _flat(t, where) -> int:
-    if not t.is_contiguous():
-        raise FlceError(2, f"{where}: not contiguous")
-    return t.numel()
-
-
 def _floats(t, n, where):
     import torch
     if t.dtype is not torch.float32 or t.numel() != n or not t.is_contiguous():
         raise FlceError(1, f"{where}: a contiguous fp32 tensor of {n} elements is wanted")
-    _here(t, where)
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        raise FlceError(1, f"{where}: on {t.device}, not on the current GPU")
     return t
 
 
@@ -262,61 +242,24 @@ class AdamW:
         step = 0 if step is None else int(step)
         if step < 0:
             raise FlceError(1, "AdamW: a negative step")
+        if state is None:
+            for i, p in enumerate(self.params):
+                small = moments == "8bit" and p.numel() >= min_8bit_size
+                kind = torch.float8_e4m3fn if small else torch.float32
+                given[0][i], given[1][i] = (torch.zeros(p.shape, dtype=kind, device=p.device) for _ in range(2))
+                if small:
+                    blocks = -(-p.numel() // ADAMW_BLOCK)
+                    given[2][i], given[3][i] = (torch.zeros(blocks, device=p.device) for _ in range(2))
+        self.exp_avg, self.exp_avg_sq, self.exp_avg_scale, self.exp_avg_sq_scale = given
         self._table = (AdamWEntry * count)()
         self._numel = (ctypes.c_int64 * count)()
-        memory = []
-        for i, p in enumerate(self.params):
-            e, where = self._table[i], f"AdamW: tensor {i}"
-            e.param_dtype, n = _code(p, where), _flat(p, where)
-            _here(p, where)
-            m, v, ms, vs = (x[i] for x in given)
-            if state is None:
-                small = moments == "8bit" and n >= min_8bit_size
-                kind = torch.float8_e4m3fn if small else torch.float32
-                m, v = (torch.zeros(p.shape, dtype=kind, device=p.device) for _ in range(2))
-                if small:
-                    ms, vs = (torch.zeros(-(-n // ADAMW_BLOCK), device=p.device) for _ in range(2))
-            e.moment_bits = self._state_bits(m, v, ms, vs, n, where)
-            c = copies[i]
-            if c is not None:
-                e.copy_dtype = _code(c, where + ", copy")
-                _here(c, where + ", copy")
-                if _flat(c, where + ", copy") != n:
-                    raise FlceError(1, f"{where}: its copy has another size")
-            for x, t in zip(given, (m, v, ms, vs)):
-                x[i] = t
-            e.param, e.exp_avg, e.exp_avg_sq, e.exp_avg_scale, e.exp_avg_sq_scale, e.copy = (
-                _ptr(t) for t in (p, m, v, ms, vs, c))
-            e.n, e.weight_decay, e.lr_scale = n, decay[i], scale[i]
-            self._numel[i] = n
-            memory += [(t.data_ptr(), t.numel() * t.element_size(), i) for t in (p, m, v, ms, vs, c) if t is not None]
-        memory = sorted(x for x in memory if x[1])
-        for (start, size, i), (after, _, k) in zip(memory, memory[1:]):
-            if start + size > after:
-                raise FlceError(1, f"AdamW: tensors {i} and {k} share memory")
-        self.exp_avg, self.exp_avg_sq, self.exp_avg_scale, self.exp_avg_sq_scale = given
+        _native().adamw_table(ctypes.addressof(self._table), ctypes.addressof(self._numel), self.params, *given, copies,
+                              decay, scale)
         self._numbers = AdamWNumbers(beta1=betas[0], beta2=betas[1], eps=eps, stochastic=int(seed is not None),
                                      seed=seed or 0)
         self._addresses = tuple(map(ctypes.addressof, (self._table, self._numel, self._numbers)))
         self._steps = step
         self._step_dev = torch.full((1,), step, dtype=torch.int64, device="cuda") if capturable else None
-
-    @staticmethod
-    def _state_bits(m, v, ms, vs, n, where):
-        import torch
-        for t in (m, v):
-            if t is None or t.dtype not in (torch.float32, torch.float8_e4m3fn) or t.dtype != m.dtype:
-                raise FlceError(2, f"{where}: moments are both fp32 or both float8_e4m3fn")
-            _here(t, where + ", moments")
-            if _flat(t, where + ", moments") != n:
-                raise FlceError(1, f"{where}: moments of another size")
-        scaled = m.dtype is torch.float8_e4m3fn
-        if (ms is not None) != scaled or (vs is not None) != scaled:
-            raise FlceError(1, f"{where}: 8-bit moments come with scales, and fp32 ones without")
-        if scaled:
-            _floats(ms, -(-n // ADAMW_BLOCK), where + ", exp_avg_scale")
-            _floats(vs, -(-n // ADAMW_BLOCK), where + ", exp_avg_sq_scale")
-        return 8 if scaled else 32
 
     @property
     def steps(self) -> int:

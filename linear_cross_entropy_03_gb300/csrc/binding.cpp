@@ -292,6 +292,69 @@ PyObject* grad_norm_of(PyObject*, PyObject* const* a, Py_ssize_t count) {
   END_HANDLE_TH_ERRORS
 }
 
+// adamw_table(table, sizes, params, exp_avg, exp_avg_sq, exp_avg_scale, exp_avg_sq_scale, copies, weight_decay,
+// lr_scale): checks an optimiser's tensors, lists of one length, and fills the table at address `table` and the
+// element counts at `sizes` with them.
+PyObject* adamw_table(PyObject*, PyObject* const* a, Py_ssize_t count) {
+  HANDLE_TH_ERRORS
+  if (count != 10) return fail(FLCE_ERR_INVALID_ARG, "AdamW: arguments");
+  auto* table = static_cast<flce_adamw_tensor_t*>(PyLong_AsVoidPtr(a[0]));
+  auto* sizes = static_cast<int64_t*>(PyLong_AsVoidPtr(a[1]));
+  if (PyErr_Occurred()) return nullptr;
+  for (int k = 2; k < 10; ++k)
+    if (!PyList_Check(a[k]) || PyList_GET_SIZE(a[k]) != PyList_GET_SIZE(a[2]))
+      return fail(FLCE_ERR_INVALID_ARG, "AdamW: lists of one length are wanted");
+  struct Span {
+    uintptr_t from, to;
+    Py_ssize_t tensor;
+  };
+  std::vector<Span> spans;
+  int device = -1;
+  for (Py_ssize_t i = 0; i < PyList_GET_SIZE(a[2]); ++i) {
+    const at::Tensor* t[6];  // parameter, moments, their scales, copy
+    for (int k = 0; k < 6; ++k) {
+      if (!tensor_of(PyList_GET_ITEM(a[2 + k], i), "AdamW: a tensor", k > 2, &t[k], &device)) return nullptr;
+      if (t[k] != nullptr && !t[k]->is_contiguous())
+        return fail(FLCE_ERR_UNSUPPORTED, "AdamW: tensor %zd: not contiguous", i);
+    }
+    const int64_t n = t[0]->numel(), blocks = (n + FLCE_ADAMW_BLOCK - 1) / FLCE_ADAMW_BLOCK;
+    flce_adamw_tensor_t& e = table[i];
+    e.param_dtype = code_of(*t[0]);
+    e.copy_dtype = t[5] != nullptr ? code_of(*t[5]) : FLCE_DTYPE_BF16;
+    if (e.param_dtype == kUnknown || e.copy_dtype == kUnknown)
+      return fail(FLCE_ERR_UNSUPPORTED, "AdamW: tensor %zd: its type, or its copy's", i);
+    const bool scaled = t[1]->scalar_type() == at::kFloat8_e4m3fn;
+    if (t[1]->scalar_type() != t[2]->scalar_type() || (!scaled && t[1]->scalar_type() != at::kFloat))
+      return fail(FLCE_ERR_UNSUPPORTED, "AdamW: tensor %zd: moments are both fp32 or both float8_e4m3fn", i);
+    if (t[1]->numel() != n || t[2]->numel() != n || (t[5] != nullptr && t[5]->numel() != n))
+      return fail(FLCE_ERR_INVALID_ARG, "AdamW: tensor %zd: moments or copy of another size", i);
+    for (int k = 3; k < 5; ++k)
+      if (scaled != (t[k] != nullptr) || (scaled && !floats_of(*t[k], blocks, "AdamW: scales")))
+        return PyErr_Occurred() ? nullptr
+                                : fail(FLCE_ERR_INVALID_ARG, "AdamW: tensor %zd: 8-bit moments come with scales, fp32 "
+                                       "ones without", i);
+    void* at[6];
+    for (int k = 0; k < 6; ++k) {
+      at[k] = t[k] != nullptr ? t[k]->data_ptr() : nullptr;
+      const uintptr_t from = reinterpret_cast<uintptr_t>(at[k]);
+      if (t[k] != nullptr && t[k]->nbytes() > 0) spans.push_back({from, from + t[k]->nbytes(), i});
+    }
+    e.param = at[0], e.exp_avg = at[1], e.exp_avg_sq = at[2];
+    e.exp_avg_scale = static_cast<float*>(at[3]), e.exp_avg_sq_scale = static_cast<float*>(at[4]), e.copy = at[5];
+    e.moment_bits = scaled ? 8 : 32;
+    e.weight_decay = static_cast<float>(PyFloat_AsDouble(PyList_GET_ITEM(a[8], i)));
+    e.lr_scale = static_cast<float>(PyFloat_AsDouble(PyList_GET_ITEM(a[9], i)));
+    if (PyErr_Occurred()) return nullptr;
+    e.n = sizes[i] = n;
+  }
+  std::sort(spans.begin(), spans.end(), [](const Span& x, const Span& y) { return x.from < y.from; });
+  for (size_t k = 1; k < spans.size(); ++k)
+    if (spans[k].from < spans[k - 1].to)
+      return fail(FLCE_ERR_INVALID_ARG, "AdamW: tensors %zd and %zd share memory", spans[k - 1].tensor, spans[k].tensor);
+  Py_RETURN_NONE;
+  END_HANDLE_TH_ERRORS
+}
+
 // adamw(table, sizes, count, numbers, grads): fills the gradients into the table of
 // flce_adamw_tensor_t at address `table` (an element count of 0 where there is none)
 // and takes the step with the flce_adamw_t at `numbers`.
@@ -341,6 +404,7 @@ PyMethodDef kMethods[] = {
      METH_FASTCALL, nullptr},
     {"grad_norm", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(grad_norm_of)), METH_FASTCALL, nullptr},
     {"adamw", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(adamw)), METH_FASTCALL, nullptr},
+    {"adamw_table", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(adamw_table)), METH_FASTCALL, nullptr},
     {"set_error", set_error, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 

@@ -32,6 +32,31 @@ __device__ __forceinline__ float row_sum(float v, float* scratch) {
   return warp_sum(lane < warps ? scratch[lane] : 0.f);
 }
 
+// (f - mu) inv weight + bias, for a vector of the row and for one element.
+template <typename ROW>
+__device__ __forceinline__ void finish_vector(const LnForward& p, const ROW& row, int j, float* f, float mu, float inv) {
+#pragma unroll
+  for (int e = 0; e < ROW::kN; ++e) f[e] = (f[e] - mu) * inv;
+  if (p.weight != nullptr) {
+    float w[ROW::kN];
+    row.params(p.weight, p.param_dtype, j, w);
+#pragma unroll
+    for (int e = 0; e < ROW::kN; ++e) f[e] *= w[e];
+  }
+  if (p.bias != nullptr) {
+    float b[ROW::kN];
+    row.params(p.bias, p.param_dtype, j, b);
+#pragma unroll
+    for (int e = 0; e < ROW::kN; ++e) f[e] += b[e];
+  }
+}
+__device__ __forceinline__ float finish_one(const LnForward& p, int c, float f, float mu, float inv) {
+  f = (f - mu) * inv;
+  if (p.weight != nullptr) f *= load_elem(p.weight, p.param_dtype, c);
+  if (p.bias != nullptr) f += load_elem(p.bias, p.param_dtype, c);
+  return f;
+}
+
 // Forward with the row in registers, VPT vectors a thread: a warp (WARP) takes ROWS
 // rows, or a CTA one.  A row is read once; the mean and then the sum of squares about
 // it are taken from the registers.  48 registers a thread let 40 warps have their rows
@@ -129,29 +154,11 @@ __global__ void __maxnreg__(VPT == 8 ? 64 : 48) ln_fwd_kernel(const LnForward p)
       if (j < row.vectors) {
         float f[V::kN];
         V::unpack(v[i][k], f);
-#pragma unroll
-        for (int e = 0; e < V::kN; ++e) f[e] = (f[e] - mu) * inv;
-        if (p.weight != nullptr) {
-          float w[V::kN];
-          row.params(p.weight, p.param_dtype, j, w);
-#pragma unroll
-          for (int e = 0; e < V::kN; ++e) f[e] *= w[e];
-        }
-        if (p.bias != nullptr) {
-          float b[V::kN];
-          row.params(p.bias, p.param_dtype, j, b);
-#pragma unroll
-          for (int e = 0; e < V::kN; ++e) f[e] += b[e];
-        }
+        finish_vector(p, row, j, f, mu, inv);
         row.store(y, j, V::pack(f));
       }
     }
-    if (c >= 0) {
-      float o = (extra[i] - mu) * inv;
-      if (p.weight != nullptr) o *= load_elem(p.weight, p.param_dtype, c);
-      if (p.bias != nullptr) o += load_elem(p.bias, p.param_dtype, c);
-      y[c] = from_float<T>(o);
-    }
+    if (c >= 0) y[c] = from_float<T>(finish_one(p, c, extra[i], mu, inv));
     if (t == 0) {
       if (p.mean != nullptr) p.mean[n] = mu;
       if (p.rstd != nullptr) p.rstd[n] = inv;
