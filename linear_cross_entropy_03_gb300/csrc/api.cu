@@ -19,7 +19,7 @@ int64_t ce_vector_elems(int dtype, bool vector_path);
 
 namespace {
 
-constexpr int kVersion = 100;  // 0.1.0
+constexpr int kVersion = 200;  // 0.2.0
 constexpr size_t kAlign = 256;
 // Default chunk: the largest multiple of 256 tokens whose bf16 logits fit in
 // 2 GiB (8192 tokens at V = 128256, 4096 at V = 256000).  Larger chunks halve

@@ -118,7 +118,9 @@ __global__ void __maxnreg__((VPT > 2 || (sizeof(T) == 2 && (BIAS || SHIFTED)) ? 
   const auto has = [&](int k) { return FULL || t + k * group < row.vectors; };  // whether there is a k-th vector
   const int arrays = p.grad_sum != nullptr ? 3 : 2;
   const uint32_t vector_bytes = blockDim.x * 16, array_bytes = vector_bytes * VPT, stage_bytes = array_bytes * arrays;
-  const uint32_t mine = smem_addr(ring) + threadIdx.x * 16;
+  // shared memory: the weights where they lie there, then the ring
+  const uint32_t my_weights = smem_addr(ring) + threadIdx.x * 16;
+  const uint32_t mine = my_weights + (kShareWeights ? 2 * array_bytes : 0);
   // this thread's first vector of the next row to fetch, in each array
   const int64_t lane_offset = row.column(t);
   const T* next_g = static_cast<const T*>(p.grad_y) + n0 * p.ld_grad_y + lane_offset;
@@ -147,12 +149,11 @@ __global__ void __maxnreg__((VPT > 2 || (sizeof(T) == 2 && (BIAS || SHIFTED)) ? 
   for (int k = 0; k < VPT; ++k)
 #pragma unroll
     for (int i = 0; i < kP; ++i) sw[k][i] = sb[k][i] = pair(0.f);
-  // kept with one or two vectors a thread, in registers or (kWeightsShared) in this
-  // thread's part of shared memory behind the ring; with more read again
+  // kept with one or two vectors a thread, in registers or (kShareWeights) in this
+  // thread's part of shared memory; with more read again
   constexpr bool kKeep = VPT <= 2;
   // whether u and xhat are formed again for grad_x instead of being kept over the barrier
   constexpr bool kAgain = !kKeep || (kShareWeights && BIAS && SHIFTED);
-  const uint32_t my_weights = mine + DEPTH * stage_bytes;
   const auto weights = [&](int k) {
     float f[kN];
     if (p.weight != nullptr && has(k)) {
@@ -474,8 +475,16 @@ cudaError_t reduce_columns(const LnBackward& p, float* grad_weight, float* grad_
   return e;
 }
 
+// Ranges of rows in the form by elements: with its strips of 64 columns, eight CTAs for each SM.
+constexpr int kMostSms = 256;  // of any GPU
+int64_t any_parts(int64_t H, int sms) {
+  return std::min<int64_t>(div_up(int64_t(8) * std::min(sms, kMostSms), div_up(H, 64)), kMaxParts);
+}
+
 // Most vectors of a row that the vector form takes (four for each thread).
 constexpr int64_t kMaxRowVectors = 2048;
+
+constexpr size_t kSharedByDefault = 48 * 1024 - 8192;  // with the kernel's own arrays, of a CTA that asks for no more
 
 template <typename T, bool RMS, bool BIAS, int VPT, bool SHIFTED, bool FULL>
 cudaError_t launch_rows(LnBackward& p, int group, cudaStream_t s) {
@@ -484,8 +493,6 @@ cudaError_t launch_rows(LnBackward& p, int group, cudaStream_t s) {
   constexpr int kDepth = VPT > 2 ? 2 : kShareWeights ? 3 : 4;  // what 227 KB hold
   const int groups = group == 32 ? kBwdThreads / 32 : std::min(kBwdThreads / group, kMaxBarriers);
   const int threads = group * groups;
-  const int slots = (p.grad_sum != nullptr ? 3 : 2) * kDepth + (kShareWeights ? 2 : 0);
-  const size_t smem = static_cast<size_t>(threads) * VPT * 16 * slots;
   int64_t grid = std::min<int64_t>({div_up(p.N, groups), device_sm_count(), kMaxParts});
   if (SHIFTED) {  // groups a multiple of kN
     int64_t unit = kN;
@@ -494,8 +501,16 @@ cudaError_t launch_rows(LnBackward& p, int group, cudaStream_t s) {
   }
   p.parts = static_cast<int>(grid);
   const auto kernel = ln_bwd_kernel<T, RMS, BIAS, VPT, kDepth, SHIFTED, FULL>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-  if (e != cudaSuccess) return e;
+  // as many stages of the ring as a group has rows, and room for the groups' sums at the end
+  const int64_t stages = std::min<int64_t>(kDepth, div_up(p.N, grid * groups));
+  const int64_t slots = (p.grad_sum != nullptr ? 3 : 2) * stages + (kShareWeights ? 2 : 0);
+  const int64_t sums = groups > 1 ? groups * p.H * 4 * 2 : 0;
+  const size_t smem = static_cast<size_t>(std::max<int64_t>(int64_t(threads) * VPT * 16 * slots, sums));
+  if (smem > kSharedByDefault) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+  }
   kernel<<<static_cast<unsigned int>(grid), threads, smem, s>>>(p, group, groups);
   return cudaGetLastError();
 }
@@ -545,7 +560,7 @@ cudaError_t backward(LnBackward p, float* grad_weight, float* grad_bias, int acc
       if (e != cudaSuccess) return e;
     }
     const int64_t strips = div_up(p.H, 64);
-    p.parts = static_cast<int>(std::min<int64_t>({div_up(int64_t(8) * sms, strips), div_up(p.N, 4), kMaxParts}));
+    p.parts = static_cast<int>(std::min<int64_t>(any_parts(p.H, sms), div_up(p.N, 4)));
     prof_begin(s, FLCE_KERNEL_LN_BWD);
     ln_bwd_cols_any_kernel<T, RMS><<<dim3(static_cast<unsigned>(strips), p.parts), kAnyThreads, 0, s>>>(p);
     e = cudaGetLastError();
@@ -561,8 +576,10 @@ struct LnLayout {
 
 LnLayout ln_layout(int64_t N, int64_t H) {
   LnLayout L;
-  // a partial row of sums for each CTA: at most one a row, rounded up to eight (the places in a vector where rows start)
-  const int64_t parts = std::min<int64_t>(div_up(std::max<int64_t>(N, 1), 8) * 8, kMaxParts);
+  // a partial row of sums for each CTA: at most one a row, rounded up to eight (the places in a vector where rows
+  // start); rows too long for vectors take ranges of rows by strips of columns, few of them
+  const int64_t most = H / 8 <= kMaxRowVectors ? kMaxParts : any_parts(H, kMostSms);
+  const int64_t parts = std::min<int64_t>(div_up(std::max<int64_t>(N, 1), 8) * 8, most);
   const size_t part = align_up(static_cast<size_t>(parts) * part_ld(H) * 4, 256);
   L.row_terms = 0;
   L.part_w = align_up(static_cast<size_t>(N) * sizeof(float2), 256);

@@ -230,6 +230,15 @@ def test_repeated_row():
 
 @pytest.mark.parametrize("h", [768, 777, 4096])
 def test_outputs_in_the_inputs_place(h):
+    check_in_place(h)
+
+
+@pytest.mark.parametrize("h", [33, 20001, 66001])
+def test_outputs_in_the_inputs_place_by_elements(h):
+    check_in_place(h)
+
+
+def check_in_place(h):
     x, r, w = rows(50, h, "bf16", 1), rows(50, h, "bf16", 2), vector(h, "bf16", 3, 1.0)
     want = flce.layer_norm(x, w, residual=r)
     a, b = x.clone(), r.clone()
