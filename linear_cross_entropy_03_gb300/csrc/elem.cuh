@@ -121,7 +121,8 @@ inline bool float_dtype(int dtype) {
   return dtype == FLCE_DTYPE_BF16 || dtype == FLCE_DTYPE_FP16 || dtype == FLCE_DTYPE_FP32;
 }
 inline size_t elem_size(int dtype) { return dtype == FLCE_DTYPE_FP32 ? 4 : 2; }
-inline bool aligned_to(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }  // a: a power of 2
+// Whether p is a multiple of `a`, a power of 2.
+inline bool aligned_to(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 inline int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 

@@ -34,7 +34,8 @@ __device__ __forceinline__ float row_sum(float v, float* scratch) {
 
 // (f - mu) inv weight + bias, for a vector of the row and for one element.
 template <typename ROW>
-__device__ __forceinline__ void finish_vector(const LnForward& p, const ROW& row, int j, float* f, float mu, float inv) {
+__device__ __forceinline__ void finish_vector(const LnForward& p, const ROW& row, int j, float* f, float mu,
+                                              float inv) {
 #pragma unroll
   for (int e = 0; e < ROW::kN; ++e) f[e] = (f[e] - mu) * inv;
   if (p.weight != nullptr) {
@@ -59,9 +60,11 @@ __device__ __forceinline__ float finish_one(const LnForward& p, int c, float f, 
 
 // Forward with the row in registers, VPT vectors a thread: a warp (WARP) takes ROWS
 // rows, or a CTA one.  A row is read once; the mean and then the sum of squares about
-// it are taken from the registers.  48 registers a thread let 40 warps have their rows
-// under way on an SM: bf16 [16384, 4096] without residual took 51.3 us with 64, 48.2
-// so, and 55.3 with 32, where some are spilled.
+// it are taken from the registers.  Memory bounds it: bf16 [16384, 4096] with residual
+// takes 82 us (6.6 TB/s), fp32 [8191, 2048] 25 us (5.4 TB/s; a plain copy 27 us).  48
+// registers a thread let 40 warps have their rows under way on an SM: bf16 [16384,
+// 4096] without residual took 51.3 us with 64, 48.2 so, and 55.3 with 32, where some
+// are spilled.
 template <typename T, bool RMS, int VPT, int ROWS, bool WARP, bool SHIFTED>
 __global__ void __maxnreg__(VPT == 8 ? 64 : 48) ln_fwd_kernel(const LnForward p) {
   using V = Vec<T>;
@@ -219,7 +222,8 @@ constexpr int64_t kMaxRowVectors = 8192;
 template <typename T, bool RMS, bool SHIFTED>
 void forward_rows(const LnForward& p, int64_t vectors, cudaStream_t s) {
   constexpr int kWarps = 4;
-  // several short rows to a warp once every SM has all the warps it holds
+  // several short rows to a warp once every SM has all the warps it holds (bf16 [65536, 256] 18.5 -> 17.5 us; below,
+  // the rows are needed to fill the SMs)
   const int rows = p.N >= int64_t(64) * device_sm_count() ? (vectors <= 32 ? 4 : vectors <= 64 ? 2 : 1) : 1;
   const unsigned int grid = static_cast<unsigned int>(div_up(p.N, kWarps * rows));
   if (vectors <= 32 && rows == 4) {
@@ -286,7 +290,8 @@ flce_status_t ln_fwd(int kind, int dtype, const void* x, int64_t ld_x, const voi
       overlap(y, ld_y, sum, ld_sum, N, H, esz))
     return FLCE_ERR_INVALID_ARG;
   if (N == 0) return FLCE_OK;
-  LnForward p = {x, residual, weight, bias, y, sum, mean, rstd, ld_x, ld_residual, ld_y, ld_sum, N, H, eps, param_dtype};
+  LnForward p = {x,    residual,    weight, bias,   y, sum, mean, rstd,
+                 ld_x, ld_residual, ld_y,   ld_sum, N, H,   eps,  param_dtype};
   return LN_BY_TYPE(forward, p, reinterpret_cast<cudaStream_t>(stream_)) == cudaSuccess ? FLCE_OK : FLCE_ERR_CUDA;
 }
 
