@@ -107,15 +107,6 @@ def _native():
     return _binding
 
 
-def _floats(t, n, where):
-    import torch
-    if t.dtype is not torch.float32 or t.numel() != n or not t.is_contiguous():
-        raise FlceError(1, f"{where}: a contiguous fp32 tensor of {n} elements is wanted")
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
-        raise FlceError(1, f"{where}: on {t.device}, not on the current GPU")
-    return t
-
-
 def _on(stream):
     """Makes `stream` torch's current one for a call, so that what it allocates is that stream's."""
     import torch
@@ -257,9 +248,12 @@ class AdamW:
                               decay, scale)
         self._numbers = AdamWNumbers(beta1=betas[0], beta2=betas[1], eps=eps, stochastic=int(seed is not None),
                                      seed=seed or 0)
-        self._addresses = tuple(map(ctypes.addressof, (self._table, self._numel, self._numbers)))
+        self._addresses = (ctypes.addressof(self._table), ctypes.addressof(self._numel), count,
+                           ctypes.addressof(self._numbers))
         self._steps = step
         self._step_dev = torch.full((1,), step, dtype=torch.int64, device="cuda") if capturable else None
+        if capturable:
+            self._numbers.step_dev = self._step_dev.data_ptr()
 
     @property
     def steps(self) -> int:
@@ -286,25 +280,17 @@ class AdamW:
         if stream is not None:
             with _on(stream):
                 return self.step(grads, lr=lr, grad_scale=grad_scale, skip_nonfinite=skip_nonfinite)
-        k = self._numbers
         lr = self.lr if lr is None else lr
-        k.lr, k.lr_dev = (0.0, _floats(lr, 1, "AdamW.step: lr").data_ptr()) if isinstance(lr, torch.Tensor) else (lr, None)
-        factor = None
-        if isinstance(grad_scale, torch.Tensor):
-            factor = _floats(grad_scale, 1, "AdamW.step: grad_scale")
-        elif skip_nonfinite and grad_scale is not None and not math.isfinite(grad_scale):
+        if skip_nonfinite and grad_scale is not None and not isinstance(grad_scale, torch.Tensor) and \
+                not math.isfinite(grad_scale):
             return
-        k.grad_scale = 1.0 if grad_scale is None or factor is not None else grad_scale
-        k.grad_scale_dev = _ptr(factor)
-        k.skip_nonfinite = skip_nonfinite
-        k.step = self._steps + 1
         if self._step_dev is not None:
             # counted on the device, and not at all where the step is skipped; taken back if the call is refused
-            one = torch.isfinite(factor).view(1) if skip_nonfinite and factor is not None else 1
+            on_device = skip_nonfinite and isinstance(grad_scale, torch.Tensor)
+            one = torch.isfinite(grad_scale).reshape(-1)[:1].to(torch.int64) if on_device else 1
             self._step_dev.add_(one)
-            k.step_dev = self._step_dev.data_ptr()
         try:
-            _native().adamw(self._addresses[0], self._addresses[1], len(self.params), self._addresses[2], grads)
+            _native().adamw(*self._addresses, grads, lr, grad_scale, skip_nonfinite, self._steps + 1)
         except Exception:
             if self._step_dev is not None:
                 self._step_dev.sub_(one)

@@ -355,16 +355,40 @@ PyObject* adamw_table(PyObject*, PyObject* const* a, Py_ssize_t count) {
   END_HANDLE_TH_ERRORS
 }
 
-// adamw(table, sizes, count, numbers, grads): fills the gradients into the table of
-// flce_adamw_tensor_t at address `table` (an element count of 0 where there is none)
-// and takes the step with the flce_adamw_t at `numbers`.
+// A number, or a device fp32 element whose address goes to *at.
+bool number_of(PyObject* o, const char* where, int* device, double* value, const float** at) {
+  *at = nullptr;
+  if (!THPVariable_Check(o)) {
+    *value = PyFloat_AsDouble(o);
+    return !PyErr_Occurred();
+  }
+  const at::Tensor* t;
+  if (!tensor_of(o, where, false, &t, device) || !floats_of(*t, 1, where)) return false;
+  *value = 0;
+  *at = t->data_ptr<float>();
+  return true;
+}
+
+// adamw(table, sizes, count, numbers, grads, lr, grad_scale, skip_nonfinite, step): fills the gradients into the table
+// of flce_adamw_tensor_t at address `table` (an element count of 0 where there is none) and the step's numbers into the
+// flce_adamw_t at `numbers`, and takes the step.
 PyObject* adamw(PyObject*, PyObject* const* a, Py_ssize_t count) {
   HANDLE_TH_ERRORS
-  if (count != 5) return fail(FLCE_ERR_INVALID_ARG, "AdamW.step: arguments");
+  if (count != 9) return fail(FLCE_ERR_INVALID_ARG, "AdamW.step: arguments");
   auto* table = static_cast<flce_adamw_tensor_t*>(PyLong_AsVoidPtr(a[0]));
   const auto* sizes = static_cast<const int64_t*>(PyLong_AsVoidPtr(a[1]));
   const Py_ssize_t tensors = PyLong_AsSsize_t(a[2]);
-  const auto* numbers = static_cast<const flce_adamw_t*>(PyLong_AsVoidPtr(a[3]));
+  auto* numbers = static_cast<flce_adamw_t*>(PyLong_AsVoidPtr(a[3]));
+  if (PyErr_Occurred()) return nullptr;
+  int on = -1;
+  double factor = 1;
+  if (!number_of(a[5], "AdamW.step: lr", &on, &numbers->lr, &numbers->lr_dev)) return nullptr;
+  numbers->grad_scale_dev = nullptr;
+  if (a[6] != Py_None && !number_of(a[6], "AdamW.step: grad_scale", &on, &factor, &numbers->grad_scale_dev))
+    return nullptr;
+  numbers->grad_scale = static_cast<float>(factor);
+  numbers->skip_nonfinite = flag(a[7]);
+  numbers->step = PyLong_AsLongLong(a[8]);
   if (PyErr_Occurred()) return nullptr;
   Py_ssize_t seen = 0;
   const bool ok = for_each(a[4], "AdamW.step", [&](Py_ssize_t i, const at::Tensor* t) {

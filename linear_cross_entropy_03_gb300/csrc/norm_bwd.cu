@@ -6,6 +6,7 @@
 // residual stream), with about fifteen operations on it: memory bandwidth bounds it.
 #include <math.h>
 
+#include "arrival.cuh"
 #include "norm.cuh"
 
 namespace flce {
@@ -27,6 +28,9 @@ struct LnBackward {
   float2* row_terms;   // [N]: mean(u) * rstd, mean(u * xhat) * rstd
   float *part_w, *part_b;  // [parts][part_ld(H)]
   int parts;
+  float *grad_weight, *grad_bias;
+  int accumulate;
+  unsigned long long *word, tag;  // of a launch whose last CTA adds up the partial rows (else null)
 };
 
 // ------------------------------------------------------- rows by 16-byte vectors
@@ -95,6 +99,26 @@ __device__ __forceinline__ float2 warp_sum2(float2 v) {
   return upper ? make_float2(other, mine) : make_float2(mine, other);
 }
 
+// The launch's last CTA adds up the partial rows.
+__device__ __forceinline__ void add_up_here(const LnBackward& p) {
+  __shared__ bool last;
+  __syncthreads();
+  if (threadIdx.x == 0) last = arrives_last(p.word, p.tag, gridDim.x);
+  __syncthreads();
+  if (!last) return;
+  for (int which = 0; which < 2; ++which) {
+    const float* const part = which == 0 ? p.part_w : p.part_b;
+    float* const out = which == 0 ? p.grad_weight : p.grad_bias;
+    if (out == nullptr) continue;
+    for (int c = threadIdx.x; c < p.H; c += blockDim.x) {
+      float a = 0.f;
+#pragma unroll 8
+      for (unsigned int k = 0; k < gridDim.x; ++k) a += __ldcg(part + k * part_ld(p.H) + c);
+      out[c] = p.accumulate ? out[c] + a : a;
+    }
+  }
+}
+
 // grad_x and column sums, with
 //   u = grad_y weight,  grad_x = rstd (u - mean(u) - xhat mean(u xhat)) + grad_sum,
 // the means over a row, and the columns' sums of grad_y xhat and grad_y over the rows.
@@ -109,7 +133,9 @@ __device__ __forceinline__ float2 warp_sum2(float2 v) {
 // another thread but the two sums over the row.
 //
 // FULL: every thread has all of its vectors (the usual widths), so nothing asks.
-template <typename T, bool RMS, bool BIAS, int VPT, int DEPTH, bool SHIFTED, bool FULL>
+// LAST: for few rows, the launch's last CTA adds up the CTAs' sums (kernels of their
+// own: with that code in it the rows' loop took 8 % longer).
+template <typename T, bool RMS, bool BIAS, int VPT, int DEPTH, bool SHIFTED, bool FULL, bool LAST>
 __global__ void __maxnreg__((VPT > 2 || (sizeof(T) == 2 && (BIAS || SHIFTED)) ? 128 : 112))
     ln_bwd_kernel(const LnBackward p, int group, int groups) {
   constexpr bool kShareWeights = share_weights<T, VPT>(BIAS, SHIFTED, FULL);
@@ -351,7 +377,10 @@ __global__ void __maxnreg__((VPT > 2 || (sizeof(T) == 2 && (BIAS || SHIFTED)) ? 
     if (part_w != nullptr) to_w[c_extra] = sw_extra;
     if (part_b != nullptr) to_b[c_extra] = sb_extra;
   }
-  if (groups == 1) return;
+  if (groups == 1) {
+    if (LAST) add_up_here(p);
+    return;
+  }
   __syncthreads();
   const float* const sums = reinterpret_cast<const float*>(ring);
   for (int c = threadIdx.x; c < row.length; c += blockDim.x) {
@@ -366,6 +395,7 @@ __global__ void __maxnreg__((VPT > 2 || (sizeof(T) == 2 && (BIAS || SHIFTED)) ? 
       part_b[c] = a;
     }
   }
+  if (LAST) add_up_here(p);
 }
 
 // ------------------------------------------------------- any layout, by elements
@@ -472,15 +502,15 @@ __global__ void __launch_bounds__(kReduceThreads)
 
 // ------------------------------------------------------------------ launches
 
-cudaError_t reduce_columns(const LnBackward& p, float* grad_weight, float* grad_bias, int accumulate,
-                           cudaStream_t s) {
-  if (grad_weight == nullptr && grad_bias == nullptr) return cudaSuccess;
+cudaError_t reduce_columns(const LnBackward& p, cudaStream_t s) {
+  float *const grad_weight = p.grad_weight, *const grad_bias = p.grad_bias;
+  if ((grad_weight == nullptr && grad_bias == nullptr) || p.word != nullptr) return cudaSuccess;
   prof_begin(s, FLCE_KERNEL_LN_REDUCE);
   const cudaError_t e =
       launch_after(ln_reduce_kernel,
                    dim3(static_cast<unsigned>(div_up(p.H, 32)), grad_weight != nullptr && grad_bias != nullptr ? 2 : 1),
                    dim3(kReduceThreads), s, static_cast<const float*>(p.part_w), static_cast<const float*>(p.part_b),
-                   p.parts, part_ld(p.H), p.H, grad_weight, grad_bias, accumulate);
+                   p.parts, part_ld(p.H), p.H, grad_weight, grad_bias, p.accumulate);
   prof_end(s);
   return e;
 }
@@ -494,43 +524,64 @@ int64_t any_parts(int64_t H, int sms) {
 // Most vectors of a row that the vector form takes (four for each thread).
 constexpr int64_t kMaxRowVectors = 2048;
 
+// Most CTAs, and partial sums (1024 times as many), that a launch's last CTA adds up
+// itself: [256, 128] in fp32 takes 6.2 us with a kernel for that and 5 so.
+constexpr int64_t kMostAddedHere = 32;
 constexpr size_t kSharedByDefault = 48 * 1024 - 8192;  // with the kernel's own arrays, of a CTA that asks for no more
 
-template <typename T, bool RMS, bool BIAS, int VPT, bool SHIFTED, bool FULL>
-cudaError_t launch_rows(LnBackward& p, int group, cudaStream_t s) {
+// A launch's shape: `group` threads a row, `groups` rows a CTA, `grid` CTAs.
+struct Shape {
+  int group, groups;
+  int64_t grid;
+};
+
+template <typename T>
+Shape shape_of(const LnBackward& p, int64_t vectors, int vpt, bool shifted) {
   constexpr int kN = Vec<T>::kN;
+  Shape r;
+  r.group = static_cast<int>(div_up(vectors, 32 * vpt) * 32);
+  r.groups = r.group == 32 ? kBwdThreads / 32 : std::min(kBwdThreads / r.group, kMaxBarriers);
+  r.grid = std::min<int64_t>({div_up(p.N, r.groups), device_sm_count(), kMaxParts});
+  if (shifted) {  // groups a multiple of kN
+    int64_t unit = kN;
+    while (unit > 1 && r.groups * (unit / 2) % kN == 0) unit /= 2;
+    r.grid = std::min<int64_t>(div_up(r.grid, unit), kMaxParts / unit) * unit;
+  }
+  return r;
+}
+
+template <typename T, bool RMS, bool BIAS, int VPT, bool SHIFTED, bool FULL, bool LAST>
+cudaError_t launch_rows(const LnBackward& p, const Shape& shape, cudaStream_t s) {
   constexpr bool kShareWeights = share_weights<T, VPT>(BIAS, SHIFTED, FULL);
   constexpr int kDepth = VPT > 2 ? 2 : kShareWeights ? 3 : 4;  // what 227 KB hold
-  const int groups = group == 32 ? kBwdThreads / 32 : std::min(kBwdThreads / group, kMaxBarriers);
-  const int threads = group * groups;
-  int64_t grid = std::min<int64_t>({div_up(p.N, groups), device_sm_count(), kMaxParts});
-  if (SHIFTED) {  // groups a multiple of kN
-    int64_t unit = kN;
-    while (unit > 1 && groups * (unit / 2) % kN == 0) unit /= 2;
-    grid = std::min<int64_t>(div_up(grid, unit), kMaxParts / unit) * unit;
-  }
-  p.parts = static_cast<int>(grid);
-  const auto kernel = ln_bwd_kernel<T, RMS, BIAS, VPT, kDepth, SHIFTED, FULL>;
+  const int threads = shape.group * shape.groups;
+  const auto kernel = ln_bwd_kernel<T, RMS, BIAS, VPT, kDepth, SHIFTED, FULL, LAST>;
   // as many stages of the ring as a group has rows, and room for the groups' sums at the end
-  const int64_t stages = std::min<int64_t>(kDepth, div_up(p.N, grid * groups));
+  const int64_t stages = std::min<int64_t>(kDepth, div_up(p.N, shape.grid * shape.groups));
   const int64_t slots = (p.grad_sum != nullptr ? 3 : 2) * stages + (kShareWeights ? 2 : 0);
-  const int64_t sums = groups > 1 ? groups * p.H * 4 * 2 : 0;
+  const int64_t sums = shape.groups > 1 ? shape.groups * p.H * 4 * 2 : 0;
   const size_t smem = static_cast<size_t>(std::max<int64_t>(int64_t(threads) * VPT * 16 * slots, sums));
   if (smem > kSharedByDefault) {
     const cudaError_t e =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
   }
-  kernel<<<static_cast<unsigned int>(grid), threads, smem, s>>>(p, group, groups);
+  kernel<<<static_cast<unsigned int>(shape.grid), threads, smem, s>>>(p, shape.group, shape.groups);
   return cudaGetLastError();
 }
 
 template <typename T, bool RMS, bool BIAS, int VPT, bool SHIFTED>
 cudaError_t backward_rows(LnBackward& p, int64_t vectors, cudaStream_t s) {
-  const int group = static_cast<int>(div_up(vectors, 32 * VPT) * 32);
-  return !SHIFTED && vectors == static_cast<int64_t>(group) * VPT
-             ? launch_rows<T, RMS, BIAS, VPT, SHIFTED, !SHIFTED>(p, group, s)
-             : launch_rows<T, RMS, BIAS, VPT, SHIFTED, false>(p, group, s);
+  const Shape shape = shape_of<T>(p, vectors, VPT, SHIFTED);
+  p.parts = static_cast<int>(shape.grid);
+  if constexpr (VPT <= 2) {
+    if (p.word != nullptr && shape.grid <= kMostAddedHere && shape.grid * p.H <= kMostAddedHere * 1024)
+      return launch_rows<T, RMS, true, VPT, SHIFTED, false, true>(p, shape, s);
+  }
+  p.word = nullptr;
+  return !SHIFTED && vectors == static_cast<int64_t>(shape.group) * VPT
+             ? launch_rows<T, RMS, BIAS, VPT, SHIFTED, !SHIFTED, false>(p, shape, s)
+             : launch_rows<T, RMS, BIAS, VPT, SHIFTED, false, false>(p, shape, s);
 }
 
 template <typename T, bool RMS, bool BIAS, bool SHIFTED>
@@ -541,8 +592,9 @@ cudaError_t backward_rows(LnBackward& p, int64_t vectors, cudaStream_t s) {
 }
 
 template <typename T, bool RMS>
-cudaError_t backward(LnBackward p, float* grad_weight, float* grad_bias, int accumulate, cudaStream_t s) {
+cudaError_t backward(LnBackward p, cudaStream_t s) {
   p.parts = 0;
+  if (p.N == 0) p.word = nullptr;
   const Fit fit = fit_of<T>(p.N, p.H, p.weight, nullptr, p.param_dtype, Matrix{p.x, p.ld_x},
                             Matrix{p.grad_y, p.ld_grad_y}, Matrix{p.grad_sum, p.ld_grad_sum},
                             Matrix{p.grad_x, p.ld_grad_x});
@@ -560,6 +612,7 @@ cudaError_t backward(LnBackward p, float* grad_weight, float* grad_bias, int acc
     prof_end(s);
     if (e != cudaSuccess) return e;
   } else if (p.N > 0) {
+    p.word = nullptr;
     const int sms = device_sm_count();
     if (p.grad_x != nullptr) {
       prof_begin(s, FLCE_KERNEL_LN_BWD);
@@ -577,11 +630,11 @@ cudaError_t backward(LnBackward p, float* grad_weight, float* grad_bias, int acc
     prof_end(s);
     if (e != cudaSuccess) return e;
   }
-  return reduce_columns(p, grad_weight, grad_bias, accumulate, s);
+  return reduce_columns(p, s);
 }
 
 struct LnLayout {
-  size_t row_terms, part_w, part_b, total;
+  size_t row_terms, part_w, part_b, word, total;
 };
 
 LnLayout ln_layout(int64_t N, int64_t H) {
@@ -594,7 +647,8 @@ LnLayout ln_layout(int64_t N, int64_t H) {
   L.row_terms = 0;
   L.part_w = align_up(static_cast<size_t>(N) * sizeof(float2), 256);
   L.part_b = L.part_w + part;
-  L.total = L.part_b + part;
+  L.word = L.part_b + part;
+  L.total = L.word + 256;
   return L;
 }
 
@@ -634,14 +688,31 @@ flce_status_t ln_bwd(int kind, int dtype, const void* grad_y, int64_t ld_grad_y,
   const LnLayout L = ln_layout(N, H);
   if (workspace == nullptr || !aligned_to(workspace, 256) || workspace_bytes < L.total) return FLCE_ERR_WORKSPACE;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  LnBackward p = {grad_y, x, weight, grad_sum, mean, rstd, grad_x, ld_grad_y, ld_x, ld_grad_sum, ld_grad_x, N, H,
-                  param_dtype, reinterpret_cast<float2*>(ws + L.row_terms),
+  const bool sums = grad_weight != nullptr || grad_bias != nullptr;
+  LnBackward p = {grad_y,
+                  x,
+                  weight,
+                  grad_sum,
+                  mean,
+                  rstd,
+                  grad_x,
+                  ld_grad_y,
+                  ld_x,
+                  ld_grad_sum,
+                  ld_grad_x,
+                  N,
+                  H,
+                  param_dtype,
+                  reinterpret_cast<float2*>(ws + L.row_terms),
                   grad_weight != nullptr ? reinterpret_cast<float*>(ws + L.part_w) : nullptr,
-                  grad_bias != nullptr ? reinterpret_cast<float*>(ws + L.part_b) : nullptr, 0};
-  return LN_BY_TYPE(backward, p, grad_weight, grad_bias, accumulate, reinterpret_cast<cudaStream_t>(stream_)) ==
-                 cudaSuccess
-             ? FLCE_OK
-             : FLCE_ERR_CUDA;
+                  grad_bias != nullptr ? reinterpret_cast<float*>(ws + L.part_b) : nullptr,
+                  0,
+                  grad_weight,
+                  grad_bias,
+                  accumulate,
+                  sums ? reinterpret_cast<unsigned long long*>(ws + L.word) : nullptr,
+                  next_arrival_tag()};
+  return LN_BY_TYPE(backward, p, reinterpret_cast<cudaStream_t>(stream_)) == cudaSuccess ? FLCE_OK : FLCE_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -10,6 +10,7 @@
 
 #include <algorithm>
 
+#include "arrival.cuh"
 #include "elem.cuh"
 #include "ptx.cuh"
 
@@ -51,8 +52,45 @@ struct NormArgs {
   NormEntry entry[MAX];
   int count;
   unsigned int chunks;
-  float* part;  // [gridDim.x]
+  float* part;  // [gridDim.x], this launch's
+  // LAST: what to make of the sums
+  unsigned long long *word, tag;
+  float grad_scale, max_norm, eps;
+  float* out;
 };
+
+// The norm and the factor from all partial sums, added in a fixed order, by a CTA of
+// kThreads.
+__device__ __forceinline__ void finish_norm(const float* part, int parts, float grad_scale, float max_norm, float eps,
+                                            float* out, float* scratch) {
+  float sum = 0.f;
+#pragma unroll 3
+  for (int k = threadIdx.x; k < parts; k += kThreads) sum += __ldcg(part + k);
+  sum = warp_sum(sum);
+  __syncthreads();  // the scratch of an earlier sum has been read
+  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < kThreads / 32; ++k) sum += scratch[k];
+    const float norm = sqrtf(sum) * fabsf(grad_scale);
+    out[0] = norm;
+    out[1] = isfinite(norm) ? grad_scale * fminf(1.f, max_norm / (norm + eps)) : __int_as_float(0x7FFFFFFF);
+  }
+}
+
+__global__ void __launch_bounds__(kThreads)
+    grad_norm_finish_kernel(const float* part, int parts, float grad_scale, float max_norm, float eps, float* out) {
+  __shared__ float scratch[kThreads / 32];
+  grid_dependency_wait();
+  finish_norm(part, parts, grad_scale, max_norm, eps, out, scratch);
+}
+
+// Most CTAs whose sums the last of them adds up itself, which saves the host a launch
+// (a call with 20 tensors 12 -> 9 us); with 608 their arrivals take longer than a second
+// kernel that waits for the first (300 packed tensors 18.1 -> 19.0 us).
+constexpr int kMostAddedHere = 64;
 
 // Squares of the elements in 16 bytes.
 __device__ __forceinline__ float squares(const uint4& r, int dtype) {
@@ -79,7 +117,8 @@ __device__ __forceinline__ float squares(const uint4& r, int dtype) {
 // takes a range of chunks, going from one tensor to the next.  A chunk is 16-byte
 // vectors from the tensor's first 16-byte boundary on; the elements before it, and
 // those after the last vector, go with the first chunk.
-template <int MAX>
+// LAST: the last CTA to finish adds up the sums.
+template <int MAX, bool LAST>
 __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_constant__ NormArgs<MAX> a) {
   grid_dependents_launch();
   __shared__ float scratch[kThreads / 32];
@@ -128,27 +167,11 @@ __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_consta
     for (int k = 0; k < kThreads / 32; ++k) t += scratch[k];
     a.part[blockIdx.x] = t;
   }
-}
-
-// Adds the partial sums in a fixed order and forms the norm and the factor.
-constexpr int kFinishThreads = 256;
-__global__ void __launch_bounds__(kFinishThreads)
-    grad_norm_finish_kernel(const float* part, int parts, float grad_scale, float max_norm, float eps, float* out) {
-  __shared__ float scratch[kFinishThreads / 32];
-  grid_dependency_wait();
-  float sum = 0.f;
-#pragma unroll 3
-  for (int k = threadIdx.x; k < parts; k += kFinishThreads) sum += part[k];
-  sum = warp_sum(sum);
-  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = sum;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    sum = 0.f;
-#pragma unroll
-    for (int k = 0; k < kFinishThreads / 32; ++k) sum += scratch[k];
-    const float norm = sqrtf(sum) * fabsf(grad_scale);
-    out[0] = norm;
-    out[1] = isfinite(norm) ? grad_scale * fminf(1.f, max_norm / (norm + eps)) : __int_as_float(0x7FFFFFFF);
+  if constexpr (LAST) {
+    __shared__ bool last;
+    if (threadIdx.x == 0) last = arrives_last(a.word, a.tag, gridDim.x);
+    __syncthreads();
+    if (last) finish_norm(a.part, gridDim.x, a.grad_scale, a.max_norm, a.eps, a.out, scratch);
   }
 }
 
@@ -568,14 +591,23 @@ __global__ void __launch_bounds__(kThreads8, 8) adamw8_kernel(const __grid_const
 }
 
 template <int MAX>
-cudaError_t launch_norm(const NormEntry* entry, int count, unsigned int chunks, float* part, int grid, cudaStream_t s) {
+cudaError_t launch_norm(const NormEntry* entry, const NormArgs<1>& rest, int grid, cudaStream_t s) {
   NormArgs<MAX> a;
-  std::copy(entry, entry + count, a.entry);
-  a.count = count;
-  a.chunks = chunks;
-  a.part = part;
+  std::copy(entry, entry + rest.count, a.entry);
+  a.count = rest.count;
+  a.chunks = rest.chunks;
+  a.part = rest.part;
+  a.word = rest.word;
+  a.tag = rest.tag;
+  a.grad_scale = rest.grad_scale;
+  a.max_norm = rest.max_norm;
+  a.eps = rest.eps;
+  a.out = rest.out;
   prof_begin(s, FLCE_KERNEL_GRAD_NORM);
-  grad_norm_kernel<MAX><<<grid, kThreads, 0, s>>>(a);
+  if (a.word != nullptr)
+    grad_norm_kernel<MAX, true><<<grid, kThreads, 0, s>>>(a);
+  else
+    grad_norm_kernel<MAX, false><<<grid, kThreads, 0, s>>>(a);
   const cudaError_t e = cudaGetLastError();
   prof_end(s);
   return e;
@@ -605,11 +637,10 @@ constexpr int kAdamEntries = 360, kAdamMore = 128, kAdamMiddle = 40, kAdamFew = 
 static_assert(sizeof(AdamArgs<kAdamEntries>) <= 32764, "kernel parameters");
 static_assert(sizeof(NormArgs<kNormEntries>) <= 32764, "kernel parameters");
 
-cudaError_t launch_norm_any(const NormEntry* entry, int count, unsigned int chunks, float* part, int grid,
-                            cudaStream_t s) {
-  if (count <= kNormFew) return launch_norm<kNormFew>(entry, count, chunks, part, grid, s);
-  if (count <= kNormMiddle) return launch_norm<kNormMiddle>(entry, count, chunks, part, grid, s);
-  return launch_norm<kNormEntries>(entry, count, chunks, part, grid, s);
+cudaError_t launch_norm_any(const NormEntry* entry, const NormArgs<1>& rest, int grid, cudaStream_t s) {
+  if (rest.count <= kNormFew) return launch_norm<kNormFew>(entry, rest, grid, s);
+  if (rest.count <= kNormMiddle) return launch_norm<kNormMiddle>(entry, rest, grid, s);
+  return launch_norm<kNormEntries>(entry, rest, grid, s);
 }
 
 cudaError_t launch_adamw_any(const AdamEntry* entry, int count, unsigned int chunks, const AdamNumbers& num, int bits,
@@ -636,9 +667,11 @@ int common_head(const flce_adamw_tensor_t& t) {
   return t.n > head ? head : -1;
 }
 
-size_t norm_workspace(int64_t count) {
+// The partial sums of every launch, then the word that finds the last CTA.
+size_t norm_parts_bytes(int64_t count) {
   return align_up(static_cast<size_t>(std::max<int64_t>(1, div_up(count, kNormEntries))) * kNormParts * 4, 256);
 }
+size_t norm_workspace(int64_t count) { return norm_parts_bytes(count) + 256; }
 
 flce_status_t check_tensor(const flce_adamw_tensor_t& t) {
   if (t.n < 0 || t.n > kMaxElems) return FLCE_ERR_INVALID_ARG;
@@ -682,29 +715,44 @@ flce_status_t grad_norm(const flce_tensor_t* tensors, int64_t count, float grad_
   if (!aligned_to(out, 4)) return FLCE_ERR_MISALIGNED;
   if (workspace == nullptr || !aligned_to(workspace, 256) || workspace_bytes < norm_workspace(count))
     return FLCE_ERR_WORKSPACE;
-  float* part = static_cast<float*>(workspace);
   const int most = std::min(kNormParts, 4 * device_sm_count());
-  int parts = 0;
   NormEntry entry[kNormEntries];
-  for (int64_t i = 0; i < count;) {
+  NormArgs<1> rest = {};
+  float* const part = static_cast<float*>(workspace);
+  int parts = 0;
+  rest.tag = next_arrival_tag();
+  rest.grad_scale = grad_scale;
+  rest.max_norm = max_norm;
+  rest.eps = eps;
+  rest.out = out;
+  int64_t i = 0;
+  const auto skip_empty = [&] {
+    while (i < count && tensors[i].n == 0) ++i;
+  };
+  skip_empty();
+  do {  // once at least: no tensors have a norm too
     int64_t chunks = 0;
-    int filled = 0;
-    for (; i < count && filled < kNormEntries; ++i) {
-      if (tensors[i].n == 0) continue;
+    rest.count = 0;
+    while (i < count && rest.count < kNormEntries) {
       // at least the vectors from the first boundary on (a chunk too many finds nothing)
       const int64_t more = div_up(tensors[i].n, kNormChunk * static_cast<int64_t>(16 / elem_size(tensors[i].dtype)));
       if (chunks + more > 0x7fffffff) break;
-      entry[filled++] = {tensors[i].data, tensors[i].n, static_cast<unsigned int>(chunks), tensors[i].dtype};
+      entry[rest.count++] = {tensors[i].data, tensors[i].n, static_cast<unsigned int>(chunks), tensors[i].dtype};
       chunks += more;
+      ++i;
+      skip_empty();
     }
-    if (filled == 0) break;
-    const int grid = static_cast<int>(std::min<int64_t>(chunks, most));
-    if (launch_norm_any(entry, filled, static_cast<unsigned int>(chunks), part + parts, grid, s) != cudaSuccess)
-      return FLCE_ERR_CUDA;
+    const int grid = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(chunks, most)));
+    rest.chunks = static_cast<unsigned int>(chunks);
+    rest.part = part + parts;
+    if (parts == 0 && i >= count && grid <= kMostAddedHere)
+      rest.word = reinterpret_cast<unsigned long long*>(static_cast<uint8_t*>(workspace) + norm_parts_bytes(count));
+    if (launch_norm_any(entry, rest, grid, s) != cudaSuccess) return FLCE_ERR_CUDA;
     parts += grid;
-  }
+  } while (i < count);
+  if (rest.word != nullptr) return FLCE_OK;
   prof_begin(s, FLCE_KERNEL_GRAD_NORM);
-  const cudaError_t e = launch_after(grad_norm_finish_kernel, dim3(1), dim3(kFinishThreads), s,
+  const cudaError_t e = launch_after(grad_norm_finish_kernel, dim3(1), dim3(kThreads), s,
                                      static_cast<const float*>(part), parts, grad_scale, max_norm, eps, out);
   prof_end(s);
   return e == cudaSuccess ? FLCE_OK : FLCE_ERR_CUDA;

@@ -374,6 +374,36 @@ def test_on_another_stream_and_in_a_graph():
         assert all(torch.equal(got[k], grads[k]) for k in grads)
 
 
+@pytest.mark.parametrize("n,h", [(1, 4096), (5, 64), (40, 200), (33, 777), (256, 128), (512, 65), (2000, 512), (9, 4098)])
+def test_backward_with_any_workspace_and_in_a_graph(n, h):
+    """What the workspace held does not matter, and a replayed call finds its last CTA again."""
+    x, gy = rows(n, h, "bf16", 1), rows(n, h, "bf16", 2, 1e-2, 0.0)
+    w = vector(h, "bf16", 3, 1.0)
+    out = flce.layer_norm(x, w)
+    stats = dict(mean=out["mean"], rstd=out["rstd"])
+    work = torch.empty(flce.ln_workspace_size(n, h), dtype=torch.uint8, device="cuda")
+    want = None
+    for fill in (0, 0xFF, 0x5A, None):
+        if fill is None:
+            work.random_(0, 256)
+        else:
+            work.fill_(fill)
+        for _ in range(3):
+            got = flce.layer_norm_backward(gy, x, w, **stats, workspace=work)
+            want = want or got
+            assert all(torch.equal(got[k], want[k]) for k in got)
+    check_backward(want, gy, x, w, out["mean"], out["rstd"], None, False, "bf16")
+    sums = torch.full((2, h), 0.25, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        flce.layer_norm_backward(gy, x, w, **stats, workspace=work, grad_weight_out=sums[0], grad_bias_out=sums[1],
+                                 accumulate=True)
+    for k in range(3):
+        sums.fill_(0.25)
+        graph.replay()
+        assert torch.equal(sums[0], want["grad_weight"] + 0.25) and torch.equal(sums[1], want["grad_bias"] + 0.25)
+
+
 def test_refusals():
     x, w = rows(4, 64, "bf16", 1), vector(64, "bf16", 2, 1.0)
     st = torch.ones(4, device="cuda")

@@ -89,6 +89,34 @@ def test_norm_is_the_same_every_run_and_clips_a_large_tensor():
         assert torch.equal(again["norm"], first["norm"]) and torch.equal(again["scale"], first["scale"])
 
 
+@pytest.mark.parametrize("count", [1, 3, 700, 3000])
+def test_norm_with_any_workspace_and_in_a_graph(count):
+    """What the workspace held does not matter, and a replayed call finds its last CTA again."""
+    grads = list(normal(count * 5003, 4).view(count, 5003))
+    want = flce.grad_norm(grads, max_norm=1.0)
+    work = torch.empty(flce.grad_norm_workspace_size(count), dtype=torch.uint8, device="cuda")
+    out = torch.empty(2, device="cuda")
+    for fill in (0, 0xFF, 0x5A, None):
+        if fill is None:
+            work.random_(0, 256)
+        else:
+            work.fill_(fill)
+        for _ in range(3):
+            out.zero_()
+            got = flce.grad_norm(grads, max_norm=1.0, workspace=work, out=out)
+            assert torch.equal(got["norm"], want["norm"]) and torch.equal(got["scale"], want["scale"])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = flce.grad_norm(grads, max_norm=1.0, workspace=work, out=out)
+    for _ in range(4):
+        out.zero_()
+        graph.replay()
+        assert torch.equal(got["norm"], want["norm"])
+    work.fill_(0xFF)
+    graph.replay()
+    assert torch.equal(got["norm"], want["norm"])
+
+
 # ------------------------------------------------------------ AdamW, fp32 moments
 
 class Reference:
@@ -271,6 +299,19 @@ def test_captured_step(moments):
         assert (a - b).abs().max() <= 1e-2 * 4 * (2.0 ** -18 if moments == "fp32" else 0.1)
     if moments == "fp32":
         assert all(torch.equal(a, b) for a, b in zip(opt.exp_avg, other.exp_avg))
+
+
+def test_refused_step_does_not_count():
+    for capturable in (False, True):
+        opt = make([100], capturable=capturable)
+        g, two = normal(100, 1), torch.ones(2, device="cuda")
+        for bad in (dict(grads=[g[:50]]), dict(grads=[g], grad_scale=two), dict(grads=[g], grad_scale=two, skip_nonfinite=True),
+                    dict(grads=[g], lr=two), dict(grads=[g], lr="fast"), dict(grads=[])):
+            with pytest.raises((flce.FlceError, TypeError)):
+                opt.step(**bad)
+        assert opt.steps == 0
+        opt.step([g])
+        assert opt.steps == 1
 
 
 def test_on_another_stream():
