@@ -24,6 +24,14 @@ inline unsigned long long next_arrival_tag() {
   return tag;
 }
 
+// By one thread of the launch as it starts: puts the tag on the word, so that the CTAs
+// that arrive later need one addition each.  Nothing waits for it; if the swap fails, a
+// CTA that has arrived already has put the tag there.
+__device__ __forceinline__ void expect_arrivals(unsigned long long* word, unsigned long long tag) {
+  const unsigned long long now = *reinterpret_cast<volatile unsigned long long*>(word);
+  if (now >> kArrivalBits != tag >> kArrivalBits) atomicCAS(word, now, tag);
+}
+
 // By one thread of each of `ctas` CTAs, once its CTA's results are written: true in the
 // one that arrives last, which then sees all of them (through loads that pass the
 // first-level cache by, such as __ldcg).  The word may hold anything at first.  A CTA

@@ -121,16 +121,23 @@ __device__ __forceinline__ void add_up_here(const LnBackward& p) {
   if (threadIdx.x == 0) last = arrives_last(p.word, p.tag, gridDim.x);
   __syncthreads();
   if (!last) return;
-  for (int which = 0; which < 2; ++which) {
-    const float* const part = which == 0 ? p.part_w : p.part_b;
-    float* const out = which == 0 ? p.grad_weight : p.grad_bias;
+  // four columns of one of the two sums for a thread, most of its loads under way at once
+  const int fours = static_cast<int>(part_ld(p.H) / 4);
+  for (int item = threadIdx.x; item < 2 * fours; item += blockDim.x) {
+    const bool weight = item < fours;
+    float* const out = weight ? p.grad_weight : p.grad_bias;
     if (out == nullptr) continue;
-    for (int c = threadIdx.x; c < p.H; c += blockDim.x) {
-      float a = 0.f;
-#pragma unroll 8
-      for (unsigned int k = 0; k < gridDim.x; ++k) a += __ldcg(part + k * part_ld(p.H) + c);
-      out[c] = p.accumulate ? out[c] + a : a;
+    const int c = (weight ? item : item - fours) * 4;
+    const float* const part = (weight ? p.part_w : p.part_b) + c;
+    float a[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 16
+    for (unsigned int k = 0; k < gridDim.x; ++k) {
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(part + k * part_ld(p.H)));
+      a[0] += v.x, a[1] += v.y, a[2] += v.z, a[3] += v.w;
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (c + i < p.H) out[c + i] = p.accumulate ? out[c + i] + a[i] : a[i];
   }
 }
 
@@ -192,6 +199,7 @@ __global__ void __maxnreg__((VPT > 2 || (sizeof(T) == 2 && (BIAS || SHIFTED)) ? 
     copies_issued();
   }
   grid_dependents_launch();
+  if (LAST && blockIdx.x == 0 && threadIdx.x == 0) expect_arrivals(p.word, p.tag);
 
   Pair sw[VPT][kP], sb[VPT][kP], w[VPT][kP];
 #pragma unroll
@@ -539,9 +547,12 @@ int64_t any_parts(int64_t H, int sms) {
 // Most vectors of a row that the vector form takes (four for each thread).
 constexpr int64_t kMaxRowVectors = 2048;
 
-// Most CTAs, and partial sums (1024 times as many), that a launch's last CTA adds up
-// itself: [256, 128] in fp32 takes 6.2 us with a kernel for that and 5 so.
-constexpr int64_t kMostAddedHere = 32;
+// Most CTAs, and columns, whose sums a launch's last CTA adds up itself, which saves the
+// host a launch where that is what a call waits for: one on [256, 128] in fp32 takes 8.3
+// to 8.9 us so and 11.0 to 12.7 with a second kernel, on bf16 [512, 256] (16 CTAs) 10.2
+// and 11.5 to 13.6; on bf16 [200, 1000] (25 CTAs) it would take 13.3 and takes 11.6.  (On
+// the GPU alone the second kernel is 1.6 us faster.)
+constexpr int64_t kMostAddedHere = 16, kMostColumnsHere = 1024;
 constexpr size_t kSharedByDefault = 48 * 1024 - 8192;  // with the kernel's own arrays, of a CTA that asks for no more
 
 // A launch's shape: `group` threads a row, `groups` rows a CTA, `grid` CTAs.
@@ -590,7 +601,7 @@ cudaError_t backward_rows(LnBackward& p, int64_t vectors, cudaStream_t s) {
   const Shape shape = shape_of<T>(p, vectors, VPT, LANES, SHIFTED);
   p.parts = static_cast<int>(shape.grid);
   if constexpr (VPT <= 2) {
-    if (p.word != nullptr && shape.grid <= kMostAddedHere && shape.grid * p.H <= kMostAddedHere * 1024)
+    if (p.word != nullptr && shape.grid <= kMostAddedHere && p.H <= kMostColumnsHere)
       return launch_rows<T, RMS, true, VPT, LANES, SHIFTED, false, true>(p, shape, s);
   }
   p.word = nullptr;

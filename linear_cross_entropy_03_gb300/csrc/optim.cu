@@ -87,9 +87,10 @@ __global__ void __launch_bounds__(kThreads)
   finish_norm(part, parts, grad_scale, max_norm, eps, out, scratch);
 }
 
-// Most CTAs whose sums the last of them adds up itself, which saves the host a launch
-// (a call with 20 tensors 12 -> 9 us); with 608 their arrivals take longer than a second
-// kernel that waits for the first (300 packed tensors 18.1 -> 19.0 us).
+// Most CTAs whose sums the last of them adds up itself, which saves the host a launch: a
+// call with 20 tensors of 1000 takes 10.5 us so and 13.2 with a second kernel (though the
+// GPU alone 4.0 and 3.0); with 608 CTAs their arrivals take longer than a second kernel
+// that waits for the first (300 packed tensors 19.0 and 18.1 us).
 constexpr int kMostAddedHere = 64;
 
 // Squares of the elements in 16 bytes.
@@ -121,6 +122,7 @@ __device__ __forceinline__ float squares(const uint4& r, int dtype) {
 template <int MAX, bool LAST>
 __global__ void __launch_bounds__(kThreads) grad_norm_kernel(const __grid_constant__ NormArgs<MAX> a) {
   grid_dependents_launch();
+  if (LAST && blockIdx.x == 0 && threadIdx.x == 0) expect_arrivals(a.word, a.tag);
   __shared__ float scratch[kThreads / 32];
   float sum = 0.f;
   const uint64_t all = a.chunks;
