@@ -100,7 +100,8 @@ def _native():
         if not os.path.exists(path):
             raise RuntimeError(f"{path} is missing: build it with `python -c 'import __graft_entry__ as g; g.build()'`")
         loader = importlib.machinery.ExtensionFileLoader("flce_torch", path)
-        module = importlib.util.module_from_spec(importlib.util.spec_from_file_location("flce_torch", path, loader=loader))
+        spec = importlib.util.spec_from_file_location("flce_torch", path, loader=loader)
+        module = importlib.util.module_from_spec(spec)
         loader.exec_module(module)
         module.set_error(FlceError)
         _binding = module
@@ -173,7 +174,8 @@ def grad_norm(grads, *, max_norm=None, grad_scale: float = 1.0, eps: float = 1e-
     if stream is not None:
         with _on(stream):
             return grad_norm(grads, max_norm=max_norm, grad_scale=grad_scale, eps=eps, out=out, workspace=workspace)
-    norm, scale = _native().grad_norm(grads, grad_scale, math.inf if max_norm is None else max_norm, eps, out, workspace)
+    max_norm = math.inf if max_norm is None else max_norm
+    norm, scale = _native().grad_norm(grads, grad_scale, max_norm, eps, out, workspace)
     return {"norm": norm, "scale": scale}
 
 

@@ -144,9 +144,12 @@ PyObject* layer_norm(PyObject*, PyObject* const* a, Py_ssize_t count) {
   if (count != 9) return fail(FLCE_ERR_INVALID_ARG, "layer_norm: arguments");
   int device = -1;
   const at::Tensor *x, *w, *b, *r, *out, *sum_out;
-  if (!tensor_of(a[0], "layer_norm: x", false, &x, &device) || !tensor_of(a[1], "layer_norm: weight", true, &w, &device) ||
-      !tensor_of(a[2], "layer_norm: bias", true, &b, &device) || !tensor_of(a[5], "layer_norm: residual", true, &r, &device) ||
-      !tensor_of(a[6], "layer_norm: out", true, &out, &device) || !tensor_of(a[7], "layer_norm: sum_out", true, &sum_out, &device))
+  if (!tensor_of(a[0], "layer_norm: x", false, &x, &device) ||
+      !tensor_of(a[1], "layer_norm: weight", true, &w, &device) ||
+      !tensor_of(a[2], "layer_norm: bias", true, &b, &device) ||
+      !tensor_of(a[5], "layer_norm: residual", true, &r, &device) ||
+      !tensor_of(a[6], "layer_norm: out", true, &out, &device) ||
+      !tensor_of(a[7], "layer_norm: sum_out", true, &sum_out, &device))
     return nullptr;
   const long kind = PyLong_AsLong(a[3]);
   const double eps = PyFloat_AsDouble(a[4]);
@@ -169,13 +172,15 @@ PyObject* layer_norm(PyObject*, PyObject* const* a, Py_ssize_t count) {
   const bool stats = flag(a[8]);
   const at::IntArrayRef rows = x->sizes().slice(0, x->dim() - 1);
   const at::Tensor y = out != nullptr ? *out : at::empty(x->sizes(), x->options());
-  const at::Tensor sum = sum_out != nullptr ? *sum_out : r != nullptr ? at::empty(x->sizes(), x->options()) : at::Tensor();
+  const at::Tensor sum = sum_out != nullptr ? *sum_out
+                         : r != nullptr     ? at::empty(x->sizes(), x->options())
+                                            : at::Tensor();
   const at::Tensor mean = stats && kind == FLCE_NORM_LAYER ? floats(rows, *x) : at::Tensor();
   const at::Tensor rstd = stats ? floats(rows, *x) : at::Tensor();
   const at::Tensor* param = w != nullptr ? w : b;
   const flce_status_t st = ln_fwd(
-      static_cast<int>(kind), dtype, data(x), m.ld, data(r), ld_r, data(w), data(b), param ? code_of(*param) : dtype, m.n,
-      m.h, static_cast<float>(eps), y.data_ptr(), ld_y, sum.defined() ? sum.data_ptr() : nullptr, ld_s,
+      static_cast<int>(kind), dtype, data(x), m.ld, data(r), ld_r, data(w), data(b),
+      param != nullptr ? code_of(*param) : dtype, m.n, m.h, static_cast<float>(eps), y.data_ptr(), ld_y, sum.defined() ? sum.data_ptr() : nullptr, ld_s,
       mean.defined() ? mean.data_ptr<float>() : nullptr, rstd.defined() ? rstd.data_ptr<float>() : nullptr, stream());
   if (st != FLCE_OK) return fail(st, "ln_fwd");
   return tuple_of({&y, &sum, &mean, &rstd});
@@ -189,7 +194,8 @@ PyObject* layer_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t count) {
   if (count != 15) return fail(FLCE_ERR_INVALID_ARG, "layer_norm_backward: arguments");
   int device = -1;
   const at::Tensor *gy, *x, *w, *mean, *rstd, *gs, *out, *gw_out, *gb_out, *ws;
-  if (!tensor_of(a[0], "layer_norm_backward: grad_y", false, &gy, &device) || !tensor_of(a[1], "layer_norm_backward: x", false, &x, &device) ||
+  if (!tensor_of(a[0], "layer_norm_backward: grad_y", false, &gy, &device) ||
+      !tensor_of(a[1], "layer_norm_backward: x", false, &x, &device) ||
       !tensor_of(a[2], "layer_norm_backward: weight", true, &w, &device) ||
       !tensor_of(a[3], "layer_norm_backward: mean", true, &mean, &device) ||
       !tensor_of(a[4], "layer_norm_backward: rstd", false, &rstd, &device) ||
@@ -274,7 +280,8 @@ PyObject* grad_norm_of(PyObject*, PyObject* const* a, Py_ssize_t count) {
   if (PyErr_Occurred()) return nullptr;
   int device = -1;
   const at::Tensor *out, *ws;
-  if (!tensor_of(a[4], "grad_norm: out", true, &out, &device) || !tensor_of(a[5], "grad_norm: workspace", true, &ws, &device) ||
+  if (!tensor_of(a[4], "grad_norm: out", true, &out, &device) ||
+      !tensor_of(a[5], "grad_norm: workspace", true, &ws, &device) ||
       (out != nullptr && !floats_of(*out, 2, "grad_norm: out")))
     return nullptr;
   const auto options = at::TensorOptions().device(at::kCUDA, c10::cuda::current_device());
@@ -350,7 +357,8 @@ PyObject* adamw_table(PyObject*, PyObject* const* a, Py_ssize_t count) {
   std::sort(spans.begin(), spans.end(), [](const Span& x, const Span& y) { return x.from < y.from; });
   for (size_t k = 1; k < spans.size(); ++k)
     if (spans[k].from < spans[k - 1].to)
-      return fail(FLCE_ERR_INVALID_ARG, "AdamW: tensors %zd and %zd share memory", spans[k - 1].tensor, spans[k].tensor);
+      return fail(FLCE_ERR_INVALID_ARG, "AdamW: tensors %zd and %zd share memory", spans[k - 1].tensor,
+                  spans[k].tensor);
   Py_RETURN_NONE;
   END_HANDLE_TH_ERRORS
 }

@@ -25,7 +25,7 @@ struct LnBackward {
   void* grad_x;
   int64_t ld_grad_y, ld_x, ld_grad_sum, ld_grad_x, N, H;
   int param_dtype;
-  float2* row_terms;   // [N]: mean(u) * rstd, mean(u * xhat) * rstd
+  float2* row_terms;       // [N]: mean(u), mean(u xhat), of the form by elements
   float *part_w, *part_b;  // [parts][part_ld(H)]
   int parts;
   float *grad_weight, *grad_bias;
@@ -68,11 +68,11 @@ __device__ __forceinline__ void group_barrier(int id, int threads) {
 }
 
 // Threads of a CTA, one CTA on each SM: 112 registers each, which leaves the kernel
-// that adds up the CTAs' sums 8192 (128 where a bias's sums need more).  What a row costs a
-// thread beside its elements (addresses, sums, a barrier) is as much as eight elements
-// do, so a thread takes two vectors rather than there being twice as many threads: at
-// [16384, 4096] in bf16 with one vector each 5000 instructions a row, near all that the
-// SM can issue while memory moves it.
+// that adds up the CTAs' sums 8192 (128 where a bias's sums need more).  What a row
+// costs a thread beside its elements (addresses, sums, a barrier) is as much as eight
+// elements do, so a thread takes two vectors rather than there being twice as many
+// threads: at [16384, 4096] in bf16 with one vector each 5000 instructions a row, near
+// all that the SM can issue while memory moves it.
 constexpr int kBwdThreads = 512;
 
 // Whether the weights lie in shared memory: where the sums for a bias with the tests
@@ -145,14 +145,15 @@ __device__ __forceinline__ void add_up_here(const LnBackward& p) {
 //   u = grad_y weight,  grad_x = rstd (u - mean(u) - xhat mean(u xhat)) + grad_sum,
 // the means over a row, and the columns' sums of grad_y xhat and grad_y over the rows.
 // Memory bounds it: bf16 [16384, 4096] without a mean, with grad_sum, takes 80 us (6.7
-// TB/s; 85 us with the kernel that adds up the sums), fp32 [8191, 2048] 37 us (5.5; a
-// plain copy of as many bytes 36).  `group` threads take a row, VPT vectors each, and a CTA
-// holds as many such groups as fit.  A thread keeps its columns from row to row, so
-// that the sums over the rows stay in its registers until the end; so where rows
-// start inside a vector, a group takes only rows that start at the same place (every
-// eighth, or every fourth fp32 one).  Rows are fetched DEPTH - 1 ahead into shared
-// memory by asynchronous copies, each thread its own vectors: nothing waits for
-// another thread but the two sums over the row.
+// TB/s; 85 us with the kernel that adds up the sums, and a plain copy of as many bytes
+// 86), fp32 [8191, 2048] 37 us (5.5 TB/s; a copy 37).  `group` threads take a row, VPT
+// vectors each, and a CTA holds as many such groups as fit.  A thread keeps its columns
+// from row to row, so that the sums over the rows stay in its registers until the end;
+// so where rows start inside a vector, a group takes only rows that start at the same
+// place (every eighth, or every fourth fp32 one).  Rows are fetched DEPTH - 1 ahead into
+// shared memory by asynchronous copies, each thread its own vectors: nothing waits for
+// another thread but the two sums over the row.  LANES: those of a warp that a row takes
+// (32 where it takes whole warps).
 //
 // FULL: every thread has all of its vectors (the usual widths), so nothing asks.
 // LAST: for few rows, the launch's last CTA adds up the CTAs' sums (kernels of their
