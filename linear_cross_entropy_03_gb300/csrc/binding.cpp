@@ -243,31 +243,40 @@ PyObject* layer_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t count) {
   END_HANDLE_TH_ERRORS
 }
 
-// Calls f(i, tensor or null) for the members of a sequence; false once f does.
-template <typename F>
-bool for_each(PyObject* sequence, const char* where, F f) {
-  PyObject* fast = PySequence_Fast(sequence, "a sequence of tensors is wanted");
-  if (fast == nullptr) return false;
-  bool ok = true;
-  int device = -1;
-  const Py_ssize_t n = PySequence_Fast_GET_SIZE(fast);
-  for (Py_ssize_t i = 0; ok && i < n; ++i) {
-    const at::Tensor* t;
-    ok = tensor_of(PySequence_Fast_GET_ITEM(fast, i), where, true, &t, &device) && f(i, t);
+// The members of a sequence, or what an iterator yields: held as long as this is, and
+// so the memory of tensors that nobody else holds.
+class Members {
+ public:
+  explicit Members(PyObject* sequence) : fast_(PySequence_Fast(sequence, "a sequence of tensors is wanted")) {}
+  Members(const Members&) = delete;
+  Members& operator=(const Members&) = delete;
+  ~Members() { Py_XDECREF(fast_); }
+  bool ok() const { return fast_ != nullptr; }  // else an error is set
+  Py_ssize_t size() const { return PySequence_Fast_GET_SIZE(fast_); }
+  // Calls f(i, tensor or null) for each; false once f does.
+  template <typename F>
+  bool for_each(const char* where, F f) const {
+    int device = -1;
+    for (Py_ssize_t i = 0; i < size(); ++i) {
+      const at::Tensor* t;
+      if (!tensor_of(PySequence_Fast_GET_ITEM(fast_, i), where, true, &t, &device) || !f(i, t)) return false;
+    }
+    return true;
   }
-  Py_DECREF(fast);
-  return ok;
-}
+
+ private:
+  PyObject* fast_;
+};
 
 // grad_norm(grads, grad_scale, max_norm, eps, out, workspace) -> (norm, scale)
 PyObject* grad_norm_of(PyObject*, PyObject* const* a, Py_ssize_t count) {
   HANDLE_TH_ERRORS
   if (count != 6) return fail(FLCE_ERR_INVALID_ARG, "grad_norm: arguments");
+  const Members grads(a[0]);
+  if (!grads.ok()) return nullptr;
   std::vector<flce_tensor_t> table;
-  const Py_ssize_t expected = PySequence_Size(a[0]);
-  if (expected < 0) PyErr_Clear();
-  table.reserve(static_cast<size_t>(std::max<Py_ssize_t>(expected, 0)));
-  const bool ok = for_each(a[0], "grad_norm", [&](Py_ssize_t, const at::Tensor* t) {
+  table.reserve(static_cast<size_t>(grads.size()));
+  const bool ok = grads.for_each("grad_norm", [&](Py_ssize_t, const at::Tensor* t) {
     if (t == nullptr) return true;
     const int dtype = code_of(*t);
     if (dtype == kUnknown) return fail(FLCE_ERR_UNSUPPORTED, "grad_norm: a tensor's type"), false;
@@ -398,9 +407,11 @@ PyObject* adamw(PyObject*, PyObject* const* a, Py_ssize_t count) {
   numbers->skip_nonfinite = flag(a[7]);
   numbers->step = PyLong_AsLongLong(a[8]);
   if (PyErr_Occurred()) return nullptr;
-  Py_ssize_t seen = 0;
-  const bool ok = for_each(a[4], "AdamW.step", [&](Py_ssize_t i, const at::Tensor* t) {
-    if (++seen > tensors) return true;
+  const Members grads(a[4]);
+  if (!grads.ok()) return nullptr;
+  if (grads.size() != tensors)
+    return fail(FLCE_ERR_INVALID_ARG, "AdamW.step: %zd gradients for %zd tensors", grads.size(), tensors);
+  const bool ok = grads.for_each("AdamW.step", [&](Py_ssize_t i, const at::Tensor* t) {
     flce_adamw_tensor_t& e = table[i];
     e.n = 0;
     if (t == nullptr) return true;
@@ -416,7 +427,6 @@ PyObject* adamw(PyObject*, PyObject* const* a, Py_ssize_t count) {
     return true;
   });
   if (!ok) return nullptr;
-  if (seen != tensors) return fail(FLCE_ERR_INVALID_ARG, "AdamW.step: %zd gradients for %zd tensors", seen, tensors);
   const flce_status_t st = adamw_step(table, tensors, numbers, stream());
   if (st != FLCE_OK) return fail(st, "adamw_step");
   Py_RETURN_NONE;
