@@ -192,7 +192,11 @@ def _each(value, count, where):
 class AdamW:
     """AdamW over many tensors at once, with decoupled weight decay.
 
-    params        contiguous bf16, fp16 or fp32 tensors, updated in place.
+    params        contiguous bf16, fp16 or fp32 tensors, updated in place.  One that
+                  is given other memory (``p.data = ...``, a model that was moved)
+                  is followed, as is another tensor put into ``params``,
+                  ``copies`` or the lists of moments; a captured step is not: it
+                  goes on with the memory that it was captured with.
     weight_decay, lr_scale  one number, or one for each tensor.
     moments       "fp32", or "8bit": e4m3 numbers with an fp32 scale for each
                   block of 256; tensors below ``min_8bit_size`` elements keep
@@ -287,12 +291,15 @@ class AdamW:
                 not math.isfinite(grad_scale):
             return
         if self._step_dev is not None:
+            if self._step_dev.get_device() != torch.cuda.current_device():
+                raise FlceError(1, "AdamW.step: its number of steps lies on another GPU")
             # counted on the device, and not at all where the step is skipped; taken back if the call is refused
             on_device = skip_nonfinite and isinstance(grad_scale, torch.Tensor)
             one = torch.isfinite(grad_scale).reshape(-1)[:1].to(torch.int64) if on_device else 1
             self._step_dev.add_(one)
         try:
-            _native().adamw(*self._addresses, grads, lr, grad_scale, skip_nonfinite, self._steps + 1)
+            _native().adamw(*self._addresses, grads, lr, grad_scale, skip_nonfinite, self._steps + 1, self.params,
+                            self.exp_avg, self.exp_avg_sq, self.exp_avg_scale, self.exp_avg_sq_scale, self.copies)
         except Exception:
             if self._step_dev is not None:
                 self._step_dev.sub_(one)

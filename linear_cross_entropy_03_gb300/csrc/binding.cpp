@@ -308,6 +308,106 @@ PyObject* grad_norm_of(PyObject*, PyObject* const* a, Py_ssize_t count) {
   END_HANDLE_TH_ERRORS
 }
 
+// The tensors of an optimiser: lists of parameters, moments, the moments' scales and
+// copies, one entry for each parameter.
+constexpr int kLists = 6;
+
+bool lists_ok(PyObject* const* lists, Py_ssize_t count) {
+  for (int k = 0; k < kLists; ++k)
+    if (!PyList_Check(lists[k]) || PyList_GET_SIZE(lists[k]) != count)
+      return fail(FLCE_ERR_INVALID_ARG, "AdamW: lists of %zd tensors are wanted", count), false;
+  return true;
+}
+
+// Checks the tensors and fills the table and the element counts with them; on an error
+// both stay as they were.
+bool fill_table(PyObject* const* lists, Py_ssize_t count, flce_adamw_tensor_t* table, int64_t* sizes) {
+  if (!lists_ok(lists, count)) return false;
+  struct Span {
+    uintptr_t from, to;
+    Py_ssize_t tensor;
+  };
+  std::vector<Span> spans;
+  std::vector<flce_adamw_tensor_t> filled(table, table + count);
+  int device = -1;
+  for (Py_ssize_t i = 0; i < count; ++i) {
+    const at::Tensor* t[kLists];
+    for (int k = 0; k < kLists; ++k) {
+      if (!tensor_of(PyList_GET_ITEM(lists[k], i), "AdamW: a tensor", k > 2, &t[k], &device)) return false;
+      if (t[k] != nullptr && !t[k]->is_contiguous())
+        return fail(FLCE_ERR_UNSUPPORTED, "AdamW: tensor %zd: not contiguous", i), false;
+    }
+    const int64_t n = t[0]->numel(), blocks = (n + FLCE_ADAMW_BLOCK - 1) / FLCE_ADAMW_BLOCK;
+    flce_adamw_tensor_t& e = filled[static_cast<size_t>(i)];
+    e.param_dtype = code_of(*t[0]);
+    e.copy_dtype = t[5] != nullptr ? code_of(*t[5]) : FLCE_DTYPE_BF16;
+    if (e.param_dtype == kUnknown || e.copy_dtype == kUnknown)
+      return fail(FLCE_ERR_UNSUPPORTED, "AdamW: tensor %zd: its type, or its copy's", i), false;
+    const bool scaled = t[1]->scalar_type() == at::kFloat8_e4m3fn;
+    if (t[1]->scalar_type() != t[2]->scalar_type() || (!scaled && t[1]->scalar_type() != at::kFloat))
+      return fail(FLCE_ERR_UNSUPPORTED, "AdamW: tensor %zd: moments are both fp32 or both float8_e4m3fn", i), false;
+    if (t[1]->numel() != n || t[2]->numel() != n || (t[5] != nullptr && t[5]->numel() != n))
+      return fail(FLCE_ERR_INVALID_ARG, "AdamW: tensor %zd: moments or copy of another size", i), false;
+    for (int k = 3; k < 5; ++k) {
+      if (scaled != (t[k] != nullptr))
+        return fail(FLCE_ERR_INVALID_ARG, "AdamW: tensor %zd: 8-bit moments come with scales, fp32 ones without", i),
+               false;
+      if (scaled && !floats_of(*t[k], blocks, "AdamW: scales")) return false;
+    }
+    void* at[kLists];
+    for (int k = 0; k < kLists; ++k) {
+      at[k] = t[k] != nullptr ? t[k]->data_ptr() : nullptr;
+      const uintptr_t from = reinterpret_cast<uintptr_t>(at[k]);
+      if (t[k] != nullptr && t[k]->nbytes() > 0) spans.push_back({from, from + t[k]->nbytes(), i});
+    }
+    e.param = at[0], e.exp_avg = at[1], e.exp_avg_sq = at[2];
+    e.exp_avg_scale = static_cast<float*>(at[3]), e.exp_avg_sq_scale = static_cast<float*>(at[4]), e.copy = at[5];
+    e.moment_bits = scaled ? 8 : 32;
+    e.n = n;
+  }
+  std::sort(spans.begin(), spans.end(), [](const Span& x, const Span& y) { return x.from < y.from; });
+  for (size_t k = 1; k < spans.size(); ++k)
+    if (spans[k].from < spans[k - 1].to)
+      return fail(FLCE_ERR_INVALID_ARG, "AdamW: tensors %zd and %zd share memory", spans[k - 1].tensor,
+                  spans[k].tensor),
+             false;
+  std::copy(filled.begin(), filled.end(), table);
+  for (Py_ssize_t i = 0; i < count; ++i) sizes[i] = table[i].n;
+  return true;
+}
+
+// Whether the table still says where the tensors lie and what they are: a parameter may
+// have been given other memory (`p.data = ...`, a model that was moved) and a list's
+// entry another tensor since it was filled.
+bool table_holds(PyObject* const* lists, Py_ssize_t count, const flce_adamw_tensor_t* table, const int64_t* sizes) {
+  int device = -1;
+  const auto same = [&](PyObject* o, const void* at, at::ScalarType type, int64_t n) {
+    if (o == Py_None) return at == nullptr;
+    if (!THPVariable_Check(o)) return false;
+    const at::Tensor& t = THPVariable_Unpack(o);
+    if (!t.is_cuda()) return false;
+    if (device < 0) device = c10::cuda::current_device();
+    return t.get_device() == device && t.numel() == n && t.scalar_type() == type && t.is_contiguous() &&
+           t.data_ptr() == at;
+  };
+  const auto type_of = [](int code) {
+    return code == FLCE_DTYPE_FP32 ? at::kFloat : code == FLCE_DTYPE_BF16 ? at::kBFloat16 : at::kHalf;
+  };
+  for (Py_ssize_t i = 0; i < count; ++i) {
+    const flce_adamw_tensor_t& e = table[i];
+    const int64_t n = sizes[i], blocks = (n + FLCE_ADAMW_BLOCK - 1) / FLCE_ADAMW_BLOCK;
+    const at::ScalarType moment = e.moment_bits == 8 ? at::kFloat8_e4m3fn : at::kFloat;
+    if (!same(PyList_GET_ITEM(lists[0], i), e.param, type_of(e.param_dtype), n) ||
+        !same(PyList_GET_ITEM(lists[1], i), e.exp_avg, moment, n) ||
+        !same(PyList_GET_ITEM(lists[2], i), e.exp_avg_sq, moment, n) ||
+        !same(PyList_GET_ITEM(lists[3], i), e.exp_avg_scale, at::kFloat, blocks) ||
+        !same(PyList_GET_ITEM(lists[4], i), e.exp_avg_sq_scale, at::kFloat, blocks) ||
+        !same(PyList_GET_ITEM(lists[5], i), e.copy, type_of(e.copy_dtype), n))
+      return false;
+  }
+  return true;
+}
+
 // adamw_table(table, sizes, params, exp_avg, exp_avg_sq, exp_avg_scale, exp_avg_sq_scale, copies, weight_decay,
 // lr_scale): checks an optimiser's tensors, lists of one length, and fills the table at address `table` and the
 // element counts at `sizes` with them.
@@ -317,57 +417,16 @@ PyObject* adamw_table(PyObject*, PyObject* const* a, Py_ssize_t count) {
   auto* table = static_cast<flce_adamw_tensor_t*>(PyLong_AsVoidPtr(a[0]));
   auto* sizes = static_cast<int64_t*>(PyLong_AsVoidPtr(a[1]));
   if (PyErr_Occurred()) return nullptr;
-  for (int k = 2; k < 10; ++k)
+  for (const int k : {2, 8, 9})
     if (!PyList_Check(a[k]) || PyList_GET_SIZE(a[k]) != PyList_GET_SIZE(a[2]))
       return fail(FLCE_ERR_INVALID_ARG, "AdamW: lists of one length are wanted");
-  struct Span {
-    uintptr_t from, to;
-    Py_ssize_t tensor;
-  };
-  std::vector<Span> spans;
-  int device = -1;
-  for (Py_ssize_t i = 0; i < PyList_GET_SIZE(a[2]); ++i) {
-    const at::Tensor* t[6];  // parameter, moments, their scales, copy
-    for (int k = 0; k < 6; ++k) {
-      if (!tensor_of(PyList_GET_ITEM(a[2 + k], i), "AdamW: a tensor", k > 2, &t[k], &device)) return nullptr;
-      if (t[k] != nullptr && !t[k]->is_contiguous())
-        return fail(FLCE_ERR_UNSUPPORTED, "AdamW: tensor %zd: not contiguous", i);
-    }
-    const int64_t n = t[0]->numel(), blocks = (n + FLCE_ADAMW_BLOCK - 1) / FLCE_ADAMW_BLOCK;
-    flce_adamw_tensor_t& e = table[i];
-    e.param_dtype = code_of(*t[0]);
-    e.copy_dtype = t[5] != nullptr ? code_of(*t[5]) : FLCE_DTYPE_BF16;
-    if (e.param_dtype == kUnknown || e.copy_dtype == kUnknown)
-      return fail(FLCE_ERR_UNSUPPORTED, "AdamW: tensor %zd: its type, or its copy's", i);
-    const bool scaled = t[1]->scalar_type() == at::kFloat8_e4m3fn;
-    if (t[1]->scalar_type() != t[2]->scalar_type() || (!scaled && t[1]->scalar_type() != at::kFloat))
-      return fail(FLCE_ERR_UNSUPPORTED, "AdamW: tensor %zd: moments are both fp32 or both float8_e4m3fn", i);
-    if (t[1]->numel() != n || t[2]->numel() != n || (t[5] != nullptr && t[5]->numel() != n))
-      return fail(FLCE_ERR_INVALID_ARG, "AdamW: tensor %zd: moments or copy of another size", i);
-    for (int k = 3; k < 5; ++k)
-      if (scaled != (t[k] != nullptr) || (scaled && !floats_of(*t[k], blocks, "AdamW: scales")))
-        return PyErr_Occurred() ? nullptr
-                                : fail(FLCE_ERR_INVALID_ARG, "AdamW: tensor %zd: 8-bit moments come with scales, fp32 "
-                                       "ones without", i);
-    void* at[6];
-    for (int k = 0; k < 6; ++k) {
-      at[k] = t[k] != nullptr ? t[k]->data_ptr() : nullptr;
-      const uintptr_t from = reinterpret_cast<uintptr_t>(at[k]);
-      if (t[k] != nullptr && t[k]->nbytes() > 0) spans.push_back({from, from + t[k]->nbytes(), i});
-    }
-    e.param = at[0], e.exp_avg = at[1], e.exp_avg_sq = at[2];
-    e.exp_avg_scale = static_cast<float*>(at[3]), e.exp_avg_sq_scale = static_cast<float*>(at[4]), e.copy = at[5];
-    e.moment_bits = scaled ? 8 : 32;
-    e.weight_decay = static_cast<float>(PyFloat_AsDouble(PyList_GET_ITEM(a[8], i)));
-    e.lr_scale = static_cast<float>(PyFloat_AsDouble(PyList_GET_ITEM(a[9], i)));
+  const Py_ssize_t tensors = PyList_GET_SIZE(a[2]);
+  for (Py_ssize_t i = 0; i < tensors; ++i) {
+    table[i].weight_decay = static_cast<float>(PyFloat_AsDouble(PyList_GET_ITEM(a[8], i)));
+    table[i].lr_scale = static_cast<float>(PyFloat_AsDouble(PyList_GET_ITEM(a[9], i)));
     if (PyErr_Occurred()) return nullptr;
-    e.n = sizes[i] = n;
   }
-  std::sort(spans.begin(), spans.end(), [](const Span& x, const Span& y) { return x.from < y.from; });
-  for (size_t k = 1; k < spans.size(); ++k)
-    if (spans[k].from < spans[k - 1].to)
-      return fail(FLCE_ERR_INVALID_ARG, "AdamW: tensors %zd and %zd share memory", spans[k - 1].tensor,
-                  spans[k].tensor);
+  if (!fill_table(a + 2, tensors, table, sizes)) return nullptr;
   Py_RETURN_NONE;
   END_HANDLE_TH_ERRORS
 }
@@ -386,17 +445,19 @@ bool number_of(PyObject* o, const char* where, int* device, double* value, const
   return true;
 }
 
-// adamw(table, sizes, count, numbers, grads, lr, grad_scale, skip_nonfinite, step): fills the gradients into the table
-// of flce_adamw_tensor_t at address `table` (an element count of 0 where there is none) and the step's numbers into the
-// flce_adamw_t at `numbers`, and takes the step.
+// adamw(table, sizes, count, numbers, grads, lr, grad_scale, skip_nonfinite, step, params, exp_avg, exp_avg_sq,
+// exp_avg_scale, exp_avg_sq_scale, copies): fills the table of flce_adamw_tensor_t at address `table` again if the
+// tensors of the lists are no longer those in it, fills in the gradients (an element count of 0 where there is none) and
+// the step's numbers (the flce_adamw_t at `numbers`), and takes the step.
 PyObject* adamw(PyObject*, PyObject* const* a, Py_ssize_t count) {
   HANDLE_TH_ERRORS
-  if (count != 9) return fail(FLCE_ERR_INVALID_ARG, "AdamW.step: arguments");
+  if (count != 9 + kLists) return fail(FLCE_ERR_INVALID_ARG, "AdamW.step: arguments");
   auto* table = static_cast<flce_adamw_tensor_t*>(PyLong_AsVoidPtr(a[0]));
-  const auto* sizes = static_cast<const int64_t*>(PyLong_AsVoidPtr(a[1]));
+  auto* sizes = static_cast<int64_t*>(PyLong_AsVoidPtr(a[1]));
   const Py_ssize_t tensors = PyLong_AsSsize_t(a[2]);
   auto* numbers = static_cast<flce_adamw_t*>(PyLong_AsVoidPtr(a[3]));
-  if (PyErr_Occurred()) return nullptr;
+  if (PyErr_Occurred() || !lists_ok(a + 9, tensors)) return nullptr;
+  if (!table_holds(a + 9, tensors, table, sizes) && !fill_table(a + 9, tensors, table, sizes)) return nullptr;
   int on = -1;
   double factor = 1;
   if (!number_of(a[5], "AdamW.step: lr", &on, &numbers->lr, &numbers->lr_dev)) return nullptr;

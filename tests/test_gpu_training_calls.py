@@ -41,3 +41,101 @@ def test_step_with_gradients_that_nobody_else_holds(moments):
     for wrong in (2, 4):
         with pytest.raises(flce.FlceError):
             opt.step(g for g in (grads * 2)[:wrong])
+
+
+# ------------------------------------------------------------ parameters that move
+
+def two_alike(moments, **kw):
+    """Two optimisers of equal tensors, and their gradients."""
+    sizes = [5000, 300]
+    made = []
+    for _ in range(2):
+        params = [normal(n, k, 0.05) for k, n in enumerate(sizes)]
+        made.append(flce.AdamW(params, lr=1e-2, moments=moments, copies=[p.bfloat16() for p in params], **kw))
+    return made, [normal(n, 50 + k, 1e-2) for k, n in enumerate(sizes)]
+
+
+def tensors_of(opt):
+    lists = (opt.params, opt.exp_avg, opt.exp_avg_sq, opt.exp_avg_scale, opt.exp_avg_sq_scale, opt.copies)
+    return [t for ts in lists for t in ts if t is not None]
+
+
+def equal(a, b):
+    return all(torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip(tensors_of(a), tensors_of(b)))
+
+
+@pytest.mark.parametrize("moments", ["fp32", "8bit"])
+def test_step_follows_tensors_that_were_given_other_memory(moments):
+    (opt, still), grads = two_alike(moments)
+    opt.step(grads), still.step(grads)
+    old = [t.detach() for t in tensors_of(opt)]      # aliases: they keep the memory, so that nothing else lies there
+    kept = [t.clone() for t in old]
+    for t in tensors_of(opt):
+        t.data = t.data.clone()
+    opt.step(grads), still.step(grads)
+    assert equal(opt, still)
+    assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(old, kept))
+
+
+@pytest.mark.parametrize("moments", ["fp32", "8bit"])
+def test_step_follows_other_tensors_in_its_lists(moments):
+    (opt, still), grads = two_alike(moments)
+    opt.step(grads), still.step(grads)
+    before = tensors_of(opt)
+    kept = [t.clone() for t in before]
+    for ts in (opt.params, opt.exp_avg, opt.exp_avg_sq, opt.exp_avg_scale, opt.exp_avg_sq_scale, opt.copies):
+        ts[:] = [t if t is None else t.clone() for t in ts]
+    opt.step(grads), still.step(grads)
+    assert equal(opt, still)
+    assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(before, kept))
+
+
+def test_step_follows_a_parameter_of_another_type():
+    (opt, still), grads = two_alike("fp32")
+    first = opt.params[0]
+    first.data = first.data.half()
+    want = flce.AdamW([first.clone()], lr=1e-2)
+    opt.step(grads), still.step(grads), want.step(grads[:1])
+    assert first.dtype == torch.float16 and torch.equal(first, want.params[0])
+    assert torch.equal(opt.params[1], still.params[1])
+
+
+def test_step_refuses_what_its_tensors_have_become():
+    def longer(o):
+        o.params[0].data = torch.zeros(5001, device="cuda")
+
+    def elsewhere(o):
+        o.params[0].data = o.params[0].data.cpu()
+
+    def strided(o):
+        o.params[0].data = torch.zeros(10000, device="cuda")[::2]
+
+    def another_type(o):
+        o.exp_avg[0].data = o.exp_avg[0].data.double()
+
+    def shared(o):
+        o.exp_avg[0] = o.exp_avg_sq[0]
+
+    def one_more(o):
+        o.params.append(torch.zeros(5, device="cuda"))
+
+    def none(o):
+        o.params[0] = None
+
+    for change in (longer, elsewhere, strided, another_type, shared, one_more, none):
+        (opt, _), grads = two_alike("fp32")
+        change(opt)
+        rest = opt.params[1].clone()
+        for _ in range(2):                      # the second time too
+            with pytest.raises(flce.FlceError):
+                opt.step(grads)
+        assert opt.steps == 0 and torch.equal(opt.params[1], rest)
+
+
+def test_captured_step_number_on_another_gpu_is_refused(monkeypatch):
+    opt = flce.AdamW([normal(10, 1)], lr=1e-2, capturable=True)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    with pytest.raises(flce.FlceError):
+        opt.step([normal(10, 2)])
+    monkeypatch.undo()
+    assert opt.steps == 0
