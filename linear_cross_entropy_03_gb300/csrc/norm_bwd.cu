@@ -6,6 +6,8 @@
 // residual stream), with about fifteen operations on it: memory bandwidth bounds it.
 #include <math.h>
 
+#include <atomic>
+
 #include "arrival.cuh"
 #include "norm.cuh"
 
@@ -577,20 +579,39 @@ Shape shape_of(const LnBackward& p, int64_t vectors, int vpt, int lanes, bool sh
   return r;
 }
 
+// Lets `kernel` have `most` bytes of shared memory, once a device: the limit belongs to
+// the kernel, so with each launch's own size one thread would lower it between another's
+// setting it and its launch.
+template <auto KERNEL>
+cudaError_t allow_shared(int most) {
+  static std::atomic<bool> allowed[64] = {};
+  int device = 0;
+  const cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess) return e;
+  const bool kept = device >= 0 && device < 64;
+  if (kept && allowed[device].load(std::memory_order_acquire)) return cudaSuccess;
+  const cudaError_t set = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+  if (set == cudaSuccess && kept) allowed[device].store(true, std::memory_order_release);
+  return set;
+}
+
 template <typename T, bool RMS, bool BIAS, int VPT, int LANES, bool SHIFTED, bool FULL, bool LAST>
 cudaError_t launch_rows(const LnBackward& p, const Shape& shape, cudaStream_t s) {
   constexpr bool kShareWeights = share_weights<T, VPT>(BIAS, SHIFTED, FULL);
   constexpr int kDepth = VPT > 2 ? 2 : kShareWeights ? 3 : 4;  // what 227 KB hold
   const int threads = shape.group * shape.groups;
-  const auto kernel = ln_bwd_kernel<T, RMS, BIAS, VPT, LANES, kDepth, SHIFTED, FULL, LAST>;
+  constexpr auto kernel = ln_bwd_kernel<T, RMS, BIAS, VPT, LANES, kDepth, SHIFTED, FULL, LAST>;
   // as many stages of the ring as a group has rows, and room for the groups' sums at the end
   const int64_t stages = std::min<int64_t>(kDepth, div_up(p.N, shape.grid * shape.groups));
   const int64_t slots = (p.grad_sum != nullptr ? 3 : 2) * stages + (kShareWeights ? 2 : 0);
   const int64_t sums = shape.groups > 1 ? shape.groups * p.H * 4 * 2 : 0;
   const size_t smem = static_cast<size_t>(std::max<int64_t>(int64_t(threads) * VPT * 16 * slots, sums));
   if (smem > kSharedByDefault) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    // the whole ring: 96 bytes or more for each of a CTA's vectors, of which the groups' sums take at most 64 (and
+    // for what lies beside shifted ones a little more)
+    constexpr int kMost = kBwdThreads * VPT * 16 * (3 * kDepth + (kShareWeights ? 2 : 0));
+    if (smem > kMost) return cudaErrorInvalidConfiguration;
+    const cudaError_t e = allow_shared<kernel>(kMost);
     if (e != cudaSuccess) return e;
   }
   kernel<<<static_cast<unsigned int>(shape.grid), threads, smem, s>>>(p, shape.group, shape.groups);

@@ -1,5 +1,7 @@
 """How a program holds the tensors that it hands to the norm and optimiser calls:
 in iterators, and in places that it gives up."""
+import threading
+
 import pytest
 import torch
 
@@ -139,3 +141,39 @@ def test_captured_step_number_on_another_gpu_is_refused(monkeypatch):
         opt.step([normal(10, 2)])
     monkeypatch.undo()
     assert opt.steps == 0
+
+
+# ------------------------------------------------------------ calls of several threads
+
+def test_norm_backward_from_several_threads():
+    """Calls of one kernel whose launches differ in shared memory do not take it from one another."""
+    shapes = [(4000, 4096, True), (152, 4096, False), (400, 4096, True), (300, 4096, False)]
+    made = []
+    for n, h, residual in shapes:
+        x, gy = normal(n * h, n, dtype=torch.bfloat16).view(n, h), normal(n * h, n + 1, dtype=torch.bfloat16).view(n, h)
+        rstd = torch.ones(n, device="cuda")
+        want = flce.layer_norm_backward(gy, x, rstd=rstd, kind="rms", grad_sum=x if residual else None, grad_bias=False)
+        size = flce.ln_workspace_size(n, h)
+        out = torch.empty_like(x), torch.empty(h, device="cuda"), torch.empty(size, dtype=torch.uint8, device="cuda")
+        made.append((n, h, residual, x, gy, rstd, want, out, size, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    codes, start = [[] for _ in made], threading.Barrier(len(made))
+
+    def calls(k):
+        n, h, residual, x, gy, rstd, _, (gx, gw, work), size, stream = made[k]
+        at = [t.data_ptr() for t in (gy, x, rstd, gx, gw, work)]
+        start.wait()
+        for _ in range(1000):
+            codes[k].append(flce.ln_bwd("rms", "bf16", at[0], h, at[1], h, None, "bf16", None, at[2],
+                                        at[1] if residual else None, h, n, h, at[3], h, at[4], None, 0, at[5], size,
+                                        stream.cuda_stream))
+
+    threads = [threading.Thread(target=calls, args=(k,)) for k in range(len(made))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert [sum(c != 0 for c in one) for one in codes] == [0] * len(made) and all(len(c) == 1000 for c in codes)
+    for *_, want, (gx, gw, _), _, _ in made:
+        assert torch.equal(gx, want["grad_x"]) and torch.equal(gw, want["grad_weight"])
