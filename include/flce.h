@@ -442,7 +442,7 @@ flce_status_t ln_bwd(int kind, int dtype, const void* grad_y, int64_t ld_grad_y,
  * returns; the pointers in them are device pointers.
  */
 
-/* A tensor of n contiguous elements of `dtype` (BF16, FP16 or FP32). */
+/* A tensor of n contiguous elements (at most 2^41) of `dtype` (BF16, FP16 or FP32). */
 typedef struct {
   const void* data;
   int64_t n;
@@ -480,7 +480,7 @@ flce_status_t grad_norm(const flce_tensor_t* tensors, int64_t count, float grad_
 #define FLCE_ADAMW_BLOCK 256
 
 /*
- * One tensor of an AdamW step: n contiguous elements each.
+ * One tensor of an AdamW step: n contiguous elements each, at most 2^41.
  *  moment_bits  32: exp_avg and exp_avg_sq are fp32 [n], the scales NULL.
  *               8:  both are e4m3 numbers (1 byte) [n], and the scales fp32
  *                   [ceil(n / FLCE_ADAMW_BLOCK)]; element i of exp_avg stands

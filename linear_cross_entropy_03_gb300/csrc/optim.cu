@@ -18,7 +18,8 @@ namespace flce {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int64_t kMaxElems = int64_t(1) << 42;  // of one tensor: its chunks fit a launch
+constexpr int64_t kMaxElems = int64_t(1) << 41;  // of one tensor
+constexpr int64_t kMaxChunks = 0x7fffffff;       // of a launch
 
 // Entries are ordered by first chunk: the one that holds chunk c.
 template <typename E>
@@ -184,6 +185,7 @@ constexpr int kAdamChunk = 4096;   // elements of a CTA
 // on, and four warps.  525M elements with a 16-bit copy took 1.42 ms so; with eight
 // warps 1.52 ms, with two 1.67; with four blocks a warp 1.63, with one 1.61 (8 warps).
 constexpr int kAdamChunk8 = 2048, kThreads8 = 128;
+static_assert(kMaxElems / kAdamChunk8 <= kMaxChunks && kMaxElems / kAdamChunk <= kMaxChunks, "a tensor fits a launch");
 static_assert(kAdamChunk8 % (FLCE_ADAMW_BLOCK * (kThreads8 / 32)) == 0, "whole blocks for every warp");
 constexpr float kE4m3Max = 448.f;
 constexpr unsigned int kE4m3Nan = 0x7Fu;
@@ -810,7 +812,7 @@ flce_status_t adamw_step(const flce_adamw_tensor_t* tensors, int64_t count, cons
         if (x.n == 0 || x.moment_bits != bits) continue;
         const int head = common_head(x);
         const int64_t more = bits == 8 ? div_up(x.n, kAdamChunk8) : div_up(head > 0 ? x.n - head : x.n, kAdamChunk);
-        if (chunks + more > 0x7fffffff) break;
+        if (chunks + more > kMaxChunks) break;  // the next launch's: by itself every tensor fits
         entry[filled++] = {x.param, x.grad, x.exp_avg, x.exp_avg_sq, x.exp_avg_scale, x.exp_avg_sq_scale, x.copy, x.n,
                            x.lr_scale, x.weight_decay, static_cast<unsigned int>(chunks), static_cast<int>(i),
                            static_cast<int8_t>(x.param_dtype), static_cast<int8_t>(x.grad_dtype),

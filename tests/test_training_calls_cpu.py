@@ -29,3 +29,21 @@ def test_a_failing_call_lets_go_of_its_gradients():
         flce.grad_norm(yields())
     gc.collect()
     assert seen() is None
+
+
+# ------------------------------------------------------------ the largest tensors
+
+FAKE, FAR = 0x10000, 1 << 40   # never dereferenced by a refused call
+INVALID = 1
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+@pytest.mark.parametrize("n", [(1 << 41) + 1, 1 << 42, 1 << 62])
+def test_a_tensor_too_long_for_a_launch_is_refused(n, bits):
+    """A step over such a tensor of 8-bit moments did nothing, to it and to those after it, and returned no error."""
+    scales = dict(exp_avg_scale=FAKE, exp_avg_sq_scale=FAKE) if bits == 8 else {}
+    table = (flce.AdamWEntry * 1)(flce.AdamWEntry(
+        param=FAKE, grad=FAR, exp_avg=2 * FAR, exp_avg_sq=3 * FAR, n=n, lr_scale=1.0, weight_decay=0.1, param_dtype=1,
+        grad_dtype=1, moment_bits=bits, **scales))
+    numbers = flce.AdamWNumbers(lr=1e-3, beta1=0.9, beta2=0.95, eps=1e-8, step=1, grad_scale=1.0)
+    assert flce.adamw_step(table, 1, numbers, 0) == INVALID
