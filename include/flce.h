@@ -462,7 +462,8 @@ size_t grad_norm_workspace_size(int64_t count);
  *  step).  Squares are summed in fp32: a gradient above 1.8e19 in size makes
  *  the norm infinite, and squares of gradients below 1e-19 lose bits.
  *
- *  tensors, count  `count` >= 0 tensors; n = 0 is allowed.
+ *  tensors, count  `count` >= 0 tensors; n = 0 is allowed.  All together, each
+ *                  rounded up to 32 KB, less than 2^46 bytes.
  *  grad_scale      finite; what the gradients are to be multiplied by (1, or
  *                  the inverse of a loss scale).
  *  max_norm, eps   >= 0; max_norm infinity: no clipping.

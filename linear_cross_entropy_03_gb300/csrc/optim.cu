@@ -671,6 +671,11 @@ int common_head(const flce_adamw_tensor_t& t) {
   return t.n > head ? head : -1;
 }
 
+// At least the vectors from the first boundary on (a chunk too many finds nothing).
+int64_t norm_chunks(const flce_tensor_t& t) {
+  return div_up(t.n, kNormChunk * static_cast<int64_t>(16 / elem_size(t.dtype)));
+}
+
 // The partial sums of every launch, then the word that finds the last CTA.
 size_t norm_parts_bytes(int64_t count) {
   return align_up(static_cast<size_t>(std::max<int64_t>(1, div_up(count, kNormEntries))) * kNormParts * 4, 256);
@@ -710,11 +715,15 @@ flce_status_t grad_norm(const flce_tensor_t* tensors, int64_t count, float grad_
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream_);
   if (count < 0 || (count > 0 && tensors == nullptr) || out == nullptr) return FLCE_ERR_INVALID_ARG;
   if (!isfinite(grad_scale) || !(max_norm >= 0.f) || !(eps >= 0.f) || isinf(eps)) return FLCE_ERR_INVALID_ARG;
+  int64_t all = 0;
   for (int64_t i = 0; i < count; ++i) {
     const flce_tensor_t& t = tensors[i];
     if (t.n < 0 || t.n > kMaxElems || (t.n > 0 && t.data == nullptr)) return FLCE_ERR_INVALID_ARG;
     if (!float_dtype(t.dtype)) return FLCE_ERR_UNSUPPORTED;
     if (!aligned_to(t.data, elem_size(t.dtype))) return FLCE_ERR_MISALIGNED;
+    // together they fit one launch's numbers, so that only their count makes launches, as the workspace has it
+    all += norm_chunks(t);
+    if (all > kMaxChunks) return FLCE_ERR_INVALID_ARG;
   }
   if (!aligned_to(out, 4)) return FLCE_ERR_MISALIGNED;
   if (workspace == nullptr || !aligned_to(workspace, 256) || workspace_bytes < norm_workspace(count))
@@ -738,11 +747,8 @@ flce_status_t grad_norm(const flce_tensor_t* tensors, int64_t count, float grad_
     int64_t chunks = 0;
     rest.count = 0;
     while (i < count && rest.count < kNormEntries) {
-      // at least the vectors from the first boundary on (a chunk too many finds nothing)
-      const int64_t more = div_up(tensors[i].n, kNormChunk * static_cast<int64_t>(16 / elem_size(tensors[i].dtype)));
-      if (chunks + more > 0x7fffffff) break;
       entry[rest.count++] = {tensors[i].data, tensors[i].n, static_cast<unsigned int>(chunks), tensors[i].dtype};
-      chunks += more;
+      chunks += norm_chunks(tensors[i]);
       ++i;
       skip_empty();
     }

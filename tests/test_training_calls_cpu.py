@@ -47,3 +47,11 @@ def test_a_tensor_too_long_for_a_launch_is_refused(n, bits):
         grad_dtype=1, moment_bits=bits, **scales))
     numbers = flce.AdamWNumbers(lr=1e-3, beta1=0.9, beta2=0.95, eps=1e-8, step=1, grad_scale=1.0)
     assert flce.adamw_step(table, 1, numbers, 0) == INVALID
+
+
+@pytest.mark.parametrize("dtype,n,count", [(1, 1 << 41, 9), (1, 1 << 40, 17), (0, 1 << 41, 17), (1, 1 << 41, 4000)])
+def test_gradients_that_make_more_launches_than_the_workspace_is_for_are_refused(dtype, n, count):
+    """Launches that ended early, at 2^31 chunks, had their partial sums written past the stated size."""
+    table = (flce.TensorEntry * count)(*[flce.TensorEntry(FAKE, n, dtype, 0)] * count)
+    size = flce.grad_norm_workspace_size(count)
+    assert flce.grad_norm_raw(table, count, 1.0, 1.0, 1e-6, FAKE, FAKE, size, 0) == INVALID
