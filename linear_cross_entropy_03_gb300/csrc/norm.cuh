@@ -149,6 +149,10 @@ struct Row {
 
 constexpr int kAnyThreads = 256;
 
+// Terms that a thread adds up before it adds their sum to the others': chains of fp32
+// additions as long as a row or a range of rows lose bits (16384 equal terms 1e-4 of their sum).
+constexpr int64_t kBatch = 64;
+
 // Sum over the CTA's threads (a multiple of 32, at most 1024), to all of them.
 __device__ __forceinline__ float2 block_sum2(float2 v, float2* scratch) {
   v.x = warp_sum(v.x);

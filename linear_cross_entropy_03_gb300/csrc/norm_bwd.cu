@@ -447,7 +447,8 @@ __global__ void __launch_bounds__(kAnyThreads) ln_bwd_rows_any_kernel(const LnBa
 }
 
 // grad_x and the column sums, 64 columns by 4 rows a CTA at a time: CTA
-// (c, s) takes columns 64 c.. and the s-th of gridDim.y ranges of rows.
+// (c, s) takes columns 64 c.. and the s-th of gridDim.y ranges of rows, of which
+// wide rows have few: a thread sums kBatch rows apart from those before.
 template <typename T, bool RMS>
 __global__ void __launch_bounds__(kAnyThreads) ln_bwd_cols_any_kernel(const LnBackward p) {
   __shared__ float2 scratch[4][64];
@@ -458,18 +459,24 @@ __global__ void __launch_bounds__(kAnyThreads) ln_bwd_cols_any_kernel(const LnBa
   float sw = 0.f, sb = 0.f;
   if (h < p.H) {
     const float w = p.weight != nullptr ? load_elem(p.weight, p.param_dtype, h) : 1.f;
-    for (int64_t n = n0 + lane; n < n1; n += 4) {
-      const float mu = RMS ? 0.f : p.mean[n], inv = p.rstd[n];
-      const float g = to_float(static_cast<const T*>(p.grad_y)[n * p.ld_grad_y + h]);
-      const float xhat = (to_float(static_cast<const T*>(p.x)[n * p.ld_x + h]) - mu) * inv;
-      sw += g * xhat;
-      sb += g;
-      if (p.grad_x != nullptr) {
-        const float2 t = p.row_terms[n];
-        float o = (g * w - t.x - xhat * t.y) * inv;
-        if (p.grad_sum != nullptr) o += to_float(static_cast<const T*>(p.grad_sum)[n * p.ld_grad_sum + h]);
-        static_cast<T*>(p.grad_x)[n * p.ld_grad_x + h] = from_float<T>(o);
+    for (int64_t n = n0 + lane; n < n1;) {
+      const int64_t end = min(n + 4 * kBatch, n1);
+      float bw = 0.f, bb = 0.f;
+      for (; n < end; n += 4) {
+        const float mu = RMS ? 0.f : p.mean[n], inv = p.rstd[n];
+        const float g = to_float(static_cast<const T*>(p.grad_y)[n * p.ld_grad_y + h]);
+        const float xhat = (to_float(static_cast<const T*>(p.x)[n * p.ld_x + h]) - mu) * inv;
+        bw += g * xhat;
+        bb += g;
+        if (p.grad_x != nullptr) {
+          const float2 t = p.row_terms[n];
+          float o = (g * w - t.x - xhat * t.y) * inv;
+          if (p.grad_sum != nullptr) o += to_float(static_cast<const T*>(p.grad_sum)[n * p.ld_grad_sum + h]);
+          static_cast<T*>(p.grad_x)[n * p.ld_grad_x + h] = from_float<T>(o);
+        }
       }
+      sw += bw;
+      sb += bb;
     }
   }
   scratch[lane][col] = make_float2(sw, sb);
