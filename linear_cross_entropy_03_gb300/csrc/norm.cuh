@@ -167,6 +167,24 @@ __device__ __forceinline__ float2 block_sum2(float2 v, float2* scratch) {
   return v;
 }
 
+// Sums of at(h).x and at(h).y over the columns of this thread of a CTA of kAnyThreads.
+template <typename F>
+__device__ __forceinline__ float2 thread_sum2(int64_t H, F at) {
+  float2 sum = make_float2(0.f, 0.f);
+  for (int64_t h = threadIdx.x; h < H;) {
+    const int64_t end = min(h + kBatch * kAnyThreads, H);
+    float2 batch = make_float2(0.f, 0.f);
+    for (; h < end; h += kAnyThreads) {
+      const float2 v = at(h);
+      batch.x += v.x;
+      batch.y += v.y;
+    }
+    sum.x += batch.x;
+    sum.y += batch.y;
+  }
+  return sum;
+}
+
 // ------------------------------------------------------------------ launches
 
 // How a call's matrices lie to 16-byte vectors.

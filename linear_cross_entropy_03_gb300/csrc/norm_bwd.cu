@@ -434,13 +434,11 @@ __global__ void __launch_bounds__(kAnyThreads) ln_bwd_rows_any_kernel(const LnBa
     const T* x = static_cast<const T*>(p.x) + n * p.ld_x;
     const T* g = static_cast<const T*>(p.grad_y) + n * p.ld_grad_y;
     const float mu = RMS ? 0.f : p.mean[n], inv = p.rstd[n];
-    float2 a = make_float2(0.f, 0.f);
-    for (int64_t h = threadIdx.x; h < p.H; h += kAnyThreads) {
+    float2 a = thread_sum2(p.H, [&](int64_t h) {
       float u = to_float(g[h]);
       if (p.weight != nullptr) u *= load_elem(p.weight, p.param_dtype, h);
-      a.x += u;
-      a.y += u * ((to_float(x[h]) - mu) * inv);
-    }
+      return make_float2(u, u * ((to_float(x[h]) - mu) * inv));
+    });
     a = block_sum2(a, scratch);
     if (threadIdx.x == 0) p.row_terms[n] = make_float2(RMS ? 0.f : a.x / p.H, a.y / p.H);
   }

@@ -188,16 +188,14 @@ __global__ void __launch_bounds__(kAnyThreads) ln_fwd_any_kernel(const LnForward
     };
     float mu = 0.f;
     if (!RMS) {
-      float a = 0.f;
-      for (int64_t h = threadIdx.x; h < p.H; h += kAnyThreads) a += at(h);
-      mu = block_sum2(make_float2(a, 0.f), scratch).x / static_cast<float>(p.H);
+      const float2 a = thread_sum2(p.H, [&](int64_t h) { return make_float2(at(h), 0.f); });
+      mu = block_sum2(a, scratch).x / static_cast<float>(p.H);
     }
-    float q = 0.f;
-    for (int64_t h = threadIdx.x; h < p.H; h += kAnyThreads) {
+    const float2 squares = thread_sum2(p.H, [&](int64_t h) {
       const float d = at(h) - mu;
-      q += d * d;
-    }
-    q = block_sum2(make_float2(q, 0.f), scratch).x / static_cast<float>(p.H);
+      return make_float2(d * d, 0.f);
+    });
+    const float q = block_sum2(squares, scratch).x / static_cast<float>(p.H);
     const float inv = rsqrtf(q + p.eps);
     for (int64_t h = threadIdx.x; h < p.H; h += kAnyThreads) {
       const float v = at(h);

@@ -38,3 +38,24 @@ def test_column_sums_by_elements(n, h, dtype):
     rows = -(-n // (4 * ranges))                          # of a thread: batches of 64, then the batches
     chain = 64 + -(-rows // 64) + 4 + -(-304 // 32) + 10  # and four threads' sums, and the ranges'
     check_column_sums(n, h, dtype, chain)
+
+
+@pytest.mark.parametrize("h", [100001, (1 << 20) + 1, (1 << 24) - 1])
+def test_row_sums_of_very_long_rows(h):
+    """Rows of one number each: their means, mean squares and, backward, the means of u and u xhat."""
+    values = torch.tensor([0.1, 0.7, 1.1, 1.7], device="cuda")
+    x = values[:, None].expand(4, h).contiguous()
+    exact = values.double()
+    chain = 64 + -(-h // (64 * 256)) + 13                 # batches of 64, then the batches, then 256 threads
+    tol = (chain + 4) * UNIT                              # and a division, a root, two products
+    out = flce.layer_norm(x)
+    assert float((out["mean"].double() / exact - 1).abs().max()) <= tol
+    out = flce.layer_norm(x, kind="rms", eps=0.0)
+    assert float((out["rstd"].double() * exact - 1).abs().max()) <= tol
+    assert float((out["y"].double() - 1).abs().max()) <= tol
+    # xhat = 0: grad_x = grad_y - mean(grad_y) = 0;  rms with xhat = 1: grad_x = grad_y - mean(grad_y) = 0
+    ones, gy = torch.ones(4, device="cuda"), x
+    back = flce.layer_norm_backward(gy, x, mean=values, rstd=ones, grad_weight=False, grad_bias=False)
+    assert float((back["grad_x"].double().abs().amax(1) / exact).max()) <= tol
+    back = flce.layer_norm_backward(gy, torch.ones_like(x), rstd=ones, kind="rms", grad_weight=False, grad_bias=False)
+    assert float((back["grad_x"].double().abs().amax(1) / exact).max()) <= tol
