@@ -561,6 +561,13 @@ constexpr int64_t kMaxRowVectors = 2048;
 // and 11.5 to 13.6; on bf16 [200, 1000] (25 CTAs) it would take 13.3 and takes 11.6.  (On
 // the GPU alone the second kernel is 1.6 us faster.)
 constexpr int64_t kMostAddedHere = 16, kMostColumnsHere = 1024;
+
+// Most rows of a group in one launch, where column sums are wanted: a thread adds up its
+// columns in one fp32 chain (2^21 equal rows of 4096 fp32 columns were off by 1.4e-4 of
+// the sum).  More rows than that take further launches that add to the sums, of half a
+// millisecond each.
+constexpr int64_t kRowsOfGroup = 1024;
+
 constexpr size_t kSharedByDefault = 48 * 1024 - 8192;  // with the kernel's own arrays, of a CTA that asks for no more
 
 // A launch's shape: `group` threads a row, `groups` rows a CTA, `grid` CTAs.
@@ -623,9 +630,13 @@ cudaError_t launch_rows(const LnBackward& p, const Shape& shape, cudaStream_t s)
   return cudaGetLastError();
 }
 
+// Launches the first rows of p (as many as one launch takes: p.N after it).
 template <typename T, bool RMS, bool BIAS, int VPT, int LANES, bool SHIFTED>
 cudaError_t backward_rows(LnBackward& p, int64_t vectors, cudaStream_t s) {
   const Shape shape = shape_of<T>(p, vectors, VPT, LANES, SHIFTED);
+  // a multiple of 1024, so that the next launch's first row starts at the same place of a vector
+  if (p.part_w != nullptr || p.part_b != nullptr)
+    p.N = std::min(p.N, kRowsOfGroup * shape.grid * shape.groups);
   p.parts = static_cast<int>(shape.grid);
   if constexpr (VPT <= 2) {
     if (p.word != nullptr && shape.grid <= kMostAddedHere && p.H <= kMostColumnsHere)
@@ -656,6 +667,21 @@ cudaError_t backward_rows(LnBackward& p, int64_t vectors, cudaStream_t s) {
   return backward_rows<T, RMS, BIAS, 4, 32, SHIFTED>(p, vectors, s);
 }
 
+// The call's rows from n on, which add to the sums of those before.
+template <typename T>
+LnBackward rows_from(LnBackward p, int64_t n) {
+  const auto at = [n](const void* m, int64_t ld) { return m != nullptr ? static_cast<const T*>(m) + n * ld : nullptr; };
+  p.grad_y = at(p.grad_y, p.ld_grad_y);
+  p.x = at(p.x, p.ld_x);
+  p.grad_sum = at(p.grad_sum, p.ld_grad_sum);
+  if (p.grad_x != nullptr) p.grad_x = static_cast<T*>(p.grad_x) + n * p.ld_grad_x;
+  if (p.mean != nullptr) p.mean += n;
+  p.rstd += n;
+  p.N -= n;
+  if (n > 0) p.accumulate = 1;
+  return p;
+}
+
 template <typename T, bool RMS>
 cudaError_t backward(LnBackward p, cudaStream_t s) {
   p.parts = 0;
@@ -666,16 +692,22 @@ cudaError_t backward(LnBackward p, cudaStream_t s) {
   const int64_t vectors = p.H / Vec<T>::kN;  // where rows start inside one, a few less
   cudaError_t e = cudaSuccess;
   if (p.N > 0 && fit != kFitNot && vectors <= kMaxRowVectors) {
-    prof_begin(s, FLCE_KERNEL_LN_BWD);
-    // a bias is rare without a mean and usual with one: without a mean it has a form of its own
-    if (RMS && p.part_b == nullptr)
-      e = fit == kFitWhole ? backward_rows<T, RMS, !RMS, false>(p, vectors, s)
-                           : backward_rows<T, RMS, !RMS, true>(p, vectors, s);
-    else
-      e = fit == kFitWhole ? backward_rows<T, RMS, true, false>(p, vectors, s)
-                           : backward_rows<T, RMS, true, true>(p, vectors, s);
-    prof_end(s);
-    if (e != cudaSuccess) return e;
+    for (int64_t n = 0; n < p.N;) {
+      LnBackward q = rows_from<T>(p, n);
+      prof_begin(s, FLCE_KERNEL_LN_BWD);
+      // a bias is rare without a mean and usual with one: without a mean it has a form of its own
+      if (RMS && p.part_b == nullptr)
+        e = fit == kFitWhole ? backward_rows<T, RMS, !RMS, false>(q, vectors, s)
+                             : backward_rows<T, RMS, !RMS, true>(q, vectors, s);
+      else
+        e = fit == kFitWhole ? backward_rows<T, RMS, true, false>(q, vectors, s)
+                             : backward_rows<T, RMS, true, true>(q, vectors, s);
+      prof_end(s);
+      if (e == cudaSuccess) e = reduce_columns(q, s);
+      if (e != cudaSuccess) return e;
+      n += q.N;
+    }
+    return cudaSuccess;
   } else if (p.N > 0) {
     p.word = nullptr;
     const int sms = device_sm_count();

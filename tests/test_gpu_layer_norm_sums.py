@@ -59,3 +59,46 @@ def test_row_sums_of_very_long_rows(h):
     assert float((back["grad_x"].double().abs().amax(1) / exact).max()) <= tol
     back = flce.layer_norm_backward(gy, torch.ones_like(x), rstd=ones, kind="rms", grad_weight=False, grad_bias=False)
     assert float((back["grad_x"].double().abs().amax(1) / exact).max()) <= tol
+
+
+ROWS = 1024   # of a group in one launch
+
+
+@pytest.mark.parametrize("n,h,dtype,groups", [(1 << 21, 4096, "fp32", 1), (1 << 23, 4096, "bf16", 2), (3 << 20, 8194, "bf16", 1)])
+def test_column_sums_of_very_many_rows(n, h, dtype, groups):
+    at_once = ROWS * min(304, torch.cuda.get_device_properties(0).multi_processor_count) * groups
+    chain = ROWS + groups + -(-n // at_once) + -(-304 // 32) + 10   # a thread's, the groups', the launches', the CTAs'
+    check_column_sums(n, h, dtype, chain)
+
+
+@pytest.mark.parametrize("h,first,kind", [(8200, 0, "layer"), (8201, 3, "layer"), (8208, 0, "rms")])
+def test_rows_of_several_launches(h, first, kind):
+    """A call of more rows than one launch takes is the calls of its parts, bit for bit."""
+    at_once = ROWS * min(304, torch.cuda.get_device_properties(0).multi_processor_count)
+    n = at_once + 1003
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    x, gy, gx, gx2 = (torch.empty(n * h + 8, dtype=torch.bfloat16, device="cuda")[first:first + n * h].view(n, h)
+                      for _ in range(4))
+    x.normal_(generator=gen), gy.normal_(generator=gen)
+    weight = positive(h, 5, "bf16")
+    mean = 0.1 * positive(n, 6) if kind == "layer" else None
+    rstd = positive(n, 7)
+    sums = [torch.ones(h, device="cuda") for _ in range(4)]
+
+    def backward(rows, out, at):
+        flce.layer_norm_backward(gy[rows], x[rows], weight, mean=None if mean is None else mean[rows], rstd=rstd[rows],
+                                 kind=kind, grad_sum=x[rows], grad_bias=mean is not None, out=out[rows],
+                                 grad_weight_out=sums[at], grad_bias_out=None if mean is None else sums[at + 1],
+                                 accumulate=True)
+
+    backward(slice(0, n), gx, 0)
+    backward(slice(0, at_once), gx2, 2)
+    backward(slice(at_once, n), gx2, 2)
+    assert torch.equal(gx, gx2) and torch.equal(sums[0], sums[2]) and torch.equal(sums[1], sums[3])
+    # and the rows of the second launch against the definition
+    some = slice(n - 200, n)
+    xhat = (x[some].double() - (0 if mean is None else mean[some].double()[:, None])) * rstd[some].double()[:, None]
+    u = gy[some].double() * weight.double()
+    want = u - xhat * (u * xhat).mean(1, keepdim=True) - (0 if mean is None else u.mean(1, keepdim=True))
+    want = want * rstd[some].double()[:, None] + x[some].double()
+    assert ((gx[some].double() - want).abs() <= 2.0 ** -8 * want.abs() + 1e-3).all()
