@@ -254,9 +254,9 @@ struct AdamStep {
   unsigned int key;  // of this tensor and step, for the random bits
 };
 
-// The new parameters.  The divisors are 0 or far above the subnormal numbers (the
-// root of the smallest positive fp32 is 3.7e-23), which the approximate
-// reciprocal needs; its error, a unit or two of 2^-23, is the update's alone.
+// The new parameters.  The divisors are 0 (with eps 0) or normal numbers (eps is at
+// least the smallest, and the root of the smallest positive fp32 is 3.7e-23), as the
+// approximate reciprocal needs; its error, a unit or two of 2^-23, is the update's alone.
 __device__ __forceinline__ Pair updated(const AdamNumbers& k, const AdamStep& st, Pair p, Pair m, Pair root) {
   const float2 d = unpair(fma_pair(root, pair(st.correction), pair(k.eps)));
   return fma_pair(m * pair(rcp_approx(d.x), rcp_approx(d.y)), pair(-st.rate), p * pair(st.keep));
@@ -796,7 +796,9 @@ flce_status_t adamw_step(const flce_adamw_tensor_t* tensors, int64_t count, cons
   num.c1 = static_cast<float>(1 - u.beta1);
   num.b2 = static_cast<float>(u.beta2);
   num.c2 = static_cast<float>(1 - u.beta2);
-  num.eps = static_cast<float>(u.eps);
+  // at least the smallest normal number (the reciprocal's input), far below any root that is not 0: a parameter whose
+  // moments are 0 stays where it is
+  num.eps = u.eps > 0 ? std::max(static_cast<float>(u.eps), 0x1p-126f) : 0.f;
   num.log_b1 = static_cast<float>(log(u.beta1));
   num.log_b2 = static_cast<float>(log(u.beta2));
   num.rate = static_cast<float>(1 / (1 - pow(u.beta1, t)));

@@ -177,3 +177,20 @@ def test_norm_backward_from_several_threads():
     assert [sum(c != 0 for c in one) for one in codes] == [0] * len(made) and all(len(c) == 1000 for c in codes)
     for *_, want, (gx, gw, _), _, _ in made:
         assert torch.equal(gx, want["grad_x"]) and torch.equal(gw, want["grad_weight"])
+
+
+# ------------------------------------------------------------ the smallest eps
+
+@pytest.mark.parametrize("eps", [2.0 ** -126, 1e-38, 1e-40, 1e-46, 1e-300])
+@pytest.mark.parametrize("moments", ["fp32", "8bit"])
+def test_a_parameter_without_gradients_stays_with_the_smallest_eps(moments, eps):
+    """0 / (0 + eps) is 0 for every eps above 0, those below the normal numbers of fp32 among them."""
+    p = normal(1000, 1)
+    before, g = p.clone(), normal(1000, 2)
+    g[::2] = 0
+    opt = flce.AdamW([p], lr=0.25, eps=eps, weight_decay=0.0, moments=moments, min_8bit_size=0)
+    opt.step([g])
+    assert torch.equal(p[::2], before[::2])
+    # the first step is lr * sign(gradient), off by 2^-18 of the update and a rounding of the parameter
+    want = before[1::2].double() - 0.25 * g[1::2].sign().double()
+    assert ((p[1::2].double() - want).abs() <= 0.25 * 2.0 ** -18 + 2.0 ** -23 * want.abs()).all()
