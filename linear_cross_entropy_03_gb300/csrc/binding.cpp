@@ -136,6 +136,13 @@ PyObject* tuple_of(std::initializer_list<const at::Tensor*> tensors) {
   return r;
 }
 
+// Tells autograd that tensors were written, as torch's own operations in place do: a
+// backward pass that saved what they held is then refused, and not run on other numbers.
+void written(std::initializer_list<const at::Tensor*> tensors) {
+  for (const at::Tensor* t : tensors)
+    if (t != nullptr && !t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
+}
+
 bool flag(PyObject* o) { return o != Py_None && PyObject_IsTrue(o) == 1; }
 
 // layer_norm(x, weight, bias, kind, eps, residual, out, sum_out, row_stats) -> (y, sum, mean, rstd)
@@ -183,6 +190,7 @@ PyObject* layer_norm(PyObject*, PyObject* const* a, Py_ssize_t count) {
       param != nullptr ? code_of(*param) : dtype, m.n, m.h, static_cast<float>(eps), y.data_ptr(), ld_y, sum.defined() ? sum.data_ptr() : nullptr, ld_s,
       mean.defined() ? mean.data_ptr<float>() : nullptr, rstd.defined() ? rstd.data_ptr<float>() : nullptr, stream());
   if (st != FLCE_OK) return fail(st, "ln_fwd");
+  written({out, sum_out});
   return tuple_of({&y, &sum, &mean, &rstd});
   END_HANDLE_TH_ERRORS
 }
@@ -239,6 +247,7 @@ PyObject* layer_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t count) {
       gx.defined() ? gx.data_ptr() : nullptr, ld_x, gw.defined() ? gw.data_ptr<float>() : nullptr,
       gb.defined() ? gb.data_ptr<float>() : nullptr, accumulate, scratch.data_ptr(), scratch.nbytes(), stream());
   if (st != FLCE_OK) return fail(st, "ln_bwd");
+  written({out, gw_out, gb_out});
   return tuple_of({&gx, &gw, &gb});
   END_HANDLE_TH_ERRORS
 }
@@ -302,6 +311,7 @@ PyObject* grad_norm_of(PyObject*, PyObject* const* a, Py_ssize_t count) {
       grad_norm(table.data(), static_cast<int64_t>(table.size()), static_cast<float>(scale), static_cast<float>(most),
                 static_cast<float>(eps), result.data_ptr<float>(), scratch.data_ptr(), scratch.nbytes(), stream());
   if (st != FLCE_OK) return fail(st, "grad_norm");
+  written({out});
   const at::Tensor flat = result.dim() == 1 ? result : result.view({2});
   const at::Tensor norm = flat.select(0, 0), factor = flat.select(0, 1);
   return tuple_of({&norm, &factor});
@@ -490,6 +500,13 @@ PyObject* adamw(PyObject*, PyObject* const* a, Py_ssize_t count) {
   if (!ok) return nullptr;
   const flce_status_t st = adamw_step(table, tensors, numbers, stream());
   if (st != FLCE_OK) return fail(st, "adamw_step");
+  for (Py_ssize_t i = 0; i < tensors; ++i) {
+    if (table[i].n == 0) continue;
+    for (int k = 0; k < kLists; ++k) {
+      PyObject* const o = PyList_GET_ITEM(a[9 + k], i);
+      if (o != Py_None) written({&THPVariable_Unpack(o)});
+    }
+  }
   Py_RETURN_NONE;
   END_HANDLE_TH_ERRORS
 }

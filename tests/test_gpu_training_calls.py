@@ -194,3 +194,66 @@ def test_a_parameter_without_gradients_stays_with_the_smallest_eps(moments, eps)
     # the first step is lr * sign(gradient), off by 2^-18 of the update and a rounding of the parameter
     want = before[1::2].double() - 0.25 * g[1::2].sign().double()
     assert ((p[1::2].double() - want).abs() <= 0.25 * 2.0 ** -18 + 2.0 ** -23 * want.abs()).all()
+
+
+# ------------------------------------------------------------ autograd
+
+@pytest.mark.parametrize("moments", ["fp32", "8bit"])
+def test_autograd_sees_what_a_step_changes(moments):
+    (opt, _), grads = two_alike(moments)
+    for p in opt.params:
+        p.requires_grad_(True)
+    versions = [t._version for t in tensors_of(opt)]
+    saved = [(p * p).sum() for p in opt.params]              # their backward passes need p as it is
+    opt.step([grads[0], None])
+    changed = {id(ts[0]) for ts in (opt.params, opt.exp_avg, opt.exp_avg_sq, opt.exp_avg_scale, opt.exp_avg_sq_scale,
+                                    opt.copies) if ts[0] is not None}
+    assert [t._version - v for t, v in zip(tensors_of(opt), versions)] == \
+        [int(id(t) in changed) for t in tensors_of(opt)]
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        saved[0].backward()
+    saved[1].backward()                                      # this one had no gradient
+    assert torch.equal(opt.params[1].grad, 2 * opt.params[1].detach())
+
+
+def test_autograd_sees_what_a_call_is_given_to_write():
+    n, h = 5, 64
+    x, r = normal(n * h, 1).view(n, h), normal(n * h, 2).view(n, h)
+    y, s, gx = (torch.zeros(n, h, device="cuda") for _ in range(3))
+    gw, gb, out = (torch.zeros(k, device="cuda") for k in (h, h, 2))
+    given = normal(n * h, 3).view(n, h)
+    written, read = (y, s, gx, gw, gb, out), (x, r, given)
+    before = [t._version for t in written + read]
+    normed = flce.layer_norm(x, residual=r, out=y, sum_out=s)
+    flce.layer_norm_backward(given, normed["sum"], mean=normed["mean"], rstd=normed["rstd"], out=gx,
+                             grad_weight_out=gw, grad_bias_out=gb)
+    flce.grad_norm([gx], out=out)
+    assert [t._version - v for t, v in zip(written + read, before)] == [1] * 6 + [0] * 3
+    # y in place of x, which a product had saved
+    w = torch.ones(h, device="cuda", requires_grad=True)
+    loss = (x * w).sum()
+    flce.layer_norm(x, out=x)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+
+
+def test_results_have_no_graph():
+    x = normal(320, 1).view(5, 64).requires_grad_(True)
+    w = torch.ones(64, device="cuda", requires_grad=True)
+    out = flce.layer_norm(x, w)
+    assert not out["y"].requires_grad
+    back = flce.layer_norm_backward(x, x, w, mean=out["mean"], rstd=out["rstd"])
+    assert not any(t.requires_grad for t in back.values())
+
+
+def test_tensors_of_inference_mode():
+    with torch.inference_mode():
+        p, g = normal(300, 1), normal(300, 2)
+        x = normal(320, 3).view(5, 64)
+    opt = flce.AdamW([p], lr=1e-2)
+    opt.step([g])
+    flce.layer_norm(x, out=x)
+    with torch.inference_mode():
+        opt.step([g])
+        flce.layer_norm(x, out=x)
+    assert opt.steps == 2 and p.isfinite().all()
