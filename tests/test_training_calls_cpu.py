@@ -1,5 +1,6 @@
 """What the norm and optimiser calls do with their tensors on the host: no GPU is needed."""
 import gc
+import sys
 import weakref
 
 import pytest
@@ -55,3 +56,41 @@ def test_gradients_that_make_more_launches_than_the_workspace_is_for_are_refused
     table = (flce.TensorEntry * count)(*[flce.TensorEntry(FAKE, n, dtype, 0)] * count)
     size = flce.grad_norm_workspace_size(count)
     assert flce.grad_norm_raw(table, count, 1.0, 1.0, 1e-6, FAKE, FAKE, size, 0) == INVALID
+
+
+# ------------------------------------------------------------ a build without the extension
+
+@pytest.mark.parametrize("without", ["torch", "Python.h"])
+def test_the_library_is_built_where_the_extension_cannot_be(without, monkeypatch, tmp_path):
+    """C callers need neither torch nor Python's headers."""
+    ran = []
+
+    def run(what, cmd):
+        ran.append(cmd)
+        open(cmd[cmd.index("-o") + 1], "w").close()
+        return ""
+
+    monkeypatch.setattr(_build, "_run", run)
+    monkeypatch.setattr(_build, "OUT_DIR", str(tmp_path))
+    monkeypatch.setattr(_build, "LIB", str(tmp_path / "libflce03.so"))
+    if without == "torch":
+        monkeypatch.setattr(_build.importlib.util, "find_spec", lambda name: None)
+        monkeypatch.setitem(sys.modules, "torch", None)      # `import torch` raises
+    else:
+        monkeypatch.setattr(_build.sysconfig, "get_paths", lambda: {"include": str(tmp_path)})
+    assert not _build.up_to_date()
+    with pytest.warns(UserWarning, match="only the library"):
+        assert _build.build() == _build.LIB
+    assert (tmp_path / "libflce03.so").exists() and not any("binding" in part for cmd in ran for part in cmd)
+    assert _build.up_to_date()
+    del ran[:]
+    assert _build.build() == _build.LIB and ran == []        # and not again
+
+
+def test_a_build_that_fails_raises(monkeypatch, tmp_path):
+    monkeypatch.setattr(_build, "OUT_DIR", str(tmp_path))
+    monkeypatch.setattr(_build, "LIB", str(tmp_path / "libflce03.so"))
+    monkeypatch.setattr(_build, "_nvcc", lambda: sys.executable)
+    monkeypatch.setenv("CXX", sys.executable)
+    with pytest.raises(RuntimeError, match="failed"):
+        _build.build()
