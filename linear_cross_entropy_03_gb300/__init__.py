@@ -368,7 +368,6 @@ def cross_entropy(logits, target, *, ignore_index: int = -100, reduction="mean",
     return dict(loss=loss if red == 0 else loss[0], grad_logits=grad, status=status)
 
 
-from . import _build  # noqa: E402,F401
 from ._training import (  # noqa: E402  (it uses the names above)
     ADAMW_BLOCK, NORM_KINDS, AdamW, AdamWEntry, AdamWNumbers, TensorEntry, adamw_step, grad_norm, grad_norm_raw,
     grad_norm_workspace_size, layer_norm, layer_norm_backward, ln_bwd, ln_fwd, ln_workspace_size)

@@ -22,7 +22,7 @@ import importlib.util
 import math
 import os
 
-from . import FlceError, _build, _dt, _ptr, _stream, lib
+from . import FlceError, _dt, _ptr, _stream, lib
 
 NORM_KINDS = {"layer": 0, "rms": 1}
 ADAMW_BLOCK = 256
@@ -101,6 +101,7 @@ def _native():
     """The extension that checks tensors and calls the library; raises if it has not been built."""
     global _binding
     if _binding is None:
+        from . import _build
         lib()
         path = _build.binding_path()
         if not os.path.exists(path):

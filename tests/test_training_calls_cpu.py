@@ -1,5 +1,6 @@
 """What the norm and optimiser calls do with their tensors on the host: no GPU is needed."""
 import gc
+import subprocess
 import sys
 import weakref
 
@@ -94,3 +95,10 @@ def test_a_build_that_fails_raises(monkeypatch, tmp_path):
     monkeypatch.setenv("CXX", sys.executable)
     with pytest.raises(RuntimeError, match="failed"):
         _build.build()
+
+
+def test_the_build_runs_as_a_program():
+    """As the README has it, without a warning."""
+    r = subprocess.run([sys.executable, "-W", "error::RuntimeWarning", "-m", _build.__name__], capture_output=True,
+                       text=True, cwd=_build.ROOT)
+    assert r.returncode == 0 and r.stdout.strip() == _build.LIB, r.stderr
