@@ -10,9 +10,9 @@ written on another stream has to be waited for by the caller.
 
 None of the calls records anything for autograd: their results have no graph, also
 where their inputs require gradients, and ``layer_norm_backward`` is called by
-the program that wants them.  What a call writes (``out`` and the like, and the
-tensors of an optimiser) counts as changed in place, so a graph that had saved it
-refuses its backward pass.
+the program that wants them.  What a call writes (``out`` and the like, an
+optimiser's parameters and copies) counts as changed in place, so a graph that
+had saved it refuses its backward pass.
 """
 from __future__ import annotations
 

@@ -206,8 +206,7 @@ def test_autograd_sees_what_a_step_changes(moments):
     versions = [t._version for t in tensors_of(opt)]
     saved = [(p * p).sum() for p in opt.params]              # their backward passes need p as it is
     opt.step([grads[0], None])
-    changed = {id(ts[0]) for ts in (opt.params, opt.exp_avg, opt.exp_avg_sq, opt.exp_avg_scale, opt.exp_avg_sq_scale,
-                                    opt.copies) if ts[0] is not None}
+    changed = {id(opt.params[0]), id(opt.copies[0])}         # and the moments, which are in no graph
     assert [t._version - v for t, v in zip(tensors_of(opt), versions)] == \
         [int(id(t) in changed) for t in tensors_of(opt)]
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
