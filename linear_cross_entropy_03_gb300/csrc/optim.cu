@@ -47,7 +47,7 @@ struct NormEntry {
   int dtype;
 };
 
-constexpr int kNormEntries = 1280, kNormMiddle = 320, kNormFew = 16;
+constexpr int kNormEntries = 1280, kNormFew = 320;
 template <int MAX>
 struct NormArgs {
   NormEntry entry[MAX];
@@ -580,7 +580,11 @@ __device__ __forceinline__ void step_chunk(const AdamEntry& e, const AdamNumbers
 }
 
 // Tensors with 8-bit moments.  What the arithmetic issues bounds this as closely as
-// memory does, so the usual types have code of their own.  Eight CTAs on an SM: 525M
+// memory does, so fp32 parameters, the master weights that such moments go with, have
+// code of their own for the gradients that FLCE (fp32) and a 16-bit model (bf16) leave:
+// 268M elements with a 16-bit copy, to nearest, take 716 and 621 us so and 774 and 739 by
+// the code for any types.  By that, fp16 gradients take 747 us and bf16 parameters and
+// gradients 663 (741 and 660 if the kernel has no other code).  Eight CTAs on an SM: 525M
 // elements with a 16-bit copy took 1.36 ms so (7.0 TB/s), 1.43 with seven, 1.48 with
 // six, 1.59 with five (the 90 registers it would take by itself).
 template <int MAX, bool STOCHASTIC>
@@ -636,21 +640,24 @@ cudaError_t launch_adamw(const AdamEntry* entry, int count, unsigned int chunks,
   return e;
 }
 
-// Tables of a few sizes: a launch copies its whole parameter block.
-constexpr int kAdamEntries = 360, kAdamMore = 128, kAdamMiddle = 40, kAdamFew = 4;
+// Tables of a few sizes, the largest what kernel parameters hold and each other a third
+// or a quarter of the next: a launch copies its whole parameter block, 32 KB of it in a
+// microsecond.  Steps of small tensors, the C call alone: 100 of them 4.4 us from the
+// table of 128 and 5.4 from that of 360, 16 of them 4.2 from the table of 40 and 4.5; the
+// norm of 100 gradients 5.9 us from the table of 320 and 7.0 from that of 1280.  Smaller
+// tables still gained nothing (4 entries 4.14 against 4.15, 16 of the norm's 6.22 and 6.26).
+constexpr int kAdamEntries = 360, kAdamMore = 128, kAdamFew = 40;
 static_assert(sizeof(AdamArgs<kAdamEntries>) <= 32764, "kernel parameters");
 static_assert(sizeof(NormArgs<kNormEntries>) <= 32764, "kernel parameters");
 
 cudaError_t launch_norm_any(const NormEntry* entry, const NormArgs<1>& rest, int grid, cudaStream_t s) {
   if (rest.count <= kNormFew) return launch_norm<kNormFew>(entry, rest, grid, s);
-  if (rest.count <= kNormMiddle) return launch_norm<kNormMiddle>(entry, rest, grid, s);
   return launch_norm<kNormEntries>(entry, rest, grid, s);
 }
 
 cudaError_t launch_adamw_any(const AdamEntry* entry, int count, unsigned int chunks, const AdamNumbers& num, int bits,
                              cudaStream_t s) {
   if (count <= kAdamFew) return launch_adamw<kAdamFew>(entry, count, chunks, num, bits, s);
-  if (count <= kAdamMiddle) return launch_adamw<kAdamMiddle>(entry, count, chunks, num, bits, s);
   if (count <= kAdamMore) return launch_adamw<kAdamMore>(entry, count, chunks, num, bits, s);
   return launch_adamw<kAdamEntries>(entry, count, chunks, num, bits, s);
 }
