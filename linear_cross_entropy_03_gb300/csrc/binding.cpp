@@ -475,8 +475,11 @@ PyObject* adamw(PyObject*, PyObject* const* a, Py_ssize_t count) {
   auto* sizes = static_cast<int64_t*>(PyLong_AsVoidPtr(a[1]));
   const Py_ssize_t tensors = PyLong_AsSsize_t(a[2]);
   auto* numbers = static_cast<flce_adamw_t*>(PyLong_AsVoidPtr(a[3]));
-  if (PyErr_Occurred() || !lists_ok(a + 9, tensors)) return nullptr;
-  if (!table_holds(a + 9, tensors, table, sizes) && !fill_table(a + 9, tensors, table, sizes)) return nullptr;
+  if (PyErr_Occurred()) return nullptr;
+  const Members grads(a[4]);  // before the rest is looked at: an iterator may move anything
+  if (!grads.ok()) return nullptr;
+  if (grads.size() != tensors)
+    return fail(FLCE_ERR_INVALID_ARG, "AdamW.step: %zd gradients for %zd tensors", grads.size(), tensors);
   int on = -1;
   double factor = 1;
   if (!number_of(a[5], "AdamW.step: lr", &on, &numbers->lr, &numbers->lr_dev)) return nullptr;
@@ -487,10 +490,8 @@ PyObject* adamw(PyObject*, PyObject* const* a, Py_ssize_t count) {
   numbers->skip_nonfinite = flag(a[7]);
   numbers->step = PyLong_AsLongLong(a[8]);
   if (PyErr_Occurred()) return nullptr;
-  const Members grads(a[4]);
-  if (!grads.ok()) return nullptr;
-  if (grads.size() != tensors)
-    return fail(FLCE_ERR_INVALID_ARG, "AdamW.step: %zd gradients for %zd tensors", grads.size(), tensors);
+  if (!lists_ok(a + 9, tensors)) return nullptr;
+  if (!table_holds(a + 9, tensors, table, sizes) && !fill_table(a + 9, tensors, table, sizes)) return nullptr;
   const bool ok = grads.for_each("AdamW.step", [&](Py_ssize_t i, const at::Tensor* t) {
     flce_adamw_tensor_t& e = table[i];
     e.n = 0;

@@ -92,6 +92,20 @@ def test_step_follows_other_tensors_in_its_lists(moments):
     assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(before, kept))
 
 
+def test_step_follows_tensors_that_the_gradients_iterator_moves():
+    (opt, still), grads = two_alike("fp32")
+    old = [t.detach() for t in tensors_of(opt)]
+    kept = [t.clone() for t in old]
+
+    def moves():
+        for t in tensors_of(opt):
+            t.data = t.data.clone()
+        yield from grads
+
+    opt.step(moves()), still.step(grads)
+    assert equal(opt, still) and all(torch.equal(a, b) for a, b in zip(old, kept))
+
+
 def test_step_follows_a_parameter_of_another_type():
     (opt, still), grads = two_alike("fp32")
     first = opt.params[0]
