@@ -376,10 +376,10 @@ flce_status_t ce_fwd_bwd_noalloc(const void* logits, int dtype, void* grad_logit
  *
  * Matrices here are rows of H contiguous elements, `ld` elements apart: for an
  * input any ld >= 0 (0 repeats one row), for an output ld >= H, at most 2^29.
- * Pointers need
- * the alignment of their elements only; 16-byte aligned rows (pointer and ld)
- * are the fast case.  Except where said, buffers do not overlap.  An infinity
- * or NaN spoils its own row (and the column sums), no other.
+ * Pointers need the alignment of their elements only; 16-byte aligned rows
+ * (pointer and ld) are the fast case.  Except where said, buffers do not
+ * overlap.  An infinity or NaN spoils its own row (and the column sums), no
+ * other, and so does an element above 1.8e19 in size, whose square is infinite.
  */
 typedef enum {
   FLCE_NORM_LAYER = 0, /* mean and variance                     */
@@ -425,8 +425,9 @@ size_t ln_workspace_size(int64_t N, int64_t H);
  *                on entry are ignored.
  *
  * grad_x may be grad_y, grad_sum or x itself (same pointer and ld; with ld at
- * least H).  The sums over rows run in an order that the sizes fix: the results
- * are the same from run to run.
+ * least H).  The sums over rows run in an order that the sizes and the layout
+ * fix: the results are the same from run to run.  Their chains of fp32 additions
+ * stay short: a call of very many rows makes several launches.
  */
 flce_status_t ln_bwd(int kind, int dtype, const void* grad_y, int64_t ld_grad_y, const void* x,
                      int64_t ld_x, const void* weight, int param_dtype, const float* mean,
@@ -544,12 +545,13 @@ typedef struct {
  * 8-bit moments: each block of FLCE_ADAMW_BLOCK elements (counted from the
  * tensor's start) has scale = its largest |m| (or sqrt v) * (1 / 448), at least
  * 2^-126 unless the block is 0, and holds m * (1 / scale) (or sqrt v) as e4m3
- * numbers, each of these operations rounded to fp32.  A root that is not 0 is held as at least the smallest number,
- * 2^-9, so that no step divides a moment by a root that was rounded to 0.  A
- * moment that is not finite is held as NaN and leaves the rest of its block
- * alone.
+ * numbers, each of these operations rounded to fp32.  A root that is not 0 is
+ * held as at least the smallest number, 2^-9, so that no step divides a moment
+ * by a root that was rounded to 0.  A moment that is not finite is held as NaN
+ * and leaves the rest of its block alone.
  *
- * betas in [0, 1), eps >= 0, lr finite.  Needs no workspace.
+ * betas in [0, 1), eps >= 0 (above 0, one below 2^-126 counts as 2^-126), lr
+ * finite.  Needs no workspace.
  */
 flce_status_t adamw_step(const flce_adamw_tensor_t* tensors, int64_t count,
                          const flce_adamw_t* numbers, flce_stream_t stream);

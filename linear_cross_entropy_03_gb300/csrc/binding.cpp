@@ -187,8 +187,9 @@ PyObject* layer_norm(PyObject*, PyObject* const* a, Py_ssize_t count) {
   const at::Tensor* param = w != nullptr ? w : b;
   const flce_status_t st = ln_fwd(
       static_cast<int>(kind), dtype, data(x), m.ld, data(r), ld_r, data(w), data(b),
-      param != nullptr ? code_of(*param) : dtype, m.n, m.h, static_cast<float>(eps), y.data_ptr(), ld_y, sum.defined() ? sum.data_ptr() : nullptr, ld_s,
-      mean.defined() ? mean.data_ptr<float>() : nullptr, rstd.defined() ? rstd.data_ptr<float>() : nullptr, stream());
+      param != nullptr ? code_of(*param) : dtype, m.n, m.h, static_cast<float>(eps), y.data_ptr(), ld_y,
+      sum.defined() ? sum.data_ptr() : nullptr, ld_s, mean.defined() ? mean.data_ptr<float>() : nullptr,
+      rstd.defined() ? rstd.data_ptr<float>() : nullptr, stream());
   if (st != FLCE_OK) return fail(st, "ln_fwd");
   written({out, sum_out});
   return tuple_of({&y, &sum, &mean, &rstd});
@@ -466,8 +467,8 @@ bool number_of(PyObject* o, const char* where, int* device, double* value, const
 
 // adamw(table, sizes, count, numbers, grads, lr, grad_scale, skip_nonfinite, step, params, exp_avg, exp_avg_sq,
 // exp_avg_scale, exp_avg_sq_scale, copies): fills the table of flce_adamw_tensor_t at address `table` again if the
-// tensors of the lists are no longer those in it, fills in the gradients (an element count of 0 where there is none) and
-// the step's numbers (the flce_adamw_t at `numbers`), and takes the step.
+// tensors of the lists are no longer those in it, fills in the gradients (an element count of 0 where there is none)
+// and the step's numbers (the flce_adamw_t at `numbers`), and takes the step.
 PyObject* adamw(PyObject*, PyObject* const* a, Py_ssize_t count) {
   HANDLE_TH_ERRORS
   if (count != 9 + kLists) return fail(FLCE_ERR_INVALID_ARG, "AdamW.step: arguments");

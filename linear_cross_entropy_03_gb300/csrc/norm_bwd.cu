@@ -426,6 +426,11 @@ __global__ void __maxnreg__((VPT > 2 || (sizeof(T) == 2 && (BIAS || SHIFTED)) ? 
 
 // ------------------------------------------------------- any layout, by elements
 
+// The form for rows that vectors do not fit: grad_y and x are read twice, element by
+// element, which is what its time goes to.  fp32 [4096, 16384] takes 364 us (floor 121),
+// bf16 [2048, 32768] 291 (60), fp16 [8191, 2047] at different places of a vector 76 (15),
+// bf16 [65536, 33] 93 (2).
+
 // The two row means of the backward pass, one CTA a row.
 template <typename T, bool RMS>
 __global__ void __launch_bounds__(kAnyThreads) ln_bwd_rows_any_kernel(const LnBackward p) {
@@ -563,9 +568,9 @@ constexpr int64_t kMaxRowVectors = 2048;
 constexpr int64_t kMostAddedHere = 16, kMostColumnsHere = 1024;
 
 // Most rows of a group in one launch, where column sums are wanted: a thread adds up its
-// columns in one fp32 chain (2^21 equal rows of 4096 fp32 columns were off by 1.4e-4 of
+// columns in one fp32 chain (3 * 2^20 equal rows of 8194 bf16 columns were off by 3e-4 of
 // the sum).  More rows than that take further launches that add to the sums, of half a
-// millisecond each.
+// millisecond or more each: bf16 [400000, 4096] 1492 us in one, 1504 in two.
 constexpr int64_t kRowsOfGroup = 1024;
 
 constexpr size_t kSharedByDefault = 48 * 1024 - 8192;  // with the kernel's own arrays, of a CTA that asks for no more

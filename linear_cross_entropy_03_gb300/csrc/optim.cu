@@ -508,7 +508,8 @@ __device__ __forceinline__ bool step_numbers(const AdamEntry& e, const AdamNumbe
 // copy take 1.13 ms, 7.0 TB/s, as fast as a plain copy.  A thread takes four elements
 // of every array at a time, four times; 32 registers let every SM hold 64 warps, whose
 // loads cover the latency without looking ahead.  What is left at a tensor's ends goes
-// one by one.
+// one by one, and so does all of a tensor whose arrays lie at different boundaries: 134M
+// elements with bf16 gradients 758 us instead of 543 (8-bit moments 827 instead of 312).
 template <int MAX>
 __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ AdamArgs<MAX> a) {
   const AdamEntry& e = a.entry[entry_of(a.entry, a.count, blockIdx.x)];

@@ -64,7 +64,8 @@ def test_row_sums_of_very_long_rows(h):
 ROWS = 1024   # of a group in one launch
 
 
-@pytest.mark.parametrize("n,h,dtype,groups", [(1 << 21, 4096, "fp32", 1), (1 << 23, 4096, "bf16", 2), (3 << 20, 8194, "bf16", 1)])
+@pytest.mark.parametrize("n,h,dtype,groups", [(1 << 21, 4096, "fp32", 1), (1 << 23, 4096, "bf16", 2),
+                                              (3 << 20, 8194, "bf16", 1)])
 def test_column_sums_of_very_many_rows(n, h, dtype, groups):
     at_once = ROWS * min(304, torch.cuda.get_device_properties(0).multi_processor_count) * groups
     chain = ROWS + groups + -(-n // at_once) + -(-304 // 32) + 10   # a thread's, the groups', the launches', the CTAs'
