@@ -34,6 +34,15 @@
  *  grad_norm, adamw_step  The norm of all gradients and one AdamW step over
  *                many tensors, with moments in fp32 or in 8 bits.
  *
+ *  policy_fwd_bwd, preference_fwd_bwd, distill_fwd_bwd  The losses of
+ *                post-training on materialised logits, each with its gradient:
+ *                the clipped policy loss with a KL term, the loss over pairs of
+ *                sequences, and the distance from a teacher's top logits.
+ *
+ *  embedding_fwd, embedding_bwd  Rows of a table by token, and the table's
+ *                gradient, which may be added to the head's where both share
+ *                one weight.
+ *
  * Conventions shared by every entry point
  * ---------------------------------------
  *  - Every tensor pointer is a DEVICE pointer to memory the caller owns.  The
@@ -97,6 +106,7 @@ typedef enum {
 /* Bits of the device status word. */
 #define FLCE_STATUS_BIT_TARGET_RANGE 0x1
 #define FLCE_STATUS_BIT_TIMEOUT 0x2
+#define FLCE_STATUS_BIT_SEQUENCE_RANGE 0x4
 
 /* Human-readable name of a status code (static storage, never NULL). */
 const char* flce_status_string(flce_status_t status);
@@ -557,6 +567,216 @@ flce_status_t adamw_step(const flce_adamw_tensor_t* tensors, int64_t count,
                          const flce_adamw_t* numbers, flce_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * Losses of post-training on materialised logits
+ * ------------------------------------------------------------------------
+ * Each takes logits [N, V], rows of V contiguous elements `ld` elements apart,
+ * and gives the loss and, unless grad_logits is NULL, its gradient on them.
+ * With p = softmax(z) of a row z:
+ *
+ *  dtype         type of logits and grad_logits: FLCE_DTYPE_BF16, _FP16, _FP32.
+ *  ld, ld_grad   >= V; N times either at most 2^58.
+ *  grad_logits   [N, V] output, rows ld_grad apart; may be logits itself (with
+ *                the same ld: the logits are consumed), else it overlaps nothing.
+ *                What lies between two rows is not written.
+ *  N, V          rows (>= 0, < 2^31) and columns (1 to 2^31 - 1).
+ *  ignore_index  rows whose target it is take no part: loss 0, gradient 0.
+ *  reduction     flce_reduction_t.
+ *  grad_scale    multiplies every gradient; grad_out_none, fp32 of the losses'
+ *                size or NULL, too, loss by loss (reduction NONE only).
+ *  loss          fp32 output: one element for SUM and MEAN.
+ *  workspace     256-byte aligned, of at least the stated size; contents on
+ *                entry are ignored.
+ *  status_dev    device status word, or NULL: then the workspace's first word
+ *                holds this call's bits when it is done.
+ *
+ * Pointers need the alignment of their elements only.  Rows (pointer and ld)
+ * that lie equally far from a 16-byte boundary in logits and grad_logits are the
+ * fast case.  Arithmetic is fp32, with one rounding to the gradient's type; sums
+ * over rows are fp64 in a fixed order: the results are the same from run to run.
+ * Logits of -inf are columns of probability 0.  A row with NaN or +inf, or of
+ * -inf alone, has a loss and gradients of NaN, and no other row has.  A row
+ * that takes no part, or whose weight is 0, gets zeros whatever it holds.
+ */
+
+/*
+ * The numbers of a policy loss.
+ *  clip_low, clip_high  >= 0; the ratio is cut to [1 - clip_low, 1 + clip_high];
+ *                       infinity: not cut on that side.
+ *  kl_weight            finite, >= 0.
+ *  temperature          > 0, finite: what the logits were divided by to sample.
+ */
+typedef struct {
+  float clip_low, clip_high;
+  float kl_weight;
+  float temperature;
+} flce_policy_t;
+
+/* Bytes of workspace policy_fwd_bwd and distill_fwd_bwd need for N rows; 0 for
+ * invalid sizes. */
+size_t row_loss_workspace_size(int64_t N);
+
+/*
+ * policy_fwd_bwd -- the clipped policy loss of sampled tokens with a KL term:
+ *     logp  = z_t / T - logsumexp(z / T),   t the row's target
+ *     ratio = exp(logp - old_logp),   A the row's advantage
+ *     loss  = row_weight * ( -min(ratio A, clip(ratio) A)
+ *                            + kl_weight (exp(d) - 1 - d) ),  d = ref_logp - logp
+ *  MEAN divides by the number of rows that take part (NaN if there is none),
+ *  whatever their weights.  Where the cut ratio is taken the first term has no
+ *  gradient.
+ *
+ *  target        int64 [N]; one outside [0, V) that is not ignore_index sets
+ *                FLCE_STATUS_BIT_TARGET_RANGE, and its row takes no part.
+ *  advantage     fp32 [N].
+ *  old_logp      fp32 [N], or NULL: the ratio is 1 and its gradient that of
+ *                logp (the first update on fresh samples).
+ *  ref_logp      fp32 [N], or NULL where kl_weight is 0.
+ *  row_weight    fp32 [N], or NULL (1).
+ *  loss          [N] for NONE.
+ *  logp          fp32 [N] output or NULL; 0 for rows that take no part.
+ */
+flce_status_t policy_fwd_bwd(const void* logits, int dtype, int64_t ld, void* grad_logits,
+                             int64_t ld_grad, const int64_t* target, const float* advantage,
+                             const float* old_logp, const float* ref_logp, const float* row_weight,
+                             int64_t N, int64_t V, const flce_policy_t* numbers,
+                             int64_t ignore_index, int reduction, float grad_scale,
+                             const float* grad_out_none, float* loss, float* logp,
+                             void* workspace, size_t workspace_bytes, int32_t* status_dev,
+                             flce_stream_t stream);
+
+/* Largest length of a teacher's list. */
+#define FLCE_DISTILL_MAX_TOP 1024
+
+/* Types of ids. */
+typedef enum { FLCE_INDEX_INT64 = 0, FLCE_INDEX_INT32 = 1 } flce_index_t;
+
+/*
+ * distill_fwd_bwd -- the distance from a teacher of which each row has the
+ * largest logits:
+ *     q    = softmax(values / T) over the row's list
+ *     loss = row_weight * T^2 * sum_k q_k (ln q_k - ln p_k),   p = softmax(z / T)
+ *  MEAN divides by the number of rows that have a list (NaN if there is none).
+ *
+ *  ids           [N, top] of index_type (flce_index_t): the list's columns, up to
+ *                the first negative one.  A row whose first id is negative takes
+ *                no part.  One of V or above sets FLCE_STATUS_BIT_TARGET_RANGE and
+ *                is left out; a column that is named twice has both shares.
+ *  values        [N, top] of value_dtype (any of the three types): the teacher's
+ *                logits or log-probabilities.  -inf: no share; a list of -inf alone
+ *                gives loss 0 and gradient 0.
+ *  top           1 to FLCE_DISTILL_MAX_TOP.
+ *  temperature   > 0, finite.
+ *  row_weight    fp32 [N], or NULL (1).
+ *  loss          [N] for NONE.
+ */
+flce_status_t distill_fwd_bwd(const void* logits, int dtype, int64_t ld, void* grad_logits,
+                              int64_t ld_grad, const void* ids, int index_type,
+                              const void* values, int value_dtype, int64_t top,
+                              const float* row_weight, int64_t N, int64_t V, float temperature,
+                              int reduction, float grad_scale, const float* grad_out_none,
+                              float* loss, void* workspace, size_t workspace_bytes,
+                              int32_t* status_dev, flce_stream_t stream);
+
+typedef enum {
+  FLCE_PREFERENCE_SIGMOID = 0,
+  FLCE_PREFERENCE_HINGE = 1,
+  FLCE_PREFERENCE_IPO = 2
+} flce_preference_kind_t;
+
+/*
+ * The numbers of a preference loss.
+ *  kind             flce_preference_kind_t.
+ *  average          1: a sequence's log-probability is the mean over its tokens
+ *                   that take part (0 without any), 0: their sum.
+ *  beta             > 0, finite.
+ *  label_smoothing  in [0, 1); SIGMOID only, else 0.
+ *  margin           finite; SIGMOID and HINGE only, else 0.
+ */
+typedef struct {
+  int32_t kind, average;
+  float beta, label_smoothing, margin;
+} flce_preference_t;
+
+/* Bytes of workspace preference_fwd_bwd needs; 0 for invalid sizes. */
+size_t preference_workspace_size(int64_t N, int64_t pairs);
+
+/*
+ * preference_fwd_bwd -- a loss over `pairs` pairs of sequences, the chosen one of
+ * pair i being sequence i and the rejected one sequence pairs + i, by
+ *     s_q = sum (or mean) of z_t - logsumexp(z) over the sequence's tokens
+ *     x   = (s_chosen - ref_chosen) - (s_rejected - ref_rejected),  u = beta x - margin
+ *     SIGMOID  -(1 - label_smoothing) ln sigmoid(u) - label_smoothing ln sigmoid(-u)
+ *     HINGE    max(0, 1 - u)
+ *     IPO      (x - 1 / (2 beta))^2
+ *  MEAN divides by `pairs` (NaN if 0).
+ *
+ *  target        int64 [N], as in policy_fwd_bwd.
+ *  offsets       int64 [2 pairs + 1], device, rising: sequence q has the rows
+ *                from offsets[q] up to offsets[q + 1]; NULL: 2 pairs sequences of
+ *                one length.  Rows of no sequence get gradients of 0.  Offsets
+ *                that fall or leave [0, N] set FLCE_STATUS_BIT_SEQUENCE_RANGE, and
+ *                sequences are then cut to what lies within.
+ *  ref_logp      fp32 [2 pairs]: the reference model's s, or NULL (0).
+ *  pairs         >= 0, < 2^30.
+ *  loss          [pairs] for NONE.
+ *  logp          fp32 [2 pairs] output or NULL: s.
+ */
+flce_status_t preference_fwd_bwd(const void* logits, int dtype, int64_t ld, void* grad_logits,
+                                 int64_t ld_grad, const int64_t* target, const int64_t* offsets,
+                                 const float* ref_logp, int64_t pairs, int64_t N, int64_t V,
+                                 const flce_preference_t* numbers, int64_t ignore_index,
+                                 int reduction, float grad_scale, const float* grad_out_none,
+                                 float* loss, float* logp, void* workspace,
+                                 size_t workspace_bytes, int32_t* status_dev,
+                                 flce_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The table at the model's other end
+ * ------------------------------------------------------------------------ */
+
+/*
+ * embedding_fwd -- y[n] = table[ids[n]] * scale, rounded once.
+ *
+ *  dtype         type of table and y: FLCE_DTYPE_BF16, _FP16 or _FP32.
+ *  table         [V, H], rows ld_table (>= H) apart.
+ *  ids           [N] of index_type (flce_index_t).  One outside [0, V) gives a
+ *                row of zeros and sets FLCE_STATUS_BIT_TARGET_RANGE.
+ *  N, V, H       N >= 0 (< 2^31), V 1 to 2^31 - 1, H 1 to 2^24 - 1.
+ *  y             [N, H] output, rows ld_y (>= H) apart.
+ *  status_dev    device status word, or NULL (not reported).
+ */
+flce_status_t embedding_fwd(int dtype, const void* table, int64_t ld_table, const void* ids,
+                            int index_type, int64_t N, int64_t V, int64_t H, float scale, void* y,
+                            int64_t ld_y, int32_t* status_dev, flce_stream_t stream);
+
+/* Bytes of workspace embedding_bwd needs; 0 for invalid sizes. */
+size_t embedding_workspace_size(int64_t N, int64_t V, int64_t H);
+
+/*
+ * embedding_bwd -- the table's gradient:
+ *     grad_table[v] = scale * sum of grad_y[n] over the tokens n with ids[n] = v
+ *
+ *  dtype          type of grad_y [N, H], rows ld_grad_y (>= 0) apart.
+ *  N, V, H        N < 2^31 - 32, V < 2^31 - 1, H < 2^21.
+ *  padding_index  tokens of this id add nothing; -1: none.
+ *  grad_table     fp32 [V, H], contiguous.
+ *  accumulate     0: every row is written (zeros where no token is); 1: added to,
+ *                 and rows of no token are not touched (a shared weight's
+ *                 gradient, as flce_fwd_bwd left it).
+ *  workspace      >= embedding_workspace_size(...) bytes, 256-byte aligned;
+ *                 contents on entry are ignored.
+ *  status_dev     device status word, or NULL (not reported).
+ *
+ * An id outside [0, V) adds nothing and sets FLCE_STATUS_BIT_TARGET_RANGE.  Sums
+ * are fp32 in an order that the ids and sizes fix: the same from run to run.
+ */
+flce_status_t embedding_bwd(int dtype, const void* grad_y, int64_t ld_grad_y, const void* ids,
+                            int index_type, int64_t N, int64_t V, int64_t H, float scale,
+                            int64_t padding_index, float* grad_table, int accumulate,
+                            void* workspace, size_t workspace_bytes, int32_t* status_dev,
+                            flce_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * Diagnostics (no counterpart on the pages)
  * ------------------------------------------------------------------------ */
 
@@ -590,7 +810,15 @@ enum {
   FLCE_KERNEL_LN_BWD = 11,
   FLCE_KERNEL_LN_REDUCE = 12,
   FLCE_KERNEL_GRAD_NORM = 13,
-  FLCE_KERNEL_ADAMW = 14
+  FLCE_KERNEL_ADAMW = 14,
+  FLCE_KERNEL_ROW_LOSS = 15,   /* policy, distill, and the row statistics of a preference loss */
+  FLCE_KERNEL_ROW_COUNT = 16,
+  FLCE_KERNEL_PAIR_LOSS = 17,
+  FLCE_KERNEL_ROW_GRAD = 18,
+  FLCE_KERNEL_EMBEDDING = 19,
+  FLCE_KERNEL_TOKEN_SORT = 20,
+  FLCE_KERNEL_EMBEDDING_BWD = 21,
+  FLCE_KERNEL_EMBEDDING_JOIN = 22
 };
 const char* flce_kernel_name(int kernel_id);
 flce_status_t flce_profile_enable(int capacity);

@@ -8,7 +8,10 @@ add output / workspace allocation with torch and raise on an error status.
 Every step of the computation runs in the library's CUDA kernels; there is
 no fallback.  If the library has not been built, every call raises.
 ``layer_norm``, ``layer_norm_backward``, ``grad_norm`` and ``AdamW`` are what a
-training step runs around the loss (``_training.py``).
+training step runs around the loss (``_training.py``); ``policy_loss``,
+``preference_loss``, ``distillation_loss``, ``embedding`` and
+``embedding_backward`` are post-training's losses and the table at the model's
+other end (``_losses.py``).
 """
 from __future__ import annotations
 
@@ -27,15 +30,21 @@ __all__ = [
     "NORM_KINDS", "ADAMW_BLOCK", "TensorEntry", "AdamWEntry", "AdamWNumbers", "ln_workspace_size", "ln_fwd", "ln_bwd",
     "grad_norm_workspace_size", "grad_norm_raw", "adamw_step", "layer_norm", "layer_norm_backward", "grad_norm",
     "AdamW",
+    "PREFERENCE_KINDS", "INDEX_TYPES", "STATUS_BIT_SEQUENCE_RANGE", "PolicyNumbers", "PreferenceNumbers",
+    "row_loss_workspace_size", "preference_workspace_size", "embedding_workspace_size", "policy_fwd_bwd",
+    "preference_fwd_bwd", "distill_fwd_bwd", "embedding_fwd", "embedding_bwd", "policy_loss", "preference_loss",
+    "distillation_loss", "embedding", "embedding_backward",
 ]
 
 REDUCTIONS = {"none": 0, "sum": 1, "mean": 2}
 DTYPES = {"bf16": 0, "fp32": 1, "fp16": 2, "fp32_rounded": 3}
 STATUS_BIT_TARGET_RANGE = 0x1
 STATUS_BIT_TIMEOUT = 0x2
+STATUS_BIT_SEQUENCE_RANGE = 0x4
 KERNEL_NAMES = ("count_targets", "gemm_forward", "row_finalize", "grad_logits", "gemm_backward",
                 "loss_reduce", "ce_rows", "zero", "bias_reduce", "gh_reduce", "ln_fwd", "ln_bwd", "ln_reduce",
-                "grad_norm", "adamw")
+                "grad_norm", "adamw", "row_loss", "row_count", "pair_loss", "row_grad", "embedding", "token_sort",
+                "embedding_bwd", "embedding_join")
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "_lib", "libflce03.so")
@@ -76,6 +85,20 @@ _SIGNATURES = {
     "grad_norm_workspace_size": (_SZ, [_I64]),
     "grad_norm": (ctypes.c_int, [_P, _I64, ctypes.c_float, ctypes.c_float, ctypes.c_float, _P, _P, _SZ, _P]),
     "adamw_step": (ctypes.c_int, [_P, _I64, _P, _P]),
+    "row_loss_workspace_size": (_SZ, [_I64]),
+    "policy_fwd_bwd": (ctypes.c_int, [_P, ctypes.c_int, _I64, _P, _I64, _P, _P, _P, _P, _P, _I64, _I64, _P, _I64,
+                                      ctypes.c_int, ctypes.c_float, _P, _P, _P, _P, _SZ, _P, _P]),
+    "preference_workspace_size": (_SZ, [_I64, _I64]),
+    "preference_fwd_bwd": (ctypes.c_int, [_P, ctypes.c_int, _I64, _P, _I64, _P, _P, _P, _I64, _I64, _I64, _P, _I64,
+                                          ctypes.c_int, ctypes.c_float, _P, _P, _P, _P, _SZ, _P, _P]),
+    "distill_fwd_bwd": (ctypes.c_int, [_P, ctypes.c_int, _I64, _P, _I64, _P, ctypes.c_int, _P, ctypes.c_int, _I64, _P,
+                                       _I64, _I64, ctypes.c_float, ctypes.c_int, ctypes.c_float, _P, _P, _P, _SZ, _P,
+                                       _P]),
+    "embedding_fwd": (ctypes.c_int, [ctypes.c_int, _P, _I64, _P, ctypes.c_int, _I64, _I64, _I64, ctypes.c_float, _P,
+                                     _I64, _P, _P]),
+    "embedding_workspace_size": (_SZ, [_I64, _I64, _I64]),
+    "embedding_bwd": (ctypes.c_int, [ctypes.c_int, _P, _I64, _P, ctypes.c_int, _I64, _I64, _I64, ctypes.c_float, _I64,
+                                     _P, ctypes.c_int, _P, _SZ, _P, _P]),
     "flce_set_wait_timeout_ns": (None, [ctypes.c_uint64]),
     "flce_selftest_wait_timeout": (ctypes.c_int, [_P, ctypes.c_uint64, _P]),
     "flce_kernel_name": (ctypes.c_char_p, [ctypes.c_int]),
@@ -371,3 +394,7 @@ def cross_entropy(logits, target, *, ignore_index: int = -100, reduction="mean",
 from ._training import (  # noqa: E402  (it uses the names above)
     ADAMW_BLOCK, NORM_KINDS, AdamW, AdamWEntry, AdamWNumbers, TensorEntry, adamw_step, grad_norm, grad_norm_raw,
     grad_norm_workspace_size, layer_norm, layer_norm_backward, ln_bwd, ln_fwd, ln_workspace_size)
+from ._losses import (  # noqa: E402
+    INDEX_TYPES, PREFERENCE_KINDS, PolicyNumbers, PreferenceNumbers, distill_fwd_bwd, distillation_loss, embedding,
+    embedding_backward, embedding_bwd, embedding_fwd, embedding_workspace_size, policy_fwd_bwd, policy_loss,
+    preference_fwd_bwd, preference_loss, preference_workspace_size, row_loss_workspace_size)

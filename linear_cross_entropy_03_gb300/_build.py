@@ -1,5 +1,5 @@
 """Builds the CUDA library in-tree: csrc/*.cu -> _lib/libflce03.so (sm_103a), and
-the Python extension that calls it with tensors: csrc/binding.cpp ->
+the Python extension that calls it with tensors: csrc/binding*.cpp ->
 _lib/flce_torch-<torch version>.so.
 
 Each translation unit is compiled by its own process (in parallel), then linked,
@@ -38,6 +38,10 @@ def _sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
+def _binding_sources():
+    return sorted(glob.glob(os.path.join(CSRC, "binding*.cpp")))
+
+
 def binding_path() -> str:
     import torch
     return os.path.join(OUT_DIR, f"flce_torch-{torch.__version__}.so")
@@ -52,7 +56,7 @@ def binding_obstacle():
 
 
 def _inputs():
-    return _sources() + [os.path.join(CSRC, "binding.cpp")] + glob.glob(os.path.join(CSRC, "*.cuh")) + \
+    return _sources() + _binding_sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + \
         glob.glob(os.path.join(CSRC, "*.h")) + [os.path.join(ROOT, "include", "flce.h"), os.path.abspath(__file__)]
 
 
@@ -71,20 +75,31 @@ def _run(what: str, cmd) -> str:
     return r.stdout + r.stderr
 
 
-def _compile_binding(nvcc: str):
-    """The extension's object file, and the command that links it once the library is there."""
+def _binding_object(src: str) -> str:
+    return os.path.join(OUT_DIR, os.path.basename(src)[:-4] + ".o")
+
+
+def _compile_binding(nvcc: str, src: str):
+    """One of the extension's object files."""
     import torch
     root = os.path.dirname(os.path.abspath(torch.__file__))
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc)))
     include = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
                sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
-    cxx, obj = os.environ.get("CXX", "g++"), os.path.join(OUT_DIR, "binding.o")
-    _run(f"{cxx} on binding.cpp", [
+    cxx = os.environ.get("CXX", "g++")
+    _run(f"{cxx} on {os.path.basename(src)}", [
         cxx, "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
         f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *(f"-I{p}" for p in include),
-        "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj])
-    return [cxx, "-shared", obj, LIB, f"-L{os.path.join(root, 'lib')}", "-ltorch_python", "-ltorch", "-ltorch_cpu",
-            "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
+        "-c", src, "-o", _binding_object(src)])
+
+
+def _link_binding():
+    """The command that links the extension once the library is there."""
+    import torch
+    root = os.path.dirname(os.path.abspath(torch.__file__))
+    return [os.environ.get("CXX", "g++"), "-shared", *map(_binding_object, _binding_sources()), LIB,
+            f"-L{os.path.join(root, 'lib')}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+            "-Wl,-rpath,$ORIGIN"]
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
@@ -104,8 +119,9 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     def compile_one(src, obj):
         return _run(f"nvcc on {os.path.basename(src)}", [nvcc, *ARCH, *FLAGS, *extra_flags, "-c", src, "-o", obj])
 
-    with concurrent.futures.ThreadPoolExecutor(len(srcs) + 1) as ex:
-        binding = None if obstacle else ex.submit(_compile_binding, nvcc)
+    parts = [] if obstacle else _binding_sources()
+    with concurrent.futures.ThreadPoolExecutor(len(srcs) + len(parts) + 1) as ex:
+        compiled = [ex.submit(_compile_binding, nvcc, part) for part in parts]
         logs = list(ex.map(compile_one, srcs, objs))
     if verbose:
         for s, log in zip(srcs, logs):
@@ -115,11 +131,13 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     _run("link", [nvcc, *ARCH, "-shared", "-Xlinker", "-soname=libflce03.so", "-o", tmp, *objs, "-lcudart_static",
                   "-ldl", "-lpthread", "-lrt"])
     os.replace(tmp, LIB)
-    if binding is None:
+    if obstacle:
         warnings.warn(f"only the library is built, and not the extension that calls it with tensors: {obstacle}")
         return LIB
     tmp = binding_path() + ".tmp"
-    _run("link", [*binding.result(), "-o", tmp])
+    for part in compiled:
+        part.result()
+    _run("link", [*_link_binding(), "-o", tmp])
     os.replace(tmp, binding_path())
     return LIB
 

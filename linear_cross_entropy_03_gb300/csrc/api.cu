@@ -19,7 +19,7 @@ int64_t ce_vector_elems(int dtype, bool vector_path);
 
 namespace {
 
-constexpr int kVersion = 200;  // 0.2.0
+constexpr int kVersion = 300;  // 0.3.0
 constexpr size_t kAlign = 256;
 // Default chunk: the largest multiple of 256 tokens whose bf16 logits fit in
 // 2 GiB (8192 tokens at V = 128256, 4096 at V = 256000).  Larger chunks halve
@@ -801,6 +801,14 @@ const char* flce_kernel_name(int id) {
     case FLCE_KERNEL_LN_REDUCE: return "ln_reduce";
     case FLCE_KERNEL_GRAD_NORM: return "grad_norm";
     case FLCE_KERNEL_ADAMW: return "adamw";
+    case FLCE_KERNEL_ROW_LOSS: return "row_loss";
+    case FLCE_KERNEL_ROW_COUNT: return "row_count";
+    case FLCE_KERNEL_PAIR_LOSS: return "pair_loss";
+    case FLCE_KERNEL_ROW_GRAD: return "row_grad";
+    case FLCE_KERNEL_EMBEDDING: return "embedding";
+    case FLCE_KERNEL_TOKEN_SORT: return "token_sort";
+    case FLCE_KERNEL_EMBEDDING_BWD: return "embedding_bwd";
+    case FLCE_KERNEL_EMBEDDING_JOIN: return "embedding_join";
   }
   return "unknown";
 }

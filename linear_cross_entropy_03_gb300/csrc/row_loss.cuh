@@ -1,0 +1,725 @@
+// Losses on materialised logits [N, V] that a row's softmax and a few numbers of its own
+// give: the clipped policy loss, the distance from a teacher's top logits, and the row
+// statistics of the preference loss.  With z the row's logits, T the temperature,
+// M = max z, S = sum exp((z - M) / T) and p = exp((z - M) / T) / S:
+//
+//   policy      logp = (z_t - M) / T - ln S, r = exp(logp - old), d = ref - logp
+//               loss = -min(r A, clip(r) A) + b (exp(d) - 1 - d)
+//               slope = dloss / dlogp = -r A [not clipped] - b (exp(d) - 1)
+//               grad = f (p - onehot(t)),  f = -slope / T
+//   distill     q = softmax of the teacher's values / T,
+//               loss = T^2 sum_k q_k (ln q_k - ln p_k),  grad = f (p - q),  f = T
+//
+// so a row is read, reduced to (M, S) and written as f p, but for the few places that the
+// target or the teacher's list names.  Everything between loading and storing is fp32,
+// sums over rows are fp64.  Differences z - M are formed before they are scaled, so that
+// logits about any common level keep their digits.
+#pragma once
+
+#include <type_traits>
+
+#include "arrival.cuh"
+#include "elem.cuh"
+#include "ptx.cuh"
+
+namespace flce {
+
+constexpr int kMaxTeacher = 1024;      // entries of a teacher's list
+constexpr int kRowLossMaxCtas = 4096;  // partial losses in the workspace
+constexpr int kCountCtas = 64;         // partial counts of the rows that take part
+
+enum RowLoss { kPolicy = 0, kDistill = 1, kStats = 2 };
+
+struct RowLossParams {
+  const void* logits;
+  void* grad;  // may be logits; null: loss only
+  int64_t ld, ld_grad;
+  int64_t N, V;
+  int64_t ignore_index;
+  const int64_t* target;  // policy, stats
+  const float* advantage;
+  const float* old_logp;  // or null
+  const float* ref_logp;  // or null
+  float ratio_low, ratio_high, kl_weight;
+  const void* ids;  // distill: [N, K]
+  const void* values;
+  int ids32, value_dtype, K;
+  const float* row_weight;  // [N] or null
+  const float* grad_out;    // [N] or null
+  float temperature, inv_t, c;  // T, 1 / T, log2(e) / T
+  int reduction;
+  float grad_scale;
+  float* loss_rows;  // reduction none, else null
+  float* loss;       // sum and mean, else null
+  float* logp;       // [N] or null
+  float2* stats;     // stats: (M, 1 / S) of each row
+  float* factor;     // stats: [N], set to 0
+  // workspace
+  const int* counts;  // kCountCtas partial counts, or null: the kernel counts itself
+  double* partial;    // [grid]
+  int* flags;         // [grid]
+  unsigned long long* arrivals;
+  unsigned long long tag;
+  int* status;
+  int own_status;  // the workspace's own word: written, and not added to
+  uint64_t timeout_ns;
+};
+
+namespace {
+
+constexpr float kLog2E = 1.4426950408889634f;
+
+__device__ __forceinline__ int64_t load_id(const void* ids, int ids32, int64_t i) {
+  return ids32 ? __ldg(static_cast<const int32_t*>(ids) + i) : __ldg(static_cast<const int64_t*>(ids) + i);
+}
+
+// ---------------------------------------------------------------- vectors of a row
+
+// Eight 16-bit elements or four of fp32.
+template <typename T>
+constexpr int kVecElems = 16 / static_cast<int>(sizeof(T));
+
+template <typename T>
+__device__ __forceinline__ void vec_pairs(const uint4& v, Pair (&to)[kVecElems<T> / 2]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  if constexpr (sizeof(T) == 4) {
+    to[0] = pair(__uint_as_float(w[0]), __uint_as_float(w[1]));
+    to[1] = pair(__uint_as_float(w[2]), __uint_as_float(w[3]));
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if constexpr (std::is_same<T, __half>::value) {
+        const float2 f = __half22float2(reinterpret_cast<const __half2&>(w[k]));
+        to[k] = pair(f.x, f.y);
+      } else {
+        to[k] = pair(bf16_lo(w[k]), bf16_hi(w[k]));
+      }
+    }
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ uint4 pack_pairs(const Pair (&from)[kVecElems<T> / 2]) {
+  uint32_t w[4];
+  if constexpr (sizeof(T) == 4) {
+    const float2 a = unpair(from[0]), b = unpair(from[1]);
+    w[0] = __float_as_uint(a.x), w[1] = __float_as_uint(a.y), w[2] = __float_as_uint(b.x), w[3] = __float_as_uint(b.y);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 f = unpair(from[k]);
+      if constexpr (std::is_same<T, __half>::value) {
+        const __half2 h = __floats2half2_rn(f.x, f.y);
+        w[k] = reinterpret_cast<const uint32_t&>(h);
+      } else {
+        w[k] = pack_bf16x2(f.x, f.y);
+      }
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// A vector that adds nothing to a row.
+template <typename T>
+__device__ __forceinline__ uint4 empty_vec() {
+  const uint32_t w = sizeof(T) == 4 ? 0xFF800000u : std::is_same<T, __half>::value ? 0xFC00FC00u : 0xFF80FF80u;
+  return make_uint4(w, w, w, w);
+}
+
+// The largest element; NaN is passed over here (the sum of exponentials shows it).
+template <typename T, int COUNT>
+__device__ __forceinline__ float vecs_max(const uint4 (&v)[COUNT]) {
+  if constexpr (sizeof(T) == 4) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < COUNT; ++i)
+      m = fmaxf(fmaxf(m, fmaxf(__uint_as_float(v[i].x), __uint_as_float(v[i].y))),
+                fmaxf(__uint_as_float(v[i].z), __uint_as_float(v[i].w)));
+    return m;
+  } else {
+    using T2 = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+    T2 m = reinterpret_cast<const T2&>(v[0].x);
+#pragma unroll
+    for (int i = 0; i < COUNT; ++i) {
+      const T2* w = reinterpret_cast<const T2*>(&v[i]);
+      m = __hmax2(m, __hmax2(__hmax2(w[0], w[1]), __hmax2(w[2], w[3])));
+    }
+    return fmaxf(__low2float(m), __high2float(m));
+  }
+}
+
+// exp((z - M) / T) of a vector's elements, with c = log2(e) / T.
+template <typename T>
+__device__ __forceinline__ void vec_exp(const uint4& v, Pair minus_m, Pair c, Pair (&e)[kVecElems<T> / 2]) {
+  vec_pairs<T>(v, e);
+#pragma unroll
+  for (int k = 0; k < kVecElems<T> / 2; ++k) {
+    const float2 x = unpair((e[k] + minus_m) * c);
+    e[k] = pair(ex2_approx(x.x), ex2_approx(x.y));
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void vec_add_exp(const uint4& v, Pair minus_m, Pair c, Pair& sum) {
+  Pair e[kVecElems<T> / 2];
+  vec_exp<T>(v, minus_m, c, e);
+#pragma unroll
+  for (int k = 0; k < kVecElems<T> / 2; ++k) sum = sum + e[k];
+}
+
+// Elements factor * exp((z - M) / T): a row's gradient but for the places that it names.
+template <typename T>
+__device__ __forceinline__ uint4 vec_grad(const uint4& v, Pair minus_m, Pair c, Pair factor) {
+  Pair e[kVecElems<T> / 2];
+  vec_exp<T>(v, minus_m, c, e);
+#pragma unroll
+  for (int k = 0; k < kVecElems<T> / 2; ++k) e[k] = e[k] * factor;
+  return pack_pairs<T>(e);
+}
+
+// A vector of a gradient's row, of which `vector` says whether it lies on a boundary there.
+template <typename T>
+__device__ __forceinline__ void store_vec(T* to, const uint4& v, bool vector) {
+  if (vector) {
+    __stcs(reinterpret_cast<uint4*>(to), v);
+  } else {
+    const T* e = reinterpret_cast<const T*>(&v);
+#pragma unroll
+    for (int k = 0; k < kVecElems<T>; ++k) to[k] = e[k];
+  }
+}
+
+// A row's elements: `head` before the first 16-byte boundary, `vecs` vectors, `tail` after.
+struct RowSplit {
+  int head, tail;
+  int64_t vecs;
+};
+
+template <typename T>
+__device__ __forceinline__ RowSplit split_row(const T* row, int64_t V) {
+  constexpr int kE = kVecElems<T>;
+  RowSplit s;
+  const int64_t head = ((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / sizeof(T);
+  s.head = static_cast<int>(head < V ? head : V);
+  s.vecs = (V - s.head) / kE;
+  s.tail = static_cast<int>(V - s.head - s.vecs * kE);
+  return s;
+}
+
+// Whether vectors of a row of logits lie on boundaries of the gradient's row too.
+template <typename T>
+__device__ __forceinline__ bool same_phase(const T* x, const T* g) {
+  return ((reinterpret_cast<uintptr_t>(x) ^ reinterpret_cast<uintptr_t>(g)) & 15) == 0;
+}
+
+// Partial results (m, s) of parts of a row, as (M, S): by all lanes, each with one part
+// (or several combined before), parts of nothing as (-inf, 0).
+__device__ __forceinline__ float2 combine_parts(float m, float s, float c) {
+  const float top = warp_max_redux(m);
+  const float shift = top > -INFINITY ? top : 0.f;
+  return make_float2(top, warp_sum(m > -INFINITY ? s * ex2_approx((m - shift) * c) : s));
+}
+
+// ---------------------------------------------------------------- what a row has beside its logits
+
+struct RowInfo {
+  float zt;  // policy, stats: the target's logit; distill: the largest logit of the list
+  float advantage, old_logp, ref_logp;
+  float weight, grad_out;
+  float a;      // distill: sum of q (ln q - (z - zt) / T)
+  int column;   // policy, stats: the target's, or -1 where the row takes no part
+  int entries;  // distill: length of the list, 0 where the row has no teacher
+};
+
+template <typename T>
+__device__ __forceinline__ float load_logit(const RowLossParams& p, int64_t row, int64_t column) {
+  return to_float(static_cast<const T*>(p.logits)[row * p.ld + column]);
+}
+
+template <typename T>
+__device__ __forceinline__ RowInfo policy_row(const RowLossParams& p, int64_t row, int* bits) {
+  RowInfo r = {};
+  const int64_t t = __ldg(p.target + row);
+  r.column = -1;
+  if (t != p.ignore_index) {
+    if (t >= 0 && t < p.V)
+      r.column = static_cast<int>(t);
+    else
+      *bits |= FLCE_STATUS_BIT_TARGET_RANGE;
+  }
+  r.weight = p.row_weight != nullptr ? __ldg(p.row_weight + row) : 1.f;
+  r.grad_out = p.grad_out != nullptr ? __ldg(p.grad_out + row) : 1.f;
+  r.advantage = p.advantage != nullptr ? __ldg(p.advantage + row) : 0.f;
+  r.old_logp = p.old_logp != nullptr ? __ldg(p.old_logp + row) : 0.f;
+  r.ref_logp = p.ref_logp != nullptr ? __ldg(p.ref_logp + row) : 0.f;
+  r.zt = r.column >= 0 ? load_logit<T>(p, row, t) : 0.f;
+  return r;
+}
+
+// A teacher's list in shared memory: columns (-1: no such place), shares and logits.
+struct TeacherList {
+  int* column;
+  float* q;
+  float* z;
+};
+__host__ __device__ constexpr int list_room(int K) { return (K + 31) & ~31; }
+__host__ __device__ constexpr size_t list_bytes(int K) { return static_cast<size_t>(list_room(K)) * 12; }
+// Slots of the table that finds columns that a list names twice: at least twice the entries.
+__host__ __device__ constexpr int table_slots(int K) {
+  int n = 64;
+  while (n < 2 * K) n *= 2;
+  return n;
+}
+__device__ __forceinline__ TeacherList list_at(uint8_t* at, int K) {
+  const int room = list_room(K);
+  return {reinterpret_cast<int*>(at), reinterpret_cast<float*>(at) + room, reinterpret_cast<float*>(at) + 2 * room};
+}
+
+// Reads a row's list, by one warp: fills `list` with the entries up to the first negative
+// id, q of columns that occur twice added up, and returns the row's numbers.  `table` has
+// table_slots(K) words.
+template <typename T>
+__device__ RowInfo teacher_row(const RowLossParams& p, int64_t row, const TeacherList& list, int* table, int* bits) {
+  const int lane = threadIdx.x & 31;
+  const int64_t base = row * p.K;
+  RowInfo r = {};
+  r.weight = p.row_weight != nullptr ? __ldg(p.row_weight + row) : 1.f;
+  r.grad_out = p.grad_out != nullptr ? __ldg(p.grad_out + row) : 1.f;
+  r.column = -1;
+  const int slots = table_slots(p.K);
+  for (int i = lane; i < slots; i += 32) table[i] = -1;
+  float vmax = -INFINITY;
+  int entries = 0;
+  for (int k0 = 0; k0 < p.K; k0 += 32) {
+    const int k = k0 + lane;
+    const int64_t id = k < p.K ? load_id(p.ids, p.ids32, base + k) : -1;
+    const float v = k < p.K ? load_elem(p.values, p.value_dtype, base + k) : -INFINITY;
+    const unsigned ends = __ballot_sync(0xffffffffu, id < 0);
+    const int first = ends != 0 ? __ffs(ends) - 1 : 32;
+    if (lane < first) {
+      const bool inside = id < p.V;
+      if (!inside) *bits |= FLCE_STATUS_BIT_TARGET_RANGE;
+      list.column[k] = inside ? static_cast<int>(id) : -1;
+      list.q[k] = inside ? v : -INFINITY;
+      if (inside) vmax = fmaxf(vmax, v);
+    }
+    entries += first;
+    if (ends != 0) break;
+  }
+  __syncwarp();
+  vmax = warp_max_redux(vmax);
+  const float shift = vmax > -INFINITY ? vmax : 0.f;
+  float sum = 0.f, zmax = -INFINITY;
+  for (int k = lane; k < entries; k += 32) {
+    const int column = list.column[k];
+    const float e = ex2_approx((list.q[k] - shift) * p.c);
+    float z = -INFINITY;
+    if (e == 0.f) {
+      list.column[k] = -1;  // no share: the place is like any other
+    } else {
+      z = load_logit<T>(p, row, column);
+      sum += e;
+      zmax = fmaxf(zmax, z);
+    }
+    list.q[k] = e;
+    list.z[k] = z;
+  }
+  sum = warp_sum(sum);
+  zmax = warp_max_redux(zmax);
+  r.zt = zmax > -INFINITY ? zmax : 0.f;
+  r.entries = sum == 0.f ? 0 : entries;  // (a list of -inf alone is no teacher)
+  const float inv = 1.f / sum, ln_sum = logf(sum);
+  float a = 0.f;
+  bool twice = false;
+  for (int k = lane; k < r.entries; k += 32) {
+    const int column = list.column[k];
+    if (column < 0) continue;
+    const float e = list.q[k], q = e * inv;
+    a += q * (logf(e) - ln_sum - (list.z[k] - r.zt) * p.inv_t);
+    list.q[k] = q;
+    // a free slot is there: the table has twice the entries
+    for (unsigned s = (static_cast<unsigned>(column) * 2654435761u) >> 8;; ++s) {
+      const int was = atomicCAS(table + (s & (slots - 1)), -1, column);
+      if (was == -1) break;
+      if (was == column) {
+        twice = true;
+        break;
+      }
+    }
+  }
+  r.a = warp_sum(a);
+  __syncwarp();
+  if (__any_sync(0xffffffffu, twice)) {
+    // every entry gets its column's whole share, so that all that name it write the same
+    float* total = reinterpret_cast<float*>(table);
+    for (int k = lane; k < r.entries; k += 32) {
+      float q = 0.f;
+      for (int j = 0; j < r.entries; ++j)
+        if (list.column[j] == list.column[k] && list.column[j] >= 0) q += list.q[j];
+      total[k] = q;
+    }
+    __syncwarp();
+    for (int k = lane; k < r.entries; k += 32) list.q[k] = total[k];
+  }
+  __syncwarp();
+  return r;
+}
+
+// ---------------------------------------------------------------- a row's loss
+
+struct RowResult {
+  float loss, logp;
+  float f;  // the gradient is f (p - ...); 0: the row's gradient is 0 whatever its logits
+};
+
+// `scale`: what multiplies all gradients (grad_scale, or that over the rows of a mean).
+template <int KIND>
+__device__ __forceinline__ RowResult row_result(const RowLossParams& p, const RowInfo& r, float m, float s,
+                                                float scale) {
+  RowResult out = {0.f, 0.f, 0.f};
+  const float ln_s = logf(s);
+  scale *= r.grad_out;
+  if constexpr (KIND == kDistill) {
+    if (r.entries == 0 || r.weight == 0.f) return out;
+    out.loss = p.temperature * p.temperature * r.weight * (r.a + ((m - r.zt) * p.inv_t + ln_s));
+    out.f = p.temperature * r.weight * scale;
+  } else {
+    if (r.column < 0) return out;
+    out.logp = (r.zt - m) * p.inv_t - ln_s;
+    if (KIND == kStats || r.weight == 0.f) return out;
+    const float a = r.advantage;
+    const float ratio = p.old_logp != nullptr ? expf(out.logp - r.old_logp) : 1.f;
+    const bool over = a > 0.f && ratio > p.ratio_high, under = a < 0.f && ratio < p.ratio_low;
+    float loss = -a * (over ? p.ratio_high : under ? p.ratio_low : ratio);
+    float slope = over || under ? 0.f : -a * ratio;
+    if (p.kl_weight != 0.f) {
+      const float d = r.ref_logp - out.logp, x = expm1f(d);
+      loss += p.kl_weight * (x - d);
+      slope -= p.kl_weight * x;
+    }
+    out.loss = loss * r.weight;
+    out.f = -slope * r.weight * scale * p.inv_t;
+  }
+  return out;
+}
+
+// The gradient at a place that the row names.
+__device__ __forceinline__ float target_grad(const RowResult& r) { return r.f * expm1f(r.logp); }
+__device__ __forceinline__ float entry_grad(const RowLossParams& p, const TeacherList& list, int k, float f, float m,
+                                            float inv_s) {
+  return f * (ex2_approx((list.z[k] - m) * p.c) * inv_s - list.q[k]);
+}
+
+// ---------------------------------------------------------------- rows that take part, and the end
+
+template <int KIND>
+__device__ __forceinline__ bool takes_part(const RowLossParams& p, int64_t n) {
+  if constexpr (KIND == kDistill) return load_id(p.ids, p.ids32, n * p.K) >= 0;
+  const int64_t t = __ldg(p.target + n);
+  return t != p.ignore_index && t >= 0 && t < p.V;
+}
+
+// Partial counts of rows n, n + step, ...: by one thread.
+template <int KIND>
+__device__ __forceinline__ int count_rows(const RowLossParams& p, int64_t n, int64_t step) {
+  int count = 0;
+#pragma unroll 4
+  for (; n < p.N; n += step) count += takes_part<KIND>(p, n);
+  return count;
+}
+
+template <int KIND>
+__global__ void __launch_bounds__(256) row_count_kernel(const RowLossParams p, int* counts) {
+  __shared__ int total;
+  if (threadIdx.x == 0) total = 0;
+  __syncthreads();
+  const int mine = count_rows<KIND>(p, static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, kCountCtas * 256);
+  if (mine != 0) atomicAdd(&total, mine);
+  __syncthreads();
+  if (threadIdx.x == 0) counts[blockIdx.x] = total;
+}
+
+// The rows of a mean, in every lane of a warp, from row_count_kernel's counts.
+__device__ __forceinline__ int counted_rows(const int* counts) {
+  int n = 0;
+  for (int i = threadIdx.x & 31; i < kCountCtas; i += 32) n += __ldcg(counts + i);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+  return n;
+}
+
+// By all threads of every CTA of a launch, at its end: adds up the CTAs' losses (of thread
+// 0) in the order of the CTAs, and their status bits, in the CTA that arrives last.
+__device__ __forceinline__ void finish_rows(const RowLossParams& p, double loss, int bits, int rows) {
+  __shared__ int last;
+  __shared__ double sums[32];
+  __shared__ int all_bits;
+  if (threadIdx.x == 0) {
+    all_bits = 0;
+    p.partial[blockIdx.x] = loss;
+    p.flags[blockIdx.x] = bits;
+    last = arrives_last(p.arrivals, p.tag, gridDim.x);
+  }
+  __syncthreads();
+  if (!last) return;
+  double total = 0;
+  int seen = 0;
+  for (unsigned i = threadIdx.x; i < gridDim.x; i += blockDim.x) {
+    total += __ldcg(p.partial + i);
+    seen |= __ldcg(p.flags + i);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = total;
+  if (seen != 0) atomicOr(&all_bits, seen);
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  total = 0;
+  for (unsigned w = 0; w < blockDim.x / 32; ++w) total += sums[w];
+  if (p.loss != nullptr)
+    *p.loss = p.reduction != FLCE_REDUCTION_MEAN ? static_cast<float>(total)
+              : rows > 0                         ? static_cast<float>(total / rows)
+                                                 : __int_as_float(0x7fc00000);
+  if (p.own_status)
+    *p.status = all_bits;
+  else if (all_bits != 0)
+    atomicOr(p.status, all_bits);
+}
+
+// What a row's result leaves beside its gradient: by one thread.
+template <int KIND>
+__device__ __forceinline__ void store_result(const RowLossParams& p, int64_t row, const RowResult& r, float m,
+                                             float s, double* loss) {
+  if constexpr (KIND == kStats) {
+    p.stats[row] = make_float2(m, 1.f / s);
+    p.factor[row] = 0.f;
+  } else {
+    *loss += r.loss;
+    if (p.loss_rows != nullptr) p.loss_rows[row] = r.loss;
+  }
+  if (p.logp != nullptr) p.logp[row] = r.logp;
+}
+
+// ---------------------------------------------------------------- rows of any length
+
+// One CTA a row, which reads it twice.  For rows that the form by parts does not hold.
+constexpr int kLongThreads = 512;
+constexpr int kLongVecs = 4;
+
+template <typename T, int KIND>
+__global__ void __launch_bounds__(kLongThreads) row_loss_long_kernel(const RowLossParams p) {
+  extern __shared__ __align__(16) uint8_t list_memory[];
+  constexpr int kWarps = kLongThreads / 32, kE = kVecElems<T>;
+  __shared__ RowInfo info;
+  __shared__ float2 parts[kWarps];
+  __shared__ int count;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const TeacherList list = list_at(list_memory, p.K);
+  if (tid == 0) {
+    count = 0;
+    if (blockIdx.x == 0) expect_arrivals(p.arrivals, p.tag);
+  }
+  __syncthreads();
+  int rows = 1, bits = 0;
+  grid_dependency_wait();
+  if (p.reduction == FLCE_REDUCTION_MEAN) {
+    if (p.counts != nullptr) {
+      rows = counted_rows(p.counts);
+    } else {
+      const int mine = count_rows<KIND>(p, tid, kLongThreads);
+      if (mine != 0) atomicAdd(&count, mine);
+      __syncthreads();
+      rows = count;
+    }
+  }
+  const float scale = p.reduction == FLCE_REDUCTION_MEAN ? p.grad_scale / static_cast<float>(rows) : p.grad_scale;
+  const Pair c = pair(p.c);
+  double loss = 0;
+  for (int64_t row = blockIdx.x; row < p.N; row += gridDim.x) {
+    const T* x = static_cast<const T*>(p.logits) + row * p.ld;
+    const RowSplit split = split_row(x, p.V);
+    const uint4* vecs = reinterpret_cast<const uint4*>(x + split.head);
+    const T* tail = x + split.head + split.vecs * kE;
+    float m = -INFINITY, s = 0.f;
+    if (warp == 0) {
+      RowInfo r;
+      if constexpr (KIND == kDistill)
+        r = teacher_row<T>(p, row, list, reinterpret_cast<int*>(list_memory + list_bytes(p.K)), &bits);
+      else
+        r = policy_row<T>(p, row, &bits);
+      if (lane == 0) info = r;
+    }
+    if (tid < split.head) m = to_float(x[tid]), s = 1.f;
+    if (tid >= 32 && tid < 32 + split.tail) m = to_float(tail[tid - 32]), s = 1.f;
+    if (s == 1.f && !(m > -INFINITY)) s = m == m ? 0.f : m;  // -inf adds nothing, NaN stays
+    for (int64_t at = tid; at < split.vecs; at += kLongThreads * kLongVecs) {
+      uint4 v[kLongVecs];
+#pragma unroll
+      for (int i = 0; i < kLongVecs; ++i) {
+        const int64_t k = at + i * kLongThreads;
+        v[i] = k < split.vecs ? vecs[k] : empty_vec<T>();
+      }
+      const float top = fmaxf(m, vecs_max<T, kLongVecs>(v));
+      const float shift = top > -INFINITY ? top : 0.f;
+      Pair sum = pair(0.f);
+#pragma unroll
+      for (int i = 0; i < kLongVecs; ++i) vec_add_exp<T>(v[i], pair(-shift), c, sum);
+      const float2 both = unpair(sum);
+      s = (m > -INFINITY ? s * ex2_approx((m - shift) * p.c) : s) + (both.x + both.y);
+      m = top;
+    }
+    const float2 mine = combine_parts(m, s, p.c);
+    if (lane == 0) parts[warp] = mine;
+    __syncthreads();
+    const float2 part = lane < kWarps ? parts[lane] : make_float2(-INFINITY, 0.f);
+    const float2 all = combine_parts(part.x, part.y, p.c);
+    const RowInfo r = info;
+    const RowResult result = row_result<KIND>(p, r, all.x, all.y, scale);
+    if (tid == 0) store_result<KIND>(p, row, result, all.x, all.y, &loss);
+    if (KIND != kStats && p.grad != nullptr) {
+      T* g = static_cast<T*>(p.grad) + row * p.ld_grad;
+      const float inv_s = 1.f / all.y, f = result.f * inv_s;
+      const Pair minus_m = pair(-all.x), factor = pair(f);
+      const bool zero = result.f == 0.f, vector = same_phase(x, g);
+      if (tid < split.head) g[tid] = from_float<T>(zero ? 0.f : f * ex2_approx((to_float(x[tid]) - all.x) * p.c));
+      if (tid >= 32 && tid < 32 + split.tail) {
+        const int64_t at = split.head + split.vecs * kE + tid - 32;
+        g[at] = from_float<T>(zero ? 0.f : f * ex2_approx((to_float(x[at]) - all.x) * p.c));
+      }
+#pragma unroll 4
+      for (int64_t at = tid; at < split.vecs; at += kLongThreads) {
+        const uint4 v = zero ? make_uint4(0, 0, 0, 0) : vec_grad<T>(__ldcs(vecs + at), minus_m, c, factor);
+        store_vec<T>(g + split.head + at * kE, v, vector);
+      }
+      __syncthreads();  // the places that the row names are written after the rest
+      if (!zero) {
+        if constexpr (KIND == kDistill) {
+          for (int k = tid; k < r.entries; k += kLongThreads)
+            if (list.column[k] >= 0)
+              g[list.column[k]] = from_float<T>(entry_grad(p, list, k, result.f, all.x, inv_s));
+        } else if (tid == 0) {
+          g[r.column] = from_float<T>(target_grad(result));
+        }
+      }
+    }
+    __syncthreads();  // info, list and parts are the next row's
+  }
+  if (warp == 0) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) bits |= __shfl_xor_sync(0xffffffffu, bits, o);
+  }
+  finish_rows(p, loss, bits, rows);
+}
+
+template <typename T, int KIND>
+cudaError_t launch_long(const RowLossParams& p, cudaStream_t s) {
+  const size_t smem = KIND == kDistill ? list_bytes(p.K) + table_slots(p.K) * 4 : 0;
+  const int64_t most = 4 * device_sm_count();
+  const unsigned grid = static_cast<unsigned>(p.N < 1 ? 1 : p.N < most ? p.N : most);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kLongThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = p.counts != nullptr ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, row_loss_long_kernel<T, KIND>, p);
+}
+
+// ---------------------------------------------------------------- host side
+
+template <typename T, int KIND>
+cudaError_t launch_rows_of(const RowLossParams& p, cudaStream_t s) {
+  return launch_long<T, KIND>(p, s);
+}
+
+// All rows of a call: the count that a mean needs first, then the rows.
+template <int KIND>
+cudaError_t launch_rows(const RowLossParams& given, int dtype, cudaStream_t s) {
+  RowLossParams p = given;
+  // every CTA counts all rows' targets itself where that is less than a launch takes
+  const bool self_count = p.N <= (KIND == kDistill ? 512 : 2048);
+  if (p.reduction != FLCE_REDUCTION_MEAN || KIND == kStats || self_count) {
+    p.counts = nullptr;
+  } else {
+    prof_begin(s, FLCE_KERNEL_ROW_COUNT);
+    row_count_kernel<KIND><<<kCountCtas, 256, 0, s>>>(p, const_cast<int*>(p.counts));
+    const cudaError_t e = cudaGetLastError();
+    prof_end(s);
+    if (e != cudaSuccess) return e;
+  }
+  prof_begin(s, FLCE_KERNEL_ROW_LOSS);
+  const cudaError_t e = dtype == FLCE_DTYPE_BF16   ? launch_rows_of<__nv_bfloat16, KIND>(p, s)
+                        : dtype == FLCE_DTYPE_FP16 ? launch_rows_of<__half, KIND>(p, s)
+                                                   : launch_rows_of<float, KIND>(p, s);
+  prof_end(s);
+  return e;
+}
+
+// Workspace of a call over rows: status, arrivals (two, for the calls of two such
+// launches), counts, flags, partial losses.
+constexpr size_t kRowLossFixed = 512 + kRowLossMaxCtas * (sizeof(int) + sizeof(double));
+static_assert(256 + kCountCtas * sizeof(int) <= 512, "counts fit before the flags");
+
+inline void use_workspace(RowLossParams* p, void* workspace, int32_t* status_dev) {
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p->status = status_dev != nullptr ? status_dev : reinterpret_cast<int*>(ws);
+  p->own_status = status_dev == nullptr ? 1 : 0;
+  p->arrivals = reinterpret_cast<unsigned long long*>(ws + 8);
+  p->tag = next_arrival_tag();
+  p->counts = reinterpret_cast<const int*>(ws + 256);
+  p->flags = reinterpret_cast<int*>(ws + 512);
+  p->partial = reinterpret_cast<double*>(ws + 512 + kRowLossMaxCtas * sizeof(int));
+  p->timeout_ns = 2000000000ull;
+}
+
+inline bool row_sizes_ok(int64_t N, int64_t V, int64_t ld) {
+  const int64_t most = int64_t(1) << 31;
+  return N >= 0 && N < most && V >= 1 && V < most && ld >= V && ld <= (int64_t(1) << 58) / (N > 0 ? N : 1);
+}
+
+// What the three losses check alike; `losses`: how many NONE leaves.
+inline flce_status_t check_rows(const void* logits, int dtype, int64_t ld, const void* grad, int64_t ld_grad,
+                                int64_t N, int64_t V, int64_t losses, int reduction, const float* grad_out,
+                                const float* loss, const void* workspace, size_t workspace_bytes, size_t size,
+                                const int32_t* status) {
+  if (!float_dtype(dtype)) return FLCE_ERR_UNSUPPORTED;
+  if (!row_sizes_ok(N, V, ld) || (grad != nullptr && !row_sizes_ok(N, V, ld_grad))) return FLCE_ERR_INVALID_ARG;
+  if (reduction < FLCE_REDUCTION_NONE || reduction > FLCE_REDUCTION_MEAN) return FLCE_ERR_INVALID_ARG;
+  if (grad_out != nullptr && reduction != FLCE_REDUCTION_NONE) return FLCE_ERR_INVALID_ARG;
+  if (N > 0 && logits == nullptr) return FLCE_ERR_INVALID_ARG;
+  if (loss == nullptr && (reduction != FLCE_REDUCTION_NONE || losses > 0)) return FLCE_ERR_INVALID_ARG;
+  const size_t esz = elem_size(dtype);
+  if (!aligned_to(logits, esz) || !aligned_to(grad, esz) || !aligned_to(loss, 4) || !aligned_to(grad_out, 4) ||
+      !aligned_to(status, 4))
+    return FLCE_ERR_MISALIGNED;
+  if (grad != nullptr && N > 0) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(logits), g = reinterpret_cast<uintptr_t>(grad);
+    const uintptr_t x_end = x + (static_cast<uintptr_t>(N - 1) * ld + V) * esz;
+    const uintptr_t g_end = g + (static_cast<uintptr_t>(N - 1) * ld_grad + V) * esz;
+    if (x == g ? (ld != ld_grad && N > 1) : (x < g_end && g < x_end)) return FLCE_ERR_INVALID_ARG;
+  }
+  if (workspace == nullptr || !aligned_to(workspace, 256) || workspace_bytes < size) return FLCE_ERR_WORKSPACE;
+  return FLCE_OK;
+}
+
+inline RowLossParams row_params(const void* logits, int64_t ld, void* grad, int64_t ld_grad, int64_t N, int64_t V,
+                                int reduction, float grad_scale, const float* grad_out, float* loss,
+                                float temperature) {
+  RowLossParams p = {};
+  p.logits = logits, p.ld = ld, p.grad = grad, p.ld_grad = ld_grad, p.N = N, p.V = V;
+  p.reduction = reduction, p.grad_scale = grad_scale, p.grad_out = grad_out;
+  p.loss_rows = reduction == FLCE_REDUCTION_NONE ? loss : nullptr;
+  p.loss = reduction == FLCE_REDUCTION_NONE ? nullptr : loss;
+  p.temperature = temperature, p.inv_t = 1.f / temperature;
+  p.c = static_cast<float>(1.4426950408889634 / static_cast<double>(temperature));
+  return p;
+}
+
+inline bool positive(float x) { return x > 0.f && x <= 3.402823466e38f; }
+
+}  // namespace
+}  // namespace flce
