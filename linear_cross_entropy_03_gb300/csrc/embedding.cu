@@ -98,6 +98,7 @@ struct SortParams {
   int N, V;            // keys are ids, or V for tokens that add nothing
   int64_t padding;
   int passes, digit;   // bits of a pass
+  int room;            // places of a CTA in shared memory
   int* keys[2];        // [N] each; the result is in keys[0], tokens[0]
   int* tokens[2];
   uint32_t* hit;       // a bit for each row of the table that gets something, or null
@@ -106,79 +107,142 @@ struct SortParams {
 
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kSortDigit = 9;  // most bits of a pass: two passes reach 2^18 ids
+constexpr int kSortDigit = 9;       // most bits of a pass: two passes reach 2^18 ids
+constexpr int kSortRoom = 8192;     // most tokens that a CTA holds in shared memory
+constexpr int kSortCtas = 8;        // of a cluster
 
-// Stable radix sort, least significant digit first, by one cluster.  Each warp owns a
-// stretch of the list: it counts its digits, the counts are added up over warps and CTAs
-// (through distributed shared memory), and it puts its keys where those before them leave
-// room.  Lanes with the same digit find one another by match.
+__device__ __forceinline__ void store_cluster_u64(uint32_t at, uint64_t v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(at), "l"(v) : "memory");
+}
+__device__ __forceinline__ void store_cluster_s32(uint32_t at, int v) {
+  asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+}
+
+constexpr int kSortEach = kSortRoom / kSortThreads;  // a thread's tokens at most
+
+// Stable radix sort, least significant digit first, by one CTA or one cluster.  Each warp
+// owns a stretch of the list: it counts its digits, the counts are added up over warps and
+// CTAs, and it puts its keys where those before them leave room.  Lanes with the same digit
+// find one another by match.  SHARED: a pass has its stretch in registers, with each token's
+// place among those of its digit, and the list is in shared memory from pass to pass, each
+// place in the CTA that reads it next.  Longer lists go through global memory.
+template <int CTAS, bool SHARED>
 __global__ void __launch_bounds__(kSortThreads) token_sort_kernel(const SortParams p) {
-  extern __shared__ int counts[];  // [warps][digits], then [digits] of the CTA, then scratch of the scan
+  extern __shared__ __align__(16) uint8_t sort_memory[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int digits = 1 << p.digit;
+  int* counts = reinterpret_cast<int*>(sort_memory);  // [warps][digits]
+  int* totals = counts + kSortWarps * digits;         // [CTAs][digits], by the CTA that has them
+  int* starts = totals + CTAS * digits;               // [digits]
+  uint64_t* list = reinterpret_cast<uint64_t*>(starts + digits);  // [room]: tokens above, keys below
   int* own = counts + warp * digits;
-  int* totals = counts + kSortWarps * digits;
   __shared__ int warp_sums[32];
-  const unsigned rank = cluster_cta_rank();
-  unsigned ctas;
-  asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(ctas));
-  const int64_t warps = static_cast<int64_t>(ctas) * kSortWarps;
+  const int rank = CTAS > 1 ? static_cast<int>(cluster_cta_rank()) : 0;
+  if (CTAS > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  const int64_t warps = static_cast<int64_t>(CTAS) * kSortWarps;
   const int64_t stretch = (p.N + warps * 32 - 1) / (warps * 32) * 32;
-  const int64_t from = (static_cast<int64_t>(rank) * kSortWarps + warp) * stretch;
+  const int64_t cta_from = rank * kSortWarps * stretch;
+  const int64_t from = cta_from + warp * stretch;
   const int64_t to = from + stretch < p.N ? from + stretch : p.N;
-  if (p.hit != nullptr) {
-    for (int i = rank * kSortThreads + threadIdx.x; i < (p.V + 31) / 32; i += ctas * kSortThreads) p.hit[i] = 0;
-    cluster_sync_all();
-  }
   int bits = 0;
+  if (p.hit != nullptr)
+    for (int i = rank * kSortThreads + threadIdx.x; i < (p.V + 31) / 32; i += CTAS * kSortThreads) p.hit[i] = 0;
+  const auto first_entry = [&](int64_t i) -> uint64_t {
+    const int64_t id = id_at(p.ids, p.ids32, i);
+    const bool inside = id >= 0 && id < p.V;
+    if (!inside) bits |= FLCE_STATUS_BIT_TARGET_RANGE;
+    return static_cast<uint64_t>(i) << 32 | static_cast<uint32_t>(!inside || id == p.padding ? p.V : id);
+  };
+  // frequent ids would queue up at their word
+  const auto set_hit = [&](int key) {
+    if (key < p.V && !(__ldcg(p.hit + (key >> 5)) >> (key & 31) & 1)) atomicOr(p.hit + (key >> 5), 1u << (key & 31));
+  };
+  uint64_t held[SHARED ? kSortEach : 1];  // entries of a pass, and their places among the warp's of that digit
+  int place[SHARED ? kSortEach : 1];
+  if constexpr (SHARED) {
+#pragma unroll
+    for (int j = 0; j < kSortEach; ++j) {
+      const int64_t i = from + j * 32 + lane;
+      held[j] = i < to ? first_entry(i) : 0;
+    }
+  }
+  if (CTAS > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // every CTA runs
   for (int pass = 0; pass < p.passes; ++pass) {
-    // the last pass ends in array 0; pass 0 reads the ids themselves
-    const int to_array = (p.passes - 1 - pass) & 1;
-    const int* keys = p.keys[to_array ^ 1];
-    const int* tokens = p.tokens[to_array ^ 1];
     const int shift = pass * p.digit;
-    const auto key_of = [&](int64_t i) -> int {
-      if (pass > 0) return __ldcg(keys + i);
-      const int64_t id = id_at(p.ids, p.ids32, i);
-      return id < 0 || id >= p.V || id == p.padding ? p.V : static_cast<int>(id);
+    const bool last = pass == p.passes - 1;
+    // in global memory the passes go to and fro, and the last one ends in array 0
+    const bool to_first = ((p.passes - 1 - pass) & 1) == 0;
+    int* const keys_to = to_first ? p.keys[0] : p.keys[1];
+    int* const tokens_to = to_first ? p.tokens[0] : p.tokens[1];
+    const int* const keys_from = to_first ? p.keys[1] : p.keys[0];
+    const int* const tokens_from = to_first ? p.tokens[1] : p.tokens[0];
+    const auto entry = [&](int64_t i) -> uint64_t {
+      if (pass == 0) return first_entry(i);
+      return static_cast<uint64_t>(__ldcg(tokens_from + i)) << 32 | static_cast<uint32_t>(__ldcg(keys_from + i));
     };
+    const auto digit_of = [&](uint64_t e) { return static_cast<int>(static_cast<uint32_t>(e) >> shift) & (digits - 1); };
     for (int d = lane; d < digits; d += 32) own[d] = 0;
     __syncwarp();
-    for (int64_t i0 = from; i0 < to; i0 += 32) {
-      const int64_t i = i0 + lane;
-      const bool valid = i < to;
-      const int key = valid ? key_of(i) : 0;
-      if (pass == 0 && valid) {
-        const int64_t id = id_at(p.ids, p.ids32, i);
-        if (id < 0 || id >= p.V) bits |= FLCE_STATUS_BIT_TARGET_RANGE;
-        // (frequent ids would queue up at their word)
-        if (p.hit != nullptr && key < p.V && !(__ldcg(p.hit + (key >> 5)) >> (key & 31) & 1))
-          atomicOr(p.hit + (key >> 5), 1u << (key & 31));
+    if constexpr (SHARED) {
+      if (pass > 0) {
+#pragma unroll
+        for (int j = 0; j < kSortEach; ++j) {
+          const int64_t i = from + j * 32 + lane;
+          if (i < to) held[j] = list[i - cta_from];
+        }
       }
-      const int d = valid ? (key >> shift) & (digits - 1) : -1;
-      const unsigned same = __match_any_sync(0xffffffffu, d);
-      if (valid && lane == __ffs(same) - 1) own[d] += __popc(same);
-      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < kSortEach; ++j) {
+        if (from + j * 32 >= to) break;
+        const bool valid = from + j * 32 + lane < to;
+        const int d = valid ? digit_of(held[j]) : -1;
+        const unsigned same = __match_any_sync(0xffffffffu, d);
+        place[j] = valid ? own[d] + __popc(same & ((1u << lane) - 1)) : 0;
+        __syncwarp();
+        if (valid && lane == __ffs(same) - 1) own[d] += __popc(same);
+        __syncwarp();
+      }
+    } else {
+      for (int64_t i0 = from; i0 < to; i0 += 32) {
+        const bool valid = i0 + lane < to;
+        const int d = valid ? digit_of(entry(i0 + lane)) : -1;
+        const unsigned same = __match_any_sync(0xffffffffu, d);
+        if (valid && lane == __ffs(same) - 1) own[d] += __popc(same);
+        __syncwarp();
+      }
     }
     __syncthreads();
-    // counts of the CTA's warps become those before each, and the CTA's totals
+    // counts of the CTA's warps become those before each; every CTA gets this one's totals
     for (int d = threadIdx.x; d < digits; d += kSortThreads) {
       int sum = 0;
-      for (int w = 0; w < kSortWarps; ++w) {
-        const int c = counts[w * digits + d];
-        counts[w * digits + d] = sum;
-        sum += c;
+#pragma unroll
+      for (int w0 = 0; w0 < kSortWarps; w0 += 16) {
+        int c[16];  // read before any is written: the compiler cannot tell the words apart
+#pragma unroll
+        for (int w = 0; w < 16; ++w) c[w] = counts[(w0 + w) * digits + d];
+#pragma unroll
+        for (int w = 0; w < 16; ++w) {
+          counts[(w0 + w) * digits + d] = sum;
+          sum += c[w];
+        }
       }
-      totals[d] = sum;
+      if (CTAS == 1) totals[d] = sum;
+#pragma unroll
+      for (int r = 0; r < CTAS && CTAS > 1; ++r)
+        store_cluster_s32(map_to_cta(smem_addr(totals + rank * digits + d), r), sum);
     }
-    cluster_sync_all();
+    // (and the bits of `hit` are cleared, before any CTA sets one; all have read their part of `list`)
+    if (CTAS > 1)
+      cluster_sync_all();
+    else
+      __syncthreads();
     // where a digit's keys start: after all smaller digits, and those of the CTAs before
     int before = 0, all = 0;
     const int d = threadIdx.x;  // digits <= threads
     if (d < digits) {
-      for (unsigned r = 0; r < ctas; ++r) {
-        int c;
-        asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(c) : "r"(map_to_cta(smem_addr(totals + d), r)) : "memory");
+#pragma unroll
+      for (int r = 0; r < CTAS; ++r) {
+        const int c = totals[r * digits + d];
         if (r < rank) before += c;
         all += c;
       }
@@ -191,36 +255,65 @@ __global__ void __launch_bounds__(kSortThreads) token_sort_kernel(const SortPara
     }
     if (lane == 31) warp_sums[warp] = scan;
     __syncthreads();
-    int start = scan - all + before;
-    for (int w = 0; w < warp; ++w) start += warp_sums[w];
-    if (d < digits)
-      for (int w = 0; w < kSortWarps; ++w) counts[w * digits + d] += start;
+    int sum = lane < warp ? warp_sums[lane] : 0;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (d < digits) starts[d] = scan - all + before + sum;
     __syncthreads();
-    for (int64_t i0 = from; i0 < to; i0 += 32) {
-      const int64_t i = i0 + lane;
-      const bool valid = i < to;
-      const int key = valid ? key_of(i) : 0;
-      const int digit = valid ? (key >> shift) & (digits - 1) : -1;
-      const unsigned same = __match_any_sync(0xffffffffu, digit);
-      int at = 0;
-      if (valid) at = own[digit] + __popc(same & ((1u << lane) - 1));
-      __syncwarp();
-      if (valid && lane == __ffs(same) - 1) own[digit] += __popc(same);
-      if (valid) {
-        p.keys[to_array][at] = key;
-        p.tokens[to_array][at] = pass > 0 ? __ldcg(tokens + i) : static_cast<int>(i);
+    if constexpr (SHARED) {
+#pragma unroll
+      for (int j = 0; j < kSortEach; ++j) {
+        const int64_t i = from + j * 32 + lane;
+        if (i >= to) break;
+        const uint64_t e = held[j];
+        const int digit = digit_of(e), at = starts[digit] + own[digit] + place[j];
+        if (last) {
+          p.keys[0][at] = static_cast<int>(e);
+          p.tokens[0][at] = static_cast<int>(e >> 32);
+        } else if (CTAS == 1) {
+          list[at] = e;
+        } else {
+          const unsigned cta = static_cast<unsigned>(at) / static_cast<unsigned>(p.room);
+          store_cluster_u64(map_to_cta(smem_addr(list + (at - cta * p.room)), cta), e);
+        }
       }
-      __syncwarp();
+      if (pass == 0 && p.hit != nullptr) {
+#pragma unroll
+        for (int j = 0; j < kSortEach; ++j)
+          if (from + j * 32 + lane < to) set_hit(static_cast<int>(held[j]));
+      }
+    } else {
+      for (int64_t i0 = from; i0 < to; i0 += 32) {
+        const bool valid = i0 + lane < to;
+        const uint64_t e = valid ? entry(i0 + lane) : 0;
+        const int digit = valid ? digit_of(e) : -1;
+        const unsigned same = __match_any_sync(0xffffffffu, digit);
+        int at = 0;
+        if (valid) at = starts[digit] + own[digit] + __popc(same & ((1u << lane) - 1));
+        __syncwarp();
+        if (valid && lane == __ffs(same) - 1) own[digit] += __popc(same);
+        if (valid) {
+          keys_to[at] = static_cast<int>(e);
+          tokens_to[at] = static_cast<int>(e >> 32);
+          if (pass == 0 && p.hit != nullptr) set_hit(static_cast<int>(e));
+        }
+        __syncwarp();
+      }
     }
-    cluster_sync_all();  // every CTA's keys are in place, and its totals have been read
+    // the keys are in place, and the totals have been read; after the last pass nobody looks
+    if (CTAS == 1)
+      __syncthreads();
+    else if (!last)
+      cluster_sync_all();
   }
   if (bits != 0 && p.status != nullptr) atomicOr(p.status, bits);
 }
 
 // ---------------------------------------------------------------- sums
 
-constexpr int kTile = 32;          // sorted tokens of a tile
-constexpr int kSumThreads = 128;
+constexpr int kTile = 32;          // sorted tokens of a tile: one a lane
+constexpr int kSumWarps = 4;
+constexpr int kAhead = 8;          // tokens whose rows are loaded at a time
 
 struct SumParams {
   const void* grad_y;
@@ -230,179 +323,368 @@ struct SumParams {
   const int* tokens;
   const uint32_t* hit;  // null: rows without tokens are not written
   float* table;
-  float* partial;       // [tiles][2][H]: what a tile has of an id that began before it, and of one that goes on
+  float* partial;       // [tiles][2][H]: of an id that began before a tile, and of one that goes on after it
+  int* joins;           // [tiles]: whether an id begins in it that goes on past the next one
   int accumulate;
   float scale;
-  int tiles, columns;   // the grid's tiles, and its pieces of a row
+  int tiles, columns;   // tiles, and pieces of a row, each a warp's
+  unsigned zero_ctas;   // the grid's first, which write zeros
+  // without sorting
+  const void* ids;
+  int ids32;
+  int64_t padding;
+  int* status;
 };
 
-// One tile's columns by each CTA; the CTAs after those write zeros to the table's rows that
-// get nothing.  A thread has GROUPS times E columns and goes through the tile's tokens in
-// order.
+__device__ __forceinline__ void write_zeros(float* row, int64_t H, int lane, bool vectors) {
+  if (vectors) {
+    for (int64_t h = lane * 4; h < H; h += 128) __stcs(reinterpret_cast<float4*>(row + h), make_float4(0, 0, 0, 0));
+  } else {
+    for (int64_t h = lane; h < H; h += 32) __stcs(row + h, 0.f);
+  }
+}
+
+// A read that stays where it is written, so that several are on their way before the first
+// is waited for (the compiler would move each to its use: 8 rows one after another took
+// 5700 cycles a warp).
+template <typename T, int E>
+__device__ __forceinline__ Elems<T, E> load_now(const T* p) {
+  Elems<T, E> r;
+  if constexpr (E > 1) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    r = *reinterpret_cast<const Elems<T, E>*>(&v);
+  } else if constexpr (sizeof(T) == 4) {
+    asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(*reinterpret_cast<float*>(&r.v[0])) : "l"(p));
+  } else {
+    asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(*reinterpret_cast<uint16_t*>(&r.v[0])) : "l"(p));
+  }
+  return r;
+}
+
+// A lane's columns of one row: GROUPS times E, 32 * E apart.  `at`: where they are in any
+// row; a lane past the row's end reads the row's last columns.
 template <typename T, int E, int GROUPS>
-__global__ void __launch_bounds__(kSumThreads) embedding_sum_kernel(const SumParams p) {
-  constexpr int kAhead = 8 / GROUPS < 1 ? 1 : 8 / GROUPS;  // tokens that are loaded at a time
-  __shared__ int keys[kTile + 2], tokens[kTile];
-  grid_dependency_wait();
-  if (blockIdx.x >= static_cast<unsigned>(p.tiles) * p.columns) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int first = (blockIdx.x - p.tiles * p.columns) * (kSumThreads / 32) + warp;
-    const int step = (gridDim.x - p.tiles * p.columns) * (kSumThreads / 32);
-    for (int64_t v = first; v < p.V; v += step) {
-      if (__ldg(p.hit + (v >> 5)) >> (v & 31) & 1) continue;
-      float* row = p.table + v * p.H;
+struct Columns {
+  Elems<T, E> v[GROUPS];
+  __device__ __forceinline__ void load(const T* row, const int (&at)[GROUPS]) {
+#pragma unroll
+    for (int g = 0; g < GROUPS; ++g) v[g] = load_now<T, E>(row + at[g]);
+  }
+};
+template <int E, int GROUPS>
+__device__ __forceinline__ void columns_at(int64_t first, int64_t H, int (&at)[GROUPS]) {
+#pragma unroll
+  for (int g = 0; g < GROUPS; ++g) {
+    const int64_t h = first + g * 32 * E;
+    at[g] = static_cast<int>(h < H ? h : H - E);
+  }
+}
+
+template <int E, int GROUPS>
+struct Sums {
+  float s[GROUPS][E];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int g = 0; g < GROUPS; ++g)
+#pragma unroll
+      for (int k = 0; k < E; ++k) s[g][k] = 0.f;
+  }
+  template <typename T>
+  __device__ __forceinline__ void add(const Columns<T, E, GROUPS>& c) {
+#pragma unroll
+    for (int g = 0; g < GROUPS; ++g)
+#pragma unroll
+      for (int k = 0; k < E; ++k) s[g][k] += to_float(c.v[g].v[k]);
+  }
+  // To a row of fp32, times `scale`; `add`: by the memory system, which nothing waits for
+  // (an element gets one such addition in a call, so that their order is no matter).
+  __device__ __forceinline__ void store(float* row, int64_t first, int64_t H, float scale, bool add) const {
+#pragma unroll
+    for (int g = 0; g < GROUPS; ++g) {
+      const int64_t h = first + g * 32 * E;
+      if (h >= H) break;
       if constexpr (E > 1) {
-        for (int64_t h = lane * 4; h < p.H; h += 128) __stcs(reinterpret_cast<float4*>(row + h), make_float4(0, 0, 0, 0));
+#pragma unroll
+        for (int q = 0; q < E; q += 4) {
+          const float4 o = make_float4(s[g][q] * scale, s[g][q + 1] * scale, s[g][q + 2] * scale, s[g][q + 3] * scale);
+          float4* at = reinterpret_cast<float4*>(row + h + q);
+          if (add)
+            red_add_f32x4(at, o);
+          else
+            *at = o;
+        }
       } else {
-        for (int64_t h = lane; h < p.H; h += 32) __stcs(row + h, 0.f);
+        if (add)
+          atomicAdd(row + h, s[g][0] * scale);
+        else
+          row[h] = s[g][0] * scale;
       }
     }
+  }
+};
+
+// One tile's columns by each warp: a lane holds the tile's keys and those of the next one,
+// and all go through the tokens in order, kAhead rows on their way.  An id that ends in the
+// next tile is finished by the tile in which it begins, so that partial rows are left for
+// ids of more than kTile tokens alone.
+template <typename T, int E, int GROUPS>
+__global__ void __launch_bounds__(32 * kSumWarps, 6) embedding_sum_kernel(const SumParams p) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  grid_dependency_wait();
+  if (blockIdx.x < p.zero_ctas) {
+    for (int64_t v = static_cast<int64_t>(blockIdx.x) * kSumWarps + warp; v < p.V; v += p.zero_ctas * kSumWarps)
+      if (!(__ldg(p.hit + (v >> 5)) >> (v & 31) & 1)) write_zeros(p.table + v * p.H, p.H, lane, E > 1);
     return;
   }
-  const int tile = blockIdx.x / p.columns, column = blockIdx.x % p.columns;
+  const int64_t item = static_cast<int64_t>(blockIdx.x - p.zero_ctas) * kSumWarps + warp;
+  if (item >= static_cast<int64_t>(p.tiles) * p.columns) return;
+  const int tile = static_cast<int>(item / p.columns), column = static_cast<int>(item % p.columns);
   const int64_t begin = static_cast<int64_t>(tile) * kTile;
-  const int count = static_cast<int>(p.N - begin < kTile ? p.N - begin : kTile);
-  // keys[0] and keys[count + 1] are the neighbours' (-1 beyond the list)
-  for (int i = threadIdx.x; i < count + 2; i += kSumThreads) {
-    const int64_t at = begin + i - 1;
-    keys[i] = at >= 0 && at < p.N ? p.keys[at] : -1;
+  const auto key_at = [&](int64_t i) { return i >= 0 && i < p.N ? __ldg(p.keys + i) : -1; };
+  const int k0 = key_at(begin + lane), k1 = key_at(begin + kTile + lane);
+  const int token0 = begin + lane < p.N ? __ldg(p.tokens + begin + lane) : 0;
+  const int token1 = begin + kTile + lane < p.N ? __ldg(p.tokens + begin + kTile + lane) : 0;
+  // neighbours: the key before this tile, before the tile before, and after the next one
+  const int around = key_at(lane == 0 ? begin - 1 : lane == 1 ? begin - 1 - kTile : begin + 2 * kTile);
+  const int before = __shfl_sync(0xffffffffu, around, 0), long_before = __shfl_sync(0xffffffffu, around, 1);
+  const int after = __shfl_sync(0xffffffffu, around, 2);
+  const int head = __shfl_sync(0xffffffffu, k0, 0), tail = __shfl_sync(0xffffffffu, k0, kTile - 1);
+  const int next = __shfl_sync(0xffffffffu, k1, 0);
+  // bit i: token i is its id's last one (places beyond the list, and tokens that add
+  // nothing, have keys of -1 and V and end it)
+  int up = __shfl_down_sync(0xffffffffu, k0, 1);
+  const unsigned ends0 = __ballot_sync(0xffffffffu, k0 != (lane == 31 ? next : up));
+  up = __shfl_down_sync(0xffffffffu, k1, 1);
+  const unsigned ends1 = __ballot_sync(0xffffffffu, k1 != (lane == 31 ? after : up));
+  const unsigned used0 = __ballot_sync(0xffffffffu, k0 >= 0 && k0 < p.V);
+  int to = __popc(used0);  // tokens of this tile (they come first)
+  if (to == 0) {
+    if (column == 0 && lane == 0) p.joins[tile] = 0;
+    return;
   }
-  for (int i = threadIdx.x; i < count; i += kSumThreads) tokens[i] = p.tokens[begin + i];
-  __syncthreads();
-  const int64_t first = (static_cast<int64_t>(column) * GROUPS * kSumThreads + threadIdx.x) * E;
-  float sum[GROUPS][E];
+  int from = 0;
+  bool head_partial = false, tail_partial = false;
+  if (before == head) {
+    // the id began before: the tile before has finished it if it began there and ends here
+    const bool ends_here = ends0 != 0;
+    if (long_before != head && ends_here)
+      from = __ffs(ends0);
+    else
+      head_partial = true;
+  }
+  const bool one_id = ends0 == 0;  // and it goes on
+  if (to == kTile && next == tail && !(one_id && before == head)) {
+    if (ends1 != 0)
+      to += __ffs(ends1);          // ends in the next tile
+    else
+      tail_partial = true;
+  }
+  if (column == 0 && lane == 0) p.joins[tile] = tail_partial;
+  if (from >= to) return;
+  const uint64_t ends = static_cast<uint64_t>(ends1) << 32 | ends0;
+  const int64_t first = (static_cast<int64_t>(column) * GROUPS * 32 + lane) * E;
+  const T* rows = static_cast<const T*>(p.grad_y);
+  int at[GROUPS];
+  columns_at<E, GROUPS>(first, p.H, at);
+  Sums<E, GROUPS> sum;
+  sum.clear();
+  float* const partial = p.partial + static_cast<int64_t>(tile) * 2 * p.H;
+  Columns<T, E, GROUPS> held[kAhead];
+  for (int t0 = from & ~(kAhead - 1); t0 < to; t0 += kAhead) {
+    const int token = t0 < kTile ? token0 : token1;
 #pragma unroll
-  for (int g = 0; g < GROUPS; ++g)
-#pragma unroll
-    for (int k = 0; k < E; ++k) sum[g][k] = 0.f;
-  int start = 0;  // where the present id's tokens start
-  for (int t0 = 0; t0 < count; t0 += kAhead) {
-    Elems<T, E> v[kAhead][GROUPS];
-#pragma unroll
-    for (int a = 0; a < kAhead; ++a) {
-      if (t0 + a < count && keys[t0 + a + 1] < p.V) {
-        const T* row = static_cast<const T*>(p.grad_y) + tokens[t0 + a] * p.ld;
-#pragma unroll
-        for (int g = 0; g < GROUPS; ++g) {
-          const int64_t h = first + static_cast<int64_t>(g) * kSumThreads * E;
-          if (h < p.H) v[a][g] = *reinterpret_cast<const Elems<T, E>*>(row + h);
-        }
-      }
+    for (int a = 0; a < kAhead; ++a) {  // places beyond the list: token 0's row
+      const int64_t n = __shfl_sync(0xffffffffu, token, (t0 + a) & 31);
+      held[a].load(rows + n * p.ld, at);
     }
 #pragma unroll
     for (int a = 0; a < kAhead; ++a) {
       const int t = t0 + a;
-      if (t >= count) break;
-      const int key = keys[t + 1];
-      if (key >= p.V) break;  // tokens that add nothing end the list
-#pragma unroll
-      for (int g = 0; g < GROUPS; ++g)
-#pragma unroll
-        for (int k = 0; k < E; ++k) sum[g][k] += to_float(v[a][g].v[k]);
-      if (t + 1 < count && keys[t + 2] == key) continue;
-      // the id's last token in this tile
-      const bool began_before = start == 0 && keys[0] == key, goes_on = keys[t + 2] == key;
-      float* to;
-      if (began_before || goes_on)
-        to = p.partial + (static_cast<int64_t>(tile) * 2 + (began_before ? 0 : 1)) * p.H;
-      else
-        to = p.table + key * p.H;
-      const bool whole = !began_before && !goes_on;
-#pragma unroll
-      for (int g = 0; g < GROUPS; ++g) {
-        const int64_t h = first + static_cast<int64_t>(g) * kSumThreads * E;
-        if (h < p.H) {
-          if constexpr (E > 1) {
-#pragma unroll
-            for (int q = 0; q < E; q += 4) {
-              float4* at = reinterpret_cast<float4*>(to + h + q);
-              float4 o = make_float4(sum[g][q], sum[g][q + 1], sum[g][q + 2], sum[g][q + 3]);
-              if (whole) {
-                o = make_float4(o.x * p.scale, o.y * p.scale, o.z * p.scale, o.w * p.scale);
-                if (p.accumulate) {
-                  const float4 old = *at;
-                  o = make_float4(old.x + o.x, old.y + o.y, old.z + o.z, old.w + o.w);
-                }
-              }
-              *at = o;
-            }
-          } else {
-            float o = sum[g][0];
-            if (whole) {
-              o *= p.scale;
-              if (p.accumulate) o += to[h];
-            }
-            to[h] = o;
-          }
-        }
-#pragma unroll
-        for (int k = 0; k < E; ++k) sum[g][k] = 0.f;
+      if (t < from || t >= to) continue;
+      sum.add(held[a]);
+      if (!(ends >> t & 1)) continue;
+      if (head_partial) {
+        sum.store(partial, first, p.H, 1.f, false);
+        head_partial = false;
+      } else {
+        const int key = __shfl_sync(0xffffffffu, t < kTile ? k0 : k1, t & 31);
+        sum.store(p.table + key * p.H, first, p.H, p.scale, p.accumulate != 0);
       }
-      start = t + 1;
+      sum.clear();
     }
   }
+  if (head_partial)  // one id, that goes on
+    sum.store(partial, first, p.H, 1.f, false);
+  else if (tail_partial)
+    sum.store(partial + p.H, first, p.H, 1.f, false);
 }
 
 constexpr int kJoinWarps = 8;
+constexpr int kJoinTiles = 8;
 
-// Adds up the partial rows of an id that goes over several tiles, in the order of the
-// tiles: each warp a stretch of them, then the warps' sums.  A CTA has 32 * E columns and
-// looks at tiles for such ids that begin there.
+// Adds up the partial rows of ids that begin in a tile and go on past the next one, in the
+// order of the tiles: each warp a stretch of them, then the warps' sums.  A CTA has 32 * E
+// columns and looks for such ids in kJoinTiles tiles at a time, one a lane.
 template <int E>
 __global__ void __launch_bounds__(32 * kJoinWarps) embedding_join_kernel(const SumParams p) {
-  using V = Elems<float, E>;
-  __shared__ V sums[kJoinWarps][32];
+  using Part = Elems<float, E>;
+  __shared__ Part sums[kJoinWarps][32];
+  __shared__ int last_tile;
   grid_dependency_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t h = (static_cast<int64_t>(blockIdx.y) * 32 + lane) * E;
-  for (int tile = blockIdx.x; tile < p.tiles; tile += gridDim.x) {
-    const int64_t begin = static_cast<int64_t>(tile) * kTile, end = begin + kTile;
-    if (end >= p.N) return;
-    const int key = __ldg(p.keys + end - 1);
-    if (key >= p.V || __ldg(p.keys + end) != key) continue;  // nothing goes on
-    if (begin > 0 && __ldg(p.keys + begin) == key && __ldg(p.keys + begin - 1) == key) continue;  // it began before
-    // the id's last token, by bisection: keys[low] == key
-    int64_t low = end, high = p.N;
-    while (high - low > 1) {
-      const int64_t mid = low + (high - low) / 2;
-      if (__ldg(p.keys + mid) == key)
-        low = mid;
-      else
-        high = mid;
-    }
-    const int parts = static_cast<int>(low / kTile) - tile + 1;
-    const int each = (parts + kJoinWarps - 1) / kJoinWarps;
-    V sum = {};
-    if (h < p.H) {
-      const int to = (warp + 1) * each < parts ? (warp + 1) * each : parts;
+  const auto key_at = [&](int64_t i) { return i >= 0 && i < p.N ? __ldg(p.keys + i) : -1; };
+  for (int tile0 = blockIdx.x * kJoinTiles; tile0 < p.tiles; tile0 += gridDim.x * kJoinTiles) {
+    const bool joins = lane < kJoinTiles && tile0 + lane < p.tiles && __ldg(p.joins + tile0 + lane) != 0;
+    unsigned left = __ballot_sync(0xffffffffu, joins);
+    while (left != 0) {  // the same in every warp
+      const int tile = tile0 + __ffs(left) - 1;
+      left &= left - 1;
+      const int key = key_at(static_cast<int64_t>(tile) * kTile + kTile - 1);
+      // the tile in which the id ends: the first whose last key is another
+      if (threadIdx.x == 0) last_tile = p.tiles - 1;
+      __syncthreads();
+      for (int t0 = tile + 1;; t0 += 32 * kJoinWarps) {
+        const int t = t0 + threadIdx.x;
+        const bool ends = t >= p.tiles - 1 || key_at(static_cast<int64_t>(t) * kTile + kTile) != key;
+        if (ends && t < p.tiles) atomicMin(&last_tile, t);
+        if (__syncthreads_or(ends)) break;
+      }
+      const int parts = last_tile - tile + 1, each = (parts + kJoinWarps - 1) / kJoinWarps;
+      Part sum = {};
+      if (h < p.H) {
+        const int to = (warp + 1) * each < parts ? (warp + 1) * each : parts;
 #pragma unroll 8
-      for (int i = warp * each; i < to; ++i) {
-        const V v = *reinterpret_cast<const V*>(p.partial + (static_cast<int64_t>(tile + i) * 2 + (i == 0)) * p.H + h);
+        for (int i = warp * each; i < to; ++i) {
+          const Part v =
+              *reinterpret_cast<const Part*>(p.partial + (static_cast<int64_t>(tile + i) * 2 + (i == 0)) * p.H + h);
 #pragma unroll
-        for (int k = 0; k < E; ++k) sum.v[k] += v.v[k];
+          for (int k = 0; k < E; ++k) sum.v[k] += v.v[k];
+        }
       }
-    }
-    sums[warp][lane] = sum;
-    __syncthreads();
-    if (warp == 0 && h < p.H) {
-      V* at = reinterpret_cast<V*>(p.table + key * p.H + h);
-      V out = {};
-      if (p.accumulate) out = *at;
+      sums[warp][lane] = sum;
+      __syncthreads();
+      if (warp == 0 && h < p.H) {
+        Part* at = reinterpret_cast<Part*>(p.table + key * p.H + h);
+        Part out = {};
+        if (p.accumulate) out = *at;
 #pragma unroll
-      for (int k = 0; k < E; ++k) {
-        float total = 0.f;
+        for (int k = 0; k < E; ++k) {
+          float total = 0.f;
 #pragma unroll
-        for (int w = 0; w < kJoinWarps; ++w) total += sums[w][lane].v[k];
-        out.v[k] += total * p.scale;
+          for (int w = 0; w < kJoinWarps; ++w) total += sums[w][lane].v[k];
+          out.v[k] += total * p.scale;
+        }
+        *at = out;
       }
-      *at = out;
+      __syncthreads();
     }
-    __syncthreads();
   }
 }
 
+// ---------------------------------------------------------------- few tokens
+
+constexpr int kFewTokens = 1024;
+constexpr int kFewWarps = 4;
+constexpr int kFewZeroRows = 32;  // rows of the table that a CTA looks after
+
+// Without sorting, in one launch: a CTA for each token and piece of a row compares the
+// token's id with all others; the first token of an id adds up its rows, each warp every
+// kFewWarps-th one of them, and then the warps' sums.  The CTAs after those write zeros to
+// rows that no token has.
+template <typename T, int E, int GROUPS>
+__global__ void __launch_bounds__(32 * kFewWarps) embedding_few_kernel(const SumParams p) {
+  __shared__ unsigned match[kFewTokens / 32];
+  __shared__ unsigned hit;
+  __shared__ Sums<E, GROUPS> sums[kFewWarps][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const unsigned sum_ctas = static_cast<unsigned>(p.N) * p.columns;
+  const auto key_of = [&](int i) -> int64_t {
+    const int64_t id = i < p.N ? id_at(p.ids, p.ids32, i) : -1;
+    return id == p.padding || id >= p.V ? -1 : id;
+  };
+  if (blockIdx.x >= sum_ctas) {
+    const int64_t v0 = static_cast<int64_t>(blockIdx.x - sum_ctas) * kFewZeroRows;
+    if (threadIdx.x == 0) hit = 0;
+    __syncthreads();
+    unsigned mine = 0;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < p.N; i += 32 * kFewWarps) {
+      const int64_t at = key_of(i) - v0;
+      if (at >= 0 && at < kFewZeroRows) mine |= 1u << at;
+    }
+    if (mine != 0) atomicOr(&hit, mine);
+    __syncthreads();
+    for (int r = warp; r < kFewZeroRows && v0 + r < p.V; r += kFewWarps)
+      if (!(hit >> r & 1)) write_zeros(p.table + (v0 + r) * p.H, p.H, lane, E > 1);
+    return;
+  }
+  const int n = blockIdx.x / p.columns, column = blockIdx.x % p.columns;
+  const int64_t key = key_of(n);
+  if (p.status != nullptr && column == 0 && threadIdx.x == 0) {
+    const int64_t id = id_at(p.ids, p.ids32, n);
+    if (id < 0 || id >= p.V) atomicOr(p.status, FLCE_STATUS_BIT_TARGET_RANGE);
+  }
+  if (key < 0) return;
+  const int words = (p.N + 31) / 32;
+  for (int w = warp; w < words; w += kFewWarps) {
+    const unsigned same = __ballot_sync(0xffffffffu, key_of(w * 32 + lane) == key);
+    if (lane == 0) match[w] = same;
+  }
+  __syncthreads();
+  // an earlier token of the id?  (the first word that has one decides, for all lanes)
+  for (int w = 0; w <= n / 32; ++w) {
+    const unsigned earlier = w == n / 32 ? match[w] & ((1u << (n & 31)) - 1) : match[w];
+    if (earlier != 0) return;
+  }
+  const int64_t first = (static_cast<int64_t>(column) * GROUPS * 32 + lane) * E;
+  const T* rows = static_cast<const T*>(p.grad_y);
+  Sums<E, GROUPS> sum;
+  sum.clear();
+  int at[GROUPS];
+  columns_at<E, GROUPS>(first, p.H, at);
+  int count = 0;  // tokens of the id so far
+  constexpr int kFewAhead = 4;
+  Columns<T, E, GROUPS> held[kFewAhead];
+  int holding = 0;
+  for (int w = n / 32; w < words; ++w) {
+    for (unsigned m = match[w]; m != 0; m &= m - 1, ++count) {
+      if (count % kFewWarps != warp) continue;
+      const int64_t t = w * 32 + __ffs(m) - 1;
+#pragma unroll
+      for (int a = 0; a < kFewAhead; ++a)
+        if (a == holding) held[a].load(rows + t * p.ld, at);
+      if (++holding == kFewAhead) {
+#pragma unroll
+        for (int a = 0; a < kFewAhead; ++a) sum.add(held[a]);
+        holding = 0;
+      }
+    }
+  }
+#pragma unroll
+  for (int a = 0; a < kFewAhead; ++a)
+    if (a < holding) sum.add(held[a]);
+  if (count > 1) {
+    sums[warp][lane] = sum;
+    __syncthreads();
+    if (warp != 0) return;
+#pragma unroll
+    for (int w = 1; w < kFewWarps; ++w)
+#pragma unroll
+      for (int g = 0; g < GROUPS; ++g)
+#pragma unroll
+        for (int k = 0; k < E; ++k) sum.s[g][k] += sums[w][lane].s[g][k];
+  } else if (warp != 0) {
+    return;
+  }
+  sum.store(p.table + key * p.H, first, p.H, p.scale, p.accumulate != 0);
+}
+
 struct EmbeddingLayout {
-  size_t keys[2], tokens[2], hit, partial, total;
+  size_t keys[2], tokens[2], hit, joins, partial, total;
 };
 
 bool embedding_layout(int64_t N, int64_t V, int64_t H, EmbeddingLayout* at) {
@@ -411,9 +693,40 @@ bool embedding_layout(int64_t N, int64_t V, int64_t H, EmbeddingLayout* at) {
   const size_t list = align_up(static_cast<size_t>(N) * 4, 256);
   at->keys[0] = 0, at->keys[1] = list, at->tokens[0] = 2 * list, at->tokens[1] = 3 * list;
   at->hit = 4 * list;
-  at->partial = align_up(at->hit + static_cast<size_t>(div_up(V, 32)) * 4, 256);
+  at->joins = align_up(at->hit + static_cast<size_t>(div_up(V, 32)) * 4, 256);
+  at->partial = align_up(at->joins + static_cast<size_t>(div_up(N, kTile)) * 4, 256);
   at->total = align_up(at->partial + static_cast<size_t>(div_up(N, kTile)) * 2 * H * 4, 256);
   return true;
+}
+
+template <int CTAS, bool SHARED>
+cudaError_t launch_sort(SortParams p, cudaStream_t s) {
+  p.room = SHARED ? static_cast<int>(div_up(p.N, CTAS * kSortThreads) * kSortThreads) : 0;
+  const auto bytes = [](int digit, int room) {
+    return static_cast<size_t>(kSortWarps + CTAS + 1) * (size_t(1) << digit) * sizeof(int) +
+           static_cast<size_t>(room) * sizeof(uint64_t);
+  };
+  static int configured[64] = {0};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64 || !configured[dev]) {
+    const cudaError_t e = cudaFuncSetAttribute(token_sort_kernel<CTAS, SHARED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(bytes(kSortDigit, SHARED ? kSortRoom : 0)));
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) configured[dev] = 1;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(CTAS);
+  cfg.blockDim = dim3(kSortThreads);
+  cfg.dynamicSmemBytes = bytes(p.digit, p.room);
+  cfg.stream = s;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = CTAS;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = CTAS > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, token_sort_kernel<CTAS, SHARED>, p);
 }
 
 cudaError_t sort_tokens(SortParams p, cudaStream_t s) {
@@ -421,45 +734,40 @@ cudaError_t sort_tokens(SortParams p, cudaStream_t s) {
   while ((int64_t(1) << bits) <= p.V) ++bits;  // keys go up to V
   p.passes = (bits + kSortDigit - 1) / kSortDigit;
   p.digit = (bits + p.passes - 1) / p.passes;
-  const size_t smem = (static_cast<size_t>(kSortWarps) + 1) * (size_t(1) << p.digit) * sizeof(int);
-  static int configured[64] = {0};
-  int dev = 0;
-  cudaGetDevice(&dev);
-  if (dev < 0 || dev >= 64 || !configured[dev]) {
-    const cudaError_t e = cudaFuncSetAttribute(token_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (kSortWarps + 1) * (1 << kSortDigit) * static_cast<int>(sizeof(int)));
-    if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < 64) configured[dev] = 1;
-  }
-  const int ctas = p.N <= 4096 ? 1 : 8;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas);
-  cfg.blockDim = dim3(kSortThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = ctas;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
   prof_begin(s, FLCE_KERNEL_TOKEN_SORT);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, token_sort_kernel, p);
+  const cudaError_t e = p.N <= kSortRoom               ? launch_sort<1, true>(p, s)
+                        : p.N <= kSortRoom * kSortCtas ? launch_sort<kSortCtas, true>(p, s)
+                                                       : launch_sort<kSortCtas, false>(p, s);
   prof_end(s);
   return e;
 }
 
+// Pieces of a row of H columns, each a warp's.
 template <typename T>
-cudaError_t sum_rows(SumParams p, bool vectors, cudaStream_t s) {
+int64_t row_pieces(int64_t H, bool vectors) {
+  return div_up(H, vectors ? 32 * (16 / static_cast<int64_t>(sizeof(T))) : 32 * 4);
+}
+
+template <typename T>
+cudaError_t sum_rows(SumParams p, bool vectors, bool few, cudaStream_t s) {
   constexpr int kE = 16 / sizeof(T);
-  p.columns = static_cast<int>(div_up(p.H, vectors ? kSumThreads * kE : kSumThreads * 4));
-  const int64_t ctas = static_cast<int64_t>(p.tiles) * p.columns + (p.hit != nullptr ? 8 * device_sm_count() : 0);
-  if (ctas >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
-  if (ctas == 0) return cudaSuccess;
+  p.columns = static_cast<int>(row_pieces<T>(p.H, vectors));
+  cudaError_t e;
   prof_begin(s, FLCE_KERNEL_EMBEDDING_BWD);
-  const dim3 grid(static_cast<unsigned>(ctas));
-  const cudaError_t e = vectors ? launch_after(embedding_sum_kernel<T, kE, 1>, grid, dim3(kSumThreads), s, p)
-                                : launch_after(embedding_sum_kernel<T, 1, 4>, grid, dim3(kSumThreads), s, p);
+  if (few) {
+    const int64_t ctas = static_cast<int64_t>(p.N) * p.columns + (p.accumulate ? 0 : div_up(p.V, kFewZeroRows));
+    const unsigned grid = static_cast<unsigned>(ctas);
+    if (vectors)
+      embedding_few_kernel<T, kE, 1><<<grid, 32 * kFewWarps, 0, s>>>(p);
+    else
+      embedding_few_kernel<T, 1, 4><<<grid, 32 * kFewWarps, 0, s>>>(p);
+    e = cudaGetLastError();
+  } else {
+    p.zero_ctas = p.accumulate ? 0 : static_cast<unsigned>(std::min<int64_t>(8 * device_sm_count(), div_up(p.V, kSumWarps)));
+    const dim3 grid(static_cast<unsigned>(p.zero_ctas + div_up(static_cast<int64_t>(p.tiles) * p.columns, kSumWarps)));
+    e = vectors ? launch_after(embedding_sum_kernel<T, kE, 1>, grid, dim3(32 * kSumWarps), s, p)
+                : launch_after(embedding_sum_kernel<T, 1, 4>, grid, dim3(32 * kSumWarps), s, p);
+  }
   prof_end(s);
   return e;
 }
@@ -523,11 +831,13 @@ flce_status_t embedding_bwd(int dtype, const void* grad_y, int64_t ld_grad_y, co
   if (workspace == nullptr || !aligned_to(workspace, 256) || workspace_bytes < at.total) return FLCE_ERR_WORKSPACE;
   if (N == 0 && accumulate) return FLCE_OK;
   const int64_t tiles = div_up(N, kTile);
-  if (tiles * div_up(H, kSumThreads * 4) + 8 * 1024 >= (int64_t(1) << 31) || div_up(H, 32) > 65535)
+  if (div_up(tiles * div_up(H, 128), kSumWarps) + 8 * 1024 >= (int64_t(1) << 31) || div_up(H, 32) > 65535)
     return FLCE_ERR_UNSUPPORTED;  // more CTAs than a launch has
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream_);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
 
+  // without the sort where the CTAs that compare and those that write zeros are few
+  const bool few = N <= kFewTokens;
   SortParams sort = {};
   sort.ids = ids, sort.ids32 = index_type == FLCE_INDEX_INT32;
   sort.N = static_cast<int>(N), sort.V = static_cast<int>(V), sort.padding = padding_index;
@@ -537,25 +847,27 @@ flce_status_t embedding_bwd(int dtype, const void* grad_y, int64_t ld_grad_y, co
   }
   sort.hit = accumulate ? nullptr : reinterpret_cast<uint32_t*>(ws + at.hit);
   sort.status = status_dev;
-  if (sort_tokens(sort, s) != cudaSuccess) return FLCE_ERR_CUDA;
+  if (!few && sort_tokens(sort, s) != cudaSuccess) return FLCE_ERR_CUDA;
 
   SumParams p = {};
   p.grad_y = grad_y, p.ld = ld_grad_y, p.H = H, p.N = sort.N, p.V = sort.V;
   p.keys = sort.keys[0], p.tokens = sort.tokens[0], p.hit = sort.hit;
   p.table = grad_table, p.partial = reinterpret_cast<float*>(ws + at.partial);
+  p.joins = reinterpret_cast<int*>(ws + at.joins);
   p.accumulate = accumulate, p.scale = scale, p.tiles = static_cast<int>(tiles);
+  p.ids = ids, p.ids32 = sort.ids32, p.padding = padding_index, p.status = status_dev;
   const int64_t elems = 16 / static_cast<int64_t>(esz);
   const bool vectors =
-      aligned_to(grad_y, 16) && aligned_to(grad_table, 16) && H % elems == 0 && (ld_grad_y % elems == 0 || N == 1);
-  const cudaError_t e = dtype == FLCE_DTYPE_BF16   ? sum_rows<__nv_bfloat16>(p, vectors, s)
-                        : dtype == FLCE_DTYPE_FP16 ? sum_rows<__half>(p, vectors, s)
-                                                   : sum_rows<float>(p, vectors, s);
+      aligned_to(grad_y, 16) && aligned_to(grad_table, 16) && H % elems == 0 && (ld_grad_y % elems == 0 || N <= 1);
+  const cudaError_t e = dtype == FLCE_DTYPE_BF16   ? sum_rows<__nv_bfloat16>(p, vectors, few, s)
+                        : dtype == FLCE_DTYPE_FP16 ? sum_rows<__half>(p, vectors, few, s)
+                                                   : sum_rows<float>(p, vectors, few, s);
   if (e != cudaSuccess) return FLCE_ERR_CUDA;
-  if (tiles > 1) {
+  if (!few) {
     const unsigned columns = static_cast<unsigned>(div_up(H, vectors ? 128 : 32));
-    const dim3 grid(static_cast<unsigned>(std::min<int64_t>(tiles, std::max<int64_t>(2048 / columns, 1))), columns);
     prof_begin(s, FLCE_KERNEL_EMBEDDING_JOIN);
-    const cudaError_t j = launch_after(vectors ? embedding_join_kernel<4> : embedding_join_kernel<1>, grid,
+    const cudaError_t j = launch_after(vectors ? embedding_join_kernel<4> : embedding_join_kernel<1>,
+                                       dim3(static_cast<unsigned>(std::min<int64_t>(div_up(tiles, kJoinTiles), 4096)), columns),
                                        dim3(32 * kJoinWarps), s, p);
     prof_end(s);
     if (j != cudaSuccess) return FLCE_ERR_CUDA;

@@ -84,32 +84,35 @@ __global__ void __launch_bounds__(kPairThreads) pair_loss_kernel(const PairParam
         s[k] /= count[k];
       }
     }
-    double x = s[0] - s[1];
-    if (p.ref_logp != nullptr) x -= static_cast<double>(p.ref_logp[pair]) - p.ref_logp[pair + p.pairs];
-    const double beta = p.numbers.beta;
-    double loss, slope;  // slope: dloss / dx
-    if (p.numbers.kind == FLCE_PREFERENCE_IPO) {
-      const double far = x - 1.0 / (2.0 * beta);
-      loss = far * far;
-      slope = 2.0 * far;
-    } else {
-      const double u = beta * x - p.numbers.margin;
-      if (p.numbers.kind == FLCE_PREFERENCE_HINGE) {
-        loss = u < 1.0 ? 1.0 - u : u >= 1.0 ? 0.0 : u;  // (NaN stays)
-        slope = u < 1.0 ? -beta : u >= 1.0 ? 0.0 : u;
-      } else {
-        // ln sigmoid(-u) = ln sigmoid(u) - u
-        const double e = exp(-fabs(u)), smooth = p.numbers.label_smoothing;
-        loss = fmax(-u, 0.0) + log1p(e) + (smooth != 0 ? smooth * u : 0.0);  // (u may be infinite)
-        if (isnan(u)) loss = u;
-        const double sigmoid = u >= 0 ? 1.0 / (1.0 + e) : e / (1.0 + e);
-        slope = beta * (sigmoid - (1.0 - smooth));
-      }
-    }
-    double scale = p.grad_scale;
-    if (p.reduction == FLCE_REDUCTION_MEAN) scale /= static_cast<double>(p.pairs);
-    if (p.grad_out != nullptr) scale *= p.grad_out[pair];
     if (threadIdx.x == 0) {
+      // differences of long sums in fp64, functions of the difference in fp32
+      double x = s[0] - s[1];
+      if (p.ref_logp != nullptr) x -= static_cast<double>(p.ref_logp[pair]) - p.ref_logp[pair + p.pairs];
+      const double beta = p.numbers.beta;
+      double loss, slope;  // slope: dloss / dx
+      if (p.numbers.kind == FLCE_PREFERENCE_IPO) {
+        const double far = x - 1.0 / (2.0 * beta);
+        loss = far * far;
+        slope = 2.0 * far;
+      } else {
+        const double wide = beta * x - p.numbers.margin;
+        const float u = static_cast<float>(wide);
+        if (p.numbers.kind == FLCE_PREFERENCE_HINGE) {
+          loss = wide < 1.0 ? 1.0 - wide : wide >= 1.0 ? 0.0 : wide;  // (NaN stays)
+          slope = wide < 1.0 ? -beta : wide >= 1.0 ? 0.0 : wide;
+        } else {
+          // ln sigmoid(-u) = ln sigmoid(u) - u
+          const float e = expf(-fabsf(u)), smooth = p.numbers.label_smoothing;
+          loss = fmax(-wide, 0.0) + log1pf(e) + (smooth != 0.f ? smooth * wide : 0.0);  // (u may be infinite)
+          if (isnan(u)) loss = wide;
+          const float less = u >= 0.f ? e / (1.f + e) : 1.f / (1.f + e);  // 1 - sigmoid(u)
+          slope = beta * (static_cast<double>(smooth) - less);
+        }
+      }
+      double scale = p.grad_scale;
+      if (p.reduction == FLCE_REDUCTION_MEAN) scale /= static_cast<double>(p.pairs);
+      if (p.grad_out != nullptr) scale *= p.grad_out[pair];
+      scratch[0] = slope * scale;
       p.pair_loss[pair] = loss;
       if (p.reduction == FLCE_REDUCTION_NONE) p.loss[pair] = static_cast<float>(loss);
       if (p.logp != nullptr) {
@@ -117,11 +120,14 @@ __global__ void __launch_bounds__(kPairThreads) pair_loss_kernel(const PairParam
         p.logp[pair + p.pairs] = static_cast<float>(s[1]);
       }
     }
+    __syncthreads();
+    const double slope = scratch[0];
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const float f = static_cast<float>(slope * scale / count[k] * (k == 0 ? -1.0 : 1.0));
+      const float f = static_cast<float>(slope / count[k] * (k == 0 ? -1.0 : 1.0));
       for (int64_t n = from[k] + threadIdx.x; n < to[k]; n += kPairThreads) p.factor[n] = f;
     }
+    __syncthreads();  // scratch is the next pair's
   }
   if (bits != 0 && threadIdx.x == 0) atomicOr(p.status, bits);
   if (p.reduction == FLCE_REDUCTION_NONE) return;
