@@ -16,6 +16,7 @@
 // logits about any common level keep their digits.
 #pragma once
 
+#include <atomic>
 #include <type_traits>
 
 #include "arrival.cuh"
@@ -629,11 +630,311 @@ cudaError_t launch_long(const RowLossParams& p, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, row_loss_long_kernel<T, KIND>, p);
 }
 
+// ---------------------------------------------------------------- rows by parts
+
+// A cluster of CTAs a row, each with one part of it in registers, so that a row is read
+// once.  Clusters take rows one after another; CTAs of several clusters share an SM, and
+// one computes while another waits.  A CTA's last warp leads: it brings the CTA's parts of
+// the next rows into shared memory by bulk copies, and reads what the rows have beside
+// their logits.  The other warps copy a part into registers, which frees its place, find
+// its maximum and sum, hand both to every CTA of the row (one 8-byte store a warp and CTA,
+// counted by the receiver's barrier), and write the gradient from the registers.
+constexpr int kPartSlots = 4;
+
+struct PartShape {
+  int cluster;    // CTAs of a row
+  int seg_vecs;   // vectors of a part
+  int slots;      // parts in shared memory
+  int slot_bytes;
+};
+
+__device__ __forceinline__ void bulk_copy(uint32_t to, const void* from, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(to),
+               "l"(reinterpret_cast<uint64_t>(from)), "r"(bytes), "r"(bar)
+               : "memory");
+}
+// Two floats to another CTA's shared memory, counted on its barrier.
+__device__ __forceinline__ void push_pair(uint32_t to, float a, float b, uint32_t bar) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v2.f32 [%0], {%1, %2}, [%3];" ::"r"(to), "f"(a),
+               "f"(b), "r"(bar)
+               : "memory");
+}
+
+template <int THREADS>
+__device__ __forceinline__ void consumers_sync() {
+  asm volatile("barrier.sync 1, %0;" ::"n"(THREADS) : "memory");
+}
+
+// THREADS: of the warps that compute; VPT: vectors a thread holds.
+template <typename T, int KIND, int THREADS, int VPT, int CTAS_PER_SM>
+__global__ void __launch_bounds__(THREADS + 32, CTAS_PER_SM)
+    row_loss_parts_kernel(const RowLossParams p, const PartShape shape) {
+  constexpr int kE = kVecElems<T>, kWarps = THREADS / 32;
+  extern __shared__ __align__(128) uint8_t part_memory[];
+  __shared__ uint64_t full[kPartSlots], empty[kPartSlots], told[2], summed[2];
+  __shared__ RowInfo infos[2];
+  __shared__ float2 parts[2][8 * kWarps];  // (maximum, sum) of every warp of the row's CTAs
+  __shared__ int aborted, count, all_bits;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int cluster = shape.cluster;
+  const int rank = static_cast<int>(cluster_cta_rank());
+  const int first_row = static_cast<int>(blockIdx.x) / cluster, row_step = static_cast<int>(gridDim.x) / cluster;
+  const int mine = p.N > first_row ? static_cast<int>((p.N - 1 - first_row) / row_step) + 1 : 0;
+  uint8_t* const lists = part_memory + static_cast<size_t>(shape.slots) * shape.slot_bytes;
+  if (tid == 0) {
+    for (int i = 0; i < kPartSlots; ++i) {
+      mbar_init(smem_addr(&full[i]), 1);
+      mbar_init(smem_addr(&empty[i]), kWarps);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_addr(&told[i]), 1);
+      mbar_init(smem_addr(&summed[i]), 1);
+    }
+    aborted = count = all_bits = 0;
+    fence_barrier_init();
+    if (blockIdx.x == 0) expect_arrivals(p.arrivals, p.tag);
+  }
+  cluster_sync_all();  // (also the CTA's own barrier)
+  const WaitCtl ctl{&aborted, nullptr, p.timeout_ns};
+  const auto row_of = [&](int i) { return static_cast<int64_t>(first_row) + static_cast<int64_t>(i) * row_step; };
+  const auto logits_of = [&](int64_t row) { return static_cast<const T*>(p.logits) + row * p.ld; };
+  const int first_vec = rank * shape.seg_vecs;
+  const auto part_vecs = [&](const RowSplit& split) {
+    const int64_t left = split.vecs - first_vec;
+    return static_cast<int>(left < 0 ? 0 : left < shape.seg_vecs ? left : shape.seg_vecs);
+  };
+  double loss = 0;
+  int rows = 1;
+
+  if (warp == kWarps) {
+    // ------------------------------------------------ the leader
+    int bits = 0, issued = 0;
+    const auto issue = [&]() {  // the next row's part, by one lane
+      const T* x = logits_of(row_of(issued));
+      const RowSplit split = split_row(x, p.V);
+      const uint32_t bytes = static_cast<uint32_t>(part_vecs(split)) * 16u;
+      const int slot = issued % shape.slots;
+      const uint32_t bar = smem_addr(&full[slot]);
+      mbar_arrive_expect_tx(bar, bytes);
+      if (bytes > 0)
+        bulk_copy(smem_addr(part_memory) + slot * shape.slot_bytes,
+                  reinterpret_cast<const uint4*>(x + split.head) + first_vec, bytes, bar);
+      ++issued;
+    };
+    if (lane == 0)
+      while (issued < shape.slots && issued < mine) issue();
+    for (int i = 0; i < mine; ++i) {
+      // infos[i & 1] was last used for row i - 2, and all warps have gone on to row i - 1
+      const int64_t row = row_of(i);
+      RowInfo r;
+      if constexpr (KIND == kDistill) {
+        const size_t at = static_cast<size_t>(i & 1) * list_bytes(p.K);
+        r = teacher_row<T>(p, row, list_at(lists + at, p.K), reinterpret_cast<int*>(lists + 2 * list_bytes(p.K)), &bits);
+      } else if (lane == 0) {
+        r = policy_row<T>(p, row, &bits);
+      }
+      if (lane == 0) {
+        infos[i & 1] = r;
+        mbar_arrive(smem_addr(&told[i & 1]));
+        const int slot = i % shape.slots;
+        const bool read = mbar_wait_sleep(smem_addr(&empty[slot]), (i / shape.slots) & 1, ctl);
+        if (read && !*ctl.abort_flag && issued < mine) issue();
+      }
+      __syncwarp();
+    }
+    if (lane == 0 && *ctl.abort_flag)  // copies under way have to land before this CTA ends
+      for (int i = issued > shape.slots ? issued - shape.slots : 0; i < issued; ++i)
+        mbar_wait_drain(smem_addr(&full[i % shape.slots]), (i / shape.slots) & 1, p.timeout_ns);
+    if (bits != 0) atomicOr(&all_bits, bits);
+  } else {
+    // ------------------------------------------------ the others
+    if (p.reduction == FLCE_REDUCTION_MEAN && KIND != kStats) {
+      if (p.counts != nullptr) {
+        grid_dependency_wait();
+        rows = counted_rows(p.counts);
+      } else {
+        int n = count_rows<KIND>(p, tid, THREADS);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+        if (lane == 0 && n != 0) atomicAdd(&count, n);
+        consumers_sync<THREADS>();
+        rows = count;
+      }
+    }
+    const float scale = p.reduction == FLCE_REDUCTION_MEAN ? p.grad_scale / static_cast<float>(rows) : p.grad_scale;
+    const Pair c = pair(p.c);
+    int slot = 0, use = 0;  // i % slots, i / slots
+    for (int i = 0; i < mine; ++i) {
+      const int64_t row = row_of(i);
+      const T* x = logits_of(row);
+      const RowSplit split = split_row(x, p.V);
+      const int n = part_vecs(split);
+      // elements before the row's first vector and after its last, by the CTAs at its ends
+      int64_t extra = -1;
+      if (rank == 0 && tid < split.head) extra = tid;
+      if (rank == cluster - 1 && tid >= 32 && tid < 32 + split.tail) extra = split.head + split.vecs * kE + tid - 32;
+      const float z = extra >= 0 ? to_float(x[extra]) : -INFINITY;
+      const int b = i & 1, phase = (i >> 1) & 1;
+      const uint32_t sum_bar = smem_addr(&summed[b]);
+      if (tid == 0) mbar_arrive_expect_tx(sum_bar, static_cast<uint32_t>(cluster) * kWarps * 8u);
+      bool ok = mbar_wait_sleep(smem_addr(&full[slot]), use & 1, ctl);
+      const uint4* from = reinterpret_cast<const uint4*>(part_memory + slot * shape.slot_bytes);
+      uint4 v[VPT];
+#pragma unroll
+      for (int k = 0; k < VPT; ++k) v[k] = k * THREADS + tid < n ? from[k * THREADS + tid] : empty_vec<T>();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&empty[slot]));
+      if (++slot == shape.slots) slot = 0, ++use;
+      const float m = warp_max_redux(fmaxf(vecs_max<T, VPT>(v), z));
+      const float shift = m > -INFINITY ? m : 0.f;
+      Pair sum = pair(0.f);
+#pragma unroll
+      for (int k = 0; k < VPT; ++k) vec_add_exp<T>(v[k], pair(-shift), c, sum);
+      float2 both = unpair(sum);
+      if (extra >= 0) both.x += ex2_approx((z - shift) * p.c);
+      const float s = warp_sum(both.x + both.y);
+      // the row's other numbers are read before any of its CTAs writes a gradient (in place)
+      ok = mbar_wait_sleep(smem_addr(&told[b]), phase, ctl) && ok;
+      if (ok && lane < cluster)
+        push_pair(map_to_cta(smem_addr(&parts[b][rank * kWarps + warp]), lane), m, s, map_to_cta(sum_bar, lane));
+      ok = mbar_wait_cluster(sum_bar, phase, ctl) && ok;
+      float pm = -INFINITY, ps = 0.f;
+      for (int k = lane; k < cluster * kWarps; k += 32) {
+        const float2 q = parts[b][k];
+        const float top = fmaxf(pm, q.x);
+        if (top > -INFINITY) {
+          ps = (pm > -INFINITY ? ps * ex2_approx((pm - top) * p.c) : ps) +
+               (q.x > -INFINITY ? q.y * ex2_approx((q.x - top) * p.c) : q.y);
+          pm = top;
+        } else {
+          ps += q.y;  // (NaN of a part that has nothing else)
+        }
+      }
+      const float2 all = combine_parts(pm, ps, p.c);
+      const RowInfo r = infos[b];
+      const RowResult result = row_result<KIND>(p, r, all.x, all.y, scale);
+      if (rank == 0 && tid == 0 && ok) store_result<KIND>(p, row, result, all.x, all.y, &loss);
+      if (KIND == kStats || p.grad == nullptr || !ok) {
+        if constexpr (KIND == kDistill)
+          if (p.grad != nullptr) consumers_sync<THREADS>();
+        continue;
+      }
+      T* g = static_cast<T*>(p.grad) + row * p.ld_grad;
+      const float inv_s = 1.f / all.y, f = result.f * inv_s;
+      const Pair minus_m = pair(-all.x), factor = pair(f);
+      const bool zero = result.f == 0.f;
+      T* to = g + split.head + (static_cast<int64_t>(first_vec) + tid) * kE;
+      // the 16-bit elements are widened again: kept from the sum, they would not fit in the registers
+#pragma unroll
+      for (int k = 0; k < VPT; ++k) asm volatile("" : "+r"(v[k].x), "+r"(v[k].y), "+r"(v[k].z), "+r"(v[k].w));
+      if (same_phase(x, g)) {
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+          const uint4 out = zero ? make_uint4(0, 0, 0, 0) : vec_grad<T>(v[k], minus_m, c, factor);
+          if (k * THREADS + tid < n) __stcs(reinterpret_cast<uint4*>(to + k * THREADS * kE), out);
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) {
+          const uint4 out = zero ? make_uint4(0, 0, 0, 0) : vec_grad<T>(v[k], minus_m, c, factor);
+          if (k * THREADS + tid < n) store_vec<T>(to + k * THREADS * kE, out, false);
+        }
+      }
+      if (extra >= 0) g[extra] = from_float<T>(zero ? 0.f : f * ex2_approx((z - all.x) * p.c));
+      // the places that the row names are written after the rest
+      if constexpr (KIND == kDistill) {
+        consumers_sync<THREADS>();
+        if (zero) continue;
+        const TeacherList list = list_at(lists + static_cast<size_t>(b) * list_bytes(p.K), p.K);
+        for (int k = tid; k < r.entries; k += THREADS) {
+          const int column = list.column[k];
+          if (column < 0) continue;
+          const int inside = column - split.head;
+          const int64_t vec = inside / kE;
+          const bool here = inside < 0            ? rank == 0
+                            : vec >= split.vecs   ? rank == cluster - 1
+                                                  : vec >= first_vec && vec < first_vec + n;
+          if (here) g[column] = from_float<T>(entry_grad(p, list, k, result.f, all.x, inv_s));
+        }
+      } else if (!zero) {
+        const int inside = r.column - split.head;
+        const int64_t vec = inside / kE - first_vec;
+        const bool here = inside >= 0 && inside / kE < split.vecs ? vec >= 0 && vec < n && vec % THREADS == tid
+                                                                  : extra == r.column;
+        if (here) g[r.column] = from_float<T>(target_grad(result));
+      }
+    }
+  }
+  __syncthreads();
+  cluster_sync_all();  // no CTA ends while another may still write to its shared memory
+  finish_rows(p, loss, all_bits | (aborted ? FLCE_STATUS_BIT_TIMEOUT : 0), rows);
+}
+
+template <typename T, int KIND, int THREADS, int VPT, int CTAS_PER_SM>
+cudaError_t launch_parts(const RowLossParams& p, PartShape shape, cudaStream_t s) {
+  constexpr auto kernel = row_loss_parts_kernel<T, KIND, THREADS, VPT, CTAS_PER_SM>;
+  constexpr size_t kLargest = 224 * 1024;
+  const size_t lists = KIND == kDistill ? 2 * list_bytes(p.K) + table_slots(p.K) * 4 : 0;
+  const size_t room = (CTAS_PER_SM > 1 ? kLargest / CTAS_PER_SM - 1024 : kLargest) - 0;
+  shape.slot_bytes = (shape.seg_vecs * 16 + 127) & ~127;
+  shape.slots = static_cast<int>(room > lists ? (room - lists) / shape.slot_bytes : 1);
+  if (shape.slots > kPartSlots) shape.slots = kPartSlots;
+  if (shape.slots < 1) shape.slots = 1;
+  const size_t smem = static_cast<size_t>(shape.slots) * shape.slot_bytes + lists;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(THREADS + 32);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attrs[2];
+  attrs[0].id = cudaLaunchAttributeClusterDimension;
+  attrs[0].val.clusterDim.x = static_cast<unsigned>(shape.cluster);
+  attrs[0].val.clusterDim.y = attrs[0].val.clusterDim.z = 1;
+  attrs[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attrs[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attrs;
+  cfg.numAttrs = 1;
+  // clusters that run at a time, by device, CTAs of a row and shared memory: asked for once
+  static std::atomic<uint64_t> known[16];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t key = static_cast<uint64_t>(dev + 1) << 48 | static_cast<uint64_t>(smem) << 16;
+  uint64_t held = known[shape.cluster].load(std::memory_order_relaxed);
+  if ((held & ~uint64_t(0xFFFF)) != key) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kLargest));
+    if (e != cudaSuccess) return e;
+    cfg.gridDim = dim3(static_cast<unsigned>(shape.cluster));
+    int clusters = 0;
+    e = cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg);
+    if (e != cudaSuccess) return e;
+    if (clusters < 1) return cudaErrorInvalidConfiguration;
+    const int most = kRowLossMaxCtas / shape.cluster;
+    held = key | static_cast<uint64_t>(clusters < most ? clusters : most);
+    known[shape.cluster].store(held, std::memory_order_relaxed);
+  }
+  const int64_t clusters = static_cast<int64_t>(held & 0xFFFF);
+  cfg.gridDim = dim3(static_cast<unsigned>((p.N < clusters ? p.N : clusters) * shape.cluster));
+  cfg.numAttrs = p.counts != nullptr ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p, shape);
+}
+
 // ---------------------------------------------------------------- host side
 
+// Parts of up to 2048 vectors by 256 threads (32 KB; three CTAs an SM, with two parts each
+// in shared memory), of up to 4224 by 384; rows beyond eight of these are read twice.
 template <typename T, int KIND>
 cudaError_t launch_rows_of(const RowLossParams& p, cudaStream_t s) {
-  return launch_long<T, KIND>(p, s);
+  const int64_t vecs = p.V / kVecElems<T>;
+  PartShape shape = {};
+  if (p.N == 0 || vecs < 128 || vecs > 8 * 4224) return launch_long<T, KIND>(p, s);
+  const int64_t wide = vecs > 8 * 2048 ? 4224 : 2048;
+  shape.cluster = 1;
+  while (div_up(vecs, shape.cluster) > wide) shape.cluster *= 2;
+  shape.seg_vecs = static_cast<int>(div_up(vecs, shape.cluster));
+  if (wide > 2048) return launch_parts<T, KIND, 384, 11, 2>(p, shape, s);
+  if (shape.seg_vecs <= 512) return launch_parts<T, KIND, 256, 2, 3>(p, shape, s);
+  if (shape.seg_vecs <= 1024) return launch_parts<T, KIND, 256, 4, 3>(p, shape, s);
+  return launch_parts<T, KIND, 256, 8, 3>(p, shape, s);
 }
 
 // All rows of a call: the count that a mean needs first, then the rows.
