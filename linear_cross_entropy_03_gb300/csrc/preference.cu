@@ -45,45 +45,61 @@ __device__ __forceinline__ void sequence_rows(const PairParams& p, int64_t q, in
   *from = a, *to = b;
 }
 
-__device__ __forceinline__ double block_sum(double v, double* scratch) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
+// The sum over the threads of each half of the CTA, for thread 0 of the half; by its first
+// warp, as an SM has two fp64 operations a cycle.
+__device__ __forceinline__ double half_sum(double v, double* scratch) {
+  scratch[threadIdx.x] = v;
   __syncthreads();
   double total = 0;
-  for (int w = 0; w < kPairThreads / 32; ++w) total += scratch[w];
+  const int t = threadIdx.x % (kPairThreads / 2);
+  if (t < 32) {
+#pragma unroll
+    for (int i = 0; i < kPairThreads / 2; i += 32) total += scratch[threadIdx.x + i];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  }
   __syncthreads();
   return total;
 }
 
-// One CTA a pair.  Sums are fp64 in an order that the lengths fix.
+// One CTA a pair, half of it for each sequence.  Sums are fp64 in an order that the lengths
+// fix.
 __global__ void __launch_bounds__(kPairThreads) pair_loss_kernel(const PairParams p) {
-  __shared__ double scratch[kPairThreads / 32];
-  __shared__ int last;
-  if (threadIdx.x == 0 && blockIdx.x == 0) expect_arrivals(p.arrivals, p.tag);
+  constexpr int kHalf = kPairThreads / 2;
+  __shared__ double scratch[kPairThreads];
+  __shared__ double sums[2], tokens_of[2], slope_of_pair;
+  __shared__ int last, all_bits;
+  const int half = threadIdx.x / kHalf, t = threadIdx.x % kHalf;
+  if (threadIdx.x == 0) {
+    all_bits = 0;
+    if (blockIdx.x == 0) expect_arrivals(p.arrivals, p.tag);
+  }
+  __syncthreads();
   grid_dependency_wait();
   int bits = 0;
   for (int64_t pair = blockIdx.x; pair < p.pairs; pair += gridDim.x) {
-    double s[2], count[2];
-    int64_t from[2], to[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      sequence_rows(p, pair + k * p.pairs, &from[k], &to[k], &bits);
-      double sum = 0;
-      int64_t tokens = 0;
-      for (int64_t n = from[k] + threadIdx.x; n < to[k]; n += kPairThreads) {
-        const int64_t t = __ldg(p.target + n);
-        if (t == p.ignore_index || t < 0 || t >= p.V) continue;
-        sum += static_cast<double>(p.logp_rows[n]);
-        ++tokens;
-      }
-      s[k] = block_sum(sum, scratch);
-      count[k] = 1;
-      if (p.numbers.average) {
-        count[k] = fmax(block_sum(static_cast<double>(tokens), scratch), 1.0);
-        s[k] /= count[k];
-      }
+    int64_t from, to;
+    sequence_rows(p, pair + half * p.pairs, &from, &to, &bits);
+    double sum = 0;
+    int64_t tokens = 0;
+#pragma unroll 4
+    for (int64_t n = from + t; n < to; n += kHalf) {
+      const int64_t target = __ldg(p.target + n);
+      const float logp = p.logp_rows[n];
+      if (target == p.ignore_index || target < 0 || target >= p.V) continue;
+      sum += static_cast<double>(logp);
+      ++tokens;
     }
+    sum = half_sum(sum, scratch);
+    double count = 1;
+    if (p.numbers.average) {
+      count = half_sum(static_cast<double>(tokens), scratch);
+      if (t == 0 && count > 1) sum /= count;
+      if (count < 1) count = 1;
+    }
+    if (t == 0) sums[half] = sum, tokens_of[half] = count;
+    __syncthreads();
+    const double s[2] = {sums[0], sums[1]};
     if (threadIdx.x == 0) {
       // differences of long sums in fp64, functions of the difference in fp32
       double x = s[0] - s[1];
@@ -112,7 +128,7 @@ __global__ void __launch_bounds__(kPairThreads) pair_loss_kernel(const PairParam
       double scale = p.grad_scale;
       if (p.reduction == FLCE_REDUCTION_MEAN) scale /= static_cast<double>(p.pairs);
       if (p.grad_out != nullptr) scale *= p.grad_out[pair];
-      scratch[0] = slope * scale;
+      slope_of_pair = slope * scale;
       p.pair_loss[pair] = loss;
       if (p.reduction == FLCE_REDUCTION_NONE) p.loss[pair] = static_cast<float>(loss);
       if (p.logp != nullptr) {
@@ -121,25 +137,28 @@ __global__ void __launch_bounds__(kPairThreads) pair_loss_kernel(const PairParam
       }
     }
     __syncthreads();
-    const double slope = scratch[0];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const float f = static_cast<float>(slope / count[k] * (k == 0 ? -1.0 : 1.0));
-      for (int64_t n = from[k] + threadIdx.x; n < to[k]; n += kPairThreads) p.factor[n] = f;
-    }
-    __syncthreads();  // scratch is the next pair's
+    float f = 0.f;
+    if (t % 32 == 0) f = static_cast<float>((half == 0 ? -slope_of_pair : slope_of_pair) / tokens_of[half]);
+    f = __shfl_sync(0xffffffffu, f, 0);
+    for (int64_t n = from + t; n < to; n += kHalf) p.factor[n] = f;
+    __syncthreads();  // the sums are the next pair's
   }
-  if (bits != 0 && threadIdx.x == 0) atomicOr(p.status, bits);
-  if (p.reduction == FLCE_REDUCTION_NONE) return;
+  if (bits != 0) atomicOr(&all_bits, bits);
   __syncthreads();
-  if (threadIdx.x == 0) last = arrives_last(p.arrivals, p.tag, gridDim.x);
+  if (threadIdx.x == 0) {
+    if (all_bits != 0) atomicOr(p.status, all_bits);
+    last = p.reduction != FLCE_REDUCTION_NONE && arrives_last(p.arrivals, p.tag, gridDim.x);
+  }
   __syncthreads();
   if (!last) return;
   double total = 0;
   for (int64_t i = threadIdx.x; i < p.pairs; i += kPairThreads) total += __ldcg(p.pair_loss + i);
-  total = block_sum(total, scratch);
-  if (threadIdx.x == 0)
-    *p.loss = static_cast<float>(p.reduction == FLCE_REDUCTION_MEAN ? total / static_cast<double>(p.pairs) : total);
+  total = half_sum(total, scratch);
+  if (t == 0) sums[half] = total;
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  total = sums[0] + sums[1];
+  *p.loss = static_cast<float>(p.reduction == FLCE_REDUCTION_MEAN ? total / static_cast<double>(p.pairs) : total);
 }
 
 struct GradParams {

@@ -192,18 +192,19 @@ __device__ __forceinline__ void store_vec(T* to, const uint4& v, bool vector) {
 
 // A row's elements: `head` before the first 16-byte boundary, `vecs` vectors, `tail` after.
 struct RowSplit {
-  int head, tail;
-  int64_t vecs;
+  int head, tail, vecs;
 };
 
 template <typename T>
 __device__ __forceinline__ RowSplit split_row(const T* row, int64_t V) {
-  constexpr int kE = kVecElems<T>;
+  constexpr unsigned kE = kVecElems<T>;
+  const unsigned v = static_cast<unsigned>(V);  // (below 2^31)
+  const unsigned place = (16u - (static_cast<unsigned>(reinterpret_cast<uintptr_t>(row)) & 15u)) & 15u;
+  const unsigned head = min(place / static_cast<unsigned>(sizeof(T)), v);
   RowSplit s;
-  const int64_t head = ((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / sizeof(T);
-  s.head = static_cast<int>(head < V ? head : V);
-  s.vecs = (V - s.head) / kE;
-  s.tail = static_cast<int>(V - s.head - s.vecs * kE);
+  s.head = static_cast<int>(head);
+  s.vecs = static_cast<int>((v - head) / kE);
+  s.tail = static_cast<int>((v - head) % kE);
   return s;
 }
 
@@ -229,7 +230,8 @@ struct RowInfo {
   float weight, grad_out;
   float a;      // distill: sum of q (ln q - (z - zt) / T)
   int column;   // policy, stats: the target's, or -1 where the row takes no part
-  int entries;  // distill: length of the list, 0 where the row has no teacher
+  bool taught;  // distill: whether the row has a teacher
+  int entries;  // distill: length of the list
 };
 
 template <typename T>
@@ -237,24 +239,41 @@ __device__ __forceinline__ float load_logit(const RowLossParams& p, int64_t row,
   return to_float(static_cast<const T*>(p.logits)[row * p.ld + column]);
 }
 
+// What a row has beside its logits is read in two steps, as the second (logits at places that
+// the first names) needs the first: a warp that leads others starts both ahead of the row.
+// Row numbers past the end are rows without anything.
+struct PolicyAhead {
+  RowInfo r;
+  int64_t target;
+};
+__device__ __forceinline__ PolicyAhead policy_ahead(const RowLossParams& p, int64_t row) {
+  PolicyAhead a = {};
+  a.r.column = -1;
+  a.target = p.ignore_index;
+  if (row >= p.N) return a;
+  a.target = __ldg(p.target + row);
+  a.r.weight = p.row_weight != nullptr ? __ldg(p.row_weight + row) : 1.f;
+  a.r.grad_out = p.grad_out != nullptr ? __ldg(p.grad_out + row) : 1.f;
+  a.r.advantage = p.advantage != nullptr ? __ldg(p.advantage + row) : 0.f;
+  a.r.old_logp = p.old_logp != nullptr ? __ldg(p.old_logp + row) : 0.f;
+  a.r.ref_logp = p.ref_logp != nullptr ? __ldg(p.ref_logp + row) : 0.f;
+  return a;
+}
+template <typename T>
+__device__ __forceinline__ void policy_logit(const RowLossParams& p, int64_t row, PolicyAhead& a, int* bits) {
+  if (a.target == p.ignore_index) return;
+  if (a.target < 0 || a.target >= p.V) {
+    *bits |= FLCE_STATUS_BIT_TARGET_RANGE;
+    return;
+  }
+  a.r.column = static_cast<int>(a.target);
+  a.r.zt = load_logit<T>(p, row, a.target);
+}
 template <typename T>
 __device__ __forceinline__ RowInfo policy_row(const RowLossParams& p, int64_t row, int* bits) {
-  RowInfo r = {};
-  const int64_t t = __ldg(p.target + row);
-  r.column = -1;
-  if (t != p.ignore_index) {
-    if (t >= 0 && t < p.V)
-      r.column = static_cast<int>(t);
-    else
-      *bits |= FLCE_STATUS_BIT_TARGET_RANGE;
-  }
-  r.weight = p.row_weight != nullptr ? __ldg(p.row_weight + row) : 1.f;
-  r.grad_out = p.grad_out != nullptr ? __ldg(p.grad_out + row) : 1.f;
-  r.advantage = p.advantage != nullptr ? __ldg(p.advantage + row) : 0.f;
-  r.old_logp = p.old_logp != nullptr ? __ldg(p.old_logp + row) : 0.f;
-  r.ref_logp = p.ref_logp != nullptr ? __ldg(p.ref_logp + row) : 0.f;
-  r.zt = r.column >= 0 ? load_logit<T>(p, row, t) : 0.f;
-  return r;
+  PolicyAhead a = policy_ahead(p, row);
+  policy_logit<T>(p, row, a, bits);
+  return a.r;
 }
 
 // A teacher's list in shared memory: columns (-1: no such place), shares and logits.
@@ -276,59 +295,183 @@ __device__ __forceinline__ TeacherList list_at(uint8_t* at, int K) {
   return {reinterpret_cast<int*>(at), reinterpret_cast<float*>(at) + room, reinterpret_cast<float*>(at) + 2 * room};
 }
 
-// Reads a row's list, by one warp: fills `list` with the entries up to the first negative
-// id, q of columns that occur twice added up, and returns the row's numbers.  `table` has
-// table_slots(K) words.
+// A list's first entries, four a lane.
+constexpr int kListAhead = 4;
+struct ListAhead {
+  int column[kListAhead];  // -1: the list has ended, -2: not a column
+  float value[kListAhead], z[kListAhead];
+  float weight, grad_out;
+};
+__device__ __forceinline__ int column_of(const RowLossParams& p, int64_t id) {
+  return id < 0 ? -1 : id < p.V ? static_cast<int>(id) : -2;
+}
+__device__ __forceinline__ ListAhead list_ahead(const RowLossParams& p, int64_t row) {
+  ListAhead a;
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int j = 0; j < kListAhead; ++j) {
+    const int k = j * 32 + lane;
+    const bool held = row < p.N && k < p.K;
+    a.column[j] = held ? column_of(p, load_id(p.ids, p.ids32, row * p.K + k)) : -1;
+    a.value[j] = held ? load_elem(p.values, p.value_dtype, row * p.K + k) : -INFINITY;
+  }
+  a.weight = row < p.N && p.row_weight != nullptr ? __ldg(p.row_weight + row) : 1.f;
+  a.grad_out = row < p.N && p.grad_out != nullptr ? __ldg(p.grad_out + row) : 1.f;
+  return a;
+}
 template <typename T>
-__device__ RowInfo teacher_row(const RowLossParams& p, int64_t row, const TeacherList& list, int* table, int* bits) {
+__device__ __forceinline__ void list_logits(const RowLossParams& p, int64_t row, ListAhead& a) {
+#pragma unroll
+  for (int j = 0; j < kListAhead; ++j) a.z[j] = a.column[j] >= 0 ? load_logit<T>(p, row, a.column[j]) : -INFINITY;
+}
+
+// Puts a column into the table of a list, which has room for all; whether it was there.
+__device__ __forceinline__ bool seen_before(int* table, int slots, int column) {
+  for (unsigned s = (static_cast<unsigned>(column) * 2654435761u) >> 8;; ++s) {
+    const int was = atomicCAS(table + (s & (slots - 1)), -1, column);
+    if (was == -1) return false;
+    if (was == column) return true;
+  }
+}
+
+// A list of up to 32 * kListAhead entries without leaving the registers; false where a column
+// is named twice.
+template <typename Wanted>
+__device__ __forceinline__ bool short_teacher_row(const RowLossParams& p, const ListAhead& ahead,
+                                                  const TeacherList& list, int* table, int* bits, Wanted wanted,
+                                                  RowInfo* out) {
+  const int lane = threadIdx.x & 31;
+  RowInfo r = {};
+  r.weight = ahead.weight;
+  r.grad_out = ahead.grad_out;
+  r.column = -1;
+  const int slots = table_slots(p.K);
+  for (int i = lane; i < slots; i += 32) table[i] = -1;
+  const int batches = (p.K + 31) / 32;
+  float v[kListAhead], e[kListAhead];
+  float vmax = -INFINITY;
+  bool ended = false;
+#pragma unroll
+  for (int j = 0; j < kListAhead; ++j) {
+    v[j] = -INFINITY;
+    if (j >= batches) break;
+    const unsigned ends = __ballot_sync(0xffffffffu, ahead.column[j] == -1);
+    const bool held = !ended && (ends == 0 || lane < __ffs(ends) - 1);
+    if (held && ahead.column[j] == -2) *bits |= FLCE_STATUS_BIT_TARGET_RANGE;
+    if (held && ahead.column[j] >= 0) v[j] = ahead.value[j];
+    ended = ended || ends != 0;
+    vmax = fmaxf(vmax, v[j]);
+  }
+  vmax = warp_max_redux(vmax);
+  const float shift = vmax > -INFINITY ? vmax : 0.f;
+  float sum = 0.f, zmax = -INFINITY;
+#pragma unroll
+  for (int j = 0; j < kListAhead; ++j) {
+    e[j] = 0.f;
+    if (j >= batches) break;
+    e[j] = ex2_approx((v[j] - shift) * p.c);  // 0: no share, the place is like any other
+    sum += e[j];
+    if (e[j] != 0.f) zmax = fmaxf(zmax, ahead.z[j]);
+  }
+  sum = warp_sum(sum);
+  zmax = warp_max_redux(zmax);
+  r.zt = zmax > -INFINITY ? zmax : 0.f;
+  r.taught = sum != 0.f;  // (a list of -inf alone is no teacher)
+  const float inv = 1.f / sum, ln_sum = logf(sum);
+  float a = 0.f;
+  bool twice = false;
+  int kept = 0;
+#pragma unroll
+  for (int j = 0; j < kListAhead; ++j) {
+    if (j >= batches) break;
+    const bool held = e[j] != 0.f;
+    const float q = e[j] * inv;
+    if (held) {
+      a += q * ((v[j] - shift) * p.inv_t - ln_sum - (ahead.z[j] - r.zt) * p.inv_t);
+      twice = seen_before(table, slots, ahead.column[j]) || twice;
+    }
+    const bool here = held && wanted(ahead.column[j]);
+    const unsigned all = __ballot_sync(0xffffffffu, here);
+    if (here) {
+      const int at = kept + __popc(all & ((1u << lane) - 1));
+      list.column[at] = ahead.column[j], list.q[at] = q, list.z[at] = ahead.z[j];
+    }
+    kept += __popc(all);
+  }
+  r.a = warp_sum(a);
+  r.entries = kept;
+  *out = r;
+  return !__any_sync(0xffffffffu, twice);
+}
+
+// A row's list, by one warp: returns the row's numbers and fills `list` with the entries
+// whose columns are `wanted`, q of columns that occur twice added up.  `ahead`: the list's
+// first entries, with their logits.  `table` has table_slots(K) words.
+template <typename T, typename Wanted>
+__device__ RowInfo teacher_row(const RowLossParams& p, int64_t row, const ListAhead& ahead, const TeacherList& list,
+                               int* table, int* bits, Wanted wanted) {
+  if (p.K <= 32 * kListAhead) {
+    RowInfo r;
+    const bool done = short_teacher_row(p, ahead, list, table, bits, wanted, &r);
+    __syncwarp();
+    if (done) return r;
+  }
   const int lane = threadIdx.x & 31;
   const int64_t base = row * p.K;
   RowInfo r = {};
-  r.weight = p.row_weight != nullptr ? __ldg(p.row_weight + row) : 1.f;
-  r.grad_out = p.grad_out != nullptr ? __ldg(p.grad_out + row) : 1.f;
+  r.weight = ahead.weight;
+  r.grad_out = ahead.grad_out;
   r.column = -1;
   const int slots = table_slots(p.K);
   for (int i = lane; i < slots; i += 32) table[i] = -1;
   float vmax = -INFINITY;
   int entries = 0;
-  for (int k0 = 0; k0 < p.K; k0 += 32) {
-    const int k = k0 + lane;
-    const int64_t id = k < p.K ? load_id(p.ids, p.ids32, base + k) : -1;
-    const float v = k < p.K ? load_elem(p.values, p.value_dtype, base + k) : -INFINITY;
-    const unsigned ends = __ballot_sync(0xffffffffu, id < 0);
+  bool ended = false;
+  const auto take = [&](int k, int column, float v, float z) {
+    const unsigned ends = __ballot_sync(0xffffffffu, column == -1);
     const int first = ends != 0 ? __ffs(ends) - 1 : 32;
     if (lane < first) {
-      const bool inside = id < p.V;
-      if (!inside) *bits |= FLCE_STATUS_BIT_TARGET_RANGE;
-      list.column[k] = inside ? static_cast<int>(id) : -1;
-      list.q[k] = inside ? v : -INFINITY;
-      if (inside) vmax = fmaxf(vmax, v);
+      if (column < 0) {
+        *bits |= FLCE_STATUS_BIT_TARGET_RANGE;
+        v = -INFINITY;
+      }
+      list.column[k] = column;
+      list.q[k] = v;
+      list.z[k] = z;
+      vmax = fmaxf(vmax, v);
     }
     entries += first;
-    if (ends != 0) break;
+    ended = ends != 0;
+  };
+#pragma unroll
+  for (int j = 0; j < kListAhead; ++j)
+    if (!ended) take(j * 32 + lane, ahead.column[j], ahead.value[j], ahead.z[j]);
+  for (int k0 = 32 * kListAhead; k0 < p.K && !ended; k0 += 32) {
+    const int k = k0 + lane;
+    const bool held = k < p.K;
+    const int column = held ? column_of(p, load_id(p.ids, p.ids32, base + k)) : -1;
+    take(k, column, held ? load_elem(p.values, p.value_dtype, base + k) : -INFINITY,
+         column >= 0 ? load_logit<T>(p, row, column) : -INFINITY);
   }
   __syncwarp();
   vmax = warp_max_redux(vmax);
   const float shift = vmax > -INFINITY ? vmax : 0.f;
   float sum = 0.f, zmax = -INFINITY;
   for (int k = lane; k < entries; k += 32) {
-    const int column = list.column[k];
     const float e = ex2_approx((list.q[k] - shift) * p.c);
-    float z = -INFINITY;
     if (e == 0.f) {
       list.column[k] = -1;  // no share: the place is like any other
     } else {
-      z = load_logit<T>(p, row, column);
       sum += e;
-      zmax = fmaxf(zmax, z);
+      zmax = fmaxf(zmax, list.z[k]);
     }
     list.q[k] = e;
-    list.z[k] = z;
   }
   sum = warp_sum(sum);
   zmax = warp_max_redux(zmax);
   r.zt = zmax > -INFINITY ? zmax : 0.f;
-  r.entries = sum == 0.f ? 0 : entries;  // (a list of -inf alone is no teacher)
+  r.taught = sum != 0.f;  // (a list of -inf alone is no teacher)
+  r.entries = r.taught ? entries : 0;
   const float inv = 1.f / sum, ln_sum = logf(sum);
   float a = 0.f;
   bool twice = false;
@@ -338,15 +481,7 @@ __device__ RowInfo teacher_row(const RowLossParams& p, int64_t row, const Teache
     const float e = list.q[k], q = e * inv;
     a += q * (logf(e) - ln_sum - (list.z[k] - r.zt) * p.inv_t);
     list.q[k] = q;
-    // a free slot is there: the table has twice the entries
-    for (unsigned s = (static_cast<unsigned>(column) * 2654435761u) >> 8;; ++s) {
-      const int was = atomicCAS(table + (s & (slots - 1)), -1, column);
-      if (was == -1) break;
-      if (was == column) {
-        twice = true;
-        break;
-      }
-    }
+    twice = seen_before(table, slots, column) || twice;
   }
   r.a = warp_sum(a);
   __syncwarp();
@@ -363,7 +498,29 @@ __device__ RowInfo teacher_row(const RowLossParams& p, int64_t row, const Teache
     for (int k = lane; k < r.entries; k += 32) list.q[k] = total[k];
   }
   __syncwarp();
+  // of the list, the caller's entries alone
+  int kept = 0;
+  for (int k0 = 0; k0 < r.entries; k0 += 32) {
+    const int k = k0 + lane;
+    const int column = k < r.entries ? list.column[k] : -1;
+    const float q = k < r.entries ? list.q[k] : 0.f, z = k < r.entries ? list.z[k] : 0.f;
+    const bool here = column >= 0 && wanted(column);
+    const unsigned all = __ballot_sync(0xffffffffu, here);
+    const int at = kept + __popc(all & ((1u << lane) - 1));  // (not past k)
+    if (here) list.column[at] = column, list.q[at] = q, list.z[at] = z;
+    kept += __popc(all);
+    __syncwarp();
+  }
+  r.entries = kept;
   return r;
+}
+
+template <typename T>
+__device__ __forceinline__ RowInfo whole_teacher_row(const RowLossParams& p, int64_t row, const TeacherList& list,
+                                                     int* table, int* bits) {
+  ListAhead a = list_ahead(p, row);
+  list_logits<T>(p, row, a);
+  return teacher_row<T>(p, row, a, list, table, bits, [](int) { return true; });
 }
 
 // ---------------------------------------------------------------- a row's loss
@@ -381,7 +538,7 @@ __device__ __forceinline__ RowResult row_result(const RowLossParams& p, const Ro
   const float ln_s = logf(s);
   scale *= r.grad_out;
   if constexpr (KIND == kDistill) {
-    if (r.entries == 0 || r.weight == 0.f) return out;
+    if (!r.taught || r.weight == 0.f) return out;
     out.loss = p.temperature * p.temperature * r.weight * (r.a + ((m - r.zt) * p.inv_t + ln_s));
     out.f = p.temperature * r.weight * scale;
   } else {
@@ -450,33 +607,40 @@ __device__ __forceinline__ int counted_rows(const int* counts) {
 }
 
 // By all threads of every CTA of a launch, at its end: adds up the CTAs' losses (of thread
-// 0) in the order of the CTAs, and their status bits, in the CTA that arrives last.
+// 0) in the order of the CTAs, and their status bits, in the CTA that arrives last.  One
+// warp adds: an SM has two fp64 operations a cycle.
 __device__ __forceinline__ void finish_rows(const RowLossParams& p, double loss, int bits, int rows) {
   __shared__ int last;
-  __shared__ double sums[32];
+  constexpr unsigned kStaged = 256;
+  __shared__ double staged[kStaged];
   __shared__ int all_bits;
   if (threadIdx.x == 0) {
     all_bits = 0;
-    p.partial[blockIdx.x] = loss;
+    if (p.loss != nullptr) p.partial[blockIdx.x] = loss;
     p.flags[blockIdx.x] = bits;
     last = arrives_last(p.arrivals, p.tag, gridDim.x);
   }
   __syncthreads();
   if (!last) return;
-  double total = 0;
   int seen = 0;
-  for (unsigned i = threadIdx.x; i < gridDim.x; i += blockDim.x) {
-    total += __ldcg(p.partial + i);
-    seen |= __ldcg(p.flags + i);
+  for (unsigned i = threadIdx.x; i < gridDim.x; i += blockDim.x) seen |= __ldcg(p.flags + i);
+  double total = 0;
+  for (unsigned base = 0; base < gridDim.x && p.loss != nullptr; base += kStaged) {
+    const unsigned here = gridDim.x - base < kStaged ? gridDim.x - base : kStaged;
+    for (unsigned i = threadIdx.x; i < here; i += blockDim.x) staged[i] = __ldcg(p.partial + base + i);
+    __syncthreads();
+    if (threadIdx.x < 32)
+      for (unsigned i = threadIdx.x; i < here; i += 32) total += staged[i];
+    __syncthreads();
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = total;
   if (seen != 0) atomicOr(&all_bits, seen);
   __syncthreads();
+  if (threadIdx.x >= 32) return;
+  if (p.loss != nullptr) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  }
   if (threadIdx.x != 0) return;
-  total = 0;
-  for (unsigned w = 0; w < blockDim.x / 32; ++w) total += sums[w];
   if (p.loss != nullptr)
     *p.loss = p.reduction != FLCE_REDUCTION_MEAN ? static_cast<float>(total)
               : rows > 0                         ? static_cast<float>(total / rows)
@@ -540,12 +704,12 @@ __global__ void __launch_bounds__(kLongThreads) row_loss_long_kernel(const RowLo
     const T* x = static_cast<const T*>(p.logits) + row * p.ld;
     const RowSplit split = split_row(x, p.V);
     const uint4* vecs = reinterpret_cast<const uint4*>(x + split.head);
-    const T* tail = x + split.head + split.vecs * kE;
+    const T* tail = x + split.head + static_cast<int64_t>(split.vecs) * kE;
     float m = -INFINITY, s = 0.f;
     if (warp == 0) {
       RowInfo r;
       if constexpr (KIND == kDistill)
-        r = teacher_row<T>(p, row, list, reinterpret_cast<int*>(list_memory + list_bytes(p.K)), &bits);
+        r = whole_teacher_row<T>(p, row, list, reinterpret_cast<int*>(list_memory + list_bytes(p.K)), &bits);
       else
         r = policy_row<T>(p, row, &bits);
       if (lane == 0) info = r;
@@ -584,7 +748,7 @@ __global__ void __launch_bounds__(kLongThreads) row_loss_long_kernel(const RowLo
       const bool zero = result.f == 0.f, vector = same_phase(x, g);
       if (tid < split.head) g[tid] = from_float<T>(zero ? 0.f : f * ex2_approx((to_float(x[tid]) - all.x) * p.c));
       if (tid >= 32 && tid < 32 + split.tail) {
-        const int64_t at = split.head + split.vecs * kE + tid - 32;
+        const int64_t at = p.V - split.tail + tid - 32;
         g[at] = from_float<T>(zero ? 0.f : f * ex2_approx((to_float(x[at]) - all.x) * p.c));
       }
 #pragma unroll 4
@@ -596,8 +760,7 @@ __global__ void __launch_bounds__(kLongThreads) row_loss_long_kernel(const RowLo
       if (!zero) {
         if constexpr (KIND == kDistill) {
           for (int k = tid; k < r.entries; k += kLongThreads)
-            if (list.column[k] >= 0)
-              g[list.column[k]] = from_float<T>(entry_grad(p, list, k, result.f, all.x, inv_s));
+            g[list.column[k]] = from_float<T>(entry_grad(p, list, k, result.f, all.x, inv_s));
         } else if (tid == 0) {
           g[r.column] = from_float<T>(target_grad(result));
         }
@@ -630,22 +793,157 @@ cudaError_t launch_long(const RowLossParams& p, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, row_loss_long_kernel<T, KIND>, p);
 }
 
+// ---------------------------------------------------------------- short rows
+
+// A warp a row, which it holds in registers: rows of up to 256 vectors.
+constexpr int kRowWarps = 8;
+
+template <typename T, int KIND, int VPT>
+__global__ void __launch_bounds__(32 * kRowWarps) row_loss_warps_kernel(const RowLossParams p) {
+  extern __shared__ __align__(16) uint8_t list_memory[];
+  constexpr int kE = kVecElems<T>;
+  __shared__ double losses[kRowWarps];
+  __shared__ int count, all_bits;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, warps = blockDim.x >> 5;
+  const size_t each = KIND == kDistill ? list_bytes(p.K) + table_slots(p.K) * 4 : 0;
+  const TeacherList list = list_at(list_memory + warp * each, p.K);
+  int* const table = reinterpret_cast<int*>(list_memory + warp * each + list_bytes(p.K));
+  if (tid == 0) {
+    count = all_bits = 0;
+    if (blockIdx.x == 0) expect_arrivals(p.arrivals, p.tag);
+  }
+  int rows = 1, bits = 0;
+  const bool mean = p.reduction == FLCE_REDUCTION_MEAN && KIND != kStats;
+  const bool self = mean && p.counts == nullptr;
+  if (self) {
+    __syncthreads();
+    int n = count_rows<KIND>(p, tid, blockDim.x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+    if (lane == 0 && n != 0) atomicAdd(&count, n);
+  }
+  __syncthreads();
+  if (self) rows = count;
+  if (mean && !self) {
+    grid_dependency_wait();
+    rows = counted_rows(p.counts);
+  }
+  const float scale = mean ? p.grad_scale / static_cast<float>(rows) : p.grad_scale;
+  const Pair c = pair(p.c);
+  double loss = 0;
+  for (int64_t row = static_cast<int64_t>(blockIdx.x) * warps + warp; row < p.N;
+       row += static_cast<int64_t>(gridDim.x) * warps) {
+    const T* x = static_cast<const T*>(p.logits) + row * p.ld;
+    const RowSplit split = split_row(x, p.V);
+    const int n = static_cast<int>(split.vecs);
+    const uint4* from = reinterpret_cast<const uint4*>(x + split.head);
+    uint4 v[VPT];
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) v[k] = k * 32 + lane < n ? from[k * 32 + lane] : empty_vec<T>();
+    int extra = -1;  // an element before or after the vectors
+    if (lane < split.head) extra = lane;
+    if (lane >= 8 && lane < 8 + split.tail) extra = static_cast<int>(p.V) - split.tail + lane - 8;
+    const float z = extra >= 0 ? to_float(x[extra]) : -INFINITY;
+    RowInfo r;
+    if constexpr (KIND == kDistill)
+      r = whole_teacher_row<T>(p, row, list, table, &bits);
+    else
+      r = policy_row<T>(p, row, &bits);
+    const float m = warp_max_redux(fmaxf(vecs_max<T, VPT>(v), z));
+    const Pair minus_m = pair(m > -INFINITY ? -m : 0.f);
+    Pair sum = pair(0.f);
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) vec_add_exp<T>(v[k], minus_m, c, sum);
+    float2 both = unpair(sum);
+    if (extra >= 0) both.x += ex2_approx((z + unpair(minus_m).x) * p.c);
+    const float s = warp_sum(both.x + both.y);
+    const RowResult result = row_result<KIND>(p, r, m, s, scale);
+    if (lane == 0) store_result<KIND>(p, row, result, m, s, &loss);
+    if (KIND == kStats || p.grad == nullptr) continue;
+    T* g = static_cast<T*>(p.grad) + row * p.ld_grad;
+    const bool zero = result.f == 0.f, vector = same_phase(x, g);
+    const float inv_s = 1.f / s, f = result.f * inv_s;
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+      const uint4 out = zero ? make_uint4(0, 0, 0, 0) : vec_grad<T>(v[k], pair(-m), c, pair(f));
+      if (k * 32 + lane < n) store_vec<T>(g + split.head + (k * 32 + lane) * kE, out, vector);
+    }
+    if (extra >= 0) g[extra] = from_float<T>(zero ? 0.f : f * ex2_approx((z - m) * p.c));
+    __syncwarp();  // the places that the row names are written after the rest
+    if (zero) continue;
+    if constexpr (KIND == kDistill) {
+      for (int k = lane; k < r.entries; k += 32)
+        g[list.column[k]] = from_float<T>(entry_grad(p, list, k, result.f, m, inv_s));
+      __syncwarp();  // the list is the next row's
+    } else if (lane == 0) {
+      g[r.column] = from_float<T>(target_grad(result));
+    }
+  }
+  if (lane == 0) losses[warp] = loss;
+  if (bits != 0) atomicOr(&all_bits, bits);
+  __syncthreads();
+  double total = 0;
+  if (tid == 0 && p.loss != nullptr)
+    for (int w = 0; w < warps; ++w) total += losses[w];
+  finish_rows(p, total, all_bits, rows);
+}
+
+template <typename T, int KIND, int VPT>
+cudaError_t launch_warps(const RowLossParams& p, cudaStream_t s) {
+  const size_t each = KIND == kDistill ? list_bytes(p.K) + table_slots(p.K) * 4 : 0;
+  int warps = kRowWarps;  // fewer where the lists are long, or the rows few
+  while (warps > 1 && (warps * each > 40 * 1024 || div_up(p.N, warps) < device_sm_count())) warps /= 2;
+  const int64_t ctas = div_up(p.N, warps), most = 8 * device_sm_count();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas < most ? ctas : most));
+  cfg.blockDim = dim3(32 * warps);
+  cfg.dynamicSmemBytes = warps * each;
+  cfg.stream = s;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = p.counts != nullptr ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, row_loss_warps_kernel<T, KIND, VPT>, p);
+}
+
 // ---------------------------------------------------------------- rows by parts
 
 // A cluster of CTAs a row, each with one part of it in registers, so that a row is read
 // once.  Clusters take rows one after another; CTAs of several clusters share an SM, and
-// one computes while another waits.  A CTA's last warp leads: it brings the CTA's parts of
-// the next rows into shared memory by bulk copies, and reads what the rows have beside
-// their logits.  The other warps copy a part into registers, which frees its place, find
-// its maximum and sum, hand both to every CTA of the row (one 8-byte store a warp and CTA,
-// counted by the receiver's barrier), and write the gradient from the registers.
+// one computes while another waits.  The roles of a CTA's warps:
+//
+//   leader    brings the CTA's parts of the next rows into shared memory by bulk copies, and
+//             reads what the rows have beside their logits
+//   others    copy a part into registers, which frees its place, find its maximum and sum,
+//             and hand both to every CTA of the row (one 8-byte store a warp and CTA, counted
+//             by the receiver's barrier); later they write the gradient from the registers
+//   closer    adds up the row's partial sums, and works out its loss and factors once for all
+//             (done by every warp it took half of the kernel's instructions); it also has the
+//             elements before the row's first vector and after its last
+//
+// Exponents here are x = z c - r with c = log2(e) / T and r = m c rounded: one rounding, of x
+// itself, as z c - r is one operation, so that a common level takes no digits.  Where m c
+// leaves the range that this holds in (|m c| >= 2^100), any two different logits are
+// infinitely far apart: the warp replaces its z by z - m, and r by 0.
 constexpr int kPartSlots = 4;
+constexpr float kFarExponent = 1.2676506002282294e30f;  // 2^100
 
 struct PartShape {
   int cluster;    // CTAs of a row
   int seg_vecs;   // vectors of a part
   int slots;      // parts in shared memory
   int slot_bytes;
+};
+
+// What the closer leaves for the CTA's other warps.
+struct PartResult {
+  float m, r;       // the row's maximum; its exponent
+  float factor;     // gradient of an element: factor 2^x
+  float f, inv_s;   // f and 1 / S, S by the maximum itself
+  float named;      // policy: the gradient at the target
+  int column;       // policy: the target's, or -1
+  int entries;
 };
 
 __device__ __forceinline__ void bulk_copy(uint32_t to, const void* from, uint32_t bytes, uint32_t bar) {
@@ -660,20 +958,47 @@ __device__ __forceinline__ void push_pair(uint32_t to, float a, float b, uint32_
                : "memory");
 }
 
-template <int THREADS>
-__device__ __forceinline__ void consumers_sync() {
-  asm volatile("barrier.sync 1, %0;" ::"n"(THREADS) : "memory");
+__device__ __forceinline__ bool far_exponent(float m, float c) { return !(fabsf(m * c) < kFarExponent); }
+
+// 2^(z c - r) of a vector's elements.
+template <typename T>
+__device__ __forceinline__ void vec_exp2(const uint4& v, Pair c, Pair minus_r, Pair (&e)[kVecElems<T> / 2]) {
+  vec_pairs<T>(v, e);
+#pragma unroll
+  for (int k = 0; k < kVecElems<T> / 2; ++k) {
+    const float2 x = unpair(fma_pair(e[k], c, minus_r));
+    e[k] = pair(ex2_approx(x.x), ex2_approx(x.y));
+  }
 }
 
-// THREADS: of the warps that compute; VPT: vectors a thread holds.
-template <typename T, int KIND, int THREADS, int VPT, int CTAS_PER_SM>
-__global__ void __launch_bounds__(THREADS + 32, CTAS_PER_SM)
+// Elements z of a vector become z - m.
+template <typename T>
+__device__ __forceinline__ void vec_subtract(uint4& v, float m) {
+  Pair e[kVecElems<T> / 2];
+  vec_pairs<T>(v, e);
+#pragma unroll
+  for (int k = 0; k < kVecElems<T> / 2; ++k) e[k] = e[k] + pair(-m);
+  v = pack_pairs<T>(e);
+}
+
+// A row of whole vectors.
+template <typename T>
+__device__ __forceinline__ RowSplit whole_row(int64_t V) {
+  return {0, 0, static_cast<int>(static_cast<unsigned>(V) / kVecElems<T>)};
+}
+
+// THREADS: of the warps that compute; VPT: vectors a thread holds; WHOLE: all rows are whole
+// vectors, in both matrices (what a row's place costs its threads was a fifth of their time).
+template <typename T, int KIND, int THREADS, int VPT, int CTAS_PER_SM, bool WHOLE>
+__global__ void __launch_bounds__(THREADS + 64, CTAS_PER_SM)
     row_loss_parts_kernel(const RowLossParams p, const PartShape shape) {
-  constexpr int kE = kVecElems<T>, kWarps = THREADS / 32;
+  constexpr int kE = kVecElems<T>, kWarps = THREADS / 32, kSums = kWarps + 1;
+  constexpr int kKept = KIND == kStats ? 4 : 2;  // rows whose numbers a CTA keeps
   extern __shared__ __align__(128) uint8_t part_memory[];
-  __shared__ uint64_t full[kPartSlots], empty[kPartSlots], told[2], summed[2];
-  __shared__ RowInfo infos[2];
-  __shared__ float2 parts[2][8 * kWarps];  // (maximum, sum) of every warp of the row's CTAs
+  __shared__ uint64_t full[kPartSlots], empty[kPartSlots], told[kKept], summed[kKept], closed[kKept];
+  __shared__ RowInfo infos[kKept];
+  __shared__ PartResult results[kKept];
+  __shared__ float2 parts[kKept][8 * kSums];  // (maximum, sum) of every warp of the row's CTAs; the closers' are empty
   __shared__ int aborted, count, all_bits;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cluster = shape.cluster;
@@ -684,99 +1009,224 @@ __global__ void __launch_bounds__(THREADS + 32, CTAS_PER_SM)
   if (tid == 0) {
     for (int i = 0; i < kPartSlots; ++i) {
       mbar_init(smem_addr(&full[i]), 1);
-      mbar_init(smem_addr(&empty[i]), kWarps);
+      mbar_init(smem_addr(&empty[i]), kWarps + (KIND == kDistill ? 1 : 0));
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < kKept; ++i) {
       mbar_init(smem_addr(&told[i]), 1);
       mbar_init(smem_addr(&summed[i]), 1);
+      mbar_init(smem_addr(&closed[i]), 1);
     }
     aborted = count = all_bits = 0;
     fence_barrier_init();
     if (blockIdx.x == 0) expect_arrivals(p.arrivals, p.tag);
   }
   cluster_sync_all();  // (also the CTA's own barrier)
+  // a wait that runs out: the CTA goes on through its rows without copying or writing, so that no warp waits for
+  // another for ever, and leaves a status bit
   const WaitCtl ctl{&aborted, nullptr, p.timeout_ns};
   const auto row_of = [&](int i) { return static_cast<int64_t>(first_row) + static_cast<int64_t>(i) * row_step; };
   const auto logits_of = [&](int64_t row) { return static_cast<const T*>(p.logits) + row * p.ld; };
+  const auto split_of = [&](const T* x) { return WHOLE ? whole_row<T>(p.V) : split_row(x, p.V); };
   const int first_vec = rank * shape.seg_vecs;
   const auto part_vecs = [&](const RowSplit& split) {
-    const int64_t left = split.vecs - first_vec;
-    return static_cast<int>(left < 0 ? 0 : left < shape.seg_vecs ? left : shape.seg_vecs);
+    const int left = split.vecs - first_vec;
+    return left < 0 ? 0 : left < shape.seg_vecs ? left : shape.seg_vecs;
   };
-  double loss = 0;
-  int rows = 1;
 
   if (warp == kWarps) {
     // ------------------------------------------------ the leader
-    int bits = 0, issued = 0;
+    int bits = 0, issued = 0, to_slot = 0;
     const auto issue = [&]() {  // the next row's part, by one lane
       const T* x = logits_of(row_of(issued));
-      const RowSplit split = split_row(x, p.V);
+      const RowSplit split = split_of(x);
       const uint32_t bytes = static_cast<uint32_t>(part_vecs(split)) * 16u;
-      const int slot = issued % shape.slots;
-      const uint32_t bar = smem_addr(&full[slot]);
+      const uint32_t bar = smem_addr(&full[to_slot]);
       mbar_arrive_expect_tx(bar, bytes);
       if (bytes > 0)
-        bulk_copy(smem_addr(part_memory) + slot * shape.slot_bytes,
+        bulk_copy(smem_addr(part_memory) + to_slot * shape.slot_bytes,
                   reinterpret_cast<const uint4*>(x + split.head) + first_vec, bytes, bar);
       ++issued;
+      if (++to_slot == shape.slots) to_slot = 0;
     };
     if (lane == 0)
       while (issued < shape.slots && issued < mine) issue();
+    int slot = 0, use = 0;  // i % slots, i / slots
+    const auto read_ahead = [&](int64_t row) {
+      if constexpr (KIND == kDistill)
+        return list_ahead(p, row);
+      else
+        return policy_ahead(p, row);
+    };
+    const auto read_logits = [&](int64_t row, auto& a) {
+      if constexpr (KIND == kDistill)
+        list_logits<T>(p, row, a);
+      else
+        policy_logit<T>(p, row, a, &bits);
+    };
+    auto ahead = read_ahead(row_of(0)), next = read_ahead(row_of(1));
+    read_logits(row_of(0), ahead);
     for (int i = 0; i < mine; ++i) {
-      // infos[i & 1] was last used for row i - 2, and all warps have gone on to row i - 1
+      // all warps have read row i - 1's part, so they have waited for row i - 2 to be closed (row i - 3 for kStats):
+      // infos of row i - 4 and the list of row i - 2 are no longer used
       const int64_t row = row_of(i);
       RowInfo r;
       if constexpr (KIND == kDistill) {
         const size_t at = static_cast<size_t>(i & 1) * list_bytes(p.K);
-        r = teacher_row<T>(p, row, list_at(lists + at, p.K), reinterpret_cast<int*>(lists + 2 * list_bytes(p.K)), &bits);
-      } else if (lane == 0) {
-        r = policy_row<T>(p, row, &bits);
+        const RowSplit split = split_of(logits_of(row));
+        const int n = part_vecs(split);
+        r = teacher_row<T>(p, row, ahead, list_at(lists + at, p.K),
+                           reinterpret_cast<int*>(lists + 2 * list_bytes(p.K)), &bits, [&](int column) {
+                             const int inside = column - split.head, vec = inside / kE;
+                             return inside < 0          ? rank == 0
+                                    : vec >= split.vecs ? rank == cluster - 1
+                                                        : vec >= first_vec && vec < first_vec + n;
+                           });
+      } else {
+        r = ahead.r;
       }
       if (lane == 0) {
-        infos[i & 1] = r;
-        mbar_arrive(smem_addr(&told[i & 1]));
-        const int slot = i % shape.slots;
-        const bool read = mbar_wait_sleep(smem_addr(&empty[slot]), (i / shape.slots) & 1, ctl);
+        infos[i % kKept] = r;
+        mbar_arrive(smem_addr(&told[i % kKept]));
+      }
+      ahead = next;
+      read_logits(row_of(i + 1), ahead);
+      next = read_ahead(row_of(i + 2));
+      if (lane == 0) {
+        const bool read = mbar_wait_sleep(smem_addr(&empty[slot]), use & 1, ctl);
         if (read && !*ctl.abort_flag && issued < mine) issue();
       }
+      if (++slot == shape.slots) slot = 0, ++use;
       __syncwarp();
     }
     if (lane == 0 && *ctl.abort_flag)  // copies under way have to land before this CTA ends
       for (int i = issued > shape.slots ? issued - shape.slots : 0; i < issued; ++i)
         mbar_wait_drain(smem_addr(&full[i % shape.slots]), (i / shape.slots) & 1, p.timeout_ns);
     if (bits != 0) atomicOr(&all_bits, bits);
-  } else {
-    // ------------------------------------------------ the others
+  }
+
+  double loss = 0;
+  int rows = 1;
+  if (warp == kWarps + 1) {
+    // ------------------------------------------------ the closer
     if (p.reduction == FLCE_REDUCTION_MEAN && KIND != kStats) {
       if (p.counts != nullptr) {
         grid_dependency_wait();
         rows = counted_rows(p.counts);
       } else {
-        int n = count_rows<KIND>(p, tid, THREADS);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-        if (lane == 0 && n != 0) atomicAdd(&count, n);
-        consumers_sync<THREADS>();
+        asm volatile("barrier.sync 2, %0;" ::"n"(THREADS + 32) : "memory");  // the others have counted
         rows = count;
       }
     }
     const float scale = p.reduction == FLCE_REDUCTION_MEAN ? p.grad_scale / static_cast<float>(rows) : p.grad_scale;
-    const Pair c = pair(p.c);
-    int slot = 0, use = 0;  // i % slots, i / slots
+    // its element of a row, if the CTA has one end of the row: read a row ahead
+    const auto edge_of = [&](int i, int* at) -> float {
+      *at = -1;
+      if (WHOLE || i >= mine) return -INFINITY;
+      const T* x = logits_of(row_of(i));
+      const RowSplit split = split_of(x);
+      if (rank == 0 && lane < split.head) *at = lane;
+      if (rank == cluster - 1 && lane >= 8 && lane < 8 + split.tail) *at = static_cast<int>(p.V) - split.tail + lane - 8;
+      return *at >= 0 ? to_float(x[*at]) : -INFINITY;
+    };
+    int edge, next_edge, slot = 0;
+    float z, next_z = edge_of(0, &next_edge);
     for (int i = 0; i < mine; ++i) {
-      const int64_t row = row_of(i);
-      const T* x = logits_of(row);
-      const RowSplit split = split_row(x, p.V);
-      const int n = part_vecs(split);
-      // elements before the row's first vector and after its last, by the CTAs at its ends
-      int64_t extra = -1;
-      if (rank == 0 && tid < split.head) extra = tid;
-      if (rank == cluster - 1 && tid >= 32 && tid < 32 + split.tail) extra = split.head + split.vecs * kE + tid - 32;
-      const float z = extra >= 0 ? to_float(x[extra]) : -INFINITY;
-      const int b = i & 1, phase = (i >> 1) & 1;
+      if (KIND == kDistill && lane == 0) mbar_arrive(smem_addr(&empty[slot]));  // done with row i - 1's list
+      if (++slot == shape.slots) slot = 0;
+      z = next_z, edge = next_edge;
+      next_z = edge_of(i + 1, &next_edge);
+      const int b = i % kKept, phase = (i / kKept) & 1;
       const uint32_t sum_bar = smem_addr(&summed[b]);
-      if (tid == 0) mbar_arrive_expect_tx(sum_bar, static_cast<uint32_t>(cluster) * kWarps * 8u);
+      if (lane == 0) mbar_arrive_expect_tx(sum_bar, static_cast<uint32_t>(cluster) * kSums * 8u);
+      // no CTA may write a row (its logits may be in the same place) before all have read what they need of it:
+      // this one's word for it is its closer's share in the sums
+      bool ok = mbar_wait(smem_addr(&told[b]), phase, ctl);
+      float edge_m = -INFINITY, edge_s = 0.f;
+      if constexpr (!WHOLE) {
+        edge_m = warp_max_redux(z);
+        // the same exponents as a part's (vec_exp2)
+        const float taken = !(edge_m > -INFINITY) ? 0.f : __fmul_rn(edge_m, p.c);
+        if (edge >= 0) edge_s = edge_m > -INFINITY && far_exponent(edge_m, p.c) ? ex2_approx((z - edge_m) * p.c)
+                                                                               : ex2_approx(fmaf(z, p.c, -taken));
+        edge_s = warp_sum(edge_s);
+      }
+      if (ok && lane < cluster)
+        push_pair(map_to_cta(smem_addr(&parts[b][rank * kSums + kWarps]), lane), edge_m, edge_s,
+                  map_to_cta(sum_bar, lane));
+      const RowInfo info = infos[b];
+      ok = mbar_wait_cluster(sum_bar, phase, ctl) && ok;
+      float top = -INFINITY;
+      for (int k = lane; k < cluster * kSums; k += 32) top = fmaxf(top, parts[b][k].x);
+      const float m = warp_max_redux(top);
+      const bool far = far_exponent(m, p.c);
+      const float r = far ? 0.f : __fmul_rn(m, p.c);
+      float sum = 0.f;
+      for (int k = lane; k < cluster * kSums; k += 32) {
+        const float2 q = parts[b][k];
+        // a warp's sum goes by its own rounded exponent; warps that have found nothing have 0, or NaN
+        const float scaled = q.y * ex2_approx(far ? (q.x == m ? 0.f : -INFINITY) : __fmul_rn(q.x, p.c) - r);
+        sum += q.x > -INFINITY ? scaled : q.y;
+      }
+      sum = warp_sum(sum);                                        // of 2^(z c - r)
+      const float s = far ? sum : sum * ex2_approx(fmaf(-m, p.c, r));  // of 2^((z - m) c)
+      const RowResult result = row_result<KIND>(p, info, m, s, scale);
+      if (lane == 0) {
+        if (rank == 0 && ok) store_result<KIND>(p, row_of(i), result, m, s, &loss);
+        PartResult out;
+        out.m = m, out.r = r, out.f = result.f, out.inv_s = 1.f / s, out.factor = result.f / sum;
+        out.named = KIND == kPolicy ? target_grad(result) : 0.f;
+        out.column = info.column, out.entries = info.entries;
+        results[b] = out;
+        mbar_arrive(smem_addr(&closed[b]));
+      }
+      __syncwarp();
+      if (!WHOLE && KIND != kStats && p.grad != nullptr && ok) {
+        T* g = static_cast<T*>(p.grad) + row_of(i) * p.ld_grad;
+        const bool zero = result.f == 0.f;
+        if (edge >= 0) {
+          float out = zero ? 0.f : result.f * (1.f / s) * ex2_approx((z - m) * p.c);
+          if (KIND == kPolicy && !zero && edge == info.column) out = target_grad(result);
+          g[edge] = from_float<T>(out);
+        }
+        if constexpr (KIND == kDistill) {
+          __syncwarp();  // the places that the row names are written after the rest
+          if (!zero) {
+            const RowSplit split = split_of(logits_of(row_of(i)));
+            const TeacherList list = list_at(lists + static_cast<size_t>(i & 1) * list_bytes(p.K), p.K);
+            for (int k = lane; k < info.entries; k += 32) {
+              const int column = list.column[k];
+              if (column < split.head || column >= static_cast<int>(p.V) - split.tail)
+                g[column] = from_float<T>(entry_grad(p, list, k, result.f, m, 1.f / s));
+            }
+          }
+          __syncwarp();
+        }
+      }
+    }
+  }
+
+  if (warp < kWarps) {
+    // ------------------------------------------------ the others
+    if (p.reduction == FLCE_REDUCTION_MEAN && KIND != kStats && p.counts == nullptr) {
+      int n = count_rows<KIND>(p, tid, THREADS);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+      if (lane == 0 && n != 0) atomicAdd(&count, n);
+      asm volatile("barrier.sync 2, %0;" ::"n"(THREADS + 32) : "memory");
+    }
+    const Pair c = pair(p.c);
+    int slot = 0, use = 0;
+    const T* x = logits_of(first_row);
+    T* g = static_cast<T*>(p.grad) + first_row * p.ld_grad;
+    const int64_t x_step = row_step * p.ld, g_step = row_step * p.ld_grad;
+    RowSplit split = split_of(x);
+    int n = part_vecs(split);
+    for (int i = 0; i < mine; ++i, x += x_step, g += g_step) {
+      if constexpr (!WHOLE) {
+        split = split_of(x);
+        n = part_vecs(split);
+      }
+      const int b = i % kKept, phase = (i / kKept) & 1;
       bool ok = mbar_wait_sleep(smem_addr(&full[slot]), use & 1, ctl);
       const uint4* from = reinterpret_cast<const uint4*>(part_memory + slot * shape.slot_bytes);
       uint4 v[VPT];
@@ -785,104 +1235,108 @@ __global__ void __launch_bounds__(THREADS + 32, CTAS_PER_SM)
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_addr(&empty[slot]));
       if (++slot == shape.slots) slot = 0, ++use;
-      const float m = warp_max_redux(fmaxf(vecs_max<T, VPT>(v), z));
-      const float shift = m > -INFINITY ? m : 0.f;
+      const float m = warp_max_redux(vecs_max<T, VPT>(v));
+      const bool far = m > -INFINITY && far_exponent(m, p.c);
+      if (far) {
+#pragma unroll
+        for (int k = 0; k < VPT; ++k) vec_subtract<T>(v[k], m);
+      }
+      float r = far || !(m > -INFINITY) ? 0.f : __fmul_rn(m, p.c);
       Pair sum = pair(0.f);
 #pragma unroll
-      for (int k = 0; k < VPT; ++k) vec_add_exp<T>(v[k], pair(-shift), c, sum);
-      float2 both = unpair(sum);
-      if (extra >= 0) both.x += ex2_approx((z - shift) * p.c);
-      const float s = warp_sum(both.x + both.y);
-      // the row's other numbers are read before any of its CTAs writes a gradient (in place)
-      ok = mbar_wait_sleep(smem_addr(&told[b]), phase, ctl) && ok;
-      if (ok && lane < cluster)
-        push_pair(map_to_cta(smem_addr(&parts[b][rank * kWarps + warp]), lane), m, s, map_to_cta(sum_bar, lane));
-      ok = mbar_wait_cluster(sum_bar, phase, ctl) && ok;
-      float pm = -INFINITY, ps = 0.f;
-      for (int k = lane; k < cluster * kWarps; k += 32) {
-        const float2 q = parts[b][k];
-        const float top = fmaxf(pm, q.x);
-        if (top > -INFINITY) {
-          ps = (pm > -INFINITY ? ps * ex2_approx((pm - top) * p.c) : ps) +
-               (q.x > -INFINITY ? q.y * ex2_approx((q.x - top) * p.c) : q.y);
-          pm = top;
-        } else {
-          ps += q.y;  // (NaN of a part that has nothing else)
-        }
+      for (int k = 0; k < VPT; ++k) {
+        Pair e[kE / 2];
+        vec_exp2<T>(v[k], c, pair(-r), e);
+#pragma unroll
+        for (int q = 0; q < kE / 2; ++q) sum = sum + e[q];
       }
-      const float2 all = combine_parts(pm, ps, p.c);
-      const RowInfo r = infos[b];
-      const RowResult result = row_result<KIND>(p, r, all.x, all.y, scale);
-      if (rank == 0 && tid == 0 && ok) store_result<KIND>(p, row, result, all.x, all.y, &loss);
-      if (KIND == kStats || p.grad == nullptr || !ok) {
-        if constexpr (KIND == kDistill)
-          if (p.grad != nullptr) consumers_sync<THREADS>();
+      const float2 both = unpair(sum);
+      const float s = warp_sum(both.x + both.y);
+      if (ok && lane < cluster)
+        push_pair(map_to_cta(smem_addr(&parts[b][rank * kSums + warp]), lane), m, s,
+                  map_to_cta(smem_addr(&summed[b]), lane));
+      if constexpr (KIND == kStats) {
+        // a row is closed while the next one is read.  What a row's sums overwrite, the row's four before, is no
+        // longer wanted: row i - 1 closed here means that every CTA has closed row i - 2
+        if (i > 0) mbar_wait_sleep(smem_addr(&closed[(i - 1) % kKept]), ((i - 1) / kKept) & 1, ctl);
         continue;
       }
-      T* g = static_cast<T*>(p.grad) + row * p.ld_grad;
-      const float inv_s = 1.f / all.y, f = result.f * inv_s;
-      const Pair minus_m = pair(-all.x), factor = pair(f);
+      ok = mbar_wait_sleep(smem_addr(&closed[b]), phase, ctl) && ok;
+      if (p.grad == nullptr) continue;
+      const PartResult result = results[b];
       const bool zero = result.f == 0.f;
+      // a warp that has taken its own maximum off: the row's, or far below it
+      r = !far ? result.r : m == result.m ? 0.f : INFINITY;
+      if (!far && far_exponent(result.m, p.c)) r = result.m > 0.f ? INFINITY : 0.f;
+      const Pair minus_r = pair(-r), factor = pair(result.factor);
       T* to = g + split.head + (static_cast<int64_t>(first_vec) + tid) * kE;
       // the 16-bit elements are widened again: kept from the sum, they would not fit in the registers
 #pragma unroll
       for (int k = 0; k < VPT; ++k) asm volatile("" : "+r"(v[k].x), "+r"(v[k].y), "+r"(v[k].z), "+r"(v[k].w));
-      if (same_phase(x, g)) {
+      const auto gradient = [&](const uint4& vec) {
+        if (zero) return make_uint4(0, 0, 0, 0);
+        Pair e[kE / 2];
+        vec_exp2<T>(vec, c, minus_r, e);
 #pragma unroll
-        for (int k = 0; k < VPT; ++k) {
-          const uint4 out = zero ? make_uint4(0, 0, 0, 0) : vec_grad<T>(v[k], minus_m, c, factor);
-          if (k * THREADS + tid < n) __stcs(reinterpret_cast<uint4*>(to + k * THREADS * kE), out);
-        }
-      } else {
+        for (int q = 0; q < kE / 2; ++q) e[q] = e[q] * factor;
+        return pack_pairs<T>(e);
+      };
+      if (ok) {
+        if (WHOLE || same_phase(x, g)) {
 #pragma unroll
-        for (int k = 0; k < VPT; ++k) {
-          const uint4 out = zero ? make_uint4(0, 0, 0, 0) : vec_grad<T>(v[k], minus_m, c, factor);
-          if (k * THREADS + tid < n) store_vec<T>(to + k * THREADS * kE, out, false);
+          for (int k = 0; k < VPT; ++k) {
+            const uint4 out = gradient(v[k]);
+            if (k * THREADS + tid < n) __stcs(reinterpret_cast<uint4*>(to + k * THREADS * kE), out);
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < VPT; ++k) {
+            const uint4 out = gradient(v[k]);
+            if (k * THREADS + tid < n) store_vec<T>(to + k * THREADS * kE, out, false);
+          }
         }
       }
-      if (extra >= 0) g[extra] = from_float<T>(zero ? 0.f : f * ex2_approx((z - all.x) * p.c));
-      // the places that the row names are written after the rest
+      // the places that the row names are written after the rest, by the warp that has written there
+      if (zero || !ok) continue;
       if constexpr (KIND == kDistill) {
-        consumers_sync<THREADS>();
-        if (zero) continue;
-        const TeacherList list = list_at(lists + static_cast<size_t>(b) * list_bytes(p.K), p.K);
-        for (int k = tid; k < r.entries; k += THREADS) {
+        const TeacherList list = list_at(lists + static_cast<size_t>(i & 1) * list_bytes(p.K), p.K);
+        __syncwarp();
+        for (int k = lane; k < result.entries; k += 32) {
           const int column = list.column[k];
-          if (column < 0) continue;
-          const int inside = column - split.head;
-          const int64_t vec = inside / kE;
-          const bool here = inside < 0            ? rank == 0
-                            : vec >= split.vecs   ? rank == cluster - 1
-                                                  : vec >= first_vec && vec < first_vec + n;
-          if (here) g[column] = from_float<T>(entry_grad(p, list, k, result.f, all.x, inv_s));
+          if (!WHOLE && (column < split.head || column >= static_cast<int>(p.V) - split.tail)) continue;  // the closer's
+          const unsigned vec = static_cast<unsigned>(column - split.head) / kE - first_vec;
+          if (vec % THREADS / 32 == static_cast<unsigned>(warp))
+            g[column] = from_float<T>(entry_grad(p, list, k, result.f, result.m, result.inv_s));
         }
-      } else if (!zero) {
-        const int inside = r.column - split.head;
-        const int64_t vec = inside / kE - first_vec;
-        const bool here = inside >= 0 && inside / kE < split.vecs ? vec >= 0 && vec < n && vec % THREADS == tid
-                                                                  : extra == r.column;
-        if (here) g[r.column] = from_float<T>(target_grad(result));
+      } else if (WHOLE || result.column >= split.head) {
+        const int vec = (result.column - split.head) / kE;
+        if (vec < split.vecs && vec >= first_vec && vec < first_vec + n && (vec - first_vec) % THREADS == tid)
+          g[result.column] = from_float<T>(result.named);
       }
     }
   }
+  // the closer's numbers are the CTA's
+  __shared__ double all_loss;
+  __shared__ int all_rows;
+  if (warp == kWarps + 1 && lane == 0) all_loss = loss, all_rows = rows;
   __syncthreads();
   cluster_sync_all();  // no CTA ends while another may still write to its shared memory
-  finish_rows(p, loss, all_bits | (aborted ? FLCE_STATUS_BIT_TIMEOUT : 0), rows);
+  finish_rows(p, all_loss, all_bits | (aborted ? FLCE_STATUS_BIT_TIMEOUT : 0), all_rows);
 }
 
-template <typename T, int KIND, int THREADS, int VPT, int CTAS_PER_SM>
-cudaError_t launch_parts(const RowLossParams& p, PartShape shape, cudaStream_t s) {
-  constexpr auto kernel = row_loss_parts_kernel<T, KIND, THREADS, VPT, CTAS_PER_SM>;
-  constexpr size_t kLargest = 224 * 1024;
+template <typename T, int KIND, int THREADS, int VPT, int CTAS_PER_SM, bool WHOLE>
+cudaError_t launch_parts_of(const RowLossParams& p, PartShape shape, cudaStream_t s) {
+  constexpr auto kernel = row_loss_parts_kernel<T, KIND, THREADS, VPT, CTAS_PER_SM, WHOLE>;
+  constexpr size_t kLargest = 216 * 1024;  // with what is not dynamic, an SM's shared memory
   const size_t lists = KIND == kDistill ? 2 * list_bytes(p.K) + table_slots(p.K) * 4 : 0;
-  const size_t room = (CTAS_PER_SM > 1 ? kLargest / CTAS_PER_SM - 1024 : kLargest) - 0;
+  const size_t room = kLargest / CTAS_PER_SM - 4096;  // less what is not part_memory
   shape.slot_bytes = (shape.seg_vecs * 16 + 127) & ~127;
   shape.slots = static_cast<int>(room > lists ? (room - lists) / shape.slot_bytes : 1);
   if (shape.slots > kPartSlots) shape.slots = kPartSlots;
   if (shape.slots < 1) shape.slots = 1;
   const size_t smem = static_cast<size_t>(shape.slots) * shape.slot_bytes + lists;
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(THREADS + 32);
+  cfg.blockDim = dim3(THREADS + 64);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute attrs[2];
@@ -920,13 +1374,25 @@ cudaError_t launch_parts(const RowLossParams& p, PartShape shape, cudaStream_t s
 
 // ---------------------------------------------------------------- host side
 
-// Parts of up to 2048 vectors by 256 threads (32 KB; three CTAs an SM, with two parts each
+template <typename T, int KIND, int THREADS, int VPT, int CTAS_PER_SM>
+cudaError_t launch_parts(const RowLossParams& p, const PartShape& shape, cudaStream_t s) {
+  constexpr int kE = kVecElems<T>;
+  const bool whole = p.V % kE == 0 && aligned_to(p.logits, 16) && p.ld % kE == 0 &&
+                     (p.grad == nullptr || (aligned_to(p.grad, 16) && p.ld_grad % kE == 0));
+  return whole ? launch_parts_of<T, KIND, THREADS, VPT, CTAS_PER_SM, true>(p, shape, s)
+               : launch_parts_of<T, KIND, THREADS, VPT, CTAS_PER_SM, false>(p, shape, s);
+}
+
+// Rows of up to 256 vectors (4 KB) by warps.  Parts of up to 2048 vectors by 256 threads (32 KB; three CTAs an SM, with two parts each
 // in shared memory), of up to 4224 by 384; rows beyond eight of these are read twice.
 template <typename T, int KIND>
 cudaError_t launch_rows_of(const RowLossParams& p, cudaStream_t s) {
   const int64_t vecs = p.V / kVecElems<T>;
   PartShape shape = {};
-  if (p.N == 0 || vecs < 128 || vecs > 8 * 4224) return launch_long<T, KIND>(p, s);
+  if (p.N == 0 || vecs > 8 * 4224) return launch_long<T, KIND>(p, s);
+  if (vecs <= 32) return launch_warps<T, KIND, 1>(p, s);
+  if (vecs <= 128) return launch_warps<T, KIND, 4>(p, s);
+  if (vecs <= 256) return launch_warps<T, KIND, 8>(p, s);
   const int64_t wide = vecs > 8 * 2048 ? 4224 : 2048;
   shape.cluster = 1;
   while (div_up(vecs, shape.cluster) > wide) shape.cluster *= 2;
