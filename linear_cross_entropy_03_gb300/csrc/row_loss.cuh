@@ -234,46 +234,80 @@ struct RowInfo {
   int entries;  // distill: length of the list
 };
 
+// What a row has beside its logits is read in two steps, as the second (logits at places that
+// the first names) needs the first: a warp that leads others starts both ahead of the row,
+// and looks at what it has read when it comes to the row (what is read stays as it lies in
+// memory until then: a conversion would wait for it).  Rows past the end have nothing.
 template <typename T>
-__device__ __forceinline__ float load_logit(const RowLossParams& p, int64_t row, int64_t column) {
-  return to_float(static_cast<const T*>(p.logits)[row * p.ld + column]);
+struct Raw {
+  T v;
+};
+template <>
+struct Raw<__half> {
+  uint16_t v;
+};
+template <>
+struct Raw<__nv_bfloat16> {
+  uint16_t v;
+};
+template <typename T>
+__device__ __forceinline__ Raw<T> raw_logit(const RowLossParams& p, int64_t row, int64_t column) {
+  return reinterpret_cast<const Raw<T>*>(p.logits)[row * p.ld + column];
+}
+template <typename T>
+__device__ __forceinline__ float raw_float(Raw<T> r) {
+  if constexpr (sizeof(T) == 4)
+    return r.v;
+  else if constexpr (std::is_same<T, __half>::value)
+    return __half2float(__ushort_as_half(r.v));
+  else
+    return __uint_as_float(static_cast<uint32_t>(r.v) << 16);
 }
 
-// What a row has beside its logits is read in two steps, as the second (logits at places that
-// the first names) needs the first: a warp that leads others starts both ahead of the row.
-// Row numbers past the end are rows without anything.
+template <typename T>
 struct PolicyAhead {
-  RowInfo r;
   int64_t target;
+  float weight, grad_out, advantage, old_logp, ref_logp;
+  Raw<T> z;
 };
-__device__ __forceinline__ PolicyAhead policy_ahead(const RowLossParams& p, int64_t row) {
-  PolicyAhead a = {};
-  a.r.column = -1;
+template <typename T>
+__device__ __forceinline__ PolicyAhead<T> policy_ahead(const RowLossParams& p, int64_t row) {
+  PolicyAhead<T> a = {};
   a.target = p.ignore_index;
+  a.weight = a.grad_out = 1.f;
   if (row >= p.N) return a;
   a.target = __ldg(p.target + row);
-  a.r.weight = p.row_weight != nullptr ? __ldg(p.row_weight + row) : 1.f;
-  a.r.grad_out = p.grad_out != nullptr ? __ldg(p.grad_out + row) : 1.f;
-  a.r.advantage = p.advantage != nullptr ? __ldg(p.advantage + row) : 0.f;
-  a.r.old_logp = p.old_logp != nullptr ? __ldg(p.old_logp + row) : 0.f;
-  a.r.ref_logp = p.ref_logp != nullptr ? __ldg(p.ref_logp + row) : 0.f;
+  if (p.row_weight != nullptr) a.weight = __ldg(p.row_weight + row);
+  if (p.grad_out != nullptr) a.grad_out = __ldg(p.grad_out + row);
+  if (p.advantage != nullptr) a.advantage = __ldg(p.advantage + row);
+  if (p.old_logp != nullptr) a.old_logp = __ldg(p.old_logp + row);
+  if (p.ref_logp != nullptr) a.ref_logp = __ldg(p.ref_logp + row);
   return a;
 }
 template <typename T>
-__device__ __forceinline__ void policy_logit(const RowLossParams& p, int64_t row, PolicyAhead& a, int* bits) {
-  if (a.target == p.ignore_index) return;
+__device__ __forceinline__ void policy_logit(const RowLossParams& p, int64_t row, PolicyAhead<T>& a) {
+  if (a.target != p.ignore_index && a.target >= 0 && a.target < p.V) a.z = raw_logit<T>(p, row, a.target);
+}
+template <typename T>
+__device__ __forceinline__ RowInfo policy_info(const RowLossParams& p, const PolicyAhead<T>& a, int* bits) {
+  RowInfo r = {};
+  r.weight = a.weight, r.grad_out = a.grad_out, r.advantage = a.advantage;
+  r.old_logp = a.old_logp, r.ref_logp = a.ref_logp;
+  r.column = -1;
+  if (a.target == p.ignore_index) return r;
   if (a.target < 0 || a.target >= p.V) {
     *bits |= FLCE_STATUS_BIT_TARGET_RANGE;
-    return;
+    return r;
   }
-  a.r.column = static_cast<int>(a.target);
-  a.r.zt = load_logit<T>(p, row, a.target);
+  r.column = static_cast<int>(a.target);
+  r.zt = raw_float<T>(a.z);
+  return r;
 }
 template <typename T>
 __device__ __forceinline__ RowInfo policy_row(const RowLossParams& p, int64_t row, int* bits) {
-  PolicyAhead a = policy_ahead(p, row);
-  policy_logit<T>(p, row, a, bits);
-  return a.r;
+  PolicyAhead<T> a = policy_ahead<T>(p, row);
+  policy_logit<T>(p, row, a);
+  return policy_info<T>(p, a, bits);
 }
 
 // A teacher's list in shared memory: columns (-1: no such place), shares and logits.
@@ -295,34 +329,64 @@ __device__ __forceinline__ TeacherList list_at(uint8_t* at, int K) {
   return {reinterpret_cast<int*>(at), reinterpret_cast<float*>(at) + room, reinterpret_cast<float*>(at) + 2 * room};
 }
 
-// A list's first entries, four a lane.
-constexpr int kListAhead = 4;
+// A list's first entries, two a lane (four took more registers than a warp of the form by
+// parts has, and what is spilled is waited for).
+constexpr int kListAhead = 2;
+template <typename T>
 struct ListAhead {
-  int column[kListAhead];  // -1: the list has ended, -2: not a column
-  float value[kListAhead], z[kListAhead];
+  uint2 id[kListAhead];          // 64 bits, or the first 32 of them
+  uint32_t value[kListAhead];    // 32 bits, or the first 16 of them
+  Raw<T> z[kListAhead];
   float weight, grad_out;
 };
-__device__ __forceinline__ int column_of(const RowLossParams& p, int64_t id) {
-  return id < 0 ? -1 : id < p.V ? static_cast<int>(id) : -2;
+// An id's column; -1: the list has ended, -2: not a column.
+__device__ __forceinline__ int column_of(const RowLossParams& p, uint2 id) {
+  const int64_t wide = p.ids32 ? static_cast<int>(id.x) : static_cast<int64_t>(static_cast<uint64_t>(id.y) << 32 | id.x);
+  return wide < 0 ? -1 : wide < p.V ? static_cast<int>(wide) : -2;
 }
-__device__ __forceinline__ ListAhead list_ahead(const RowLossParams& p, int64_t row) {
-  ListAhead a;
+__device__ __forceinline__ uint2 raw_id(const RowLossParams& p, int64_t i) {
+  uint2 r = make_uint2(0, 0);
+  if (p.ids32)
+    r.x = __ldg(static_cast<const uint32_t*>(p.ids) + i);
+  else
+    r = __ldg(static_cast<const uint2*>(p.ids) + i);
+  return r;
+}
+__device__ __forceinline__ uint32_t raw_value(const RowLossParams& p, int64_t i) {
+  return p.value_dtype == FLCE_DTYPE_FP32 ? __ldg(static_cast<const uint32_t*>(p.values) + i)
+                                          : __ldg(static_cast<const uint16_t*>(p.values) + i);
+}
+__device__ __forceinline__ float value_of(const RowLossParams& p, uint32_t raw) {
+  return p.value_dtype == FLCE_DTYPE_FP32   ? __uint_as_float(raw)
+         : p.value_dtype == FLCE_DTYPE_FP16 ? __half2float(__ushort_as_half(static_cast<unsigned short>(raw)))
+                                            : __uint_as_float(raw << 16);
+}
+template <typename T>
+__device__ __forceinline__ ListAhead<T> list_ahead(const RowLossParams& p, int64_t row) {
+  ListAhead<T> a;
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int j = 0; j < kListAhead; ++j) {
     const int k = j * 32 + lane;
-    const bool held = row < p.N && k < p.K;
-    a.column[j] = held ? column_of(p, load_id(p.ids, p.ids32, row * p.K + k)) : -1;
-    a.value[j] = held ? load_elem(p.values, p.value_dtype, row * p.K + k) : -INFINITY;
+    a.id[j] = make_uint2(0xFFFFFFFFu, 0xFFFFFFFFu);
+    a.value[j] = 0;
+    if (row < p.N && k < p.K) {
+      a.id[j] = raw_id(p, row * p.K + k);
+      a.value[j] = raw_value(p, row * p.K + k);
+    }
   }
-  a.weight = row < p.N && p.row_weight != nullptr ? __ldg(p.row_weight + row) : 1.f;
-  a.grad_out = row < p.N && p.grad_out != nullptr ? __ldg(p.grad_out + row) : 1.f;
+  a.weight = a.grad_out = 1.f;
+  if (row < p.N && p.row_weight != nullptr) a.weight = __ldg(p.row_weight + row);
+  if (row < p.N && p.grad_out != nullptr) a.grad_out = __ldg(p.grad_out + row);
   return a;
 }
 template <typename T>
-__device__ __forceinline__ void list_logits(const RowLossParams& p, int64_t row, ListAhead& a) {
+__device__ __forceinline__ void list_logits(const RowLossParams& p, int64_t row, ListAhead<T>& a) {
 #pragma unroll
-  for (int j = 0; j < kListAhead; ++j) a.z[j] = a.column[j] >= 0 ? load_logit<T>(p, row, a.column[j]) : -INFINITY;
+  for (int j = 0; j < kListAhead; ++j) {
+    const int column = column_of(p, a.id[j]);
+    if (column >= 0) a.z[j] = raw_logit<T>(p, row, column);
+  }
 }
 
 // Puts a column into the table of a list, which has room for all; whether it was there.
@@ -336,8 +400,8 @@ __device__ __forceinline__ bool seen_before(int* table, int slots, int column) {
 
 // A list of up to 32 * kListAhead entries without leaving the registers; false where a column
 // is named twice.
-template <typename Wanted>
-__device__ __forceinline__ bool short_teacher_row(const RowLossParams& p, const ListAhead& ahead,
+template <typename T, typename Wanted>
+__device__ __forceinline__ bool short_teacher_row(const RowLossParams& p, const ListAhead<T>& ahead,
                                                   const TeacherList& list, int* table, int* bits, Wanted wanted,
                                                   RowInfo* out) {
   const int lane = threadIdx.x & 31;
@@ -348,17 +412,20 @@ __device__ __forceinline__ bool short_teacher_row(const RowLossParams& p, const 
   const int slots = table_slots(p.K);
   for (int i = lane; i < slots; i += 32) table[i] = -1;
   const int batches = (p.K + 31) / 32;
-  float v[kListAhead], e[kListAhead];
+  float v[kListAhead], e[kListAhead], z[kListAhead];
+  int column[kListAhead];
   float vmax = -INFINITY;
   bool ended = false;
 #pragma unroll
   for (int j = 0; j < kListAhead; ++j) {
     v[j] = -INFINITY;
     if (j >= batches) break;
-    const unsigned ends = __ballot_sync(0xffffffffu, ahead.column[j] == -1);
+    column[j] = column_of(p, ahead.id[j]);
+    z[j] = raw_float<T>(ahead.z[j]);
+    const unsigned ends = __ballot_sync(0xffffffffu, column[j] == -1);
     const bool held = !ended && (ends == 0 || lane < __ffs(ends) - 1);
-    if (held && ahead.column[j] == -2) *bits |= FLCE_STATUS_BIT_TARGET_RANGE;
-    if (held && ahead.column[j] >= 0) v[j] = ahead.value[j];
+    if (held && column[j] == -2) *bits |= FLCE_STATUS_BIT_TARGET_RANGE;
+    if (held && column[j] >= 0) v[j] = value_of(p, ahead.value[j]);
     ended = ended || ends != 0;
     vmax = fmaxf(vmax, v[j]);
   }
@@ -371,7 +438,7 @@ __device__ __forceinline__ bool short_teacher_row(const RowLossParams& p, const 
     if (j >= batches) break;
     e[j] = ex2_approx((v[j] - shift) * p.c);  // 0: no share, the place is like any other
     sum += e[j];
-    if (e[j] != 0.f) zmax = fmaxf(zmax, ahead.z[j]);
+    if (e[j] != 0.f) zmax = fmaxf(zmax, z[j]);
   }
   sum = warp_sum(sum);
   zmax = warp_max_redux(zmax);
@@ -387,14 +454,14 @@ __device__ __forceinline__ bool short_teacher_row(const RowLossParams& p, const 
     const bool held = e[j] != 0.f;
     const float q = e[j] * inv;
     if (held) {
-      a += q * ((v[j] - shift) * p.inv_t - ln_sum - (ahead.z[j] - r.zt) * p.inv_t);
-      twice = seen_before(table, slots, ahead.column[j]) || twice;
+      a += q * ((v[j] - shift) * p.inv_t - ln_sum - (z[j] - r.zt) * p.inv_t);
+      twice = seen_before(table, slots, column[j]) || twice;
     }
-    const bool here = held && wanted(ahead.column[j]);
+    const bool here = held && wanted(column[j]);
     const unsigned all = __ballot_sync(0xffffffffu, here);
     if (here) {
       const int at = kept + __popc(all & ((1u << lane) - 1));
-      list.column[at] = ahead.column[j], list.q[at] = q, list.z[at] = ahead.z[j];
+      list.column[at] = column[j], list.q[at] = q, list.z[at] = z[j];
     }
     kept += __popc(all);
   }
@@ -408,11 +475,11 @@ __device__ __forceinline__ bool short_teacher_row(const RowLossParams& p, const 
 // whose columns are `wanted`, q of columns that occur twice added up.  `ahead`: the list's
 // first entries, with their logits.  `table` has table_slots(K) words.
 template <typename T, typename Wanted>
-__device__ RowInfo teacher_row(const RowLossParams& p, int64_t row, const ListAhead& ahead, const TeacherList& list,
-                               int* table, int* bits, Wanted wanted) {
+__device__ RowInfo teacher_row(const RowLossParams& p, int64_t row, const ListAhead<T>& ahead,
+                               const TeacherList& list, int* table, int* bits, Wanted wanted) {
   if (p.K <= 32 * kListAhead) {
     RowInfo r;
-    const bool done = short_teacher_row(p, ahead, list, table, bits, wanted, &r);
+    const bool done = short_teacher_row<T>(p, ahead, list, table, bits, wanted, &r);
     __syncwarp();
     if (done) return r;
   }
@@ -445,13 +512,15 @@ __device__ RowInfo teacher_row(const RowLossParams& p, int64_t row, const ListAh
   };
 #pragma unroll
   for (int j = 0; j < kListAhead; ++j)
-    if (!ended) take(j * 32 + lane, ahead.column[j], ahead.value[j], ahead.z[j]);
+    if (!ended)
+      take(j * 32 + lane, column_of(p, ahead.id[j]), value_of(p, ahead.value[j]), raw_float<T>(ahead.z[j]));
+#pragma unroll 2
   for (int k0 = 32 * kListAhead; k0 < p.K && !ended; k0 += 32) {
     const int k = k0 + lane;
     const bool held = k < p.K;
-    const int column = held ? column_of(p, load_id(p.ids, p.ids32, base + k)) : -1;
-    take(k, column, held ? load_elem(p.values, p.value_dtype, base + k) : -INFINITY,
-         column >= 0 ? load_logit<T>(p, row, column) : -INFINITY);
+    const int column = held ? column_of(p, raw_id(p, base + k)) : -1;
+    take(k, column, held ? value_of(p, raw_value(p, base + k)) : -INFINITY,
+         column >= 0 ? raw_float<T>(raw_logit<T>(p, row, column)) : -INFINITY);
   }
   __syncwarp();
   vmax = warp_max_redux(vmax);
@@ -518,7 +587,7 @@ __device__ RowInfo teacher_row(const RowLossParams& p, int64_t row, const ListAh
 template <typename T>
 __device__ __forceinline__ RowInfo whole_teacher_row(const RowLossParams& p, int64_t row, const TeacherList& list,
                                                      int* table, int* bits) {
-  ListAhead a = list_ahead(p, row);
+  ListAhead<T> a = list_ahead<T>(p, row);
   list_logits<T>(p, row, a);
   return teacher_row<T>(p, row, a, list, table, bits, [](int) { return true; });
 }
@@ -1053,15 +1122,15 @@ __global__ void __launch_bounds__(THREADS + 64, CTAS_PER_SM)
     int slot = 0, use = 0;  // i % slots, i / slots
     const auto read_ahead = [&](int64_t row) {
       if constexpr (KIND == kDistill)
-        return list_ahead(p, row);
+        return list_ahead<T>(p, row);
       else
-        return policy_ahead(p, row);
+        return policy_ahead<T>(p, row);
     };
     const auto read_logits = [&](int64_t row, auto& a) {
       if constexpr (KIND == kDistill)
         list_logits<T>(p, row, a);
       else
-        policy_logit<T>(p, row, a, &bits);
+        policy_logit<T>(p, row, a);
     };
     auto ahead = read_ahead(row_of(0)), next = read_ahead(row_of(1));
     read_logits(row_of(0), ahead);
@@ -1082,7 +1151,7 @@ __global__ void __launch_bounds__(THREADS + 64, CTAS_PER_SM)
                                                         : vec >= first_vec && vec < first_vec + n;
                            });
       } else {
-        r = ahead.r;
+        r = policy_info<T>(p, ahead, &bits);
       }
       if (lane == 0) {
         infos[i % kKept] = r;
