@@ -98,7 +98,8 @@ def _link_binding():
     import torch
     root = os.path.dirname(os.path.abspath(torch.__file__))
     return [os.environ.get("CXX", "g++"), "-shared", *map(_binding_object, _binding_sources()), LIB,
-            f"-L{os.path.join(root, 'lib')}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+            f"-L{os.path.join(root, 'lib')}", "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10",
+            "-lc10_cuda",
             "-Wl,-rpath,$ORIGIN"]
 
 

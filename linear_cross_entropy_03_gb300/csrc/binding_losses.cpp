@@ -2,10 +2,26 @@
 // embedding_backward (binding.cpp says why this is C++).
 #include "binding.h"
 
-#include <ATen/ops/empty_like.h>
+#include <ATen/cuda/EmptyTensor.h>
 
 namespace flce_binding {
 namespace {
+
+// An uninitialised tensor on the GPU of another one.  (at::empty takes twice as long to get
+// to the same place, and a call makes up to four.)
+at::Tensor empty(at::IntArrayRef shape, at::ScalarType type, const at::Tensor& by) {
+  return at::detail::empty_cuda(shape, type, by.device(), std::nullopt);
+}
+
+// The first four bytes of a workspace (its status word), as a tensor that shares its memory.
+at::Tensor first_word(const at::Tensor& workspace) {
+  auto impl = c10::make_intrusive<c10::TensorImpl>(c10::Storage(workspace.storage()),
+                                                   c10::DispatchKeySet(c10::DispatchKey::CUDA),
+                                                   caffe2::TypeMeta::Make<int32_t>());
+  impl->set_sizes_contiguous({1});
+  impl->set_storage_offset(workspace.storage_offset() * static_cast<int64_t>(workspace.itemsize()) / 4);
+  return at::Tensor(std::move(impl));
+}
 
 // What the losses on logits take and return alike.
 struct Call {
@@ -72,20 +88,15 @@ struct Call {
   at::IntArrayRef row_shape() const { return logits->sizes().slice(0, logits->dim() - 1); }
 
   void allocate(int64_t workspace_bytes, at::IntArrayRef loss_shape) {
-    const auto options = logits->options();
-    loss = reduction == FLCE_REDUCTION_NONE ? floats(loss_shape, *logits) : floats({}, *logits);
+    loss = empty(reduction == FLCE_REDUCTION_NONE ? loss_shape : at::IntArrayRef{}, at::kFloat, *logits);
     if (buffer != nullptr)
       grad = *buffer;
     else if (want_grad)
-      grad = at::empty(logits->sizes(), options);
+      grad = empty(logits->sizes(), logits->scalar_type(), *logits);
     const bool given = workspace != nullptr && workspace->is_contiguous() &&
                        static_cast<int64_t>(workspace->nbytes()) >= workspace_bytes;
-    scratch = given ? *workspace : at::empty({workspace_bytes / 4}, options.dtype(at::kInt));
-    // without a status word of the caller's, the workspace's first
-    if (status != nullptr)
-      word = *status;
-    else
-      word = (given ? scratch.reshape({-1}).view(at::kInt) : scratch).narrow(0, 0, 1);
+    scratch = given ? *workspace : empty({workspace_bytes}, at::kByte, *logits);
+    word = status != nullptr ? *status : first_word(scratch);
   }
 
   int32_t* status_ptr() const { return status != nullptr ? status->data_ptr<int32_t>() : nullptr; }
@@ -126,7 +137,7 @@ PyObject* policy_loss(PyObject*, PyObject* const* a, Py_ssize_t count) {
   const size_t size = row_loss_workspace_size(c.rows.n);
   if (size == 0) return c.bad(FLCE_ERR_INVALID_ARG, "too many rows");
   c.allocate(static_cast<int64_t>(size), c.row_shape());
-  const at::Tensor logp = floats(c.row_shape(), *c.logits);
+  const at::Tensor logp = empty(c.row_shape(), at::kFloat, *c.logits);
   const flce_status_t st = policy_fwd_bwd(
       data(c.logits), c.dtype, c.rows.ld, c.grad_ptr(), c.ld_grad, target->data_ptr<int64_t>(), f32(advantage),
       f32(old_logp), f32(ref_logp), f32(weight), c.rows.n, c.rows.h, &numbers, ignore_index, c.reduction, c.grad_scale,
@@ -207,7 +218,7 @@ PyObject* preference_loss(PyObject*, PyObject* const* a, Py_ssize_t count) {
   const size_t size = preference_workspace_size(c.rows.n, sequences / 2);
   if (size == 0) return c.bad(FLCE_ERR_INVALID_ARG, "too many rows");
   c.allocate(static_cast<int64_t>(size), {sequences / 2});
-  const at::Tensor logp = floats({sequences}, *c.logits);
+  const at::Tensor logp = empty({sequences}, at::kFloat, *c.logits);
   const flce_status_t st = preference_fwd_bwd(
       data(c.logits), c.dtype, c.rows.ld, c.grad_ptr(), c.ld_grad, target->data_ptr<int64_t>(),
       offsets != nullptr ? offsets->data_ptr<int64_t>() : nullptr, f32(ref_logp), sequences / 2, c.rows.n, c.rows.h,
@@ -262,7 +273,7 @@ PyObject* embedding(PyObject*, PyObject* const* a, Py_ssize_t count) {
       return fail(FLCE_ERR_INVALID_ARG, "embedding: out: of another shape or type than the rows looked up");
     if (!rows_of(*out, "embedding: out", &y_rows)) return nullptr;
   }
-  const at::Tensor y = out != nullptr ? *out : at::empty(shape, weight->options());
+  const at::Tensor y = out != nullptr ? *out : empty(shape, weight->scalar_type(), *weight);
   const flce_status_t st =
       embedding_fwd(dtype, data(weight), table.ld, data(ids), index_type, ids->numel(), table.n, table.h,
                     static_cast<float>(scale), y.data_ptr(), y_rows.ld, status, stream());
@@ -312,10 +323,10 @@ PyObject* embedding_backward(PyObject*, PyObject* const* a, Py_ssize_t count) {
   }
   const size_t size = embedding_workspace_size(rows.n, v, rows.h);
   if (size == 0) return fail(FLCE_ERR_INVALID_ARG, "embedding_workspace_size");
-  const at::Tensor grad = out != nullptr ? *out : at::empty({v, rows.h}, gy->options().dtype(at::kFloat));
+  const at::Tensor grad = out != nullptr ? *out : empty({v, rows.h}, at::kFloat, *gy);
   const bool given = ws != nullptr && ws->is_contiguous() && ws->nbytes() >= size;
   const at::Tensor scratch =
-      given ? *ws : at::empty({static_cast<int64_t>(size)}, gy->options().dtype(at::kByte));
+      given ? *ws : empty({static_cast<int64_t>(size)}, at::kByte, *gy);
   const flce_status_t st = embedding_bwd(
       dtype, data(gy), rows.ld, data(ids), index_type, rows.n, v, rows.h, static_cast<float>(scale), padding,
       grad.data_ptr<float>(), accumulate, scratch.data_ptr(), scratch.nbytes(), status, stream());

@@ -67,7 +67,10 @@ __global__ void __launch_bounds__(32 * kLookupWarps) embedding_kernel(const Look
       if (at >= p.H) break;
 #pragma unroll
       for (int k = 0; k < E; ++k) v[i].v[k] = from_float<T>(inside ? to_float(v[i].v[k]) * p.scale : 0.f);
-      *reinterpret_cast<Elems<T, E>*>(to + at) = v[i];
+      if constexpr (E > 1)
+        __stcs(reinterpret_cast<uint4*>(to + at), *reinterpret_cast<const uint4*>(&v[i]));
+      else
+        to[at] = v[i].v[0];
     }
   }
 }

@@ -21,7 +21,7 @@ struct PairParams {
   int64_t N, V, pairs, ignore_index;
   flce_preference_t numbers;
   int reduction;
-  float grad_scale;
+  double scale;        // grad_scale, or that over the pairs of a mean
   float* factor;       // [N]
   double* pair_loss;   // [pairs]
   float* loss;
@@ -80,6 +80,8 @@ __global__ void __launch_bounds__(kPairThreads) pair_loss_kernel(const PairParam
   for (int64_t pair = blockIdx.x; pair < p.pairs; pair += gridDim.x) {
     int64_t from, to;
     sequence_rows(p, pair + half * p.pairs, &from, &to, &bits);
+    const float ref[2] = {p.ref_logp != nullptr ? __ldg(p.ref_logp + pair) : 0.f,
+                          p.ref_logp != nullptr ? __ldg(p.ref_logp + pair + p.pairs) : 0.f};
     double sum = 0;
     int64_t tokens = 0;
 #pragma unroll 4
@@ -103,7 +105,7 @@ __global__ void __launch_bounds__(kPairThreads) pair_loss_kernel(const PairParam
     if (threadIdx.x == 0) {
       // differences of long sums in fp64, functions of the difference in fp32
       double x = s[0] - s[1];
-      if (p.ref_logp != nullptr) x -= static_cast<double>(p.ref_logp[pair]) - p.ref_logp[pair + p.pairs];
+      x -= static_cast<double>(ref[0]) - ref[1];
       const double beta = p.numbers.beta;
       double loss, slope;  // slope: dloss / dx
       if (p.numbers.kind == FLCE_PREFERENCE_IPO) {
@@ -125,10 +127,7 @@ __global__ void __launch_bounds__(kPairThreads) pair_loss_kernel(const PairParam
           slope = beta * (static_cast<double>(smooth) - less);
         }
       }
-      double scale = p.grad_scale;
-      if (p.reduction == FLCE_REDUCTION_MEAN) scale /= static_cast<double>(p.pairs);
-      if (p.grad_out != nullptr) scale *= p.grad_out[pair];
-      slope_of_pair = slope * scale;
+      slope_of_pair = slope * p.scale * (p.grad_out != nullptr ? p.grad_out[pair] : 1.f);
       p.pair_loss[pair] = loss;
       if (p.reduction == FLCE_REDUCTION_NONE) p.loss[pair] = static_cast<float>(loss);
       if (p.logp != nullptr) {
@@ -308,7 +307,8 @@ flce_status_t preference_fwd_bwd(const void* logits, int dtype, int64_t ld, void
   q.target = target, q.offsets = offsets, q.length = pairs > 0 ? N / (2 * pairs) : 0;
   q.ref_logp = ref_logp, q.grad_out = grad_out_none, q.logp_rows = p.logp;
   q.N = N, q.V = V, q.pairs = pairs, q.ignore_index = ignore_index, q.numbers = *numbers;
-  q.reduction = reduction, q.grad_scale = grad_scale, q.factor = p.factor;
+  q.reduction = reduction, q.factor = p.factor;
+  q.scale = reduction == FLCE_REDUCTION_MEAN && pairs > 0 ? grad_scale / static_cast<double>(pairs) : grad_scale;
   q.pair_loss = reinterpret_cast<double*>(ws + at.pairs);
   q.loss = loss, q.logp = logp, q.status = p.status;
   q.arrivals = p.arrivals + 1, q.tag = next_arrival_tag();
