@@ -27,6 +27,7 @@ struct PairParams {
   float* loss;
   float* logp;
   int* status;
+  int add_up;          // whether the losses are added up here (else by the gradients' launch)
   unsigned long long* arrivals;
   unsigned long long tag;
 };
@@ -62,6 +63,18 @@ __device__ __forceinline__ double half_sum(double v, double* scratch) {
   return total;
 }
 
+// The loss of SUM and MEAN, by a CTA's first warp, in an order that the number of pairs fixes.
+__device__ __forceinline__ void add_up_losses(const double* pair_loss, int64_t pairs, int reduction, float* loss) {
+  if (threadIdx.x >= 32) return;
+  double total = 0;
+#pragma unroll 4
+  for (int64_t i = threadIdx.x; i < pairs; i += 32) total += __ldcg(pair_loss + i);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  if (threadIdx.x == 0)
+    *loss = static_cast<float>(reduction == FLCE_REDUCTION_MEAN ? total / static_cast<double>(pairs) : total);
+}
+
 // One CTA a pair, half of it for each sequence.  Sums are fp64 in an order that the lengths
 // fix.
 __global__ void __launch_bounds__(kPairThreads) pair_loss_kernel(const PairParams p) {
@@ -72,7 +85,7 @@ __global__ void __launch_bounds__(kPairThreads) pair_loss_kernel(const PairParam
   const int half = threadIdx.x / kHalf, t = threadIdx.x % kHalf;
   if (threadIdx.x == 0) {
     all_bits = 0;
-    if (blockIdx.x == 0) expect_arrivals(p.arrivals, p.tag);
+    if (blockIdx.x == 0 && p.add_up) expect_arrivals(p.arrivals, p.tag);
   }
   __syncthreads();
   grid_dependency_wait();
@@ -137,7 +150,10 @@ __global__ void __launch_bounds__(kPairThreads) pair_loss_kernel(const PairParam
     }
     __syncthreads();
     float f = 0.f;
-    if (t % 32 == 0) f = static_cast<float>((half == 0 ? -slope_of_pair : slope_of_pair) / tokens_of[half]);
+    if (t % 32 == 0) {
+      const double slope = half == 0 ? -slope_of_pair : slope_of_pair;
+      f = static_cast<float>(p.numbers.average ? slope / tokens_of[half] : slope);
+    }
     f = __shfl_sync(0xffffffffu, f, 0);
     for (int64_t n = from + t; n < to; n += kHalf) p.factor[n] = f;
     __syncthreads();  // the sums are the next pair's
@@ -146,18 +162,10 @@ __global__ void __launch_bounds__(kPairThreads) pair_loss_kernel(const PairParam
   __syncthreads();
   if (threadIdx.x == 0) {
     if (all_bits != 0) atomicOr(p.status, all_bits);
-    last = p.reduction != FLCE_REDUCTION_NONE && arrives_last(p.arrivals, p.tag, gridDim.x);
+    last = p.add_up && arrives_last(p.arrivals, p.tag, gridDim.x);
   }
   __syncthreads();
-  if (!last) return;
-  double total = 0;
-  for (int64_t i = threadIdx.x; i < p.pairs; i += kPairThreads) total += __ldcg(p.pair_loss + i);
-  total = half_sum(total, scratch);
-  if (t == 0) sums[half] = total;
-  __syncthreads();
-  if (threadIdx.x != 0) return;
-  total = sums[0] + sums[1];
-  *p.loss = static_cast<float>(p.reduction == FLCE_REDUCTION_MEAN ? total / static_cast<double>(p.pairs) : total);
+  if (last) add_up_losses(p.pair_loss, p.pairs, p.reduction, p.loss);
 }
 
 struct GradParams {
@@ -170,6 +178,10 @@ struct GradParams {
   const float* logp;
   int64_t parts;         // pieces of a row
   int64_t items;         // rows times parts
+  const double* pair_loss;
+  int64_t pairs;
+  int reduction;
+  float* loss;           // of SUM and MEAN: by the first CTA
 };
 
 constexpr int kGradThreads = 256;
@@ -181,7 +193,12 @@ template <typename T, int GROUP>
 __global__ void __launch_bounds__(kGradThreads) row_grad_kernel(const GradParams p) {
   constexpr int kE = kVecElems<T>;
   const int lane = threadIdx.x % GROUP;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * (kGradThreads / GROUP) + threadIdx.x / GROUP;
+  if (blockIdx.x == 0) {
+    grid_dependency_wait();
+    if (p.reduction != FLCE_REDUCTION_NONE) add_up_losses(p.pair_loss, p.pairs, p.reduction, p.loss);
+    return;
+  }
+  const int64_t item = static_cast<int64_t>(blockIdx.x - 1) * (kGradThreads / GROUP) + threadIdx.x / GROUP;
   if (item >= p.items) return;
   const int64_t row = p.N - 1 - item / p.parts, part = item % p.parts;
   const T* x = static_cast<const T*>(p.logits) + row * p.ld;
@@ -231,7 +248,7 @@ cudaError_t launch_grad(GradParams p, cudaStream_t s) {
   const bool by_warps = vecs <= 32 * kGradVecs;
   p.parts = vecs < 1 ? 1 : div_up(vecs, (by_warps ? 32 : kGradThreads) * kGradVecs);
   p.items = p.N * p.parts;
-  const int64_t ctas = by_warps ? div_up(p.items, kGradThreads / 32) : p.items;
+  const int64_t ctas = 1 + (by_warps ? div_up(p.items, kGradThreads / 32) : p.items);
   if (ctas >= (int64_t(1) << 31)) return cudaErrorInvalidValue;
   const dim3 grid(static_cast<unsigned>(ctas));
   return by_warps ? launch_after(row_grad_kernel<T, 32>, grid, dim3(kGradThreads), s, p)
@@ -311,6 +328,8 @@ flce_status_t preference_fwd_bwd(const void* logits, int dtype, int64_t ld, void
   q.scale = reduction == FLCE_REDUCTION_MEAN && pairs > 0 ? grad_scale / static_cast<double>(pairs) : grad_scale;
   q.pair_loss = reinterpret_cast<double*>(ws + at.pairs);
   q.loss = loss, q.logp = logp, q.status = p.status;
+  const bool grads = grad_logits != nullptr && N > 0;
+  q.add_up = reduction != FLCE_REDUCTION_NONE && !grads;
   q.arrivals = p.arrivals + 1, q.tag = next_arrival_tag();
   const int64_t most = 8 * device_sm_count();
   prof_begin(stream, FLCE_KERNEL_PAIR_LOSS);
@@ -318,10 +337,10 @@ flce_status_t preference_fwd_bwd(const void* logits, int dtype, int64_t ld, void
                                dim3(kPairThreads), stream, q);
   prof_end(stream);
   if (e != cudaSuccess) return FLCE_ERR_CUDA;
-  if (grad_logits == nullptr || N == 0) return FLCE_OK;
+  if (!grads) return FLCE_OK;
 
-  const GradParams g = {logits, grad_logits, ld,       ld_grad, N, V, ignore_index, target, p.stats,
-                        p.factor, p.logp,    0,        0};
+  const GradParams g = {logits, grad_logits, ld, ld_grad, N,     V,         ignore_index, target, p.stats, p.factor,
+                        p.logp, 0,           0,  q.pair_loss, pairs, reduction, loss};
   prof_begin(stream, FLCE_KERNEL_ROW_GRAD);
   e = dtype == FLCE_DTYPE_BF16   ? launch_grad<__nv_bfloat16>(g, stream)
       : dtype == FLCE_DTYPE_FP16 ? launch_grad<__half>(g, stream)
