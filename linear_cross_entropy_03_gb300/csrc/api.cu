@@ -191,6 +191,8 @@ unsigned long long next_ce_nonce() {
 
 }  // namespace
 
+uint64_t wait_timeout_ns() { return g_timeout_ns.load(); }
+
 void prof_begin(cudaStream_t s, int kernel_id) {
   if (!g_prof.enabled || g_prof.count >= g_prof.capacity) return;
   cudaEventRecord(g_prof.start[g_prof.count], s);

@@ -316,7 +316,9 @@ __global__ void __launch_bounds__(kSortThreads) token_sort_kernel(const SortPara
 
 constexpr int kTile = 32;          // sorted tokens of a tile: one a lane
 constexpr int kSumWarps = 4;
-constexpr int kAhead = 8;          // tokens whose rows are loaded at a time
+constexpr int kAhead = 8;          // tokens whose rows are loaded at a time, by elements
+constexpr int kRing = 16;          // tokens whose rows are on their way, by vectors
+constexpr int kRingStep = 4;       // of them at a time
 
 struct SumParams {
   const void* grad_y;
@@ -429,6 +431,10 @@ struct Sums {
   }
 };
 
+__device__ __forceinline__ void copy_async(void* to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(to)), "l"(from) : "memory");
+}
+
 // One tile's columns by each warp: a lane holds the tile's keys and those of the next one,
 // and all go through the tokens in order, kAhead rows on their way.  An id that ends in the
 // next tile is finished by the tile in which it begins, so that partial rows are left for
@@ -495,28 +501,54 @@ __global__ void __launch_bounds__(32 * kSumWarps, 6) embedding_sum_kernel(const 
   Sums<E, GROUPS> sum;
   sum.clear();
   float* const partial = p.partial + static_cast<int64_t>(tile) * 2 * p.H;
-  Columns<T, E, GROUPS> held[kAhead];
-  for (int t0 = from & ~(kAhead - 1); t0 < to; t0 += kAhead) {
-    const int token = t0 < kTile ? token0 : token1;
-#pragma unroll
-    for (int a = 0; a < kAhead; ++a) {  // places beyond the list: token 0's row
-      const int64_t n = __shfl_sync(0xffffffffu, token, (t0 + a) & 31);
-      held[a].load(rows + n * p.ld, at);
+  const auto add = [&](int t, const Columns<T, E, GROUPS>& row) {
+    sum.add(row);
+    if (!(ends >> t & 1)) return;
+    if (head_partial) {
+      sum.store(partial, first, p.H, 1.f, false);
+      head_partial = false;
+    } else {
+      const int key = __shfl_sync(0xffffffffu, t < kTile ? k0 : k1, t & 31);
+      sum.store(p.table + key * p.H, first, p.H, p.scale, p.accumulate != 0);
     }
+    sum.clear();
+  };
+  const auto token_at = [&](int t) -> int64_t { return __shfl_sync(0xffffffffu, t < kTile ? token0 : token1, t & 31); };
+  if constexpr (E > 1) {
+    // each lane's vectors of the next kRing tokens are on their way into its own places of shared memory
+    extern __shared__ __align__(16) uint4 ring_memory[];
+    uint4* const ring = ring_memory + warp * kRing * 32 + lane;
+    const auto fetch = [&](int t) {
 #pragma unroll
-    for (int a = 0; a < kAhead; ++a) {
-      const int t = t0 + a;
-      if (t < from || t >= to) continue;
-      sum.add(held[a]);
-      if (!(ends >> t & 1)) continue;
-      if (head_partial) {
-        sum.store(partial, first, p.H, 1.f, false);
-        head_partial = false;
-      } else {
-        const int key = __shfl_sync(0xffffffffu, t < kTile ? k0 : k1, t & 31);
-        sum.store(p.table + key * p.H, first, p.H, p.scale, p.accumulate != 0);
+      for (int a = 0; a < kRingStep; ++a) {
+        const int64_t n = token_at(t + a < to ? t + a : to - 1);
+        if (t + a < to) copy_async(ring + (t + a - from) % kRing * 32, rows + n * p.ld + at[0]);
       }
-      sum.clear();
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int g = 0; g < kRing / kRingStep; ++g) fetch(from + g * kRingStep);
+    for (int t0 = from; t0 < to; t0 += kRingStep) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kRing / kRingStep - 1) : "memory");
+      Columns<T, E, GROUPS> held[kRingStep];
+#pragma unroll
+      for (int a = 0; a < kRingStep; ++a)
+        held[a].v[0] = *reinterpret_cast<const Elems<T, E>*>(ring + (t0 + a - from) % kRing * 32);
+#pragma unroll
+      for (int a = 0; a < kRingStep; ++a)
+        if (t0 + a < to) add(t0 + a, held[a]);
+      fetch(t0 + kRing);
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else {
+    Columns<T, E, GROUPS> held[kAhead];
+    for (int t0 = from; t0 < to; t0 += kAhead) {
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a)  // past the end: the last one again
+        held[a].load(rows + token_at(t0 + a < to ? t0 + a : to - 1) * p.ld, at);
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a)
+        if (t0 + a < to) add(t0 + a, held[a]);
     }
   }
   if (head_partial)  // one id, that goes on
@@ -768,7 +800,8 @@ cudaError_t sum_rows(SumParams p, bool vectors, bool few, cudaStream_t s) {
   } else {
     p.zero_ctas = p.accumulate ? 0 : static_cast<unsigned>(std::min<int64_t>(8 * device_sm_count(), div_up(p.V, kSumWarps)));
     const dim3 grid(static_cast<unsigned>(p.zero_ctas + div_up(static_cast<int64_t>(p.tiles) * p.columns, kSumWarps)));
-    e = vectors ? launch_after(embedding_sum_kernel<T, kE, 1>, grid, dim3(32 * kSumWarps), s, p)
+    constexpr size_t kRingBytes = sizeof(uint4) * kSumWarps * kRing * 32;
+    e = vectors ? launch_after_with(kRingBytes, embedding_sum_kernel<T, kE, 1>, grid, dim3(32 * kSumWarps), s, p)
                 : launch_after(embedding_sum_kernel<T, 1, 4>, grid, dim3(32 * kSumWarps), s, p);
   }
   prof_end(s);

@@ -236,6 +236,8 @@ bool ce_rows_single_launch_ok(int64_t V, int dtype, bool vector_path, bool align
 cudaError_t launch_wait_selftest(int* status, uint64_t timeout_ns, cudaStream_t s);
 
 int device_sm_count();
+// The time limit of waits inside kernels (flce_set_wait_timeout_ns).
+uint64_t wait_timeout_ns();
 
 // ---------------------------------------------------------------- profiler
 void prof_begin(cudaStream_t s, int kernel_id);

@@ -1090,8 +1090,9 @@ __global__ void __launch_bounds__(THREADS + 64, CTAS_PER_SM)
     if (blockIdx.x == 0) expect_arrivals(p.arrivals, p.tag);
   }
   cluster_sync_all();  // (also the CTA's own barrier)
-  // a wait that runs out: the CTA goes on through its rows without copying or writing, so that no warp waits for
-  // another for ever, and leaves a status bit
+  // A wait that runs out leaves a status bit.  The warp that waited goes on through its rows, but no longer copies,
+  // writes, or arrives at a barrier that others arrive at too (its last phase may not be over); the others' waits end
+  // by the flag or run out, in the row's other CTAs as well.
   const WaitCtl ctl{&aborted, nullptr, p.timeout_ns};
   const auto row_of = [&](int i) { return static_cast<int64_t>(first_row) + static_cast<int64_t>(i) * row_step; };
   const auto logits_of = [&](int64_t row) { return static_cast<const T*>(p.logits) + row * p.ld; };
@@ -1199,17 +1200,18 @@ __global__ void __launch_bounds__(THREADS + 64, CTAS_PER_SM)
     };
     int edge, next_edge, slot = 0;
     float z, next_z = edge_of(0, &next_edge);
+    bool alive = true;
     for (int i = 0; i < mine; ++i) {
-      if (KIND == kDistill && lane == 0) mbar_arrive(smem_addr(&empty[slot]));  // done with row i - 1's list
+      if (KIND == kDistill && lane == 0 && alive) mbar_arrive(smem_addr(&empty[slot]));  // done with row i - 1's list
       if (++slot == shape.slots) slot = 0;
       z = next_z, edge = next_edge;
       next_z = edge_of(i + 1, &next_edge);
       const int b = i % kKept, phase = (i / kKept) & 1;
       const uint32_t sum_bar = smem_addr(&summed[b]);
-      if (lane == 0) mbar_arrive_expect_tx(sum_bar, static_cast<uint32_t>(cluster) * kSums * 8u);
+      if (lane == 0 && alive) mbar_arrive_expect_tx(sum_bar, static_cast<uint32_t>(cluster) * kSums * 8u);
       // no CTA may write a row (its logits may be in the same place) before all have read what they need of it:
       // this one's word for it is its closer's share in the sums
-      bool ok = mbar_wait(smem_addr(&told[b]), phase, ctl);
+      alive = __all_sync(0xffffffffu, mbar_wait(smem_addr(&told[b]), phase, ctl)) && alive;
       float edge_m = -INFINITY, edge_s = 0.f;
       if constexpr (!WHOLE) {
         edge_m = warp_max_redux(z);
@@ -1219,11 +1221,12 @@ __global__ void __launch_bounds__(THREADS + 64, CTAS_PER_SM)
                                                                                : ex2_approx(fmaf(z, p.c, -taken));
         edge_s = warp_sum(edge_s);
       }
-      if (ok && lane < cluster)
+      if (alive && lane < cluster)
         push_pair(map_to_cta(smem_addr(&parts[b][rank * kSums + kWarps]), lane), edge_m, edge_s,
                   map_to_cta(sum_bar, lane));
       const RowInfo info = infos[b];
-      ok = mbar_wait_cluster(sum_bar, phase, ctl) && ok;
+      alive = __all_sync(0xffffffffu, mbar_wait_cluster(sum_bar, phase, ctl)) && alive;
+      if (!alive) continue;
       float top = -INFINITY;
       for (int k = lane; k < cluster * kSums; k += 32) top = fmaxf(top, parts[b][k].x);
       const float m = warp_max_redux(top);
@@ -1240,7 +1243,7 @@ __global__ void __launch_bounds__(THREADS + 64, CTAS_PER_SM)
       const float s = far ? sum : sum * ex2_approx(fmaf(-m, p.c, r));  // of 2^((z - m) c)
       const RowResult result = row_result<KIND>(p, info, m, s, scale);
       if (lane == 0) {
-        if (rank == 0 && ok) store_result<KIND>(p, row_of(i), result, m, s, &loss);
+        if (rank == 0) store_result<KIND>(p, row_of(i), result, m, s, &loss);
         PartResult out;
         out.m = m, out.r = r, out.f = result.f, out.inv_s = 1.f / s, out.factor = result.f / sum;
         out.named = KIND == kPolicy ? target_grad(result) : 0.f;
@@ -1249,7 +1252,7 @@ __global__ void __launch_bounds__(THREADS + 64, CTAS_PER_SM)
         mbar_arrive(smem_addr(&closed[b]));
       }
       __syncwarp();
-      if (!WHOLE && KIND != kStats && p.grad != nullptr && ok) {
+      if (!WHOLE && KIND != kStats && p.grad != nullptr) {
         T* g = static_cast<T*>(p.grad) + row_of(i) * p.ld_grad;
         const bool zero = result.f == 0.f;
         if (edge >= 0) {
@@ -1290,19 +1293,20 @@ __global__ void __launch_bounds__(THREADS + 64, CTAS_PER_SM)
     const int64_t x_step = row_step * p.ld, g_step = row_step * p.ld_grad;
     RowSplit split = split_of(x);
     int n = part_vecs(split);
+    bool alive = true;
     for (int i = 0; i < mine; ++i, x += x_step, g += g_step) {
       if constexpr (!WHOLE) {
         split = split_of(x);
         n = part_vecs(split);
       }
       const int b = i % kKept, phase = (i / kKept) & 1;
-      bool ok = mbar_wait_sleep(smem_addr(&full[slot]), use & 1, ctl);
+      alive = mbar_wait_sleep(smem_addr(&full[slot]), use & 1, ctl) && alive;
       const uint4* from = reinterpret_cast<const uint4*>(part_memory + slot * shape.slot_bytes);
       uint4 v[VPT];
 #pragma unroll
       for (int k = 0; k < VPT; ++k) v[k] = k * THREADS + tid < n ? from[k * THREADS + tid] : empty_vec<T>();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_addr(&empty[slot]));
+      if (lane == 0 && alive) mbar_arrive(smem_addr(&empty[slot]));
       if (++slot == shape.slots) slot = 0, ++use;
       const float m = warp_max_redux(vecs_max<T, VPT>(v));
       const bool far = m > -INFINITY && far_exponent(m, p.c);
@@ -1321,17 +1325,17 @@ __global__ void __launch_bounds__(THREADS + 64, CTAS_PER_SM)
       }
       const float2 both = unpair(sum);
       const float s = warp_sum(both.x + both.y);
-      if (ok && lane < cluster)
+      if (alive && lane < cluster)
         push_pair(map_to_cta(smem_addr(&parts[b][rank * kSums + warp]), lane), m, s,
                   map_to_cta(smem_addr(&summed[b]), lane));
       if constexpr (KIND == kStats) {
         // a row is closed while the next one is read.  What a row's sums overwrite, the row's four before, is no
         // longer wanted: row i - 1 closed here means that every CTA has closed row i - 2
-        if (i > 0) mbar_wait_sleep(smem_addr(&closed[(i - 1) % kKept]), ((i - 1) / kKept) & 1, ctl);
+        if (i > 0) alive = mbar_wait_sleep(smem_addr(&closed[(i - 1) % kKept]), ((i - 1) / kKept) & 1, ctl) && alive;
         continue;
       }
-      ok = mbar_wait_sleep(smem_addr(&closed[b]), phase, ctl) && ok;
-      if (p.grad == nullptr) continue;
+      alive = mbar_wait_sleep(smem_addr(&closed[b]), phase, ctl) && alive;
+      if (p.grad == nullptr || !alive) continue;
       const PartResult result = results[b];
       const bool zero = result.f == 0.f;
       // a warp that has taken its own maximum off: the row's, or far below it
@@ -1350,23 +1354,21 @@ __global__ void __launch_bounds__(THREADS + 64, CTAS_PER_SM)
         for (int q = 0; q < kE / 2; ++q) e[q] = e[q] * factor;
         return pack_pairs<T>(e);
       };
-      if (ok) {
-        if (WHOLE || same_phase(x, g)) {
+      if (WHOLE || same_phase(x, g)) {
 #pragma unroll
-          for (int k = 0; k < VPT; ++k) {
-            const uint4 out = gradient(v[k]);
-            if (k * THREADS + tid < n) __stcs(reinterpret_cast<uint4*>(to + k * THREADS * kE), out);
-          }
-        } else {
+        for (int k = 0; k < VPT; ++k) {
+          const uint4 out = gradient(v[k]);
+          if (k * THREADS + tid < n) __stcs(reinterpret_cast<uint4*>(to + k * THREADS * kE), out);
+        }
+      } else {
 #pragma unroll
-          for (int k = 0; k < VPT; ++k) {
-            const uint4 out = gradient(v[k]);
-            if (k * THREADS + tid < n) store_vec<T>(to + k * THREADS * kE, out, false);
-          }
+        for (int k = 0; k < VPT; ++k) {
+          const uint4 out = gradient(v[k]);
+          if (k * THREADS + tid < n) store_vec<T>(to + k * THREADS * kE, out, false);
         }
       }
       // the places that the row names are written after the rest, by the warp that has written there
-      if (zero || !ok) continue;
+      if (zero) continue;
       if constexpr (KIND == kDistill) {
         const TeacherList list = list_at(lists + static_cast<size_t>(i & 1) * list_bytes(p.K), p.K);
         __syncwarp();
@@ -1390,6 +1392,8 @@ __global__ void __launch_bounds__(THREADS + 64, CTAS_PER_SM)
   if (warp == kWarps + 1 && lane == 0) all_loss = loss, all_rows = rows;
   __syncthreads();
   cluster_sync_all();  // no CTA ends while another may still write to its shared memory
+  if (aborted)         // pushes that nobody waited for land meanwhile
+    for (int i = 0; i < 100; ++i) __nanosleep(1000);
   finish_rows(p, all_loss, all_bits | (aborted ? FLCE_STATUS_BIT_TIMEOUT : 0), all_rows);
 }
 
@@ -1465,6 +1469,9 @@ cudaError_t launch_rows_of(const RowLossParams& p, cudaStream_t s) {
   const int64_t wide = vecs > 8 * 2048 ? 4224 : 2048;
   shape.cluster = 1;
   while (div_up(vecs, shape.cluster) > wide) shape.cluster *= 2;
+  // few rows: shorter parts, while every one has an SM or half of one to itself
+  while (shape.cluster < 8 && p.N * shape.cluster * 4 <= 2 * device_sm_count() && vecs / shape.cluster >= 512)
+    shape.cluster *= 2;
   shape.seg_vecs = static_cast<int>(div_up(vecs, shape.cluster));
   if (wide > 2048) return launch_parts<T, KIND, 384, 11, 2>(p, shape, s);
   if (shape.seg_vecs <= 512) return launch_parts<T, KIND, 256, 2, 3>(p, shape, s);
@@ -1509,7 +1516,7 @@ inline void use_workspace(RowLossParams* p, void* workspace, int32_t* status_dev
   p->counts = reinterpret_cast<const int*>(ws + 256);
   p->flags = reinterpret_cast<int*>(ws + 512);
   p->partial = reinterpret_cast<double*>(ws + 512 + kRowLossMaxCtas * sizeof(int));
-  p->timeout_ns = 2000000000ull;
+  p->timeout_ns = wait_timeout_ns();
 }
 
 inline bool row_sizes_ok(int64_t N, int64_t V, int64_t ld) {
