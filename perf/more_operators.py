@@ -264,8 +264,8 @@ def _policy_own(s):
     import linear_cross_entropy_03_gb300 as flce
     c = s["case"]
     out = flce.policy_loss(s["logits"], s["target"], s["advantage"], old_logp=s["old_logp"], ref_logp=s["ref_logp"],
-                           clip=c["clip"], kl_weight=c["kl"], temperature=c["temperature"], row_weight=s["weight"],
-                           ignore_index=IGNORE, reduction=c["reduction"])
+                           clip=c["clip"], kl_weight=c["kl"] if c["reference"] else 0.0, temperature=c["temperature"],
+                           row_weight=s["weight"], ignore_index=IGNORE, reduction=c["reduction"])
     return [out["loss"], out["logp"], out["grad_logits"]]
 
 
