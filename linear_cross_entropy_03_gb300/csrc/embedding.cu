@@ -42,9 +42,10 @@ struct LookupParams {
 constexpr int kLookupUnroll = 4;
 constexpr int kLookupWarps = 4;
 
-// A part of a row by each warp.
-template <typename T, int E>
+// A part of a row by each warp, of rows that are whole vectors.
+template <typename T>
 __global__ void __launch_bounds__(32 * kLookupWarps) embedding_kernel(const LookupParams p) {
+  constexpr int E = 16 / sizeof(T);
   const int lane = threadIdx.x & 31;
   for (int64_t item = static_cast<int64_t>(blockIdx.x) * kLookupWarps + (threadIdx.x >> 5); item < p.N * p.parts;
        item += static_cast<int64_t>(gridDim.x) * kLookupWarps) {
@@ -67,10 +68,82 @@ __global__ void __launch_bounds__(32 * kLookupWarps) embedding_kernel(const Look
       if (at >= p.H) break;
 #pragma unroll
       for (int k = 0; k < E; ++k) v[i].v[k] = from_float<T>(inside ? to_float(v[i].v[k]) * p.scale : 0.f);
-      if constexpr (E > 1)
-        __stcs(reinterpret_cast<uint4*>(to + at), *reinterpret_cast<const uint4*>(&v[i]));
-      else
-        to[at] = v[i].v[0];
+      // past the caches, which keep the table's rows for the next token of the id (37.7 -> 31.0 us)
+      __stcs(reinterpret_cast<uint4*>(to + at), *reinterpret_cast<const uint4*>(&v[i]));
+    }
+  }
+}
+
+// The 16 bytes that start `from` bytes (0 to 15, a multiple of 2) into two vectors.
+__device__ __forceinline__ uint4 across(const uint4& a, const uint4& b, unsigned from) {
+  const unsigned bits = (from & 3) * 8;
+  const auto shifted = [&](uint32_t v, uint32_t w, uint32_t x, uint32_t y, uint32_t z) {
+    return make_uint4(__funnelshift_r(v, w, bits), __funnelshift_r(w, x, bits), __funnelshift_r(x, y, bits),
+                      __funnelshift_r(y, z, bits));
+  };
+  switch (from >> 2) {  // the same for a whole row
+    case 0: return shifted(a.x, a.y, a.z, a.w, b.x);
+    case 1: return shifted(a.y, a.z, a.w, b.x, b.y);
+    case 2: return shifted(a.z, a.w, b.x, b.y, b.z);
+    default: return shifted(a.w, b.x, b.y, b.z, b.w);
+  }
+}
+
+// Rows that start anywhere: vectors by the places of y's row, each made of the two vectors of
+// the table's row that it lies across; what has no two such vectors within the row goes by
+// elements, at both ends.  (By elements alone bf16 [16384, 4095] took 86 us.)
+template <typename T>
+__global__ void __launch_bounds__(32 * kLookupWarps) embedding_shifted_kernel(const LookupParams p) {
+  constexpr int kE = 16 / sizeof(T);
+  const int lane = threadIdx.x & 31;
+  const int bytes = static_cast<int>(p.H * sizeof(T));
+  for (int64_t item = static_cast<int64_t>(blockIdx.x) * kLookupWarps + (threadIdx.x >> 5); item < p.N * p.parts;
+       item += static_cast<int64_t>(gridDim.x) * kLookupWarps) {
+    const int64_t n = item / p.parts;
+    const int part = static_cast<int>(item % p.parts);
+    const int64_t id = id_at(p.ids, p.ids32, n);
+    const bool inside = id >= 0 && id < p.V;
+    if (!inside && p.status != nullptr && lane == 0 && part == 0) atomicOr(p.status, FLCE_STATUS_BIT_TARGET_RANGE);
+    const T* from = static_cast<const T*>(p.table) + (inside ? id : 0) * p.ld_table;
+    T* to = static_cast<T*>(p.y) + n * p.ld_y;
+    // vector j is y's bytes head + 16 j on; it starts `shift` bytes into a vector of the table
+    const int head = static_cast<int>((16 - (reinterpret_cast<uintptr_t>(to) & 15)) & 15);
+    const unsigned shift = static_cast<unsigned>(reinterpret_cast<uintptr_t>(from) + head) & 15;
+    const int vecs = bytes > head ? (bytes - head) / 16 : 0;
+    const int first = static_cast<int>(shift) > head ? 1 : 0;
+    int end = vecs;
+    if (shift != 0) {
+      const int room = bytes - head + static_cast<int>(shift) - 16;  // from vector 0's first part on, less one vector
+      end = room >= 16 ? min(vecs, room / 16) : 0;
+    }
+    if (end < first) end = first;
+    const uint4* source = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(from) + head - shift);
+    uint4* target = reinterpret_cast<uint4*>(reinterpret_cast<uintptr_t>(to) + head);
+    uint4 a[kLookupUnroll], b[kLookupUnroll];
+    const int j0 = part * 32 * kLookupUnroll + lane;
+#pragma unroll
+    for (int i = 0; i < kLookupUnroll; ++i) {
+      const int j = j0 + i * 32;
+      if (j < first || j >= end || !inside) continue;
+      a[i] = __ldg(source + j);
+      b[i] = shift != 0 ? __ldg(source + j + 1) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < kLookupUnroll; ++i) {
+      const int j = j0 + i * 32;
+      if (j < first || j >= end) continue;
+      uint4 v = inside ? across(a[i], b[i], shift) : make_uint4(0, 0, 0, 0);
+      T* e = reinterpret_cast<T*>(&v);
+#pragma unroll
+      for (int k = 0; k < kE; ++k) e[k] = from_float<T>(inside ? to_float(e[k]) * p.scale : 0.f);
+      __stcs(target + j, v);
+    }
+    if (part != 0) continue;
+    const int before = min((head + 16 * first) / static_cast<int>(sizeof(T)), static_cast<int>(p.H));
+    const int after = min(max(before, (head + 16 * end) / static_cast<int>(sizeof(T))), static_cast<int>(p.H));
+    for (int h = lane; h < before + static_cast<int>(p.H) - after; h += 32) {
+      const int at = h < before ? h : after + h - before;
+      to[at] = from_float<T>(inside ? to_float(from[at]) * p.scale : 0.f);
     }
   }
 }
@@ -80,14 +153,14 @@ cudaError_t lookup(LookupParams p, cudaStream_t s) {
   constexpr int kE = 16 / sizeof(T);
   const bool vectors = aligned_to(p.table, 16) && aligned_to(p.y, 16) && p.H % kE == 0 &&
                        (p.ld_table % kE == 0 || p.V == 1) && (p.ld_y % kE == 0 || p.N == 1);
-  p.parts = div_up(p.H, 32 * kLookupUnroll * (vectors ? kE : 1));
+  p.parts = div_up(p.H, 32 * kLookupUnroll * kE);
   const int64_t ctas = div_up(p.N * p.parts, kLookupWarps), most = int64_t(1) << 30;
   const unsigned grid = static_cast<unsigned>(ctas < most ? ctas : most);
   prof_begin(s, FLCE_KERNEL_EMBEDDING);
   if (vectors)
-    embedding_kernel<T, kE><<<grid, 32 * kLookupWarps, 0, s>>>(p);
+    embedding_kernel<T><<<grid, 32 * kLookupWarps, 0, s>>>(p);
   else
-    embedding_kernel<T, 1><<<grid, 32 * kLookupWarps, 0, s>>>(p);
+    embedding_shifted_kernel<T><<<grid, 32 * kLookupWarps, 0, s>>>(p);
   const cudaError_t e = cudaGetLastError();
   prof_end(s);
   return e;
@@ -113,6 +186,7 @@ constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kSortDigit = 9;       // most bits of a pass: two passes reach 2^18 ids
 constexpr int kSortRoom = 8192;     // most tokens that a CTA holds in shared memory
 constexpr int kSortCtas = 8;        // of a cluster
+constexpr int kSortAlone = 2048;    // most tokens that one CTA sorts without a cluster
 
 __device__ __forceinline__ void store_cluster_u64(uint32_t at, uint64_t v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(at), "l"(v) : "memory");
@@ -623,12 +697,14 @@ __global__ void __launch_bounds__(32 * kJoinWarps) embedding_join_kernel(const S
 // ---------------------------------------------------------------- few tokens
 
 constexpr int kFewTokens = 1024;
+constexpr int kFewCtas = 8192;      // most CTAs that compare an id with all others
 constexpr int kFewWarps = 4;
-constexpr int kFewZeroRows = 32;  // rows of the table that a CTA looks after
+constexpr int kFewZeroRows = 32;    // rows of the table that a CTA looks after,
+constexpr int kFewZeroColumns = 2048;  // and so many of their columns
 
 // Without sorting, in one launch: a CTA for each token and piece of a row compares the
 // token's id with all others; the first token of an id adds up its rows, each warp every
-// kFewWarps-th one of them, and then the warps' sums.  The CTAs after those write zeros to
+// kFewWarps-th one of them, and then the warps' sums.  The CTAs before those write zeros to
 // rows that no token has.
 template <typename T, int E, int GROUPS>
 __global__ void __launch_bounds__(32 * kFewWarps) embedding_few_kernel(const SumParams p) {
@@ -636,13 +712,14 @@ __global__ void __launch_bounds__(32 * kFewWarps) embedding_few_kernel(const Sum
   __shared__ unsigned hit;
   __shared__ Sums<E, GROUPS> sums[kFewWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const unsigned sum_ctas = static_cast<unsigned>(p.N) * p.columns;
   const auto key_of = [&](int i) -> int64_t {
     const int64_t id = i < p.N ? id_at(p.ids, p.ids32, i) : -1;
     return id == p.padding || id >= p.V ? -1 : id;
   };
-  if (blockIdx.x >= sum_ctas) {
-    const int64_t v0 = static_cast<int64_t>(blockIdx.x - sum_ctas) * kFewZeroRows;
+  if (blockIdx.x < p.zero_ctas) {
+    const unsigned pieces = static_cast<unsigned>((p.H + kFewZeroColumns - 1) / kFewZeroColumns);
+    const int64_t v0 = static_cast<int64_t>(blockIdx.x / pieces) * kFewZeroRows;
+    const int64_t h0 = static_cast<int64_t>(blockIdx.x % pieces) * kFewZeroColumns;
     if (threadIdx.x == 0) hit = 0;
     __syncthreads();
     unsigned mine = 0;
@@ -654,10 +731,11 @@ __global__ void __launch_bounds__(32 * kFewWarps) embedding_few_kernel(const Sum
     if (mine != 0) atomicOr(&hit, mine);
     __syncthreads();
     for (int r = warp; r < kFewZeroRows && v0 + r < p.V; r += kFewWarps)
-      if (!(hit >> r & 1)) write_zeros(p.table + (v0 + r) * p.H, p.H, lane, E > 1);
+      if (!(hit >> r & 1))
+        write_zeros(p.table + (v0 + r) * p.H + h0, p.H - h0 < kFewZeroColumns ? p.H - h0 : kFewZeroColumns, lane, E > 1);
     return;
   }
-  const int n = blockIdx.x / p.columns, column = blockIdx.x % p.columns;
+  const int n = (blockIdx.x - p.zero_ctas) / p.columns, column = (blockIdx.x - p.zero_ctas) % p.columns;
   const int64_t key = key_of(n);
   if (p.status != nullptr && column == 0 && threadIdx.x == 0) {
     const int64_t id = id_at(p.ids, p.ids32, n);
@@ -770,7 +848,7 @@ cudaError_t sort_tokens(SortParams p, cudaStream_t s) {
   p.passes = (bits + kSortDigit - 1) / kSortDigit;
   p.digit = (bits + p.passes - 1) / p.passes;
   prof_begin(s, FLCE_KERNEL_TOKEN_SORT);
-  const cudaError_t e = p.N <= kSortRoom               ? launch_sort<1, true>(p, s)
+  const cudaError_t e = p.N <= kSortAlone              ? launch_sort<1, true>(p, s)
                         : p.N <= kSortRoom * kSortCtas ? launch_sort<kSortCtas, true>(p, s)
                                                        : launch_sort<kSortCtas, false>(p, s);
   prof_end(s);
@@ -790,8 +868,8 @@ cudaError_t sum_rows(SumParams p, bool vectors, bool few, cudaStream_t s) {
   cudaError_t e;
   prof_begin(s, FLCE_KERNEL_EMBEDDING_BWD);
   if (few) {
-    const int64_t ctas = static_cast<int64_t>(p.N) * p.columns + (p.accumulate ? 0 : div_up(p.V, kFewZeroRows));
-    const unsigned grid = static_cast<unsigned>(ctas);
+    p.zero_ctas = p.accumulate ? 0 : static_cast<unsigned>(div_up(p.V, kFewZeroRows) * div_up(p.H, kFewZeroColumns));
+    const unsigned grid = static_cast<unsigned>(p.N) * p.columns + p.zero_ctas;
     if (vectors)
       embedding_few_kernel<T, kE, 1><<<grid, 32 * kFewWarps, 0, s>>>(p);
     else
@@ -872,8 +950,11 @@ flce_status_t embedding_bwd(int dtype, const void* grad_y, int64_t ld_grad_y, co
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream_);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
 
-  // without the sort where the CTAs that compare and those that write zeros are few
-  const bool few = N <= kFewTokens;
+  // without the sort (11 us) where the CTAs that compare ids are few
+  const bool vectors = aligned_to(grad_y, 16) && aligned_to(grad_table, 16) && H % (16 / esz) == 0 &&
+                          (ld_grad_y % static_cast<int64_t>(16 / esz) == 0 || N <= 1);
+  const bool few = N <= kFewTokens && N * div_up(H, vectors ? 32 * (16 / esz) : 128) <= kFewCtas &&
+                   div_up(V, kFewZeroRows) * div_up(H, kFewZeroColumns) < (int64_t(1) << 30);
   SortParams sort = {};
   sort.ids = ids, sort.ids32 = index_type == FLCE_INDEX_INT32;
   sort.N = static_cast<int>(N), sort.V = static_cast<int>(V), sort.padding = padding_index;
@@ -892,9 +973,6 @@ flce_status_t embedding_bwd(int dtype, const void* grad_y, int64_t ld_grad_y, co
   p.joins = reinterpret_cast<int*>(ws + at.joins);
   p.accumulate = accumulate, p.scale = scale, p.tiles = static_cast<int>(tiles);
   p.ids = ids, p.ids32 = sort.ids32, p.padding = padding_index, p.status = status_dev;
-  const int64_t elems = 16 / static_cast<int64_t>(esz);
-  const bool vectors =
-      aligned_to(grad_y, 16) && aligned_to(grad_table, 16) && H % elems == 0 && (ld_grad_y % elems == 0 || N <= 1);
   const cudaError_t e = dtype == FLCE_DTYPE_BF16   ? sum_rows<__nv_bfloat16>(p, vectors, few, s)
                         : dtype == FLCE_DTYPE_FP16 ? sum_rows<__half>(p, vectors, few, s)
                                                    : sum_rows<float>(p, vectors, few, s);
@@ -902,8 +980,9 @@ flce_status_t embedding_bwd(int dtype, const void* grad_y, int64_t ld_grad_y, co
   if (!few) {
     const unsigned columns = static_cast<unsigned>(div_up(H, vectors ? 128 : 32));
     prof_begin(s, FLCE_KERNEL_EMBEDDING_JOIN);
-    const cudaError_t j = launch_after(vectors ? embedding_join_kernel<4> : embedding_join_kernel<1>,
-                                       dim3(static_cast<unsigned>(std::min<int64_t>(div_up(tiles, kJoinTiles), 4096)), columns),
+    const int64_t most = std::max<int64_t>(1, 4096 / columns);
+    const dim3 grid(static_cast<unsigned>(std::min<int64_t>(div_up(tiles, kJoinTiles), most)), columns);
+    const cudaError_t j = launch_after(vectors ? embedding_join_kernel<4> : embedding_join_kernel<1>, grid,
                                        dim3(32 * kJoinWarps), s, p);
     prof_end(s);
     if (j != cudaSuccess) return FLCE_ERR_CUDA;
