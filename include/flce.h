@@ -594,8 +594,9 @@ flce_status_t adamw_step(const flce_adamw_tensor_t* tensors, int64_t count,
  * fast case.  Arithmetic is fp32, with one rounding to the gradient's type; sums
  * over rows are fp64 in a fixed order: the results are the same from run to run.
  * Logits of -inf are columns of probability 0.  A row with NaN or +inf, or of
- * -inf alone, has a loss and gradients of NaN, and no other row has.  A row
- * that takes no part, or whose weight is 0, gets zeros whatever it holds.
+ * -inf alone, has a loss and gradients of NaN, and no other row has (but the
+ * rows of its pair).  A row that takes no part, or whose weight is 0, gets zeros
+ * whatever it holds.
  */
 
 /*
@@ -603,7 +604,7 @@ flce_status_t adamw_step(const flce_adamw_tensor_t* tensors, int64_t count,
  *  clip_low, clip_high  >= 0; the ratio is cut to [1 - clip_low, 1 + clip_high];
  *                       infinity: not cut on that side.
  *  kl_weight            finite, >= 0.
- *  temperature          > 0, finite: what the logits were divided by to sample.
+ *  temperature          1e-4 to 1e4: what the logits were divided by to sample.
  */
 typedef struct {
   float clip_low, clip_high;
@@ -663,9 +664,9 @@ typedef enum { FLCE_INDEX_INT64 = 0, FLCE_INDEX_INT32 = 1 } flce_index_t;
  *                is left out; a column that is named twice has both shares.
  *  values        [N, top] of value_dtype (any of the three types): the teacher's
  *                logits or log-probabilities.  -inf: no share; a list of -inf alone
- *                gives loss 0 and gradient 0.
+ *                gives loss 0 and gradient 0; NaN or +inf: the row's loss is NaN.
  *  top           1 to FLCE_DISTILL_MAX_TOP.
- *  temperature   > 0, finite.
+ *  temperature   1e-4 to 1e4.
  *  row_weight    fp32 [N], or NULL (1).
  *  loss          [N] for NONE.
  */

@@ -17,7 +17,7 @@ flce_status_t distill_fwd_bwd(const void* logits, int dtype, int64_t ld, void* g
                                       loss, workspace, workspace_bytes, kRowLossFixed, status_dev);
   if (st != FLCE_OK) return st;
   if (index_type != FLCE_INDEX_INT64 && index_type != FLCE_INDEX_INT32) return FLCE_ERR_INVALID_ARG;
-  if (top < 1 || !positive(temperature) || (N > 0 && (ids == nullptr || values == nullptr)))
+  if (top < 1 || !temperature_ok(temperature) || (N > 0 && (ids == nullptr || values == nullptr)))
     return FLCE_ERR_INVALID_ARG;
   if (top > kMaxTeacher) return FLCE_ERR_UNSUPPORTED;
   if (!aligned_to(ids, index_type == FLCE_INDEX_INT64 ? 8 : 4) || !aligned_to(values, elem_size(value_dtype)) ||

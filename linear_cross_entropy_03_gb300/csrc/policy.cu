@@ -18,7 +18,7 @@ flce_status_t policy_fwd_bwd(const void* logits, int dtype, int64_t ld, void* gr
                                       loss, workspace, workspace_bytes, kRowLossFixed, status_dev);
   if (st != FLCE_OK) return st;
   if (numbers == nullptr || (N > 0 && (target == nullptr || advantage == nullptr))) return FLCE_ERR_INVALID_ARG;
-  if (!(numbers->clip_low >= 0.f) || !(numbers->clip_high >= 0.f) || !positive(numbers->temperature) ||
+  if (!(numbers->clip_low >= 0.f) || !(numbers->clip_high >= 0.f) || !temperature_ok(numbers->temperature) ||
       !(numbers->kl_weight == 0.f || positive(numbers->kl_weight)))
     return FLCE_ERR_INVALID_ARG;
   if (numbers->kl_weight != 0.f && ref_logp == nullptr && N > 0) return FLCE_ERR_INVALID_ARG;

@@ -1563,6 +1563,8 @@ inline RowLossParams row_params(const void* logits, int64_t ld, void* grad, int6
 }
 
 inline bool positive(float x) { return x > 0.f && x <= 3.402823466e38f; }
+// Temperatures: T, 1 / T and T^2 times a loss stay in the range of fp32.
+inline bool temperature_ok(float t) { return t >= 1e-4f && t <= 1e4f; }
 
 }  // namespace
 }  // namespace flce

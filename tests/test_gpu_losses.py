@@ -504,3 +504,37 @@ def test_preference_many_target_errors():
     t[3], t[7] = 90, -5
     check_preference(z, np.where((t < 0) | (t >= 90), -100, t), offsets, "bf16",
                      out=flce.preference_loss(z, cuda(t), offsets=cuda(offsets)), status=flce.STATUS_BIT_TARGET_RANGE)
+
+
+@pytest.mark.parametrize("temperature", [1e-4, 1e4])
+@pytest.mark.parametrize("v", [700, 40000])
+def test_the_ends_of_the_temperature(temperature, v):
+    """Where all but the largest have no share, and where all have the same."""
+    z = make_logits(12, v, "fp32", 5, scale=3.0)
+    t = np.array([int(x) for x in wide(z).argmax(1)])
+    t[3] = (t[3] + 1) % v
+    a = f32(np.random.default_rng(1).normal(size=12))
+    check_policy(z, t, a, dict(temperature=temperature), "fp32")
+    ids, values = teacher(12, v, 20, v)
+    # the teacher's and the student's differences over 1e-4 reach 1e5: fp32 leaves 2^-23 of that in the exponents
+    out = flce.distillation_loss(z, cuda(ids), cuda(values, torch.float32), temperature=temperature, reduction="none")
+    want = L.distill(wide(z), ids, f32(values), temperature=temperature, reduction="none")
+    tol = temperature ** 2 * (LNS + 2.0 ** -19 * (60 / temperature + 16))
+    close(wide(out["loss"]), want["loss"], tol, "loss")
+
+
+@pytest.mark.parametrize("v", [500, 9000, 70001, 290000])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_rows_of_the_lowest_value(v, dtype):
+    """Where a mask of the type's lowest value leaves nothing, all columns are alike; beside others they have no share."""
+    z = make_logits(4, v, dtype, 3)
+    low = torch.finfo(TYPES[dtype]).min
+    z[0] = low
+    z[1, : v // 2] = low
+    z[2] = torch.finfo(TYPES[dtype]).max
+    z[3, 1:] = low
+    t = np.array([3, v - 1, 5, 0])
+    check_policy(z, t, f32(np.ones(4)), {}, dtype)
+    ids = np.array([[0, 2], [v - 1, v - 2], [1, 3], [0, 0]])
+    check_distill(z, ids, np.zeros((4, 2)), dtype, reduction="none")
+    check_preference(z, t, np.array([0, 2, 4]), dtype)

@@ -52,7 +52,8 @@ def _policy(numbers=None, **kw):
     (dict(numbers=(0.2, 0.2, -1.0, 1.0)), INVALID), (dict(numbers=(0.2, 0.2, INF, 1.0)), INVALID),
     (dict(numbers=(0.2, 0.2, NAN, 1.0)), INVALID), (dict(numbers=(0.2, 0.2, 0.0, 0.0)), INVALID),
     (dict(numbers=(0.2, 0.2, 0.0, -1.0)), INVALID), (dict(numbers=(0.2, 0.2, 0.0, INF)), INVALID),
-    (dict(numbers=(0.2, 0.2, 0.0, NAN)), INVALID), (dict(target=FAKE + 4), MISALIGNED),
+    (dict(numbers=(0.2, 0.2, 0.0, NAN)), INVALID), (dict(numbers=(0.2, 0.2, 0.0, 9e-5)), INVALID),
+    (dict(numbers=(0.2, 0.2, 0.0, 1.1e4)), INVALID), (dict(target=FAKE + 4), MISALIGNED),
     (dict(advantage=FAKE + 2), MISALIGNED), (dict(old_logp=FAKE + 1), MISALIGNED), (dict(logp=FAKE + 2), MISALIGNED),
     (dict(row_weight=FAKE + 2), MISALIGNED), (dict(ref_logp=FAKE + 2), MISALIGNED),
 ])
@@ -77,7 +78,8 @@ def _distill(**kw):
     (dict(ids=None), INVALID), (dict(values=None), INVALID), (dict(index_type=2), INVALID),
     (dict(index_type="int16"), INVALID), (dict(value_dtype=3), UNSUPPORTED), (dict(top=0), INVALID),
     (dict(top=1025), UNSUPPORTED), (dict(temperature=0.0), INVALID), (dict(temperature=NAN), INVALID),
-    (dict(temperature=INF), INVALID), (dict(ids=FAKE + 4), MISALIGNED), (dict(values=FAKE + 1), MISALIGNED),
+    (dict(temperature=INF), INVALID), (dict(temperature=1e-5), INVALID), (dict(temperature=1e5), INVALID),
+    (dict(ids=FAKE + 4), MISALIGNED), (dict(values=FAKE + 1), MISALIGNED),
     (dict(index_type="int32", ids=FAKE + 2), MISALIGNED), (dict(row_weight=FAKE + 2), MISALIGNED),
 ])
 def test_distill_refuses(kw, code):
