@@ -1406,7 +1406,9 @@ cudaError_t launch_parts_of(const RowLossParams& p, PartShape shape, cudaStream_
   shape.slot_bytes = (shape.seg_vecs * 16 + 127) & ~127;
   shape.slots = static_cast<int>(room > lists ? (room - lists) / shape.slot_bytes : 1);
   if (shape.slots > kPartSlots) shape.slots = kPartSlots;
-  if (shape.slots < 1) shape.slots = 1;
+  // where gradients are written, one part ahead: with two, more reads among the writes made
+  // memory slower (policy loss, bf16 [4096, 128256], 341 -> 328 us; fp32 [1000, 50257] 74 -> 73)
+  if (shape.slots < 1 || p.grad != nullptr) shape.slots = 1;
   const size_t smem = static_cast<size_t>(shape.slots) * shape.slot_bytes + lists;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(THREADS + 64);
@@ -1456,27 +1458,27 @@ cudaError_t launch_parts(const RowLossParams& p, const PartShape& shape, cudaStr
                : launch_parts_of<T, KIND, THREADS, VPT, CTAS_PER_SM, false>(p, shape, s);
 }
 
-// Rows of up to 256 vectors (4 KB) by warps.  Parts of up to 2048 vectors by 256 threads (32 KB; three CTAs an SM, with two parts each
-// in shared memory), of up to 4224 by 384; rows beyond eight of these are read twice.
+// Rows of up to 256 vectors (4 KB) by warps; then by parts of up to 2048 vectors (32 KB) by 256
+// threads, three CTAs an SM; rows of more than eight of these by parts of up to 4096, two
+// CTAs an SM; and what is longer is read twice.  For a teacher's list, which every CTA of a
+// row reads, the larger parts from more than four on: bf16 [4096, 128256] 350 -> 325 us (but
+// fp32 [1999, 32001], of four parts, 86 -> 94; the policy loss on [4096, 128256] 328 -> 344).
 template <typename T, int KIND>
 cudaError_t launch_rows_of(const RowLossParams& p, cudaStream_t s) {
   const int64_t vecs = p.V / kVecElems<T>;
   PartShape shape = {};
-  if (p.N == 0 || vecs > 8 * 4224) return launch_long<T, KIND>(p, s);
+  if (p.N == 0 || vecs > 8 * 4096) return launch_long<T, KIND>(p, s);
   if (vecs <= 32) return launch_warps<T, KIND, 1>(p, s);
   if (vecs <= 128) return launch_warps<T, KIND, 4>(p, s);
   if (vecs <= 256) return launch_warps<T, KIND, 8>(p, s);
-  const int64_t wide = vecs > 8 * 2048 ? 4224 : 2048;
+  const bool wide = vecs > (KIND == kDistill ? 4 : 8) * 2048;
   shape.cluster = 1;
-  while (div_up(vecs, shape.cluster) > wide) shape.cluster *= 2;
-  // few rows: shorter parts, while every one has an SM or half of one to itself
-  while (shape.cluster < 8 && p.N * shape.cluster * 4 <= 2 * device_sm_count() && vecs / shape.cluster >= 512)
-    shape.cluster *= 2;
+  while (div_up(vecs, shape.cluster) > (wide ? 4096 : 2048)) shape.cluster *= 2;
   shape.seg_vecs = static_cast<int>(div_up(vecs, shape.cluster));
-  if (wide > 2048) return launch_parts<T, KIND, 384, 11, 2>(p, shape, s);
   if (shape.seg_vecs <= 512) return launch_parts<T, KIND, 256, 2, 3>(p, shape, s);
   if (shape.seg_vecs <= 1024) return launch_parts<T, KIND, 256, 4, 3>(p, shape, s);
-  return launch_parts<T, KIND, 256, 8, 3>(p, shape, s);
+  if (shape.seg_vecs <= 2048) return launch_parts<T, KIND, 256, 8, 3>(p, shape, s);
+  return launch_parts<T, KIND, 256, 16, 2>(p, shape, s);
 }
 
 // All rows of a call: the count that a mean needs first, then the rows.
