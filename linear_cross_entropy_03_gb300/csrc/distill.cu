@@ -2,6 +2,10 @@
 // on the student's logits (row_loss.cuh).
 #include "row_loss.cuh"
 
+namespace flce {
+cudaError_t launch_distill_long(const RowLossParams& p, int dtype, cudaStream_t s);  // distill_long.cu
+}
+
 using namespace flce;
 
 extern "C" {
@@ -29,8 +33,9 @@ flce_status_t distill_fwd_bwd(const void* logits, int dtype, int64_t ld, void* g
   p.K = static_cast<int>(top);
   p.row_weight = row_weight;
   use_workspace(&p, workspace, status_dev);
-  return launch_rows<kDistill>(p, dtype, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? FLCE_OK
-                                                                                                 : FLCE_ERR_CUDA;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const cudaError_t e = top <= 32 * kListAhead ? launch_rows<kDistill>(p, dtype, s) : launch_distill_long(p, dtype, s);
+  return e == cudaSuccess ? FLCE_OK : FLCE_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -29,7 +29,9 @@ constexpr int kMaxTeacher = 1024;      // entries of a teacher's list
 constexpr int kRowLossMaxCtas = 4096;  // partial losses in the workspace
 constexpr int kCountCtas = 64;         // partial counts of the rows that take part
 
-enum RowLoss { kPolicy = 0, kDistill = 1, kStats = 2 };
+// kDistill: lists of up to 64 entries; kDistillLong: any.
+enum RowLoss { kPolicy = 0, kDistill = 1, kStats = 2, kDistillLong = 3 };
+constexpr bool has_list(int kind) { return kind == kDistill || kind == kDistillLong; }
 
 struct RowLossParams {
   const void* logits;
@@ -361,7 +363,7 @@ __device__ __forceinline__ float value_of(const RowLossParams& p, uint32_t raw) 
          : p.value_dtype == FLCE_DTYPE_FP16 ? __half2float(__ushort_as_half(static_cast<unsigned short>(raw)))
                                             : __uint_as_float(raw << 16);
 }
-template <typename T>
+template <typename T, int KIND>
 __device__ __forceinline__ ListAhead<T> list_ahead(const RowLossParams& p, int64_t row) {
   ListAhead<T> a;
   const int lane = threadIdx.x & 31;
@@ -370,7 +372,7 @@ __device__ __forceinline__ ListAhead<T> list_ahead(const RowLossParams& p, int64
     const int k = j * 32 + lane;
     a.id[j] = make_uint2(0xFFFFFFFFu, 0xFFFFFFFFu);
     a.value[j] = 0;
-    if (row < p.N && k < p.K) {
+    if (KIND == kDistill && row < p.N && k < p.K) {
       a.id[j] = raw_id(p, row * p.K + k);
       a.value[j] = raw_value(p, row * p.K + k);
     }
@@ -398,12 +400,27 @@ __device__ __forceinline__ bool seen_before(int* table, int slots, int column) {
   }
 }
 
-// A list of up to 32 * kListAhead entries without leaving the registers; false where a column
-// is named twice.
+// Where a column is named twice: every entry gets its column's whole share, so that all that
+// name it write the same.  `table` is free.
+__device__ __forceinline__ void join_shares(const TeacherList& list, int entries, int* table) {
+  float* total = reinterpret_cast<float*>(table);
+  __syncwarp();
+  for (int k = threadIdx.x & 31; k < entries; k += 32) {
+    float q = 0.f;
+    for (int j = 0; j < entries; ++j)
+      if (list.column[j] == list.column[k]) q += list.q[j];
+    total[k] = q;
+  }
+  __syncwarp();
+  for (int k = threadIdx.x & 31; k < entries; k += 32) list.q[k] = total[k];
+  __syncwarp();
+}
+
+// A list of up to 32 * kListAhead entries, without leaving the registers.
 template <typename T, typename Wanted>
-__device__ __forceinline__ bool short_teacher_row(const RowLossParams& p, const ListAhead<T>& ahead,
-                                                  const TeacherList& list, int* table, int* bits, Wanted wanted,
-                                                  RowInfo* out) {
+__device__ __forceinline__ RowInfo short_teacher_row(const RowLossParams& p, const ListAhead<T>& ahead,
+                                                     const TeacherList& list, int* table, int* bits,
+                                                     const Wanted& wanted) {
   const int lane = threadIdx.x & 31;
   RowInfo r = {};
   r.weight = ahead.weight;
@@ -411,6 +428,7 @@ __device__ __forceinline__ bool short_teacher_row(const RowLossParams& p, const 
   r.column = -1;
   const int slots = table_slots(p.K);
   for (int i = lane; i < slots; i += 32) table[i] = -1;
+  __syncwarp();
   const int batches = (p.K + 31) / 32;
   float v[kListAhead], e[kListAhead], z[kListAhead];
   int column[kListAhead];
@@ -455,9 +473,9 @@ __device__ __forceinline__ bool short_teacher_row(const RowLossParams& p, const 
     const float q = e[j] * inv;
     if (held) {
       a += q * ((v[j] - shift) * p.inv_t - ln_sum - (z[j] - r.zt) * p.inv_t);
-      twice = seen_before(table, slots, column[j]) || twice;
     }
     const bool here = held && wanted(column[j]);
+    if (here) twice = seen_before(table, slots, column[j]) || twice;
     const unsigned all = __ballot_sync(0xffffffffu, here);
     if (here) {
       const int at = kept + __popc(all & ((1u << lane) - 1));
@@ -467,129 +485,133 @@ __device__ __forceinline__ bool short_teacher_row(const RowLossParams& p, const 
   }
   r.a = warp_sum(a);
   r.entries = kept;
-  *out = r;
-  return !__any_sync(0xffffffffu, twice);
+  if (__any_sync(0xffffffffu, twice)) join_shares(list, kept, table);
+  __syncwarp();
+  return r;
+}
+
+// Any list, through shared memory.
+template <typename T, typename Wanted>
+__device__ __forceinline__ RowInfo long_teacher_row(const RowLossParams& p, int64_t row, float weight, float grad_out,
+                                                    const TeacherList& list, int* table, int* bits,
+                                                    const Wanted& wanted) {
+  constexpr int kBatch = 4;
+  const int lane = threadIdx.x & 31;
+  const int64_t base = row * p.K;
+  RowInfo r = {};
+  r.weight = weight;
+  r.grad_out = grad_out;
+  r.column = -1;
+  // ids and values, and where the list ends
+  int entries = p.K;
+  for (int k0 = 0; k0 < p.K; k0 += 32 * kBatch) {
+    uint2 id[kBatch];
+    uint32_t value[kBatch];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int k = k0 + j * 32 + lane;
+      if (k < p.K) id[j] = raw_id(p, base + k), value[j] = raw_value(p, base + k);
+    }
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int k = k0 + j * 32 + lane;
+      if (k >= p.K) break;
+      const int column = column_of(p, id[j]);
+      list.column[k] = column;
+      list.q[k] = column >= 0 ? value_of(p, value[j]) : -INFINITY;
+      if (column == -1) entries = min(entries, k);
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) entries = min(entries, __shfl_xor_sync(0xffffffffu, entries, o));
+  __syncwarp();
+  float vmax = -INFINITY;
+  for (int k = lane; k < entries; k += 32) {
+    if (list.column[k] < 0) *bits |= FLCE_STATUS_BIT_TARGET_RANGE;
+    vmax = fmaxf(vmax, list.q[k]);
+  }
+  vmax = warp_max_redux(vmax);
+  const float shift = vmax > -INFINITY ? vmax : 0.f;
+  // sum e, and sum e ((v - shift) - (z - zt)) / T with zt any finite logit of the list; the
+  // wanted entries move to the front of the list, to places that have been read
+  float sum = 0.f, a = 0.f;
+  bool have = false;
+  int kept = 0;
+  for (int k0 = 0; k0 < entries; k0 += 32 * kBatch) {
+    int column[kBatch];
+    float v[kBatch];
+    Raw<T> raw[kBatch];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int k = k0 + j * 32 + lane;
+      column[j] = k < entries ? list.column[k] : -1;
+      v[j] = k < entries ? list.q[k] - shift : -INFINITY;
+      if (column[j] >= 0) raw[j] = raw_logit<T>(p, row, column[j]);
+    }
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      if (k0 + j * 32 >= entries) break;
+      const float e = ex2_approx(v[j] * p.c);  // 0: no share, the place is like any other
+      const bool held = column[j] >= 0 && e != 0.f;
+      const float z = held ? raw_float<T>(raw[j]) : 0.f;
+      if (!have) {
+        const unsigned finite = __ballot_sync(0xffffffffu, held && fabsf(z) < INFINITY);
+        if (finite != 0) {
+          r.zt = __shfl_sync(0xffffffffu, z, __ffs(finite) - 1);
+          have = true;
+        }
+      }
+      if (held) {
+        sum += e;
+        a += e * ((v[j] - (z - r.zt)) * p.inv_t);
+      }
+      const bool here = held && wanted(column[j]);
+      const unsigned all = __ballot_sync(0xffffffffu, here);
+      if (here) {
+        const int at = kept + __popc(all & ((1u << lane) - 1));
+        list.column[at] = column[j], list.q[at] = e, list.z[at] = z;
+      }
+      kept += __popc(all);
+    }
+    __syncwarp();
+  }
+  sum = warp_sum(sum);
+  r.taught = sum != 0.f;  // (a list of -inf alone is no teacher)
+  r.entries = r.taught ? kept : 0;
+  const float inv = 1.f / sum;
+  r.a = warp_sum(a) * inv - logf(sum);
+  // a column that is named twice is twice among the wanted entries
+  const int slots = table_slots(p.K);
+  for (int i = lane; i < slots; i += 32) table[i] = -1;
+  __syncwarp();
+  bool twice = false;
+  for (int k = lane; k < r.entries; k += 32) {
+    list.q[k] *= inv;
+    twice = seen_before(table, slots, list.column[k]) || twice;
+  }
+  if (__any_sync(0xffffffffu, twice)) join_shares(list, r.entries, table);
+  __syncwarp();
+  return r;
 }
 
 // A row's list, by one warp: returns the row's numbers and fills `list` with the entries
 // whose columns are `wanted`, q of columns that occur twice added up.  `ahead`: the list's
 // first entries, with their logits.  `table` has table_slots(K) words.
-template <typename T, typename Wanted>
-__device__ RowInfo teacher_row(const RowLossParams& p, int64_t row, const ListAhead<T>& ahead,
-                               const TeacherList& list, int* table, int* bits, Wanted wanted) {
-  if (p.K <= 32 * kListAhead) {
-    RowInfo r;
-    const bool done = short_teacher_row<T>(p, ahead, list, table, bits, wanted, &r);
-    __syncwarp();
-    if (done) return r;
-  }
-  const int lane = threadIdx.x & 31;
-  const int64_t base = row * p.K;
-  RowInfo r = {};
-  r.weight = ahead.weight;
-  r.grad_out = ahead.grad_out;
-  r.column = -1;
-  const int slots = table_slots(p.K);
-  for (int i = lane; i < slots; i += 32) table[i] = -1;
-  float vmax = -INFINITY;
-  int entries = 0;
-  bool ended = false;
-  const auto take = [&](int k, int column, float v, float z) {
-    const unsigned ends = __ballot_sync(0xffffffffu, column == -1);
-    const int first = ends != 0 ? __ffs(ends) - 1 : 32;
-    if (lane < first) {
-      if (column < 0) {
-        *bits |= FLCE_STATUS_BIT_TARGET_RANGE;
-        v = -INFINITY;
-      }
-      list.column[k] = column;
-      list.q[k] = v;
-      list.z[k] = z;
-      vmax = fmaxf(vmax, v);
-    }
-    entries += first;
-    ended = ends != 0;
-  };
-#pragma unroll
-  for (int j = 0; j < kListAhead; ++j)
-    if (!ended)
-      take(j * 32 + lane, column_of(p, ahead.id[j]), value_of(p, ahead.value[j]), raw_float<T>(ahead.z[j]));
-#pragma unroll 2
-  for (int k0 = 32 * kListAhead; k0 < p.K && !ended; k0 += 32) {
-    const int k = k0 + lane;
-    const bool held = k < p.K;
-    const int column = held ? column_of(p, raw_id(p, base + k)) : -1;
-    take(k, column, held ? value_of(p, raw_value(p, base + k)) : -INFINITY,
-         column >= 0 ? raw_float<T>(raw_logit<T>(p, row, column)) : -INFINITY);
-  }
-  __syncwarp();
-  vmax = warp_max_redux(vmax);
-  const float shift = vmax > -INFINITY ? vmax : 0.f;
-  float sum = 0.f, zmax = -INFINITY;
-  for (int k = lane; k < entries; k += 32) {
-    const float e = ex2_approx((list.q[k] - shift) * p.c);
-    if (e == 0.f) {
-      list.column[k] = -1;  // no share: the place is like any other
-    } else {
-      sum += e;
-      zmax = fmaxf(zmax, list.z[k]);
-    }
-    list.q[k] = e;
-  }
-  sum = warp_sum(sum);
-  zmax = warp_max_redux(zmax);
-  r.zt = zmax > -INFINITY ? zmax : 0.f;
-  r.taught = sum != 0.f;  // (a list of -inf alone is no teacher)
-  r.entries = r.taught ? entries : 0;
-  const float inv = 1.f / sum, ln_sum = logf(sum);
-  float a = 0.f;
-  bool twice = false;
-  for (int k = lane; k < r.entries; k += 32) {
-    const int column = list.column[k];
-    if (column < 0) continue;
-    const float e = list.q[k], q = e * inv;
-    a += q * (logf(e) - ln_sum - (list.z[k] - r.zt) * p.inv_t);
-    list.q[k] = q;
-    twice = seen_before(table, slots, column) || twice;
-  }
-  r.a = warp_sum(a);
-  __syncwarp();
-  if (__any_sync(0xffffffffu, twice)) {
-    // every entry gets its column's whole share, so that all that name it write the same
-    float* total = reinterpret_cast<float*>(table);
-    for (int k = lane; k < r.entries; k += 32) {
-      float q = 0.f;
-      for (int j = 0; j < r.entries; ++j)
-        if (list.column[j] == list.column[k] && list.column[j] >= 0) q += list.q[j];
-      total[k] = q;
-    }
-    __syncwarp();
-    for (int k = lane; k < r.entries; k += 32) list.q[k] = total[k];
-  }
-  __syncwarp();
-  // of the list, the caller's entries alone
-  int kept = 0;
-  for (int k0 = 0; k0 < r.entries; k0 += 32) {
-    const int k = k0 + lane;
-    const int column = k < r.entries ? list.column[k] : -1;
-    const float q = k < r.entries ? list.q[k] : 0.f, z = k < r.entries ? list.z[k] : 0.f;
-    const bool here = column >= 0 && wanted(column);
-    const unsigned all = __ballot_sync(0xffffffffu, here);
-    const int at = kept + __popc(all & ((1u << lane) - 1));  // (not past k)
-    if (here) list.column[at] = column, list.q[at] = q, list.z[at] = z;
-    kept += __popc(all);
-    __syncwarp();
-  }
-  r.entries = kept;
-  return r;
+template <typename T, int KIND, typename Wanted>
+__device__ __forceinline__ RowInfo teacher_row(const RowLossParams& p, int64_t row, const ListAhead<T>& ahead,
+                                               const TeacherList& list, int* table, int* bits, const Wanted& wanted) {
+  if constexpr (KIND == kDistill)
+    return short_teacher_row<T>(p, ahead, list, table, bits, wanted);
+  else
+    return long_teacher_row<T>(p, row, ahead.weight, ahead.grad_out, list, table, bits, wanted);
 }
-
-template <typename T>
+template <typename T, int KIND>
 __device__ __forceinline__ RowInfo whole_teacher_row(const RowLossParams& p, int64_t row, const TeacherList& list,
                                                      int* table, int* bits) {
-  ListAhead<T> a = list_ahead<T>(p, row);
-  list_logits<T>(p, row, a);
-  return teacher_row<T>(p, row, a, list, table, bits, [](int) { return true; });
+  ListAhead<T> a = list_ahead<T, KIND>(p, row);
+  if constexpr (KIND == kDistill) list_logits<T>(p, row, a);
+  return teacher_row<T, KIND>(p, row, a, list, table, bits, [](int) { return true; });
 }
 
 // ---------------------------------------------------------------- a row's loss
@@ -606,7 +628,7 @@ __device__ __forceinline__ RowResult row_result(const RowLossParams& p, const Ro
   RowResult out = {0.f, 0.f, 0.f};
   const float ln_s = logf(s);
   scale *= r.grad_out;
-  if constexpr (KIND == kDistill) {
+  if constexpr (has_list(KIND)) {
     if (!r.taught || r.weight == 0.f) return out;
     out.loss = p.temperature * p.temperature * r.weight * (r.a + ((m - r.zt) * p.inv_t + ln_s));
     out.f = p.temperature * r.weight * scale;
@@ -641,7 +663,7 @@ __device__ __forceinline__ float entry_grad(const RowLossParams& p, const Teache
 
 template <int KIND>
 __device__ __forceinline__ bool takes_part(const RowLossParams& p, int64_t n) {
-  if constexpr (KIND == kDistill) return load_id(p.ids, p.ids32, n * p.K) >= 0;
+  if constexpr (has_list(KIND)) return load_id(p.ids, p.ids32, n * p.K) >= 0;
   const int64_t t = __ldg(p.target + n);
   return t != p.ignore_index && t >= 0 && t < p.V;
 }
@@ -777,8 +799,8 @@ __global__ void __launch_bounds__(kLongThreads) row_loss_long_kernel(const RowLo
     float m = -INFINITY, s = 0.f;
     if (warp == 0) {
       RowInfo r;
-      if constexpr (KIND == kDistill)
-        r = whole_teacher_row<T>(p, row, list, reinterpret_cast<int*>(list_memory + list_bytes(p.K)), &bits);
+      if constexpr (has_list(KIND))
+        r = whole_teacher_row<T, KIND>(p, row, list, reinterpret_cast<int*>(list_memory + list_bytes(p.K)), &bits);
       else
         r = policy_row<T>(p, row, &bits);
       if (lane == 0) info = r;
@@ -827,7 +849,7 @@ __global__ void __launch_bounds__(kLongThreads) row_loss_long_kernel(const RowLo
       }
       __syncthreads();  // the places that the row names are written after the rest
       if (!zero) {
-        if constexpr (KIND == kDistill) {
+        if constexpr (has_list(KIND)) {
           for (int k = tid; k < r.entries; k += kLongThreads)
             g[list.column[k]] = from_float<T>(entry_grad(p, list, k, result.f, all.x, inv_s));
         } else if (tid == 0) {
@@ -846,7 +868,7 @@ __global__ void __launch_bounds__(kLongThreads) row_loss_long_kernel(const RowLo
 
 template <typename T, int KIND>
 cudaError_t launch_long(const RowLossParams& p, cudaStream_t s) {
-  const size_t smem = KIND == kDistill ? list_bytes(p.K) + table_slots(p.K) * 4 : 0;
+  const size_t smem = has_list(KIND) ? list_bytes(p.K) + table_slots(p.K) * 4 : 0;
   const int64_t most = 4 * device_sm_count();
   const unsigned grid = static_cast<unsigned>(p.N < 1 ? 1 : p.N < most ? p.N : most);
   cudaLaunchConfig_t cfg = {};
@@ -874,7 +896,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) row_loss_warps_kernel(const Ro
   __shared__ double losses[kRowWarps];
   __shared__ int count, all_bits;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, warps = blockDim.x >> 5;
-  const size_t each = KIND == kDistill ? list_bytes(p.K) + table_slots(p.K) * 4 : 0;
+  const size_t each = has_list(KIND) ? list_bytes(p.K) + table_slots(p.K) * 4 : 0;
   const TeacherList list = list_at(list_memory + warp * each, p.K);
   int* const table = reinterpret_cast<int*>(list_memory + warp * each + list_bytes(p.K));
   if (tid == 0) {
@@ -914,8 +936,8 @@ __global__ void __launch_bounds__(32 * kRowWarps) row_loss_warps_kernel(const Ro
     if (lane >= 8 && lane < 8 + split.tail) extra = static_cast<int>(p.V) - split.tail + lane - 8;
     const float z = extra >= 0 ? to_float(x[extra]) : -INFINITY;
     RowInfo r;
-    if constexpr (KIND == kDistill)
-      r = whole_teacher_row<T>(p, row, list, table, &bits);
+    if constexpr (has_list(KIND))
+      r = whole_teacher_row<T, KIND>(p, row, list, table, &bits);
     else
       r = policy_row<T>(p, row, &bits);
     const float m = warp_max_redux(fmaxf(vecs_max<T, VPT>(v), z));
@@ -940,7 +962,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) row_loss_warps_kernel(const Ro
     if (extra >= 0) g[extra] = from_float<T>(zero ? 0.f : f * ex2_approx((z - m) * p.c));
     __syncwarp();  // the places that the row names are written after the rest
     if (zero) continue;
-    if constexpr (KIND == kDistill) {
+    if constexpr (has_list(KIND)) {
       for (int k = lane; k < r.entries; k += 32)
         g[list.column[k]] = from_float<T>(entry_grad(p, list, k, result.f, m, inv_s));
       __syncwarp();  // the list is the next row's
@@ -959,7 +981,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) row_loss_warps_kernel(const Ro
 
 template <typename T, int KIND, int VPT>
 cudaError_t launch_warps(const RowLossParams& p, cudaStream_t s) {
-  const size_t each = KIND == kDistill ? list_bytes(p.K) + table_slots(p.K) * 4 : 0;
+  const size_t each = has_list(KIND) ? list_bytes(p.K) + table_slots(p.K) * 4 : 0;
   int warps = kRowWarps;  // fewer where the lists are long, or the rows few
   while (warps > 1 && (warps * each > 40 * 1024 || div_up(p.N, warps) < device_sm_count())) warps /= 2;
   const int64_t ctas = div_up(p.N, warps), most = 8 * device_sm_count();
@@ -1078,7 +1100,7 @@ __global__ void __launch_bounds__(THREADS + 64, CTAS_PER_SM)
   if (tid == 0) {
     for (int i = 0; i < kPartSlots; ++i) {
       mbar_init(smem_addr(&full[i]), 1);
-      mbar_init(smem_addr(&empty[i]), kWarps + (KIND == kDistill ? 1 : 0));
+      mbar_init(smem_addr(&empty[i]), kWarps + (has_list(KIND) ? 1 : 0));
     }
     for (int i = 0; i < kKept; ++i) {
       mbar_init(smem_addr(&told[i]), 1);
@@ -1122,15 +1144,15 @@ __global__ void __launch_bounds__(THREADS + 64, CTAS_PER_SM)
       while (issued < shape.slots && issued < mine) issue();
     int slot = 0, use = 0;  // i % slots, i / slots
     const auto read_ahead = [&](int64_t row) {
-      if constexpr (KIND == kDistill)
-        return list_ahead<T>(p, row);
+      if constexpr (has_list(KIND))
+        return list_ahead<T, KIND>(p, row);
       else
         return policy_ahead<T>(p, row);
     };
     const auto read_logits = [&](int64_t row, auto& a) {
       if constexpr (KIND == kDistill)
         list_logits<T>(p, row, a);
-      else
+      else if constexpr (!has_list(KIND))
         policy_logit<T>(p, row, a);
     };
     auto ahead = read_ahead(row_of(0)), next = read_ahead(row_of(1));
@@ -1140,11 +1162,11 @@ __global__ void __launch_bounds__(THREADS + 64, CTAS_PER_SM)
       // infos of row i - 4 and the list of row i - 2 are no longer used
       const int64_t row = row_of(i);
       RowInfo r;
-      if constexpr (KIND == kDistill) {
+      if constexpr (has_list(KIND)) {
         const size_t at = static_cast<size_t>(i & 1) * list_bytes(p.K);
         const RowSplit split = split_of(logits_of(row));
         const int n = part_vecs(split);
-        r = teacher_row<T>(p, row, ahead, list_at(lists + at, p.K),
+        r = teacher_row<T, KIND>(p, row, ahead, list_at(lists + at, p.K),
                            reinterpret_cast<int*>(lists + 2 * list_bytes(p.K)), &bits, [&](int column) {
                              const int inside = column - split.head, vec = inside / kE;
                              return inside < 0          ? rank == 0
@@ -1202,7 +1224,7 @@ __global__ void __launch_bounds__(THREADS + 64, CTAS_PER_SM)
     float z, next_z = edge_of(0, &next_edge);
     bool alive = true;
     for (int i = 0; i < mine; ++i) {
-      if (KIND == kDistill && lane == 0 && alive) mbar_arrive(smem_addr(&empty[slot]));  // done with row i - 1's list
+      if (has_list(KIND) && lane == 0 && alive) mbar_arrive(smem_addr(&empty[slot]));  // done with row i - 1's list
       if (++slot == shape.slots) slot = 0;
       z = next_z, edge = next_edge;
       next_z = edge_of(i + 1, &next_edge);
@@ -1260,7 +1282,7 @@ __global__ void __launch_bounds__(THREADS + 64, CTAS_PER_SM)
           if (KIND == kPolicy && !zero && edge == info.column) out = target_grad(result);
           g[edge] = from_float<T>(out);
         }
-        if constexpr (KIND == kDistill) {
+        if constexpr (has_list(KIND)) {
           __syncwarp();  // the places that the row names are written after the rest
           if (!zero) {
             const RowSplit split = split_of(logits_of(row_of(i)));
@@ -1369,7 +1391,7 @@ __global__ void __launch_bounds__(THREADS + 64, CTAS_PER_SM)
       }
       // the places that the row names are written after the rest, by the warp that has written there
       if (zero) continue;
-      if constexpr (KIND == kDistill) {
+      if constexpr (has_list(KIND)) {
         const TeacherList list = list_at(lists + static_cast<size_t>(i & 1) * list_bytes(p.K), p.K);
         __syncwarp();
         for (int k = lane; k < result.entries; k += 32) {
@@ -1401,7 +1423,7 @@ template <typename T, int KIND, int THREADS, int VPT, int CTAS_PER_SM, bool WHOL
 cudaError_t launch_parts_of(const RowLossParams& p, PartShape shape, cudaStream_t s) {
   constexpr auto kernel = row_loss_parts_kernel<T, KIND, THREADS, VPT, CTAS_PER_SM, WHOLE>;
   constexpr size_t kLargest = 216 * 1024;  // with what is not dynamic, an SM's shared memory
-  const size_t lists = KIND == kDistill ? 2 * list_bytes(p.K) + table_slots(p.K) * 4 : 0;
+  const size_t lists = has_list(KIND) ? 2 * list_bytes(p.K) + table_slots(p.K) * 4 : 0;
   const size_t room = kLargest / CTAS_PER_SM - 4096;  // less what is not part_memory
   shape.slot_bytes = (shape.seg_vecs * 16 + 127) & ~127;
   shape.slots = static_cast<int>(room > lists ? (room - lists) / shape.slot_bytes : 1);
@@ -1458,11 +1480,15 @@ cudaError_t launch_parts(const RowLossParams& p, const PartShape& shape, cudaStr
                : launch_parts_of<T, KIND, THREADS, VPT, CTAS_PER_SM, false>(p, shape, s);
 }
 
-// Rows of up to 256 vectors (4 KB) by warps; then by parts of up to 2048 vectors (32 KB) by 256
-// threads, three CTAs an SM; rows of more than eight of these by parts of up to 4096, two
-// CTAs an SM; and what is longer is read twice.  For a teacher's list, which every CTA of a
-// row reads, the larger parts from more than four on: bf16 [4096, 128256] 350 -> 325 us (but
-// fp32 [1999, 32001], of four parts, 86 -> 94; the policy loss on [4096, 128256] 328 -> 344).
+// Rows of up to 256 vectors (4 KB) by warps (of 512, bf16 [32768, 4096]: 151 us, by parts 154,
+// no gain worth a kernel); then by parts of up to 2048 vectors (32 KB) by 256 threads, three
+// CTAs an SM; rows of more than eight of these by parts of up to 4096, two CTAs an SM; and what
+// is longer is read twice.  For a teacher's list, which every CTA of a row reads, the larger
+// parts from more than four on: bf16 [4096, 128256] 350 -> 325 us (but fp32 [1999, 32001], of
+// four parts, 86 -> 94; the policy loss on [4096, 128256] 328 -> 344).  Lists of more than 64
+// entries are what takes time themselves: fewest CTAs a row, and kernels of their own, whose
+// registers are the list's (bf16 [4096, 32768] with 256 entries 239 -> 134 us, [2048, 128256]
+// with 1000 1039 -> 424).
 template <typename T, int KIND>
 cudaError_t launch_rows_of(const RowLossParams& p, cudaStream_t s) {
   const int64_t vecs = p.V / kVecElems<T>;
@@ -1471,13 +1497,13 @@ cudaError_t launch_rows_of(const RowLossParams& p, cudaStream_t s) {
   if (vecs <= 32) return launch_warps<T, KIND, 1>(p, s);
   if (vecs <= 128) return launch_warps<T, KIND, 4>(p, s);
   if (vecs <= 256) return launch_warps<T, KIND, 8>(p, s);
-  const bool wide = vecs > (KIND == kDistill ? 4 : 8) * 2048;
+  const bool wide = KIND == kDistillLong ? vecs > 1024 : vecs > (KIND == kDistill ? 4 : 8) * 2048;
   shape.cluster = 1;
   while (div_up(vecs, shape.cluster) > (wide ? 4096 : 2048)) shape.cluster *= 2;
   shape.seg_vecs = static_cast<int>(div_up(vecs, shape.cluster));
-  if (shape.seg_vecs <= 512) return launch_parts<T, KIND, 256, 2, 3>(p, shape, s);
-  if (shape.seg_vecs <= 1024) return launch_parts<T, KIND, 256, 4, 3>(p, shape, s);
-  if (shape.seg_vecs <= 2048) return launch_parts<T, KIND, 256, 8, 3>(p, shape, s);
+  if (shape.seg_vecs <= 1024 && !wide) return launch_parts<T, KIND, 256, 4, 3>(p, shape, s);
+  if constexpr (KIND != kDistillLong)
+    if (shape.seg_vecs <= 2048 && !wide) return launch_parts<T, KIND, 256, 8, 3>(p, shape, s);
   return launch_parts<T, KIND, 256, 16, 2>(p, shape, s);
 }
 
@@ -1486,7 +1512,7 @@ template <int KIND>
 cudaError_t launch_rows(const RowLossParams& given, int dtype, cudaStream_t s) {
   RowLossParams p = given;
   // every CTA counts all rows' targets itself where that is less than a launch takes
-  const bool self_count = p.N <= (KIND == kDistill ? 512 : 2048);
+  const bool self_count = p.N <= (has_list(KIND) ? 512 : 2048);
   if (p.reduction != FLCE_REDUCTION_MEAN || KIND == kStats || self_count) {
     p.counts = nullptr;
   } else {
