@@ -758,7 +758,9 @@ __device__ __forceinline__ void store_result(const RowLossParams& p, int64_t row
 
 // ---------------------------------------------------------------- rows of any length
 
-// One CTA a row, which reads it twice.  For rows that the form by parts does not hold.
+// One CTA a row, which reads it twice: for rows that the form by parts does not hold (more
+// than 512 KB).  Two readings and a write bound it: fp32 [1000, 256000] 539 us, of which L2
+// gives some of the second reading (301 would be one reading at the copy rate).
 constexpr int kLongThreads = 512;
 constexpr int kLongVecs = 4;
 
@@ -886,14 +888,18 @@ cudaError_t launch_long(const RowLossParams& p, cudaStream_t s) {
 
 // ---------------------------------------------------------------- short rows
 
-// A warp a row, which it holds in registers: rows of up to 256 vectors.
-constexpr int kRowWarps = 8;
+// A warp a row, which it holds in registers: rows of up to 512 vectors.  Bound by what a row
+// costs beside its elements: bf16 [65536, 2048] 115 us against 79 at the copy rate, [32768,
+// 4096] 120 against 79.  CTAs of eight warps, but of four where a thread's 16 vectors take 168
+// registers, of which an SM has room for 12 warps (with eight: 152 us; four for eight vectors
+// made fp32 [65536, 1000] 92 -> 110).
+constexpr int row_warps(int vecs) { return vecs > 8 ? 4 : 8; }
 
 template <typename T, int KIND, int VPT>
-__global__ void __launch_bounds__(32 * kRowWarps) row_loss_warps_kernel(const RowLossParams p) {
+__global__ void __launch_bounds__(32 * row_warps(VPT)) row_loss_warps_kernel(const RowLossParams p) {
   extern __shared__ __align__(16) uint8_t list_memory[];
   constexpr int kE = kVecElems<T>;
-  __shared__ double losses[kRowWarps];
+  __shared__ double losses[row_warps(VPT)];
   __shared__ int count, all_bits;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, warps = blockDim.x >> 5;
   const size_t each = has_list(KIND) ? list_bytes(p.K) + table_slots(p.K) * 4 : 0;
@@ -982,7 +988,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) row_loss_warps_kernel(const Ro
 template <typename T, int KIND, int VPT>
 cudaError_t launch_warps(const RowLossParams& p, cudaStream_t s) {
   const size_t each = has_list(KIND) ? list_bytes(p.K) + table_slots(p.K) * 4 : 0;
-  int warps = kRowWarps;  // fewer where the lists are long, or the rows few
+  int warps = row_warps(VPT);  // fewer where the lists are long, or the rows few
   while (warps > 1 && (warps * each > 40 * 1024 || div_up(p.N, warps) < device_sm_count())) warps /= 2;
   const int64_t ctas = div_up(p.N, warps), most = 8 * device_sm_count();
   cudaLaunchConfig_t cfg = {};
@@ -1017,6 +1023,12 @@ cudaError_t launch_warps(const RowLossParams& p, cudaStream_t s) {
 // itself, as z c - r is one operation, so that a common level takes no digits.  Where m c
 // leaves the range that this holds in (|m c| >= 2^100), any two different logits are
 // infinitely far apart: the warp replaces its z by z - m, and r by 0.
+//
+// Bound by memory where rows are many and long: bf16 [4096, 128256] 328 us for the policy loss
+// and as much for a teacher's 64 entries, 94 % of the copy rate; fp32 [1000, 50257] 72 us, 82 %,
+// as its last rows leave half of the SMs idle.  Rows of 8 to 32 KB cost their exchange of sums
+// and the closer's arithmetic, 60 to 80 % of the copy rate.  Few rows cost what one does: bf16
+// [1, 128256] 10.9 us, [256, 1024] (by warps) 7.9 on the GPU.
 constexpr int kPartSlots = 4;
 constexpr float kFarExponent = 1.2676506002282294e30f;  // 2^100
 
@@ -1427,10 +1439,12 @@ cudaError_t launch_parts_of(const RowLossParams& p, PartShape shape, cudaStream_
   const size_t room = kLargest / CTAS_PER_SM - 4096;  // less what is not part_memory
   shape.slot_bytes = (shape.seg_vecs * 16 + 127) & ~127;
   shape.slots = static_cast<int>(room > lists ? (room - lists) / shape.slot_bytes : 1);
-  if (shape.slots > kPartSlots) shape.slots = kPartSlots;
   // where gradients are written, one part ahead: with two, more reads among the writes made
   // memory slower (policy loss, bf16 [4096, 128256], 341 -> 328 us; fp32 [1000, 50257] 74 -> 73)
-  if (shape.slots < 1 || p.grad != nullptr) shape.slots = 1;
+  // (short parts beside lists: two, bf16 [16384, 8192] 131 -> 122 us)
+  const int most = p.grad == nullptr ? kPartSlots : has_list(KIND) && shape.slot_bytes <= 16384 ? 2 : 1;
+  if (shape.slots > most) shape.slots = most;
+  if (shape.slots < 1) shape.slots = 1;
   const size_t smem = static_cast<size_t>(shape.slots) * shape.slot_bytes + lists;
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(THREADS + 64);
@@ -1480,9 +1494,9 @@ cudaError_t launch_parts(const RowLossParams& p, const PartShape& shape, cudaStr
                : launch_parts_of<T, KIND, THREADS, VPT, CTAS_PER_SM, false>(p, shape, s);
 }
 
-// Rows of up to 256 vectors (4 KB) by warps (of 512, bf16 [32768, 4096]: 151 us, by parts 154,
-// no gain worth a kernel); then by parts of up to 2048 vectors (32 KB) by 256 threads, three
-// CTAs an SM; rows of more than eight of these by parts of up to 4096, two CTAs an SM; and what
+// Rows of up to 512 vectors (8 KB) by warps (bf16 [32768, 4096] 120 us, by parts 192; of 1024
+// vectors, [32768, 8192], 259 and 194); then by parts of up to 2048 vectors (32 KB) by 256
+// threads, three CTAs an SM; rows of more than eight of these by parts of up to 4096, two CTAs an SM; and what
 // is longer is read twice.  For a teacher's list, which every CTA of a row reads, the larger
 // parts from more than four on: bf16 [4096, 128256] 350 -> 325 us (but fp32 [1999, 32001], of
 // four parts, 86 -> 94; the policy loss on [4096, 128256] 328 -> 344).  Lists of more than 64
@@ -1497,6 +1511,7 @@ cudaError_t launch_rows_of(const RowLossParams& p, cudaStream_t s) {
   if (vecs <= 32) return launch_warps<T, KIND, 1>(p, s);
   if (vecs <= 128) return launch_warps<T, KIND, 4>(p, s);
   if (vecs <= 256) return launch_warps<T, KIND, 8>(p, s);
+  if (vecs <= 512) return launch_warps<T, KIND, 16>(p, s);
   const bool wide = KIND == kDistillLong ? vecs > 1024 : vecs > (KIND == kDistill ? 4 : 8) * 2048;
   shape.cluster = 1;
   while (div_up(vecs, shape.cluster) > (wide ? 4096 : 2048)) shape.cluster *= 2;
