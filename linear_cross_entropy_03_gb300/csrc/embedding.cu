@@ -633,10 +633,13 @@ __global__ void __launch_bounds__(32 * kSumWarps, 6) embedding_sum_kernel(const 
 
 constexpr int kJoinWarps = 8;
 constexpr int kJoinTiles = 8;
+constexpr int kJoinBatch = 64;
 
 // Adds up the partial rows of ids that begin in a tile and go on past the next one, in the
-// order of the tiles: each warp a stretch of them, then the warps' sums.  A CTA has 32 * E
-// columns and looks for such ids in kJoinTiles tiles at a time, one a lane.
+// order of the tiles: each warp a stretch of them by batches, then the warps' sums, so that no
+// chain of additions is long (3 * 2^20 equal rows of one id, without batches: off by 1e-4 of
+// the sum).  A CTA has 32 * E columns and looks for such ids in kJoinTiles tiles at a time,
+// one a lane.
 template <int E>
 __global__ void __launch_bounds__(32 * kJoinWarps) embedding_join_kernel(const SumParams p) {
   using Part = Elems<float, E>;
@@ -666,12 +669,18 @@ __global__ void __launch_bounds__(32 * kJoinWarps) embedding_join_kernel(const S
       Part sum = {};
       if (h < p.H) {
         const int to = (warp + 1) * each < parts ? (warp + 1) * each : parts;
+        for (int i0 = warp * each; i0 < to; i0 += kJoinBatch) {
+          Part batch = {};
+          const int end = i0 + kJoinBatch < to ? i0 + kJoinBatch : to;
 #pragma unroll 8
-        for (int i = warp * each; i < to; ++i) {
-          const Part v =
-              *reinterpret_cast<const Part*>(p.partial + (static_cast<int64_t>(tile + i) * 2 + (i == 0)) * p.H + h);
+          for (int i = i0; i < end; ++i) {
+            const Part v =
+                *reinterpret_cast<const Part*>(p.partial + (static_cast<int64_t>(tile + i) * 2 + (i == 0)) * p.H + h);
 #pragma unroll
-          for (int k = 0; k < E; ++k) sum.v[k] += v.v[k];
+            for (int k = 0; k < E; ++k) batch.v[k] += v.v[k];
+          }
+#pragma unroll
+          for (int k = 0; k < E; ++k) sum.v[k] += batch.v[k];
         }
       }
       sums[warp][lane] = sum;

@@ -172,6 +172,18 @@ def test_gradient_is_the_same_every_time():
         assert torch.equal(flce.embedding_backward(gy, ids, 400)["grad_weight"], first)
 
 
+@pytest.mark.parametrize("value", [0.1, 0.7, 3.14159])
+def test_gradient_of_one_id_over_millions_of_tokens(value):
+    """The longest chain: 32 tokens of a tile, 64 tiles of a batch, 192 batches of a warp, 8
+    warps; each addition rounds by 2^-24 of a sum that is at most the whole."""
+    n = 3 * 2 ** 20
+    gy = torch.full((n, 4), value, dtype=torch.float32, device="cuda")
+    out = flce.embedding_backward(gy, torch.full((n,), 2, device="cuda"), 5)["grad_weight"]
+    want = n * float(np.float32(value))
+    assert (out[2].double() / want - 1).abs().max() <= (32 + 64 + 192 + 8) * 2.0 ** -24
+    assert (out[[0, 1, 3, 4]] == 0).all()
+
+
 def test_gradient_in_a_dirty_workspace():
     gy = table_of(5000, 64, "bf16", 1)
     size = flce.embedding_workspace_size(5000, 2000, 64)
