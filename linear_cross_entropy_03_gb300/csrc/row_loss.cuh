@@ -763,6 +763,7 @@ __device__ __forceinline__ void store_result(const RowLossParams& p, int64_t row
 // gives some of the second reading (301 would be one reading at the copy rate).
 constexpr int kLongThreads = 512;
 constexpr int kLongVecs = 4;
+constexpr int kLongBatch = 64;  // steps whose sums are added up before they join the rest, for short chains
 
 template <typename T, int KIND>
 __global__ void __launch_bounds__(kLongThreads) row_loss_long_kernel(const RowLossParams p) {
@@ -810,6 +811,8 @@ __global__ void __launch_bounds__(kLongThreads) row_loss_long_kernel(const RowLo
     if (tid < split.head) m = to_float(x[tid]), s = 1.f;
     if (tid >= 32 && tid < 32 + split.tail) m = to_float(tail[tid - 32]), s = 1.f;
     if (s == 1.f && !(m > -INFINITY)) s = m == m ? 0.f : m;  // -inf adds nothing, NaN stays
+    float whole = 0.f;  // of the batches of kLongBatch steps that are done, by the same m
+    int step = 0;
     for (int64_t at = tid; at < split.vecs; at += kLongThreads * kLongVecs) {
       uint4 v[kLongVecs];
 #pragma unroll
@@ -823,10 +826,13 @@ __global__ void __launch_bounds__(kLongThreads) row_loss_long_kernel(const RowLo
 #pragma unroll
       for (int i = 0; i < kLongVecs; ++i) vec_add_exp<T>(v[i], pair(-shift), c, sum);
       const float2 both = unpair(sum);
-      s = (m > -INFINITY ? s * ex2_approx((m - shift) * p.c) : s) + (both.x + both.y);
+      const float less = m > -INFINITY ? ex2_approx((m - shift) * p.c) : 1.f;
+      s = s * less + (both.x + both.y);
+      whole *= less;
       m = top;
+      if (++step % kLongBatch == 0) whole += s, s = 0.f;
     }
-    const float2 mine = combine_parts(m, s, p.c);
+    const float2 mine = combine_parts(m, s + whole, p.c);
     if (lane == 0) parts[warp] = mine;
     __syncthreads();
     const float2 part = lane < kWarps ? parts[lane] : make_float2(-INFINITY, 0.f);

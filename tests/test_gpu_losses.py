@@ -231,6 +231,20 @@ def test_policy_leading_dimensions_and_no_gradient():
     assert none["grad_logits"] is None and torch.equal(none["loss"], want["loss"])
 
 
+@pytest.mark.parametrize("rest", [-0.3, -0.1])
+def test_policy_sum_over_a_row_of_millions(rest):
+    """One column of 0 and 2^26 - 1 equal ones.  A thread adds 16 terms, 64 steps of those, 128
+    batches, and 512 threads are joined; ln S is off by these roundings and the exponent's 2^-21."""
+    v = 2 ** 26
+    z = torch.full((1, v), rest, dtype=torch.float32, device="cuda")
+    z[0, 12345] = 0
+    out = flce.policy_loss(z, torch.tensor([12345], device="cuda"), torch.ones(1, device="cuda"), want_grad=False,
+                           reduction="none")
+    want = -math.log((v - 1) * math.exp(float(np.float32(rest))) + 1)
+    tol = (16 + 64 + 128 + 16 + 8) * 2.0 ** -24 + 2.0 ** -21 + abs(want) * 2.0 ** -23
+    assert abs(float(out["logp"][0]) - want) <= tol
+
+
 # ------------------------------------------------------------ distillation
 
 def teacher(n, v, k, seed, id_type=np.int64):
