@@ -12,8 +12,9 @@
 //
 // so a row is read, reduced to (M, S) and written as f p, but for the few places that the
 // target or the teacher's list names.  Everything between loading and storing is fp32,
-// sums over rows are fp64.  Differences z - M are formed before they are scaled, so that
-// logits about any common level keep their digits.
+// sums over rows are fp64.  Logits about any common level keep their digits: differences
+// z - M are formed before they are scaled (rows by warps, rows that are read twice), or in
+// the operation that scales (rows by parts, below kFarExponent).
 #pragma once
 
 #include <atomic>
@@ -1026,9 +1027,13 @@ cudaError_t launch_warps(const RowLossParams& p, cudaStream_t s) {
 //             elements before the row's first vector and after its last
 //
 // Exponents here are x = z c - r with c = log2(e) / T and r = m c rounded: one rounding, of x
-// itself, as z c - r is one operation, so that a common level takes no digits.  Where m c
-// leaves the range that this holds in (|m c| >= 2^100), any two different logits are
-// infinitely far apart: the warp replaces its z by z - m, and r by 0.
+// itself, as z c - r is one operation, so that a common level takes no digits.  At z = m this
+// leaves x = m c - r, up to half a unit in the last place of r, for the sums' last step to take
+// out: 2^-5 below |m c| = 2^20, which harms nothing, but from 2^31 on 2^x would overflow or
+// vanish.  So a warp whose |m c| is 2^20 and more (far_exponent) replaces its z by z - m, and r by
+// 0.  That rounds nothing that has a share: an fp32 difference is exact unless it is 2^19 and more
+// in x, and different 16-bit logits are 2^9 and more apart.  A row's warps may be of both kinds,
+// also about one maximum: what joins them looks at the kind of each.
 //
 // Bound by memory where rows are many and long: bf16 [4096, 128256] 328 us for the policy loss
 // and as much for a teacher's 64 entries, 94 % of the copy rate; fp32 [1000, 50257] 72 us, 82 %,
@@ -1036,7 +1041,7 @@ cudaError_t launch_warps(const RowLossParams& p, cudaStream_t s) {
 // and the closer's arithmetic, 60 to 80 % of the copy rate.  Few rows cost what one does: bf16
 // [1, 128256] 10.9 us, [256, 1024] (by warps) 7.9 on the GPU.
 constexpr int kPartSlots = 4;
-constexpr float kFarExponent = 1.2676506002282294e30f;  // 2^100
+constexpr float kFarExponent = 1048576.f;  // 2^20
 
 struct PartShape {
   int cluster;    // CTAs of a row
@@ -1275,9 +1280,13 @@ __global__ void __launch_bounds__(THREADS + 64, CTAS_PER_SM)
       float sum = 0.f;
       for (int k = lane; k < cluster * kSums; k += 32) {
         const float2 q = parts[b][k];
-        // a warp's sum goes by its own rounded exponent; warps that have found nothing have 0, or NaN
-        const float scaled = q.y * ex2_approx(far ? (q.x == m ? 0.f : -INFINITY) : __fmul_rn(q.x, p.c) - r);
-        sum += q.x > -INFINITY ? scaled : q.y;
+        // a warp's sum goes by its own maximum, or by that one's rounded exponent; warps that have found nothing
+        // have 0, or NaN
+        const float r_q = __fmul_rn(q.x, p.c);
+        const bool far_q = far_exponent(q.x, p.c);
+        const float by = far ? (far_q ? (q.x - m) * p.c : fmaf(-m, p.c, r_q))
+                             : (far_q ? fmaf(q.x, p.c, -r) : r_q - r);
+        sum += q.x > -INFINITY ? q.y * ex2_approx(by) : q.y;
       }
       sum = warp_sum(sum);                                        // of 2^(z c - r)
       const float s = far ? sum : sum * ex2_approx(fmaf(-m, p.c, r));  // of 2^((z - m) c)
@@ -1354,7 +1363,7 @@ __global__ void __launch_bounds__(THREADS + 64, CTAS_PER_SM)
 #pragma unroll
         for (int k = 0; k < VPT; ++k) vec_subtract<T>(v[k], m);
       }
-      float r = far || !(m > -INFINITY) ? 0.f : __fmul_rn(m, p.c);
+      const float r = far || !(m > -INFINITY) ? 0.f : __fmul_rn(m, p.c);
       Pair sum = pair(0.f);
 #pragma unroll
       for (int k = 0; k < VPT; ++k) {
@@ -1378,10 +1387,20 @@ __global__ void __launch_bounds__(THREADS + 64, CTAS_PER_SM)
       if (p.grad == nullptr || !alive) continue;
       const PartResult result = results[b];
       const bool zero = result.f == 0.f;
-      // a warp that has taken its own maximum off: the row's, or far below it
-      r = !far ? result.r : m == result.m ? 0.f : INFINITY;
-      if (!far && far_exponent(result.m, p.c)) r = result.m > 0.f ? INFINITY : 0.f;
-      const Pair minus_r = pair(-r), factor = pair(result.factor);
+      // the factor goes by the row's exponent, or by its maximum itself where that is far; z - m by the warp's
+      float by = -result.r, scale = result.factor;
+      if (far_exponent(result.m, p.c)) {
+        const float taken = __fmul_rn(result.m, p.c);
+        if (far)
+          by = (m - result.m) * p.c;
+        else if (fabsf(taken) < 2.f * kFarExponent)
+          by = -taken, scale *= ex2_approx(fmaf(-result.m, p.c, taken));
+        else
+          by = result.m > 0.f ? -INFINITY : 0.f;  // the warp lies 2^20 lower, or has -inf alone
+      } else if (far) {
+        by = fmaf(m, p.c, -result.r);
+      }
+      const Pair minus_r = pair(by), factor = pair(scale);
       T* to = g + split.head + (static_cast<int64_t>(first_vec) + tid) * kE;
       // the 16-bit elements are widened again: kept from the sum, they would not fit in the registers
 #pragma unroll
