@@ -624,7 +624,9 @@ size_t row_loss_workspace_size(int64_t N);
  *                            + kl_weight (exp(d) - 1 - d) ),  d = ref_logp - logp
  *  MEAN divides by the number of rows that take part (NaN if there is none),
  *  whatever their weights.  Where the cut ratio is taken the first term has no
- *  gradient.
+ *  gradient.  A ratio that is not cut, or an exp(d), beyond the range of fp32
+ *  makes its row's loss infinite and its gradients infinite or NaN; an advantage
+ *  of 0 takes no ratio.
  *
  *  target        int64 [N]; one outside [0, V) that is not ignore_index sets
  *                FLCE_STATUS_BIT_TARGET_RANGE, and its row takes no part.

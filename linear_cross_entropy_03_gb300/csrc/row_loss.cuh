@@ -18,6 +18,7 @@
 #pragma once
 
 #include <atomic>
+#include <cfloat>
 #include <type_traits>
 
 #include "arrival.cuh"
@@ -640,8 +641,10 @@ __device__ __forceinline__ RowResult row_result(const RowLossParams& p, const Ro
     const float a = r.advantage;
     const float ratio = p.old_logp != nullptr ? expf(out.logp - r.old_logp) : 1.f;
     const bool over = a > 0.f && ratio > p.ratio_high, under = a < 0.f && ratio < p.ratio_low;
-    float loss = -a * (over ? p.ratio_high : under ? p.ratio_low : ratio);
-    float slope = over || under ? 0.f : -a * ratio;
+    // an advantage of 0 takes nothing of a ratio that fp32 holds as infinite (NaN stays)
+    const float gain = a == 0.f && ratio > FLT_MAX ? 0.f : a * ratio;
+    float loss = over ? -a * p.ratio_high : under ? -a * p.ratio_low : -gain;
+    float slope = over || under ? 0.f : -gain;
     if (p.kl_weight != 0.f) {
       const float d = r.ref_logp - out.logp, x = expm1f(d);
       loss += p.kl_weight * (x - d);
