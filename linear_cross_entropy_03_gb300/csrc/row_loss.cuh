@@ -639,7 +639,8 @@ __device__ __forceinline__ RowResult row_result(const RowLossParams& p, const Ro
     out.logp = (r.zt - m) * p.inv_t - ln_s;
     if (KIND == kStats || r.weight == 0.f) return out;
     const float a = r.advantage;
-    const float ratio = p.old_logp != nullptr ? expf(out.logp - r.old_logp) : 1.f;
+    // fresh samples have a ratio of 1, but a row of no number has none
+    const float ratio = p.old_logp != nullptr ? expf(out.logp - r.old_logp) : isnan(out.logp) ? out.logp : 1.f;
     const bool over = a > 0.f && ratio > p.ratio_high, under = a < 0.f && ratio < p.ratio_low;
     // an advantage of 0 takes nothing of a ratio that fp32 holds as infinite (NaN stays)
     const float gain = a == 0.f && ratio > FLT_MAX ? 0.f : a * ratio;

@@ -30,3 +30,23 @@ def test_an_advantage_of_zero_takes_no_ratio(dtype, v, reference):
     assert got["loss"].isfinite() and got["grad_logits"].isfinite().all()
     if not reference:
         assert (got["grad_logits"][:4] == 0).all()
+
+
+@pytest.mark.parametrize("v", [700, 9000, 70001, 290000])
+@pytest.mark.parametrize("clip", [0.2, math.inf])
+def test_rows_of_no_number_on_fresh_samples(v, clip):
+    """Without old log-probabilities a row with NaN or infinity has a loss of NaN as well, and no other has."""
+    z = make_logits(8, v, "bf16", v)
+    t = np.arange(8)
+    z[1, 300], z[2, 301], z[3] = float("nan"), float("inf"), float("-inf")
+    z[4, 4] = float("-inf")                        # a target of no probability: the ratio is 1
+    z[5, 5] = float("nan")                         # the target itself
+    t[7], z[7] = -100, float("nan")
+    a = torch.tensor([1.0, 2, -1, 1, 1.5, 0, 2, 1], device="cuda")
+    out = flce.policy_loss(z, cuda(t), a, clip=clip, reduction="none")
+    bad, good = [1, 2, 3, 5], [0, 4, 6, 7]
+    assert out["loss"][bad].isnan().all() and out["grad_logits"][bad].isnan().all()
+    assert torch.equal(out["loss"][good], -a[good] * torch.tensor([1.0, 1, 1, 0], device="cuda"))
+    assert out["grad_logits"][good].isfinite().all() and (out["grad_logits"][7] == 0).all()
+    mean = flce.policy_loss(z, cuda(t), a, clip=clip)
+    assert mean["loss"].isnan()
