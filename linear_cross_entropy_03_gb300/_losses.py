@@ -114,7 +114,7 @@ def policy_loss(logits, target, advantage, *, old_logp=None, ref_logp=None, clip
 
     logits [..., V] bf16, fp16 or fp32, rows contiguous and one stride apart;
     target [...] int64; advantage, old_logp, ref_logp and row_weight [...] fp32,
-    contiguous.  Without old_logp the ratio is 1 and its gradient that of logp;
+    contiguous, of the logits' leading dimensions (or either of them flat).  Without old_logp the ratio is 1 and its gradient that of logp;
     without clip_high it is clip; infinity does not cut; temperature lies in
     [1e-4, 1e4].  row_weight multiplies a
     row's loss; "mean" divides by the rows that take part, whatever their weights.

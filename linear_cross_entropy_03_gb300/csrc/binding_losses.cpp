@@ -23,6 +23,17 @@ at::Tensor first_word(const at::Tensor& workspace) {
   return at::Tensor(std::move(impl));
 }
 
+// Whether a tensor of as many elements as `shape` has them in the same order: both are alike
+// but for dimensions of one element, or one of them is flat.
+bool in_order(at::IntArrayRef sizes, at::IntArrayRef shape) {
+  c10::SmallVector<int64_t, 6> a, b;
+  for (const int64_t n : sizes)
+    if (n != 1) a.push_back(n);
+  for (const int64_t n : shape)
+    if (n != 1) b.push_back(n);
+  return a.size() <= 1 || b.size() <= 1 || a == b;
+}
+
 // What the losses on logits take and return alike.
 struct Call {
   const char* name;
@@ -68,21 +79,35 @@ struct Call {
     if (buffer != nullptr && !like(*buffer, *logits, name, &ld_grad, "logits")) return false;
     if (status != nullptr && (status->scalar_type() != at::kInt || status->numel() != 1))
       return bad(FLCE_ERR_INVALID_ARG, "status: one int32 element is wanted"), false;
-    if (grad_out != nullptr && !floats_of(*grad_out, losses(), name)) return false;
-    return true;
+    if (losses_of_none >= 0) return list_floats(grad_out, {1, losses_of_none}, "grad_out");
+    return row_floats(grad_out, "grad_out");
   }
 
   int64_t losses_of_none = -1;  // where they are not the rows
-  int64_t losses() const { return losses_of_none >= 0 ? losses_of_none : rows.n; }
 
-  // a vector with an element for each row
-  bool row_floats(const at::Tensor* t) const { return t == nullptr || floats_of(*t, rows.n, name); }
+  // floats of a shape that is not the rows'
+  bool list_floats(const at::Tensor* t, at::IntArrayRef shape, const char* what) const {
+    if (t == nullptr || (t->scalar_type() == at::kFloat && t->is_contiguous() && t->numel() == c10::multiply_integers(shape) &&
+                         in_order(t->sizes(), shape)))
+      return true;
+    return fail(FLCE_ERR_INVALID_ARG, "%s: %s: a contiguous fp32 vector of %lld elements is wanted", name, what,
+                static_cast<long long>(c10::multiply_integers(shape))), false;
+  }
 
+  // an element for each row
+  bool row_floats(const at::Tensor* t, const char* what) const {
+    if (t == nullptr || (t->scalar_type() == at::kFloat && of_rows(*t))) return true;
+    return fail(FLCE_ERR_INVALID_ARG, "%s: %s: a contiguous fp32 tensor of the logits' shape without the last "
+                "dimension is wanted", name, what), false;
+  }
   bool row_targets(const at::Tensor& t) const {
     if (t.scalar_type() != at::kLong) return bad(FLCE_ERR_UNSUPPORTED, "target: int64 is wanted"), false;
-    if (t.numel() != rows.n || !t.is_contiguous())
-      return bad(FLCE_ERR_INVALID_ARG, "target: a contiguous tensor with one element a row is wanted"), false;
-    return true;
+    if (of_rows(t)) return true;
+    return bad(FLCE_ERR_INVALID_ARG, "target: a contiguous tensor of the logits' shape without the last dimension is "
+               "wanted"), false;
+  }
+  bool of_rows(const at::Tensor& t) const {
+    return t.is_contiguous() && t.numel() == rows.n && in_order(t.sizes(), row_shape());
   }
 
   at::IntArrayRef row_shape() const { return logits->sizes().slice(0, logits->dim() - 1); }
@@ -131,8 +156,8 @@ PyObject* policy_loss(PyObject*, PyObject* const* a, Py_ssize_t count) {
   numbers.temperature = static_cast<float>(PyFloat_AsDouble(a[17]));
   const int64_t ignore_index = PyLong_AsLongLong(a[18]);
   if (PyErr_Occurred()) return nullptr;
-  if (!c.row_targets(*target) || !c.row_floats(advantage) || !c.row_floats(old_logp) || !c.row_floats(ref_logp) ||
-      !c.row_floats(weight))
+  if (!c.row_targets(*target) || !c.row_floats(advantage, "advantage") || !c.row_floats(old_logp, "old_logp") ||
+      !c.row_floats(ref_logp, "ref_logp") || !c.row_floats(weight, "row_weight"))
     return nullptr;
   const size_t size = row_loss_workspace_size(c.rows.n);
   if (size == 0) return c.bad(FLCE_ERR_INVALID_ARG, "too many rows");
@@ -168,7 +193,7 @@ PyObject* distillation_loss(PyObject*, PyObject* const* a, Py_ssize_t count) {
   if (top < 1 || ids->sizes() != values->sizes() || ids->dim() != c.logits->dim() ||
       ids->sizes().slice(0, ids->dim() - 1) != c.row_shape() || !ids->is_contiguous() || !values->is_contiguous())
     return c.bad(FLCE_ERR_INVALID_ARG, "teacher: contiguous ids and logits, a list for each row, are wanted");
-  if (!c.row_floats(weight)) return nullptr;
+  if (!c.row_floats(weight, "row_weight")) return nullptr;
   const size_t size = row_loss_workspace_size(c.rows.n);
   if (size == 0) return c.bad(FLCE_ERR_INVALID_ARG, "too many rows");
   c.allocate(static_cast<int64_t>(size), c.row_shape());
@@ -213,8 +238,7 @@ PyObject* preference_loss(PyObject*, PyObject* const* a, Py_ssize_t count) {
   numbers.average = flag(a[16]) ? 1 : 0;
   const int64_t ignore_index = PyLong_AsLongLong(a[17]);
   if (PyErr_Occurred()) return nullptr;
-  if (!c.row_targets(*target) || (ref_logp != nullptr && !floats_of(*ref_logp, sequences, "preference_loss: ref_logp")))
-    return nullptr;
+  if (!c.row_targets(*target) || !c.list_floats(ref_logp, {2, sequences / 2}, "ref_logp")) return nullptr;
   const size_t size = preference_workspace_size(c.rows.n, sequences / 2);
   if (size == 0) return c.bad(FLCE_ERR_INVALID_ARG, "too many rows");
   c.allocate(static_cast<int64_t>(size), {sequences / 2});
