@@ -114,10 +114,11 @@ def policy_loss(logits, target, advantage, *, old_logp=None, ref_logp=None, clip
 
     logits [..., V] bf16, fp16 or fp32, rows contiguous and one stride apart;
     target [...] int64; advantage, old_logp, ref_logp and row_weight [...] fp32,
-    contiguous, of the logits' leading dimensions (or either of them flat).  Without old_logp the ratio is 1 and its gradient that of logp;
-    without clip_high it is clip; infinity does not cut; temperature lies in
-    [1e-4, 1e4].  row_weight multiplies a
-    row's loss; "mean" divides by the rows that take part, whatever their weights.
+    contiguous, of the logits' leading dimensions (or either of them flat).
+    Without old_logp the ratio is 1 and its gradient that of logp; a kl_weight
+    other than 0 wants ref_logp; without clip_high it is clip; infinity does not
+    cut; temperature lies in [1e-4, 1e4].  row_weight multiplies a row's loss;
+    "mean" divides by the rows that take part, whatever their weights.
     Returns a dict with ``loss``, ``grad_logits`` (or None), ``logp`` (fp32, 0 for
     ignored rows: the next update's old_logp) and ``status``: the one that was
     given, which bits are added to, or the workspace's own, which is this call's

@@ -159,6 +159,8 @@ PyObject* policy_loss(PyObject*, PyObject* const* a, Py_ssize_t count) {
   if (!c.row_targets(*target) || !c.row_floats(advantage, "advantage") || !c.row_floats(old_logp, "old_logp") ||
       !c.row_floats(ref_logp, "ref_logp") || !c.row_floats(weight, "row_weight"))
     return nullptr;
+  if (numbers.kl_weight != 0.f && ref_logp == nullptr && c.rows.n > 0)
+    return c.bad(FLCE_ERR_INVALID_ARG, "ref_logp: wanted where kl_weight is not 0");
   const size_t size = row_loss_workspace_size(c.rows.n);
   if (size == 0) return c.bad(FLCE_ERR_INVALID_ARG, "too many rows");
   c.allocate(static_cast<int64_t>(size), c.row_shape());

@@ -73,3 +73,9 @@ def test_flat_logits_take_what_has_their_rows(made):
     want = flce.policy_loss(z, t, f, row_weight=f)
     got = flce.policy_loss(z.view(B * T, V), t, f, row_weight=f)
     assert torch.equal(got["loss"], want["loss"]) and torch.equal(got["grad_logits"].view_as(z), want["grad_logits"])
+
+
+def test_a_term_without_its_reference_is_refused_by_name(made):
+    z, t, f = made
+    with pytest.raises(flce.FlceError, match="policy_loss: ref_logp"):
+        flce.policy_loss(z, t, f, old_logp=f, kl_weight=0.1)
