@@ -752,7 +752,7 @@ flce_status_t embedding_fwd(int dtype, const void* table, int64_t ld_table, cons
                             int index_type, int64_t N, int64_t V, int64_t H, float scale, void* y,
                             int64_t ld_y, int32_t* status_dev, flce_stream_t stream);
 
-/* Bytes of workspace embedding_bwd needs; 0 for invalid sizes. */
+/* Bytes of workspace embedding_bwd needs; 0 for sizes that it refuses. */
 size_t embedding_workspace_size(int64_t N, int64_t V, int64_t H);
 
 /*
@@ -760,7 +760,8 @@ size_t embedding_workspace_size(int64_t N, int64_t V, int64_t H);
  *     grad_table[v] = scale * sum of grad_y[n] over the tokens n with ids[n] = v
  *
  *  dtype          type of grad_y [N, H], rows ld_grad_y (>= 0) apart.
- *  N, V, H        N < 2^31 - 32, V < 2^31 - 1, H < 2^21.
+ *  N, V, H        N < 2^31 - 32, V < 2^31 - 1, H <= 2097120, and
+ *                 ceil(N / 32) * ceil(H / 128) <= 2^33 - 2^15 - 4.
  *  padding_index  tokens of this id add nothing; -1: none.
  *  grad_table     fp32 [V, H], contiguous.
  *  accumulate     0: every row is written (zeros where no token is); 1: added to,

@@ -348,7 +348,7 @@ PyObject* embedding_backward(PyObject*, PyObject* const* a, Py_ssize_t count) {
                                                                            : "vocabulary is wanted");
   }
   const size_t size = embedding_workspace_size(rows.n, v, rows.h);
-  if (size == 0) return fail(FLCE_ERR_INVALID_ARG, "embedding_workspace_size");
+  if (size == 0) return fail(FLCE_ERR_INVALID_ARG, "embedding_backward: no rows, or more rows or columns than it takes");
   const at::Tensor grad = out != nullptr ? *out : empty({v, rows.h}, at::kFloat, *gy);
   const bool given = ws != nullptr && ws->is_contiguous() && ws->nbytes() >= size;
   const at::Tensor scratch =

@@ -805,6 +805,12 @@ __global__ void __launch_bounds__(32 * kFewWarps) embedding_few_kernel(const Sum
   sum.store(p.table + key * p.H, first, p.H, p.scale, p.accumulate != 0);
 }
 
+// Whether the launches hold the tiles' pieces of a row (whether they go by vectors or not)
+// and the join's columns, 32 a CTA: 65535 of these.
+bool launches_hold(int64_t N, int64_t H) {
+  return div_up(div_up(N, kTile) * div_up(H, 128), kSumWarps) + 8 * 1024 < (int64_t(1) << 31) && div_up(H, 32) <= 65535;
+}
+
 struct EmbeddingLayout {
   size_t keys[2], tokens[2], hit, joins, partial, total;
 };
@@ -928,7 +934,7 @@ flce_status_t embedding_fwd(int dtype, const void* table, int64_t ld_table, cons
 
 size_t embedding_workspace_size(int64_t N, int64_t V, int64_t H) {
   EmbeddingLayout at;
-  return embedding_layout(N, V, H, &at) ? at.total : 0;
+  return embedding_layout(N, V, H, &at) && launches_hold(N, H) ? at.total : 0;
 }
 
 flce_status_t embedding_bwd(int dtype, const void* grad_y, int64_t ld_grad_y, const void* ids, int index_type,
@@ -951,11 +957,10 @@ flce_status_t embedding_bwd(int dtype, const void* grad_y, int64_t ld_grad_y, co
     if (a < b + static_cast<uintptr_t>(V) * H * 4 && b < a + ((N - 1) * ld_grad_y + H) * esz)
       return FLCE_ERR_INVALID_ARG;
   }
+  if (!launches_hold(N, H)) return FLCE_ERR_UNSUPPORTED;
   if (workspace == nullptr || !aligned_to(workspace, 256) || workspace_bytes < at.total) return FLCE_ERR_WORKSPACE;
   if (N == 0 && accumulate) return FLCE_OK;
   const int64_t tiles = div_up(N, kTile);
-  if (div_up(tiles * div_up(H, 128), kSumWarps) + 8 * 1024 >= (int64_t(1) << 31) || div_up(H, 32) > 65535)
-    return FLCE_ERR_UNSUPPORTED;  // more CTAs than a launch has
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream_);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
 
