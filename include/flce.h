@@ -721,6 +721,7 @@ size_t preference_workspace_size(int64_t N, int64_t pairs);
  *                sequences are then cut to what lies within.
  *  ref_logp      fp32 [2 pairs]: the reference model's s, or NULL (0).
  *  pairs         >= 0, < 2^30.
+ *  grad_logits   as above; N * ceil(V / 1024) < 2^31 unless it is NULL.
  *  loss          [pairs] for NONE.
  *  logp          fp32 [2 pairs] output or NULL: s.
  */

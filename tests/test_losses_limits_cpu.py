@@ -16,3 +16,15 @@ def test_embedding_sizes(dtype, n, v, h, code):
     assert (size > 0) == (code == WORKSPACE)
     far = dict(dtype=dtype, N=n, V=v, H=h, ld_grad_y=0, grad_y=FAKE, grad_table=FAR)
     assert _gradient(**far, workspace_bytes=max(size, 1) - 1) == code
+
+
+@pytest.mark.parametrize("n,v,grad,code", [
+    ((1 << 31) - 1, 1024, True, WORKSPACE), ((1 << 30) - 1, 2048, True, WORKSPACE), (1 << 30, 2048, True, UNSUPPORTED),
+    (1 << 30, 1025, True, UNSUPPORTED), (1 << 30, 2048, False, WORKSPACE), ((1 << 31) - 1, 1 << 20, False, WORKSPACE)])
+def test_preference_sizes(n, v, grad, code):
+    """Rows times pieces of 1024 columns below 2^31 where a gradient is wanted, as the header has it."""
+    size = flce.preference_workspace_size(n, 4)
+    assert size > 0
+    got = _preference(N=n, V=v, ld=v, ld_grad=v, grad_logits=1 << 62 if grad else None,
+                      workspace_bytes=size - (code == WORKSPACE))       # (what has room would be launched)
+    assert got == code
