@@ -9,6 +9,7 @@
 // than many rare ones.  A tile writes the sums of ids that lie within it; of an id that
 // goes on in the next tile it leaves a partial row, and a last kernel adds those up.
 #include <algorithm>
+#include <atomic>
 
 #include "elem.cuh"
 #include "ptx.cuh"
@@ -834,14 +835,14 @@ cudaError_t launch_sort(SortParams p, cudaStream_t s) {
     return static_cast<size_t>(kSortWarps + CTAS + 1) * (size_t(1) << digit) * sizeof(int) +
            static_cast<size_t>(room) * sizeof(uint64_t);
   };
-  static int configured[64] = {0};
+  static std::atomic<int> configured[64];  // (several threads may come here at once)
   int dev = 0;
   cudaGetDevice(&dev);
-  if (dev < 0 || dev >= 64 || !configured[dev]) {
+  if (dev < 0 || dev >= 64 || !configured[dev].load(std::memory_order_relaxed)) {
     const cudaError_t e = cudaFuncSetAttribute(token_sort_kernel<CTAS, SHARED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(bytes(kSortDigit, SHARED ? kSortRoom : 0)));
     if (e != cudaSuccess) return e;
-    if (dev >= 0 && dev < 64) configured[dev] = 1;
+    if (dev >= 0 && dev < 64) configured[dev].store(1, std::memory_order_relaxed);
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(CTAS);
