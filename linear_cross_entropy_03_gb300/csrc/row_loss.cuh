@@ -534,10 +534,11 @@ __device__ __forceinline__ RowInfo long_teacher_row(const RowLossParams& p, int6
   }
   vmax = warp_max_redux(vmax);
   const float shift = vmax > -INFINITY ? vmax : 0.f;
-  // sum e, and sum e ((v - shift) - (z - zt)) / T with zt any finite logit of the list; the
-  // wanted entries move to the front of the list, to places that have been read
-  float sum = 0.f, a = 0.f;
-  bool have = false;
+  // sum e, and sum e ((v - shift) - (z - zt)) / T with zt the largest logit of a lane's entries
+  // so far, and then of all lanes' (another one, which a mask has put far below the rest, would
+  // take the digits of the sum); the wanted entries move to the front of the list, to places
+  // that have been read
+  float sum = 0.f, a = 0.f, zt = -FLT_MAX;
   int kept = 0;
   for (int k0 = 0; k0 < entries; k0 += 32 * kBatch) {
     int column[kBatch];
@@ -557,16 +558,13 @@ __device__ __forceinline__ RowInfo long_teacher_row(const RowLossParams& p, int6
       const float e = ex2_approx(v[j] * p.c);  // 0: no share, the place is like any other
       const bool held = column[j] >= 0 && e != 0.f;
       const float z = held ? raw_float<T>(raw[j]) : 0.f;
-      if (!have) {
-        const unsigned finite = __ballot_sync(0xffffffffu, held && fabsf(z) < INFINITY);
-        if (finite != 0) {
-          r.zt = __shfl_sync(0xffffffffu, z, __ffs(finite) - 1);
-          have = true;
-        }
-      }
       if (held) {
+        if (z > zt) {
+          if (sum != 0.f) a += sum * ((z - zt) * p.inv_t);
+          zt = z;
+        }
         sum += e;
-        a += e * ((v[j] - (z - r.zt)) * p.inv_t);
+        a += e * ((v[j] - (z - zt)) * p.inv_t);
       }
       const bool here = held && wanted(column[j]);
       const unsigned all = __ballot_sync(0xffffffffu, here);
@@ -578,6 +576,8 @@ __device__ __forceinline__ RowInfo long_teacher_row(const RowLossParams& p, int6
     }
     __syncwarp();
   }
+  r.zt = warp_max_redux(zt);
+  if (sum != 0.f) a += sum * ((r.zt - zt) * p.inv_t);
   sum = warp_sum(sum);
   r.taught = sum != 0.f;  // (a list of -inf alone is no teacher)
   r.entries = r.taught ? kept : 0;
