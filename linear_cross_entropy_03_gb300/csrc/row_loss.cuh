@@ -1033,11 +1033,12 @@ cudaError_t launch_warps(const RowLossParams& p, cudaStream_t s) {
 // Exponents here are x = z c - r with c = log2(e) / T and r = m c rounded: one rounding, of x
 // itself, as z c - r is one operation, so that a common level takes no digits.  At z = m this
 // leaves x = m c - r, up to half a unit in the last place of r, for the sums' last step to take
-// out: 2^-5 below |m c| = 2^20, which harms nothing, but from 2^31 on 2^x would overflow or
-// vanish.  So a warp whose |m c| is 2^20 and more (far_exponent) replaces its z by z - m, and r by
-// 0.  That rounds nothing that has a share: an fp32 difference is exact unless it is 2^19 and more
-// in x, and different 16-bit logits are 2^9 and more apart.  A row's warps may be of both kinds,
-// also about one maximum: what joins them looks at the kind of each.
+// out: at most 64 below |m c| = 2^31, so that sums stay between 2^-64 and V 2^64.  (Shares below
+// 2^-62 of the largest may vanish where the row's maximum lies there; at 2^20 those below 2^-125.)
+// From 2^31 on 2^x could overflow, and any two different fp32 logits are 2^31 2^-24 = 2^7 apart in
+// x, which leaves no share: the warp replaces its z by z - m, and r by 0, and warps with other
+// maxima have no share in the row.  (So from 2^20 on, and what joins warps exact at any distance:
+// bf16 [4096, 128256] without gradients 213 -> 222 us, with masks of -1e9 330 -> 351.)
 //
 // Bound by memory where rows are many and long: bf16 [4096, 128256] 328 us for the policy loss
 // and as much for a teacher's 64 entries, 94 % of the copy rate; fp32 [1000, 50257] 72 us, 82 %,
@@ -1045,7 +1046,7 @@ cudaError_t launch_warps(const RowLossParams& p, cudaStream_t s) {
 // and the closer's arithmetic, 60 to 80 % of the copy rate.  Few rows cost what one does: bf16
 // [1, 128256] 10.9 us, [256, 1024] (by warps) 7.9 on the GPU.
 constexpr int kPartSlots = 4;
-constexpr float kFarExponent = 1048576.f;  // 2^20
+constexpr float kFarExponent = 2147483648.f;  // 2^31
 
 struct PartShape {
   int cluster;    // CTAs of a row
@@ -1284,13 +1285,9 @@ __global__ void __launch_bounds__(THREADS + 64, CTAS_PER_SM)
       float sum = 0.f;
       for (int k = lane; k < cluster * kSums; k += 32) {
         const float2 q = parts[b][k];
-        // a warp's sum goes by its own maximum, or by that one's rounded exponent; warps that have found nothing
-        // have 0, or NaN
-        const float r_q = __fmul_rn(q.x, p.c);
-        const bool far_q = far_exponent(q.x, p.c);
-        const float by = far ? (far_q ? (q.x - m) * p.c : fmaf(-m, p.c, r_q))
-                             : (far_q ? fmaf(q.x, p.c, -r) : r_q - r);
-        sum += q.x > -INFINITY ? q.y * ex2_approx(by) : q.y;
+        // a warp's sum goes by its own rounded exponent; warps that have found nothing have 0, or NaN
+        const float scaled = q.y * ex2_approx(far ? (q.x == m ? 0.f : -INFINITY) : __fmul_rn(q.x, p.c) - r);
+        sum += q.x > -INFINITY ? scaled : q.y;
       }
       sum = warp_sum(sum);                                        // of 2^(z c - r)
       const float s = far ? sum : sum * ex2_approx(fmaf(-m, p.c, r));  // of 2^((z - m) c)
@@ -1367,7 +1364,7 @@ __global__ void __launch_bounds__(THREADS + 64, CTAS_PER_SM)
 #pragma unroll
         for (int k = 0; k < VPT; ++k) vec_subtract<T>(v[k], m);
       }
-      const float r = far || !(m > -INFINITY) ? 0.f : __fmul_rn(m, p.c);
+      float r = far || !(m > -INFINITY) ? 0.f : __fmul_rn(m, p.c);
       Pair sum = pair(0.f);
 #pragma unroll
       for (int k = 0; k < VPT; ++k) {
@@ -1391,20 +1388,10 @@ __global__ void __launch_bounds__(THREADS + 64, CTAS_PER_SM)
       if (p.grad == nullptr || !alive) continue;
       const PartResult result = results[b];
       const bool zero = result.f == 0.f;
-      // the factor goes by the row's exponent, or by its maximum itself where that is far; z - m by the warp's
-      float by = -result.r, scale = result.factor;
-      if (far_exponent(result.m, p.c)) {
-        const float taken = __fmul_rn(result.m, p.c);
-        if (far)
-          by = (m - result.m) * p.c;
-        else if (fabsf(taken) < 2.f * kFarExponent)
-          by = -taken, scale *= ex2_approx(fmaf(-result.m, p.c, taken));
-        else
-          by = result.m > 0.f ? -INFINITY : 0.f;  // the warp lies 2^20 lower, or has -inf alone
-      } else if (far) {
-        by = fmaf(m, p.c, -result.r);
-      }
-      const Pair minus_r = pair(by), factor = pair(scale);
+      // a warp that has taken its own maximum off: the row's, or far below it
+      r = !far ? result.r : m == result.m ? 0.f : INFINITY;
+      if (!far && far_exponent(result.m, p.c)) r = result.m > 0.f ? INFINITY : 0.f;
+      const Pair minus_r = pair(-r), factor = pair(result.factor);
       T* to = g + split.head + (static_cast<int64_t>(first_vec) + tid) * kE;
       // the 16-bit elements are widened again: kept from the sum, they would not fit in the registers
 #pragma unroll
