@@ -1044,7 +1044,7 @@ cudaError_t launch_warps(const RowLossParams& p, cudaStream_t s) {
 // and as much for a teacher's 64 entries, 94 % of the copy rate; fp32 [1000, 50257] 72 us, 82 %,
 // as its last rows leave half of the SMs idle.  Rows of 8 to 32 KB cost their exchange of sums
 // and the closer's arithmetic, 60 to 80 % of the copy rate.  Few rows cost what one does: bf16
-// [1, 128256] 10.9 us, [256, 1024] (by warps) 7.9 on the GPU.
+// [1, 128256] 10.4 us, [256, 1024] (by warps) 7.9 on the GPU.
 constexpr int kPartSlots = 4;
 constexpr float kFarExponent = 2147483648.f;  // 2^31
 
@@ -1517,8 +1517,8 @@ cudaError_t launch_parts(const RowLossParams& p, const PartShape& shape, cudaStr
 // parts from more than four on: bf16 [4096, 128256] 350 -> 325 us (but fp32 [1999, 32001], of
 // four parts, 86 -> 94; the policy loss on [4096, 128256] 328 -> 344).  Lists of more than 64
 // entries are what takes time themselves: fewest CTAs a row, and kernels of their own, whose
-// registers are the list's (bf16 [4096, 32768] with 256 entries 239 -> 134 us, [2048, 128256]
-// with 1000 1039 -> 424).
+// registers are the list's (bf16 [4096, 32768] with 256 entries 239 -> 130 us, [2048, 128256]
+// with 1000 1039 -> 421).
 template <typename T, int KIND>
 cudaError_t launch_rows_of(const RowLossParams& p, cudaStream_t s) {
   const int64_t vecs = p.V / kVecElems<T>;
