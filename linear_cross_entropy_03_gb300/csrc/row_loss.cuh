@@ -623,31 +623,62 @@ struct RowResult {
   float f;  // the gradient is f (p - ...); 0: the row's gradient is 0 whatever its logits
 };
 
+// What a + b loses as its fp32 sum is rounded (Knuth's two-sum), 0 where that is no number.
+__device__ __forceinline__ float sum_error(float a, float b, float sum) {
+  const float from_b = sum - a;
+  const float e = (a - (sum - from_b)) + (b - from_b);
+  return fabsf(sum) < INFINITY ? e : 0.f;
+}
+
+// (zt - m) / T - ln s as `high` plus `low`.  A log-probability of -12 is rounded by 5e-7 in fp32,
+// and a policy's loss knows it by its difference to another one of that size, which takes these
+// digits whole: with the rest apart that difference is as good as s is.  ln s goes by s's own
+// exponent, whose multiple of ln 2 is split so that its larger part is exact.
+struct LogP {
+  float high, low;
+};
+__device__ __forceinline__ LogP split_logp(const RowLossParams& p, float zt, float m, float s) {
+  constexpr float kLn2High = 2839.f / 4096.f;  // 12 bits: exact times an exponent
+  constexpr float kLn2Low = 3.194618494528623e-5f;
+  const int k = (__float_as_int(s) >> 23 & 255) - 127;
+  const float f = s * __uint_as_float(static_cast<unsigned>(127 - k) << 23), exponent = static_cast<float>(k);
+  const float d = zt - m, t = d * p.inv_t;
+  const float rest = fabsf(t) < INFINITY ? fmaf(-t, p.temperature, d) + sum_error(zt, -m, d) : 0.f;
+  LogP r;
+  r.high = fmaf(-exponent, kLn2High, t);
+  r.low = sum_error(t, -exponent * kLn2High, r.high) + rest * p.inv_t - fmaf(exponent, kLn2Low, logf(f));
+  return r;
+}
+
 // `scale`: what multiplies all gradients (grad_scale, or that over the rows of a mean).
 template <int KIND>
 __device__ __forceinline__ RowResult row_result(const RowLossParams& p, const RowInfo& r, float m, float s,
                                                 float scale) {
   RowResult out = {0.f, 0.f, 0.f};
-  const float ln_s = logf(s);
   scale *= r.grad_out;
   if constexpr (has_list(KIND)) {
     if (!r.taught || r.weight == 0.f) return out;
-    out.loss = p.temperature * p.temperature * r.weight * (r.a + ((m - r.zt) * p.inv_t + ln_s));
+    out.loss = p.temperature * p.temperature * r.weight * (r.a + ((m - r.zt) * p.inv_t + logf(s)));
     out.f = p.temperature * r.weight * scale;
+  } else if constexpr (KIND == kStats) {
+    if (r.column >= 0) out.logp = (r.zt - m) * p.inv_t - logf(s);
   } else {
     if (r.column < 0) return out;
-    out.logp = (r.zt - m) * p.inv_t - ln_s;
-    if (KIND == kStats || r.weight == 0.f) return out;
+    const LogP logp = split_logp(p, r.zt, m, s);
+    out.logp = logp.high + logp.low;
+    if (r.weight == 0.f) return out;
     const float a = r.advantage;
     // fresh samples have a ratio of 1, but a row of no number has none
-    const float ratio = p.old_logp != nullptr ? expf(out.logp - r.old_logp) : isnan(out.logp) ? out.logp : 1.f;
+    const float ratio = p.old_logp != nullptr ? expf((logp.high - r.old_logp) + logp.low)
+                        : isnan(out.logp)     ? out.logp
+                                              : 1.f;
     const bool over = a > 0.f && ratio > p.ratio_high, under = a < 0.f && ratio < p.ratio_low;
     // an advantage of 0 takes nothing of a ratio that fp32 holds as infinite (NaN stays)
     const float gain = a == 0.f && ratio > FLT_MAX ? 0.f : a * ratio;
     float loss = over ? -a * p.ratio_high : under ? -a * p.ratio_low : -gain;
     float slope = over || under ? 0.f : -gain;
     if (p.kl_weight != 0.f) {
-      const float d = r.ref_logp - out.logp, x = expm1f(d);
+      const float d = (r.ref_logp - logp.high) - logp.low, x = expm1f(d);
       loss += p.kl_weight * (x - d);
       slope -= p.kl_weight * x;
     }

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import linear_cross_entropy_03_gb300 as flce
-from losses_util import cuda, f32, make_logits
+from losses_util import cuda, f32, make_logits, wide
 from test_gpu_losses import DTYPES, check_policy, policy_inputs
 
 pytestmark = pytest.mark.gpu
@@ -50,3 +50,27 @@ def test_rows_of_no_number_on_fresh_samples(v, clip):
     assert out["grad_logits"][good].isfinite().all() and (out["grad_logits"][7] == 0).all()
     mean = flce.policy_loss(z, cuda(t), a, clip=clip)
     assert mean["loss"].isnan()
+
+
+@pytest.mark.parametrize("v", [2, 700, 9000, 70001, 290000])
+@pytest.mark.parametrize("temperature", [1.0, 0.7, 3.0])
+def test_a_difference_of_log_probabilities_keeps_its_digits(temperature, v):
+    """A target far below the one column that has a share: logp is a number of -60 to -120, where fp32 has steps
+    of 2^-18 and 2^-17, and logp - old_logp of at most 0.5.  The ratio is off by expf's two units, and three roundings
+    of numbers of at most its size: below 2^-21 of it."""
+    n, rng = 64, np.random.default_rng(v)
+    t32 = float(np.float32(temperature))
+    z = torch.full((n, v), -4000.0, device="cuda")
+    z[:, 0] = torch.linspace(-9, 9, n, device="cuda")
+    t = rng.integers(1, v, n)
+    z[torch.arange(n), cuda(t)] = cuda(rng.uniform(-120, -60, n) * temperature, torch.float32)
+    zw = z.double().cpu().numpy()
+    logp = (zw[np.arange(n), t] - zw[:, 0]) / t32
+    old, a = f32(logp - rng.uniform(-0.5, 0.5, n)), f32(rng.normal(size=n))
+    out = flce.policy_loss(z, cuda(t), cuda(a, torch.float32), old_logp=cuda(old, torch.float32), clip=math.inf,
+                           temperature=temperature, reduction="none")
+    want = a * np.exp(logp - old)
+    assert (np.abs(-wide(out["loss"]) - want) <= np.abs(want) * 2.0 ** -21).all()
+    assert (np.abs(wide(out["logp"]) - logp) <= np.abs(logp) * 2.0 ** -24 + 2.0 ** -30).all()    # half a step of fp32
+    slope = wide(out["grad_logits"])[np.arange(n), t] * t32
+    assert (np.abs(slope + want) <= np.abs(want) * 2.0 ** -20).all()                             # two products more
